@@ -265,6 +265,173 @@ int attnres_block_merge_update(const void *inter_out, const float *inter_lse, co
 int attnres_rms_norm(const void *x, int64_t B, int64_t T, int64_t D, int dtype, const float *weight,
                      float eps, void *y, void *stream);
 
+/* -------------------------------------------------------------------------
+ * The attention sublayer's operators.  They work on head tensors: a query,
+ * key or value tensor is [B, T, H, d] with the heads of a token side by side
+ * (head stride d) and the B*T token rows evenly spaced, `stride` elements
+ * apart (H * d when contiguous; more when q, k and v are views of one
+ * projection's output).  Strides are multiples of 8 (bf16) or 4 (fp32).
+ * As above, pointers are 16-byte aligned (those to positions, lengths, page
+ * tables, decays, frequencies and lse: to their element), arithmetic and
+ * statistics are fp32, outputs are rounded once, nothing is allocated and the
+ * calls return without waiting.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * RMS norm of every query and key head with the position rotation in the
+ * same pass (the norm of attnres_rms_norm over each head's d elements, the
+ * weight shared by the heads):
+ *   z = x / sqrt(mean_d x^2 + eps) (.) weight,
+ *   y = z with its first `rot` elements turned in pairs by the angle
+ *       position * inv_freq[i], i = 0 .. rot/2 - 1:
+ *       (z_a, z_b) -> (z_a cos - z_b sin, z_b cos + z_a sin), where (a, b) is
+ *       (i, i + rot/2), or (2i, 2i + 1) with interleaved = 1.
+ *   q, k        device [B,T,Hq,d], [B,T,Hk,d]; d a multiple of 16 (bf16, up
+ *               to 512) or 8 (fp32, up to 256)
+ *   q_weight, k_weight  device fp32 [d] or NULL (ones)
+ *   positions   device int32 [B,T], or NULL for 0 .. T-1 in every sequence;
+ *               any value: angles are exact to 2^-25 of a half turn however
+ *               far the position
+ *   inv_freq    device fp64 [rot/2], radians per position (NULL if rot == 0)
+ *   rot         0 .. d, a multiple of 16 (bf16) or 8 (fp32)
+ *   q_out, k_out  device, rows q_out_stride / k_out_stride elements apart;
+ *               may be q / k themselves with the same stride
+ */
+int attnres_head_norm_rotate(const void *q, const void *k, int64_t B, int64_t T, int Hq, int Hk, int64_t d, int dtype,
+                             int64_t q_stride, int64_t k_stride, const float *q_weight, const float *k_weight,
+                             const int32_t *positions, const double *inv_freq, int rot, int interleaved, float eps,
+                             void *q_out, void *k_out, int64_t q_out_stride, int64_t k_out_stride, void *stream);
+
+/*
+ * The same for serving: the normed, rotated keys and the values go into a
+ * paged cache in the same pass; only q_out is a tensor of its own.
+ *   v           device [B,T,Hk,d]
+ *   k_cache, v_cache  device [num_pages, Hk, page_size, d]
+ *   page_table  device int32 [B, max_pages]: page i of sequence b holds its
+ *               positions i * page_size .. (i + 1) * page_size - 1
+ * A token's place in the cache is its position.  A token whose position is
+ * negative or behind the table, or whose page number is outside
+ * [0, num_pages), is rotated into q_out but not stored (padding).  Two
+ * tokens of one call with the same place race: one of them is stored, for
+ * each 16-byte vector on its own.
+ */
+int attnres_head_norm_rotate_append(const void *q, const void *k, const void *v, int64_t B, int64_t T, int Hq, int Hk,
+                                    int64_t d, int dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                    const float *q_weight, const float *k_weight, const int32_t *positions,
+                                    const double *inv_freq, int rot, int interleaved, float eps, void *q_out,
+                                    int64_t q_out_stride, void *k_cache, void *v_cache, int64_t num_pages,
+                                    int page_size, const int32_t *page_table, int max_pages, void *stream);
+
+/*
+ * Backward of attnres_head_norm_rotate for the upstream gradients grad_q,
+ * grad_k of its outputs (nothing from the forward is needed but its inputs):
+ *   dz = the gradient turned back, u = dz (.) weight, r = (mean x^2 + eps)^(-1/2)
+ *   dx = r (u - x r^2 mean(u (.) x)),   grad_weight = sum over tokens and heads of dz (.) x r
+ *   dq, dk      device, contiguous [B,T,Hq,d], [B,T,Hk,d]
+ *   grad_q_weight, grad_k_weight  device fp32 [d] or NULL
+ *   workspace   device fp32 [workspace_rows, d], needed for a weight gradient;
+ *               attnres_head_norm_rotate_backward_workspace_rows() rows fill
+ *               the current device, fewer (at least 2) run fewer CTAs.  Its
+ *               contents on entry do not matter.
+ * The weight sums run in a fixed order: the same inputs give the same bits.
+ * B*T == 0: the weight gradients are set to zero.
+ */
+int attnres_head_norm_rotate_backward(const void *q, const void *k, int64_t B, int64_t T, int Hq, int Hk, int64_t d,
+                                      int dtype, int64_t q_stride, int64_t k_stride, const float *q_weight,
+                                      const float *k_weight, const int32_t *positions, const double *inv_freq, int rot,
+                                      int interleaved, float eps, const void *grad_q, const void *grad_k,
+                                      int64_t grad_q_stride, int64_t grad_k_stride, void *dq, void *dk,
+                                      float *grad_q_weight, float *grad_k_weight, float *workspace,
+                                      int64_t workspace_rows, void *stream);
+int64_t attnres_head_norm_rotate_backward_workspace_rows(void);
+
+/*
+ * Attention of one new token per sequence over a paged key-value cache, split
+ * over the cache's length and joined by the online-softmax merge (OS2):
+ *   s_j = scale q . k_j (j < lengths[b]),  out = sum_j softmax(s)_j v_j,
+ *   lse = ln sum_j e^{s_j}
+ * for every query head; query heads h / (Hq / Hk) share a key head.
+ *   q           device [B,Hq,d], sequences q_stride elements apart
+ *   k_cache, v_cache, page_table, page_size: as attnres_head_norm_rotate_append
+ *   lengths     device int32 [B]: cached tokens to attend over, the new one
+ *               among them; taken as 0 if negative and at most max_pages * page_size
+ *   d           up to 256, a multiple of 8 (bf16) or 4 (fp32)
+ *   Hq          a multiple of Hk, at most 16 times
+ *   out         device [B,Hq,d], contiguous;  lse device fp32 [B,Hq] or NULL
+ *   workspace   device, attnres_paged_attention_workspace_bytes() bytes; its
+ *               contents on entry do not matter.  Two calls that may overlap
+ *               (other streams, graphs launched side by side) need one each.
+ * An empty sequence gives zeros and lse = -infinity.  Cache contents behind
+ * lengths[b] are never used, whatever they hold; tokens on a page whose
+ * number is outside [0, num_pages) are left out.
+ */
+int attnres_paged_attention(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
+                            int64_t num_pages, int page_size, const int32_t *page_table, int max_pages,
+                            const int32_t *lengths, int64_t B, int Hq, int Hk, int64_t d, int dtype, float scale,
+                            void *out, float *lse, void *workspace, int64_t workspace_bytes, void *stream);
+/* Workspace bytes of attnres_paged_attention on the current device: they do not depend on B or the lengths. */
+int64_t attnres_paged_attention_workspace_bytes(int Hq, int Hk, int64_t d, int dtype);
+
+/*
+ * Linear attention with one decay per head, over prompts (the delta-free
+ * linear layers that "Attention Residuals：当网络深度也拥有寻址能力", section "Kimi
+ * Linear 与 K3 中的接入", puts between the aggregations):
+ *   S_t = e^{g_h} S_{t-1} + k_t v_t^T,   out_t = scale S_t^T q_t
+ *   q, k        device [B,T,H,dk];  v device [B,T,H,dv];  dk, dv up to 128,
+ *               multiples of 8 (bf16) or 4 (fp32)
+ *   log_decay   device fp32 [H]: g_h <= 0
+ *   scale       finite, with a finite reciprocal
+ *   lengths     device int32 [B] or NULL (T): tokens of each sequence, held
+ *               within 0 .. T; out behind them is zero
+ *   state       device fp32 [B,H,dk,dv] S_0, or NULL (zeros)
+ *   out         device [B,T,H,dv], contiguous
+ *   state_out   device fp32 [B,H,dk,dv] S after each sequence's last token, or NULL; may be state
+ *   workspace   device, attnres_linear_attention_workspace_bytes() bytes (may
+ *               be 0, then NULL is allowed); contents on entry do not matter
+ * bf16 inputs: products on the tensor cores with fp32 accumulators and an
+ * fp32 state; the masked products and the state are rounded to bf16 where
+ * they enter the product that forms out.
+ */
+int attnres_linear_attention(const void *q, const void *k, const void *v, int64_t B, int64_t T, int H, int64_t dk,
+                             int64_t dv, int dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                             const float *log_decay, float scale, const int32_t *lengths, const float *state,
+                             void *out, float *state_out, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Its backward for the upstream gradients grad_out of out and grad_state of
+ * the final state (NULL: zero); the decay is not a parameter.  With G_t =
+ * e^g G_{t+1} + scale q_t grad_out_t^T (grad_state entering undecayed at the
+ * last token):
+ *   dq_t = scale S_t grad_out_t,  dk_t = G_t v_t,  dv_t = G_t^T k_t,
+ *   grad_initial = e^g G_1
+ *   grad_out    device [B,T,H,dv], rows grad_out_stride elements apart
+ *   dq, dk, dv_out  device, contiguous; zero behind the sequences
+ *   grad_initial  device fp32 [B,H,dk,dv] or NULL; must not be grad_state
+ *   workspace   attnres_linear_attention_backward_workspace_bytes() bytes
+ * The sums run in a fixed order: the same inputs give the same bits.
+ */
+int attnres_linear_attention_backward(const void *q, const void *k, const void *v, int64_t B, int64_t T, int H,
+                                      int64_t dk, int64_t dv, int dtype, int64_t q_stride, int64_t k_stride,
+                                      int64_t v_stride, const float *log_decay, float scale, const int32_t *lengths,
+                                      const float *state, const void *grad_out, int64_t grad_out_stride,
+                                      const float *grad_state, void *dq, void *dk_out, void *dv_out,
+                                      float *grad_initial, void *workspace, int64_t workspace_bytes, void *stream);
+int64_t attnres_linear_attention_workspace_bytes(int64_t B, int64_t T, int H, int64_t dk, int64_t dv, int dtype);
+int64_t attnres_linear_attention_backward_workspace_bytes(int64_t B, int64_t T, int H, int64_t dk, int64_t dv,
+                                                          int dtype);
+
+/*
+ * The recurrent form for one token per sequence: S' = e^g S + k v^T, out =
+ * scale S'^T q.
+ *   q, k        device [B,H,dk], v device [B,H,dv], sequences `stride` elements apart
+ *   state       device fp32 [B,H,dk,dv];  state_out the same, may be state
+ *   out         device [B,H,dv], contiguous
+ */
+int attnres_linear_attention_step(const void *q, const void *k, const void *v, int64_t B, int H, int64_t dk,
+                                  int64_t dv, int dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                  const float *log_decay, float scale, const float *state, float *state_out, void *out,
+                                  void *stream);
+
 /*
  * Full AttnRes stack forward ("FullAttnResStack", eq. A1-A4) with the
  * synthetic sublayer f_l(h) = 0.5 * tanh(u_l (.) h):

@@ -1,7 +1,9 @@
 """GB300-native (sm_103a) hot path of Attention Residuals.
 
 The depth-wise softmax aggregation -- Full, Block and the two-phase Block
-inference scheme -- as hand-written CUDA kernels behind a C ABI
+inference scheme -- and the attention sublayer's operators between two
+aggregations (head norm with rotation, paged attention of one token, linear
+attention with decay) as hand-written CUDA kernels behind a C ABI
 (include/attnres.h, libattnres.so), with thin PyTorch wrappers.
 
 ``workloads`` (seeded synthetic inputs) imports without the CUDA library;
@@ -12,7 +14,9 @@ from . import workloads  # noqa: F401
 __all__ = [
     "depth_aggregate", "block_phase1", "block_phase2_merge", "partial_update",
     "full_stack_forward", "TwoPhaseBlock", "block_two_phase", "block_schedule",
-    "atomic_block_size", "workloads",
+    "atomic_block_size", "head_norm_rotate", "head_norm_rotate_append", "head_norm_rotate_backward",
+    "rotary_frequencies", "paged_attention", "linear_attention", "linear_attention_backward",
+    "linear_attention_step", "workloads",
 ]
 
 

@@ -56,6 +56,27 @@ SIGNATURES = {
                                                         _vp, _int, _vp, _vp, _vp]),
     "attnres_full_stack_forward": (_int, [_pp, _int, _i64, _i64, _i64, _int, _vp, _vp, _vp, _f, _vp,
                                           _vp]),
+    "attnres_head_norm_rotate": (_int, [_vp, _vp, _i64, _i64, _int, _int, _i64, _int, _i64, _i64, _vp, _vp, _vp, _vp,
+                                        _int, _int, _f, _vp, _vp, _i64, _i64, _vp]),
+    "attnres_head_norm_rotate_append": (_int, [_vp, _vp, _vp, _i64, _i64, _int, _int, _i64, _int, _i64, _i64, _i64,
+                                               _vp, _vp, _vp, _vp, _int, _int, _f, _vp, _i64, _vp, _vp, _i64, _int,
+                                               _vp, _int, _vp]),
+    "attnres_head_norm_rotate_backward": (_int, [_vp, _vp, _i64, _i64, _int, _int, _i64, _int, _i64, _i64, _vp, _vp,
+                                                 _vp, _vp, _int, _int, _f, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp,
+                                                 _vp, _i64, _vp]),
+    "attnres_head_norm_rotate_backward_workspace_rows": (_i64, []),
+    "attnres_paged_attention": (_int, [_vp, _i64, _vp, _vp, _i64, _int, _vp, _int, _vp, _i64, _int, _int, _i64, _int,
+                                       _f, _vp, _vp, _vp, _i64, _vp]),
+    "attnres_paged_attention_workspace_bytes": (_i64, [_int, _int, _i64, _int]),
+    "attnres_linear_attention": (_int, [_vp, _vp, _vp, _i64, _i64, _int, _i64, _i64, _int, _i64, _i64, _i64, _vp, _f,
+                                        _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "attnres_linear_attention_workspace_bytes": (_i64, [_i64, _i64, _int, _i64, _i64, _int]),
+    "attnres_linear_attention_backward": (_int, [_vp, _vp, _vp, _i64, _i64, _int, _i64, _i64, _int, _i64, _i64, _i64,
+                                                 _vp, _f, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
+                                                 _vp]),
+    "attnres_linear_attention_backward_workspace_bytes": (_i64, [_i64, _i64, _int, _i64, _i64, _int]),
+    "attnres_linear_attention_step": (_int, [_vp, _vp, _vp, _i64, _int, _i64, _i64, _int, _i64, _i64, _i64, _vp, _f,
+                                             _vp, _vp, _vp, _vp]),
     "attnres_block_schedule": (_int, [_int, _int, _ip, _ip, _int]),
     "attnres_atomic_block_size": (_int, [_int, _int]),
     "attnres_take_device_error": (_int, []),

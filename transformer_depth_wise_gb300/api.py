@@ -617,6 +617,329 @@ def block_two_phase(blocks, queries, gains, u, eps: float = 1e-8, fused: bool = 
     return p, blk.h
 
 
+# --------------------------------------------------------------------------
+# The attention sublayer: head norm with rotation, paged attention of one
+# token, linear attention with a decay per head.
+# --------------------------------------------------------------------------
+def _call(name: str, device: torch.device, *args) -> None:
+    """The C entry point on `device`'s current stream, with that device current."""
+    fn = getattr(_lib.lib(), name)
+    if device.index is None or device.index == torch.cuda.current_device():
+        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    _lib.check(name, rc)
+
+
+def _sized(name: str, device: torch.device, *args) -> int:
+    """A workspace query with `device` current."""
+    fn = getattr(_lib.lib(), name)
+    if device.index is None or device.index == torch.cuda.current_device():
+        n = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            n = fn(*args)
+    return _lib.check(name, int(n))
+
+
+def _heads(t, name: str, like=None, shape=None) -> int:
+    """Row stride of a head tensor [.., H, d]: the heads of a token side by side, the rows evenly spaced."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if like is not None:
+        if t.dtype != like.dtype:
+            raise TypeError(f"{name} must be {like.dtype}")
+        if t.device != like.device:
+            raise ValueError(f"{name} must be on {like.device}")
+    elif t.dtype not in _CODES:
+        _code(t)
+    H, d = t.shape[-2:]
+    st = t.stride()
+    if t.numel() and ((d > 1 and st[-1] != 1) or (H > 1 and st[-2] != d)):
+        raise ValueError(f"{name}: the heads of a token must lie side by side")
+    if t.dim() == 3:
+        return st[0] if t.shape[0] > 1 else H * d
+    if t.dim() != 4:
+        raise ValueError(f"{name} must be [B, T, H, d]")
+    B, T = t.shape[:2]
+    if B > 1 and T > 1:
+        if st[0] != T * st[1] and t.numel():
+            raise ValueError(f"{name}: its token rows must be evenly spaced")
+        return st[1]
+    return st[1] if T > 1 else st[0] if B > 1 else H * d
+
+
+def _plain(t, name: str, dtype, shape, device):
+    """A contiguous CUDA tensor of this dtype and shape on `device` (None stays None)."""
+    if t is None:
+        return None
+    _cuda(t, name)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    return t
+
+
+def _workspace(t, nbytes: int, device):
+    """The caller's workspace, or one of `nbytes` allocated here; (tensor, address, bytes)."""
+    if t is None:
+        t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    else:
+        _cuda(t, "workspace")
+        if t.device != device:
+            raise ValueError(f"workspace must be on {device}")
+    return t, t.data_ptr() or None, t.numel() * t.element_size()
+
+
+def rotary_frequencies(rot: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """inv_freq of head_norm_rotate: base^(-2i / rot) radians per position, i = 0 .. rot/2 - 1, float64."""
+    return base ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / max(rot, 1))
+
+
+def _norm_args(q, k, q_weight, k_weight, positions, inv_freq):
+    """Checks shared by the head norm's three calls; (B, T, Hq, Hk, d, q's and k's row strides, rot)."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a [B, T, H, d] tensor")
+    qs = _heads(q, "q")
+    B, T, Hq, d = q.shape
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be a [B, T, H, d] tensor")
+    Hk = k.shape[2]
+    ks = _heads(k, "k", q, (B, T, Hk, d))
+    dev = q.device
+    _plain(q_weight, "q_weight", torch.float32, (d,), dev)
+    _plain(k_weight, "k_weight", torch.float32, (d,), dev)
+    _plain(positions, "positions", torch.int32, (B, T), dev)
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        _plain(inv_freq, "inv_freq", torch.float64, (rot // 2,), dev)
+    return B, T, Hq, Hk, d, qs, ks, rot
+
+
+def head_norm_rotate(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=None, eps: float = 1e-6,
+                     interleaved: bool = False, q_out=None, k_out=None):
+    """RMS norm of every query and key head and the position rotation, in one pass; returns (q_out, k_out).
+
+    q [B,T,Hq,d], k [B,T,Hk,d]: contiguous, or views of one projection's output.  positions int32 [B,T]
+    (None: 0 .. T-1), inv_freq float64 [rot/2] (rotary_frequencies; None: no rotation).  q_out / k_out may be q / k.
+    """
+    B, T, Hq, Hk, d, qs, ks, rot = _norm_args(q, k, q_weight, k_weight, positions, inv_freq)
+    if q_out is None:
+        q_out = torch.empty((B, T, Hq, d), dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty((B, T, Hk, d), dtype=q.dtype, device=q.device)
+    qos, kos = _heads(q_out, "q_out", q, q.shape), _heads(k_out, "k_out", q, k.shape)
+    _call("attnres_head_norm_rotate", q.device, q.data_ptr(), k.data_ptr(), B, T, Hq, Hk, d, _CODES[q.dtype], qs, ks,
+          _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq), rot, 1 if interleaved else 0, float(eps),
+          q_out.data_ptr(), k_out.data_ptr(), qos, kos)
+    return q_out, k_out
+
+
+def head_norm_rotate_append(q, k, v, q_weight, k_weight, positions, inv_freq, k_cache, v_cache, page_table,
+                            eps: float = 1e-6, interleaved: bool = False, q_out=None):
+    """head_norm_rotate whose keys go into a paged cache with the values, at each token's position; returns q_out.
+
+    k_cache, v_cache [num_pages, Hk, page_size, d]; page_table int32 [B, max_pages].  Tokens whose position has no
+    page (negative, behind the table, a page number outside the pool) are not stored.
+    """
+    B, T, Hq, Hk, d, qs, ks, rot = _norm_args(q, k, q_weight, k_weight, positions, inv_freq)
+    dev = q.device
+    vs = _heads(v, "v", q, (B, T, Hk, d))
+    num_pages, page_size, max_pages = _cache_args(k_cache, v_cache, page_table, q, B, Hk, d)
+    if q_out is None:
+        q_out = torch.empty((B, T, Hq, d), dtype=q.dtype, device=dev)
+    qos = _heads(q_out, "q_out", q, q.shape)
+    _call("attnres_head_norm_rotate_append", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), B, T, Hq, Hk, d,
+          _CODES[q.dtype], qs, ks, vs, _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq), rot,
+          1 if interleaved else 0, float(eps), q_out.data_ptr(), qos, k_cache.data_ptr(), v_cache.data_ptr(),
+          num_pages, page_size, page_table.data_ptr(), max_pages)
+    return q_out
+
+
+def _cache_args(k_cache, v_cache, page_table, q, B, Hk, d):
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        _cuda(t, name)
+        if t.dim() != 4 or t.shape[1] != Hk or t.shape[3] != d or t.shape != k_cache.shape:
+            raise ValueError(f"{name} must be [num_pages, {Hk}, page_size, {d}]")
+        if t.dtype != q.dtype:
+            raise TypeError(f"{name} must be {q.dtype}")
+        if t.device != q.device:
+            raise ValueError(f"{name} must be on {q.device}")
+    if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+        raise ValueError("page_table must be a [B, max_pages] tensor")
+    _plain(page_table, "page_table", torch.int32, (B, page_table.shape[1]), q.device)
+    return k_cache.shape[0], k_cache.shape[2], page_table.shape[1]
+
+
+def head_norm_rotate_backward(q, k, q_weight, k_weight, positions, inv_freq, eps: float, grad_q, grad_k,
+                              interleaved: bool = False, want_weights: bool = True, workspace=None):
+    """Gradients of head_norm_rotate for the upstream grad_q, grad_k.
+
+    Returns (dq, dk, grad_q_weight [d] fp32, grad_k_weight [d] fp32); the last two are None without want_weights.
+    workspace: fp32 [rows, d] scratch (allocated when None).
+    """
+    B, T, Hq, Hk, d, qs, ks, rot = _norm_args(q, k, q_weight, k_weight, positions, inv_freq)
+    dev = q.device
+    gqs, gks = _heads(grad_q, "grad_q", q, q.shape), _heads(grad_k, "grad_k", q, k.shape)
+    dq = torch.empty((B, T, Hq, d), dtype=q.dtype, device=dev)
+    dk = torch.empty((B, T, Hk, d), dtype=q.dtype, device=dev)
+    gw = gkw = None
+    rows = 0
+    if want_weights:
+        gw, gkw = torch.empty((2, d), dtype=torch.float32, device=dev).unbind(0)
+        if workspace is None:
+            rows = _sized("attnres_head_norm_rotate_backward_workspace_rows", dev)
+            workspace = torch.empty((rows, d), dtype=torch.float32, device=dev)
+        else:
+            rows = _f32(workspace, "workspace").numel() // d
+            if workspace.device != dev:
+                raise ValueError(f"workspace must be on {dev}")
+    _call("attnres_head_norm_rotate_backward", dev, q.data_ptr(), k.data_ptr(), B, T, Hq, Hk, d, _CODES[q.dtype], qs,
+          ks, _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq), rot, 1 if interleaved else 0,
+          float(eps), grad_q.data_ptr(), grad_k.data_ptr(), gqs, gks, dq.data_ptr(), dk.data_ptr(), _ptr(gw),
+          _ptr(gkw), _ptr(workspace) if want_weights else None, rows)
+    return dq, dk, gw, gkw
+
+
+def paged_attention(q, k_cache, v_cache, page_table, lengths, scale: float, out=None, lse=None, workspace=None):
+    """Attention of one new token per sequence over a paged cache; returns (out [B,Hq,d], lse [B,Hq] fp32).
+
+    q [B,Hq,d]; k_cache, v_cache [num_pages, Hk, page_size, d]; page_table int32 [B, max_pages]; lengths int32 [B],
+    the new token among them.  workspace: uint8 CUDA scratch of attnres_paged_attention_workspace_bytes (allocated
+    when None); calls that may overlap need one each.
+    """
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a [B, H, d] tensor")
+    qs = _heads(q, "q")
+    B, Hq, d = q.shape
+    dev, code = q.device, _CODES[q.dtype]
+    Hk = k_cache.shape[1] if isinstance(k_cache, torch.Tensor) and k_cache.dim() == 4 else 0
+    num_pages, page_size, max_pages = _cache_args(k_cache, v_cache, page_table, q, B, Hk, d)
+    _cuda(lengths, "lengths")
+    _plain(lengths, "lengths", torch.int32, (B,), dev)
+    if out is None:
+        out = torch.empty((B, Hq, d), dtype=q.dtype, device=dev)
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+    _plain(out, "out", q.dtype, q.shape, dev)
+    _plain(lse, "lse", torch.float32, (B, Hq), dev)
+    need = 0
+    if workspace is None:
+        need = _sized("attnres_paged_attention_workspace_bytes", dev, Hq, Hk, d, code)
+    ws, wp, wn = _workspace(workspace, need, dev)
+    _call("attnres_paged_attention", dev, q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), num_pages,
+          page_size, page_table.data_ptr(), max_pages, lengths.data_ptr(), B, Hq, Hk, d, code, float(scale),
+          out.data_ptr(), lse.data_ptr(), wp, wn)
+    return out, lse
+
+
+def _linear_args(q, k, v, log_decay, lengths, state):
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a [B, T, H, d] tensor")
+    qs = _heads(q, "q")
+    B, T, H, dk = q.shape
+    ks = _heads(k, "k", q, q.shape)
+    if not isinstance(v, torch.Tensor) or v.dim() != 4:
+        raise ValueError("v must be a [B, T, H, d] tensor")
+    dv = v.shape[3]
+    vs = _heads(v, "v", q, (B, T, H, dv))
+    dev = q.device
+    _cuda(log_decay, "log_decay")
+    _plain(log_decay, "log_decay", torch.float32, (H,), dev)
+    _plain(lengths, "lengths", torch.int32, (B,), dev)
+    _plain(state, "state", torch.float32, (B, H, dk, dv), dev)
+    return B, T, H, dk, dv, qs, ks, vs
+
+
+def linear_attention(q, k, v, log_decay, scale: float, state=None, lengths=None, out=None, state_out=None,
+                     want_state: bool = True, workspace=None):
+    """Linear attention with one decay per head over prompts; returns (out [B,T,H,dv], final state or None).
+
+    q, k [B,T,H,dk], v [B,T,H,dv] (contiguous, or views of one projection's output); log_decay fp32 [H] (<= 0);
+    state fp32 [B,H,dk,dv], the state to start from; lengths int32 [B], tokens per sequence of a padded batch
+    (out is zero behind them).  state_out may be state.
+    """
+    B, T, H, dk, dv, qs, ks, vs = _linear_args(q, k, v, log_decay, lengths, state)
+    dev, code = q.device, _CODES[q.dtype]
+    if out is None:
+        out = torch.empty((B, T, H, dv), dtype=q.dtype, device=dev)
+    _plain(out, "out", q.dtype, (B, T, H, dv), dev)
+    if state_out is None and want_state:
+        state_out = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+    _plain(state_out, "state_out", torch.float32, (B, H, dk, dv), dev)
+    need = 0
+    if workspace is None:
+        need = _sized("attnres_linear_attention_workspace_bytes", dev, B, T, H, dk, dv, code)
+    ws, wp, wn = _workspace(workspace, need, dev)
+    _call("attnres_linear_attention", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), B, T, H, dk, dv, code, qs, ks, vs,
+          log_decay.data_ptr(), float(scale), _ptr(lengths), _ptr(state), out.data_ptr(), _ptr(state_out), wp, wn)
+    return out, state_out
+
+
+def linear_attention_backward(q, k, v, log_decay, scale: float, grad_out, state=None, lengths=None, grad_state=None,
+                              want_initial=None, workspace=None):
+    """Gradients of linear_attention for the upstream grad_out and, when given, grad_state of its final state.
+
+    Returns (dq, dk, dv, gradient of `state` or None); the last is formed when a state was given, or as
+    want_initial says.  The decay is a constant, not a parameter.
+    """
+    B, T, H, dk, dv, qs, ks, vs = _linear_args(q, k, v, log_decay, lengths, state)
+    dev, code = q.device, _CODES[q.dtype]
+    gs = _heads(grad_out, "grad_out", q, (B, T, H, dv))
+    _plain(grad_state, "grad_state", torch.float32, (B, H, dk, dv), dev)
+    dq, dkey = (torch.empty((B, T, H, dk), dtype=q.dtype, device=dev) for _ in range(2))
+    dval = torch.empty((B, T, H, dv), dtype=q.dtype, device=dev)
+    ds = None
+    if want_initial or (want_initial is None and state is not None):
+        ds = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+    need = 0
+    if workspace is None:
+        need = _sized("attnres_linear_attention_backward_workspace_bytes", dev, B, T, H, dk, dv, code)
+    ws, wp, wn = _workspace(workspace, need, dev)
+    _call("attnres_linear_attention_backward", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), B, T, H, dk, dv, code,
+          qs, ks, vs, log_decay.data_ptr(), float(scale), _ptr(lengths), _ptr(state), grad_out.data_ptr(), gs,
+          _ptr(grad_state), dq.data_ptr(), dkey.data_ptr(), dval.data_ptr(), _ptr(ds), wp, wn)
+    return dq, dkey, dval, ds
+
+
+def linear_attention_step(q, k, v, log_decay, scale: float, state, state_out=None, out=None):
+    """The recurrent form for one token per sequence: state <- e^g state + k v^T, out = scale state^T q; returns out.
+
+    q, k [B,H,dk], v [B,H,dv]; state fp32 [B,H,dk,dv], updated in place unless state_out is given.
+    """
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a [B, H, d] tensor")
+    qs = _heads(q, "q")
+    B, H, dk = q.shape
+    ks = _heads(k, "k", q, q.shape)
+    if not isinstance(v, torch.Tensor) or v.dim() != 3:
+        raise ValueError("v must be a [B, H, d] tensor")
+    dv = v.shape[2]
+    vs = _heads(v, "v", q, (B, H, dv))
+    dev = q.device
+    _cuda(log_decay, "log_decay")
+    _plain(log_decay, "log_decay", torch.float32, (H,), dev)
+    _cuda(state, "state")
+    _plain(state, "state", torch.float32, (B, H, dk, dv), dev)
+    if state_out is None:
+        state_out = state
+    _plain(state_out, "state_out", torch.float32, (B, H, dk, dv), dev)
+    if out is None:
+        out = torch.empty((B, H, dv), dtype=q.dtype, device=dev)
+    _plain(out, "out", q.dtype, (B, H, dv), dev)
+    _call("attnres_linear_attention_step", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), B, H, dk, dv,
+          _CODES[q.dtype], qs, ks, vs, log_decay.data_ptr(), float(scale), state.data_ptr(), state_out.data_ptr(),
+          out.data_ptr())
+    return out
+
+
 def block_schedule(num_atomic: int, block_size: int):
     """forward_naive's source lists (host bookkeeping): num_atomic+1 lists, -1 = partial."""
     cap = (num_atomic + 1) * (num_atomic + 2)

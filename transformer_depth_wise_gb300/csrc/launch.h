@@ -176,6 +176,106 @@ struct Phase1ManyArgs {
 bool phase1_many_supported(int n, int D, int dtype, int S, int64_t rows);
 cudaError_t launch_phase1_many(const Phase1ManyArgs &a);
 
+struct HeadNormArgs {
+  const void *q, *k, *v;       // [rows, Hq, d], [rows, Hk, d]; v only into a cache
+  int64_t q_stride, k_stride, v_stride;
+  int64_t rows, T;             // rows = B * T
+  int Hq, Hk, d, dtype;
+  const float *q_weight, *k_weight;    // [d] or nullptr
+  const int32_t *positions;    // [rows] or nullptr (0 .. T - 1)
+  const double *inv_freq;      // [rot / 2]
+  int rot, interleaved;
+  float eps;
+  void *q_out, *k_out;         // k_out: the key cache when page_size > 0
+  int64_t q_out_stride, k_out_stride;
+  void *v_cache;
+  const int32_t *page_table;   // [B, max_pages]
+  int64_t num_pages;
+  int page_size, max_pages;
+  cudaStream_t stream;
+};
+bool head_norm_supported(int64_t d, int dtype);
+cudaError_t launch_head_norm(const HeadNormArgs &a);
+
+struct HeadNormBackwardArgs {
+  const void *q, *k, *grad_q, *grad_k;
+  int64_t q_stride, k_stride, gq_stride, gk_stride;
+  int64_t rows, T;
+  int Hq, Hk, d, dtype;
+  const float *q_weight, *k_weight;
+  const int32_t *positions;
+  const double *inv_freq;
+  int rot, interleaved;
+  float eps;
+  void *dq, *dk;               // contiguous
+  float *grad_q_weight, *grad_k_weight;   // [d] or nullptr
+  float *workspace;            // [workspace_rows, d], nullptr without weight gradients
+  int64_t workspace_rows;      // two per CTA
+  cudaStream_t stream;
+};
+int head_norm_backward_ctas();   // CTAs that fill the current device
+cudaError_t launch_head_norm_backward(const HeadNormBackwardArgs &a);
+
+struct PagedArgs {
+  const void *q;               // [B, Hq, d]
+  int64_t q_stride;
+  const void *k_cache, *v_cache;   // [num_pages, Hk, page_size, d]
+  int64_t num_pages;
+  int page_size, max_pages;
+  const int32_t *page_table;   // [B, max_pages]
+  const int32_t *lengths;      // [B]
+  int64_t B;
+  int Hq, Hk, d, dtype;
+  float scale;
+  void *out;                   // [B, Hq, d]
+  float *lse;                  // [B, Hq] or nullptr
+  float *workspace;            // paged_workspace_floats()
+  cudaStream_t stream;
+};
+bool paged_supported(int64_t d, int dtype);
+int paged_ctas();                // CTAs the split runs on the current device
+cudaError_t launch_paged(const PagedArgs &a);
+
+struct LinearArgs {              // out_i = alpha (sum_{j <= i} e^{g (i - j)} (a_i . b_j) c_j + e^{g (i + first_pow)} a_i . first)
+  const void *a, *b, *c;         // [B, T, H, da], [.., da], [.., dc]
+  int64_t a_stride, b_stride, c_stride;   // elements from one token row to the next
+  void *out;                     // [B, T, H, dc], contiguous
+  int64_t B, T;
+  int H, da, dc, dtype;
+  const float *log_decay;        // [H]
+  const int32_t *lengths;        // [B] or nullptr
+  float alpha;
+  bool reverse;                  // i counts from a sequence's last token back
+  const float *first;            // [B, H, da, dc] or nullptr; first_t: stored as [.., dc, da]
+  bool first_t;
+  int first_pow;
+  float first_scale;             // `first` is taken times this
+  float *last;                   // [B, H, da, dc] or nullptr: the state after the last token
+  float last_scale;              // times this ...
+  int last_pow;                  // ... and e^{g last_pow}
+  float *workspace;
+  cudaStream_t stream;
+};
+bool linear_supported(int64_t da, int64_t dc, int dtype);
+// Segments the time axis is cut into, and the fp32 workspace they need.
+int linear_segments(int64_t B, int64_t T, int H, int da, int dc, int dtype);
+int64_t linear_workspace_floats(int64_t B, int64_t T, int H, int da, int dc, int dtype);
+cudaError_t launch_linear(const LinearArgs &a);
+
+struct LinearStepArgs {
+  const void *q, *k, *v;         // [B, H, dk], [B, H, dk], [B, H, dv]
+  int64_t q_stride, k_stride, v_stride;
+  int64_t B;
+  int H, dk, dv, dtype;
+  const float *log_decay;
+  float scale;
+  const float *state;            // [B, H, dk, dv]
+  float *state_out;              // the same, may be `state`
+  void *out;                     // [B, H, dv]
+  cudaStream_t stream;
+};
+cudaError_t launch_linear_step(const LinearStepArgs &a);
+
 // Read and clear the per-file flag that records a kernel wait that ran out
 // (non-zero: at least one wait gave up).
 unsigned int take_error_aggregate();

@@ -1,0 +1,483 @@
+// linear.cu -- linear attention with one decay per head: over prompts
+// (chunked), its gradients, and for single tokens (recurrent).
+//
+// Per sequence and head, with lambda = e^g:
+//   S_t = lambda S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t.
+// Written out, o_t = scale (sum_{s <= t} lambda^{t-s} (q_t . k_s) v_s +
+// lambda^{t+1} S_0^T q_t), one form F(a, b, c; first) = sum_{j <= i}
+// lambda^{i-j} (a_i . b_j) c_j + lambda^{i+1} a_i . first that the gradients
+// share: dq = scale F(do, v, k; S_0^T), and with time running backwards
+// dk = scale F'(v, do, q; dS^T), dv = scale F'(k, q, do; dS), where dS, the
+// gradient of the final state, meets the last token undecayed, and
+// dS_0 = lambda times the state that the last of them ends with.
+//
+// Chunks.  Within a chunk of kC tokens the masked, decayed product matrix
+// P_ij = lambda^{i-j} a_i . b_j is formed once and applied to c; what came
+// before enters through the state.  Decay weights never exceed one: rows are
+// weighted by lambda^{i+1} on the way out and by lambda^{n-1-j} on the way
+// into the state, so a strong decay underflows to zero and nothing overflows.
+//
+// Segments.  The chunks of one (sequence, head) follow one another, so where
+// there are too few of those to fill the GPU the time axis is cut into
+// segments: one kernel forms every segment's own state, a scan turns them
+// into the states that the segments begin with, and the main kernel runs all
+// segments at once.
+#include <type_traits>
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace attnres {
+namespace {
+
+constexpr int kC = 64;                 // tokens per chunk
+constexpr int kThreads = 256;
+constexpr int kNS = 64;                // columns of c a CTA takes
+constexpr int kPadS = kNS + 4;         // row pitch of [.][kNS] tiles (floats)
+constexpr int kMaxDim = 128;
+
+struct LinearParams {
+  const void *a, *b, *c;
+  int64_t a_stride, b_stride, c_stride;
+  void *out;
+  int64_t T, seg_len;
+  int H, da, dc, nseg, slices;
+  const float *log_decay;
+  const int32_t *lengths;
+  float alpha;
+  int reverse;
+  const float *first;
+  int first_t, first_pow;
+  float first_scale;
+  float *last;
+  float last_scale;
+  int last_pow;
+  float *states;                       // [B, H, nseg, da, dc] (nseg > 1)
+};
+
+__device__ __forceinline__ int64_t seq_length(const LinearParams &p, int64_t b) {
+  if (!p.lengths) return p.T;
+  const int64_t n = p.lengths[b];
+  return n < 0 ? 0 : n < p.T ? n : p.T;
+}
+// lambda^n; lambda^0 = 1 whatever g is.
+__device__ __forceinline__ float decay_pow(float g, int64_t n) { return n == 0 ? 1.f : expf(g * (float)n); }
+
+// The first state's element (m, n), scaled.
+__device__ __forceinline__ float first_at(const LinearParams &p, int64_t bh, int m, int n) {
+  const float *f = p.first + bh * p.da * p.dc;
+  return p.first_scale * (p.first_t ? f[(int64_t)n * p.da + m] : f[(int64_t)m * p.dc + n]);
+}
+
+// Token i of the walk (reverse: from the last token back) as a row of the [B, T] axis.
+__device__ __forceinline__ int64_t walk_row(const LinearParams &p, int64_t b, int64_t n, int64_t i) {
+  return b * p.T + (p.reverse ? n - 1 - i : i);
+}
+
+// Rows i0 .. i0 + kC of a [.., H, d] tensor, columns col0 .. col0 + W, to fp32
+// shared memory [kC][pitch]; rows behind `stop` and columns behind d are zero.
+template <typename T, int W>
+__device__ __forceinline__ void load_rows(const LinearParams &p, float *dst, int pitch, const void *src, int64_t stride,
+                                          int h, int d, int col0, int64_t b, int64_t n, int64_t i0, int64_t stop) {
+  constexpr int E = Elt<T>::EPV, V = W / E;
+  for (int k = threadIdx.x; k < kC * V; k += kThreads) {
+    const int r = k / V, c = (k % V) * E;
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (i0 + r < stop && col0 + c < d)
+      v = ld_stream((const T *)src + walk_row(p, b, n, i0 + r) * stride + (int64_t)h * d + col0 + c);
+    float x[E];
+    Elt<T>::unpack(v, x);
+#pragma unroll
+    for (int e = 0; e < E; ++e) dst[r * pitch + c + e] = x[e];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The general kernel: fp32 arithmetic on the CUDA cores, any width up to 128
+// (padded with zeros to DA).  A CTA of 16 x 16 threads owns kNS columns of c
+// and of the state for one segment; each thread forms 4 x 4 elements of every
+// product.  STATES: only the segment's own state is formed.
+// ---------------------------------------------------------------------------
+template <typename T, int DA, bool STATES>
+__global__ void __launch_bounds__(kThreads) linear_general_kernel(const LinearParams p) {
+  constexpr int kPitch = DA + 4, MB = DA / 64;
+  extern __shared__ float4 smem4[];
+  float *sa = reinterpret_cast<float *>(smem4);        // [kC][kPitch]
+  float *sb = sa + kC * kPitch;                        // [kC][kPitch]
+  float *sc = sb + kC * kPitch;                        // [kC][kPadS]
+  float *sp = sc + kC * kPadS;                         // [kC][kPadS]
+  float *ss = sp + kC * kPadS;                         // [DA][kPadS]
+  float *pw = ss + DA * kPadS;                         // [kC + 1]
+  grid_dependency_wait();
+  const int seg = blockIdx.x % p.nseg, slice = blockIdx.x / p.nseg % p.slices;
+  const int64_t bh = blockIdx.x / (p.nseg * p.slices), b = bh / p.H;
+  const int h = (int)(bh % p.H), col0 = slice * kNS;
+  const int64_t n = seq_length(p, b);
+  const int64_t begin = seg * p.seg_len, end = min(p.T, begin + p.seg_len), stop = min(n, end);
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  const float g = p.log_decay[h];
+  if (threadIdx.x <= kC) pw[threadIdx.x] = decay_pow(g, threadIdx.x);
+
+  float s[MB * 4][4];                                  // state rows mb * 64 + ty * 4 + i, columns tx * 4 + j
+  float *states = p.states + ((bh * p.nseg + seg) * p.da) * p.dc;
+#pragma unroll
+  for (int m = 0; m < MB * 4; ++m) {
+    const int row = (m / 4) * 64 + ty * 4 + m % 4;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int col = col0 + tx * 4 + j;
+      s[m][j] = 0.f;
+      if (!STATES && row < p.da && col < p.dc) {
+        if (p.nseg > 1) s[m][j] = states[(int64_t)row * p.dc + col];
+        else if (p.first) s[m][j] = first_at(p, bh, row, col);
+      }
+    }
+  }
+  for (int64_t i0 = begin; i0 < stop; i0 += kC) {
+    const int len = (int)min((int64_t)kC, stop - i0);
+    const int lead = (i0 == 0) ? p.first_pow : 1;      // the first row's weight of the state: lambda^lead
+    __syncthreads();                                   // the last chunk's tiles are read
+    if (!STATES) load_rows<T, DA>(p, sa, kPitch, p.a, p.a_stride, h, p.da, 0, b, n, i0, stop);
+    load_rows<T, DA>(p, sb, kPitch, p.b, p.b_stride, h, p.da, 0, b, n, i0, stop);
+    load_rows<T, kNS>(p, sc, kPadS, p.c, p.c_stride, h, p.dc, col0, b, n, i0, stop);
+    if (!STATES) {
+#pragma unroll
+      for (int m = 0; m < MB * 4; ++m) {
+        const int row = (m / 4) * 64 + ty * 4 + m % 4;
+        *reinterpret_cast<float4 *>(ss + row * kPadS + tx * 4) = make_float4(s[m][0], s[m][1], s[m][2], s[m][3]);
+      }
+    }
+    __syncthreads();
+    if (!STATES) {
+      // P: rows ty + 16 i, columns tx + 16 j
+      float acc[4][4] = {};
+#pragma unroll 4
+      for (int k = 0; k < DA; k += 4) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(sa + (ty + 16 * i) * kPitch + k);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4 *>(sb + (tx + 16 * j) * kPitch + k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            acc[i][j] = fmaf(x[i].x, y[j].x, fmaf(x[i].y, y[j].y, fmaf(x[i].z, y[j].z, fmaf(x[i].w, y[j].w, acc[i][j]))));
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int r = ty + 16 * i, c = tx + 16 * j;
+          sp[r * kPadS + c] = r >= c ? acc[i][j] * pw[r - c] : 0.f;
+        }
+      __syncthreads();
+      // rows ty * 4 + i, columns tx * 4 + j: the state's part, weighted by row, then the chunk's own
+      float o[4][4] = {};
+#pragma unroll 4
+      for (int k = 0; k < DA; k += 4) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(sa + (ty * 4 + i) * kPitch + k);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4 *>(ss + (k + j) * kPadS + tx * 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            o[i][0] = fmaf(xs[j], y[j].x, o[i][0]);
+            o[i][1] = fmaf(xs[j], y[j].y, o[i][1]);
+            o[i][2] = fmaf(xs[j], y[j].z, o[i][2]);
+            o[i][3] = fmaf(xs[j], y[j].w, o[i][3]);
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][j] *= pw[ty * 4 + i + lead];
+#pragma unroll 4
+      for (int k = 0; k < kC; k += 4) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(sp + (ty * 4 + i) * kPadS + k);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4 *>(sc + (k + j) * kPadS + tx * 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            o[i][0] = fmaf(xs[j], y[j].x, o[i][0]);
+            o[i][1] = fmaf(xs[j], y[j].y, o[i][1]);
+            o[i][2] = fmaf(xs[j], y[j].z, o[i][2]);
+            o[i][3] = fmaf(xs[j], y[j].w, o[i][3]);
+          }
+        }
+      }
+      const int col = col0 + tx * 4;
+      if (col < p.dc) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = ty * 4 + i;
+          if (r >= len) continue;
+          T *y = (T *)p.out + (walk_row(p, b, n, i0 + r) * p.H + h) * p.dc + col;
+          float z[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) z[j] = o[i][j] * p.alpha;
+          if constexpr (std::is_same<T, float>::value)
+            *reinterpret_cast<float4 *>(y) = make_float4(z[0], z[1], z[2], z[3]);
+          else
+            *reinterpret_cast<uint2 *>(y) = make_uint2(Elt<T>::pack_word(z[0], z[1]), Elt<T>::pack_word(z[2], z[3]));
+        }
+      }
+    }
+    // S = lambda^len S + sum_j lambda^{len-1-j} b_j c_j^T
+    const float keep = decay_pow(g, len - 1 + lead);
+#pragma unroll
+    for (int m = 0; m < MB * 4; ++m)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[m][j] *= keep;
+#pragma unroll 4
+    for (int k = 0; k < len; ++k) {
+      float4 y = *reinterpret_cast<const float4 *>(sc + k * kPadS + tx * 4);
+      const float wk = pw[len - 1 - k];
+      y.x *= wk; y.y *= wk; y.z *= wk; y.w *= wk;
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) {
+        const float4 x = *reinterpret_cast<const float4 *>(sb + k * kPitch + mb * 64 + ty * 4);
+        const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[mb * 4 + i][0] = fmaf(xs[i], y.x, s[mb * 4 + i][0]);
+          s[mb * 4 + i][1] = fmaf(xs[i], y.y, s[mb * 4 + i][1]);
+          s[mb * 4 + i][2] = fmaf(xs[i], y.z, s[mb * 4 + i][2]);
+          s[mb * 4 + i][3] = fmaf(xs[i], y.w, s[mb * 4 + i][3]);
+        }
+      }
+    }
+  }
+  const bool write_last = !STATES && p.nseg == 1 && p.last;
+  if (STATES || write_last) {
+    float *dst = STATES ? states : p.last + bh * p.da * p.dc;
+    // no token at all: the state passes through unchanged
+    const float f = STATES ? 1.f : p.last_scale * (n > 0 ? decay_pow(g, p.last_pow) : 1.f);
+#pragma unroll
+    for (int m = 0; m < MB * 4; ++m) {
+      const int row = (m / 4) * 64 + ty * 4 + m % 4;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int col = col0 + tx * 4 + j;
+        if (row < p.da && col < p.dc) dst[(int64_t)row * p.dc + col] = s[m][j] * f;
+      }
+    }
+  }
+  if (!STATES) {
+    // rows behind the sequence are zero
+    const int64_t from = max(stop, begin);
+    const int w = min(kNS, p.dc - col0);
+    for (int64_t k = threadIdx.x; k < (end - from) * w; k += kThreads)
+      ((T *)p.out)[((b * p.T + from + k / w) * p.H + h) * p.dc + col0 + k % w] = T(0.f);
+  }
+}
+
+// The segments' own states become the states they begin with; the state
+// after the last token is written where it is wanted.  One thread per element.
+__global__ void __launch_bounds__(kThreads) linear_scan_kernel(const LinearParams p) {
+  grid_dependency_wait();
+  const int per = p.da * p.dc;
+  const int64_t bh = blockIdx.y;
+  const int e = blockIdx.x * kThreads + threadIdx.x;
+  if (e >= per) return;
+  const int64_t n = seq_length(p, bh / p.H);
+  const float g = p.log_decay[bh % p.H];
+  float cur = p.first ? first_at(p, bh, e / p.dc, e % p.dc) : 0.f;
+  float *st = p.states + bh * p.nseg * per + e;
+  const float full = decay_pow(g, p.seg_len);
+  float next = st[0];
+  for (int s = 0; s < p.nseg; ++s) {
+    const float own = next;
+    if (s + 1 < p.nseg) next = st[(int64_t)(s + 1) * per];
+    st[(int64_t)s * per] = cur;
+    const int64_t len = min(p.T, (s + 1) * p.seg_len) - s * p.seg_len, left = n - s * p.seg_len;
+    if (left <= 0) continue;
+    if (s > 0 && left >= p.seg_len && len == p.seg_len) cur = fmaf(cur, full, own);
+    else cur = fmaf(cur, decay_pow(g, min(len, left) - (s == 0 ? 1 - p.first_pow : 0)), own);
+  }
+  if (p.last) p.last[bh * per + e] = cur * p.last_scale * (n > 0 ? decay_pow(g, p.last_pow) : 1.f);
+}
+
+// ---------------------------------------------------------------------------
+// One token: S' = lambda S + k v^T, o = scale S'^T q.  Bound by the state,
+// read and written once.  A CTA takes `cols` columns of one (sequence, head)
+// and all its rows, four columns per thread; the row groups' parts of o meet
+// in shared memory.
+// ---------------------------------------------------------------------------
+struct StepParams {
+  const void *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride;
+  int H, dk, dv, cols;
+  const float *log_decay;
+  float scale;
+  const float *state;
+  float *state_out;
+  void *out;
+};
+
+template <typename T>
+__device__ __forceinline__ float elt_at(const T *x, int64_t i) {
+  if constexpr (std::is_same<T, float>::value) return x[i];
+  else return __bfloat162float(x[i]);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) linear_step_kernel(const StepParams p) {
+  constexpr int RPT = 4;                               // rows in flight per thread
+  __shared__ float sq[kMaxDim], sk[kMaxDim];
+  __shared__ float4 red[kThreads];
+  grid_dependency_wait();
+  const int64_t bh = blockIdx.x, b = bh / p.H;
+  const int h = (int)(bh % p.H);
+  const int lanes = p.cols / 4, groups = kThreads / lanes;
+  const int lane = threadIdx.x % lanes, grp = threadIdx.x / lanes;
+  const int col = blockIdx.y * p.cols + lane * 4;
+  const bool active = grp < groups && col < p.dv;
+  const float lam = expf(p.log_decay[h]);
+  if (threadIdx.x < p.dk) {
+    sq[threadIdx.x] = elt_at((const T *)p.q, b * p.q_stride + (int64_t)h * p.dk + threadIdx.x);
+    sk[threadIdx.x] = elt_at((const T *)p.k, b * p.k_stride + (int64_t)h * p.dk + threadIdx.x);
+  }
+  float v[4] = {};
+  if (active) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = elt_at((const T *)p.v, b * p.v_stride + (int64_t)h * p.dv + col + j);
+  }
+  __syncthreads();
+  float o[4] = {};
+  const float *src = p.state + bh * p.dk * p.dv + col;
+  float *dst = p.state_out + bh * p.dk * p.dv + col;
+  if (active) {
+    for (int r0 = grp; r0 < p.dk; r0 += groups * RPT) {
+      float4 s[RPT];
+#pragma unroll
+      for (int i = 0; i < RPT; ++i) {
+        const int r = r0 + i * groups;
+        if (r < p.dk) s[i] = *reinterpret_cast<const float4 *>(src + (int64_t)r * p.dv);
+      }
+#pragma unroll
+      for (int i = 0; i < RPT; ++i) {
+        const int r = r0 + i * groups;
+        if (r >= p.dk) continue;
+        const float kr = sk[r], qr = sq[r];
+        s[i].x = fmaf(lam, s[i].x, kr * v[0]);
+        s[i].y = fmaf(lam, s[i].y, kr * v[1]);
+        s[i].z = fmaf(lam, s[i].z, kr * v[2]);
+        s[i].w = fmaf(lam, s[i].w, kr * v[3]);
+        o[0] = fmaf(qr, s[i].x, o[0]);
+        o[1] = fmaf(qr, s[i].y, o[1]);
+        o[2] = fmaf(qr, s[i].z, o[2]);
+        o[3] = fmaf(qr, s[i].w, o[3]);
+        *reinterpret_cast<float4 *>(dst + (int64_t)r * p.dv) = s[i];
+      }
+    }
+  }
+  red[threadIdx.x] = make_float4(o[0], o[1], o[2], o[3]);
+  __syncthreads();
+  if (threadIdx.x < lanes && active) {
+    float4 t = red[threadIdx.x];
+    for (int k = 1; k < groups; ++k) {
+      const float4 x = red[k * lanes + threadIdx.x];
+      t.x += x.x; t.y += x.y; t.z += x.z; t.w += x.w;
+    }
+    T *y = (T *)p.out + bh * p.dv + col;
+    t.x *= p.scale; t.y *= p.scale; t.z *= p.scale; t.w *= p.scale;
+    if constexpr (std::is_same<T, float>::value) *reinterpret_cast<float4 *>(y) = t;
+    else *reinterpret_cast<uint2 *>(y) = make_uint2(Elt<T>::pack_word(t.x, t.y), Elt<T>::pack_word(t.z, t.w));
+  }
+}
+
+int general_slices(int dc) { return (dc + kNS - 1) / kNS; }
+
+template <typename K>
+cudaError_t launch_big(K kern, int64_t ctas, size_t smem, cudaStream_t st, const LinearParams &p) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kern, dim3((unsigned)ctas), dim3(kThreads), smem, st, p);
+}
+
+}  // namespace
+
+bool linear_supported(int64_t da, int64_t dc, int dtype) {
+  const int e = dtype == ATTNRES_BF16 ? 8 : 4;
+  return da >= e && dc >= e && da <= kMaxDim && dc <= kMaxDim && da % e == 0 && dc % e == 0;
+}
+
+// Segments: enough CTAs for two per SM, but none shorter than 256 tokens (a
+// segment's state costs as much traffic as about 128 tokens).
+int linear_segments(int64_t B, int64_t T, int H, int da, int dc, int dtype) {
+  (void)da;
+  (void)dtype;
+  const int64_t have = B * H * general_slices(dc), want = 2 * (int64_t)sm_count();
+  int64_t n = have > 0 ? (want + have - 1) / have : 1;
+  const int64_t most = T / 256;
+  if (n > most) n = most;
+  return n < 1 ? 1 : (int)n;
+}
+
+int64_t linear_workspace_floats(int64_t B, int64_t T, int H, int da, int dc, int dtype) {
+  const int n = linear_segments(B, T, H, da, dc, dtype);
+  return n > 1 ? B * H * n * da * dc : 0;
+}
+
+cudaError_t launch_linear(const LinearArgs &a) {
+  LinearParams p{};
+  p.a = a.a; p.b = a.b; p.c = a.c;
+  p.a_stride = a.a_stride; p.b_stride = a.b_stride; p.c_stride = a.c_stride;
+  p.out = a.out; p.T = a.T; p.H = a.H; p.da = a.da; p.dc = a.dc;
+  p.slices = general_slices(a.dc);
+  p.nseg = linear_segments(a.B, a.T, a.H, a.da, a.dc, a.dtype);
+  p.seg_len = (a.T + p.nseg - 1) / p.nseg;
+  p.seg_len = a.T > 0 ? (p.seg_len + kC - 1) / kC * kC : kC;
+  p.nseg = a.T > 0 ? (int)((a.T + p.seg_len - 1) / p.seg_len) : 1;
+  p.log_decay = a.log_decay; p.lengths = a.lengths; p.alpha = a.alpha; p.reverse = a.reverse;
+  p.first = a.first; p.first_t = a.first_t; p.first_pow = a.first_pow; p.first_scale = a.first_scale;
+  p.last = a.last; p.last_scale = a.last_scale; p.last_pow = a.last_pow;
+  p.states = a.workspace;
+  const int64_t ctas = a.B * a.H * p.nseg * p.slices;
+  auto go = [&](auto elt, auto da) -> cudaError_t {
+    using T = decltype(elt);
+    constexpr int DA = decltype(da)::value;
+    const size_t smem = (size_t)(2 * kC * (DA + 4) + 2 * kC * kPadS + DA * kPadS + kC + 4) * sizeof(float);
+    if (p.nseg > 1) {
+      cudaError_t e = launch_big(linear_general_kernel<T, DA, true>, ctas, smem, a.stream, p);
+      if (e != cudaSuccess) return e;
+      e = launch_dependent(linear_scan_kernel, dim3((unsigned)((a.da * a.dc + kThreads - 1) / kThreads), (unsigned)(a.B * a.H)),
+                           dim3(kThreads), 0, a.stream, p);
+      if (e != cudaSuccess) return e;
+    }
+    return launch_big(linear_general_kernel<T, DA, false>, ctas, smem, a.stream, p);
+  };
+  auto with_da = [&](auto elt) -> cudaError_t {
+    return a.da <= 64 ? go(elt, std::integral_constant<int, 64>{}) : go(elt, std::integral_constant<int, 128>{});
+  };
+  return a.dtype == ATTNRES_BF16 ? with_da(__nv_bfloat16{}) : with_da(float{});
+}
+
+cudaError_t launch_linear_step(const LinearStepArgs &a) {
+  StepParams p{};
+  p.q = a.q; p.k = a.k; p.v = a.v;
+  p.q_stride = a.q_stride; p.k_stride = a.k_stride; p.v_stride = a.v_stride;
+  p.H = a.H; p.dk = a.dk; p.dv = a.dv;
+  p.log_decay = a.log_decay; p.scale = a.scale; p.state = a.state; p.state_out = a.state_out; p.out = a.out;
+  // Whole rows of the state while the (sequence, head) pairs fill the SMs,
+  // else slices of 32 columns (128 bytes of a row).
+  p.cols = a.dv;
+  if (a.B * a.H < 2 * (int64_t)sm_count() && a.dv > 32) p.cols = 32;
+  const dim3 grid((unsigned)(a.B * a.H), (unsigned)((a.dv + p.cols - 1) / p.cols));
+  return a.dtype == ATTNRES_BF16
+             ? launch_dependent(linear_step_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, a.stream, p)
+             : launch_dependent(linear_step_kernel<float>, grid, dim3(kThreads), 0, a.stream, p);
+}
+
+}  // namespace attnres
