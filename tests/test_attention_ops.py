@@ -289,6 +289,23 @@ def test_paged(gpu, dtype, Hq, Hk, d, page, lengths):
 
 
 @gpu_only
+@pytest.mark.parametrize("dtype,B,Hq,Hk,d,page,longest,seed", [
+    (BF, 400, 2, 1, 64, 16, 300, 1), (BF, 90, 4, 4, 128, 32, 900, 2), (F32, 200, 3, 1, 64, 16, 200, 3),
+    (BF, 1000, 1, 1, 32, 1, 70, 4), (BF, 3, 16, 4, 256, 64, 9000, 5), (F32, 2, 5, 5, 96, 64, 4000, 6)])
+def test_paged_ragged_batches(gpu, dtype, B, Hq, Hk, d, page, longest, seed):
+    # pairs cut at any place, whole ones, empty sequences in a row, more CTAs than tiles and fewer
+    rng = torch.Generator().manual_seed(seed)
+    lengths = torch.randint(0, longest + 1, (B,), generator=rng)
+    lengths[torch.rand(B, generator=rng) < 0.3] = 0
+    lengths[-1] = longest
+    q, kc, vc, table, n, scale = paged_inputs(gpu, dtype, B, Hq, Hk, d, page, lengths.tolist(), seed)
+    out, lse = api.paged_attention(q, kc, vc, table, n, scale)
+    want, wlse, tol, ltol = paged_ref(q, kc, vc, table, n, scale)
+    within(out, want, U[dtype] * want.abs() + tol, "out")
+    within(lse, wlse, ltol, "lse")
+
+
+@gpu_only
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_paged_unused_cache_is_never_used(gpu, dtype):
     lengths = [0, 5, 64, 100, 129]

@@ -180,7 +180,7 @@ int64_t attnres_paged_attention_workspace_bytes(int Hq, int Hk, int64_t d, int d
   if (Hk < 1 || Hq < Hk || Hq > kMaxHeads || Hq % Hk || Hq / Hk > kMaxGroup || d < 1) return ATTNRES_ERR_SHAPE;
   if (d % vec_elems(dtype)) return ATTNRES_ERR_ALIGNMENT;
   if (!paged_supported(d, dtype)) return ATTNRES_ERR_SHAPE;
-  return (int64_t)paged_ctas() * 2 * (Hq / Hk) * (d + 1) * 4;
+  return paged_workspace_bytes(Hq / Hk, d, dtype);
 }
 
 int attnres_paged_attention(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
@@ -205,7 +205,7 @@ int attnres_paged_attention(const void *q, int64_t q_stride, const void *k_cache
   a.q = q; a.q_stride = q_stride; a.k_cache = k_cache; a.v_cache = v_cache; a.num_pages = num_pages;
   a.page_size = page_size; a.max_pages = num_pages > 0 ? max_pages : 0; a.page_table = page_table; a.lengths = lengths;
   a.B = B; a.Hq = Hq; a.Hk = Hk; a.d = (int)d; a.dtype = dtype; a.scale = scale; a.out = out; a.lse = lse;
-  a.workspace = static_cast<float *>(workspace); a.stream = static_cast<cudaStream_t>(stream);
+  a.workspace = workspace; a.stream = static_cast<cudaStream_t>(stream);
   return cuda_status(launch_paged(a));
 }
 

@@ -229,11 +229,13 @@ struct PagedArgs {
   float scale;
   void *out;                   // [B, Hq, d]
   float *lse;                  // [B, Hq] or nullptr
-  float *workspace;            // paged_workspace_floats()
+  void *workspace;             // paged_workspace_bytes()
   cudaStream_t stream;
 };
 bool paged_supported(int64_t d, int dtype);
-int paged_ctas();                // CTAs the split runs on the current device
+// CTAs the split runs on the current device, and the workspace they need.
+int paged_ctas(int64_t d, int dtype);
+int64_t paged_workspace_bytes(int G, int64_t d, int dtype);
 cudaError_t launch_paged(const PagedArgs &a);
 
 struct LinearArgs {              // out_i = alpha (sum_{j <= i} e^{g (i - j)} (a_i . b_j) c_j + e^{g (i + first_pow)} a_i . first)
