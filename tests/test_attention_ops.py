@@ -431,6 +431,9 @@ LINEAR = [  # dtype, B, T, H, dk, dv, ragged lengths or None, with a state
     (BF, 1, 65, 1, 128, 64, None, False), (BF, 3, 200, 2, 64, 128, [200, 0, 77], True),
     (BF, 2, 129, 4, 96, 80, [64, 129], False), (BF, 1, 1500, 2, 128, 128, None, True),
     (BF, 2, 700, 1, 16, 24, [700, 300], True), (BF, 5, 130, 2, 8, 8, [1, 2, 128, 129, 130], True),
+    # several segments of the time axis, cut sequences in some of them, an empty last segment
+    (BF, 1, 2100, 2, 128, 128, None, True), (BF, 2, 1300, 3, 128, 96, [1300, 700], True),
+    (BF, 2, 1000, 2, 72, 128, [100, 993], False), (BF, 40, 64, 5, 128, 128, None, False),
     (F32, 1, 100, 2, 128, 128, None, True), (F32, 2, 1100, 1, 64, 64, [1100, 513], True),
     (F32, 1, 70, 3, 100, 4, None, False), (F32, 3, 5, 1, 4, 12, [0, 5, 3], True),
 ]

@@ -284,5 +284,6 @@ unsigned int take_error_aggregate();
 unsigned int take_error_merge();
 unsigned int take_error_phase1();
 unsigned int take_error_phase1_tc();
+unsigned int take_error_linear();
 
 }  // namespace attnres

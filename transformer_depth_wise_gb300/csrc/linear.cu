@@ -24,55 +24,16 @@
 // segments at once.
 #include <type_traits>
 
-#include "common.cuh"
-#include "launch.h"
+#include "linear.cuh"
 
 namespace attnres {
 namespace {
 
-constexpr int kC = 64;                 // tokens per chunk
+constexpr int kC = kChunk;             // tokens per chunk
 constexpr int kThreads = 256;
 constexpr int kNS = 64;                // columns of c a CTA takes
 constexpr int kPadS = kNS + 4;         // row pitch of [.][kNS] tiles (floats)
 constexpr int kMaxDim = 128;
-
-struct LinearParams {
-  const void *a, *b, *c;
-  int64_t a_stride, b_stride, c_stride;
-  void *out;
-  int64_t T, seg_len;
-  int H, da, dc, nseg, slices;
-  const float *log_decay;
-  const int32_t *lengths;
-  float alpha;
-  int reverse;
-  const float *first;
-  int first_t, first_pow;
-  float first_scale;
-  float *last;
-  float last_scale;
-  int last_pow;
-  float *states;                       // [B, H, nseg, da, dc] (nseg > 1)
-};
-
-__device__ __forceinline__ int64_t seq_length(const LinearParams &p, int64_t b) {
-  if (!p.lengths) return p.T;
-  const int64_t n = p.lengths[b];
-  return n < 0 ? 0 : n < p.T ? n : p.T;
-}
-// lambda^n; lambda^0 = 1 whatever g is.
-__device__ __forceinline__ float decay_pow(float g, int64_t n) { return n == 0 ? 1.f : expf(g * (float)n); }
-
-// The first state's element (m, n), scaled.
-__device__ __forceinline__ float first_at(const LinearParams &p, int64_t bh, int m, int n) {
-  const float *f = p.first + bh * p.da * p.dc;
-  return p.first_scale * (p.first_t ? f[(int64_t)n * p.da + m] : f[(int64_t)m * p.dc + n]);
-}
-
-// Token i of the walk (reverse: from the last token back) as a row of the [B, T] axis.
-__device__ __forceinline__ int64_t walk_row(const LinearParams &p, int64_t b, int64_t n, int64_t i) {
-  return b * p.T + (p.reverse ? n - 1 - i : i);
-}
 
 // Rows i0 .. i0 + kC of a [.., H, d] tensor, columns col0 .. col0 + W, to fp32
 // shared memory [kC][pitch]; rows behind `stop` and columns behind d are zero.
@@ -413,13 +374,15 @@ bool linear_supported(int64_t da, int64_t dc, int dtype) {
   return da >= e && dc >= e && da <= kMaxDim && dc <= kMaxDim && da % e == 0 && dc % e == 0;
 }
 
-// Segments: enough CTAs for two per SM, but none shorter than 256 tokens (a
-// segment's state costs as much traffic as about 128 tokens).
+// Segments of the general kernel: enough CTAs for two per SM, but none
+// shorter than 256 tokens (a segment's state costs as much traffic as about
+// 128 tokens).
 int linear_segments(int64_t B, int64_t T, int H, int da, int dc, int dtype) {
   (void)da;
-  (void)dtype;
+  if (B * H < 1) return 1;
+  if (linear_tc_supported(T, dtype)) return linear_tc_segments(B * H, T);
   const int64_t have = B * H * general_slices(dc), want = 2 * (int64_t)sm_count();
-  int64_t n = have > 0 ? (want + have - 1) / have : 1;
+  int64_t n = (want + have - 1) / have;
   const int64_t most = T / 256;
   if (n > most) n = most;
   return n < 1 ? 1 : (int)n;
@@ -444,24 +407,33 @@ cudaError_t launch_linear(const LinearArgs &a) {
   p.first = a.first; p.first_t = a.first_t; p.first_pow = a.first_pow; p.first_scale = a.first_scale;
   p.last = a.last; p.last_scale = a.last_scale; p.last_pow = a.last_pow;
   p.states = a.workspace;
-  const int64_t ctas = a.B * a.H * p.nseg * p.slices;
-  auto go = [&](auto elt, auto da) -> cudaError_t {
-    using T = decltype(elt);
-    constexpr int DA = decltype(da)::value;
-    const size_t smem = (size_t)(2 * kC * (DA + 4) + 2 * kC * kPadS + DA * kPadS + kC + 4) * sizeof(float);
-    if (p.nseg > 1) {
-      cudaError_t e = launch_big(linear_general_kernel<T, DA, true>, ctas, smem, a.stream, p);
-      if (e != cudaSuccess) return e;
-      e = launch_dependent(linear_scan_kernel, dim3((unsigned)((a.da * a.dc + kThreads - 1) / kThreads), (unsigned)(a.B * a.H)),
-                           dim3(kThreads), 0, a.stream, p);
-      if (e != cudaSuccess) return e;
-    }
-    return launch_big(linear_general_kernel<T, DA, false>, ctas, smem, a.stream, p);
+  p.wait_limit = wait_limit_cycles();
+  const int64_t BH = a.B * a.H;
+  const bool tc = linear_tc_supported(a.T, a.dtype);
+  // The states' kernel (states = true) or the main one.
+  auto chunks = [&](bool states) -> cudaError_t {
+    if (tc) return launch_linear_tc(p, BH, states, a.stream);
+    const int64_t ctas = BH * p.nseg * p.slices;
+    auto go = [&](auto elt, auto da) -> cudaError_t {
+      using T = decltype(elt);
+      constexpr int DA = decltype(da)::value;
+      const size_t smem = (size_t)(2 * kC * (DA + 4) + 2 * kC * kPadS + DA * kPadS + kC + 4) * sizeof(float);
+      return states ? launch_big(linear_general_kernel<T, DA, true>, ctas, smem, a.stream, p)
+                    : launch_big(linear_general_kernel<T, DA, false>, ctas, smem, a.stream, p);
+    };
+    auto with_da = [&](auto elt) -> cudaError_t {
+      return a.da <= 64 ? go(elt, std::integral_constant<int, 64>{}) : go(elt, std::integral_constant<int, 128>{});
+    };
+    return a.dtype == ATTNRES_BF16 ? with_da(__nv_bfloat16{}) : with_da(float{});
   };
-  auto with_da = [&](auto elt) -> cudaError_t {
-    return a.da <= 64 ? go(elt, std::integral_constant<int, 64>{}) : go(elt, std::integral_constant<int, 128>{});
-  };
-  return a.dtype == ATTNRES_BF16 ? with_da(__nv_bfloat16{}) : with_da(float{});
+  if (p.nseg > 1) {
+    cudaError_t e = chunks(true);
+    if (e != cudaSuccess) return e;
+    e = launch_dependent(linear_scan_kernel, dim3((unsigned)((a.da * a.dc + kThreads - 1) / kThreads), (unsigned)BH),
+                         dim3(kThreads), 0, a.stream, p);
+    if (e != cudaSuccess) return e;
+  }
+  return chunks(false);
 }
 
 cudaError_t launch_linear_step(const LinearStepArgs &a) {

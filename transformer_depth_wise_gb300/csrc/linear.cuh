@@ -1,0 +1,58 @@
+// linear.cuh -- what the linear-attention kernels share: a launch's
+// parameters, the sequences' lengths, decay powers, first states.
+#pragma once
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace attnres {
+
+struct LinearParams {
+  const void *a, *b, *c;
+  int64_t a_stride, b_stride, c_stride;
+  void *out;
+  int64_t T, seg_len;
+  int H, da, dc, nseg, slices;         // slices: CTAs over the columns of c (general kernel)
+  const float *log_decay;
+  const int32_t *lengths;
+  float alpha;
+  int reverse;
+  const float *first;
+  int first_t, first_pow;
+  float first_scale;
+  float *last;
+  float last_scale;
+  int last_pow;
+  float *states;                       // [B, H, nseg, da, dc] (nseg > 1)
+  long long wait_limit;                // SM clock cycles any wait of the tensor-core kernel may take
+};
+
+__device__ __forceinline__ int64_t seq_length(const LinearParams &p, int64_t b) {
+  if (!p.lengths) return p.T;
+  const int64_t n = p.lengths[b];
+  return n < 0 ? 0 : n < p.T ? n : p.T;
+}
+// lambda^n; lambda^0 = 1 whatever g is.
+__device__ __forceinline__ float decay_pow(float g, int64_t n) { return n == 0 ? 1.f : expf(g * (float)n); }
+
+// The first state's element (m, n), scaled.
+__device__ __forceinline__ float first_at(const LinearParams &p, int64_t bh, int m, int n) {
+  const float *f = p.first + bh * p.da * p.dc;
+  return p.first_scale * (p.first_t ? f[(int64_t)n * p.da + m] : f[(int64_t)m * p.dc + n]);
+}
+
+// Token i of the walk (reverse: from the last token back) as a row of the [B, T] axis.
+__device__ __forceinline__ int64_t walk_row(const LinearParams &p, int64_t b, int64_t n, int64_t i) {
+  return b * p.T + (p.reverse ? n - 1 - i : i);
+}
+
+// Segments hold whole chunks of 64 tokens.
+constexpr int kChunk = 64;
+
+// The tensor-core form (bf16): its segments, and the launches of the states'
+// kernel and of the main one.
+bool linear_tc_supported(int64_t T, int dtype);
+int linear_tc_segments(int64_t BH, int64_t T);
+cudaError_t launch_linear_tc(const LinearParams &p, int64_t BH, bool states, cudaStream_t stream);
+
+}  // namespace attnres
