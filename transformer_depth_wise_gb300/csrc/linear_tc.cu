@@ -17,15 +17,19 @@
 // outputs are rounded to bf16 once: each adds an error of the size of the
 // output's own rounding at most.
 //
-// Roles of a CTA, one per SM: eight worker warps, two warps that copy tiles
+// Roles of a CTA, one per SM (a warpgroup of four warps each, but for the
+// last): the state (a thread per row of S, all its columns in registers); two
+// for the weighted parts; P; the outputs; and three warps that copy tiles
 // (cp.async, 16 bytes a lane, straight into the swizzled layout, rows behind
 // the sequence and columns behind the width as zeros; tensor-map copies are
 // served one box at a time per CTA and would cap one CTA per SM at about
-// 4.2 TB/s), one thread that issues the products.  Tensor memory holds P, the
-// update of S, and two pairs of output accumulators.  Workers, per chunk c:
-// split w c (starts the update of S), form P (starts c^T P^T), store the
-// outputs of chunk c - 1, then S (starts S^T a^T of chunk c + 1); so the
-// products run beside the next piece of the workers' work.
+// 4.2 TB/s) beside the thread that issues the products.  A warp runs its
+// dependent instructions one in five cycles or so, so what counts is how few
+// instructions each role needs per chunk, and that the roles run side by side
+// on code short enough for the instruction cache: with eight warps doing all
+// of the work in turn a chunk took 7900 cycles, 3.4 us.  Tensor memory holds
+// P, the update of S, and two pairs of output accumulators.  Order of the
+// products: update(c), S^T a^T (c), c^T P^T (c), a b^T (c + 1).
 //
 // Every wait is bounded: one that runs out records a flag and an abort mark
 // in shared memory, on which every other wait returns at once; the issuing
@@ -39,30 +43,53 @@ namespace attnres {
 namespace {
 
 constexpr int kC = kChunk;
-constexpr int kWorkers = 8, kCopiers = 2;             // warps
-constexpr int kMmaWarp = kWorkers + kCopiers;
-constexpr int kThreads = (kMmaWarp + 1) * 32;
-constexpr int kCopyThreads = kCopiers * 32;
 constexpr uint32_t kTile = kC * 128 * 2;              // bytes: 64 tokens x 128 columns, two blocks of 64 columns
 constexpr uint32_t kBlock = kTile / 2;
+constexpr uint32_t kHalf = 32 * 128;                  // 32 tokens of a block
 constexpr uint32_t kSBlock = 128 * 128;               // 64 columns of S's 128 rows
-constexpr int kOutPitch = 320;                        // bytes per token of the output staging (no bank met twice)
+constexpr int kOutPitch = 272;                        // bytes per token of the output staging (no bank met twice)
+constexpr int kCopiers = 3;                           // warps
 
-// Tensor memory columns (main kernel): P, update of S, outputs by parity.
-constexpr uint32_t kColP = 0, kColKV = 64, kColInter = 192, kColIntra = 320;
-
-template <bool STATES> struct Smem {
-  static constexpr uint32_t kStage = (STATES ? 2 : 3) * kTile;      // [a], b, c
-  static constexpr uint32_t kOffParts = 2 * kStage;                 // STATES: the first part replaces c itself
-  static constexpr uint32_t kOffP = kOffParts + (STATES ? 2 : 3) * kTile;
+// The main kernel's warpgroups: S, parts, parts, P, outputs, copies + products;
+// the states' kernel: S, parts, parts, copies + products.
+template <bool STATES> struct Shape {
+  static constexpr int kGroups = STATES ? 4 : 6;
+  static constexpr int kThreads = kGroups * 128;
+  static constexpr int kStages = STATES ? 4 : 2;
+  // Registers per thread: as launched (checked at the launch), then each
+  // role's share; their sum stays within the launch's.
+  static constexpr int kRegs = STATES ? 128 : 80;
+  static constexpr int kRegsS = STATES ? 184 : 168, kRegsParts = STATES ? 96 : 56, kRegsP = 72, kRegsOut = 88,
+                       kRegsCopy = STATES ? 96 : 40;
+  static_assert(kRegsS + 2 * kRegsParts + (STATES ? 0 : kRegsP + kRegsOut) + kRegsCopy <= kGroups * kRegs,
+                "more registers than the launch has");
+  static constexpr uint32_t kStage = (STATES ? 2 : 3) * kTile;      // b, c, [a]
+  static constexpr uint32_t kOffParts = kStages * kStage;
+  static constexpr uint32_t kOffP = kOffParts + 3 * kTile;
   static constexpr uint32_t kOffS = kOffP + (STATES ? 0 : kC * 128);
   static constexpr uint32_t kOffOut = kOffS + (STATES ? 0 : 2 * kSBlock);
   static constexpr uint32_t kOffPow = kOffOut + (STATES ? 0 : kC * kOutPitch);
-  static constexpr uint32_t kOffBar = kOffPow + 68 * 4;
-  static constexpr uint32_t kBytes = kOffBar + 16 * 8 + 1024;       // and the alignment's slack
+  static constexpr uint32_t kOffBar = kOffPow + 72 * 4;
+  static constexpr uint32_t kBytes = kOffBar + 26 * 8 + 1024;       // and the alignment's slack
 };
 
-enum Bar { kFull0, kFull1, kEmpty0, kEmpty1, kQK, kS, kV, kKV, kP, kPV, kDrain, kBars };
+// Tensor memory columns: the update of S first; P, outputs by parity.
+constexpr uint32_t kColKV = 0, kColP = 128, kColInter = 192, kColIntra = 320;
+
+// Barriers, one phase per chunk (full and empty: one per use of a stage).  A
+// waiter may be at most one phase behind its barrier, or the parity deceives
+// it; the outputs, which run up to two chunks behind the products, therefore
+// have a pair of each, by the chunk's parity.
+enum Bar { kFull = 0, kEmpty = 4, kPartsFull = 8, kPartsEmpty = 10, kPV = 12, kOutFree = 14, kQK = 16, kSReady, kQS, kKV,
+           kKVFree, kPReady, kDrain, kBars };
+
+// A role's share of the registers: it gives some of the launch's back, or
+// takes some that others have given.
+template <int N, int LAUNCHED> __device__ __forceinline__ void share_registers() {
+  static_assert(N % 8 == 0 && N >= 24 && N <= 256, "what the instruction takes");
+  if constexpr (N < LAUNCHED) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+  if constexpr (N > LAUNCHED) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live) {
@@ -74,27 +101,79 @@ __device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&w)[4]) {
 __device__ __forceinline__ void sts128(uint32_t addr, const uint32_t (&w)[4]) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
 }
-__device__ __forceinline__ void sts32(uint32_t addr, uint32_t w) {
-  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(w) : "memory");
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+  return one != 0;
 }
-__device__ __forceinline__ void worker_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(kWorkers * 32) : "memory"); }
+// The outputs' four warps.
+__device__ __forceinline__ void output_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// A chunk of the walk: its physical rows are t0 .. t0 + 63 of the sequence;
-// row r is the chunk's token r, or 63 - r when time runs backwards.
-struct Chunk {
-  int64_t t0;
-  int len;
+// Descriptors from a tile's address: K-major tiles (groups of eight rows 1024
+// bytes apart) and MN-major ones; `d` moves along them by whole 16-byte units.
+struct Desc {
+  uint32_t lo;
+  __device__ __forceinline__ uint64_t at(uint32_t bytes) const {
+    return ((uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32) | (lo + (bytes >> 4));
+  }
 };
-__device__ __forceinline__ Chunk chunk_at(const LinearParams &p, int64_t n, int64_t i0, int64_t stop) {
-  Chunk c;
-  c.len = (int)min((int64_t)kC, stop - i0);
-  c.t0 = p.reverse ? n - i0 - kC : i0;
-  return c;
+__device__ __forceinline__ Desc desc_k(uint32_t addr) { return {((addr & 0x3FFFFu) >> 4) | 1u << 16}; }
+__device__ __forceinline__ Desc desc_mn(uint32_t addr, uint32_t lbo) { return {((addr & 0x3FFFFu) >> 4) | (lbo >> 4) << 16}; }
+
+// Two fp32 values in a register pair, from and to bf16 pairs.
+__device__ __forceinline__ uint64_t widen(uint32_t w) { return ((uint64_t)(w & 0xffff0000u) << 32) | (uint64_t)(w << 16); }
+__device__ __forceinline__ uint32_t narrow(uint64_t v) {
+  float lo, hi;
+  unpair(v, lo, hi);
+  return Elt<__nv_bfloat16>::pack_word(lo, hi);
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// 32 columns of this thread's tensor-memory lane, as pairs.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint64_t (&v)[16]) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = ((uint64_t)r[2 * i + 1] << 32) | r[2 * i];
+}
+// 16 lanes x 32 columns spread over the warp as four matrix fragments of 16 x
+// 8: pair 2 i + j of a thread is row lane / 4 + 8 j, columns 8 i + 2 (lane %
+// 4) and the next.
+__device__ __forceinline__ void tmem_ld_fragments(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+}
+__device__ __forceinline__ uint64_t joined(uint32_t lo, uint32_t hi) { return ((uint64_t)hi << 32) | lo; }
+// Four 8 x 8 bf16 fragments to shared memory, as they lie or transposed;
+// lane l names row l % 8 of matrix l / 8.
+__device__ __forceinline__ void stmatrix4(uint32_t addr, const uint32_t (&w)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};"
+               ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+}
+__device__ __forceinline__ void stmatrix4_t(uint32_t addr, const uint32_t (&w)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};"
+               ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
 }
 
 template <bool STATES>
-__global__ void __launch_bounds__(kThreads, STATES ? 2 : 1) linear_tc_kernel(const LinearParams p) {
-  using L = Smem<STATES>;
+__global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(const LinearParams p) {
+  using L = Shape<STATES>;
   extern __shared__ unsigned char smem_raw[];
   grid_dependency_wait();
   unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -102,7 +181,7 @@ __global__ void __launch_bounds__(kThreads, STATES ? 2 : 1) linear_tc_kernel(con
   float *pw = reinterpret_cast<float *>(sm + L::kOffPow);                       // lambda^0 .. lambda^65
   volatile uint32_t *ctl = reinterpret_cast<uint32_t *>(sm + L::kOffBar + kBars * 8);   // TMEM address, skip, abort
   auto bar = [&](int b) { return base + L::kOffBar + 8u * b; };
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp >> 2, quad = warp & 3;
 
   const int seg = blockIdx.x % p.nseg;
   const int64_t bh = blockIdx.x / p.nseg, b = bh / p.H;
@@ -118,31 +197,38 @@ __global__ void __launch_bounds__(kThreads, STATES ? 2 : 1) linear_tc_kernel(con
     if (reach < (float)(stop - begin)) from = max(begin, (stop - 1 - (int64_t)reach) / kC * kC);
   }
   const int chunks = stop > from ? (int)((stop - from + kC - 1) / kC) : 0;
+  const int tail = chunks > 0 ? (int)(stop - from - (int64_t)(chunks - 1) * kC) : 0;   // tokens of the last chunk
 
   if (threadIdx.x == 0) {
     ctl[1] = *reinterpret_cast<volatile unsigned int *>(&g_error_flag) != 0 ? 1u : 0u;
     ctl[2] = 0;
-    mbar_init(bar(kFull0), kCopyThreads);
-    mbar_init(bar(kFull1), kCopyThreads);
-    mbar_init(bar(kEmpty0), 1);
-    mbar_init(bar(kEmpty1), 1);
+    for (int i = 0; i < L::kStages; ++i) {
+      mbar_init(bar(kFull + i), kCopiers * 32);
+      mbar_init(bar(kEmpty + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kPartsFull + i), 8);
+      mbar_init(bar(kPartsEmpty + i), 1);
+      mbar_init(bar(kPV + i), 1);
+      mbar_init(bar(kOutFree + i), 4);
+    }
     mbar_init(bar(kQK), 1);
-    mbar_init(bar(kS), kWorkers);
-    mbar_init(bar(kV), kWorkers);
+    mbar_init(bar(kSReady), 4);
+    mbar_init(bar(kQS), 1);
     mbar_init(bar(kKV), 1);
-    mbar_init(bar(kP), kWorkers);
-    mbar_init(bar(kPV), 1);
+    mbar_init(bar(kKVFree), 4);
+    mbar_init(bar(kPReady), 4);
     mbar_init(bar(kDrain), 1);
     fence_mbar_init();
   }
   if (threadIdx.x < 66) pw[threadIdx.x] = decay_pow(g, threadIdx.x);
   __syncthreads();
   if (ctl[1]) return;                                 // an earlier error has not been taken: nothing is issued
+  constexpr int kMmaWarp = L::kGroups * 4 - 1;
   if (warp == kMmaWarp) tmem_alloc(base + L::kOffBar + kBars * 8, STATES ? 128 : 512);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl[0];
-  const uint32_t kv_col = STATES ? 0 : kColKV;
 
   // Wait for the phase; false once any wait of the CTA has run out.
   auto wait = [&](int which, uint32_t parity) -> bool {
@@ -158,271 +244,339 @@ __global__ void __launch_bounds__(kThreads, STATES ? 2 : 1) linear_tc_kernel(con
       }
     }
   };
-  // A worker warp's arrival: its shared-memory writes and tensor-memory reads come first.
+  // A warp's arrival: its shared-memory writes and tensor-memory reads come first.
   auto arrive = [&](int which) {
     tc_fence_before();
     fence_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(which));
   };
+  // Token count of chunk c, and a row's place in the walk.
+  auto length_of = [&](int c) { return c + 1 < chunks ? kC : tail; };
+  auto place = [&](int r) { return p.reverse ? kC - 1 - r : r; };
+  const uint32_t quad_addr = tmem + ((uint32_t)(quad * 32) << 16);
 
-  if (warp >= kWorkers && warp < kMmaWarp) {
-    // ---------------- copies ----------------
-    const int tid = threadIdx.x - kWorkers * 32;
-    const int chunk8 = tid % 8, row0 = tid / 8;         // a 16-byte piece of rows row0 + 8 i
-    auto copy_tile = [&](uint32_t dst, const void *src, int64_t stride, int d, const Chunk &ck) {
-      const __nv_bfloat16 *x = (const __nv_bfloat16 *)src + (b * p.T + ck.t0) * stride + (int64_t)h * d;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const int r = row0 + 8 * (i % 8), col = (i / 8) * 64 + chunk8 * 8;
-        const bool live = (p.reverse ? kC - 1 - r : r) < ck.len && col < d;
-        copy16(dst + (i / 8) * kBlock + r * 128 + ((chunk8 ^ (r & 7)) << 4), live ? (const void *)(x + r * stride + col) : src,
-               live);
-      }
-    };
-    for (int c = 0; c < chunks; ++c) {
-      const int s = c & 1;
-      if (c >= 2 && !wait(kEmpty0 + s, ((c >> 1) - 1))) break;
-      const Chunk ck = chunk_at(p, n, from + (int64_t)c * kC, stop);
-      uint32_t dst = base + s * L::kStage;
-      copy_tile(dst, p.b, p.b_stride, p.da, ck);
-      copy_tile(dst + kTile, p.c, p.c_stride, p.dc, ck);
-      if (!STATES) copy_tile(dst + 2 * kTile, p.a, p.a_stride, p.da, ck);
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(kFull0 + s)) : "memory");
-    }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (warp == kMmaWarp) {
-    // ---------------- products ----------------
-    if (lane == 0) {
-      const int ka = (p.da + 15) / 16;                  // K steps over da
-      const uint32_t nkv = p.dc <= 64 ? 64 : 128;
+  if (group == L::kGroups - 1) {
+    share_registers<L::kRegsCopy, L::kRegs>();
+    if (warp != kMmaWarp) {
+      // ---------------- copies ----------------
+      // A warp per tensor; the states' kernel has no a, and its third warp only keeps the count.
+      const int chunk8 = lane % 8, row0 = lane / 8;     // a 16-byte piece of rows row0 + 4 i
+      const int t = warp - (L::kGroups - 1) * 4;
+      const __nv_bfloat16 *src = (const __nv_bfloat16 *)(t == 0 ? p.b : t == 1 ? p.c : p.a);
+      const int64_t stride = t == 0 ? p.b_stride : t == 1 ? p.c_stride : p.a_stride;
+      const int d = t == 1 ? p.dc : p.da;
+      const bool low = chunk8 * 8 < d, high = 64 + chunk8 * 8 < d, mine = !STATES || t < 2;
+      const uint32_t swz0 = (chunk8 ^ row0) << 4, swz1 = swz0 ^ 64;                 // rows row0 + 4 i, i even and odd
+      const int64_t step = 4 * stride;
       for (int c = 0; c < chunks; ++c) {
-        const int s = c & 1;
-        const uint32_t tb = base + s * L::kStage, tcl = tb + kTile, ta = tb + 2 * kTile;
-        if (!wait(kFull0 + s, c >> 1)) break;
+        const int s = c % L::kStages;
+        if (c >= L::kStages && !wait(kEmpty + s, c / L::kStages - 1)) break;
+        if (mine) {
+          const int len = length_of(c);
+          const int64_t i0 = from + (int64_t)c * kC;
+          const __nv_bfloat16 *x = src + (b * p.T + (p.reverse ? n - i0 - kC : i0) + row0) * stride + (int64_t)h * d + chunk8 * 8;
+          const uint32_t dst = base + s * L::kStage + t * kTile + row0 * 128;
+          if (len == kC && low && high) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i, x += step) {
+              copy16(dst + (i & 1 ? swz1 : swz0) + i * 512, x, true);
+              copy16(dst + (i & 1 ? swz1 : swz0) + i * 512 + kBlock, x + 64, true);
+            }
+          } else {
+#pragma unroll 1
+            for (int i = 0; i < 16; ++i, x += step) {
+              const bool live = place(row0 + 4 * i) < len;
+              const uint32_t to = dst + (i & 1 ? swz1 : swz0) + i * 512;
+              copy16(to, live && low ? x : src, live && low);
+              copy16(to + kBlock, live && high ? x + 64 : src, live && high);
+            }
+          }
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(kFull + s)) : "memory");
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (elect_one()) {
+      // ---------------- products ----------------
+      const int ka = (p.da + 15) / 16;                  // K steps over da
+      const uint32_t kv_desc = idesc_bf16(128, p.dc <= 64 ? 64 : 128) | kIdescMnA | kIdescMnB;
+      auto qk = [&](int c) -> bool {
+        const uint32_t tb = base + (c % L::kStages) * L::kStage;
+        if (!wait(kFull + c % L::kStages, c / L::kStages)) return false;
         fence_async_smem();                             // the copies' writes, before the products read them
         tc_fence_after();
-        if (!STATES) {
-          for (int k = 0; k < ka; ++k) {
-            const uint32_t off = (k / 4) * kBlock + (k % 4) * 32;
-            mma_bf16(tmem + kColP, sw128_desc(ta + off, 1024), sw128_desc(tb + off, 1024), idesc_bf16(64, 64), k > 0);
-          }
-          mma_commit(bar(kQK));
-          if (!wait(kS, c)) break;
+        if (STATES) return true;
+        const Desc a = desc_k(tb + 2 * kTile), x = desc_k(tb);
+#pragma unroll 4
+        for (int k = 0; k < ka; ++k) {
+          const uint32_t off = (k / 4) * kBlock + (k % 4) * 32;
+          mma_bf16(tmem + kColP, a.at(off), x.at(off), idesc_bf16(64, 64), k > 0);
+        }
+        mma_commit(bar(kQK));
+        return true;
+      };
+      bool ok = chunks > 0 && qk(0);
+      for (int c = 0; ok && c < chunks; ++c) {
+        const int s = c % L::kStages;
+        const uint32_t tb = base + s * L::kStage;
+        // the update of S, 32 tokens at a time
+        if (c > 0 && !wait(kKVFree, c - 1)) break;
+        const Desc kt = desc_mn(tb, kBlock);
+#pragma unroll 1
+        for (int half = 0; half < 2 && ok; ++half) {
+          if (!(ok = wait(kPartsFull + half, c))) break;
           tc_fence_after();
-          for (int k = 0; k < ka; ++k) {
-            const uint32_t off = (k / 4) * kBlock + (k % 4) * 32;
-            mma_bf16(tmem + kColInter + 64 * s, sw128_desc_mn(base + L::kOffS + k * 2048, kSBlock, 1024),
-                     sw128_desc(ta + off, 1024), idesc_bf16(128, 64) | kIdescMnA, k > 0);
-          }
-        }
-        if (!wait(kV, c)) break;
-        tc_fence_after();
-        for (int part = 0; part < 3; ++part) {
-          const uint32_t w = STATES ? (part == 0 ? tcl : base + L::kOffParts + (part - 1) * kTile)
-                                    : base + L::kOffParts + part * kTile;
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            mma_bf16(tmem + kv_col, sw128_desc_mn(tb + k * 2048, kBlock, 1024), sw128_desc_mn(w + k * 2048, kBlock, 1024),
-                     idesc_bf16(128, (int)nkv) | kIdescMnA | kIdescMnB, part > 0 || k > 0);
+          for (int part = 0; part < 3; ++part) {
+            const Desc w = desc_mn(base + L::kOffParts + part * kTile, kBlock);
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              mma_bf16(tmem + kColKV, kt.at(half * kHalf + k * 2048), w.at(half * kHalf + k * 2048), kv_desc,
+                       half + part + k > 0);
+          }
+          mma_commit(bar(kPartsEmpty + half));
         }
+        if (!ok) break;
         mma_commit(bar(kKV));
         if (!STATES) {
-          if (!wait(kP, c)) break;
+          if (!wait(kSReady, c) || (c >= 2 && !wait(kOutFree + (c & 1), (c >> 1) - 1))) break;
           tc_fence_after();
+          const Desc st = desc_mn(base + L::kOffS, kSBlock), a = desc_k(tb + 2 * kTile);
+#pragma unroll 4
+          for (int k = 0; k < ka; ++k)
+            mma_bf16(tmem + kColInter + 64 * (c & 1), st.at(k * 2048), a.at((k / 4) * kBlock + (k % 4) * 32),
+                     idesc_bf16(128, 64) | kIdescMnA, k > 0);
+          mma_commit(bar(kQS));
+          if (!wait(kPReady, c)) break;
+          tc_fence_after();
+          const Desc v = desc_mn(tb + kTile, kBlock), pt = desc_k(base + L::kOffP);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_bf16(tmem + kColIntra + 64 * s, sw128_desc_mn(tcl + k * 2048, kBlock, 1024),
-                     sw128_desc(base + L::kOffP + k * 32, 1024), idesc_bf16(128, 64) | kIdescMnA, k > 0);
-          mma_commit(bar(kPV));
+            mma_bf16(tmem + kColIntra + 64 * (c & 1), v.at(k * 2048), pt.at(k * 32), idesc_bf16(128, 64) | kIdescMnA, k > 0);
+          mma_commit(bar(kPV + (c & 1)));
         }
-        mma_commit(bar(kEmpty0 + s));
+        mma_commit(bar(kEmpty + s));
+        if (c + 1 < chunks) ok = qk(c + 1);
       }
       // every product issued has completed before the memory it uses goes
       mma_commit(bar(kDrain));
       if (!mbar_wait_for(bar(kDrain), 0, kDrainLimitCycles)) raise_timeout();
     }
-  } else {
-    // ---------------- workers ----------------
-    const int half = warp / 4, quad = warp % 4;
-    const uint32_t quad_addr = tmem + ((uint32_t)(quad * 32) << 16);
-    const int row = quad * 32 + lane;                   // of S (and, of the outputs, the column of c)
-    const bool has = row < p.da && half * 64 < p.dc;    // this thread's 64 columns of S exist
-    float st[64];
+  } else if (group == 0) {
+    // ---------------- the state ----------------
+    share_registers<L::kRegsS, L::kRegs>();
+    const int row = quad * 32 + lane;
+    const bool has = row < p.da;
+    uint64_t st[64];                                    // columns 2 j and 2 j + 1
     float *states = p.states + ((bh * p.nseg + seg) * p.da) * p.dc;
 #pragma unroll
     for (int j = 0; j < 64; ++j) {
-      const int col = half * 64 + j;
-      st[j] = 0.f;
-      if (!STATES && has && col < p.dc) {
-        if (p.nseg > 1) st[j] = states[(int64_t)row * p.dc + col];
-        else if (p.first) st[j] = first_at(p, bh, row, col);
+      float x[2] = {0.f, 0.f};
+      if (!STATES && has && 2 * j < p.dc) {             // dc is even
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          if (p.nseg > 1) x[e] = states[(int64_t)row * p.dc + 2 * j + e];
+          else if (p.first) x[e] = first_at(p, bh, row, 2 * j + e);
+        }
       }
+      st[j] = pair(x[0], x[1]);
     }
     // The state's bf16 copy, [da][dc] in blocks of 64 columns.
-    auto publish_state = [&]() {
-      const uint32_t dst = base + L::kOffS + half * kSBlock + row * 128;
+    auto publish = [&]() {
+      const uint32_t dst = base + L::kOffS + row * 128;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 16; ++j) {
         uint32_t w[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = Elt<__nv_bfloat16>::pack_word(st[j * 8 + 2 * i], st[j * 8 + 2 * i + 1]);
-        sts128(dst + ((j ^ (row & 7)) << 4), w);
+        for (int i = 0; i < 4; ++i) w[i] = narrow(st[j * 4 + i]);
+        sts128(dst + (j / 8) * kSBlock + (((j % 8) ^ (row & 7)) << 4), w);
       }
-      arrive(kS);
+      arrive(kSReady);
     };
-    // The outputs of chunk c: weights, sum, transposition through shared memory, store.
-    auto store_outputs = [&](int c) {
-      const Chunk ck = chunk_at(p, n, from + (int64_t)c * kC, stop);
-      const int lead = from + (int64_t)c * kC == 0 ? p.first_pow : 1;
-      const int s = c & 1;
-      worker_barrier();                                 // the last outputs have left the staging
-      tc_fence_after();
-#pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const int t0 = half * 32 + q * 16;              // this thread: column `row` of tokens t0 .. t0 + 15
-        float x[16], y[16];
-        tmem_ld16(quad_addr + kColInter + 64 * s + t0, x);
-        tmem_ld16(quad_addr + kColIntra + 64 * s + t0, y);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int r = t0 + i;
-          x[i] = p.alpha * fmaf(pw[(p.reverse ? kC - 1 - r : r) + lead], x[i], y[i]);
-        }
-        // neighbouring lanes swap, so that each stores two columns of one token
-#pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? x[i] : x[i + 1], 1);
-          const uint32_t w = lane & 1 ? Elt<__nv_bfloat16>::pack_word(other, x[i + 1])
-                                      : Elt<__nv_bfloat16>::pack_word(x[i], other);
-          sts32(base + L::kOffOut + (t0 + i + (lane & 1)) * kOutPitch + (row & ~1) * 2, w);
-        }
-      }
-      worker_barrier();
-      __nv_bfloat16 *dst = (__nv_bfloat16 *)p.out + ((b * p.T + ck.t0) * p.H + h) * p.dc;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int k = i * (kWorkers * 32) + threadIdx.x, r = k / 16, col = (k % 16) * 8;
-        if ((p.reverse ? kC - 1 - r : r) < ck.len && col < p.dc) {
-          uint32_t w[4];
-          lds128(base + L::kOffOut + r * kOutPitch + col * 2, w);
-          st_vec(dst + (int64_t)r * p.H * p.dc + col, make_uint4(w[0], w[1], w[2], w[3]));
-        }
-      }
-    };
-    if (!STATES && chunks > 0) publish_state();
     for (int c = 0; c < chunks; ++c) {
-      const int s = c & 1;
-      const Chunk ck = chunk_at(p, n, from + (int64_t)c * kC, stop);
-      const int lead = from + (int64_t)c * kC == 0 ? p.first_pow : 1;
-      const uint32_t tcl = base + s * L::kStage + kTile;
-      // w c in three parts, each in the tile's own layout
-      wait(kFull0 + s, c >> 1);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t off = (i * (kWorkers * 32) + threadIdx.x) * 16;
-        const int r = (off / 128) % kC, li = p.reverse ? kC - 1 - r : r;
-        const float w = li < ck.len ? pw[ck.len - 1 - li] : 0.f;
-        uint32_t v[4], p0[4], p1[4], p2[4];
-        lds128(tcl + off, v);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x0, x1, h0, h1;
-          Elt<__nv_bfloat16>::unpack_word(v[e], x0, x1);
-          x0 *= w;
-          x1 *= w;
-          p0[e] = Elt<__nv_bfloat16>::pack_word(x0, x1);
-          Elt<__nv_bfloat16>::unpack_word(p0[e], h0, h1);
-          x0 -= h0;
-          x1 -= h1;
-          p1[e] = Elt<__nv_bfloat16>::pack_word(x0, x1);
-          Elt<__nv_bfloat16>::unpack_word(p1[e], h0, h1);
-          p2[e] = Elt<__nv_bfloat16>::pack_word(x0 - h0, x1 - h1);
-        }
-        if (STATES) {
-          sts128(tcl + off, p0);
-          sts128(base + L::kOffParts + off, p1);
-          sts128(base + L::kOffParts + kTile + off, p2);
-        } else {
-          sts128(base + L::kOffParts + off, p0);
-          sts128(base + L::kOffParts + kTile + off, p1);
-          sts128(base + L::kOffParts + 2 * kTile + off, p2);
-        }
-      }
-      arrive(kV);
       if (!STATES) {
-        // P: 64 rows in 16 lanes of each quadrant; this warp's half of the columns
-        if (c > 0) wait(kPV, c - 1);                    // P's last copy is read
-        wait(kQK, c);
-        __syncwarp();
-        tc_fence_after();
-        float x[32];
-        tmem_ld16(quad_addr + kColP + half * 32, x);
-        tmem_ld16(quad_addr + kColP + half * 32 + 16, x + 16);
-        tmem_wait_ld();
-        if (lane < 16) {
-          const int r = quad * 16 + lane;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int col = half * 32 + j * 8 + i, back = p.reverse ? col - r : r - col;
-              x[j * 8 + i] = back >= 0 ? x[j * 8 + i] * pw[back] : 0.f;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = Elt<__nv_bfloat16>::pack_word(x[j * 8 + 2 * i], x[j * 8 + 2 * i + 1]);
-            sts128(base + L::kOffP + r * 128 + (((half * 4 + j) ^ (r & 7)) << 4), w);
-          }
-        }
-        arrive(kP);
-        if (c > 0) store_outputs(c - 1);
+        if (c > 0) wait(kQS, c - 1);                    // the last copy is read
+        publish();
       }
-      // S <- lambda^len S + its update
+      const int lead = from + (int64_t)c * kC == 0 ? p.first_pow : 1;
+      const float keep = decay_pow(g, length_of(c) - 1 + lead);
+      const uint64_t keep2 = pair(keep, keep);
       wait(kKV, c);
       __syncwarp();
       tc_fence_after();
-      if (half * 64 < p.dc) {
-        const float keep = decay_pow(g, ck.len - 1 + lead);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float x[16];
-          tmem_ld16(quad_addr + kv_col + half * 64 + q * 16, x);
-          tmem_wait_ld();
+      for (int q = 0; q < 4; ++q) {
+        if (q < 2 || p.dc > 64) {                       // narrow states: the upper columns stay zero
+          uint64_t x[16];
+          tmem_ld32(quad_addr + kColKV + q * 32, x);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) st[q * 16 + i] = fmaf(st[q * 16 + i], keep, x[i]);
+          for (int i = 0; i < 16; ++i) st[q * 16 + i] = fma2(st[q * 16 + i], keep2, x[i]);
         }
       }
-      if (!STATES && c + 1 < chunks) publish_state();
-    }
-    if (!STATES && chunks > 0) {
-      wait(kPV, chunks - 1);
-      store_outputs(chunks - 1);
+      arrive(kKVFree);
     }
     if (has && (STATES || (p.nseg == 1 && p.last))) {
       float *dst = STATES ? states : p.last + bh * p.da * p.dc;
       // no token at all: the state passes through unchanged
       const float f = STATES ? 1.f : p.last_scale * (n > 0 ? decay_pow(g, p.last_pow) : 1.f);
 #pragma unroll
-      for (int j = 0; j < 64; j += 4) {
-        const int col = half * 64 + j;                  // dc is a multiple of 8
-        if (col < p.dc)
-          *reinterpret_cast<float4 *>(dst + (int64_t)row * p.dc + col) =
-              make_float4(st[j] * f, st[j + 1] * f, st[j + 2] * f, st[j + 3] * f);
+      for (int j = 0; j < 64; j += 2) {
+        if (2 * j < p.dc) {                             // dc is a multiple of 8
+          float4 x;
+          unpair(st[j], x.x, x.y);
+          unpair(st[j + 1], x.z, x.w);
+          x.x *= f; x.y *= f; x.z *= f; x.w *= f;
+          *reinterpret_cast<float4 *>(dst + (int64_t)row * p.dc + 2 * j) = x;
+        }
       }
     }
-    if (!STATES) {
-      // rows behind the sequence are zero
-      const int64_t first_row = max(stop, begin);
-      const int v = p.dc / 8;
-      for (int64_t k = threadIdx.x; k < (end - first_row) * v; k += kWorkers * 32)
-        st_vec((__nv_bfloat16 *)p.out + ((b * p.T + first_row + k / v) * p.H + h) * p.dc + k % v * 8, make_uint4(0, 0, 0, 0));
+  } else if (group <= 2) {
+    // ---------------- w c in three parts, each in the tile's own layout ----------------
+    share_registers<L::kRegsParts, L::kRegs>();
+    const int tid = threadIdx.x - 128;
+    const uint64_t minus = pair(-1.f, -1.f);
+    const int li0 = place(tid / 8), li1 = place(32 + tid / 8);          // the thread's two rows
+    float w0 = pw[kC - 1 - li0], w1 = pw[kC - 1 - li1];
+    for (int c = 0; c < chunks; ++c) {
+      const int s = c % L::kStages, len = length_of(c);
+      if (len < kC) {
+        w0 = li0 < len ? pw[len - 1 - li0] : 0.f;
+        w1 = li1 < len ? pw[len - 1 - li1] : 0.f;
+      }
+      const uint32_t src = base + s * L::kStage + kTile;
+      wait(kFull + s, c / L::kStages);
+#pragma unroll 1
+      for (int half = 0; half < 2; ++half) {
+        if (c > 0) wait(kPartsEmpty + half, c - 1);
+        const float w = half ? w1 : w0;
+        const uint64_t w2 = pair(w, w);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {                   // block i, row half * 32 + tid / 8
+          const uint32_t off = i * kBlock + half * kHalf + tid * 16;
+          uint32_t v[4], p0[4], p1[4], p2[4];
+          lds128(src + off, v);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint64_t x = widen(v[e]);
+            scale_pair(x, w2);
+            p0[e] = narrow(x);
+            x = fma2(widen(p0[e]), minus, x);
+            p1[e] = narrow(x);
+            p2[e] = narrow(fma2(widen(p1[e]), minus, x));
+          }
+          sts128(base + L::kOffParts + off, p0);
+          sts128(base + L::kOffParts + kTile + off, p1);
+          sts128(base + L::kOffParts + 2 * kTile + off, p2);
+        }
+        arrive(kPartsFull + half);
+      }
     }
+  } else if (group == 3) {
+    // ---------------- P: 64 rows in the first 16 lanes of each quadrant ----------------
+    share_registers<L::kRegsP, L::kRegs>();
+    const int row = quad * 16 + lane / 4, col = 2 * (lane % 4);         // of the thread's first element
+    float w[32];                                        // its 32 weights (alpha, the decay, the mask) stay the same
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = row + 8 * (j / 2), k = col + 8 * i + j % 2, back = p.reverse ? k - r : r - k;
+        w[4 * i + j] = back >= 0 ? p.alpha * pw[back] : 0.f;
+      }
+    const int srow = quad * 16 + lane % 16;             // the row this lane names for the matrix stores
+    const uint32_t dst = base + L::kOffP + srow * 128;
+    for (int c = 0; c < chunks; ++c) {
+      wait(kQK, c);
+      if (c > 0) wait(kPV + ((c - 1) & 1), (c - 1) >> 1);               // the last copy is read
+      __syncwarp();
+      tc_fence_after();
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t x[16];
+        tmem_ld_fragments(quad_addr + kColP + q * 32, x);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {                // columns 32 q + 8 i: two fragments of 16 x 8
+          uint32_t v[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int e = 4 * i + 2 * j;
+            uint64_t y = joined(x[e], x[e + 1]);
+            scale_pair(y, pair(w[16 * q + e], w[16 * q + e + 1]));
+            v[j] = narrow(y);
+          }
+          stmatrix4(dst + (((q * 4 + i + lane / 16) ^ (srow & 7)) << 4), v);
+        }
+      }
+      arrive(kPReady);
+    }
+  } else {
+    // ---------------- outputs: weights, sum, transposition through shared memory, store ----------------
+    share_registers<L::kRegsOut, L::kRegs>();
+    const int tid = threadIdx.x - 4 * 128;
+    float w[16];                                        // alpha and the decay of the thread's 16 tokens
+    int lead = -1;
+    // the matrix stores: this lane names a token's row and 8 columns of c
+    const uint32_t put = base + L::kOffOut + (8 * (lane / 16) + lane % 8) * kOutPitch + (quad * 4 + lane / 8 % 2) * 16;
+    const int col = tid % 16 * 8;
+    const uint32_t get = base + L::kOffOut + tid / 16 * kOutPitch + col * 2;
+    const int64_t step = (int64_t)8 * p.H * p.dc;
+    for (int c = 0; c < chunks; ++c) {
+      const int len = length_of(c);
+      const int64_t i0 = from + (int64_t)c * kC;
+      const int now = i0 == 0 ? p.first_pow : 1;
+      if (now != lead) {
+        lead = now;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = p.alpha * pw[place(8 * (i / 2) + 2 * (lane % 4) + i % 2) + lead];
+      }
+      wait(kPV + (c & 1), c >> 1);
+      __syncwarp();
+      tc_fence_after();
+      output_barrier();                                 // the last outputs have left the staging
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {                     // columns 16 (q / 2) of c, tokens 32 (q % 2)
+        const uint32_t at = quad_addr + ((uint32_t)(q / 2 * 16) << 16) + 64 * (c & 1) + q % 2 * 32;
+        uint32_t x[16], y[16];
+        tmem_ld_fragments(at + kColInter, x);
+        tmem_ld_fragments(at + kColIntra, y);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+          uint32_t v[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int e = 4 * i + 2 * j, t = 8 * (q % 2) + 2 * (i + j / 2);
+            v[j] = narrow(fma2(joined(x[e], x[e + 1]), pair(w[t], w[t + 1]), joined(y[e], y[e + 1])));
+          }
+          stmatrix4_t(put + (q % 2 * 32 + i * 8) * kOutPitch + q / 2 * 32, v);
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kOutFree + (c & 1)));
+      output_barrier();
+      __nv_bfloat16 *dst = (__nv_bfloat16 *)p.out +
+                           ((b * p.T + (p.reverse ? n - i0 - kC : i0) + tid / 16) * p.H + h) * p.dc + col;
+#pragma unroll
+      for (int i = 0; i < 8; ++i, dst += step) {
+        if (place(i * 8 + tid / 16) < len && col < p.dc) {
+          uint32_t v[4];
+          lds128(get + i * 8 * kOutPitch, v);
+          st_vec(dst, make_uint4(v[0], v[1], v[2], v[3]));
+        }
+      }
+    }
+    // rows behind the sequence are zero
+    const int64_t first_row = max(stop, begin);
+    const int v = p.dc / 8;
+    for (int64_t k = tid; k < (end - first_row) * v; k += 128)
+      st_vec((__nv_bfloat16 *)p.out + ((b * p.T + first_row + k / v) * p.H + h) * p.dc + k % v * 8, make_uint4(0, 0, 0, 0));
     tc_fence_before();
   }
   __syncthreads();
   if (warp == kMmaWarp) {
+    __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, STATES ? 128 : 512);
   }
@@ -452,13 +606,28 @@ int linear_tc_segments(int64_t BH, int64_t T) {
   return best;
 }
 
+namespace {
+// The shares above start from the registers a launch gives each thread: what
+// the compiler chose has to be that number, or a role would wait for
+// registers that nobody gives.
+template <bool STATES> bool registers_as_planned() {
+  static const bool ok = [] {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, linear_tc_kernel<STATES>) == cudaSuccess && a.numRegs == Shape<STATES>::kRegs;
+  }();
+  return ok;
+}
+template <bool STATES> cudaError_t launch_chunks(const LinearParams &p, int64_t BH, cudaStream_t stream) {
+  using L = Shape<STATES>;
+  if (!registers_as_planned<STATES>()) return cudaErrorInvalidConfiguration;
+  const cudaError_t e = cudaFuncSetAttribute(linear_tc_kernel<STATES>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kBytes);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(linear_tc_kernel<STATES>, dim3((unsigned)(BH * p.nseg)), dim3(L::kThreads), L::kBytes, stream, p);
+}
+}  // namespace
+
 cudaError_t launch_linear_tc(const LinearParams &p, int64_t BH, bool states, cudaStream_t stream) {
-  auto go = [&](auto kern, uint32_t smem) -> cudaError_t {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    return launch_dependent(kern, dim3((unsigned)(BH * p.nseg)), dim3(kThreads), smem, stream, p);
-  };
-  return states ? go(linear_tc_kernel<true>, Smem<true>::kBytes) : go(linear_tc_kernel<false>, Smem<false>::kBytes);
+  return states ? launch_chunks<true>(p, BH, stream) : launch_chunks<false>(p, BH, stream);
 }
 
 }  // namespace attnres
