@@ -19,17 +19,16 @@
 //
 // Roles of a CTA, one per SM (a warpgroup of four warps each, but for the
 // last): the state (a thread per row of S, all its columns in registers); two
-// for the weighted parts; P; the outputs; and three warps that copy tiles
+// for the weighted parts; P; the outputs; and two warps that copy tiles
 // (cp.async, 16 bytes a lane, straight into the swizzled layout, rows behind
 // the sequence and columns behind the width as zeros; tensor-map copies are
 // served one box at a time per CTA and would cap one CTA per SM at about
-// 4.2 TB/s) beside the thread that issues the products.  A warp runs its
-// dependent instructions one in five cycles or so, so what counts is how few
-// instructions each role needs per chunk, and that the roles run side by side
-// on code short enough for the instruction cache: with eight warps doing all
-// of the work in turn a chunk took 7900 cycles, 3.4 us.  Tensor memory holds
-// P, the update of S, and two pairs of output accumulators.  Order of the
-// products: update(c), S^T a^T (c), c^T P^T (c), a b^T (c + 1).
+// 4.2 TB/s) beside two threads that issue products, one the updates of S and
+// one all others, so that neither waits for the other's operands.  A warp runs
+// its dependent instructions one in five cycles or so, so what counts is how
+// few instructions each role needs per chunk, and that the roles run side by
+// side: with eight warps doing all of the work in turn a chunk took 7900
+// cycles.
 //
 // Every wait is bounded: one that runs out records a flag and an abort mark
 // in shared memory, on which every other wait returns at once; the issuing
@@ -45,17 +44,18 @@ namespace {
 constexpr int kC = kChunk;
 constexpr uint32_t kTile = kC * 128 * 2;              // bytes: 64 tokens x 128 columns, two blocks of 64 columns
 constexpr uint32_t kBlock = kTile / 2;
-constexpr uint32_t kHalf = 32 * 128;                  // 32 tokens of a block
+constexpr int kStep = 16;                             // tokens per step of the weighted parts (an MMA's K)
+constexpr uint32_t kPart = kStep * 128 * 2;           // a part of them: two blocks of 64 columns
 constexpr uint32_t kSBlock = 128 * 128;               // 64 columns of S's 128 rows
 constexpr int kOutPitch = 272;                        // bytes per token of the output staging (no bank met twice)
-constexpr int kCopiers = 3;                           // warps
+constexpr int kCopiers = 2;                           // warps
 
 // The main kernel's warpgroups: S, parts, parts, P, outputs, copies + products;
 // the states' kernel: S, parts, parts, copies + products.
 template <bool STATES> struct Shape {
   static constexpr int kGroups = STATES ? 4 : 6;
   static constexpr int kThreads = kGroups * 128;
-  static constexpr int kStages = STATES ? 4 : 2;
+  static constexpr int kStages = STATES ? 6 : 3;
   // Registers per thread: as launched (checked at the launch), then each
   // role's share; their sum stays within the launch's.
   static constexpr int kRegs = STATES ? 128 : 80;
@@ -65,23 +65,23 @@ template <bool STATES> struct Shape {
                 "more registers than the launch has");
   static constexpr uint32_t kStage = (STATES ? 2 : 3) * kTile;      // b, c, [a]
   static constexpr uint32_t kOffParts = kStages * kStage;
-  static constexpr uint32_t kOffP = kOffParts + 3 * kTile;
+  static constexpr uint32_t kOffP = kOffParts + 2 * 3 * kPart;
   static constexpr uint32_t kOffS = kOffP + (STATES ? 0 : kC * 128);
   static constexpr uint32_t kOffOut = kOffS + (STATES ? 0 : 2 * kSBlock);
   static constexpr uint32_t kOffPow = kOffOut + (STATES ? 0 : kC * kOutPitch);
   static constexpr uint32_t kOffBar = kOffPow + 72 * 4;
-  static constexpr uint32_t kBytes = kOffBar + 26 * 8 + 1024;       // and the alignment's slack
+  static constexpr uint32_t kBytes = kOffBar + 30 * 8 + 1024;       // and the alignment's slack
 };
 
-// Tensor memory columns: the update of S first; P, outputs by parity.
-constexpr uint32_t kColKV = 0, kColP = 128, kColInter = 192, kColIntra = 320;
+// Tensor memory columns: the update of S by the chunk's parity, P, the outputs' two sums.
+constexpr uint32_t kColKV = 0, kColP = 256, kColInter = 320, kColIntra = 384;
 
-// Barriers, one phase per chunk (full and empty: one per use of a stage).  A
-// waiter may be at most one phase behind its barrier, or the parity deceives
-// it; the outputs, which run up to two chunks behind the products, therefore
-// have a pair of each, by the chunk's parity.
-enum Bar { kFull = 0, kEmpty = 4, kPartsFull = 8, kPartsEmpty = 10, kPV = 12, kOutFree = 14, kQK = 16, kSReady, kQS, kKV,
-           kKVFree, kPReady, kDrain, kBars };
+// Barriers, one phase per chunk (full, empty and parts: one per use of a
+// stage or buffer).  A waiter may be at most one phase behind its barrier, or
+// the parity deceives it; the updates of S, which run up to two chunks ahead
+// of the state, therefore have a pair of each, by the chunk's parity.
+enum Bar { kFull = 0, kEmpty = 6, kPartsFull = 12, kPartsEmpty = 14, kKV = 16, kKVFree = 18, kPV = 20, kOutFree, kQK, kSReady,
+           kQS, kPReady, kDrain, kDrainKV, kBars };
 
 // A role's share of the registers: it gives some of the launch's back, or
 // takes some that others have given.
@@ -204,28 +204,29 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(c
     ctl[2] = 0;
     for (int i = 0; i < L::kStages; ++i) {
       mbar_init(bar(kFull + i), kCopiers * 32);
-      mbar_init(bar(kEmpty + i), 1);
+      mbar_init(bar(kEmpty + i), STATES ? 1 : 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kPartsFull + i), 8);
       mbar_init(bar(kPartsEmpty + i), 1);
-      mbar_init(bar(kPV + i), 1);
-      mbar_init(bar(kOutFree + i), 4);
+      mbar_init(bar(kKV + i), 1);
+      mbar_init(bar(kKVFree + i), 4);
     }
     mbar_init(bar(kQK), 1);
     mbar_init(bar(kSReady), 4);
     mbar_init(bar(kQS), 1);
-    mbar_init(bar(kKV), 1);
-    mbar_init(bar(kKVFree), 4);
+    mbar_init(bar(kPV), 1);
+    mbar_init(bar(kOutFree), 4);
     mbar_init(bar(kPReady), 4);
     mbar_init(bar(kDrain), 1);
+    mbar_init(bar(kDrainKV), 1);
     fence_mbar_init();
   }
   if (threadIdx.x < 66) pw[threadIdx.x] = decay_pow(g, threadIdx.x);
   __syncthreads();
   if (ctl[1]) return;                                 // an earlier error has not been taken: nothing is issued
   constexpr int kMmaWarp = L::kGroups * 4 - 1;
-  if (warp == kMmaWarp) tmem_alloc(base + L::kOffBar + kBars * 8, STATES ? 128 : 512);
+  if (warp == kMmaWarp) tmem_alloc(base + L::kOffBar + kBars * 8, STATES ? 256 : 512);
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = ctl[0];
@@ -258,34 +259,35 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(c
 
   if (group == L::kGroups - 1) {
     share_registers<L::kRegsCopy, L::kRegs>();
-    if (warp != kMmaWarp) {
+    if (warp < kMmaWarp - 1) {
       // ---------------- copies ----------------
-      // A warp per tensor; the states' kernel has no a, and its third warp only keeps the count.
-      const int chunk8 = lane % 8, row0 = lane / 8;     // a 16-byte piece of rows row0 + 4 i
-      const int t = warp - (L::kGroups - 1) * 4;
-      const __nv_bfloat16 *src = (const __nv_bfloat16 *)(t == 0 ? p.b : t == 1 ? p.c : p.a);
-      const int64_t stride = t == 0 ? p.b_stride : t == 1 ? p.c_stride : p.a_stride;
-      const int d = t == 1 ? p.dc : p.da;
-      const bool low = chunk8 * 8 < d, high = 64 + chunk8 * 8 < d, mine = !STATES || t < 2;
-      const uint32_t swz0 = (chunk8 ^ row0) << 4, swz1 = swz0 ^ 64;                 // rows row0 + 4 i, i even and odd
-      const int64_t step = 4 * stride;
+      // Each warp takes half of the rows of every tensor.
+      const int chunk8 = lane % 8, row0 = (warp - (kMmaWarp - 3)) * 32 + lane / 8;   // a 16-byte piece of rows row0 + 4 i
+      const uint32_t swz0 = row0 * 128 + ((chunk8 ^ (row0 & 7)) << 4), swz1 = swz0 ^ 64;   // i even and odd
       for (int c = 0; c < chunks; ++c) {
         const int s = c % L::kStages;
         if (c >= L::kStages && !wait(kEmpty + s, c / L::kStages - 1)) break;
-        if (mine) {
-          const int len = length_of(c);
-          const int64_t i0 = from + (int64_t)c * kC;
-          const __nv_bfloat16 *x = src + (b * p.T + (p.reverse ? n - i0 - kC : i0) + row0) * stride + (int64_t)h * d + chunk8 * 8;
-          const uint32_t dst = base + s * L::kStage + t * kTile + row0 * 128;
-          if (len == kC && low && high) {
+        const int len = length_of(c);
+        const int64_t i0 = from + (int64_t)c * kC;
+        const int64_t at = b * p.T + (p.reverse ? n - i0 - kC : i0) + row0;
+#pragma unroll 1
+        for (int t = 0; t < (STATES ? 2 : 3); ++t) {
+          const __nv_bfloat16 *src = (const __nv_bfloat16 *)(t == 0 ? p.b : t == 1 ? p.c : p.a);
+          const int64_t stride = t == 0 ? p.b_stride : t == 1 ? p.c_stride : p.a_stride;
+          const int d = t == 1 ? p.dc : p.da;
+          const bool low = chunk8 * 8 < d, high = 64 + chunk8 * 8 < d;
+          const __nv_bfloat16 *x = src + at * stride + (int64_t)h * d + chunk8 * 8;
+          const int64_t step = 4 * stride;
+          const uint32_t dst = base + s * L::kStage + t * kTile;
+          if (len == kC && d == 128) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i, x += step) {
+            for (int i = 0; i < 8; ++i, x += step) {
               copy16(dst + (i & 1 ? swz1 : swz0) + i * 512, x, true);
               copy16(dst + (i & 1 ? swz1 : swz0) + i * 512 + kBlock, x + 64, true);
             }
           } else {
 #pragma unroll 1
-            for (int i = 0; i < 16; ++i, x += step) {
+            for (int i = 0; i < 8; ++i, x += step) {
               const bool live = place(row0 + 4 * i) < len;
               const uint32_t to = dst + (i & 1 ? swz1 : swz0) + i * 512;
               copy16(to, live && low ? x : src, live && low);
@@ -296,71 +298,73 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(c
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(kFull + s)) : "memory");
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (elect_one()) {
-      // ---------------- products ----------------
-      const int ka = (p.da + 15) / 16;                  // K steps over da
-      const uint32_t kv_desc = idesc_bf16(128, p.dc <= 64 ? 64 : 128) | kIdescMnA | kIdescMnB;
-      auto qk = [&](int c) -> bool {
-        const uint32_t tb = base + (c % L::kStages) * L::kStage;
-        if (!wait(kFull + c % L::kStages, c / L::kStages)) return false;
-        fence_async_smem();                             // the copies' writes, before the products read them
-        tc_fence_after();
-        if (STATES) return true;
-        const Desc a = desc_k(tb + 2 * kTile), x = desc_k(tb);
-#pragma unroll 4
-        for (int k = 0; k < ka; ++k) {
-          const uint32_t off = (k / 4) * kBlock + (k % 4) * 32;
-          mma_bf16(tmem + kColP, a.at(off), x.at(off), idesc_bf16(64, 64), k > 0);
-        }
-        mma_commit(bar(kQK));
-        return true;
-      };
-      bool ok = chunks > 0 && qk(0);
-      for (int c = 0; ok && c < chunks; ++c) {
-        const int s = c % L::kStages;
-        const uint32_t tb = base + s * L::kStage;
-        // the update of S, 32 tokens at a time
-        if (c > 0 && !wait(kKVFree, c - 1)) break;
-        const Desc kt = desc_mn(tb, kBlock);
+    } else if (warp == kMmaWarp - 1) {
+      // ---------------- products: the update of S, 16 tokens at a time ----------------
+      if (elect_one()) {
+        const uint32_t kind = idesc_bf16(128, p.dc <= 64 ? 64 : 128) | kIdescMnA | kIdescMnB;
+        bool ok = true;
+        for (int c = 0; ok && c < chunks; ++c) {
+          const int s = c % L::kStages;
+          if (!wait(kFull + s, c / L::kStages)) break;
+          fence_async_smem();                           // the copies' writes, before the products read them
+          if (c >= 2 && !wait(kKVFree + (c & 1), (c >> 1) - 1)) break;
+          const Desc kt = desc_mn(base + s * L::kStage, kBlock);
 #pragma unroll 1
-        for (int half = 0; half < 2 && ok; ++half) {
-          if (!(ok = wait(kPartsFull + half, c))) break;
-          tc_fence_after();
+          for (int k = 0; k < kC / kStep; ++k) {
+            const int use = c * (kC / kStep) + k;
+            if (!(ok = wait(kPartsFull + (use & 1), use >> 1))) break;
+            tc_fence_after();
+            const Desc w = desc_mn(base + L::kOffParts + (use & 1) * 3 * kPart, kPart / 2);
 #pragma unroll
-          for (int part = 0; part < 3; ++part) {
-            const Desc w = desc_mn(base + L::kOffParts + part * kTile, kBlock);
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-              mma_bf16(tmem + kColKV, kt.at(half * kHalf + k * 2048), w.at(half * kHalf + k * 2048), kv_desc,
-                       half + part + k > 0);
+            for (int part = 0; part < 3; ++part)
+              mma_bf16(tmem + kColKV + 128 * (c & 1), kt.at(k * 2048), w.at(part * kPart), kind, k + part > 0);
+            mma_commit(bar(kPartsEmpty + (use & 1)));
           }
-          mma_commit(bar(kPartsEmpty + half));
+          if (!ok) break;
+          mma_commit(bar(kKV + (c & 1)));
+          mma_commit(bar(kEmpty + s));
         }
-        if (!ok) break;
-        mma_commit(bar(kKV));
-        if (!STATES) {
-          if (!wait(kSReady, c) || (c >= 2 && !wait(kOutFree + (c & 1), (c >> 1) - 1))) break;
+        // every product issued has completed before the memory it uses goes
+        mma_commit(bar(kDrainKV));
+        if (!mbar_wait_for(bar(kDrainKV), 0, kDrainLimitCycles)) raise_timeout();
+      }
+    } else if (!STATES) {
+      // ---------------- products: P, the outputs ----------------
+      if (elect_one()) {
+        const int ka = (p.da + 15) / 16;                // K steps over da
+        const Desc st = desc_mn(base + L::kOffS, kSBlock), pt = desc_k(base + L::kOffP);
+        for (int c = 0; c < chunks; ++c) {
+          const int s = c % L::kStages;
+          const uint32_t tb = base + s * L::kStage;
+          if (!wait(kFull + s, c / L::kStages)) break;
+          fence_async_smem();
           tc_fence_after();
-          const Desc st = desc_mn(base + L::kOffS, kSBlock), a = desc_k(tb + 2 * kTile);
+          const Desc a = desc_k(tb + 2 * kTile), kt = desc_k(tb);
+#pragma unroll 4
+          for (int k = 0; k < ka; ++k) {
+            const uint32_t off = (k / 4) * kBlock + (k % 4) * 32;
+            mma_bf16(tmem + kColP, a.at(off), kt.at(off), idesc_bf16(64, 64), k > 0);
+          }
+          mma_commit(bar(kQK));
+          if ((c > 0 && !wait(kOutFree, c - 1)) || !wait(kSReady, c)) break;
+          tc_fence_after();
 #pragma unroll 4
           for (int k = 0; k < ka; ++k)
-            mma_bf16(tmem + kColInter + 64 * (c & 1), st.at(k * 2048), a.at((k / 4) * kBlock + (k % 4) * 32),
+            mma_bf16(tmem + kColInter, st.at(k * 2048), a.at((k / 4) * kBlock + (k % 4) * 32),
                      idesc_bf16(128, 64) | kIdescMnA, k > 0);
           mma_commit(bar(kQS));
           if (!wait(kPReady, c)) break;
           tc_fence_after();
-          const Desc v = desc_mn(tb + kTile, kBlock), pt = desc_k(base + L::kOffP);
+          const Desc v = desc_mn(tb + kTile, kBlock);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_bf16(tmem + kColIntra + 64 * (c & 1), v.at(k * 2048), pt.at(k * 32), idesc_bf16(128, 64) | kIdescMnA, k > 0);
-          mma_commit(bar(kPV + (c & 1)));
+            mma_bf16(tmem + kColIntra, v.at(k * 2048), pt.at(k * 32), idesc_bf16(128, 64) | kIdescMnA, k > 0);
+          mma_commit(bar(kPV));
+          mma_commit(bar(kEmpty + s));
         }
-        mma_commit(bar(kEmpty + s));
-        if (c + 1 < chunks) ok = qk(c + 1);
+        mma_commit(bar(kDrain));
+        if (!mbar_wait_for(bar(kDrain), 0, kDrainLimitCycles)) raise_timeout();
       }
-      // every product issued has completed before the memory it uses goes
-      mma_commit(bar(kDrain));
-      if (!mbar_wait_for(bar(kDrain), 0, kDrainLimitCycles)) raise_timeout();
     }
   } else if (group == 0) {
     // ---------------- the state ----------------
@@ -401,19 +405,19 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(c
       const int lead = from + (int64_t)c * kC == 0 ? p.first_pow : 1;
       const float keep = decay_pow(g, length_of(c) - 1 + lead);
       const uint64_t keep2 = pair(keep, keep);
-      wait(kKV, c);
+      wait(kKV + (c & 1), c >> 1);
       __syncwarp();
       tc_fence_after();
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         if (q < 2 || p.dc > 64) {                       // narrow states: the upper columns stay zero
           uint64_t x[16];
-          tmem_ld32(quad_addr + kColKV + q * 32, x);
+          tmem_ld32(quad_addr + kColKV + 128 * (c & 1) + q * 32, x);
 #pragma unroll
           for (int i = 0; i < 16; ++i) st[q * 16 + i] = fma2(st[q * 16 + i], keep2, x[i]);
         }
       }
-      arrive(kKVFree);
+      arrive(kKVFree + (c & 1));
     }
     if (has && (STATES || (p.nseg == 1 && p.last))) {
       float *dst = STATES ? states : p.last + bh * p.da * p.dc;
@@ -435,40 +439,47 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(c
     share_registers<L::kRegsParts, L::kRegs>();
     const int tid = threadIdx.x - 128;
     const uint64_t minus = pair(-1.f, -1.f);
-    const int li0 = place(tid / 8), li1 = place(32 + tid / 8);          // the thread's two rows
-    float w0 = pw[kC - 1 - li0], w1 = pw[kC - 1 - li1];
+    const int row = tid / 8 % kStep;                    // of each step's 16; block tid / 128
+    const uint32_t from_tile = tid / 128 * kBlock + row * 128 + tid % 8 * 16;
+    const uint32_t to = base + L::kOffParts + tid / 128 * (kPart / 2) + row * 128 + tid % 8 * 16;
+    float w[kC / kStep];
+#pragma unroll
+    for (int k = 0; k < kC / kStep; ++k) w[k] = pw[kC - 1 - place(k * kStep + row)];
     for (int c = 0; c < chunks; ++c) {
       const int s = c % L::kStages, len = length_of(c);
       if (len < kC) {
-        w0 = li0 < len ? pw[len - 1 - li0] : 0.f;
-        w1 = li1 < len ? pw[len - 1 - li1] : 0.f;
-      }
-      const uint32_t src = base + s * L::kStage + kTile;
-      wait(kFull + s, c / L::kStages);
-#pragma unroll 1
-      for (int half = 0; half < 2; ++half) {
-        if (c > 0) wait(kPartsEmpty + half, c - 1);
-        const float w = half ? w1 : w0;
-        const uint64_t w2 = pair(w, w);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {                   // block i, row half * 32 + tid / 8
-          const uint32_t off = i * kBlock + half * kHalf + tid * 16;
-          uint32_t v[4], p0[4], p1[4], p2[4];
-          lds128(src + off, v);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint64_t x = widen(v[e]);
-            scale_pair(x, w2);
-            p0[e] = narrow(x);
-            x = fma2(widen(p0[e]), minus, x);
-            p1[e] = narrow(x);
-            p2[e] = narrow(fma2(widen(p1[e]), minus, x));
-          }
-          sts128(base + L::kOffParts + off, p0);
-          sts128(base + L::kOffParts + kTile + off, p1);
-          sts128(base + L::kOffParts + 2 * kTile + off, p2);
+        for (int k = 0; k < kC / kStep; ++k) {
+          const int li = place(k * kStep + row);
+          w[k] = li < len ? pw[len - 1 - li] : 0.f;
         }
-        arrive(kPartsFull + half);
+      }
+      wait(kFull + s, c / L::kStages);
+      uint32_t next[4];
+#pragma unroll
+      for (int k = 0; k < kC / kStep; ++k) {
+        uint32_t v[4], p0[4], p1[4], p2[4];
+        if (k == 0) lds128(base + s * L::kStage + kTile + from_tile, next);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = next[e];
+        if (k + 1 < kC / kStep) lds128(base + s * L::kStage + kTile + from_tile + (k + 1) * (kStep * 128), next);
+        const uint64_t w2 = pair(w[k], w[k]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint64_t x = widen(v[e]);
+          scale_pair(x, w2);
+          p0[e] = narrow(x);
+          x = fma2(widen(p0[e]), minus, x);
+          p1[e] = narrow(x);
+          p2[e] = narrow(fma2(widen(p1[e]), minus, x));
+        }
+        const int use = c * (kC / kStep) + k;
+        if (use >= 2) wait(kPartsEmpty + (k & 1), (use >> 1) - 1);
+        const uint32_t dst = to + (k & 1) * 3 * kPart;
+        sts128(dst, p0);
+        sts128(dst + kPart, p1);
+        sts128(dst + 2 * kPart, p2);
+        arrive(kPartsFull + (k & 1));
       }
     }
   } else if (group == 3) {
@@ -487,7 +498,7 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(c
     const uint32_t dst = base + L::kOffP + srow * 128;
     for (int c = 0; c < chunks; ++c) {
       wait(kQK, c);
-      if (c > 0) wait(kPV + ((c - 1) & 1), (c - 1) >> 1);               // the last copy is read
+      if (c > 0) wait(kPV, c - 1);               // the last copy is read
       __syncwarp();
       tc_fence_after();
 #pragma unroll
@@ -530,13 +541,13 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(c
 #pragma unroll
         for (int i = 0; i < 16; ++i) w[i] = p.alpha * pw[place(8 * (i / 2) + 2 * (lane % 4) + i % 2) + lead];
       }
-      wait(kPV + (c & 1), c >> 1);
+      wait(kPV, c);
       __syncwarp();
       tc_fence_after();
       output_barrier();                                 // the last outputs have left the staging
 #pragma unroll
       for (int q = 0; q < 4; ++q) {                     // columns 16 (q / 2) of c, tokens 32 (q % 2)
-        const uint32_t at = quad_addr + ((uint32_t)(q / 2 * 16) << 16) + 64 * (c & 1) + q % 2 * 32;
+        const uint32_t at = quad_addr + ((uint32_t)(q / 2 * 16) << 16) + q % 2 * 32;
         uint32_t x[16], y[16];
         tmem_ld_fragments(at + kColInter, x);
         tmem_ld_fragments(at + kColIntra, y);
@@ -554,7 +565,7 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(c
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kOutFree + (c & 1)));
+      if (lane == 0) mbar_arrive(bar(kOutFree));
       output_barrier();
       __nv_bfloat16 *dst = (__nv_bfloat16 *)p.out +
                            ((b * p.T + (p.reverse ? n - i0 - kC : i0) + tid / 16) * p.H + h) * p.dc + col;
@@ -578,7 +589,7 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(c
   if (warp == kMmaWarp) {
     __syncwarp();
     tc_fence_after();
-    tmem_dealloc(tmem, STATES ? 128 : 512);
+    tmem_dealloc(tmem, STATES ? 256 : 512);
   }
 }
 
