@@ -22,9 +22,9 @@ bool good_eps(float eps) { return std::isfinite(eps) && eps >= 0.f; }
 // Finite, and 1 / scale is too (the backward divides by it).
 bool good_scale(float s) { return std::isfinite(s) && s != 0.f && std::isfinite(1.f / s); }
 
-// A row stride: a multiple of the vector width, wide enough for the row where the tensor is written.
-int check_stride(int64_t stride, int64_t width, int dtype, bool written) {
-  if (stride < 0 || stride > kMaxStride || (written && stride < width)) return ATTNRES_ERR_SHAPE;
+// A row stride: a multiple of the vector width; `apart`: no less than the row's width.
+int check_stride(int64_t stride, int64_t width, int dtype, bool apart) {
+  if (stride < 0 || stride > kMaxStride || (apart && stride < width)) return ATTNRES_ERR_SHAPE;
   return stride % vec_elems(dtype) ? ATTNRES_ERR_ALIGNMENT : ATTNRES_OK;
 }
 
@@ -229,8 +229,8 @@ int attnres_linear_attention(const void *q, const void *k, const void *v, int64_
   int st = check_linear(B, T, H, dk, dv, dtype, rows);
   if (st) return st;
   if (!good_scale(scale)) return ATTNRES_ERR_VALUE;
-  if ((st = check_stride(q_stride, H * dk, dtype, false)) || (st = check_stride(k_stride, H * dk, dtype, false)) ||
-      (st = check_stride(v_stride, H * dv, dtype, false)))
+  if ((st = check_stride(q_stride, H * dk, dtype, true)) || (st = check_stride(k_stride, H * dk, dtype, true)) ||
+      (st = check_stride(v_stride, H * dv, dtype, true)))
     return st;
   if (B == 0 || (rows == 0 && !state_out)) return ATTNRES_OK;
   if (!log_decay || (rows && (!q || !k || !v || !out))) return ATTNRES_ERR_NULL;
@@ -259,9 +259,9 @@ int attnres_linear_attention_backward(const void *q, const void *k, const void *
   int st = check_linear(B, T, H, dk, dv, dtype, rows);
   if (st) return st;
   if (!good_scale(scale)) return ATTNRES_ERR_VALUE;
-  if ((st = check_stride(q_stride, H * dk, dtype, false)) || (st = check_stride(k_stride, H * dk, dtype, false)) ||
-      (st = check_stride(v_stride, H * dv, dtype, false)) ||
-      (st = check_stride(grad_out_stride, H * dv, dtype, false)))
+  if ((st = check_stride(q_stride, H * dk, dtype, true)) || (st = check_stride(k_stride, H * dk, dtype, true)) ||
+      (st = check_stride(v_stride, H * dv, dtype, true)) ||
+      (st = check_stride(grad_out_stride, H * dv, dtype, true)))
     return st;
   if (grad_initial && grad_initial == grad_state) return ATTNRES_ERR_VALUE;
   if (B == 0 || (rows == 0 && !grad_initial)) return ATTNRES_OK;
@@ -304,8 +304,8 @@ int attnres_linear_attention_step(const void *q, const void *k, const void *v, i
   int st = check_linear(B, 1, H, dk, dv, dtype, rows);
   if (st) return st;
   if (!good_scale(scale)) return ATTNRES_ERR_VALUE;
-  if ((st = check_stride(q_stride, H * dk, dtype, false)) || (st = check_stride(k_stride, H * dk, dtype, false)) ||
-      (st = check_stride(v_stride, H * dv, dtype, false)))
+  if ((st = check_stride(q_stride, H * dk, dtype, true)) || (st = check_stride(k_stride, H * dk, dtype, true)) ||
+      (st = check_stride(v_stride, H * dv, dtype, true)))
     return st;
   if (B == 0) return ATTNRES_OK;
   if (!q || !k || !v || !log_decay || !state || !state_out || !out) return ATTNRES_ERR_NULL;

@@ -5,34 +5,42 @@
 // Per chunk of 64 tokens, with S the state before it (da x dc, fp32):
 //   P  = a b^T, masked and decayed                    (M 64,  N 64,  K da)
 //   O^T = S^T a^T (weighted by token) + c^T P^T       (M dc,  N 64,  K da; K 64)
-//   S  <- lambda^n S + b^T (w c), w_j = lambda^{n-1-j} (M da,  N dc,  K 64)
-// The outputs are formed transposed, so that every product but the small P
-// has M = 128, the full rate.  c^T, S^T and b^T are MN-major operands: the
-// tiles are used as they lie in memory, nothing is transposed by threads.
+//   S^T <- lambda^n S^T + (w c)^T b, w_j = lambda^{n-1-j} (M dc, N da, K 64)
+// The outputs and the state are formed transposed, so that every product but
+// the small P has M = 128, the full rate, and S^T is a left operand as it
+// lies: a thread's row of it goes to tensor memory as bf16.  c^T, (w c)^T and
+// b are MN-major operands: the tiles are used as they lie in memory, nothing
+// is transposed by threads.
 //
-// Accuracy.  The state has to keep fp32 accuracy over any number of chunks.
-// w c is therefore split into three bf16 parts (24 bits), so its product is
-// exact to fp32's rounding, and S itself lives in fp32 registers (a thread
-// per row and half of the columns).  P and the copy of S that forms the
-// outputs are rounded to bf16 once: each adds an error of the size of the
-// output's own rounding at most.
+// Accuracy.  The state has to keep fp32 accuracy over any number of chunks:
+// S itself lives in fp32 registers, and w c, which the product takes in bf16,
+// is split into parts.  Three of them (24 bits) make the product exact to
+// fp32's rounding, for a state that may be handed out; two (16 bits, an error
+// of 2^-17 at most) serve the main kernel's where the states' kernel has
+// formed the exact ones.  P and the copy of S that
+// forms the outputs are rounded to bf16 once: each adds an error of the size
+// of the output's own rounding at most.
 //
-// Roles of a CTA, one per SM (a warpgroup of four warps each, but for the
-// last): the state (a thread per row of S, all its columns in registers); two
-// for the weighted parts; P; the outputs; and two warps that copy tiles
-// (cp.async, 16 bytes a lane, straight into the swizzled layout, rows behind
-// the sequence and columns behind the width as zeros; tensor-map copies are
-// served one box at a time per CTA and would cap one CTA per SM at about
-// 4.2 TB/s) beside two threads that issue products, one the updates of S and
-// one all others, so that neither waits for the other's operands.  A warp runs
-// its dependent instructions one in five cycles or so, so what counts is how
-// few instructions each role needs per chunk, and that the roles run side by
-// side: with eight warps doing all of the work in turn a chunk took 7900
-// cycles.
+// Roles of a CTA, one per SM (a warpgroup of four warps each): two for the
+// state (a thread per row of S^T and half of its columns, in registers); two
+// for the weighted parts; P; the outputs; and one with the lanes that copy
+// tiles (tensor-map boxes of 64 tokens x 64 columns, six of them in flight
+// per stage: rows outside the tensor and columns behind the width arrive as
+// zeros) and two threads that issue products, one the updates of S and one
+// all others, so that neither waits for the other's operands.  What binds is
+// the shared memory's 128 bytes per cycle, which the products' operands, the
+// copies and the threads share: S^T as a smem operand, and tiles copied by
+// threads (cp.async), each cost a fifth of it and of the time.  A warp runs
+// its dependent instructions one in five cycles or so, and the roles' code
+// together has to stay within the instruction cache, so what counts besides
+// is how few instructions each role needs per chunk.
 //
 // Every wait is bounded: one that runs out records a flag and an abort mark
 // in shared memory, on which every other wait returns at once; the issuing
 // roles stop and drain what they have in flight, and the CTA ends.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "linear.cuh"
 #include "tcgen05.cuh"
 
@@ -46,42 +54,39 @@ constexpr uint32_t kTile = kC * 128 * 2;              // bytes: 64 tokens x 128 
 constexpr uint32_t kBlock = kTile / 2;
 constexpr int kStep = 16;                             // tokens per step of the weighted parts (an MMA's K)
 constexpr uint32_t kPart = kStep * 128 * 2;           // a part of them: two blocks of 64 columns
-constexpr uint32_t kSBlock = 128 * 128;               // 64 columns of S's 128 rows
 constexpr int kOutPitch = 272;                        // bytes per token of the output staging (no bank met twice)
-constexpr int kCopiers = 2;                           // warps
 
-// The main kernel's warpgroups: S, parts, parts, P, outputs, copies + products;
-// the states' kernel: S, parts, parts, copies + products.
+// The main kernel's warpgroups: S, S, parts, parts, P, outputs, copies and
+// products; the states' kernel: S, S, parts, parts, copies and products.
 template <bool STATES> struct Shape {
-  static constexpr int kGroups = STATES ? 4 : 6;
+  static constexpr int kGroups = STATES ? 5 : 7;
   static constexpr int kThreads = kGroups * 128;
-  static constexpr int kStages = STATES ? 6 : 3;
+  static constexpr int kStages = STATES ? 4 : 3;
   // Registers per thread: as launched (checked at the launch), then each
   // role's share; their sum stays within the launch's.
-  static constexpr int kRegs = STATES ? 128 : 80;
-  static constexpr int kRegsS = STATES ? 184 : 168, kRegsParts = STATES ? 96 : 56, kRegsP = 72, kRegsOut = 88,
-                       kRegsCopy = STATES ? 96 : 40;
-  static_assert(kRegsS + 2 * kRegsParts + (STATES ? 0 : kRegsP + kRegsOut) + kRegsCopy <= kGroups * kRegs,
+  static constexpr int kRegs = STATES ? 96 : 72;
+  static constexpr int kRegsS = STATES ? 104 : 96, kRegsParts = 64, kRegsP = 72, kRegsOut = 80, kRegsMma = 32;
+  static_assert(2 * kRegsS + 2 * kRegsParts + (STATES ? 0 : kRegsP + kRegsOut) + kRegsMma <= kGroups * kRegs,
                 "more registers than the launch has");
   static constexpr uint32_t kStage = (STATES ? 2 : 3) * kTile;      // b, c, [a]
   static constexpr uint32_t kOffParts = kStages * kStage;
-  static constexpr uint32_t kOffP = kOffParts + 2 * 3 * kPart;
-  static constexpr uint32_t kOffS = kOffP + (STATES ? 0 : kC * 128);
-  static constexpr uint32_t kOffOut = kOffS + (STATES ? 0 : 2 * kSBlock);
+  static constexpr uint32_t kOffP = kOffParts + 4 * 3 * kPart;
+  static constexpr uint32_t kOffOut = kOffP + (STATES ? 0 : kC * 128);
   static constexpr uint32_t kOffPow = kOffOut + (STATES ? 0 : kC * kOutPitch);
   static constexpr uint32_t kOffBar = kOffPow + 72 * 4;
-  static constexpr uint32_t kBytes = kOffBar + 30 * 8 + 1024;       // and the alignment's slack
+  static constexpr uint32_t kBytes = kOffBar + 36 * 8 + 1024;       // and the alignment's slack
 };
 
-// Tensor memory columns: the update of S by the chunk's parity, P, the outputs' two sums.
-constexpr uint32_t kColKV = 0, kColP = 256, kColInter = 320, kColIntra = 384;
+// Tensor memory columns: the update of S by the chunk's parity, P, the outputs'
+// two sums, S^T as bf16 pairs.
+constexpr uint32_t kColKV = 0, kColP = 256, kColInter = 320, kColIntra = 384, kColST = 448;
 
 // Barriers, one phase per chunk (full, empty and parts: one per use of a
 // stage or buffer).  A waiter may be at most one phase behind its barrier, or
 // the parity deceives it; the updates of S, which run up to two chunks ahead
 // of the state, therefore have a pair of each, by the chunk's parity.
-enum Bar { kFull = 0, kEmpty = 6, kPartsFull = 12, kPartsEmpty = 14, kKV = 16, kKVFree = 18, kPV = 20, kOutFree, kQK, kSReady,
-           kQS, kPReady, kDrain, kDrainKV, kBars };
+enum Bar { kFull = 0, kEmpty = 4, kPartsFull = 8, kPartsEmpty = 12, kKV = 16, kKVFree = 18, kPV = 20, kOutFree, kQK, kSReady,
+           kQS, kPReady, kClean, kDrain, kDrainKV, kBars };
 
 // A role's share of the registers: it gives some of the launch's back, or
 // takes some that others have given.
@@ -92,9 +97,28 @@ template <int N, int LAUNCHED> __device__ __forceinline__ void share_registers()
 }
 
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+// A box of a [B][H][T][d] view (coordinates innermost first) to shared memory.
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int x, int t, int h, int b, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(t), "r"(h), "r"(b), "r"(bar) : "memory");
 }
+// D[tmem] += A[tmem] B: the left operand from tensor memory, a row per lane.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+// 16 columns of this thread's tensor-memory lane.
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&w)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]),
+        "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15]) : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&w)[4]) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
 }
@@ -134,21 +158,6 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return r;
 }
 
-// 32 columns of this thread's tensor-memory lane, as pairs.
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint64_t (&v)[16]) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(addr));
-  tmem_wait_ld();
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = ((uint64_t)r[2 * i + 1] << 32) | r[2 * i];
-}
 // 16 lanes x 32 columns spread over the warp as four matrix fragments of 16 x
 // 8: pair 2 i + j of a thread is row lane / 4 + 8 j, columns 8 i + 2 (lane %
 // 4) and the next.
@@ -171,8 +180,14 @@ __device__ __forceinline__ void stmatrix4_t(uint32_t addr, const uint32_t (&w)[4
                ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
 }
 
+// The tensors as [B][H][T][d], boxes of 64 tokens x 64 columns.
+struct Maps {
+  CUtensorMap b, c, a;
+};
+
 template <bool STATES>
-__global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(const LinearParams p) {
+__global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
+    linear_tc_kernel(const __grid_constant__ Maps maps, const __grid_constant__ LinearParams p) {
   using L = Shape<STATES>;
   extern __shared__ unsigned char smem_raw[];
   grid_dependency_wait();
@@ -183,8 +198,10 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(c
   auto bar = [&](int b) { return base + L::kOffBar + 8u * b; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp >> 2, quad = warp & 3;
 
-  const int seg = blockIdx.x % p.nseg;
-  const int64_t bh = blockIdx.x / p.nseg, b = bh / p.H;
+  // Neighbouring CTAs take the heads of the same tokens: their rows lie side
+  // by side in memory.
+  const int64_t BH = gridDim.x / p.nseg, bh = blockIdx.x % BH, b = bh / p.H;
+  const int seg = (int)(blockIdx.x / BH);
   const int h = (int)(bh % p.H);
   const int64_t n = seq_length(p, b);
   const int64_t begin = seg * p.seg_len, end = min(p.T, begin + p.seg_len), stop = min(n, end);
@@ -197,27 +214,33 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(c
     if (reach < (float)(stop - begin)) from = max(begin, (stop - 1 - (int64_t)reach) / kC * kC);
   }
   const int chunks = stop > from ? (int)((stop - from + kC - 1) / kC) : 0;
+  // The last chunk of a sequence that ends before the tensor does also gets
+  // the rows behind the sequence; they are cleared in shared memory.
+  const bool unclean = !p.reverse && n < p.T && stop == n;
   const int tail = chunks > 0 ? (int)(stop - from - (int64_t)(chunks - 1) * kC) : 0;   // tokens of the last chunk
 
   if (threadIdx.x == 0) {
     ctl[1] = *reinterpret_cast<volatile unsigned int *>(&g_error_flag) != 0 ? 1u : 0u;
     ctl[2] = 0;
     for (int i = 0; i < L::kStages; ++i) {
-      mbar_init(bar(kFull + i), kCopiers * 32);
+      mbar_init(bar(kFull + i), 1);
       mbar_init(bar(kEmpty + i), STATES ? 1 : 2);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       mbar_init(bar(kPartsFull + i), 8);
       mbar_init(bar(kPartsEmpty + i), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(bar(kKV + i), 1);
-      mbar_init(bar(kKVFree + i), 4);
+      mbar_init(bar(kKVFree + i), 8);
     }
     mbar_init(bar(kQK), 1);
-    mbar_init(bar(kSReady), 4);
+    mbar_init(bar(kSReady), 8);
     mbar_init(bar(kQS), 1);
     mbar_init(bar(kPV), 1);
     mbar_init(bar(kOutFree), 4);
     mbar_init(bar(kPReady), 4);
+    mbar_init(bar(kClean), 8);
     mbar_init(bar(kDrain), 1);
     mbar_init(bar(kDrainKV), 1);
     fence_mbar_init();
@@ -231,19 +254,21 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(c
   tc_fence_after();
   const uint32_t tmem = ctl[0];
 
-  // Wait for the phase; false once any wait of the CTA has run out.
+  // Wait for the phase; false once any wait of the CTA has run out.  The limit
+  // counts from the CTA's start: its whole work takes a few milliseconds, and
+  // a short loop at every wait keeps the roles' code within the instruction
+  // cache.
+  const long long deadline = clock64() + p.wait_limit;
   auto wait = [&](int which, uint32_t parity) -> bool {
-    if (mbar_try(bar(which), parity & 1)) return true;
-    const long long since = clock64();
-    for (;;) {
-      if (mbar_try(bar(which), parity & 1)) return true;
+    const uint32_t at = bar(which);
+    while (!mbar_try(at, parity & 1)) {
       if (ctl[2]) return false;
-      if (clock64() - since > p.wait_limit) {
+      if (clock64() > deadline) {
         ctl[2] = 1;
         raise_timeout();
-        return false;
       }
     }
+    return true;
   };
   // A warp's arrival: its shared-memory writes and tensor-memory reads come first.
   auto arrive = [&](int which) {
@@ -252,73 +277,61 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(c
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(which));
   };
+  // The same where only tensor memory was read.
+  auto release = [&](int which) {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(which));
+  };
   // Token count of chunk c, and a row's place in the walk.
   auto length_of = [&](int c) { return c + 1 < chunks ? kC : tail; };
   auto place = [&](int r) { return p.reverse ? kC - 1 - r : r; };
+  const bool three = STATES || p.nseg == 1;            // parts of w c: this kernel's state is the one handed out
   const uint32_t quad_addr = tmem + ((uint32_t)(quad * 32) << 16);
 
   if (group == L::kGroups - 1) {
-    share_registers<L::kRegsCopy, L::kRegs>();
-    if (warp < kMmaWarp - 1) {
-      // ---------------- copies ----------------
-      // Each warp takes half of the rows of every tensor.
-      const int chunk8 = lane % 8, row0 = (warp - (kMmaWarp - 3)) * 32 + lane / 8;   // a 16-byte piece of rows row0 + 4 i
-      const uint32_t swz0 = row0 * 128 + ((chunk8 ^ (row0 & 7)) << 4), swz1 = swz0 ^ 64;   // i even and odd
+    share_registers<L::kRegsMma, L::kRegs>();
+    auto clean = [&](int c) -> bool { return !(unclean && tail < kC && c + 1 == chunks) || wait(kClean, 0); };
+    if (warp == kMmaWarp - 3) {
+      // ---------------- copies: a box per lane ----------------
+      constexpr int kBoxes = STATES ? 4 : 6;
+      const int t = lane >> 1;
+      const CUtensorMap *map = t == 0 ? &maps.b : t == 1 ? &maps.c : &maps.a;
+      int last = -1;
       for (int c = 0; c < chunks; ++c) {
         const int s = c % L::kStages;
-        if (c >= L::kStages && !wait(kEmpty + s, c / L::kStages - 1)) break;
-        const int len = length_of(c);
+        const bool ok = c < L::kStages || wait(kEmpty + s, c / L::kStages - 1);
+        if (!__all_sync(0xffffffffu, ok)) break;
         const int64_t i0 = from + (int64_t)c * kC;
-        const int64_t at = b * p.T + (p.reverse ? n - i0 - kC : i0) + row0;
-#pragma unroll 1
-        for (int t = 0; t < (STATES ? 2 : 3); ++t) {
-          const __nv_bfloat16 *src = (const __nv_bfloat16 *)(t == 0 ? p.b : t == 1 ? p.c : p.a);
-          const int64_t stride = t == 0 ? p.b_stride : t == 1 ? p.c_stride : p.a_stride;
-          const int d = t == 1 ? p.dc : p.da;
-          const bool low = chunk8 * 8 < d, high = 64 + chunk8 * 8 < d;
-          const __nv_bfloat16 *x = src + at * stride + (int64_t)h * d + chunk8 * 8;
-          const int64_t step = 4 * stride;
-          const uint32_t dst = base + s * L::kStage + t * kTile;
-          if (len == kC && d == 128) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i, x += step) {
-              copy16(dst + (i & 1 ? swz1 : swz0) + i * 512, x, true);
-              copy16(dst + (i & 1 ? swz1 : swz0) + i * 512 + kBlock, x + 64, true);
-            }
-          } else {
-#pragma unroll 1
-            for (int i = 0; i < 8; ++i, x += step) {
-              const bool live = place(row0 + 4 * i) < len;
-              const uint32_t to = dst + (i & 1 ? swz1 : swz0) + i * 512;
-              copy16(to, live && low ? x : src, live && low);
-              copy16(to + kBlock, live && high ? x + 64 : src, live && high);
-            }
-          }
-        }
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar(kFull + s)) : "memory");
+        if (lane == 0) mbar_expect_tx(bar(kFull + s), L::kStage);
+        __syncwarp();
+        if (lane < kBoxes)
+          copy_box(base + s * L::kStage + lane * kBlock, map, (lane & 1) * 64, (int)(p.reverse ? n - i0 - kC : i0), h, (int)b,
+                   bar(kFull + s));
+        last = c;
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
+      // what was copied has landed before the CTA may end
+      for (int c = max(0, last + 1 - L::kStages); c <= last; ++c)
+        if (!mbar_wait_for(bar(kFull + c % L::kStages), (c / L::kStages) & 1, kDrainLimitCycles)) raise_timeout();
     } else if (warp == kMmaWarp - 1) {
       // ---------------- products: the update of S, 16 tokens at a time ----------------
       if (elect_one()) {
-        const uint32_t kind = idesc_bf16(128, p.dc <= 64 ? 64 : 128) | kIdescMnA | kIdescMnB;
+        const uint32_t kind = idesc_bf16(128, p.da <= 64 ? 64 : 128) | kIdescMnA | kIdescMnB;
         bool ok = true;
         for (int c = 0; ok && c < chunks; ++c) {
           const int s = c % L::kStages;
-          if (!wait(kFull + s, c / L::kStages)) break;
-          fence_async_smem();                           // the copies' writes, before the products read them
+          if (!wait(kFull + s, c / L::kStages) || !clean(c)) break;
           if (c >= 2 && !wait(kKVFree + (c & 1), (c >> 1) - 1)) break;
-          const Desc kt = desc_mn(base + s * L::kStage, kBlock);
+          const Desc x = desc_mn(base + s * L::kStage, kBlock);
 #pragma unroll 1
           for (int k = 0; k < kC / kStep; ++k) {
-            const int use = c * (kC / kStep) + k;
-            if (!(ok = wait(kPartsFull + (use & 1), use >> 1))) break;
+            if (!(ok = wait(kPartsFull + k, c))) break;
             tc_fence_after();
-            const Desc w = desc_mn(base + L::kOffParts + (use & 1) * 3 * kPart, kPart / 2);
-#pragma unroll
-            for (int part = 0; part < 3; ++part)
-              mma_bf16(tmem + kColKV + 128 * (c & 1), kt.at(k * 2048), w.at(part * kPart), kind, k + part > 0);
-            mma_commit(bar(kPartsEmpty + (use & 1)));
+            const Desc w = desc_mn(base + L::kOffParts + k * 3 * kPart, kPart / 2);
+            mma_bf16(tmem + kColKV + 128 * (c & 1), w.at(0), x.at(k * 2048), kind, k > 0);
+            mma_bf16(tmem + kColKV + 128 * (c & 1), w.at(kPart), x.at(k * 2048), kind, 1);
+            if (three) mma_bf16(tmem + kColKV + 128 * (c & 1), w.at(2 * kPart), x.at(k * 2048), kind, 1);
+            mma_commit(bar(kPartsEmpty + k));
           }
           if (!ok) break;
           mma_commit(bar(kKV + (c & 1)));
@@ -328,19 +341,18 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(c
         mma_commit(bar(kDrainKV));
         if (!mbar_wait_for(bar(kDrainKV), 0, kDrainLimitCycles)) raise_timeout();
       }
-    } else if (!STATES) {
+    } else if (!STATES && warp == kMmaWarp) {
       // ---------------- products: P, the outputs ----------------
       if (elect_one()) {
         const int ka = (p.da + 15) / 16;                // K steps over da
-        const Desc st = desc_mn(base + L::kOffS, kSBlock), pt = desc_k(base + L::kOffP);
+        const Desc pt = desc_k(base + L::kOffP);
         for (int c = 0; c < chunks; ++c) {
           const int s = c % L::kStages;
           const uint32_t tb = base + s * L::kStage;
-          if (!wait(kFull + s, c / L::kStages)) break;
-          fence_async_smem();
+          if (!wait(kFull + s, c / L::kStages) || !clean(c)) break;
           tc_fence_after();
           const Desc a = desc_k(tb + 2 * kTile), kt = desc_k(tb);
-#pragma unroll 4
+#pragma unroll 2
           for (int k = 0; k < ka; ++k) {
             const uint32_t off = (k / 4) * kBlock + (k % 4) * 32;
             mma_bf16(tmem + kColP, a.at(off), kt.at(off), idesc_bf16(64, 64), k > 0);
@@ -348,10 +360,10 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(c
           mma_commit(bar(kQK));
           if ((c > 0 && !wait(kOutFree, c - 1)) || !wait(kSReady, c)) break;
           tc_fence_after();
-#pragma unroll 4
+#pragma unroll 2
           for (int k = 0; k < ka; ++k)
-            mma_bf16(tmem + kColInter, st.at(k * 2048), a.at((k / 4) * kBlock + (k % 4) * 32),
-                     idesc_bf16(128, 64) | kIdescMnA, k > 0);
+            mma_bf16_ts(tmem + kColInter, tmem + kColST + 8 * k, a.at((k / 4) * kBlock + (k % 4) * 32), idesc_bf16(128, 64),
+                        k > 0);
           mma_commit(bar(kQS));
           if (!wait(kPReady, c)) break;
           tc_fence_after();
@@ -366,78 +378,77 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(c
         if (!mbar_wait_for(bar(kDrain), 0, kDrainLimitCycles)) raise_timeout();
       }
     }
-  } else if (group == 0) {
-    // ---------------- the state ----------------
+  } else if (group <= 1) {
+    // ---------------- the state: a row of S^T per thread, 64 columns per group ----------------
     share_registers<L::kRegsS, L::kRegs>();
-    const int row = quad * 32 + lane;
-    const bool has = row < p.da;
-    uint64_t st[64];                                    // columns 2 j and 2 j + 1
-    float *states = p.states + ((bh * p.nseg + seg) * p.da) * p.dc;
+    const int row = quad * 32 + lane, col0 = group * 64;               // dc, da
+    uint64_t st[32];                                    // columns col0 + 2 j and the next
+    float *states = p.states + ((bh * p.nseg + seg) * p.da + col0) * p.dc + row;
+    const int cols = row < p.dc ? p.da - col0 : 0;      // of this thread's row that exist (da is even)
+    {
+      // the segment's first state, or the call's (which may lie transposed)
+      const bool own = p.nseg > 1, across = !own && p.first_t;
+      const float *src = own ? states : p.first + bh * p.da * p.dc + (across ? (int64_t)row * p.da + col0 : (int64_t)col0 * p.dc + row);
+      const int step = across ? 1 : p.dc;
+      const float f = own ? 1.f : p.first_scale;
+      const int have = !STATES && (own || p.first) ? cols : 0;
 #pragma unroll
-    for (int j = 0; j < 64; ++j) {
-      float x[2] = {0.f, 0.f};
-      if (!STATES && has && 2 * j < p.dc) {             // dc is even
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          if (p.nseg > 1) x[e] = states[(int64_t)row * p.dc + 2 * j + e];
-          else if (p.first) x[e] = first_at(p, bh, row, 2 * j + e);
-        }
-      }
-      st[j] = pair(x[0], x[1]);
+      for (int j = 0; j < 32; ++j, src += 2 * step) st[j] = 2 * j < have ? pair(f * src[0], f * src[step]) : 0ull;
     }
-    // The state's bf16 copy, [da][dc] in blocks of 64 columns.
-    auto publish = [&]() {
-      const uint32_t dst = base + L::kOffS + row * 128;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = narrow(st[j * 4 + i]);
-        sts128(dst + (j / 8) * kSBlock + (((j % 8) ^ (row & 7)) << 4), w);
-      }
-      arrive(kSReady);
-    };
+    const float keep_full = decay_pow(g, kC);
     for (int c = 0; c < chunks; ++c) {
       if (!STATES) {
+        // its bf16 copy in tensor memory
         if (c > 0) wait(kQS, c - 1);                    // the last copy is read
-        publish();
+        __syncwarp();
+        tc_fence_after();
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = narrow(st[q * 16 + i]);
+          tmem_st16(quad_addr + kColST + group * 32 + q * 16, w);
+        }
+        tmem_wait_st();
+        release(kSReady);
       }
       const int lead = from + (int64_t)c * kC == 0 ? p.first_pow : 1;
-      const float keep = decay_pow(g, length_of(c) - 1 + lead);
+      const int steps = length_of(c) - 1 + lead;
+      const float keep = steps == kC ? keep_full : decay_pow(g, steps);
       const uint64_t keep2 = pair(keep, keep);
       wait(kKV + (c & 1), c >> 1);
       __syncwarp();
       tc_fence_after();
+      if (col0 < p.da) {                                // else these columns stay zero
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (q < 2 || p.dc > 64) {                       // narrow states: the upper columns stay zero
-          uint64_t x[16];
-          tmem_ld32(quad_addr + kColKV + 128 * (c & 1) + q * 32, x);
+        for (int q = 0; q < 4; ++q) {
+          float x[16];
+          tmem_ld16(quad_addr + kColKV + 128 * (c & 1) + col0 + q * 16, x);
+          tmem_wait_ld();
 #pragma unroll
-          for (int i = 0; i < 16; ++i) st[q * 16 + i] = fma2(st[q * 16 + i], keep2, x[i]);
+          for (int i = 0; i < 8; ++i) st[q * 8 + i] = fma2(st[q * 8 + i], keep2, pair(x[2 * i], x[2 * i + 1]));
         }
       }
-      arrive(kKVFree + (c & 1));
+      release(kKVFree + (c & 1));
     }
-    if (has && (STATES || (p.nseg == 1 && p.last))) {
-      float *dst = STATES ? states : p.last + bh * p.da * p.dc;
+    if (STATES || (p.nseg == 1 && p.last)) {
+      float *out = STATES ? states : p.last + (bh * p.da + col0) * p.dc + row;
       // no token at all: the state passes through unchanged
       const float f = STATES ? 1.f : p.last_scale * (n > 0 ? decay_pow(g, p.last_pow) : 1.f);
 #pragma unroll
-      for (int j = 0; j < 64; j += 2) {
-        if (2 * j < p.dc) {                             // dc is a multiple of 8
-          float4 x;
-          unpair(st[j], x.x, x.y);
-          unpair(st[j + 1], x.z, x.w);
-          x.x *= f; x.y *= f; x.z *= f; x.w *= f;
-          *reinterpret_cast<float4 *>(dst + (int64_t)row * p.dc + 2 * j) = x;
+      for (int j = 0; j < 32; ++j, out += 2 * p.dc) {
+        if (2 * j < cols) {
+          float x, y;
+          unpair(st[j], x, y);
+          out[0] = x * f;
+          out[p.dc] = y * f;
         }
       }
     }
-  } else if (group <= 2) {
+  } else if (group <= 3) {
     // ---------------- w c in three parts, each in the tile's own layout ----------------
     share_registers<L::kRegsParts, L::kRegs>();
-    const int tid = threadIdx.x - 128;
+    const int tid = threadIdx.x - 2 * 128;
     const uint64_t minus = pair(-1.f, -1.f);
     const int row = tid / 8 % kStep;                    // of each step's 16; block tid / 128
     const uint32_t from_tile = tid / 128 * kBlock + row * 128 + tid % 8 * 16;
@@ -447,23 +458,32 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(c
     for (int k = 0; k < kC / kStep; ++k) w[k] = pw[kC - 1 - place(k * kStep + row)];
     for (int c = 0; c < chunks; ++c) {
       const int s = c % L::kStages, len = length_of(c);
+      wait(kFull + s, c / L::kStages);
       if (len < kC) {
 #pragma unroll
         for (int k = 0; k < kC / kStep; ++k) {
           const int li = place(k * kStep + row);
           w[k] = li < len ? pw[len - 1 - li] : 0.f;
         }
+        if (unclean) {
+          // the rows behind the sequence, of b and c (those of a only reach outputs that are not stored)
+          const uint32_t zero[4] = {0, 0, 0, 0};
+          for (int i = tid; i < (kC - len) * 16; i += 256) {
+            const uint32_t at = base + s * L::kStage + i % 16 / 8 * kBlock + (len + i / 16) * 128 + i % 8 * 16;
+            sts128(at, zero);
+            sts128(at + kTile, zero);
+          }
+          arrive(kClean);
+          wait(kClean, 0);                              // all of them, before the parts are formed
+        }
       }
-      wait(kFull + s, c / L::kStages);
-      uint32_t next[4];
-#pragma unroll
+      const uint32_t src = base + s * L::kStage + kTile + from_tile;
+#pragma unroll 1
       for (int k = 0; k < kC / kStep; ++k) {
         uint32_t v[4], p0[4], p1[4], p2[4];
-        if (k == 0) lds128(base + s * L::kStage + kTile + from_tile, next);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = next[e];
-        if (k + 1 < kC / kStep) lds128(base + s * L::kStage + kTile + from_tile + (k + 1) * (kStep * 128), next);
-        const uint64_t w2 = pair(w[k], w[k]);
+        lds128(src + k * (kStep * 128), v);
+        const float wk = k < 2 ? (k ? w[1] : w[0]) : k == 2 ? w[2] : w[3];
+        const uint64_t w2 = pair(wk, wk);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           uint64_t x = widen(v[e]);
@@ -471,21 +491,20 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(c
           p0[e] = narrow(x);
           x = fma2(widen(p0[e]), minus, x);
           p1[e] = narrow(x);
-          p2[e] = narrow(fma2(widen(p1[e]), minus, x));
+          if (three) p2[e] = narrow(fma2(widen(p1[e]), minus, x));
         }
-        const int use = c * (kC / kStep) + k;
-        if (use >= 2) wait(kPartsEmpty + (k & 1), (use >> 1) - 1);
-        const uint32_t dst = to + (k & 1) * 3 * kPart;
+        if (c > 0) wait(kPartsEmpty + k, c - 1);
+        const uint32_t dst = to + k * 3 * kPart;
         sts128(dst, p0);
         sts128(dst + kPart, p1);
-        sts128(dst + 2 * kPart, p2);
-        arrive(kPartsFull + (k & 1));
+        if (three) sts128(dst + 2 * kPart, p2);
+        arrive(kPartsFull + k);
       }
     }
-  } else if (group == 3) {
+  } else if (!STATES && group == 4) {
     // ---------------- P: 64 rows in the first 16 lanes of each quadrant ----------------
     share_registers<L::kRegsP, L::kRegs>();
-    const int row = quad * 16 + lane / 4, col = 2 * (lane % 4);         // of the thread's first element
+    const int row = quad * 16 + lane / 4, col = 2 * (lane % 4);         // of P: the thread's first element
     float w[32];                                        // its 32 weights (alpha, the decay, the mask) stay the same
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -498,7 +517,7 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(c
     const uint32_t dst = base + L::kOffP + srow * 128;
     for (int c = 0; c < chunks; ++c) {
       wait(kQK, c);
-      if (c > 0) wait(kPV, c - 1);               // the last copy is read
+      if (c > 0) wait(kPV, c - 1);                    // the last copy of P is read
       __syncwarp();
       tc_fence_after();
 #pragma unroll
@@ -507,7 +526,7 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(c
         tmem_ld_fragments(quad_addr + kColP + q * 32, x);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 4; i += 2) {                // columns 32 q + 8 i: two fragments of 16 x 8
+        for (int i = 0; i < 4; i += 2) {              // columns 32 q + 8 i: two fragments of 16 x 8
           uint32_t v[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -521,10 +540,10 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(c
       }
       arrive(kPReady);
     }
-  } else {
+  } else if (!STATES) {
     // ---------------- outputs: weights, sum, transposition through shared memory, store ----------------
     share_registers<L::kRegsOut, L::kRegs>();
-    const int tid = threadIdx.x - 4 * 128;
+    const int tid = threadIdx.x - 5 * 128;
     float w[16];                                        // alpha and the decay of the thread's 16 tokens
     int lead = -1;
     // the matrix stores: this lane names a token's row and 8 columns of c
@@ -545,31 +564,32 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(c
       __syncwarp();
       tc_fence_after();
       output_barrier();                                 // the last outputs have left the staging
+#pragma unroll 1
+      for (int m = 0; m < 2; ++m) {                     // columns 16 m of this warp's 32
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {                     // columns 16 (q / 2) of c, tokens 32 (q % 2)
-        const uint32_t at = quad_addr + ((uint32_t)(q / 2 * 16) << 16) + q % 2 * 32;
-        uint32_t x[16], y[16];
-        tmem_ld_fragments(at + kColInter, x);
-        tmem_ld_fragments(at + kColIntra, y);
-        tmem_wait_ld();
+        for (int q = 0; q < 2; ++q) {                   // tokens 32 q
+          const uint32_t at = quad_addr + ((uint32_t)(m * 16) << 16) + q * 32;
+          uint32_t x[16], y[16];
+          tmem_ld_fragments(at + kColInter, x);
+          tmem_ld_fragments(at + kColIntra, y);
+          tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-          uint32_t v[4];
+          for (int i = 0; i < 4; i += 2) {
+            uint32_t v[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int e = 4 * i + 2 * j, t = 8 * (q % 2) + 2 * (i + j / 2);
-            v[j] = narrow(fma2(joined(x[e], x[e + 1]), pair(w[t], w[t + 1]), joined(y[e], y[e + 1])));
+            for (int j = 0; j < 4; ++j) {
+              const int e = 4 * i + 2 * j, t = 8 * q + 2 * (i + j / 2);
+              v[j] = narrow(fma2(joined(x[e], x[e + 1]), pair(w[t], w[t + 1]), joined(y[e], y[e + 1])));
+            }
+            stmatrix4_t(put + (q * 32 + i * 8) * kOutPitch + m * 32, v);
           }
-          stmatrix4_t(put + (q % 2 * 32 + i * 8) * kOutPitch + q / 2 * 32, v);
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kOutFree));
+      release(kOutFree);
       output_barrier();
       __nv_bfloat16 *dst = (__nv_bfloat16 *)p.out +
                            ((b * p.T + (p.reverse ? n - i0 - kC : i0) + tid / 16) * p.H + h) * p.dc + col;
-#pragma unroll
+#pragma unroll 2
       for (int i = 0; i < 8; ++i, dst += step) {
         if (place(i * 8 + tid / 16) < len && col < p.dc) {
           uint32_t v[4];
@@ -579,10 +599,8 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1) linear_tc_kernel(c
       }
     }
     // rows behind the sequence are zero
-    const int64_t first_row = max(stop, begin);
-    const int v = p.dc / 8;
-    for (int64_t k = tid; k < (end - first_row) * v; k += 128)
-      st_vec((__nv_bfloat16 *)p.out + ((b * p.T + first_row + k / v) * p.H + h) * p.dc + k % v * 8, make_uint4(0, 0, 0, 0));
+    for (int64_t t = max(stop, begin) + tid / 16; t < end; t += 8)
+      if (col < p.dc) st_vec((__nv_bfloat16 *)p.out + ((b * p.T + t) * p.H + h) * p.dc + col, make_uint4(0, 0, 0, 0));
     tc_fence_before();
   }
   __syncthreads();
@@ -628,12 +646,38 @@ template <bool STATES> bool registers_as_planned() {
   }();
   return ok;
 }
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+    void *ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+  }();
+  return fn;
+}
+// A [B, T, H, d] tensor whose token rows are `stride` elements apart.
+bool encode(CUtensorMap &m, const void *x, int64_t stride, int64_t B, int64_t T, int H, int d) {
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)T, (cuuint64_t)H, (cuuint64_t)B};
+  const cuuint64_t strides[3] = {(cuuint64_t)stride * 2, (cuuint64_t)d * 2, (cuuint64_t)(T * stride) * 2};
+  const cuuint32_t box[4] = {64, kC, 1, 1}, ones[4] = {1, 1, 1, 1};
+  return encode_fn()(&m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(x), dims, strides, box, ones,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool STATES> cudaError_t launch_chunks(const LinearParams &p, int64_t BH, cudaStream_t stream) {
   using L = Shape<STATES>;
-  if (!registers_as_planned<STATES>()) return cudaErrorInvalidConfiguration;
+  if (!registers_as_planned<STATES>() || !encode_fn()) return cudaErrorInvalidConfiguration;
+  Maps m;
+  const int64_t B = BH / p.H;
+  if (!encode(m.b, p.b, p.b_stride, B, p.T, p.H, p.da) || !encode(m.c, p.c, p.c_stride, B, p.T, p.H, p.dc) ||
+      !encode(m.a, p.a, p.a_stride, B, p.T, p.H, p.da))
+    return cudaErrorInvalidValue;
   const cudaError_t e = cudaFuncSetAttribute(linear_tc_kernel<STATES>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kBytes);
   if (e != cudaSuccess) return e;
-  return launch_dependent(linear_tc_kernel<STATES>, dim3((unsigned)(BH * p.nseg)), dim3(L::kThreads), L::kBytes, stream, p);
+  return launch_dependent(linear_tc_kernel<STATES>, dim3((unsigned)(BH * p.nseg)), dim3(L::kThreads), L::kBytes, stream, m, p);
 }
 }  // namespace
 
