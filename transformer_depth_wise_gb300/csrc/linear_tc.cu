@@ -52,25 +52,26 @@ namespace {
 constexpr int kC = kChunk;
 constexpr uint32_t kTile = kC * 128 * 2;              // bytes: 64 tokens x 128 columns, two blocks of 64 columns
 constexpr uint32_t kBlock = kTile / 2;
-constexpr int kStep = 16;                             // tokens per step of the weighted parts (an MMA's K)
+constexpr int kStep = 32;                             // tokens per step of the weighted parts
 constexpr uint32_t kPart = kStep * 128 * 2;           // a part of them: two blocks of 64 columns
 constexpr int kOutPitch = 272;                        // bytes per token of the output staging (no bank met twice)
 
 // The main kernel's warpgroups: S, S, parts, parts, P, outputs, copies and
-// products; the states' kernel: S, S, parts, parts, copies and products.
+// products; the states' kernel: S, S, four for the parts, copies and products.
 template <bool STATES> struct Shape {
-  static constexpr int kGroups = STATES ? 5 : 7;
+  static constexpr int kGroups = 7;
   static constexpr int kThreads = kGroups * 128;
   static constexpr int kStages = STATES ? 4 : 3;
   // Registers per thread: as launched (checked at the launch), then each
   // role's share; their sum stays within the launch's.
-  static constexpr int kRegs = STATES ? 96 : 72;
-  static constexpr int kRegsS = STATES ? 104 : 96, kRegsParts = 64, kRegsP = 72, kRegsOut = 80, kRegsMma = 32;
-  static_assert(2 * kRegsS + 2 * kRegsParts + (STATES ? 0 : kRegsP + kRegsOut) + kRegsMma <= kGroups * kRegs,
+  static constexpr int kRegs = 72;
+  static constexpr int kPartGroups = STATES ? 4 : 2;
+  static constexpr int kRegsS = 96, kRegsParts = 64, kRegsP = 72, kRegsOut = 80, kRegsMma = 32;
+  static_assert(2 * kRegsS + kPartGroups * kRegsParts + (STATES ? 0 : kRegsP + kRegsOut) + kRegsMma <= kGroups * kRegs,
                 "more registers than the launch has");
   static constexpr uint32_t kStage = (STATES ? 2 : 3) * kTile;      // b, c, [a]
   static constexpr uint32_t kOffParts = kStages * kStage;
-  static constexpr uint32_t kOffP = kOffParts + 4 * 3 * kPart;
+  static constexpr uint32_t kOffP = kOffParts + 2 * 3 * kPart;
   static constexpr uint32_t kOffOut = kOffP + (STATES ? 0 : kC * 128);
   static constexpr uint32_t kOffPow = kOffOut + (STATES ? 0 : kC * kOutPitch);
   static constexpr uint32_t kOffBar = kOffPow + 72 * 4;
@@ -85,7 +86,7 @@ constexpr uint32_t kColKV = 0, kColP = 256, kColInter = 320, kColIntra = 384, kC
 // stage or buffer).  A waiter may be at most one phase behind its barrier, or
 // the parity deceives it; the updates of S, which run up to two chunks ahead
 // of the state, therefore have a pair of each, by the chunk's parity.
-enum Bar { kFull = 0, kEmpty = 4, kPartsFull = 8, kPartsEmpty = 12, kKV = 16, kKVFree = 18, kPV = 20, kOutFree, kQK, kSReady,
+enum Bar { kFull = 0, kEmpty = 4, kPartsFull = 8, kPartsEmpty = 10, kKV = 12, kKVFree = 14, kPV = 16, kOutFree, kQK, kSReady,
            kQS, kPReady, kClean, kDrain, kDrainKV, kBars };
 
 // A role's share of the registers: it gives some of the launch's back, or
@@ -226,11 +227,9 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
       mbar_init(bar(kFull + i), 1);
       mbar_init(bar(kEmpty + i), STATES ? 1 : 2);
     }
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(bar(kPartsFull + i), 8);
-      mbar_init(bar(kPartsEmpty + i), 1);
-    }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(bar(kPartsFull + i), 4 * L::kPartGroups);
+      mbar_init(bar(kPartsEmpty + i), 1);
       mbar_init(bar(kKV + i), 1);
       mbar_init(bar(kKVFree + i), 8);
     }
@@ -240,7 +239,7 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
     mbar_init(bar(kPV), 1);
     mbar_init(bar(kOutFree), 4);
     mbar_init(bar(kPReady), 4);
-    mbar_init(bar(kClean), 8);
+    mbar_init(bar(kClean), 4 * L::kPartGroups);
     mbar_init(bar(kDrain), 1);
     mbar_init(bar(kDrainKV), 1);
     fence_mbar_init();
@@ -314,7 +313,7 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
       for (int c = max(0, last + 1 - L::kStages); c <= last; ++c)
         if (!mbar_wait_for(bar(kFull + c % L::kStages), (c / L::kStages) & 1, kDrainLimitCycles)) raise_timeout();
     } else if (warp == kMmaWarp - 1) {
-      // ---------------- products: the update of S, 16 tokens at a time ----------------
+      // ---------------- products: the update of S, 32 tokens at a time ----------------
       if (elect_one()) {
         const uint32_t kind = idesc_bf16(128, p.da <= 64 ? 64 : 128) | kIdescMnA | kIdescMnB;
         bool ok = true;
@@ -328,9 +327,13 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
             if (!(ok = wait(kPartsFull + k, c))) break;
             tc_fence_after();
             const Desc w = desc_mn(base + L::kOffParts + k * 3 * kPart, kPart / 2);
-            mma_bf16(tmem + kColKV + 128 * (c & 1), w.at(0), x.at(k * 2048), kind, k > 0);
-            mma_bf16(tmem + kColKV + 128 * (c & 1), w.at(kPart), x.at(k * 2048), kind, 1);
-            if (three) mma_bf16(tmem + kColKV + 128 * (c & 1), w.at(2 * kPart), x.at(k * 2048), kind, 1);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint64_t y = x.at((2 * k + i) * 2048);
+              mma_bf16(tmem + kColKV + 128 * (c & 1), w.at(i * 2048), y, kind, k + i > 0);
+              mma_bf16(tmem + kColKV + 128 * (c & 1), w.at(kPart + i * 2048), y, kind, 1);
+              if (three) mma_bf16(tmem + kColKV + 128 * (c & 1), w.at(2 * kPart + i * 2048), y, kind, 1);
+            }
             mma_commit(bar(kPartsEmpty + k));
           }
           if (!ok) break;
@@ -445,30 +448,32 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
         }
       }
     }
-  } else if (group <= 3) {
+  } else if (group < 2 + L::kPartGroups) {
     // ---------------- w c in three parts, each in the tile's own layout ----------------
     share_registers<L::kRegsParts, L::kRegs>();
     const int tid = threadIdx.x - 2 * 128;
     const uint64_t minus = pair(-1.f, -1.f);
-    const int row = tid / 8 % kStep;                    // of each step's 16; block tid / 128
-    const uint32_t from_tile = tid / 128 * kBlock + row * 128 + tid % 8 * 16;
-    const uint32_t to = base + L::kOffParts + tid / 128 * (kPart / 2) + row * 128 + tid % 8 * 16;
-    float w[kC / kStep];
+    // 16 bytes of a row at a time; kPer of them per step, kRows rows apart
+    constexpr int kRows = L::kPartGroups * 8, kPer = kStep / kRows;
+    const int row = tid / 8 % kRows, block = tid / 8 / kRows;
+    const uint32_t from_tile = block * kBlock + row * 128 + tid % 8 * 16;
+    const uint32_t to = base + L::kOffParts + block * (kPart / 2) + row * 128 + tid % 8 * 16;
+    float w[kC / kRows];
 #pragma unroll
-    for (int k = 0; k < kC / kStep; ++k) w[k] = pw[kC - 1 - place(k * kStep + row)];
+    for (int k = 0; k < kC / kRows; ++k) w[k] = pw[kC - 1 - place(k * kRows + row)];
     for (int c = 0; c < chunks; ++c) {
       const int s = c % L::kStages, len = length_of(c);
       wait(kFull + s, c / L::kStages);
       if (len < kC) {
 #pragma unroll
-        for (int k = 0; k < kC / kStep; ++k) {
-          const int li = place(k * kStep + row);
+        for (int k = 0; k < kC / kRows; ++k) {
+          const int li = place(k * kRows + row);
           w[k] = li < len ? pw[len - 1 - li] : 0.f;
         }
         if (unclean) {
           // the rows behind the sequence, of b and c (those of a only reach outputs that are not stored)
           const uint32_t zero[4] = {0, 0, 0, 0};
-          for (int i = tid; i < (kC - len) * 16; i += 256) {
+          for (int i = tid; i < (kC - len) * 16; i += L::kPartGroups * 128) {
             const uint32_t at = base + s * L::kStage + i % 16 / 8 * kBlock + (len + i / 16) * 128 + i % 8 * 16;
             sts128(at, zero);
             sts128(at + kTile, zero);
@@ -480,24 +485,29 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
       const uint32_t src = base + s * L::kStage + kTile + from_tile;
 #pragma unroll 1
       for (int k = 0; k < kC / kStep; ++k) {
-        uint32_t v[4], p0[4], p1[4], p2[4];
-        lds128(src + k * (kStep * 128), v);
-        const float wk = k < 2 ? (k ? w[1] : w[0]) : k == 2 ? w[2] : w[3];
-        const uint64_t w2 = pair(wk, wk);
+        uint32_t v[kPer][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint64_t x = widen(v[e]);
-          scale_pair(x, w2);
-          p0[e] = narrow(x);
-          x = fma2(widen(p0[e]), minus, x);
-          p1[e] = narrow(x);
-          if (three) p2[e] = narrow(fma2(widen(p1[e]), minus, x));
-        }
+        for (int i = 0; i < kPer; ++i) lds128(src + (k * kStep + i * kRows) * 128, v[i]);
         if (c > 0) wait(kPartsEmpty + k, c - 1);
-        const uint32_t dst = to + k * 3 * kPart;
-        sts128(dst, p0);
-        sts128(dst + kPart, p1);
-        if (three) sts128(dst + 2 * kPart, p2);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+          const float wk = k ? w[kPer + i] : w[i];
+          const uint64_t w2 = pair(wk, wk);
+          uint32_t p0[4], p1[4], p2[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint64_t x = widen(v[i][e]);
+            scale_pair(x, w2);
+            p0[e] = narrow(x);
+            x = fma2(widen(p0[e]), minus, x);
+            p1[e] = narrow(x);
+            if (three) p2[e] = narrow(fma2(widen(p1[e]), minus, x));
+          }
+          const uint32_t dst = to + k * 3 * kPart + i * kRows * 128;
+          sts128(dst, p0);
+          sts128(dst + kPart, p1);
+          if (three) sts128(dst + 2 * kPart, p2);
+        }
         arrive(kPartsFull + k);
       }
     }
