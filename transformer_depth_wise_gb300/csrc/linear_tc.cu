@@ -52,8 +52,6 @@ namespace {
 constexpr int kC = kChunk;
 constexpr uint32_t kTile = kC * 128 * 2;              // bytes: 64 tokens x 128 columns, two blocks of 64 columns
 constexpr uint32_t kBlock = kTile / 2;
-constexpr int kStep = 32;                             // tokens per step of the weighted parts
-constexpr uint32_t kPart = kStep * 128 * 2;           // a part of them: two blocks of 64 columns
 constexpr int kOutPitch = 272;                        // bytes per token of the output staging (no bank met twice)
 
 // The main kernel's warpgroups: S, S, parts, parts, P, outputs, copies and
@@ -66,6 +64,11 @@ template <bool STATES> struct Shape {
   // role's share; their sum stays within the launch's.
   static constexpr int kRegs = 72;
   static constexpr int kPartGroups = STATES ? 4 : 2;
+  // The weighted parts are formed in steps of kStep tokens, two steps' buffers
+  // alternating: whole chunks in the states' kernel, half of one where the
+  // outputs need the room.
+  static constexpr int kStep = STATES ? 64 : 32;
+  static constexpr uint32_t kPart = kStep * 128 * 2;                // one part: two blocks of 64 columns
   static constexpr int kRegsS = 96, kRegsParts = 64, kRegsP = 72, kRegsOut = 80, kRegsMma = 32;
   static_assert(2 * kRegsS + kPartGroups * kRegsParts + (STATES ? 0 : kRegsP + kRegsOut) + kRegsMma <= kGroups * kRegs,
                 "more registers than the launch has");
@@ -313,7 +316,7 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
       for (int c = max(0, last + 1 - L::kStages); c <= last; ++c)
         if (!mbar_wait_for(bar(kFull + c % L::kStages), (c / L::kStages) & 1, kDrainLimitCycles)) raise_timeout();
     } else if (warp == kMmaWarp - 1) {
-      // ---------------- products: the update of S, 32 tokens at a time ----------------
+      // ---------------- products: the update of S, step by step ----------------
       if (elect_one()) {
         const uint32_t kind = idesc_bf16(128, p.da <= 64 ? 64 : 128) | kIdescMnA | kIdescMnB;
         bool ok = true;
@@ -323,18 +326,19 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
           if (c >= 2 && !wait(kKVFree + (c & 1), (c >> 1) - 1)) break;
           const Desc x = desc_mn(base + s * L::kStage, kBlock);
 #pragma unroll 1
-          for (int k = 0; k < kC / kStep; ++k) {
-            if (!(ok = wait(kPartsFull + k, c))) break;
+          for (int k = 0; k < kC / L::kStep; ++k) {
+            const int use = c * (kC / L::kStep) + k;
+            if (!(ok = wait(kPartsFull + (use & 1), use >> 1))) break;
             tc_fence_after();
-            const Desc w = desc_mn(base + L::kOffParts + k * 3 * kPart, kPart / 2);
+            const Desc w = desc_mn(base + L::kOffParts + (use & 1) * 3 * L::kPart, L::kPart / 2);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint64_t y = x.at((2 * k + i) * 2048);
+            for (int i = 0; i < L::kStep / 16; ++i) {
+              const uint64_t y = x.at((L::kStep / 16 * k + i) * 2048);
               mma_bf16(tmem + kColKV + 128 * (c & 1), w.at(i * 2048), y, kind, k + i > 0);
-              mma_bf16(tmem + kColKV + 128 * (c & 1), w.at(kPart + i * 2048), y, kind, 1);
-              if (three) mma_bf16(tmem + kColKV + 128 * (c & 1), w.at(2 * kPart + i * 2048), y, kind, 1);
+              mma_bf16(tmem + kColKV + 128 * (c & 1), w.at(L::kPart + i * 2048), y, kind, 1);
+              if (three) mma_bf16(tmem + kColKV + 128 * (c & 1), w.at(2 * L::kPart + i * 2048), y, kind, 1);
             }
-            mma_commit(bar(kPartsEmpty + k));
+            mma_commit(bar(kPartsEmpty + (use & 1)));
           }
           if (!ok) break;
           mma_commit(bar(kKV + (c & 1)));
@@ -454,10 +458,10 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
     const int tid = threadIdx.x - 2 * 128;
     const uint64_t minus = pair(-1.f, -1.f);
     // 16 bytes of a row at a time; kPer of them per step, kRows rows apart
-    constexpr int kRows = L::kPartGroups * 8, kPer = kStep / kRows;
+    constexpr int kRows = L::kPartGroups * 8, kPer = L::kStep / kRows;
     const int row = tid / 8 % kRows, block = tid / 8 / kRows;
     const uint32_t from_tile = block * kBlock + row * 128 + tid % 8 * 16;
-    const uint32_t to = base + L::kOffParts + block * (kPart / 2) + row * 128 + tid % 8 * 16;
+    const uint32_t to = base + L::kOffParts + block * (L::kPart / 2) + row * 128 + tid % 8 * 16;
     float w[kC / kRows];
 #pragma unroll
     for (int k = 0; k < kC / kRows; ++k) w[k] = pw[kC - 1 - place(k * kRows + row)];
@@ -484,14 +488,15 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
       }
       const uint32_t src = base + s * L::kStage + kTile + from_tile;
 #pragma unroll 1
-      for (int k = 0; k < kC / kStep; ++k) {
+      for (int k = 0; k < kC / L::kStep; ++k) {
         uint32_t v[kPer][4];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) lds128(src + (k * kStep + i * kRows) * 128, v[i]);
-        if (c > 0) wait(kPartsEmpty + k, c - 1);
+        for (int i = 0; i < kPer; ++i) lds128(src + (k * L::kStep + i * kRows) * 128, v[i]);
+        const int use = c * (kC / L::kStep) + k;
+        if (use >= 2) wait(kPartsEmpty + (use & 1), (use >> 1) - 1);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-          const float wk = k ? w[kPer + i] : w[i];
+          const float wk = k ? w[kC / kRows - kPer + i] : w[i];
           const uint64_t w2 = pair(wk, wk);
           uint32_t p0[4], p1[4], p2[4];
 #pragma unroll
@@ -503,12 +508,12 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
             p1[e] = narrow(x);
             if (three) p2[e] = narrow(fma2(widen(p1[e]), minus, x));
           }
-          const uint32_t dst = to + k * 3 * kPart + i * kRows * 128;
+          const uint32_t dst = to + (use & 1) * 3 * L::kPart + i * kRows * 128;
           sts128(dst, p0);
-          sts128(dst + kPart, p1);
-          if (three) sts128(dst + 2 * kPart, p2);
+          sts128(dst + L::kPart, p1);
+          if (three) sts128(dst + 2 * L::kPart, p2);
         }
-        arrive(kPartsFull + k);
+        arrive(kPartsFull + (use & 1));
       }
     }
   } else if (!STATES && group == 4) {
