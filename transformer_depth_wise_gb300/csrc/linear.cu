@@ -244,29 +244,41 @@ __global__ void __launch_bounds__(kThreads) linear_general_kernel(const LinearPa
 }
 
 // The segments' own states become the states they begin with; the state
-// after the last token is written where it is wanted.  One thread per element.
+// after the last token is written where it is wanted.  Four elements of a row
+// per thread, the next segments' on their way while one is added.
 __global__ void __launch_bounds__(kThreads) linear_scan_kernel(const LinearParams p) {
   grid_dependency_wait();
-  const int per = p.da * p.dc;
+  const int per = p.da * p.dc / 4;
   const int64_t bh = blockIdx.y;
   const int e = blockIdx.x * kThreads + threadIdx.x;
   if (e >= per) return;
   const int64_t n = seq_length(p, bh / p.H);
   const float g = p.log_decay[bh % p.H];
-  float cur = p.first ? first_at(p, bh, e / p.dc, e % p.dc) : 0.f;
-  float *st = p.states + bh * p.nseg * per + e;
+  const int row = e * 4 / p.dc, col = e * 4 % p.dc;      // dc is a multiple of 4
+  float4 cur = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (p.first)
+    cur = make_float4(first_at(p, bh, row, col), first_at(p, bh, row, col + 1), first_at(p, bh, row, col + 2),
+                      first_at(p, bh, row, col + 3));
+  float4 *st = reinterpret_cast<float4 *>(p.states) + bh * p.nseg * per + e;
   const float full = decay_pow(g, p.seg_len);
-  float next = st[0];
+  auto read = [&](int s) { return s < p.nseg ? st[(int64_t)s * per] : make_float4(0.f, 0.f, 0.f, 0.f); };
+  float4 own = read(0), next = read(1), after = read(2);
   for (int s = 0; s < p.nseg; ++s) {
-    const float own = next;
-    if (s + 1 < p.nseg) next = st[(int64_t)(s + 1) * per];
+    const float4 later = read(s + 3);
     st[(int64_t)s * per] = cur;
-    const int64_t len = min(p.T, (s + 1) * p.seg_len) - s * p.seg_len, left = n - s * p.seg_len;
-    if (left <= 0) continue;
-    if (s > 0 && left >= p.seg_len && len == p.seg_len) cur = fmaf(cur, full, own);
-    else cur = fmaf(cur, decay_pow(g, min(len, left) - (s == 0 ? 1 - p.first_pow : 0)), own);
+    const int64_t left = n - s * p.seg_len;
+    if (left > 0) {
+      const float keep = s > 0 && left >= p.seg_len ? full : decay_pow(g, min(p.seg_len, left) - (s == 0 ? 1 - p.first_pow : 0));
+      cur = make_float4(fmaf(cur.x, keep, own.x), fmaf(cur.y, keep, own.y), fmaf(cur.z, keep, own.z), fmaf(cur.w, keep, own.w));
+    }
+    own = next;
+    next = after;
+    after = later;
   }
-  if (p.last) p.last[bh * per + e] = cur * p.last_scale * (n > 0 ? decay_pow(g, p.last_pow) : 1.f);
+  if (p.last) {
+    const float f = p.last_scale * (n > 0 ? decay_pow(g, p.last_pow) : 1.f);
+    reinterpret_cast<float4 *>(p.last)[bh * per + e] = make_float4(cur.x * f, cur.y * f, cur.z * f, cur.w * f);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -429,7 +441,7 @@ cudaError_t launch_linear(const LinearArgs &a) {
   if (p.nseg > 1) {
     cudaError_t e = chunks(true);
     if (e != cudaSuccess) return e;
-    e = launch_dependent(linear_scan_kernel, dim3((unsigned)((a.da * a.dc + kThreads - 1) / kThreads), (unsigned)BH),
+    e = launch_dependent(linear_scan_kernel, dim3((unsigned)((a.da * a.dc / 4 + kThreads - 1) / kThreads), (unsigned)BH),
                          dim3(kThreads), 0, a.stream, p);
     if (e != cudaSuccess) return e;
   }

@@ -50,6 +50,7 @@ namespace attnres {
 namespace {
 
 constexpr int kC = kChunk;
+constexpr int kMaxRanked = 512;                       // heads that the states' kernel orders by their decay
 constexpr uint32_t kTile = kC * 128 * 2;              // bytes: 64 tokens x 128 columns, two blocks of 64 columns
 constexpr uint32_t kBlock = kTile / 2;
 constexpr int kOutPitch = 272;                        // bytes per token of the output staging (no bank met twice)
@@ -64,11 +65,12 @@ template <bool STATES> struct Shape {
   // role's share; their sum stays within the launch's.
   static constexpr int kRegs = 72;
   static constexpr int kPartGroups = STATES ? 4 : 2;
-  // The weighted parts are formed in steps of kStep tokens, two steps' buffers
-  // alternating: whole chunks in the states' kernel, half of one where the
-  // outputs need the room.
+  // The weighted parts are formed in steps of kStep tokens (whole chunks in
+  // the states' kernel, half of one where the outputs need the room) by two
+  // teams, each with a buffer of its own, that take the steps in turn.
   static constexpr int kStep = STATES ? 64 : 32;
   static constexpr uint32_t kPart = kStep * 128 * 2;                // one part: two blocks of 64 columns
+  static constexpr int kTeam = kPartGroups * 64;                    // threads of a team
   static constexpr int kRegsS = 96, kRegsParts = 64, kRegsP = 72, kRegsOut = 80, kRegsMma = 32;
   static_assert(2 * kRegsS + kPartGroups * kRegsParts + (STATES ? 0 : kRegsP + kRegsOut) + kRegsMma <= kGroups * kRegs,
                 "more registers than the launch has");
@@ -204,8 +206,32 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
 
   // Neighbouring CTAs take the heads of the same tokens: their rows lie side
   // by side in memory.
-  const int64_t BH = gridDim.x / p.nseg, bh = blockIdx.x % BH, b = bh / p.H;
-  const int seg = (int)(blockIdx.x / BH);
+  const int64_t BH = gridDim.x / p.nseg;
+  int64_t bh = blockIdx.x % BH;
+  int seg = (int)(blockIdx.x / BH);
+  if (STATES && p.H > 1 && p.H <= kMaxRanked) {
+    // A head with a strong decay needs the end of a segment only (below), so
+    // the slow ones, a segment's whole length of work, go first: CTAs in
+    // the order of the heads' decays.
+    int *decays = reinterpret_cast<int *>(sm);          // as integers of the same order (any bits at all have one)
+    int *found = reinterpret_cast<int *>(sm + kMaxRanked * 4);
+    for (int i = threadIdx.x; i < p.H; i += L::kThreads) {
+      const int x = __float_as_int(p.log_decay[i]);
+      decays[i] = x ^ ((x >> 31) & 0x7fffffff);
+    }
+    __syncthreads();
+    const int64_t per = BH / p.H * p.nseg, rank = blockIdx.x / per, rest = blockIdx.x % per;
+    for (int i = threadIdx.x; i < p.H; i += L::kThreads) {
+      int before = 0;
+      for (int j = 0; j < p.H; ++j) before += decays[j] > decays[i] || (decays[j] == decays[i] && j < i);
+      if (before == rank) *found = i;
+    }
+    __syncthreads();
+    bh = rest % (BH / p.H) * p.H + *found;
+    seg = (int)(rest / (BH / p.H));
+    __syncthreads();
+  }
+  const int64_t b = bh / p.H;
   const int h = (int)(bh % p.H);
   const int64_t n = seq_length(p, b);
   const int64_t begin = seg * p.seg_len, end = min(p.T, begin + p.seg_len), stop = min(n, end);
@@ -231,7 +257,7 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
       mbar_init(bar(kEmpty + i), STATES ? 1 : 2);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(kPartsFull + i), 4 * L::kPartGroups);
+      mbar_init(bar(kPartsFull + i), L::kTeam / 32);
       mbar_init(bar(kPartsEmpty + i), 1);
       mbar_init(bar(kKV + i), 1);
       mbar_init(bar(kKVFree + i), 8);
@@ -242,7 +268,7 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
     mbar_init(bar(kPV), 1);
     mbar_init(bar(kOutFree), 4);
     mbar_init(bar(kPReady), 4);
-    mbar_init(bar(kClean), 4 * L::kPartGroups);
+    mbar_init(bar(kClean), 8);
     mbar_init(bar(kDrain), 1);
     mbar_init(bar(kDrainKV), 1);
     fence_mbar_init();
@@ -455,29 +481,33 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
   } else if (group < 2 + L::kPartGroups) {
     // ---------------- w c in three parts, each in the tile's own layout ----------------
     share_registers<L::kRegsParts, L::kRegs>();
-    const int tid = threadIdx.x - 2 * 128;
-    const uint64_t minus = pair(-1.f, -1.f);
+    constexpr int kSteps = kC / L::kStep;               // per chunk
+    constexpr int kRows = L::kTeam / 16, kPer = L::kStep / kRows;
+    const int team = (threadIdx.x - 2 * 128) / L::kTeam, tid = (threadIdx.x - 2 * 128) % L::kTeam;
     // 16 bytes of a row at a time; kPer of them per step, kRows rows apart
-    constexpr int kRows = L::kPartGroups * 8, kPer = L::kStep / kRows;
     const int row = tid / 8 % kRows, block = tid / 8 / kRows;
-    const uint32_t from_tile = block * kBlock + row * 128 + tid % 8 * 16;
-    const uint32_t to = base + L::kOffParts + block * (L::kPart / 2) + row * 128 + tid % 8 * 16;
-    float w[kC / kRows];
+    const int row0 = (kSteps == 2 ? team * L::kStep : 0) + row;        // of the chunk
+    const uint32_t src = base + kTile + block * kBlock + row0 * 128 + tid % 8 * 16;
+    const uint32_t dst = base + L::kOffParts + team * 3 * L::kPart + block * (L::kPart / 2) + row * 128 + tid % 8 * 16;
+    const uint64_t minus = pair(-1.f, -1.f);
+    float w[kPer];
 #pragma unroll
-    for (int k = 0; k < kC / kRows; ++k) w[k] = pw[kC - 1 - place(k * kRows + row)];
-    for (int c = 0; c < chunks; ++c) {
-      const int s = c % L::kStages, len = length_of(c);
+    for (int i = 0; i < kPer; ++i) w[i] = pw[kC - 1 - place(row0 + i * kRows)];
+    for (int use = team; use < chunks * kSteps; use += 2) {
+      const int c = use / kSteps, s = c % L::kStages, len = length_of(c);
       wait(kFull + s, c / L::kStages);
       if (len < kC) {
 #pragma unroll
-        for (int k = 0; k < kC / kRows; ++k) {
-          const int li = place(k * kRows + row);
-          w[k] = li < len ? pw[len - 1 - li] : 0.f;
+        for (int i = 0; i < kPer; ++i) {
+          const int li = place(row0 + i * kRows);
+          w[i] = li < len ? pw[len - 1 - li] : 0.f;
         }
         if (unclean) {
-          // the rows behind the sequence, of b and c (those of a only reach outputs that are not stored)
+          // the rows behind the sequence, of b and c (those of a only reach
+          // outputs that are not stored), by the 256 threads that work on
+          // this chunk
           const uint32_t zero[4] = {0, 0, 0, 0};
-          for (int i = tid; i < (kC - len) * 16; i += L::kPartGroups * 128) {
+          for (int i = kSteps == 2 ? threadIdx.x - 2 * 128 : tid; i < (kC - len) * 16; i += 256) {
             const uint32_t at = base + s * L::kStage + i % 16 / 8 * kBlock + (len + i / 16) * 128 + i % 8 * 16;
             sts128(at, zero);
             sts128(at + kTile, zero);
@@ -486,18 +516,15 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
           wait(kClean, 0);                              // all of them, before the parts are formed
         }
       }
-      const uint32_t src = base + s * L::kStage + kTile + from_tile;
-#pragma unroll 1
-      for (int k = 0; k < kC / L::kStep; ++k) {
-        uint32_t v[kPer][4];
+      if (use >= 2) wait(kPartsEmpty + team, (use >> 1) - 1);
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) lds128(src + (k * L::kStep + i * kRows) * 128, v[i]);
-        const int use = c * (kC / L::kStep) + k;
-        if (use >= 2) wait(kPartsEmpty + (use & 1), (use >> 1) - 1);
+      for (int i0 = 0; i0 < kPer; i0 += 2) {
+        uint32_t v[2][4];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          const float wk = k ? w[kC / kRows - kPer + i] : w[i];
-          const uint64_t w2 = pair(wk, wk);
+        for (int i = 0; i < 2; ++i) lds128(src + s * L::kStage + (i0 + i) * kRows * 128, v[i]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint64_t w2 = pair(w[i0 + i], w[i0 + i]);
           uint32_t p0[4], p1[4], p2[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -508,13 +535,13 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
             p1[e] = narrow(x);
             if (three) p2[e] = narrow(fma2(widen(p1[e]), minus, x));
           }
-          const uint32_t dst = to + (use & 1) * 3 * L::kPart + i * kRows * 128;
-          sts128(dst, p0);
-          sts128(dst + L::kPart, p1);
-          if (three) sts128(dst + 2 * L::kPart, p2);
+          const uint32_t to = dst + (i0 + i) * kRows * 128;
+          sts128(to, p0);
+          sts128(to + L::kPart, p1);
+          if (three) sts128(to + 2 * L::kPart, p2);
         }
-        arrive(kPartsFull + (use & 1));
       }
+      arrive(kPartsFull + team);
     }
   } else if (!STATES && group == 4) {
     // ---------------- P: 64 rows in the first 16 lanes of each quadrant ----------------
