@@ -282,17 +282,19 @@ int attnres_linear_attention_backward(const void *q, const void *k, const void *
   a.first = state; a.first_t = true; a.first_pow = 1; a.first_scale = 1.f;
   cudaError_t e = cudaSuccess;
   if (rows) e = launch_linear(a);
-  // dk, backwards: scale F(v, grad_out, q) + grad_state^T's part, which scale does not multiply
+  // dv, backwards: scale F(k, q, grad_out) + grad_state's part, which scale
+  // does not multiply; its last state is the initial one's gradient
   a.reverse = true;
-  a.first = grad_state; a.first_pow = 0; a.first_scale = 1.f / scale;
-  a.a = v; a.a_stride = v_stride; a.b = grad_out; a.b_stride = grad_out_stride; a.c = q; a.c_stride = q_stride;
-  a.out = dk_out;
-  if (rows && e == cudaSuccess) e = launch_linear(a);
-  // dv, backwards: scale F(k, q, grad_out) + grad_state's part; its last state is the initial one's gradient
+  a.first = grad_state; a.first_t = false; a.first_pow = 0; a.first_scale = 1.f / scale;
   a.a = k; a.a_stride = k_stride; a.b = q; a.b_stride = q_stride; a.c = grad_out; a.c_stride = grad_out_stride;
-  a.da = (int)dk; a.dc = (int)dv; a.first_t = false; a.out = dv_out;
+  a.da = (int)dk; a.dc = (int)dv; a.out = dv_out;
   a.last = grad_initial; a.last_scale = scale; a.last_pow = 1;
   if (e == cudaSuccess) e = launch_linear(a);
+  // dk, backwards: scale F(v, grad_out, q) + grad_state^T's part; its states are dv's, transposed
+  a.a = v; a.a_stride = v_stride; a.b = grad_out; a.b_stride = grad_out_stride; a.c = q; a.c_stride = q_stride;
+  a.da = (int)dv; a.dc = (int)dk; a.first_t = true; a.out = dk_out; a.last = nullptr;
+  a.states_ready = a.states_t = true;
+  if (rows && e == cudaSuccess) e = launch_linear(a);
   return cuda_status(e);
 }
 

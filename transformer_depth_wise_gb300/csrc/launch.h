@@ -256,6 +256,8 @@ struct LinearArgs {              // out_i = alpha (sum_{j <= i} e^{g (i - j)} (a
   float last_scale;              // times this ...
   int last_pow;                  // ... and e^{g last_pow}
   float *workspace;
+  bool states_ready;             // the workspace holds the segments' first states already ...
+  bool states_t;                 // ... as [.., dc, da]: another call's with a and c's roles exchanged
   cudaStream_t stream;
 };
 bool linear_supported(int64_t da, int64_t dc, int dtype);

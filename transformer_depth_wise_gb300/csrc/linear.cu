@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kThreads) linear_general_kernel(const LinearPa
       const int col = col0 + tx * 4 + j;
       s[m][j] = 0.f;
       if (!STATES && row < p.da && col < p.dc) {
-        if (p.nseg > 1) s[m][j] = states[(int64_t)row * p.dc + col];
+        if (p.nseg > 1) s[m][j] = p.states_t ? states[(int64_t)col * p.da + row] : states[(int64_t)row * p.dc + col];
         else if (p.first) s[m][j] = first_at(p, bh, row, col);
       }
     }
@@ -388,12 +388,12 @@ bool linear_supported(int64_t da, int64_t dc, int dtype) {
 
 // Segments of the general kernel: enough CTAs for two per SM, but none
 // shorter than 256 tokens (a segment's state costs as much traffic as about
-// 128 tokens).
+// 128 tokens).  The same with da and dc exchanged, so that two calls can share
+// the segments' states.
 int linear_segments(int64_t B, int64_t T, int H, int da, int dc, int dtype) {
-  (void)da;
   if (B * H < 1) return 1;
   if (linear_tc_supported(T, dtype)) return linear_tc_segments(B * H, T);
-  const int64_t have = B * H * general_slices(dc), want = 2 * (int64_t)sm_count();
+  const int64_t have = B * H * general_slices(da > dc ? da : dc), want = 2 * (int64_t)sm_count();
   int64_t n = (want + have - 1) / have;
   const int64_t most = T / 256;
   if (n > most) n = most;
@@ -419,6 +419,7 @@ cudaError_t launch_linear(const LinearArgs &a) {
   p.first = a.first; p.first_t = a.first_t; p.first_pow = a.first_pow; p.first_scale = a.first_scale;
   p.last = a.last; p.last_scale = a.last_scale; p.last_pow = a.last_pow;
   p.states = a.workspace;
+  p.states_t = a.states_t;
   p.wait_limit = wait_limit_cycles();
   const int64_t BH = a.B * a.H;
   const bool tc = linear_tc_supported(a.T, a.dtype);
@@ -438,7 +439,7 @@ cudaError_t launch_linear(const LinearArgs &a) {
     };
     return a.dtype == ATTNRES_BF16 ? with_da(__nv_bfloat16{}) : with_da(float{});
   };
-  if (p.nseg > 1) {
+  if (p.nseg > 1 && !a.states_ready) {
     cudaError_t e = chunks(true);
     if (e != cudaSuccess) return e;
     e = launch_dependent(linear_scan_kernel, dim3((unsigned)((a.da * a.dc / 4 + kThreads - 1) / kThreads), (unsigned)BH),

@@ -24,6 +24,7 @@ struct LinearParams {
   float last_scale;
   int last_pow;
   float *states;                       // [B, H, nseg, da, dc] (nseg > 1)
+  int states_t;                        // or [.., dc, da], for the main kernel
   long long wait_limit;                // SM clock cycles any wait of the tensor-core kernel may take
 };
 

@@ -420,8 +420,9 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
     const int cols = row < p.dc ? p.da - col0 : 0;      // of this thread's row that exist (da is even)
     {
       // the segment's first state, or the call's (which may lie transposed)
-      const bool own = p.nseg > 1, across = !own && p.first_t;
-      const float *src = own ? states : p.first + bh * p.da * p.dc + (across ? (int64_t)row * p.da + col0 : (int64_t)col0 * p.dc + row);
+      const bool own = p.nseg > 1, across = own ? p.states_t : p.first_t;
+      const float *src = (own ? p.states + (bh * p.nseg + seg) * p.da * p.dc : p.first + bh * p.da * p.dc) +
+                         (across ? (int64_t)row * p.da + col0 : (int64_t)col0 * p.dc + row);
       const int step = across ? 1 : p.dc;
       const float f = own ? 1.f : p.first_scale;
       const int have = !STATES && (own || p.first) ? cols : 0;
