@@ -270,7 +270,8 @@ int attnres_rms_norm(const void *x, int64_t B, int64_t T, int64_t D, int dtype, 
  * key or value tensor is [B, T, H, d] with the heads of a token side by side
  * (head stride d) and the B*T token rows evenly spaced, `stride` elements
  * apart (H * d when contiguous; more when q, k and v are views of one
- * projection's output).  Strides are multiples of 8 (bf16) or 4 (fp32).
+ * projection's output; linear attention wants no less than H * d, so rows may
+ * not overlap).  Strides are multiples of 8 (bf16) or 4 (fp32).
  * As above, pointers are 16-byte aligned (those to positions, lengths, page
  * tables, decays, frequencies and lse: to their element), arithmetic and
  * statistics are fp32, outputs are rounded once, nothing is allocated and the
@@ -388,9 +389,11 @@ int64_t attnres_paged_attention_workspace_bytes(int Hq, int Hk, int64_t d, int d
  *   state_out   device fp32 [B,H,dk,dv] S after each sequence's last token, or NULL; may be state
  *   workspace   device, attnres_linear_attention_workspace_bytes() bytes (may
  *               be 0, then NULL is allowed); contents on entry do not matter
- * bf16 inputs: products on the tensor cores with fp32 accumulators and an
- * fp32 state; the masked products and the state are rounded to bf16 where
- * they enter the product that forms out.
+ * bf16 inputs of 64 tokens and more: products on the tensor cores with fp32
+ * accumulators and an fp32 state; the masked products and the state are
+ * rounded to bf16 where they enter the product that forms out.  Prompts are
+ * worked on in chunks of 64 tokens: a NaN or infinity in a token's q, k or v
+ * may also show in out of the tokens before it in its chunk.
  */
 int attnres_linear_attention(const void *q, const void *k, const void *v, int64_t B, int64_t T, int H, int64_t dk,
                              int64_t dv, int dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride,

@@ -93,6 +93,7 @@ def test_linear_refusals():
     assert linear(q=None) == NULL and linear(g=None) == NULL and linear(out=None) == NULL
     assert linear(qs=4) == ALIGN and linear(q=FAKE + 8) == ALIGN and linear(state=FAKE + 8) == ALIGN
     assert linear(g=FAKE + 2) == ALIGN and linear(n=FAKE + 1) == ALIGN
+    assert linear(qs=64) == SHAPE and linear(qs=0) == SHAPE                # overlapping rows
     assert linear(B=0, q=None, g=None, out=None, ws=None) == OK and linear(T=0, q=None, out=None) == OK
     size = _lib.lib().attnres_linear_attention_workspace_bytes
     assert size(1, 100, 2, 64, 64, 1) >= 0 and size(1, 100, 0, 64, 64, 1) == SHAPE and size(1, 1, 1, 4, 8, 1) == ALIGN

@@ -624,31 +624,39 @@ def block_two_phase(blocks, queries, gains, u, eps: float = 1e-8, fused: bool = 
 def _call(name: str, device: torch.device, *args) -> None:
     """The C entry point on `device`'s current stream, with that device current."""
     fn = getattr(_lib.lib(), name)
-    if device.index is None or device.index == torch.cuda.current_device():
-        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    index = device.index
+    if index == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(device):
-            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    _lib.check(name, rc)
+            rc = fn(*args, _raw_stream(index))
+    if rc < 0:
+        _lib.check(name, rc)
+
+
+# The current stream's handle without a Stream object in between.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _sized(name: str, device: torch.device, *args) -> int:
     """A workspace query with `device` current."""
     fn = getattr(_lib.lib(), name)
-    if device.index is None or device.index == torch.cuda.current_device():
+    if device.index == torch.cuda.current_device():
         n = fn(*args)
     else:
         with torch.cuda.device(device):
             n = fn(*args)
-    return _lib.check(name, int(n))
+    return n if n >= 0 else _lib.check(name, int(n))
 
 
 def _heads(t, name: str, like=None, shape=None) -> int:
     """Row stride of a head tensor [.., H, d]: the heads of a token side by side, the rows evenly spaced."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    have = t.shape
+    if shape is not None and have != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(have)}")
     if like is not None:
         if t.dtype != like.dtype:
             raise TypeError(f"{name} must be {like.dtype}")
@@ -656,44 +664,54 @@ def _heads(t, name: str, like=None, shape=None) -> int:
             raise ValueError(f"{name} must be on {like.device}")
     elif t.dtype not in _CODES:
         _code(t)
-    H, d = t.shape[-2:]
     st = t.stride()
-    if t.numel() and ((d > 1 and st[-1] != 1) or (H > 1 and st[-2] != d)):
-        raise ValueError(f"{name}: the heads of a token must lie side by side")
-    if t.dim() == 3:
-        return st[0] if t.shape[0] > 1 else H * d
-    if t.dim() != 4:
+    if len(st) == 4:
+        B, T, H, d = have
+        sb, stt = st[0], st[1]
+    elif len(st) == 3:
+        T, H, d = have
+        B, sb, stt = 1, 0, st[0]
+    else:
         raise ValueError(f"{name} must be [B, T, H, d]")
-    B, T = t.shape[:2]
-    if B > 1 and T > 1:
-        if st[0] != T * st[1] and t.numel():
+    if (d > 1 and st[-1] != 1) or (H > 1 and st[-2] != d):
+        if t.numel():
+            raise ValueError(f"{name}: the heads of a token must lie side by side")
+    if T > 1:
+        if B > 1 and sb != T * stt and t.numel():
             raise ValueError(f"{name}: its token rows must be evenly spaced")
-        return st[1]
-    return st[1] if T > 1 else st[0] if B > 1 else H * d
+        return stt
+    return sb if B > 1 else H * d
 
 
 def _plain(t, name: str, dtype, shape, device):
     """A contiguous CUDA tensor of this dtype and shape on `device` (None stays None)."""
     if t is None:
         return None
+    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t
     _cuda(t, name)
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    return t
+    raise ValueError(f"{name} must be on {device}")
+
+
+def _given(t, name: str, dtype, shape, device):
+    """_plain for a tensor that may not be None."""
+    if t is None:
+        _cuda(t, name)
+    return _plain(t, name, dtype, shape, device)
 
 
 def _workspace(t, nbytes: int, device):
     """The caller's workspace, or one of `nbytes` allocated here; (tensor, address, bytes)."""
     if t is None:
         t = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    else:
-        _cuda(t, "workspace")
-        if t.device != device:
-            raise ValueError(f"workspace must be on {device}")
+        return t, t.data_ptr() or None, nbytes
+    _cuda(t, "workspace")
+    if t.device != device:
+        raise ValueError(f"workspace must be on {device}")
     return t, t.data_ptr() or None, t.numel() * t.element_size()
 
 
@@ -718,8 +736,9 @@ def _norm_args(q, k, q_weight, k_weight, positions, inv_freq):
     _plain(positions, "positions", torch.int32, (B, T), dev)
     rot = 0
     if inv_freq is not None:
-        rot = 2 * inv_freq.numel()
-        _plain(inv_freq, "inv_freq", torch.float64, (rot // 2,), dev)
+        pairs = inv_freq.numel()
+        rot = 2 * pairs
+        _plain(inv_freq, "inv_freq", torch.float64, (pairs,), dev)
     return B, T, Hq, Hk, d, qs, ks, rot
 
 
@@ -732,10 +751,13 @@ def head_norm_rotate(q, k, q_weight=None, k_weight=None, positions=None, inv_fre
     """
     B, T, Hq, Hk, d, qs, ks, rot = _norm_args(q, k, q_weight, k_weight, positions, inv_freq)
     if q_out is None:
-        q_out = torch.empty((B, T, Hq, d), dtype=q.dtype, device=q.device)
+        q_out, qos = torch.empty((B, T, Hq, d), dtype=q.dtype, device=q.device), Hq * d
+    else:
+        qos = _heads(q_out, "q_out", q, q.shape)
     if k_out is None:
-        k_out = torch.empty((B, T, Hk, d), dtype=q.dtype, device=q.device)
-    qos, kos = _heads(q_out, "q_out", q, q.shape), _heads(k_out, "k_out", q, k.shape)
+        k_out, kos = torch.empty((B, T, Hk, d), dtype=q.dtype, device=q.device), Hk * d
+    else:
+        kos = _heads(k_out, "k_out", q, k.shape)
     _call("attnres_head_norm_rotate", q.device, q.data_ptr(), k.data_ptr(), B, T, Hq, Hk, d, _CODES[q.dtype], qs, ks,
           _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq), rot, 1 if interleaved else 0, float(eps),
           q_out.data_ptr(), k_out.data_ptr(), qos, kos)
@@ -754,8 +776,9 @@ def head_norm_rotate_append(q, k, v, q_weight, k_weight, positions, inv_freq, k_
     vs = _heads(v, "v", q, (B, T, Hk, d))
     num_pages, page_size, max_pages = _cache_args(k_cache, v_cache, page_table, q, B, Hk, d)
     if q_out is None:
-        q_out = torch.empty((B, T, Hq, d), dtype=q.dtype, device=dev)
-    qos = _heads(q_out, "q_out", q, q.shape)
+        q_out, qos = torch.empty((B, T, Hq, d), dtype=q.dtype, device=dev), Hq * d
+    else:
+        qos = _heads(q_out, "q_out", q, q.shape)
     _call("attnres_head_norm_rotate_append", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), B, T, Hq, Hk, d,
           _CODES[q.dtype], qs, ks, vs, _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq), rot,
           1 if interleaved else 0, float(eps), q_out.data_ptr(), qos, k_cache.data_ptr(), v_cache.data_ptr(),
@@ -764,18 +787,20 @@ def head_norm_rotate_append(q, k, v, q_weight, k_weight, positions, inv_freq, k_
 
 
 def _cache_args(k_cache, v_cache, page_table, q, B, Hk, d):
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        _cuda(t, name)
-        if t.dim() != 4 or t.shape[1] != Hk or t.shape[3] != d or t.shape != k_cache.shape:
-            raise ValueError(f"{name} must be [num_pages, {Hk}, page_size, {d}]")
-        if t.dtype != q.dtype:
-            raise TypeError(f"{name} must be {q.dtype}")
-        if t.device != q.device:
-            raise ValueError(f"{name} must be on {q.device}")
+    _cuda(k_cache, "k_cache")
+    have = k_cache.shape
+    if len(have) != 4 or have[1] != Hk or have[3] != d:
+        raise ValueError(f"k_cache must be [num_pages, {Hk}, page_size, {d}]")
+    if k_cache.dtype != q.dtype:
+        raise TypeError(f"k_cache must be {q.dtype}")
+    if k_cache.device != q.device:
+        raise ValueError(f"k_cache must be on {q.device}")
+    _given(v_cache, "v_cache", q.dtype, have, q.device)
     if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
         raise ValueError("page_table must be a [B, max_pages] tensor")
-    _plain(page_table, "page_table", torch.int32, (B, page_table.shape[1]), q.device)
-    return k_cache.shape[0], k_cache.shape[2], page_table.shape[1]
+    pages = page_table.shape[1]
+    _plain(page_table, "page_table", torch.int32, (B, pages), q.device)
+    return have[0], have[2], pages
 
 
 def head_norm_rotate_backward(q, k, q_weight, k_weight, positions, inv_freq, eps: float, grad_q, grad_k,
@@ -822,14 +847,15 @@ def paged_attention(q, k_cache, v_cache, page_table, lengths, scale: float, out=
     dev, code = q.device, _CODES[q.dtype]
     Hk = k_cache.shape[1] if isinstance(k_cache, torch.Tensor) and k_cache.dim() == 4 else 0
     num_pages, page_size, max_pages = _cache_args(k_cache, v_cache, page_table, q, B, Hk, d)
-    _cuda(lengths, "lengths")
-    _plain(lengths, "lengths", torch.int32, (B,), dev)
+    _given(lengths, "lengths", torch.int32, (B,), dev)
     if out is None:
         out = torch.empty((B, Hq, d), dtype=q.dtype, device=dev)
+    else:
+        _plain(out, "out", q.dtype, q.shape, dev)
     if lse is None:
         lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
-    _plain(out, "out", q.dtype, q.shape, dev)
-    _plain(lse, "lse", torch.float32, (B, Hq), dev)
+    else:
+        _plain(lse, "lse", torch.float32, (B, Hq), dev)
     need = 0
     if workspace is None:
         need = _sized("attnres_paged_attention_workspace_bytes", dev, Hq, Hk, d, code)
@@ -851,8 +877,7 @@ def _linear_args(q, k, v, log_decay, lengths, state):
     dv = v.shape[3]
     vs = _heads(v, "v", q, (B, T, H, dv))
     dev = q.device
-    _cuda(log_decay, "log_decay")
-    _plain(log_decay, "log_decay", torch.float32, (H,), dev)
+    _given(log_decay, "log_decay", torch.float32, (H,), dev)
     _plain(lengths, "lengths", torch.int32, (B,), dev)
     _plain(state, "state", torch.float32, (B, H, dk, dv), dev)
     return B, T, H, dk, dv, qs, ks, vs
@@ -924,16 +949,16 @@ def linear_attention_step(q, k, v, log_decay, scale: float, state, state_out=Non
     dv = v.shape[2]
     vs = _heads(v, "v", q, (B, H, dv))
     dev = q.device
-    _cuda(log_decay, "log_decay")
-    _plain(log_decay, "log_decay", torch.float32, (H,), dev)
-    _cuda(state, "state")
-    _plain(state, "state", torch.float32, (B, H, dk, dv), dev)
+    _given(log_decay, "log_decay", torch.float32, (H,), dev)
+    _given(state, "state", torch.float32, (B, H, dk, dv), dev)
     if state_out is None:
         state_out = state
-    _plain(state_out, "state_out", torch.float32, (B, H, dk, dv), dev)
+    else:
+        _plain(state_out, "state_out", torch.float32, (B, H, dk, dv), dev)
     if out is None:
         out = torch.empty((B, H, dv), dtype=q.dtype, device=dev)
-    _plain(out, "out", q.dtype, (B, H, dv), dev)
+    else:
+        _plain(out, "out", q.dtype, (B, H, dv), dev)
     _call("attnres_linear_attention_step", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), B, H, dk, dv,
           _CODES[q.dtype], qs, ks, vs, log_decay.data_ptr(), float(scale), state.data_ptr(), state_out.data_ptr(),
           out.data_ptr())

@@ -24,8 +24,8 @@ bool good_scale(float s) { return std::isfinite(s) && s != 0.f && std::isfinite(
 
 // A row stride: a multiple of the vector width; `apart`: no less than the row's width.
 int check_stride(int64_t stride, int64_t width, int dtype, bool apart) {
-  if (stride < 0 || stride > kMaxStride || (apart && stride < width)) return ATTNRES_ERR_SHAPE;
-  return stride % vec_elems(dtype) ? ATTNRES_ERR_ALIGNMENT : ATTNRES_OK;
+  if (stride % vec_elems(dtype)) return ATTNRES_ERR_ALIGNMENT;
+  return stride < 0 || stride > kMaxStride || (apart && stride < width) ? ATTNRES_ERR_SHAPE : ATTNRES_OK;
 }
 
 int check_batch(int64_t B, int64_t T, int dtype, int64_t &rows) {
