@@ -11,15 +11,18 @@
 // Everything is bound by memory (each element is read and written once, with
 // a few dozen operations).  A head is held by a team of TEAM lanes, each
 // with the two 16-byte vectors whose elements pair up, so the rotation needs
-// no exchange and the norm one shuffle reduction.  A CTA takes a few token
-// rows at a time: its threads first form the rows' angles once in shared
-// memory (one cosine and sine per token and pair instead of one per head),
-// with the first heads' loads already in flight.
+// no exchange and the norm one shuffle reduction.  A warp takes a token row
+// (or a part of its heads) at a time: its lanes form the row's angles once in
+// shared memory of the warp's own, one cosine and sine per token and pair
+// instead of one per head, and go through the heads with several of them in
+// flight; no warp waits for another.
 //
 // Angles.  A frequency is kept as a 64-bit fraction of a turn per position,
 // and position * step wraps modulo one turn exactly, so far positions lose
 // nothing: the angle is off by the rounding of inv_freq / 2 pi in 64 bits and
 // by 2^-25 of half a turn when its upper 32 bits become an fp32 argument.
+// The fraction is formed in integers (the mantissa times 2^66 / 2 pi), since
+// fp64 instructions run at a sixty-fourth of the rate.
 #include <type_traits>
 
 #include "common.cuh"
@@ -29,13 +32,21 @@ namespace attnres {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr double kInvTwoPi = 0.15915494309189533577;
+constexpr int kWarps = kThreads / 32;
 
-// inv_freq (radians per position) as 2^-64ths of a turn per position.
+// inv_freq (radians per position) as 2^-64ths of a turn per position, modulo
+// one turn; 0 for what is no number.
 __device__ __forceinline__ uint64_t turn_step(double inv_freq) {
-  double turns = inv_freq * kInvTwoPi;
-  turns -= floor(turns);                       // in [0, 1]: 1 only by rounding of a tiny negative
-  return turns < 1.0 ? (uint64_t)(turns * 18446744073709551616.0) : 0ull;
+  const uint64_t bits = (uint64_t)__double_as_longlong(inv_freq);
+  const int exponent = (int)((bits >> 52) & 0x7ff) - 1023;
+  if (exponent < -1000 || exponent > 53) return 0;          // nothing, or beyond any use
+  const uint64_t mantissa = (bits & 0xfffffffffffffull) | 0x10000000000000ull;
+  constexpr uint64_t kPerTurn = 11743562013128004906ull;    // 2^66 / (2 pi), rounded
+  const uint64_t lo = mantissa * kPerTurn, hi = __umul64hi(mantissa, kPerTurn);
+  // the product times 2^(exponent - 52 - 66 + 64)
+  const int right = 54 - exponent;
+  const uint64_t t = right >= 128 ? 0 : right >= 64 ? hi >> (right - 64) : right == 0 ? lo : (lo >> right) | (hi << (64 - right));
+  return bits >> 63 ? 0 - t : t;
 }
 
 // cosine and sine of `position` steps.
@@ -84,6 +95,41 @@ __device__ __forceinline__ void turn(float *x, const float2 *cs, float dir) {
   }
 }
 
+// A lane's share of the weight, or ones.
+template <typename T>
+__device__ __forceinline__ void load_weight(float *w, const float *src, int off0, int off1) {
+  constexpr int E = Elt<T>::EPV;
+#pragma unroll
+  for (int j = 0; j < E; j += 4) {
+    const float4 a = src ? ld_f4(src + off0 + j) : make_float4(1.f, 1.f, 1.f, 1.f);
+    const float4 b = src ? ld_f4(src + off1 + j) : make_float4(1.f, 1.f, 1.f, 1.f);
+    w[j] = a.x; w[j + 1] = a.y; w[j + 2] = a.z; w[j + 3] = a.w;
+    w[E + j] = b.x; w[E + j + 1] = b.y; w[E + j + 2] = b.z; w[E + j + 3] = b.w;
+  }
+}
+
+// The frequencies' steps, once per CTA; then each warp forms its rows' angles
+// from them.
+struct Angles {
+  const uint64_t *steps;             // [rot / 2]
+  float2 *cs;                        // [rot / 2], the warp's own
+  int n;
+  __device__ __forceinline__ Angles(char *smem, const double *inv_freq, int rot) {
+    n = rot / 2;
+    uint64_t *s = reinterpret_cast<uint64_t *>(smem);
+    for (int i = threadIdx.x; i < n; i += kThreads) s[i] = turn_step(inv_freq[i]);
+    steps = s;
+    cs = reinterpret_cast<float2 *>(s + n) + threadIdx.x / 32 * n;
+    __syncthreads();
+  }
+  __device__ __forceinline__ void form(int position) const {
+    __syncwarp();                    // the last row's are read
+    for (int i = threadIdx.x % 32; i < n; i += 32) cs[i] = turned(steps[i], position);
+    __syncwarp();
+  }
+  static size_t bytes(int rot) { return (size_t)(rot / 2) * 8 * (1 + kWarps); }
+};
+
 struct HeadParams {
   const void *q, *k, *v;
   void *q_out, *k_out, *v_out;       // k_out, v_out: the caches when page > 0
@@ -94,137 +140,106 @@ struct HeadParams {
   const int32_t *table;              // [B, max_pages]
   int64_t rows, T;
   int Hq, Hk, d, rot;
-  int H;                             // heads a token has in this pass (q, k and, into a cache, v)
-  int R;                             // rows per CTA and pass
-  int head_parts, heads_per_part;    // a token's heads over gridDim.y CTAs
+  int parts, per_part;               // a row's heads (q, then k, then v into a cache) in parts, one per work item
   int64_t num_pages;
   int page, max_pages;
   float eps, inv_d;
 };
 
-// Rows' angles into shared memory: thread i forms angle i % nang of row
-// i / nang.  Also the rows' cache slots (-1: none).
-struct RowAngles {
-  int nang, row, angle;
-  uint64_t step;
-  __device__ __forceinline__ RowAngles(const double *inv_freq, int rot) {
-    nang = rot / 2;
-    row = nang ? threadIdx.x / nang : 0;
-    angle = nang ? threadIdx.x % nang : 0;
-    step = nang ? turn_step(inv_freq[angle]) : 0;
-  }
-  __device__ __forceinline__ void form(float2 *cs, const int32_t *positions, int64_t row0, int R, int64_t rows,
-                                       int64_t T) const {
-    if (nang == 0) return;
-    const int per = kThreads / nang;             // rows formed at once (rot <= 512: at least one)
-    if (row >= per) return;
-    for (int r = row; r < R; r += per) {
-      const int64_t t = row0 + r;
-      if (t < rows) cs[r * nang + angle] = turned(step, positions ? positions[t] : (int)(t % T));
-    }
-  }
-};
-
 template <typename T, int TEAM, bool INTER, bool CACHE>
 __global__ void __launch_bounds__(kThreads) head_norm_kernel(const HeadParams p) {
   constexpr int E = Elt<T>::EPV;
-  constexpr int kTeams = kThreads / TEAM;
-  constexpr int UNROLL = 2;                      // heads in flight per team
+  constexpr int kTeams = 32 / TEAM;              // of a warp
+  constexpr int kFlight = 4;                     // heads in flight per team
   extern __shared__ char smem[];
-  float2 *cs = reinterpret_cast<float2 *>(smem);                          // [R][rot / 2]
-  int64_t *slot = reinterpret_cast<int64_t *>(cs + p.R * (p.rot / 2));    // [R]: the row's first cache element
   grid_dependency_wait();
-  const int lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
+  const Angles ang(smem, p.inv_freq, p.rot);
+  const int lane = threadIdx.x % TEAM, team = threadIdx.x % 32 / TEAM;
   const bool active = lane * 2 * E < p.d;
   const Unit<T, INTER> u(lane, p.rot);
-  const RowAngles ang(p.inv_freq, p.rot);
-  const int h0 = blockIdx.y * p.heads_per_part, h1 = min(p.H, h0 + p.heads_per_part), nh = h1 - h0;
+  const int64_t items = p.rows * p.parts, stride = (int64_t)gridDim.x * kWarps;
+  const int heads = p.Hq + (CACHE ? 2 : 1) * p.Hk;
 
-  for (int64_t row0 = (int64_t)blockIdx.x * p.R; row0 < p.rows; row0 += (int64_t)gridDim.x * p.R) {
-    const int nrow = (int)min((int64_t)p.R, p.rows - row0);
-    const int units = nrow * nh;
-    uint4 va[UNROLL], vb[UNROLL];
-    auto load = [&](int i, int k) {
-      const int r = i / nh, h = h0 + i % nh;
-      const int64_t row = row0 + r;
-      const T *x;
-      if (h < p.Hq) x = (const T *)p.q + row * p.q_stride + (int64_t)h * p.d;
-      else if (!CACHE || h < p.Hq + p.Hk) x = (const T *)p.k + row * p.k_stride + (int64_t)(h - p.Hq) * p.d;
-      else x = (const T *)p.v + row * p.v_stride + (int64_t)(h - p.Hq - p.Hk) * p.d;
-      va[k] = *reinterpret_cast<const uint4 *>(x + u.off0);
-      vb[k] = *reinterpret_cast<const uint4 *>(x + u.off1);
-    };
-#pragma unroll
-    for (int k = 0; k < UNROLL; ++k)
-      if (active && team + k * kTeams < units) load(team + k * kTeams, k);
-    ang.form(cs, p.positions, row0, nrow, p.rows, p.T);
-    if (CACHE && threadIdx.x < nrow) {
-      // A row without a place in the cache (a negative position, one behind
-      // the table, a page outside the pool) is rotated but not stored.
-      const int64_t row = row0 + threadIdx.x;
-      const int pos = p.positions ? p.positions[row] : (int)(row % p.T);
-      int64_t s = -1;
-      if (pos >= 0 && pos / p.page < p.max_pages) {
-        const int64_t pg = p.table[(row / p.T) * p.max_pages + pos / p.page];
-        if (pg >= 0 && pg < p.num_pages) s = (pg * p.Hk * p.page + pos % p.page) * p.d;
-      }
-      slot[threadIdx.x] = s;
+  for (int64_t item = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32; item < items; item += stride) {
+    const int64_t row = p.parts == 1 ? item : item / p.parts;
+    const int from = p.parts == 1 ? 0 : (int)(item - row * p.parts) * p.per_part, to = min(heads, from + p.per_part);
+    const int position = p.positions ? p.positions[row] : (int)(row % p.T);
+    // A row without a place in the cache (a negative position, one behind the
+    // table, a page outside the pool) is rotated but not stored.
+    int64_t slot = -1;
+    if (CACHE && position >= 0 && position / p.page < p.max_pages) {
+      const int64_t pg = p.table[row / p.T * p.max_pages + position / p.page];
+      if (pg >= 0 && pg < p.num_pages) slot = (pg * p.Hk * p.page + position % p.page) * p.d;
     }
-    __syncthreads();
-    for (int i0 = 0; i0 < units; i0 += kTeams * UNROLL) {
+    bool formed = false;
+    // The queries', then the keys' heads.
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+      const int first = which ? p.Hq : 0, count = which ? p.Hk : p.Hq;
+      const int h0 = max(from, first) - first, h1 = min(to, first + count) - first;
+      if (h0 >= h1) continue;
+      const T *x0 = which ? (const T *)p.k + row * p.k_stride : (const T *)p.q + row * p.q_stride;
+      T *y0;
+      int64_t step = p.d;                        // from one head of the output to the next
+      bool store = true;
+      if (!which) y0 = (T *)p.q_out + row * p.qo_stride;
+      else if (!CACHE) y0 = (T *)p.k_out + row * p.ko_stride;
+      else {
+        y0 = (T *)p.k_out + slot;
+        step = (int64_t)p.page * p.d;
+        store = slot >= 0;
+      }
+      float w[2 * E];
+      if (active) load_weight<T>(w, which ? p.wk : p.wq, u.off0, u.off1);
+      for (int hb = h0; hb < h1; hb += kTeams * kFlight) {
+        uint4 va[kFlight], vb[kFlight];
 #pragma unroll
-      for (int k = 0; k < UNROLL; ++k) {
-        const int i = i0 + k * kTeams + team;
-        const bool live = i < units;               // the same for a whole team
-        const int r = live ? i / nh : 0, h = h0 + (live ? i % nh : 0);
-        const bool copy = CACHE && h >= p.Hq + p.Hk;
-        float x[2 * E];
-        float ss = 0.f;
-        if (active && live) {
+        for (int k = 0; k < kFlight; ++k) {
+          const int h = hb + k * kTeams + team;
+          va[k] = vb[k] = make_uint4(0, 0, 0, 0);
+          if (active && h < h1) {
+            va[k] = *reinterpret_cast<const uint4 *>(x0 + h * p.d + u.off0);
+            vb[k] = *reinterpret_cast<const uint4 *>(x0 + h * p.d + u.off1);
+          }
+        }
+        if (!formed) {                           // with the first heads on their way
+          ang.form(position);
+          formed = true;
+        }
+#pragma unroll
+        for (int k = 0; k < kFlight; ++k) {
+          const int h = hb + k * kTeams + team;
+          if (hb + k * kTeams >= h1) break;      // the same for the whole warp
+          float x[2 * E], ss = 0.f;
           Elt<T>::unpack(va[k], x);
           Elt<T>::unpack(vb[k], x + E);
 #pragma unroll
           for (int e = 0; e < 2 * E; ++e) ss = fmaf(x[e], x[e], ss);
-        }
-        ss = team_sum_shfl<TEAM>(ss);
-        if (!active || !live) continue;
-        const int64_t row = row0 + r;
-        T *y;
-        if (h < p.Hq) y = (T *)p.q_out + row * p.qo_stride + (int64_t)h * p.d;
-        else if (!CACHE) y = (T *)p.k_out + row * p.ko_stride + (int64_t)(h - p.Hq) * p.d;
-        else {
-          if (slot[r] < 0) continue;
-          y = (T *)(copy ? p.v_out : p.k_out) + slot[r] + (int64_t)((h - p.Hq) % p.Hk) * p.page * p.d;
-        }
-        if (copy) {
-          st_vec(y + u.off0, va[k]);
-          st_vec(y + u.off1, vb[k]);
-          continue;
-        }
-        const float rms = rsqrtf(ss * p.inv_d + p.eps);
-        const float *w = h < p.Hq ? p.wq : p.wk;
+          ss = team_sum_shfl<TEAM>(ss);
+          if (!active || h >= h1 || !store) continue;
+          const float rms = rsqrtf(ss * p.inv_d + p.eps);
 #pragma unroll
-        for (int e = 0; e < 2 * E; ++e) x[e] *= rms;
-        if (w) {
-#pragma unroll
-          for (int j = 0; j < E; j += 4) {
-            const float4 a = ld_f4(w + u.off0 + j), b = ld_f4(w + u.off1 + j);
-            x[j] *= a.x; x[j + 1] *= a.y; x[j + 2] *= a.z; x[j + 3] *= a.w;
-            x[E + j] *= b.x; x[E + j + 1] *= b.y; x[E + j + 2] *= b.z; x[E + j + 3] *= b.w;
-          }
+          for (int e = 0; e < 2 * E; ++e) x[e] = x[e] * rms * w[e];
+          if (u.turn) turn<T, INTER>(x, ang.cs + u.angle, 1.f);
+          T *y = y0 + h * step;
+          st_vec(y + u.off0, Elt<T>::pack(x));
+          st_vec(y + u.off1, Elt<T>::pack(x + E));
         }
-        if (u.turn) turn<T, INTER>(x, cs + r * (p.rot / 2) + u.angle, 1.f);
-        st_vec(y + u.off0, Elt<T>::pack(x));
-        st_vec(y + u.off1, Elt<T>::pack(x + E));
-      }
-      // the next heads (all lanes are done with the vectors above)
-#pragma unroll
-      for (int k = 0; k < UNROLL; ++k) {
-        const int i = i0 + (UNROLL + k) * kTeams + team;
-        if (active && i < units) load(i, k);
       }
     }
-    __syncthreads();                               // the angles are rewritten
+    if (CACHE && slot >= 0) {
+      // the values, as they are
+      const int first = p.Hq + p.Hk, h0 = max(from, first) - first, h1 = to - first;
+      const T *x0 = (const T *)p.v + row * p.v_stride;
+      T *y0 = (T *)p.v_out + slot;
+      for (int h = h0 + team; h < h1; h += kTeams) {
+        if (!active) continue;
+        const uint4 a = *reinterpret_cast<const uint4 *>(x0 + h * p.d + u.off0);
+        const uint4 b = *reinterpret_cast<const uint4 *>(x0 + h * p.d + u.off1);
+        st_vec(y0 + (int64_t)h * p.page * p.d + u.off0, a);
+        st_vec(y0 + (int64_t)h * p.page * p.d + u.off1, b);
+      }
+    }
   }
 }
 
@@ -237,114 +252,122 @@ struct HeadBackwardParams {
   const int32_t *positions;
   const double *inv_freq;
   int64_t rows, T;
-  int H[2], d, rot, R;
+  int H[2], d, rot;
+  int parts, per_part;               // a row's heads (q, then k) in parts, one per work item
   float eps, inv_d;
 };
 
 template <typename T, int TEAM, bool INTER>
-__global__ void __launch_bounds__(kThreads) head_norm_backward_kernel(const HeadBackwardParams p) {
+__global__ void __launch_bounds__(kThreads, 2) head_norm_backward_kernel(const HeadBackwardParams p) {
   constexpr int E = Elt<T>::EPV;
-  constexpr int kTeams = kThreads / TEAM;
+  constexpr int kTeams = 32 / TEAM;
+  constexpr int kFlight = 2;
   extern __shared__ char smem[];
-  float2 *cs = reinterpret_cast<float2 *>(smem);
   grid_dependency_wait();
-  const int lane = threadIdx.x % TEAM, team = threadIdx.x / TEAM;
+  const Angles ang(smem, p.inv_freq, p.rot);
+  const int lane = threadIdx.x % TEAM, team = threadIdx.x % 32 / TEAM;
   const bool active = lane * 2 * E < p.d;
   const Unit<T, INTER> u(lane, p.rot);
-  const RowAngles ang(p.inv_freq, p.rot);
+  const int64_t items = p.rows * p.parts, stride = (int64_t)gridDim.x * kWarps;
 
-#pragma unroll 1
-  for (int which = 0; which < 2; ++which) {
-    const int H = p.H[which];
-    float w[2 * E], dw[2 * E];
+  float dw[2][2 * E];                            // this lane's sums, of the queries' and the keys' weight
 #pragma unroll
-    for (int e = 0; e < 2 * E; ++e) {
-      w[e] = 1.f;
-      dw[e] = 0.f;
-    }
-    if (active && p.w[which]) {
+  for (int e = 0; e < 2 * E; ++e) dw[0][e] = dw[1][e] = 0.f;
+  for (int64_t item = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32; item < items; item += stride) {
+    const int64_t row = p.parts == 1 ? item : item / p.parts;
+    const int from = p.parts == 1 ? 0 : (int)(item - row * p.parts) * p.per_part;
+    const int to = min(p.H[0] + p.H[1], from + p.per_part);
+    const int position = p.positions ? p.positions[row] : (int)(row % p.T);
+    bool formed = false;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        w[e] = __ldg(p.w[which] + u.off0 + e);
-        w[E + e] = __ldg(p.w[which] + u.off1 + e);
-      }
-    }
-    for (int64_t row0 = (int64_t)blockIdx.x * p.R; row0 < p.rows && H > 0; row0 += (int64_t)gridDim.x * p.R) {
-      const int nrow = (int)min((int64_t)p.R, p.rows - row0);
-      const int units = nrow * H;
-      uint4 xa, xb, ga, gb;
-      auto load = [&](int i) {
-        const int64_t row = row0 + i / H;
-        const int h = i % H;
-        const T *x = (const T *)p.x[which] + row * p.stride[which] + (int64_t)h * p.d;
-        const T *g = (const T *)p.g[which] + row * p.gstride[which] + (int64_t)h * p.d;
-        xa = *reinterpret_cast<const uint4 *>(x + u.off0);
-        xb = *reinterpret_cast<const uint4 *>(x + u.off1);
-        ga = *reinterpret_cast<const uint4 *>(g + u.off0);
-        gb = *reinterpret_cast<const uint4 *>(g + u.off1);
-      };
-      if (active && team < units) load(team);
-      ang.form(cs, p.positions, row0, nrow, p.rows, p.T);
-      __syncthreads();
-      for (int i0 = 0; i0 < units; i0 += kTeams) {
-        const int i = i0 + team;
-        const bool live = active && i < units;
-        float x[2 * E], g[2 * E], ss = 0.f, ux = 0.f;
-        if (live) {
-          Elt<T>::unpack(xa, x);
-          Elt<T>::unpack(xb, x + E);
-          Elt<T>::unpack(ga, g);
-          Elt<T>::unpack(gb, g + E);
-          if (u.turn) turn<T, INTER>(g, cs + (i / H) * (p.rot / 2) + u.angle, -1.f);
+    for (int which = 0; which < 2; ++which) {
+      const int first = which ? p.H[0] : 0;
+      const int h0 = max(from, first) - first, h1 = min(to, first + p.H[which]) - first;
+      if (h0 >= h1) continue;
+      const T *x0 = (const T *)p.x[which] + row * p.stride[which];
+      const T *g0 = (const T *)p.g[which] + row * p.gstride[which];
+      T *y0 = (T *)p.dx[which] + row * p.H[which] * p.d;
+      float w[2 * E];
+      if (active) load_weight<T>(w, p.w[which], u.off0, u.off1);
+      for (int hb = h0; hb < h1; hb += kTeams * kFlight) {
+        uint4 xa[kFlight], xb[kFlight], ga[kFlight], gb[kFlight];
 #pragma unroll
-          for (int e = 0; e < 2 * E; ++e) {
-            ss = fmaf(x[e], x[e], ss);
-            ux = fmaf(g[e] * w[e], x[e], ux);
+        for (int k = 0; k < kFlight; ++k) {
+          const int h = hb + k * kTeams + team;
+          xa[k] = xb[k] = ga[k] = gb[k] = make_uint4(0, 0, 0, 0);
+          if (active && h < h1) {
+            xa[k] = *reinterpret_cast<const uint4 *>(x0 + h * p.d + u.off0);
+            xb[k] = *reinterpret_cast<const uint4 *>(x0 + h * p.d + u.off1);
+            ga[k] = *reinterpret_cast<const uint4 *>(g0 + h * p.d + u.off0);
+            gb[k] = *reinterpret_cast<const uint4 *>(g0 + h * p.d + u.off1);
           }
         }
-        if (active && i + kTeams < units) load(i + kTeams);
-        ss = team_sum_shfl<TEAM>(ss);
-        ux = team_sum_shfl<TEAM>(ux);
-        if (!live) continue;
-        const float r = rsqrtf(ss * p.inv_d + p.eps);
-        const float c = ux * p.inv_d * r * r;
-        float dx[2 * E];
-#pragma unroll
-        for (int e = 0; e < 2 * E; ++e) {
-          dw[e] = fmaf(g[e], x[e] * r, dw[e]);
-          dx[e] = r * fmaf(-c, x[e], g[e] * w[e]);
+        if (!formed) {
+          ang.form(position);
+          formed = true;
         }
-        T *y = (T *)p.dx[which] + ((row0 + i / H) * H + i % H) * p.d;
-        st_vec(y + u.off0, Elt<T>::pack(dx));
-        st_vec(y + u.off1, Elt<T>::pack(dx + E));
+#pragma unroll
+        for (int k = 0; k < kFlight; ++k) {
+          const int h = hb + k * kTeams + team;
+          if (hb + k * kTeams >= h1) break;      // the same for the whole warp
+          float x[2 * E], g[2 * E], ss = 0.f, ux = 0.f;
+          if (active && h < h1) {
+            Elt<T>::unpack(xa[k], x);
+            Elt<T>::unpack(xb[k], x + E);
+            Elt<T>::unpack(ga[k], g);
+            Elt<T>::unpack(gb[k], g + E);
+            if (u.turn) turn<T, INTER>(g, ang.cs + u.angle, -1.f);
+#pragma unroll
+            for (int e = 0; e < 2 * E; ++e) {
+              ss = fmaf(x[e], x[e], ss);
+              ux = fmaf(g[e] * w[e], x[e], ux);
+            }
+          }
+          ss = team_sum_shfl<TEAM>(ss);
+          ux = team_sum_shfl<TEAM>(ux);
+          if (!active || h >= h1) continue;
+          const float r = rsqrtf(ss * p.inv_d + p.eps);
+          const float c = ux * p.inv_d * r * r;
+          float dx[2 * E];
+#pragma unroll
+          for (int e = 0; e < 2 * E; ++e) {
+            dw[which][e] = fmaf(g[e], x[e] * r, dw[which][e]);
+            dx[e] = r * fmaf(-c, x[e], g[e] * w[e]);
+          }
+          T *y = y0 + h * p.d;
+          st_vec(y + u.off0, Elt<T>::pack(dx));
+          st_vec(y + u.off1, Elt<T>::pack(dx + E));
+        }
       }
-      __syncthreads();
     }
-    if (!p.partials) continue;
-    // The CTA's sum of dw: over the teams of a warp by shuffles, over the
-    // warps through shared memory in a fixed order (reproducible).
-    float *red = reinterpret_cast<float *>(smem);      // [warps][d]: the angles are no longer needed
-    const int warp = threadIdx.x / 32, wl = threadIdx.x % 32;
+  }
+  if (!p.partials) return;
+  // The CTA's sums: over the teams of a warp by shuffles, over the warps
+  // through shared memory in a fixed order (reproducible).
+  float *red = reinterpret_cast<float *>(smem);      // [warps][d]: the angles are no longer needed
+  const int warp = threadIdx.x / 32;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    __syncthreads();
 #pragma unroll
     for (int e = 0; e < 2 * E; ++e) {
 #pragma unroll
-      for (int o = TEAM; o < 32; o <<= 1) dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], o);
+      for (int o = TEAM; o < 32; o <<= 1) dw[which][e] += __shfl_xor_sync(0xffffffffu, dw[which][e], o);
     }
-    if (wl < TEAM && active) {
+    if (team == 0 && active) {
 #pragma unroll
       for (int e = 0; e < E; ++e) {
-        red[warp * p.d + u.off0 + e] = dw[e];
-        red[warp * p.d + u.off1 + e] = dw[E + e];
+        red[warp * p.d + u.off0 + e] = dw[which][e];
+        red[warp * p.d + u.off1 + e] = dw[which][E + e];
       }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < p.d; i += kThreads) {
       float s = 0.f;
 #pragma unroll
-      for (int k = 0; k < kThreads / 32; ++k) s += red[k * p.d + i];
+      for (int k = 0; k < kWarps; ++k) s += red[k * p.d + i];
       p.partials[((int64_t)blockIdx.x * 2 + which) * p.d + i] = s;
     }
-    __syncthreads();
   }
 }
 
@@ -360,6 +383,16 @@ __global__ void __launch_bounds__(256) head_norm_weights_kernel(const float *par
   s = team_sum_shfl<32>(s);
   float *out = warp < d ? dwq : dwk;
   if (lane == 0 && out) out[warp % d] = s;
+}
+
+// Parts that a row's heads are cut into so that there are `want` work items,
+// none below `least` heads.
+int row_parts(int64_t rows, int heads, int least, int64_t want, int &per_part) {
+  int64_t parts = (want + rows - 1) / rows;
+  const int most = (heads + least - 1) / least;
+  if (parts > most) parts = most;
+  per_part = (int)((heads + parts - 1) / parts);
+  return (heads + per_part - 1) / per_part;
 }
 
 // Call f with the element type, the lanes per head and the pairing as types.
@@ -397,33 +430,24 @@ cudaError_t launch_head_norm(const HeadNormArgs &a) {
   p.num_pages = a.num_pages; p.page = a.page_size; p.max_pages = a.max_pages;
   p.eps = a.eps; p.inv_d = 1.f / (float)a.d;
   const bool cache = a.page_size > 0;
-  p.H = a.Hq + (cache ? 2 : 1) * a.Hk;
   const int sms = sm_count();
-  // Rows per pass: as many as the threads form angles for at once, but no
-  // more than leave every SM a few CTAs; a token's heads are split over
-  // several CTAs where the rows alone would not fill the SMs.
-  const int most = a.rot ? kThreads / (a.rot / 2) : 16;
-  const int64_t fill = a.rows / (4 * (int64_t)sms);
-  p.R = (int)(fill < 1 ? 1 : fill < most ? fill : most);
-  if (p.R > 16) p.R = 16;
   return dispatch(a.dtype, a.d, a.interleaved, [&](auto elt, auto team, auto inter) -> cudaError_t {
     using T = decltype(elt);
-    constexpr int TEAM = decltype(team)::value, kTeams = kThreads / TEAM;
+    constexpr int TEAM = decltype(team)::value;
     constexpr bool INTER = decltype(inter)::value;
-    const int64_t ctas = (a.rows + p.R - 1) / p.R;
-    int parts = 1;
-    while (ctas * parts < 2 * sms && p.H > parts * kTeams) ++parts;
-    p.heads_per_part = (p.H + parts - 1) / parts;
-    p.head_parts = (p.H + p.heads_per_part - 1) / p.heads_per_part;
-    const int64_t most_x = (int64_t)sms * 8;
-    dim3 grid((unsigned)(ctas < most_x ? ctas : most_x), (unsigned)p.head_parts);
-    const size_t smem = (size_t)p.R * (a.rot / 2) * sizeof(float2) + (size_t)p.R * sizeof(int64_t);
+    // A row per work item, cut into parts of no less than one round of a
+    // warp's teams where the rows alone would not give every SM eight warps.
+    const int heads = a.Hq + (cache ? 2 : 1) * a.Hk;
+    p.parts = row_parts(a.rows, heads, 32 / TEAM, 8 * (int64_t)sms, p.per_part);
+    const int64_t ctas = (a.rows * p.parts + kWarps - 1) / kWarps, most = (int64_t)sms * 8;
+    const dim3 grid((unsigned)(ctas < most ? ctas : most));
+    const size_t smem = Angles::bytes(a.rot);
     return cache ? launch_dependent(head_norm_kernel<T, TEAM, INTER, true>, grid, dim3(kThreads), smem, a.stream, p)
                  : launch_dependent(head_norm_kernel<T, TEAM, INTER, false>, grid, dim3(kThreads), smem, a.stream, p);
   });
 }
 
-int head_norm_backward_ctas() { return 4 * sm_count(); }
+int head_norm_backward_ctas() { return 2 * sm_count(); }
 
 cudaError_t launch_head_norm_backward(const HeadNormBackwardArgs &a) {
   HeadBackwardParams p{};
@@ -436,21 +460,22 @@ cudaError_t launch_head_norm_backward(const HeadNormBackwardArgs &a) {
   p.positions = a.positions; p.inv_freq = a.inv_freq;
   p.rows = a.rows; p.T = a.T; p.H[0] = a.Hq; p.H[1] = a.Hk; p.d = a.d; p.rot = a.rot;
   p.eps = a.eps; p.inv_d = 1.f / (float)a.d;
-  const int sms = sm_count();
-  const int most = a.rot ? kThreads / (a.rot / 2) : 16;
-  const int64_t fill = a.rows / (4 * (int64_t)sms);
-  p.R = (int)(fill < 1 ? 1 : fill < most ? fill : most);
-  if (p.R > 16) p.R = 16;
-  const int64_t want = (a.rows + p.R - 1) / p.R;
-  const int64_t limit = a.workspace ? a.workspace_rows / 2 : head_norm_backward_ctas();
-  const int ctas = (int)(want < limit ? want : limit);
+  const int limit = a.workspace && a.workspace_rows / 2 < head_norm_backward_ctas() ? (int)(a.workspace_rows / 2)
+                                                                                : head_norm_backward_ctas();
+  int ctas = 0;
   cudaError_t e = dispatch(a.dtype, a.d, a.interleaved, [&](auto elt, auto team, auto inter) -> cudaError_t {
     using T = decltype(elt);
-    size_t smem = (size_t)p.R * (a.rot / 2) * sizeof(float2);
-    const size_t red = (size_t)(kThreads / 32) * a.d * sizeof(float);
+    constexpr int TEAM = decltype(team)::value;
+    // Enough work items that the last round of the warps, which only some of
+    // them have work in, is a small part of the whole.
+    p.parts = row_parts(a.rows, a.Hq + a.Hk, 2 * (32 / TEAM), 16 * (int64_t)limit * kWarps, p.per_part);
+    const int64_t want = (a.rows * p.parts + kWarps - 1) / kWarps;
+    ctas = (int)(want < limit ? want : limit);
+    size_t smem = Angles::bytes(a.rot);
+    const size_t red = (size_t)kWarps * a.d * sizeof(float);
     if (smem < red) smem = red;
-    return launch_dependent(head_norm_backward_kernel<T, decltype(team)::value, decltype(inter)::value>,
-                            dim3((unsigned)ctas), dim3(kThreads), smem, a.stream, p);
+    return launch_dependent(head_norm_backward_kernel<T, TEAM, decltype(inter)::value>, dim3((unsigned)ctas),
+                            dim3(kThreads), smem, a.stream, p);
   });
   if (e != cudaSuccess || !a.workspace) return e;
   return launch_dependent(head_norm_weights_kernel, dim3((unsigned)((2 * a.d + 7) / 8)), dim3(256), 0, a.stream,
