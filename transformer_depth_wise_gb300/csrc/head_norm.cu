@@ -80,31 +80,66 @@ struct Unit {
   }
 };
 
-// Turn the pairs of x (2 EPV elements: vector 0 then vector 1) by the angles
-// in cs, forwards (dir = 1) or back (-1).
-template <typename T, bool INTER>
-__device__ __forceinline__ void turn(float *x, const float2 *cs, float dir) {
-  constexpr int E = Elt<T>::EPV;
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t swapped(uint64_t a) { return a >> 32 | a << 32; }
+
+// A vector from pairs of fp32 values, rounded to the element type.
+template <typename T>
+__device__ __forceinline__ uint4 from_pairs(const uint64_t *x) {
+  constexpr int NP = Pairs<T>::NP;
+  float f[2 * NP];
 #pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const float c = cs[i].x, s = cs[i].y * dir;
-    const int a = INTER ? 2 * i : i, b = INTER ? 2 * i + 1 : i + E;
-    const float xa = x[a], xb = x[b];
-    x[a] = xa * c - xb * s;
-    x[b] = xb * c + xa * s;
+  for (int i = 0; i < NP; ++i) unpair(x[i], f[2 * i], f[2 * i + 1]);
+  return Elt<T>::pack(f);
+}
+
+// Turn a unit (2 NP pairs of fp32 values: vector 0, then vector 1) by the
+// angles at c and s, forwards or back.
+template <typename T, bool INTER, bool BACK>
+__device__ __forceinline__ void turn(uint64_t *x, const float *c, const float *s) {
+  constexpr int NP = Pairs<T>::NP;
+  if constexpr (INTER) {
+    // a pair is (a, b) itself
+#pragma unroll
+    for (int i = 0; i < 2 * NP; ++i) {
+      const float si = BACK ? -s[i] : s[i];
+      x[i] = fma2(x[i], pair(c[i], c[i]), mul2(swapped(x[i]), pair(-si, si)));
+    }
+  } else {
+    // vector 0 holds a, vector 1 b
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const uint64_t ci = pair(c[2 * i], c[2 * i + 1]);
+      const uint64_t up = BACK ? pair(-s[2 * i], -s[2 * i + 1]) : pair(s[2 * i], s[2 * i + 1]);
+      const uint64_t down = BACK ? pair(s[2 * i], s[2 * i + 1]) : pair(-s[2 * i], -s[2 * i + 1]);
+      const uint64_t a = x[i], b = x[NP + i];
+      x[i] = fma2(b, down, mul2(a, ci));
+      x[NP + i] = fma2(a, up, mul2(b, ci));
+    }
   }
 }
 
 // A lane's share of the weight, or ones.
 template <typename T>
-__device__ __forceinline__ void load_weight(float *w, const float *src, int off0, int off1) {
-  constexpr int E = Elt<T>::EPV;
+__device__ __forceinline__ void load_weight(uint64_t *w, const float *src, int off0, int off1) {
+  constexpr int NP = Pairs<T>::NP;
 #pragma unroll
-  for (int j = 0; j < E; j += 4) {
-    const float4 a = src ? ld_f4(src + off0 + j) : make_float4(1.f, 1.f, 1.f, 1.f);
-    const float4 b = src ? ld_f4(src + off1 + j) : make_float4(1.f, 1.f, 1.f, 1.f);
-    w[j] = a.x; w[j + 1] = a.y; w[j + 2] = a.z; w[j + 3] = a.w;
-    w[E + j] = b.x; w[E + j + 1] = b.y; w[E + j + 2] = b.z; w[E + j + 3] = b.w;
+  for (int j = 0; j < NP; j += 2) {
+    const float4 a = src ? ld_f4(src + off0 + 2 * j) : make_float4(1.f, 1.f, 1.f, 1.f);
+    const float4 b = src ? ld_f4(src + off1 + 2 * j) : make_float4(1.f, 1.f, 1.f, 1.f);
+    w[j] = pair(a.x, a.y);
+    w[j + 1] = pair(a.z, a.w);
+    w[NP + j] = pair(b.x, b.y);
+    w[NP + j + 1] = pair(b.z, b.w);
   }
 }
 
@@ -112,20 +147,34 @@ __device__ __forceinline__ void load_weight(float *w, const float *src, int off0
 // from them.
 struct Angles {
   const uint64_t *steps;             // [rot / 2]
-  float2 *cs;                        // [rot / 2], the warp's own
+  float *c, *s;                      // cosines and sines [rot / 2], the warp's own
   int n;
   __device__ __forceinline__ Angles(char *smem, const double *inv_freq, int rot) {
-    n = rot / 2;
-    uint64_t *s = reinterpret_cast<uint64_t *>(smem);
-    for (int i = threadIdx.x; i < n; i += kThreads) s[i] = turn_step(inv_freq[i]);
-    steps = s;
-    cs = reinterpret_cast<float2 *>(s + n) + threadIdx.x / 32 * n;
+    n = rot / 2;                     // a multiple of 4
+    uint64_t *st = reinterpret_cast<uint64_t *>(smem);
+    for (int i = threadIdx.x; i < n; i += kThreads) st[i] = turn_step(inv_freq[i]);
+    steps = st;
+    c = reinterpret_cast<float *>(st + n) + threadIdx.x / 32 * 2 * n;
+    s = c + n;
     __syncthreads();
   }
   __device__ __forceinline__ void form(int position) const {
     __syncwarp();                    // the last row's are read
-    for (int i = threadIdx.x % 32; i < n; i += 32) cs[i] = turned(steps[i], position);
+    for (int i = threadIdx.x % 32; i < n; i += 32) {
+      const float2 cs = turned(steps[i], position);
+      c[i] = cs.x;
+      s[i] = cs.y;
+    }
     __syncwarp();
+  }
+  // A lane's angles (a unit has 2 NP of them), in 16-byte reads.
+  template <int N> __device__ __forceinline__ void read(int at, float *cosines, float *sines) const {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const float4 x = *reinterpret_cast<const float4 *>(c + at + i), y = *reinterpret_cast<const float4 *>(s + at + i);
+      cosines[i] = x.x; cosines[i + 1] = x.y; cosines[i + 2] = x.z; cosines[i + 3] = x.w;
+      sines[i] = y.x; sines[i + 1] = y.y; sines[i + 2] = y.z; sines[i + 3] = y.w;
+    }
   }
   static size_t bytes(int rot) { return (size_t)(rot / 2) * 8 * (1 + kWarps); }
 };
@@ -147,8 +196,8 @@ struct HeadParams {
 };
 
 template <typename T, int TEAM, bool INTER, bool CACHE>
-__global__ void __launch_bounds__(kThreads) head_norm_kernel(const HeadParams p) {
-  constexpr int E = Elt<T>::EPV;
+__global__ void __launch_bounds__(kThreads, 2) head_norm_kernel(const HeadParams p) {
+  constexpr int E = Elt<T>::EPV, NP = Pairs<T>::NP;
   constexpr int kTeams = 32 / TEAM;              // of a warp
   constexpr int kFlight = 4;                     // heads in flight per team
   extern __shared__ char smem[];
@@ -189,7 +238,7 @@ __global__ void __launch_bounds__(kThreads) head_norm_kernel(const HeadParams p)
         step = (int64_t)p.page * p.d;
         store = slot >= 0;
       }
-      float w[2 * E];
+      uint64_t w[2 * NP];
       if (active) load_weight<T>(w, which ? p.wk : p.wq, u.off0, u.off1);
       for (int hb = h0; hb < h1; hb += kTeams * kFlight) {
         uint4 va[kFlight], vb[kFlight];
@@ -210,20 +259,25 @@ __global__ void __launch_bounds__(kThreads) head_norm_kernel(const HeadParams p)
         for (int k = 0; k < kFlight; ++k) {
           const int h = hb + k * kTeams + team;
           if (hb + k * kTeams >= h1) break;      // the same for the whole warp
-          float x[2 * E], ss = 0.f;
-          Elt<T>::unpack(va[k], x);
-          Elt<T>::unpack(vb[k], x + E);
+          uint64_t x[2 * NP], sum = 0;
+          Pairs<T>::split(va[k], x);
+          Pairs<T>::split(vb[k], x + NP);
 #pragma unroll
-          for (int e = 0; e < 2 * E; ++e) ss = fmaf(x[e], x[e], ss);
-          ss = team_sum_shfl<TEAM>(ss);
+          for (int i = 0; i < 2 * NP; ++i) fma_pair(sum, x[i], x[i]);
+          const float ss = team_sum_shfl<TEAM>(pair_sum(sum));
           if (!active || h >= h1 || !store) continue;
           const float rms = rsqrtf(ss * p.inv_d + p.eps);
+          const uint64_t rms2 = pair(rms, rms);
 #pragma unroll
-          for (int e = 0; e < 2 * E; ++e) x[e] = x[e] * rms * w[e];
-          if (u.turn) turn<T, INTER>(x, ang.cs + u.angle, 1.f);
+          for (int i = 0; i < 2 * NP; ++i) x[i] = mul2(mul2(x[i], rms2), w[i]);
+          if (u.turn) {
+            float c[2 * NP], sn[2 * NP];
+            ang.template read<2 * NP>(u.angle, c, sn);
+            turn<T, INTER, false>(x, c, sn);
+          }
           T *y = y0 + h * step;
-          st_vec(y + u.off0, Elt<T>::pack(x));
-          st_vec(y + u.off1, Elt<T>::pack(x + E));
+          st_vec(y + u.off0, from_pairs<T>(x));
+          st_vec(y + u.off1, from_pairs<T>(x + NP));
         }
       }
     }
@@ -259,7 +313,7 @@ struct HeadBackwardParams {
 
 template <typename T, int TEAM, bool INTER>
 __global__ void __launch_bounds__(kThreads, 2) head_norm_backward_kernel(const HeadBackwardParams p) {
-  constexpr int E = Elt<T>::EPV;
+  constexpr int E = Elt<T>::EPV, NP = Pairs<T>::NP;
   constexpr int kTeams = 32 / TEAM;
   constexpr int kFlight = 2;
   extern __shared__ char smem[];
@@ -270,9 +324,9 @@ __global__ void __launch_bounds__(kThreads, 2) head_norm_backward_kernel(const H
   const Unit<T, INTER> u(lane, p.rot);
   const int64_t items = p.rows * p.parts, stride = (int64_t)gridDim.x * kWarps;
 
-  float dw[2][2 * E];                            // this lane's sums, of the queries' and the keys' weight
+  uint64_t dw[2][2 * NP];                        // this lane's sums, of the queries' and the keys' weight
 #pragma unroll
-  for (int e = 0; e < 2 * E; ++e) dw[0][e] = dw[1][e] = 0.f;
+  for (int i = 0; i < 2 * NP; ++i) dw[0][i] = dw[1][i] = 0;
   for (int64_t item = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32; item < items; item += stride) {
     const int64_t row = p.parts == 1 ? item : item / p.parts;
     const int from = p.parts == 1 ? 0 : (int)(item - row * p.parts) * p.per_part;
@@ -287,7 +341,7 @@ __global__ void __launch_bounds__(kThreads, 2) head_norm_backward_kernel(const H
       const T *x0 = (const T *)p.x[which] + row * p.stride[which];
       const T *g0 = (const T *)p.g[which] + row * p.gstride[which];
       T *y0 = (T *)p.dx[which] + row * p.H[which] * p.d;
-      float w[2 * E];
+      uint64_t w[2 * NP];
       if (active) load_weight<T>(w, p.w[which], u.off0, u.off1);
       for (int hb = h0; hb < h1; hb += kTeams * kFlight) {
         uint4 xa[kFlight], xb[kFlight], ga[kFlight], gb[kFlight];
@@ -310,33 +364,36 @@ __global__ void __launch_bounds__(kThreads, 2) head_norm_backward_kernel(const H
         for (int k = 0; k < kFlight; ++k) {
           const int h = hb + k * kTeams + team;
           if (hb + k * kTeams >= h1) break;      // the same for the whole warp
-          float x[2 * E], g[2 * E], ss = 0.f, ux = 0.f;
-          if (active && h < h1) {
-            Elt<T>::unpack(xa[k], x);
-            Elt<T>::unpack(xb[k], x + E);
-            Elt<T>::unpack(ga[k], g);
-            Elt<T>::unpack(gb[k], g + E);
-            if (u.turn) turn<T, INTER>(g, ang.cs + u.angle, -1.f);
-#pragma unroll
-            for (int e = 0; e < 2 * E; ++e) {
-              ss = fmaf(x[e], x[e], ss);
-              ux = fmaf(g[e] * w[e], x[e], ux);
-            }
+          uint64_t x[2 * NP], g[2 * NP], v[2 * NP], sum = 0, dot = 0;
+          Pairs<T>::split(xa[k], x);
+          Pairs<T>::split(xb[k], x + NP);
+          Pairs<T>::split(ga[k], g);
+          Pairs<T>::split(gb[k], g + NP);
+          if (u.turn && active) {
+            float c[2 * NP], sn[2 * NP];
+            ang.template read<2 * NP>(u.angle, c, sn);
+            turn<T, INTER, true>(g, c, sn);
           }
-          ss = team_sum_shfl<TEAM>(ss);
-          ux = team_sum_shfl<TEAM>(ux);
-          if (!active || h >= h1) continue;
-          const float r = rsqrtf(ss * p.inv_d + p.eps);
-          const float c = ux * p.inv_d * r * r;
-          float dx[2 * E];
 #pragma unroll
-          for (int e = 0; e < 2 * E; ++e) {
-            dw[which][e] = fmaf(g[e], x[e] * r, dw[which][e]);
-            dx[e] = r * fmaf(-c, x[e], g[e] * w[e]);
+          for (int i = 0; i < 2 * NP; ++i) {
+            v[i] = mul2(g[i], w[i]);
+            fma_pair(sum, x[i], x[i]);
+            fma_pair(dot, v[i], x[i]);
+          }
+          const bool live = active && h < h1;
+          const float ss = team_sum_shfl<TEAM>(live ? pair_sum(sum) : 0.f);
+          const float ux = team_sum_shfl<TEAM>(live ? pair_sum(dot) : 0.f);
+          if (!live) continue;
+          const float r = rsqrtf(ss * p.inv_d + p.eps), rc = -ux * p.inv_d * r * r * r;
+          const uint64_t r2 = pair(r, r), rc2 = pair(rc, rc);
+#pragma unroll
+          for (int i = 0; i < 2 * NP; ++i) {
+            fma_pair(dw[which][i], g[i], mul2(x[i], r2));
+            v[i] = fma2(x[i], rc2, mul2(v[i], r2));
           }
           T *y = y0 + h * p.d;
-          st_vec(y + u.off0, Elt<T>::pack(dx));
-          st_vec(y + u.off1, Elt<T>::pack(dx + E));
+          st_vec(y + u.off0, from_pairs<T>(v));
+          st_vec(y + u.off1, from_pairs<T>(v + NP));
         }
       }
     }
@@ -350,15 +407,18 @@ __global__ void __launch_bounds__(kThreads, 2) head_norm_backward_kernel(const H
   for (int which = 0; which < 2; ++which) {
     __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 2 * E; ++e) {
+    for (int i = 0; i < 2 * NP; ++i) {
+      float lo, hi;
+      unpair(dw[which][i], lo, hi);
 #pragma unroll
-      for (int o = TEAM; o < 32; o <<= 1) dw[which][e] += __shfl_xor_sync(0xffffffffu, dw[which][e], o);
-    }
-    if (team == 0 && active) {
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        red[warp * p.d + u.off0 + e] = dw[which][e];
-        red[warp * p.d + u.off1 + e] = dw[which][E + e];
+      for (int o = TEAM; o < 32; o <<= 1) {
+        lo += __shfl_xor_sync(0xffffffffu, lo, o);
+        hi += __shfl_xor_sync(0xffffffffu, hi, o);
+      }
+      if (team == 0 && active) {
+        float *at = red + warp * p.d + (i < NP ? u.off0 + 2 * i : u.off1 + 2 * (i - NP));
+        at[0] = lo;
+        at[1] = hi;
       }
     }
     __syncthreads();
@@ -385,13 +445,13 @@ __global__ void __launch_bounds__(256) head_norm_weights_kernel(const float *par
   if (lane == 0 && out) out[warp % d] = s;
 }
 
-// Parts that a row's heads are cut into so that there are `want` work items,
-// none below `least` heads.
-int row_parts(int64_t rows, int heads, int least, int64_t want, int &per_part) {
+// Parts that a row's heads are cut into so that there are about `want` work
+// items, each of a multiple of `round` heads.
+int row_parts(int64_t rows, int heads, int round, int64_t want, int &per_part) {
   int64_t parts = (want + rows - 1) / rows;
-  const int most = (heads + least - 1) / least;
+  const int most = (heads + round - 1) / round;
   if (parts > most) parts = most;
-  per_part = (int)((heads + parts - 1) / parts);
+  per_part = (int)((heads + parts - 1) / parts + round - 1) / round * round;
   return (heads + per_part - 1) / per_part;
 }
 
@@ -466,9 +526,8 @@ cudaError_t launch_head_norm_backward(const HeadNormBackwardArgs &a) {
   cudaError_t e = dispatch(a.dtype, a.d, a.interleaved, [&](auto elt, auto team, auto inter) -> cudaError_t {
     using T = decltype(elt);
     constexpr int TEAM = decltype(team)::value;
-    // Enough work items that the last round of the warps, which only some of
-    // them have work in, is a small part of the whole.
-    p.parts = row_parts(a.rows, a.Hq + a.Hk, 2 * (32 / TEAM), 16 * (int64_t)limit * kWarps, p.per_part);
+    // A few items per warp, of whole rounds of its teams (two heads each in flight).
+    p.parts = row_parts(a.rows, a.Hq + a.Hk, 2 * (32 / TEAM), 4 * (int64_t)limit * kWarps, p.per_part);
     const int64_t want = (a.rows * p.parts + kWarps - 1) / kWarps;
     ctas = (int)(want < limit ? want : limit);
     size_t smem = Angles::bytes(a.rot);

@@ -196,6 +196,8 @@ __global__ void __launch_bounds__(kWarpsF * 32) paged_f32_kernel(const PagedPara
   const int64_t total = all_tiles(p, red) * p.Hk;
   Walk w = walk_begin(p, total);
   if (threadIdx.x == 0) p.cuts[blockIdx.x].b = -1;
+  if (!w.more())                                    // an empty range's part weighs nothing
+    for (int g = threadIdx.x; g < p.G; g += blockDim.x) p.part_lse[(int64_t)blockIdx.x * 2 * p.G + g] = -INFINITY;
   const int64_t first = w.at;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, team = lane / 8, l8 = lane % 8;
   const int groups = (p.G + GQ - 1) / GQ;           // of query heads
@@ -411,6 +413,8 @@ __global__ void __launch_bounds__(kWarpsM * 32, MmaShape<D>::kCtas) paged_mma_ke
   const int64_t total = all_tiles(p, red) * p.Hk;
   Walk w = walk_begin(p, total);
   if (threadIdx.x == 0) p.cuts[blockIdx.x].b = -1;
+  if (!w.more())                                    // an empty range's part weighs nothing
+    for (int g = threadIdx.x; g < p.G; g += blockDim.x) p.part_lse[(int64_t)blockIdx.x * 2 * p.G + g] = -INFINITY;
   const int64_t first = w.at;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g4 = lane / 4, t4 = lane % 4;
   const uint32_t ring = smem_u32(smem) + warp * S::kStages * S::kStage;
@@ -607,60 +611,64 @@ __global__ void __launch_bounds__(kWarpsM * 32, MmaShape<D>::kCtas) paged_mma_ke
   write_empty<__nv_bfloat16>(p);
 }
 
-// One CTA per (noted pair, query head): the parts' weights, then their sum,
-// four elements per thread.
-constexpr int kJoinThreads = 64;
+// One CTA per (noted pair, query head): the parts' weights, then their sum.
+// A warp takes every eighth part, 16 bytes per lane, and the warps' sums meet
+// in shared memory in a fixed order.
+constexpr int kJoinWarps = 8;
 
 template <typename T>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const PagedParams p, int ctas) {
-  extern __shared__ float weight[];                 // [parts]
-  __shared__ float red[kJoinThreads / 32];
-  __shared__ int64_t red_tiles[kJoinThreads / 32];
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const PagedParams p) {
+  extern __shared__ float weight[];                 // [parts], then the warps' sums [kJoinWarps][d]
+  __shared__ float red[kJoinWarps];
   grid_dependency_wait();
-  const int c0 = blockIdx.x, g = blockIdx.y;
+  const int c0 = blockIdx.x, g = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const Cut cut = p.cuts[c0];
   if (cut.b < 0) return;
-  const int64_t total = all_tiles(p, red_tiles) * p.Hk;
   const int parts = cut.last - c0 + 1;
+  float *sums = weight + (gridDim.x + 3) / 4 * 4;
   // a later CTA's range begins with its part: slot 0
   auto row_of = [&](int k) { return ((int64_t)(c0 + k) * 2 + (k == 0 ? cut.slot : 0)) * p.G + g; };
-  auto empty = [&](int k) { return range_begin(total, c0 + k + 1, ctas) == range_begin(total, c0 + k, ctas); };
   float M = -INFINITY;
-  for (int k = threadIdx.x; k < parts; k += kJoinThreads) {
-    const float x = empty(k) ? -INFINITY : p.part_lse[row_of(k)];
+  for (int k = threadIdx.x; k < parts; k += kJoinWarps * 32) {
+    const float x = p.part_lse[row_of(k)];          // -infinity also where a CTA's range is empty
     weight[k] = x;
     M = fmaxf(M, x);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = M;
+  if (lane == 0) red[warp] = M;
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < kJoinThreads / 32; ++k) M = fmaxf(M, red[k]);
-  for (int k = threadIdx.x; k < parts; k += kJoinThreads)
+  for (int k = 0; k < kJoinWarps; ++k) M = fmaxf(M, red[k]);
+  for (int k = threadIdx.x; k < parts; k += kJoinWarps * 32)
     weight[k] = weight[k] == -INFINITY ? 0.f : expf(weight[k] - M);
   __syncthreads();
   float L = 0.f;
   for (int k = 0; k < parts; ++k) L += weight[k];
-  const float r = L == 0.f ? 0.f : 1.f / L;
-  const int64_t row = (int64_t)cut.b * p.Hq + cut.hk * p.G + g;
-  for (int e = threadIdx.x * 4; e < p.d; e += kJoinThreads * 4) {
+  for (int e = lane * 4; e < p.d; e += 128) {
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int k = 0; k < parts; ++k) {
+    for (int k = warp; k < parts; k += kJoinWarps) {
       const float h = weight[k];
       float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (h != 0.f)                                 // an empty range's slot holds nothing
+      if (h != 0.f)                                 // a part without a weight may hold nothing
         y = *reinterpret_cast<const float4 *>(p.part_o + row_of(k) * p.d + e);
       x.x = fmaf(y.x, h, x.x);
       x.y = fmaf(y.y, h, x.y);
       x.z = fmaf(y.z, h, x.z);
       x.w = fmaf(y.w, h, x.w);
     }
-    T *dst = (T *)p.out + row * p.d + e;
-    x.x *= r; x.y *= r; x.z *= r; x.w *= r;
-    if constexpr (std::is_same<T, float>::value) *reinterpret_cast<float4 *>(dst) = x;
-    else *reinterpret_cast<uint2 *>(dst) = make_uint2(Elt<T>::pack_word(x.x, x.y), Elt<T>::pack_word(x.z, x.w));
+    *reinterpret_cast<float4 *>(sums + warp * p.d + e) = x;
+  }
+  __syncthreads();
+  const float r = L == 0.f ? 0.f : 1.f / L;
+  const int64_t row = (int64_t)cut.b * p.Hq + cut.hk * p.G + g;
+  for (int e = threadIdx.x; e < p.d; e += kJoinWarps * 32) {
+    float x = 0.f;
+#pragma unroll
+    for (int k = 0; k < kJoinWarps; ++k) x += sums[k * p.d + e];
+    if constexpr (std::is_same<T, float>::value) ((float *)p.out)[row * p.d + e] = x * r;
+    else ((__nv_bfloat16 *)p.out)[row * p.d + e] = __float2bfloat16_rn(x * r);
   }
   if (threadIdx.x == 0 && p.lse) p.lse[row] = L == 0.f ? -INFINITY : M + logf(L);
 }
@@ -694,6 +702,7 @@ cudaError_t launch_paged(const PagedArgs &a) {
   p.part_o = reinterpret_cast<float *>(p.cuts + ctas);
   p.part_lse = p.part_o + (int64_t)ctas * 2 * p.G * p.d;
   const dim3 grid((unsigned)ctas), join((unsigned)ctas, (unsigned)p.G);
+  const size_t join_smem = ((size_t)(ctas + 3) / 4 * 4 + (size_t)kJoinWarps * a.d) * sizeof(float);
   cudaError_t err;
   if (a.dtype == ATTNRES_BF16) {
     auto go = [&](auto D) -> cudaError_t {
@@ -706,8 +715,7 @@ cudaError_t launch_paged(const PagedArgs &a) {
     err = a.d <= 64 ? go(std::integral_constant<int, 64>{}) : a.d <= 96 ? go(std::integral_constant<int, 96>{})
         : a.d <= 128 ? go(std::integral_constant<int, 128>{}) : go(std::integral_constant<int, 256>{});
     if (err != cudaSuccess) return err;
-    return launch_dependent(paged_join_kernel<__nv_bfloat16>, join, dim3(kJoinThreads), ctas * sizeof(float), a.stream,
-                            p, ctas);
+    return launch_dependent(paged_join_kernel<__nv_bfloat16>, join, dim3(kJoinWarps * 32), join_smem, a.stream, p);
   }
   auto go = [&](auto NV) -> cudaError_t {
     constexpr int N = decltype(NV)::value * 4, GQ = N > 16 ? 2 : 4;
@@ -718,7 +726,7 @@ cudaError_t launch_paged(const PagedArgs &a) {
   err = nv <= 2 ? go(std::integral_constant<int, 2>{}) : nv <= 4 ? go(std::integral_constant<int, 4>{})
                 : go(std::integral_constant<int, 8>{});
   if (err != cudaSuccess) return err;
-  return launch_dependent(paged_join_kernel<float>, join, dim3(kJoinThreads), ctas * sizeof(float), a.stream, p, ctas);
+  return launch_dependent(paged_join_kernel<float>, join, dim3(kJoinWarps * 32), join_smem, a.stream, p);
 }
 
 }  // namespace attnres
