@@ -231,19 +231,35 @@ __global__ void __launch_bounds__(kWarpsF * 32) paged_f32_kernel(const PagedPara
       }
     }
     if (working) {
-      for (int j = j0 + strip * 4; j < j1; j += strips * 4) {   // the same trip count for a whole warp
+      // The next tokens' rows are on their way while the present ones are
+      // added, where the registers allow it.
+      constexpr bool kAhead = GQ * N <= 32;
+      uint4 nk[NV], nv[NV];
+      bool next_live;
+      auto read = [&](int j) {
         const int tok = j + team;
         const int64_t row = tok < j1 ? cache_row(p, pages[p.page_of(tok)], tok, w.hk) : -1;
-        const bool live = row >= 0;                 // a token on a page outside the pool is left out
-        uint4 kv[NV], vv[NV];
+        next_live = row >= 0;                       // a token on a page outside the pool is left out
 #pragma unroll
         for (int v = 0; v < NV; ++v) {
-          kv[v] = vv[v] = make_uint4(0, 0, 0, 0);
-          if (live && v * 8 + l8 < nvec) {
-            kv[v] = ld_stream((const float *)p.k + row + (v * 8 + l8) * E);
-            vv[v] = ld_stream((const float *)p.v + row + (v * 8 + l8) * E);
+          nk[v] = nv[v] = make_uint4(0, 0, 0, 0);
+          if (next_live && v * 8 + l8 < nvec) {
+            nk[v] = ld_stream((const float *)p.k + row + (v * 8 + l8) * E);
+            nv[v] = ld_stream((const float *)p.v + row + (v * 8 + l8) * E);
           }
         }
+      };
+      if (kAhead) read(j0 + strip * 4);
+      for (int j = j0 + strip * 4; j < j1; j += strips * 4) {   // the same trip count for a whole warp
+        uint4 kv[NV], vv[NV];
+        if (!kAhead) read(j);
+        const bool live = next_live;
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          kv[v] = nk[v];
+          vv[v] = nv[v];
+        }
+        if (kAhead) read(j + strips * 4);
         float s[GQ];
 #pragma unroll
         for (int g = 0; g < GQ; ++g) s[g] = 0.f;
@@ -359,7 +375,7 @@ constexpr int kWarpsM = 4;
 constexpr int kRow = 16;               // tokens per warp tile
 
 template <int D> struct MmaShape {
-  static constexpr int kPitch = (D + 63) / 64 * 128;            // bytes of a token's row in shared memory
+  static constexpr int kPitch = D > 128 ? 512 : (D + 63) / 64 * 128;   // bytes of a token's row in shared memory
   static constexpr int kStage = 2 * kRow * kPitch;              // keys, then values
   static constexpr int kStages = D <= 64 ? 6 : 3;
   static constexpr int kCtas = D <= 128 ? 2 : 1;                // per SM
@@ -435,23 +451,49 @@ __global__ void __launch_bounds__(kWarpsM * 32, MmaShape<D>::kCtas) paged_mma_ke
     }
   };
   settle();
+  constexpr int CH = S::kPitch / 16;                // pieces of a padded row
+  constexpr int kPerRow = kRow * CH / 32;           // copies per lane and tensor
+  const bool aligned = p.page % kRow == 0;          // a tile never spans two pages
   auto copy_tile = [&]() {
     if (cw.more()) {
       const int64_t row = cache_row(p, page_no, cj + lane % kRow, cw.hk);
       const unsigned bits = __ballot_sync(0xffffffffu, row >= 0) & 0xffffu;
       if (lane == 0) live_bits[warp][issue] = bits;
       const uint32_t dst = ring + issue * S::kStage;
-      constexpr int CH = S::kPitch / 16;            // pieces of a padded row
+      if (aligned && bits == 0xffffu) {
+        // sixteen rows side by side in one page
+        const int64_t at = __shfl_sync(0xffffffffu, row, 0) + (lane / CH) * p.d + (lane % CH) * 8;
+        const __nv_bfloat16 *ks = (const __nv_bfloat16 *)p.k + at, *vs = (const __nv_bfloat16 *)p.v + at;
+        const int step = 32 / CH * p.d;
+        if (lane % CH < chunks) {
 #pragma unroll
-      for (int i = 0; i < kRow * CH / 32; ++i) {
-        const int r = (i * 32 + lane) / CH, c = (i * 32 + lane) % CH;
-        const int64_t off = __shfl_sync(0xffffffffu, row, r);
-        const bool live = off >= 0 && c < chunks;
-        const int64_t at = live ? off + c * 8 : 0;
-        const uint32_t to = dst + r * S::kPitch + ((c ^ (r & 7)) * 16);
-        if (c * 8 < D) {
-          cp_async16(to, (const __nv_bfloat16 *)p.k + at, live);
-          cp_async16(to + kRow * S::kPitch, (const __nv_bfloat16 *)p.v + at, live);
+          for (int i = 0; i < kPerRow; ++i, ks += step, vs += step) {
+            const int r = (i * 32 + lane) / CH;
+            const uint32_t to = dst + r * S::kPitch + (((lane % CH) ^ (r & 7)) * 16);
+            cp_async16(to, ks, true);
+            cp_async16(to + kRow * S::kPitch, vs, true);
+          }
+        } else if (lane % CH * 8 < D) {             // a row's padding
+#pragma unroll
+          for (int i = 0; i < kPerRow; ++i) {
+            const int r = (i * 32 + lane) / CH;
+            const uint32_t to = dst + r * S::kPitch + (((lane % CH) ^ (r & 7)) * 16);
+            cp_async16(to, p.k, false);
+            cp_async16(to + kRow * S::kPitch, p.v, false);
+          }
+        }
+      } else {
+#pragma unroll 2
+        for (int i = 0; i < kPerRow; ++i) {
+          const int r = (i * 32 + lane) / CH, c = (i * 32 + lane) % CH;
+          const int64_t off = __shfl_sync(0xffffffffu, row, r);
+          const bool live = off >= 0 && c < chunks;
+          const int64_t at = live ? off + c * 8 : 0;
+          const uint32_t to = dst + r * S::kPitch + ((c ^ (r & 7)) * 16);
+          if (c * 8 < D) {
+            cp_async16(to, (const __nv_bfloat16 *)p.k + at, live);
+            cp_async16(to + kRow * S::kPitch, (const __nv_bfloat16 *)p.v + at, live);
+          }
         }
       }
       cj += kWarpsM * kRow;
@@ -713,14 +755,22 @@ cudaError_t launch_paged(const PagedArgs &a) {
       return launch_dependent(kern, grid, dim3(kWarpsM * 32), S::kSmem, a.stream, p);
     };
     err = a.d <= 64 ? go(std::integral_constant<int, 64>{}) : a.d <= 96 ? go(std::integral_constant<int, 96>{})
-        : a.d <= 128 ? go(std::integral_constant<int, 128>{}) : go(std::integral_constant<int, 256>{});
+        : a.d <= 128 ? go(std::integral_constant<int, 128>{}) : a.d <= 192 ? go(std::integral_constant<int, 192>{})
+        : go(std::integral_constant<int, 256>{});
     if (err != cudaSuccess) return err;
     return launch_dependent(paged_join_kernel<__nv_bfloat16>, join, dim3(kJoinWarps * 32), join_smem, a.stream, p);
   }
   auto go = [&](auto NV) -> cudaError_t {
-    constexpr int N = decltype(NV)::value * 4, GQ = N > 16 ? 2 : 4;
-    const size_t smem = (size_t)kWarpsF * GQ * (p.d + 2) * sizeof(float);
-    return launch_dependent(paged_f32_kernel<decltype(NV)::value, GQ>, grid, dim3(kWarpsF * 32), smem, a.stream, p);
+    // Query heads per warp: as many as its registers hold, two of them beyond
+    // 128 wide, but no more than a key head has.
+    constexpr int N = decltype(NV)::value * 4, kMost = N > 16 ? 2 : 4;
+    auto with = [&](auto gq) -> cudaError_t {
+      constexpr int GQ = decltype(gq)::value;
+      const size_t smem = (size_t)kWarpsF * GQ * (p.d + 2) * sizeof(float);
+      return launch_dependent(paged_f32_kernel<decltype(NV)::value, GQ>, grid, dim3(kWarpsF * 32), smem, a.stream, p);
+    };
+    return p.G == 1 ? with(std::integral_constant<int, 1>{}) : p.G == 2 ? with(std::integral_constant<int, 2>{})
+                    : with(std::integral_constant<int, kMost>{});
   };
   const int nv = (a.d / 4 + 7) / 8;
   err = nv <= 2 ? go(std::integral_constant<int, 2>{}) : nv <= 4 ? go(std::integral_constant<int, 4>{})
