@@ -261,8 +261,7 @@ struct LinearArgs {              // out_i = alpha (sum_{j <= i} e^{g (i - j)} (a
   cudaStream_t stream;
 };
 bool linear_supported(int64_t da, int64_t dc, int dtype);
-// Segments the time axis is cut into, and the fp32 workspace they need.
-int linear_segments(int64_t B, int64_t T, int H, int da, int dc, int dtype);
+// The fp32 workspace of a call: the segments' states.
 int64_t linear_workspace_floats(int64_t B, int64_t T, int H, int da, int dc, int dtype);
 cudaError_t launch_linear(const LinearArgs &a);
 

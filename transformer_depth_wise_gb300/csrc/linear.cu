@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kThreads) linear_general_kernel(const LinearPa
   if (threadIdx.x <= kC) pw[threadIdx.x] = decay_pow(g, threadIdx.x);
 
   float s[MB * 4][4];                                  // state rows mb * 64 + ty * 4 + i, columns tx * 4 + j
-  float *states = p.states + ((bh * p.nseg + seg) * p.da) * p.dc;
+  float *states = p.states + ((bh * p.nstates + seg * p.step) * p.da) * p.dc;
 #pragma unroll
   for (int m = 0; m < MB * 4; ++m) {
     const int row = (m / 4) * 64 + ty * 4 + m % 4;
@@ -244,7 +244,8 @@ __global__ void __launch_bounds__(kThreads) linear_general_kernel(const LinearPa
 }
 
 // The segments' own states become the states they begin with; the state
-// after the last token is written where it is wanted.  Four elements of a row
+// after the last token is written where it is wanted (else the last segment's
+// own state is not used, whatever is there).  Four elements of a row
 // per thread, the next segments' on their way while one is added.
 __global__ void __launch_bounds__(kThreads) linear_scan_kernel(const LinearParams p) {
   grid_dependency_wait();
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(kThreads) linear_scan_kernel(const LinearParam
   if (p.first)
     cur = make_float4(first_at(p, bh, row, col), first_at(p, bh, row, col + 1), first_at(p, bh, row, col + 2),
                       first_at(p, bh, row, col + 3));
-  float4 *st = reinterpret_cast<float4 *>(p.states) + bh * p.nseg * per + e;
+  float4 *st = reinterpret_cast<float4 *>(p.states) + bh * p.nstates * per + e;
   const float full = decay_pow(g, p.seg_len);
   auto read = [&](int s) { return s < p.nseg ? st[(int64_t)s * per] : make_float4(0.f, 0.f, 0.f, 0.f); };
   float4 own = read(0), next = read(1), after = read(2);
@@ -390,19 +391,21 @@ bool linear_supported(int64_t da, int64_t dc, int dtype) {
 // shorter than 256 tokens (a segment's state costs as much traffic as about
 // 128 tokens).  The same with da and dc exchanged, so that two calls can share
 // the segments' states.
-int linear_segments(int64_t B, int64_t T, int H, int da, int dc, int dtype) {
-  if (B * H < 1) return 1;
-  if (linear_tc_supported(T, dtype)) return linear_tc_segments(B * H, T);
+static Split linear_split(int64_t B, int64_t T, int H, int da, int dc, int dtype) {
+  if (B * H < 1 || T < 1) return {kChunk, 1, 1};
+  if (linear_tc_supported(T, dtype)) return linear_tc_split(B * H, T);
   const int64_t have = B * H * general_slices(da > dc ? da : dc), want = 2 * (int64_t)sm_count();
   int64_t n = (want + have - 1) / have;
   const int64_t most = T / 256;
   if (n > most) n = most;
-  return n < 1 ? 1 : (int)n;
+  if (n < 1) n = 1;
+  const int64_t len = ((T + n - 1) / n + kC - 1) / kC * kC;
+  return {len, (int)((T + len - 1) / len), 1};
 }
 
 int64_t linear_workspace_floats(int64_t B, int64_t T, int H, int da, int dc, int dtype) {
-  const int n = linear_segments(B, T, H, da, dc, dtype);
-  return n > 1 ? B * H * n * da * dc : 0;
+  const Split s = linear_split(B, T, H, da, dc, dtype);
+  return s.nseg > 1 ? B * H * s.nseg * s.nsub * da * dc : 0;
 }
 
 cudaError_t launch_linear(const LinearArgs &a) {
@@ -411,10 +414,11 @@ cudaError_t launch_linear(const LinearArgs &a) {
   p.a_stride = a.a_stride; p.b_stride = a.b_stride; p.c_stride = a.c_stride;
   p.out = a.out; p.T = a.T; p.H = a.H; p.da = a.da; p.dc = a.dc;
   p.slices = general_slices(a.dc);
-  p.nseg = linear_segments(a.B, a.T, a.H, a.da, a.dc, a.dtype);
-  p.seg_len = (a.T + p.nseg - 1) / p.nseg;
-  p.seg_len = a.T > 0 ? (p.seg_len + kC - 1) / kC * kC : kC;
-  p.nseg = a.T > 0 ? (int)((a.T + p.seg_len - 1) / p.seg_len) : 1;
+  const Split split = linear_split(a.B, a.T, a.H, a.da, a.dc, a.dtype);
+  p.nseg = split.nseg;
+  p.seg_len = split.seg_len;
+  p.nstates = split.nseg * split.nsub;
+  p.step = split.nsub;
   p.log_decay = a.log_decay; p.lengths = a.lengths; p.alpha = a.alpha; p.reverse = a.reverse;
   p.first = a.first; p.first_t = a.first_t; p.first_pow = a.first_pow; p.first_scale = a.first_scale;
   p.last = a.last; p.last_scale = a.last_scale; p.last_pow = a.last_pow;
@@ -424,7 +428,7 @@ cudaError_t launch_linear(const LinearArgs &a) {
   const int64_t BH = a.B * a.H;
   const bool tc = linear_tc_supported(a.T, a.dtype);
   // The states' kernel (states = true) or the main one.
-  auto chunks = [&](bool states) -> cudaError_t {
+  auto chunks = [&](const LinearParams &p, bool states) -> cudaError_t {
     if (tc) return launch_linear_tc(p, BH, states, a.stream);
     const int64_t ctas = BH * p.nseg * p.slices;
     auto go = [&](auto elt, auto da) -> cudaError_t {
@@ -440,13 +444,20 @@ cudaError_t launch_linear(const LinearArgs &a) {
     return a.dtype == ATTNRES_BF16 ? with_da(__nv_bfloat16{}) : with_da(float{});
   };
   if (p.nseg > 1 && !a.states_ready) {
-    cudaError_t e = chunks(true);
+    // The pieces' own states (the last segment's only where the final state
+    // is wanted), then the states they begin with.
+    LinearParams s = p;
+    s.seg_len = p.seg_len / split.nsub;
+    s.step = 1;
+    s.nseg = (a.last ? p.nseg : p.nseg - 1) * split.nsub;
+    cudaError_t e = chunks(s, true);
     if (e != cudaSuccess) return e;
+    if (!a.last) ++s.nseg;
     e = launch_dependent(linear_scan_kernel, dim3((unsigned)((a.da * a.dc / 4 + kThreads - 1) / kThreads), (unsigned)BH),
-                         dim3(kThreads), 0, a.stream, p);
+                         dim3(kThreads), 0, a.stream, s);
     if (e != cudaSuccess) return e;
   }
-  return chunks(false);
+  return chunks(p, false);
 }
 
 cudaError_t launch_linear_step(const LinearStepArgs &a) {

@@ -23,7 +23,11 @@ struct LinearParams {
   float *last;
   float last_scale;
   int last_pow;
-  float *states;                       // [B, H, nseg, da, dc] (nseg > 1)
+  // The states that the segments begin with (nseg > 1): [B, H, nstates, da, dc],
+  // segment s of this launch's begins with state s * step.  The states' kernel
+  // may cut the segments finer than the main one.
+  float *states;
+  int nstates, step;
   int states_t;                        // or [.., dc, da], for the main kernel
   long long wait_limit;                // SM clock cycles any wait of the tensor-core kernel may take
 };
@@ -50,10 +54,16 @@ __device__ __forceinline__ int64_t walk_row(const LinearParams &p, int64_t b, in
 // Segments hold whole chunks of 64 tokens.
 constexpr int kChunk = 64;
 
-// The tensor-core form (bf16): its segments, and the launches of the states'
+// How the time axis is cut: nseg segments of seg_len tokens, each of nsub
+// pieces (whole chunks) for the states' kernel.
+struct Split {
+  int64_t seg_len;
+  int nseg, nsub;
+};
+// The tensor-core form (bf16): its split, and the launches of the states'
 // kernel and of the main one.
 bool linear_tc_supported(int64_t T, int dtype);
-int linear_tc_segments(int64_t BH, int64_t T);
+Split linear_tc_split(int64_t BH, int64_t T);
 cudaError_t launch_linear_tc(const LinearParams &p, int64_t BH, bool states, cudaStream_t stream);
 
 }  // namespace attnres

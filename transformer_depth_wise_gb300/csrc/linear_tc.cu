@@ -416,12 +416,12 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
     share_registers<L::kRegsS, L::kRegs>();
     const int row = quad * 32 + lane, col0 = group * 64;               // dc, da
     uint64_t st[32];                                    // columns col0 + 2 j and the next
-    float *states = p.states + ((bh * p.nseg + seg) * p.da + col0) * p.dc + row;
+    float *states = p.states + ((bh * p.nstates + seg * p.step) * p.da + col0) * p.dc + row;
     const int cols = row < p.dc ? p.da - col0 : 0;      // of this thread's row that exist (da is even)
     {
       // the segment's first state, or the call's (which may lie transposed)
       const bool own = p.nseg > 1, across = own ? p.states_t : p.first_t;
-      const float *src = (own ? p.states + (bh * p.nseg + seg) * p.da * p.dc : p.first + bh * p.da * p.dc) +
+      const float *src = (own ? p.states + (bh * p.nstates + seg * p.step) * p.da * p.dc : p.first + bh * p.da * p.dc) +
                          (across ? (int64_t)row * p.da + col0 : (int64_t)col0 * p.dc + row);
       const int step = across ? 1 : p.dc;
       const float f = own ? 1.f : p.first_scale;
@@ -660,19 +660,26 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
 // fp32 products also spare a handful of tokens the rounding of P.
 bool linear_tc_supported(int64_t T, int dtype) { return dtype == ATTNRES_BF16 && T >= kChunk; }
 
-// Segments: the count with the least waves of CTAs times their length.  A
-// CTA's fixed cost is worth about six chunks, and with more than one segment
-// the states' kernel and the scan add about half of the main kernel's time.
-int linear_tc_segments(int64_t BH, int64_t T) {
+// The split with the least cost in waves of CTAs, one per SM, times their
+// chunks.  A CTA's fixed cost is worth about eight chunks of the main kernel's,
+// a chunk of the states' kernel a bit more than half of one and its fixed cost
+// three; the scan and the launches make up for four, and every state written,
+// scanned and read for a fiftieth.
+Split linear_tc_split(int64_t BH, int64_t T) {
   const int64_t slots = sm_count(), chunks = (T + kChunk - 1) / kChunk;
-  int best = 1;
-  double least = 0.;
-  for (int n = 1; n <= 64 && n * 4 <= chunks + 3; ++n) {
-    const int64_t per = (chunks + n - 1) / n, waves = (BH * ((chunks + per - 1) / per) + slots - 1) / slots;
-    const double cost = (double)waves * (double)(per + 6) * (n > 1 ? 1.5 : 1.0) + (n > 1 ? 8. : 0.);
-    if (n == 1 || cost < least) {
-      least = cost;
-      best = n;
+  auto waves = [&](int64_t ctas) { return (double)((ctas + slots - 1) / slots); };
+  Split best{chunks * kChunk, 1, 1};
+  double least = waves(BH) * (double)(chunks + 8);
+  for (int n = 2; n <= 64 && n * 4 <= chunks; ++n) {
+    for (int k = 1; k <= 4 && n * k * 4 <= chunks; k *= 2) {
+      const int64_t piece = (chunks + (int64_t)n * k - 1) / ((int64_t)n * k), per = piece * k;
+      const int64_t segments = (chunks + per - 1) / per;
+      const double cost = waves(BH * segments) * (double)(per + 8) + 0.55 * waves(BH * (segments - 1) * k) * (double)(piece + 3) +
+                          4. + 0.02 * (double)(BH * segments * k);
+      if (segments > 1 && cost < least) {
+        least = cost;
+        best = {per * kChunk, (int)segments, k};
+      }
     }
   }
   return best;
