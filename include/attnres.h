@@ -309,7 +309,8 @@ int attnres_head_norm_rotate(const void *q, const void *k, int64_t B, int64_t T,
  *   v           device [B,T,Hk,d]
  *   k_cache, v_cache  device [num_pages, Hk, page_size, d]
  *   page_table  device int32 [B, max_pages]: page i of sequence b holds its
- *               positions i * page_size .. (i + 1) * page_size - 1
+ *               positions i * page_size .. (i + 1) * page_size - 1;
+ *               page_size * max_pages at most 2^30
  * A token's place in the cache is its position.  A token whose position is
  * negative or behind the table, or whose page number is outside
  * [0, num_pages), is rotated into q_out but not stored (padding).  Two
@@ -385,7 +386,7 @@ int64_t attnres_paged_attention_workspace_bytes(int Hq, int Hk, int64_t d, int d
  *   lengths     device int32 [B] or NULL (T): tokens of each sequence, held
  *               within 0 .. T; out behind them is zero
  *   state       device fp32 [B,H,dk,dv] S_0, or NULL (zeros)
- *   out         device [B,T,H,dv], contiguous
+ *   out         device [B,T,H,dv], contiguous; overlaps none of the inputs
  *   state_out   device fp32 [B,H,dk,dv] S after each sequence's last token, or NULL; may be state
  *   workspace   device, attnres_linear_attention_workspace_bytes() bytes (may
  *               be 0, then NULL is allowed); contents on entry do not matter
@@ -408,7 +409,8 @@ int attnres_linear_attention(const void *q, const void *k, const void *v, int64_
  *   dq_t = scale S_t grad_out_t,  dk_t = G_t v_t,  dv_t = G_t^T k_t,
  *   grad_initial = e^g G_1
  *   grad_out    device [B,T,H,dv], rows grad_out_stride elements apart
- *   dq, dk, dv_out  device, contiguous; zero behind the sequences
+ *   dq, dk, dv_out  device, contiguous, overlapping none of the inputs; zero
+ *               behind the sequences
  *   grad_initial  device fp32 [B,H,dk,dv] or NULL; must not be grad_state
  *   workspace   attnres_linear_attention_backward_workspace_bytes() bytes
  * The sums run in a fixed order: the same inputs give the same bits.

@@ -38,7 +38,7 @@ def append(q=FAKE, v=FAKE, B=1, T=1, Hk=2, vs=128, kc=FAKE, vc=FAKE, num=4, page
 
 def test_append_refusals():
     assert append(page=0) == SHAPE and append(num=-1) == SHAPE and append(maxp=-1) == SHAPE
-    assert append(page=1 << 20, maxp=1 << 12) == SHAPE
+    assert append(page=1 << 20, maxp=1 << 12) == SHAPE and append(page=1 << 20, maxp=1025) == SHAPE
     assert append(vs=4) == ALIGN and append(qos=128) == SHAPE
     assert append(v=None) == NULL and append(kc=None) == NULL and append(vc=None) == NULL and append(table=None) == NULL
     assert append(kc=FAKE + 8) == ALIGN and append(table=FAKE + 2) == ALIGN

@@ -480,6 +480,54 @@ def test_linear_extreme_decays(gpu, dtype, decay):
 
 
 @gpu_only
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,g,back", [(3000, -0.25, 5), (3000, -0.25, 400), (65536, -1.0, 150), (65536, -1.0, 165)])
+def test_linear_old_large_tokens_are_not_forgotten(gpu, dtype, T, g, back):
+    # one token of 1e18 among zeros: its trace in the final state, 1e36 e^{g back}, is small but no zero, also when
+    # it comes from an earlier segment of the time axis, and when its weight alone is below fp32's smallest number
+    q, k, v, _, scale = linear_inputs(gpu, dtype, 1, T, 1, 64, 64, 3)
+    k.zero_(), v.zero_()
+    k[0, T - 1 - back, 0, 3] = v[0, T - 1 - back, 0, 5] = 1e18
+    ld = torch.full((1,), g, device=gpu)
+    _, last = api.linear_attention(q, k, v, ld, scale)
+    want = torch.zeros(1, 1, 64, 64, dtype=torch.float64)
+    want[0, 0, 3, 5] = float(k[0, T - 1 - back, 0, 3].double()) * float(v[0, T - 1 - back, 0, 5].double()) * math.exp(g * back)
+    # products of decays over chunks: each a rounding of its exponent (at most 64 |g| E) and of itself
+    within(last, want, want.abs() * (back / 64 + 2) * (64 * abs(g) + 4) * E)
+
+
+@gpu_only
+def test_linear_nan_and_large_decays_stay_in_their_heads(gpu):
+    q, k, v, ld, scale = linear_inputs(gpu, BF, 2, 700, 4, 64, 128, 5)
+    want = api.linear_attention(q, k, v, ld, scale)
+    ld[2] = float("nan")
+    out, last = api.linear_attention(q, k, v, ld, scale)
+    keep = [0, 1, 3]
+    assert torch.equal(out[:, :, keep], want[0][:, :, keep]) and torch.equal(last[:, keep], want[1][:, keep])
+
+
+@gpu_only
+def test_linear_wait_that_runs_out_reports_timeout(gpu):
+    """With a limit of one clock cycle the tensor-core kernels' waits give up: every role stops or runs to its end
+    without waiting, the CTA drains what it has in flight, the error is reported, and the device stays usable."""
+    from transformer_depth_wise_gb300 import _lib
+    L = _lib.lib()
+    q, k, v, ld, scale = linear_inputs(gpu, BF, 2, 2000, 4, 128, 128, 6)
+    want = api.linear_attention(q, k, v, ld, scale)
+    assert L.attnres_take_device_error() == 0
+    assert L.attnres_set_wait_limit(1) == 0
+    try:
+        api.linear_attention(q, k, v, ld, scale)
+        rc = L.attnres_take_device_error()
+    finally:
+        assert L.attnres_set_wait_limit(0) == 0
+    assert rc == -9, _lib.STATUS.get(rc, rc)                              # ATTNRES_ERR_TIMEOUT
+    got = api.linear_attention(q, k, v, ld, scale)
+    assert L.attnres_take_device_error() == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@gpu_only
 def test_linear_views_of_one_projection_and_split_prompts(gpu):
     B, T, H, d = 2, 300, 4, 64
     g = wk.generator(31, gpu)

@@ -52,8 +52,9 @@ int check_heads(int64_t B, int64_t T, int Hq, int Hk, int64_t d, int dtype, int6
 
 bool misaligned(const void *p, int to = 16) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) != 0; }
 
+// Token indices, and the loops that step past their ends, stay within 32 bits.
 int check_pages(int64_t num_pages, int page_size, int max_pages) {
-  return num_pages < 0 || page_size < 1 || max_pages < 0 || (int64_t)page_size * max_pages > INT32_MAX
+  return num_pages < 0 || page_size < 1 || max_pages < 0 || (int64_t)page_size * max_pages > (int64_t)1 << 30
              ? ATTNRES_ERR_SHAPE : ATTNRES_OK;
 }
 

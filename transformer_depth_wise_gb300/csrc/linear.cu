@@ -393,7 +393,10 @@ bool linear_supported(int64_t da, int64_t dc, int dtype) {
 // the segments' states.
 static Split linear_split(int64_t B, int64_t T, int H, int da, int dc, int dtype) {
   if (B * H < 1 || T < 1) return {kChunk, 1, 1};
-  if (linear_tc_supported(T, dtype)) return linear_tc_split(B * H, T);
+  if (linear_tc_supported(T, dtype)) {
+    if (B * H > 65535) return {(T + kC - 1) / kC * kC, 1, 1};    // the scan's grid; and the SMs are full
+    return linear_tc_split(B * H, T);
+  }
   const int64_t have = B * H * general_slices(da > dc ? da : dc), want = 2 * (int64_t)sm_count();
   int64_t n = (want + have - 1) / have;
   const int64_t most = T / 256;

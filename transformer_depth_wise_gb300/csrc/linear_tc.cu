@@ -238,9 +238,10 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
   const float g = p.log_decay[h];
   int64_t from = begin;
   if (STATES && g < 0.f && stop > begin) {
-    // Tokens whose weight in the segment's last state is below fp32's
-    // smallest number (e^-104) add exactly nothing: start behind them.
-    const float reach = 104.f / -g;
+    // Tokens whose weight in the segment's last state is so small that even
+    // the largest finite product of a b and a c comes below fp32's smallest
+    // number (e^-193 of e^88.8) add exactly nothing: start behind them.
+    const float reach = 193.f / -g;
     if (reach < (float)(stop - begin)) from = max(begin, (stop - 1 - (int64_t)reach) / kC * kC);
   }
   const int chunks = stop > from ? (int)((stop - from + kC - 1) / kC) : 0;
