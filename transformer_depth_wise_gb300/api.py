@@ -621,9 +621,24 @@ def block_two_phase(blocks, queries, gains, u, eps: float = 1e-8, fused: bool = 
 # The attention sublayer: head norm with rotation, paged attention of one
 # token, linear attention with a decay per head.
 # --------------------------------------------------------------------------
+_FUNCTIONS = {}                       # C entry points by name
+
+
+def _function(name: str):
+    fn = _FUNCTIONS.get(name)
+    if fn is None:
+        fn = _FUNCTIONS[name] = getattr(_lib.lib(), name)
+    return fn
+
+
+# The current stream's handle without a Stream object in between.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(name: str, device: torch.device, *args) -> None:
     """The C entry point on `device`'s current stream, with that device current."""
-    fn = getattr(_lib.lib(), name)
+    fn = _function(name)
     index = device.index
     if index == torch.cuda.current_device():
         rc = fn(*args, _raw_stream(index))
@@ -634,20 +649,20 @@ def _call(name: str, device: torch.device, *args) -> None:
         _lib.check(name, rc)
 
 
-# The current stream's handle without a Stream object in between.
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
-    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+_SIZES = {}                           # workspace sizes by query, arguments and device
 
 
 def _sized(name: str, device: torch.device, *args) -> int:
-    """A workspace query with `device` current."""
-    fn = getattr(_lib.lib(), name)
-    if device.index == torch.cuda.current_device():
-        n = fn(*args)
-    else:
+    """A workspace query with `device` current (its answer depends on nothing else)."""
+    key = (name, device.index, args)
+    n = _SIZES.get(key)
+    if n is None:
         with torch.cuda.device(device):
-            n = fn(*args)
-    return n if n >= 0 else _lib.check(name, int(n))
+            n = int(_lib.check(name, _function(name)(*args)))
+        if len(_SIZES) >= 4096:
+            _SIZES.clear()
+        _SIZES[key] = n
+    return n
 
 
 def _heads(t, name: str, like=None, shape=None) -> int:
@@ -658,7 +673,7 @@ def _heads(t, name: str, like=None, shape=None) -> int:
     if shape is not None and have != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(have)}")
     if like is not None:
-        if t.dtype != like.dtype:
+        if t.dtype is not like.dtype:
             raise TypeError(f"{name} must be {like.dtype}")
         if t.device != like.device:
             raise ValueError(f"{name} must be on {like.device}")
@@ -667,13 +682,14 @@ def _heads(t, name: str, like=None, shape=None) -> int:
     st = t.stride()
     if len(st) == 4:
         B, T, H, d = have
-        sb, stt = st[0], st[1]
+        sb, stt, sh, sd = st
     elif len(st) == 3:
         T, H, d = have
-        B, sb, stt = 1, 0, st[0]
+        stt, sh, sd = st
+        B, sb = 1, 0
     else:
         raise ValueError(f"{name} must be [B, T, H, d]")
-    if (d > 1 and st[-1] != 1) or (H > 1 and st[-2] != d):
+    if (sd != 1 and d > 1) or (sh != d and H > 1):
         if t.numel():
             raise ValueError(f"{name}: the heads of a token must lie side by side")
     if T > 1:
@@ -687,10 +703,10 @@ def _plain(t, name: str, dtype, shape, device):
     """A contiguous CUDA tensor of this dtype and shape on `device` (None stays None)."""
     if t is None:
         return None
-    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape and t.device == device and t.is_contiguous():
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device:
         return t
     _cuda(t, name)
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
@@ -942,8 +958,9 @@ def linear_attention_step(q, k, v, log_decay, scale: float, state, state_out=Non
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a [B, H, d] tensor")
     qs = _heads(q, "q")
-    B, H, dk = q.shape
-    ks = _heads(k, "k", q, q.shape)
+    shape = q.shape
+    B, H, dk = shape
+    ks = _heads(k, "k", q, shape)
     if not isinstance(v, torch.Tensor) or v.dim() != 3:
         raise ValueError("v must be a [B, H, d] tensor")
     dv = v.shape[2]
