@@ -33,6 +33,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
+constexpr int kBackFlight = 2;         // heads a team of the backward kernel has in flight
 
 // inv_freq (radians per position) as 2^-64ths of a turn per position, modulo
 // one turn; 0 for what is no number.
@@ -240,6 +241,7 @@ __global__ void __launch_bounds__(kThreads, 2) head_norm_kernel(const HeadParams
       }
       uint64_t w[2 * NP];
       if (active) load_weight<T>(w, which ? p.wk : p.wq, u.off0, u.off1);
+      float c[2 * NP] = {}, sn[2 * NP] = {};     // the lane's angles
       for (int hb = h0; hb < h1; hb += kTeams * kFlight) {
         uint4 va[kFlight], vb[kFlight];
 #pragma unroll
@@ -255,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, 2) head_norm_kernel(const HeadParams
           ang.form(position);
           formed = true;
         }
+        if (hb == h0 && active && u.turn) ang.template read<2 * NP>(u.angle, c, sn);
 #pragma unroll
         for (int k = 0; k < kFlight; ++k) {
           const int h = hb + k * kTeams + team;
@@ -270,11 +273,7 @@ __global__ void __launch_bounds__(kThreads, 2) head_norm_kernel(const HeadParams
           const uint64_t rms2 = pair(rms, rms);
 #pragma unroll
           for (int i = 0; i < 2 * NP; ++i) x[i] = mul2(mul2(x[i], rms2), w[i]);
-          if (u.turn) {
-            float c[2 * NP], sn[2 * NP];
-            ang.template read<2 * NP>(u.angle, c, sn);
-            turn<T, INTER, false>(x, c, sn);
-          }
+          if (u.turn) turn<T, INTER, false>(x, c, sn);
           T *y = y0 + h * step;
           st_vec(y + u.off0, from_pairs<T>(x));
           st_vec(y + u.off1, from_pairs<T>(x + NP));
@@ -307,7 +306,7 @@ struct HeadBackwardParams {
   const double *inv_freq;
   int64_t rows, T;
   int H[2], d, rot;
-  int parts, per_part;               // a row's heads (q, then k) in parts, one per work item
+  int parts[2], per_part[2];         // a row's heads in parts, one per work item
   float eps, inv_d;
 };
 
@@ -315,34 +314,31 @@ template <typename T, int TEAM, bool INTER>
 __global__ void __launch_bounds__(kThreads, 2) head_norm_backward_kernel(const HeadBackwardParams p) {
   constexpr int E = Elt<T>::EPV, NP = Pairs<T>::NP;
   constexpr int kTeams = 32 / TEAM;
-  constexpr int kFlight = 2;
+  constexpr int kFlight = kBackFlight;
   extern __shared__ char smem[];
   grid_dependency_wait();
   const Angles ang(smem, p.inv_freq, p.rot);
   const int lane = threadIdx.x % TEAM, team = threadIdx.x % 32 / TEAM;
   const bool active = lane * 2 * E < p.d;
   const Unit<T, INTER> u(lane, p.rot);
-  const int64_t items = p.rows * p.parts, stride = (int64_t)gridDim.x * kWarps;
+  const int64_t stride = (int64_t)gridDim.x * kWarps;
 
-  uint64_t dw[2][2 * NP];                        // this lane's sums, of the queries' and the keys' weight
+  // All of the queries' heads, then the keys', so that the sums of one weight
+  // are in registers at a time.
+#pragma unroll 1
+  for (int which = 0; which < 2; ++which) {
+    uint64_t dw[2 * NP], w[2 * NP];
 #pragma unroll
-  for (int i = 0; i < 2 * NP; ++i) dw[0][i] = dw[1][i] = 0;
-  for (int64_t item = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32; item < items; item += stride) {
-    const int64_t row = p.parts == 1 ? item : item / p.parts;
-    const int from = p.parts == 1 ? 0 : (int)(item - row * p.parts) * p.per_part;
-    const int to = min(p.H[0] + p.H[1], from + p.per_part);
-    const int position = p.positions ? p.positions[row] : (int)(row % p.T);
-    bool formed = false;
-#pragma unroll
-    for (int which = 0; which < 2; ++which) {
-      const int first = which ? p.H[0] : 0;
-      const int h0 = max(from, first) - first, h1 = min(to, first + p.H[which]) - first;
-      if (h0 >= h1) continue;
+    for (int i = 0; i < 2 * NP; ++i) dw[i] = 0;
+    if (active) load_weight<T>(w, p.w[which], u.off0, u.off1);
+    const int parts = p.parts[which], H = p.H[which];
+    for (int64_t item = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32; item < p.rows * parts; item += stride) {
+      const int64_t row = parts == 1 ? item : item / parts;
+      const int h0 = parts == 1 ? 0 : (int)(item - row * parts) * p.per_part[which], h1 = min(H, h0 + p.per_part[which]);
+      const int position = p.positions ? p.positions[row] : (int)(row % p.T);
       const T *x0 = (const T *)p.x[which] + row * p.stride[which];
       const T *g0 = (const T *)p.g[which] + row * p.gstride[which];
-      T *y0 = (T *)p.dx[which] + row * p.H[which] * p.d;
-      uint64_t w[2 * NP];
-      if (active) load_weight<T>(w, p.w[which], u.off0, u.off1);
+      T *y0 = (T *)p.dx[which] + row * H * p.d;
       for (int hb = h0; hb < h1; hb += kTeams * kFlight) {
         uint4 xa[kFlight], xb[kFlight], ga[kFlight], gb[kFlight];
 #pragma unroll
@@ -356,10 +352,7 @@ __global__ void __launch_bounds__(kThreads, 2) head_norm_backward_kernel(const H
             gb[k] = *reinterpret_cast<const uint4 *>(g0 + h * p.d + u.off1);
           }
         }
-        if (!formed) {
-          ang.form(position);
-          formed = true;
-        }
+        if (hb == h0) ang.form(position);        // with the first heads on their way
 #pragma unroll
         for (int k = 0; k < kFlight; ++k) {
           const int h = hb + k * kTeams + team;
@@ -388,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 2) head_norm_backward_kernel(const H
           const uint64_t r2 = pair(r, r), rc2 = pair(rc, rc);
 #pragma unroll
           for (int i = 0; i < 2 * NP; ++i) {
-            fma_pair(dw[which][i], g[i], mul2(x[i], r2));
+            fma_pair(dw[i], g[i], mul2(x[i], r2));
             v[i] = fma2(x[i], rc2, mul2(v[i], r2));
           }
           T *y = y0 + h * p.d;
@@ -397,26 +390,21 @@ __global__ void __launch_bounds__(kThreads, 2) head_norm_backward_kernel(const H
         }
       }
     }
-  }
-  if (!p.partials) return;
-  // The CTA's sums: over the teams of a warp by shuffles, over the warps
-  // through shared memory in a fixed order (reproducible).
-  float *red = reinterpret_cast<float *>(smem);      // [warps][d]: the angles are no longer needed
-  const int warp = threadIdx.x / 32;
-#pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    __syncthreads();
+    if (!p.partials) continue;
+    // The CTA's sums: over the teams of a warp by shuffles, over the warps
+    // through shared memory in a fixed order (reproducible).
+    float *red = reinterpret_cast<float *>(smem) + p.rot / 2 * 2 * (1 + kWarps);   // [warps][d], behind the angles
 #pragma unroll
     for (int i = 0; i < 2 * NP; ++i) {
       float lo, hi;
-      unpair(dw[which][i], lo, hi);
+      unpair(dw[i], lo, hi);
 #pragma unroll
       for (int o = TEAM; o < 32; o <<= 1) {
         lo += __shfl_xor_sync(0xffffffffu, lo, o);
         hi += __shfl_xor_sync(0xffffffffu, hi, o);
       }
       if (team == 0 && active) {
-        float *at = red + warp * p.d + (i < NP ? u.off0 + 2 * i : u.off1 + 2 * (i - NP));
+        float *at = red + threadIdx.x / 32 * p.d + (i < NP ? u.off0 + 2 * i : u.off1 + 2 * (i - NP));
         at[0] = lo;
         at[1] = hi;
       }
@@ -428,6 +416,7 @@ __global__ void __launch_bounds__(kThreads, 2) head_norm_backward_kernel(const H
       for (int k = 0; k < kWarps; ++k) s += red[k * p.d + i];
       p.partials[((int64_t)blockIdx.x * 2 + which) * p.d + i] = s;
     }
+    __syncthreads();
   }
 }
 
@@ -526,13 +515,15 @@ cudaError_t launch_head_norm_backward(const HeadNormBackwardArgs &a) {
   cudaError_t e = dispatch(a.dtype, a.d, a.interleaved, [&](auto elt, auto team, auto inter) -> cudaError_t {
     using T = decltype(elt);
     constexpr int TEAM = decltype(team)::value;
-    // A few items per warp, of whole rounds of its teams (two heads each in flight).
-    p.parts = row_parts(a.rows, a.Hq + a.Hk, 2 * (32 / TEAM), 4 * (int64_t)limit * kWarps, p.per_part);
-    const int64_t want = (a.rows * p.parts + kWarps - 1) / kWarps;
+    // Two items per warp, of whole rounds of its teams (kBackFlight heads each in flight).
+    int64_t most = 0;
+    for (int i = 0; i < 2; ++i) {
+      p.parts[i] = row_parts(a.rows, p.H[i], kBackFlight * (32 / TEAM), 2 * (int64_t)limit * kWarps, p.per_part[i]);
+      if (a.rows * p.parts[i] > most) most = a.rows * p.parts[i];
+    }
+    const int64_t want = (most + kWarps - 1) / kWarps;
     ctas = (int)(want < limit ? want : limit);
-    size_t smem = Angles::bytes(a.rot);
-    const size_t red = (size_t)kWarps * a.d * sizeof(float);
-    if (smem < red) smem = red;
+    const size_t smem = Angles::bytes(a.rot) + (size_t)kWarps * a.d * sizeof(float);
     return launch_dependent(head_norm_backward_kernel<T, TEAM, decltype(inter)::value>, dim3((unsigned)ctas),
                             dim3(kThreads), smem, a.stream, p);
   });
