@@ -834,7 +834,8 @@ def head_norm_rotate_backward(q, k, q_weight, k_weight, positions, inv_freq, eps
     gw = gkw = None
     rows = 0
     if want_weights:
-        gw, gkw = torch.empty((2, d), dtype=torch.float32, device=dev).unbind(0)
+        gw = torch.empty(d, dtype=torch.float32, device=dev)
+        gkw = torch.empty(d, dtype=torch.float32, device=dev)
         if workspace is None:
             rows = _sized("attnres_head_norm_rotate_backward_workspace_rows", dev)
             workspace = torch.empty((rows, d), dtype=torch.float32, device=dev)
