@@ -17,6 +17,12 @@
 // noted pairs' parts in order with the same (lse, o) rule as the two-phase
 // merge.  At most one pair per CTA is cut, so the workspace depends on the
 // grid alone, and the result on nothing but the inputs and the device.
+//
+// The cache's bytes bind.  Measured on GB300, bf16, heads of 128: 256 sequences
+// of up to 8192 tokens, 56 query over 8 key heads, 4.3 GB in 681 us (6.3 TB/s)
+// and 9 us for the join; 65537 and 131071 tokens, 32 over 4, 403 MB in 65 us
+// (6.2 TB/s) and 7 us.  fp32: 6.0 TB/s with one query head per key head, 4.1
+// with four, 1.05 with 16, where the CUDA cores bind.
 #include <type_traits>
 
 #include "common.cuh"
