@@ -521,10 +521,25 @@ cudaError_t launch_head_norm_backward(const HeadNormBackwardArgs &a) {
   cudaError_t e = dispatch(a.dtype, a.d, a.interleaved, [&](auto elt, auto team, auto inter) -> cudaError_t {
     using T = decltype(elt);
     constexpr int TEAM = decltype(team)::value;
-    // Two items per warp, of whole rounds of its teams (kBackFlight heads each in flight).
+    // The parts with the least work for the busiest warp.  An item costs its
+    // heads, in whole rounds of the warp's teams (kBackFlight heads each in
+    // flight), and the row's angles, worth six heads.  Against two items per
+    // warp: 1024 rows of 32 + 8 heads 14.0 against 15.4 us, 2048 18.3 against 19.7,
+    // 512 and 3000 (cut into four and two) the same.
     int64_t most = 0;
     for (int i = 0; i < 2; ++i) {
-      p.parts[i] = row_parts(a.rows, p.H[i], kBackFlight * (32 / TEAM), 2 * (int64_t)limit * kWarps, p.per_part[i]);
+      const int round = kBackFlight * (32 / TEAM), all = (p.H[i] + round - 1) / round;
+      const int64_t warps = (int64_t)limit * kWarps;
+      int64_t least = INT64_MAX;
+      for (int n = 1; n <= all; ++n) {
+        const int per = (all + n - 1) / n * round, parts = (p.H[i] + per - 1) / per;
+        const int64_t cost = (a.rows * parts + warps - 1) / warps * (per + 6);
+        if (cost < least) {
+          least = cost;
+          p.parts[i] = parts;
+          p.per_part[i] = per;
+        }
+      }
       if (a.rows * p.parts[i] > most) most = a.rows * p.parts[i];
     }
     const int64_t want = (most + kWarps - 1) / kWarps;
