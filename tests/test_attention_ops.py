@@ -434,6 +434,11 @@ LINEAR = [  # dtype, B, T, H, dk, dv, ragged lengths or None, with a state
     # several segments of the time axis, cut sequences in some of them, an empty last segment
     (BF, 1, 2100, 2, 128, 128, None, True), (BF, 2, 1300, 3, 128, 96, [1300, 700], True),
     (BF, 2, 1000, 2, 72, 128, [100, 993], False), (BF, 40, 64, 5, 128, 128, None, False),
+    # less than a chunk of 64 tokens, alone and in a batch
+    (BF, 1, 2, 3, 128, 64, None, True), (BF, 7, 33, 2, 40, 128, [0, 1, 33, 32, 17, 5, 31], True),
+    (BF, 1, 17, 1, 8, 16, None, False),
+    # fp32 in as many segments as chunks, and in fewer
+    (F32, 1, 257, 1, 128, 128, None, True), (F32, 2, 640, 2, 32, 64, [640, 65], True),
     (F32, 1, 100, 2, 128, 128, None, True), (F32, 2, 1100, 1, 64, 64, [1100, 513], True),
     (F32, 1, 70, 3, 100, 4, None, False), (F32, 3, 5, 1, 4, 12, [0, 5, 3], True),
 ]

@@ -22,6 +22,7 @@
 // segments: one kernel forms every segment's own state, a scan turns them
 // into the states that the segments begin with, and the main kernel runs all
 // segments at once.
+#include <algorithm>
 #include <type_traits>
 
 #include "linear.cuh"
@@ -37,29 +38,30 @@ constexpr int kMaxDim = 128;
 
 // Rows i0 .. i0 + kC of a [.., H, d] tensor, columns col0 .. col0 + W, to fp32
 // shared memory [kC][pitch]; rows behind `stop` and columns behind d are zero.
-template <typename T, int W>
+template <int W>
 __device__ __forceinline__ void load_rows(const LinearParams &p, float *dst, int pitch, const void *src, int64_t stride,
                                           int h, int d, int col0, int64_t b, int64_t n, int64_t i0, int64_t stop) {
-  constexpr int E = Elt<T>::EPV, V = W / E;
+  constexpr int E = Elt<float>::EPV, V = W / E;
   for (int k = threadIdx.x; k < kC * V; k += kThreads) {
     const int r = k / V, c = (k % V) * E;
     uint4 v = make_uint4(0, 0, 0, 0);
     if (i0 + r < stop && col0 + c < d)
-      v = ld_stream((const T *)src + walk_row(p, b, n, i0 + r) * stride + (int64_t)h * d + col0 + c);
+      v = ld_stream((const float *)src + walk_row(p, b, n, i0 + r) * stride + (int64_t)h * d + col0 + c);
     float x[E];
-    Elt<T>::unpack(v, x);
+    Elt<float>::unpack(v, x);
 #pragma unroll
     for (int e = 0; e < E; ++e) dst[r * pitch + c + e] = x[e];
   }
 }
 
 // ---------------------------------------------------------------------------
-// The general kernel: fp32 arithmetic on the CUDA cores, any width up to 128
-// (padded with zeros to DA).  A CTA of 16 x 16 threads owns kNS columns of c
+// The general kernel: fp32 on the CUDA cores (and, for no tokens at all, the
+// states of either type), any width up to 128 (padded with zeros to DA).  A CTA of 16 x 16 threads owns kNS columns of c
 // and of the state for one segment; each thread forms 4 x 4 elements of every
-// product.  STATES: only the segment's own state is formed.
+// product.  STATES: only the segment's own state is formed.  The CUDA cores
+// bind: about 24 us for a chunk of 64 tokens, 128 x 128, of one slice.
 // ---------------------------------------------------------------------------
-template <typename T, int DA, bool STATES>
+template <int DA, bool STATES>
 __global__ void __launch_bounds__(kThreads) linear_general_kernel(const LinearParams p) {
   constexpr int kPitch = DA + 4, MB = DA / 64;
   extern __shared__ float4 smem4[];
@@ -98,9 +100,9 @@ __global__ void __launch_bounds__(kThreads) linear_general_kernel(const LinearPa
     const int len = (int)min((int64_t)kC, stop - i0);
     const int lead = (i0 == 0) ? p.first_pow : 1;      // the first row's weight of the state: lambda^lead
     __syncthreads();                                   // the last chunk's tiles are read
-    if (!STATES) load_rows<T, DA>(p, sa, kPitch, p.a, p.a_stride, h, p.da, 0, b, n, i0, stop);
-    load_rows<T, DA>(p, sb, kPitch, p.b, p.b_stride, h, p.da, 0, b, n, i0, stop);
-    load_rows<T, kNS>(p, sc, kPadS, p.c, p.c_stride, h, p.dc, col0, b, n, i0, stop);
+    if (!STATES) load_rows<DA>(p, sa, kPitch, p.a, p.a_stride, h, p.da, 0, b, n, i0, stop);
+    load_rows<DA>(p, sb, kPitch, p.b, p.b_stride, h, p.da, 0, b, n, i0, stop);
+    load_rows<kNS>(p, sc, kPadS, p.c, p.c_stride, h, p.dc, col0, b, n, i0, stop);
     if (!STATES) {
 #pragma unroll
       for (int m = 0; m < MB * 4; ++m) {
@@ -183,14 +185,9 @@ __global__ void __launch_bounds__(kThreads) linear_general_kernel(const LinearPa
         for (int i = 0; i < 4; ++i) {
           const int r = ty * 4 + i;
           if (r >= len) continue;
-          T *y = (T *)p.out + (walk_row(p, b, n, i0 + r) * p.H + h) * p.dc + col;
-          float z[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) z[j] = o[i][j] * p.alpha;
-          if constexpr (std::is_same<T, float>::value)
-            *reinterpret_cast<float4 *>(y) = make_float4(z[0], z[1], z[2], z[3]);
-          else
-            *reinterpret_cast<uint2 *>(y) = make_uint2(Elt<T>::pack_word(z[0], z[1]), Elt<T>::pack_word(z[2], z[3]));
+          float *y = (float *)p.out + (walk_row(p, b, n, i0 + r) * p.H + h) * p.dc + col;
+          *reinterpret_cast<float4 *>(y) =
+              make_float4(o[i][0] * p.alpha, o[i][1] * p.alpha, o[i][2] * p.alpha, o[i][3] * p.alpha);
         }
       }
     }
@@ -239,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) linear_general_kernel(const LinearPa
     const int64_t from = max(stop, begin);
     const int w = min(kNS, p.dc - col0);
     for (int64_t k = threadIdx.x; k < (end - from) * w; k += kThreads)
-      ((T *)p.out)[((b * p.T + from + k / w) * p.H + h) * p.dc + col0 + k % w] = T(0.f);
+      ((float *)p.out)[((b * p.T + from + k / w) * p.H + h) * p.dc + col0 + k % w] = 0.f;
   }
 }
 
@@ -387,23 +384,36 @@ bool linear_supported(int64_t da, int64_t dc, int dtype) {
   return da >= e && dc >= e && da <= kMaxDim && dc <= kMaxDim && da % e == 0 && dc % e == 0;
 }
 
-// Segments of the general kernel: enough CTAs for two per SM, but none
-// shorter than 256 tokens (a segment's state costs as much traffic as about
-// 128 tokens).  The same with da and dc exchanged, so that two calls can share
+// Segments of the general kernel: the split with the least cost in waves of CTAs
+// (two per SM up to 64 wide, else one: 137 KB of shared memory) times their
+// chunks, in units of a chunk of the main kernel.  A chunk of the states' kernel
+// is worth a third of one, a CTA's start 0.3 (with its state 0.6), the scan and
+// the launches 0.4, a state written, scanned and read 0.0015.  Measured, fp32, 128 x 128,
+// uncut against cut: 4 heads x 512 tokens 195 against 43 us, 4 heads x 4096
+// 1506 against 145, 64 heads x 2048 767 against 1097 (three segments: uncut
+// it stays).  The same with da and dc exchanged, so that two calls can share
 // the segments' states.
 static Split linear_split(int64_t B, int64_t T, int H, int da, int dc, int dtype) {
   if (B * H < 1 || T < 1) return {kChunk, 1, 1};
-  if (linear_tc_supported(T, dtype)) {
-    if (B * H > 65535) return {(T + kC - 1) / kC * kC, 1, 1};    // the scan's grid; and the SMs are full
-    return linear_tc_split(B * H, T);
+  const int64_t chunks = (T + kC - 1) / kC;
+  if (B * H > 65535) return {chunks * kC, 1, 1};                 // the scan's grid; and the SMs are full
+  if (linear_tc_supported(T, dtype)) return linear_tc_split(B * H, T);
+  const int wide = da > dc ? da : dc;
+  const int64_t have = B * H * general_slices(wide), slots = sm_count() * (int64_t)(wide <= 64 ? 2 : 1);
+  auto waves = [&](int64_t ctas) { return (double)((ctas + slots - 1) / slots); };
+  int64_t per = chunks;
+  double least = waves(have) * ((double)chunks + 0.3);
+  for (int n = 2; n <= 128 && n <= chunks; ++n) {
+    const int64_t len = (chunks + n - 1) / n, segments = (chunks + len - 1) / len;
+    const double cost = waves(have * segments) * ((double)len + 0.3) +
+                        0.35 * waves(have * (segments - 1)) * ((double)len + 1.) + 0.4 +
+                        0.0015 * (double)(B * H * segments);
+    if (cost < least) {
+      least = cost;
+      per = len;
+    }
   }
-  const int64_t have = B * H * general_slices(da > dc ? da : dc), want = 2 * (int64_t)sm_count();
-  int64_t n = (want + have - 1) / have;
-  const int64_t most = T / 256;
-  if (n > most) n = most;
-  if (n < 1) n = 1;
-  const int64_t len = ((T + n - 1) / n + kC - 1) / kC * kC;
-  return {len, (int)((T + len - 1) / len), 1};
+  return {per * kC, (int)((chunks + per - 1) / per), 1};
 }
 
 int64_t linear_workspace_floats(int64_t B, int64_t T, int H, int da, int dc, int dtype) {
@@ -427,24 +437,20 @@ cudaError_t launch_linear(const LinearArgs &a) {
   p.last = a.last; p.last_scale = a.last_scale; p.last_pow = a.last_pow;
   p.states = a.workspace;
   p.states_t = a.states_t;
-  p.wait_limit = wait_limit_cycles();
+  p.wait_limit = std::min(wait_limit_cycles(), 1ll << 48);    // times a CTA's length, within 63 bits
   const int64_t BH = a.B * a.H;
   const bool tc = linear_tc_supported(a.T, a.dtype);
   // The states' kernel (states = true) or the main one.
   auto chunks = [&](const LinearParams &p, bool states) -> cudaError_t {
     if (tc) return launch_linear_tc(p, BH, states, a.stream);
     const int64_t ctas = BH * p.nseg * p.slices;
-    auto go = [&](auto elt, auto da) -> cudaError_t {
-      using T = decltype(elt);
+    auto go = [&](auto da) -> cudaError_t {
       constexpr int DA = decltype(da)::value;
       const size_t smem = (size_t)(2 * kC * (DA + 4) + 2 * kC * kPadS + DA * kPadS + kC + 4) * sizeof(float);
-      return states ? launch_big(linear_general_kernel<T, DA, true>, ctas, smem, a.stream, p)
-                    : launch_big(linear_general_kernel<T, DA, false>, ctas, smem, a.stream, p);
+      return states ? launch_big(linear_general_kernel<DA, true>, ctas, smem, a.stream, p)
+                    : launch_big(linear_general_kernel<DA, false>, ctas, smem, a.stream, p);
     };
-    auto with_da = [&](auto elt) -> cudaError_t {
-      return a.da <= 64 ? go(elt, std::integral_constant<int, 64>{}) : go(elt, std::integral_constant<int, 128>{});
-    };
-    return a.dtype == ATTNRES_BF16 ? with_da(__nv_bfloat16{}) : with_da(float{});
+    return a.da <= 64 ? go(std::integral_constant<int, 64>{}) : go(std::integral_constant<int, 128>{});
   };
   if (p.nseg > 1 && !a.states_ready) {
     // The pieces' own states (the last segment's only where the final state
@@ -469,10 +475,12 @@ cudaError_t launch_linear_step(const LinearStepArgs &a) {
   p.q_stride = a.q_stride; p.k_stride = a.k_stride; p.v_stride = a.v_stride;
   p.H = a.H; p.dk = a.dk; p.dv = a.dv;
   p.log_decay = a.log_decay; p.scale = a.scale; p.state = a.state; p.state_out = a.state_out; p.out = a.out;
-  // Whole rows of the state while the (sequence, head) pairs fill the SMs,
-  // else slices of 32 columns (128 bytes of a row).
+  // Slices of 32 columns (128 bytes of a row) while there is no (sequence, head)
+  // pair for every SM, else whole rows.  Measured, 128 x 128, sliced against
+  // whole: 64 pairs 4.2 against 6.5 us, 152 5.7 against 7.1, 176 7.7 against 7.5, 256
+  // 8.5 against 7.8, 2048 47.8 against 38.9.
   p.cols = a.dv;
-  if (a.B * a.H < 2 * (int64_t)sm_count() && a.dv > 32) p.cols = 32;
+  if (a.B * a.H <= sm_count() && a.dv > 32) p.cols = 32;
   const dim3 grid((unsigned)(a.B * a.H), (unsigned)((a.dv + p.cols - 1) / p.cols));
   return a.dtype == ATTNRES_BF16
              ? launch_dependent(linear_step_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, a.stream, p)

@@ -286,10 +286,10 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
   const uint32_t tmem = ctl[0];
 
   // Wait for the phase; false once any wait of the CTA has run out.  The limit
-  // counts from the CTA's start: its whole work takes a few milliseconds, and
-  // a short loop at every wait keeps the roles' code within the instruction
-  // cache.
-  const long long deadline = clock64() + p.wait_limit;
+  // counts from the CTA's start and once more for every 8192 chunks that it
+  // goes through (some 10 ms of work), so that no length runs into it; a short
+  // loop at every wait keeps the roles' code small.
+  const long long deadline = clock64() + p.wait_limit * (1 + chunks / 8192);
   auto wait = [&](int which, uint32_t parity) -> bool {
     const uint32_t at = bar(which);
     while (!mbar_try(at, parity & 1)) {
@@ -658,10 +658,6 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
 }
 
 }  // namespace
-
-// From one full chunk on; shorter prompts stay on the general kernel, whose
-// fp32 products also spare a handful of tokens the rounding of P.
-bool linear_tc_supported(int64_t T, int dtype) { return dtype == ATTNRES_BF16 && T >= kChunk; }
 
 // The split with the least cost in waves of CTAs, one per SM, times their
 // chunks.  A CTA's fixed cost is worth about eight chunks of the main kernel's,
