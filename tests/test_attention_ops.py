@@ -271,7 +271,8 @@ PAGED = [  # dtype, Hq, Hk, d, page, lengths
     (BF, 8, 1, 64, 32, [5000, 3, 0, 31]), (BF, 16, 1, 128, 64, [1000, 17]), (BF, 32, 2, 64, 16, [129, 128, 127]),
     (BF, 6, 2, 96, 16, [100, 211]), (BF, 4, 4, 80, 8, [90, 1]), (BF, 8, 2, 256, 64, [70, 400]),
     (BF, 3, 1, 8, 1, [33]), (BF, 9, 1, 128, 128, [300]), (BF, 10, 2, 128, 7, [100, 50]), (BF, 2, 2, 192, 3, [65]),
-    (F32, 4, 4, 64, 16, [70, 0, 300]), (F32, 7, 1, 128, 32, [513]), (F32, 32, 2, 256, 64, [65, 130]),
+    (F32, 4, 4, 64, 16, [70, 0, 300]), (F32, 6, 3, 128, 16, [65, 0, 333]), (F32, 3, 3, 256, 8, [77]),
+    (F32, 4, 2, 48, 16, [300, 1]), (F32, 7, 1, 128, 32, [513]), (F32, 32, 2, 256, 64, [65, 130]),
     (F32, 2, 1, 4, 1, [9]), (F32, 12, 4, 100, 5, [64, 1]), (BF, 4, 2, 128, 64, [20000]),
 ]
 

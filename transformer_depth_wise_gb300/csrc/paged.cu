@@ -21,8 +21,9 @@
 // The cache's bytes bind.  Measured on GB300, bf16, heads of 128: 256 sequences
 // of up to 8192 tokens, 56 query over 8 key heads, 4.3 GB in 681 us (6.3 TB/s)
 // and 9 us for the join; 65537 and 131071 tokens, 32 over 4, 403 MB in 65 us
-// (6.2 TB/s) and 7 us.  fp32: 6.0 TB/s with one query head per key head, 4.1
-// with four, 1.05 with 16, where the CUDA cores bind.
+// (6.2 TB/s) and 7 us.  fp32, 16 sequences of 2048 to 4096 tokens, 8 key heads of
+// 128: 71 us with one or two query heads each, 113 with four, 195 with eight,
+// where the CUDA cores bind.
 #include <type_traits>
 
 #include "common.cuh"
@@ -193,8 +194,18 @@ __device__ __forceinline__ void store_piece(const PagedParams &p, const Walk &w,
 // ---------------------------------------------------------------------------
 constexpr int kWarpsF = 8;
 
+// Whether the next tokens' rows are on their way while the present ones are
+// added, and the instances held to 128 registers so that two CTAs run on an SM
+// (0: as the compiler chooses).  Measured (16 sequences of 2048 to 4096 tokens, 8
+// key heads; reading ahead against two CTAs without): 64 wide with four
+// query heads a warp 104 against 58 us, 128 wide with two 119 against 73.  128
+// wide with four does not fit twice (ahead 124, without 113), 256 wide neither (two
+// query heads: ahead 124, without 128; one: ahead 142, two CTAs 166).
+constexpr bool reads_ahead(int nv, int gq) { return nv * gq <= 4 || nv == 8; }
+constexpr int resident(int nv, int gq) { return nv < 8 && nv * gq == 8 ? 2 : 0; }
+
 template <int NV, int GQ>
-__global__ void __launch_bounds__(kWarpsF * 32) paged_f32_kernel(const PagedParams p) {
+__global__ void __launch_bounds__(kWarpsF * 32, resident(NV, GQ)) paged_f32_kernel(const PagedParams p) {
   constexpr int E = 4, N = NV * E;
   extern __shared__ float sm[];                     // [warps][GQ][d] outputs, then [warps][GQ] m, then l
   __shared__ int64_t red[kWarpsF];
@@ -237,9 +248,7 @@ __global__ void __launch_bounds__(kWarpsF * 32) paged_f32_kernel(const PagedPara
       }
     }
     if (working) {
-      // The next tokens' rows are on their way while the present ones are
-      // added, where the registers allow it.
-      constexpr bool kAhead = GQ * N <= 32;
+      constexpr bool kAhead = reads_ahead(NV, GQ);
       uint4 nk[NV], nv[NV];
       bool next_live;
       auto read = [&](int j) {
