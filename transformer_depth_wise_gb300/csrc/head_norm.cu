@@ -492,6 +492,9 @@ cudaError_t launch_head_norm(const HeadNormArgs &a) {
     constexpr bool INTER = decltype(inter)::value;
     // A row per work item, cut into parts of no less than one round of a
     // warp's teams where the rows alone would not give every SM eight warps.
+    // Measured, 32 + 8 heads of 128, cut against whole rows: 1 to 64 rows 4.0 against 7.4
+    // to 9.0 us, 512 5.8 against 8.3; for 16 warps per SM 512 rows take 6.9, 2048 12.3
+    // against 10.2.
     const int heads = a.Hq + (cache ? 2 : 1) * a.Hk;
     p.parts = row_parts(a.rows, heads, 32 / TEAM, 8 * (int64_t)sms, p.per_part);
     const int64_t ctas = (a.rows * p.parts + kWarps - 1) / kWarps, most = (int64_t)sms * 8;

@@ -20,20 +20,6 @@ __device__ __forceinline__ uint64_t sw128_desc(uint32_t addr, uint32_t sbo) {
   return d;
 }
 
-// Shared-memory matrix descriptor of an MN-major operand (the product's K
-// axis runs over rows of the tile), 128-byte swizzle: 64 elements of the M or
-// N axis side by side, `lbo` bytes from one such block to the next, groups of
-// eight K rows `sbo` bytes apart.
-__device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  uint64_t d = 0;
-  d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-  d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-  d |= (uint64_t)1 << 46;
-  d |= (uint64_t)2 << 61;
-  return d;
-}
-
 // Bits of the instruction descriptor for MN-major A and B.
 constexpr uint32_t kIdescMnA = 1u << 15, kIdescMnB = 1u << 16;
 
