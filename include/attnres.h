@@ -387,10 +387,12 @@ int64_t attnres_paged_attention_workspace_bytes(int Hq, int Hk, int64_t d, int d
  *               within 0 .. T; out behind them is zero
  *   state       device fp32 [B,H,dk,dv] S_0, or NULL (zeros)
  *   out         device [B,T,H,dv], contiguous; overlaps none of the inputs
+ *               (VALUE for one that starts where an input does)
  *   state_out   device fp32 [B,H,dk,dv] S after each sequence's last token, or NULL; may be state
  *   workspace   device, attnres_linear_attention_workspace_bytes() bytes (may
- *               be 0, then NULL is allowed); contents on entry do not matter
- * bf16 inputs of 64 tokens and more: products on the tensor cores with fp32
+ *               be 0, then NULL is allowed); contents on entry do not matter.
+ *               Two calls that may overlap need one each
+ * bf16 inputs: products on the tensor cores with fp32
  * accumulators and an fp32 state; the masked products and the state are
  * rounded to bf16 where they enter the product that forms out.  Prompts are
  * worked on in chunks of 64 tokens: a NaN or infinity in a token's q, k or v
@@ -430,7 +432,7 @@ int64_t attnres_linear_attention_backward_workspace_bytes(int64_t B, int64_t T, 
  * scale S'^T q.
  *   q, k        device [B,H,dk], v device [B,H,dv], sequences `stride` elements apart
  *   state       device fp32 [B,H,dk,dv];  state_out the same, may be state
- *   out         device [B,H,dv], contiguous
+ *   out         device [B,H,dv], contiguous; overlaps none of the inputs
  */
 int attnres_linear_attention_step(const void *q, const void *k, const void *v, int64_t B, int H, int64_t dk,
                                   int64_t dv, int dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride,

@@ -95,6 +95,7 @@ def test_linear_refusals():
     assert linear(g=FAKE + 2) == ALIGN and linear(n=FAKE + 1) == ALIGN
     assert linear(qs=64) == SHAPE and linear(qs=0) == SHAPE                # overlapping rows
     assert linear(B=0, q=None, g=None, out=None, ws=None) == OK and linear(T=0, q=None, out=None) == OK
+    assert linear(out=FAKE) == VALUE                                       # out is q, k and v
     size = _lib.lib().attnres_linear_attention_workspace_bytes
     assert size(1, 100, 2, 64, 64, 1) >= 0 and size(1, 100, 0, 64, 64, 1) == SHAPE and size(1, 1, 1, 4, 8, 1) == ALIGN
 
@@ -108,6 +109,7 @@ def test_linear_backward_refusals():
     assert linear_bwd(go=None) == NULL and linear_bwd(dq=None) == NULL and linear_bwd(gos=12) == ALIGN
     assert linear_bwd(gs=FAKE, ds=FAKE) == VALUE and linear_bwd(scale=0.0) == VALUE and linear_bwd(B=0) == OK
     assert linear_bwd(T=0) == OK
+    assert linear_bwd(dq=FAKE) == VALUE                                    # the gradients are the inputs
 
 
 def test_step_refusals():

@@ -556,6 +556,40 @@ def test_linear_views_of_one_projection_and_split_prompts(gpu):
 
 
 @gpu_only
+@pytest.mark.parametrize("dtype,T", [(BF, 33), (BF, 100), (BF, 1500), (F32, 33), (F32, 300)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_linear_whatever_is_behind_the_sequences(gpu, dtype, T, bad):
+    q, k, v, ld, scale = linear_inputs(gpu, dtype, 3, T, 2, 64, 72, T)
+    go = rand(wk.generator(5, gpu), 3, T, 2, 72, dtype=dtype)
+    state = rand(wk.generator(4, gpu), 3, 2, 64, 72, dtype=F32)
+    n = torch.tensor([0, 17, T - 1], device=gpu).int()
+
+    def run():
+        out, last = api.linear_attention(q, k, v, ld, scale, state=state, lengths=n)
+        return (out, last, *api.linear_attention_backward(q, k, v, ld, scale, go, state=state, lengths=n, grad_state=state))
+    want = run()
+    for b in range(3):
+        for t in (q, k, v, go):
+            t[b, int(n[b]):] = bad
+    for x, y in zip(run(), want):
+        assert bool(torch.isfinite(x).all()) and torch.equal(x, y)
+
+
+@gpu_only
+def test_linear_outputs_are_not_inputs(gpu):
+    from transformer_depth_wise_gb300 import _lib
+    q, k, v, ld, scale = linear_inputs(gpu, BF, 1, 70, 2, 64, 64, 1)
+    state = torch.zeros(1, 2, 64, 64, device=gpu)
+    for x in (q, k, v):
+        with pytest.raises(_lib.AttnResError):
+            api.linear_attention(q, k, v, ld, scale, out=x)
+        one = x[:, 0].contiguous()
+        with pytest.raises(_lib.AttnResError):
+            api.linear_attention_step(one, one, one, ld, scale, state, out=one)
+    assert bool((state == 0).all())
+
+
+@gpu_only
 def test_linear_empty(gpu):
     q, k, v, ld, scale = linear_inputs(gpu, BF, 2, 0, 3, 64, 64, 1)
     state = rand(wk.generator(4, gpu), 2, 3, 64, 64, dtype=F32)

@@ -906,7 +906,8 @@ def linear_attention(q, k, v, log_decay, scale: float, state=None, lengths=None,
 
     q, k [B,T,H,dk], v [B,T,H,dv] (contiguous, or views of one projection's output); log_decay fp32 [H] (<= 0);
     state fp32 [B,H,dk,dv], the state to start from; lengths int32 [B], tokens per sequence of a padded batch
-    (out is zero behind them).  state_out may be state.
+    (out is zero behind them).  state_out may be state; out overlaps none of the inputs.  workspace: uint8 CUDA
+    scratch (allocated when None); calls that may overlap need one each.
     """
     B, T, H, dk, dv, qs, ks, vs = _linear_args(q, k, v, log_decay, lengths, state)
     dev, code = q.device, _CODES[q.dtype]

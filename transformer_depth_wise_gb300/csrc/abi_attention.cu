@@ -58,6 +58,11 @@ int check_pages(int64_t num_pages, int page_size, int max_pages) {
              ? ATTNRES_ERR_SHAPE : ATTNRES_OK;
 }
 
+// An output that is one of the inputs: CTAs would read what others have written.
+bool among(const void *out, const void *x, const void *y, const void *z, const void *w = nullptr) {
+  return out && (out == x || out == y || out == z || out == w);
+}
+
 int check_linear(int64_t B, int64_t T, int H, int64_t dk, int64_t dv, int dtype, int64_t &rows) {
   int st = check_batch(B, T, dtype, rows);
   if (st) return st;
@@ -241,6 +246,7 @@ int attnres_linear_attention(const void *q, const void *k, const void *v, int64_
   if (misaligned(q) || misaligned(k) || misaligned(v) || misaligned(out) || misaligned(log_decay, 4) ||
       misaligned(lengths, 4) || misaligned(state) || misaligned(state_out) || misaligned(workspace))
     return ATTNRES_ERR_ALIGNMENT;
+  if (rows && among(out, q, k, v)) return ATTNRES_ERR_VALUE;
   LinearArgs a{};
   a.a = q; a.b = k; a.c = v; a.a_stride = q_stride; a.b_stride = k_stride; a.c_stride = v_stride;
   a.out = out; a.B = B; a.T = T; a.H = H; a.da = (int)dk; a.dc = (int)dv; a.dtype = dtype;
@@ -274,6 +280,8 @@ int attnres_linear_attention_backward(const void *q, const void *k, const void *
       misaligned(dk_out) || misaligned(dv_out) || misaligned(log_decay, 4) || misaligned(lengths, 4) || misaligned(state) ||
       misaligned(grad_state) || misaligned(grad_initial) || misaligned(workspace))
     return ATTNRES_ERR_ALIGNMENT;
+  if (rows && (among(dq, q, k, v, grad_out) || among(dk_out, q, k, v, grad_out) || among(dv_out, q, k, v, grad_out)))
+    return ATTNRES_ERR_VALUE;
   LinearArgs a{};
   a.B = B; a.T = T; a.H = H; a.dtype = dtype; a.log_decay = log_decay; a.lengths = lengths; a.alpha = scale;
   a.workspace = static_cast<float *>(workspace); a.stream = static_cast<cudaStream_t>(stream);
@@ -315,6 +323,7 @@ int attnres_linear_attention_step(const void *q, const void *k, const void *v, i
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || misaligned(log_decay, 4) || !aligned16(state) ||
       !aligned16(state_out) || !aligned16(out))
     return ATTNRES_ERR_ALIGNMENT;
+  if (among(out, q, k, v)) return ATTNRES_ERR_VALUE;
   LinearStepArgs a{};
   a.q = q; a.k = k; a.v = v; a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
   a.B = B; a.H = H; a.dk = (int)dk; a.dv = (int)dv; a.dtype = dtype; a.log_decay = log_decay; a.scale = scale;
