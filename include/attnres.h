@@ -394,7 +394,9 @@ int64_t attnres_paged_attention_workspace_bytes(int Hq, int Hk, int64_t d, int d
  *               Two calls that may overlap need one each
  * bf16 inputs: products on the tensor cores with fp32
  * accumulators and an fp32 state; the masked products and the state are
- * rounded to bf16 where they enter the product that forms out.  Prompts are
+ * rounded to bf16 where they enter the product that forms out.  fp32 inputs:
+ * products there too, of operands split into two parts, exact to 2^-19 at worst
+ * and 2^-22 on average, and an fp32 state.  Prompts are
  * worked on in chunks of 64 tokens: a NaN or infinity in a token's q, k or v
  * may also show in out of the tokens before it in its chunk.
  */

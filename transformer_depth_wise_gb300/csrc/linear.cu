@@ -33,203 +33,293 @@ namespace {
 constexpr int kC = kChunk;             // tokens per chunk
 constexpr int kThreads = 256;
 constexpr int kNS = 64;                // columns of c a CTA takes
-constexpr int kPadS = kNS + 4;         // row pitch of [.][kNS] tiles (floats)
 constexpr int kMaxDim = 128;
 
-// Rows i0 .. i0 + kC of a [.., H, d] tensor, columns col0 .. col0 + W, to fp32
-// shared memory [kC][pitch]; rows behind `stop` and columns behind d are zero.
+// ---------------------------------------------------------------------------
+// The fp32 kernel (and, for no tokens at all, the states of either type), any
+// width up to 128, padded with zeros to DA.  A CTA owns kNS columns of c and of
+// the state for one segment.
+//
+// Products.  On the tensor cores: an fp32 operand is split into a tf32 (its upper
+// bits) and the nearest tf32 of what is left, both by integer instructions (by
+// conversions, which take several issue slots each, the kernel takes 15 % longer).
+// x y = xh yh + (xh yl + xl yh); what is missing is below 2^-19 of |x y|, 2^-22
+// on average.  The tensor cores' accumulators cut off instead of rounding
+// (measured: 1 plus 3/4 of the last place stays 1), so the large and the small
+// products have accumulators of their own, none of which runs for longer than a
+// chunk: the state itself is kept in fp32 registers and takes one rounded
+// addition per chunk.
+//
+// Roles.  Four warps hold 16 rows of P = a b^T each, which stay in registers as
+// the left operand of P c (the pairs of columns that a lane holds name the rows
+// of c that it reads), and the four others the state, 32 x 32 elements at a
+// time; only the state goes through shared memory, for a S.  In the
+// states' kernel all eight warps hold the state.  The next chunk's rows are
+// copied while one is worked on.  What binds is the rate at which instructions
+// are issued: splitting, loads of operands, and 1100 products a scheduler.
+//
+// Measured on GB300, 128 x 128: 11.3 us for a chunk and slice (on the CUDA
+// cores 24), 2.8 in the states' kernel; 64 heads x 4096 tokens 733 us (1532).
+// Twelve and sixteen warps (a S by four of its own, the state in eight) take
+// 708 and 738 there, and 4 to 9 % longer with 64 x 64.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void copy_or_zero(float *dst, const float *src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(live ? 16 : 0)
+               : "memory");
+}
+
+// Rows i0 .. i0 + kC of a [.., H, d] tensor, columns col0 .. col0 + W, on their
+// way to shared memory [kC][pitch]; rows behind `stop` and columns behind d are zero.
 template <int W>
-__device__ __forceinline__ void load_rows(const LinearParams &p, float *dst, int pitch, const void *src, int64_t stride,
+__device__ __forceinline__ void copy_rows(const LinearParams &p, float *dst, int pitch, const void *src, int64_t stride,
                                           int h, int d, int col0, int64_t b, int64_t n, int64_t i0, int64_t stop) {
-  constexpr int E = Elt<float>::EPV, V = W / E;
-  for (int k = threadIdx.x; k < kC * V; k += kThreads) {
-    const int r = k / V, c = (k % V) * E;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (i0 + r < stop && col0 + c < d)
-      v = ld_stream((const float *)src + walk_row(p, b, n, i0 + r) * stride + (int64_t)h * d + col0 + c);
-    float x[E];
-    Elt<float>::unpack(v, x);
+  constexpr int V = W / 4, kRows = kThreads / V;        // rows per turn
+  static_assert(kC % kRows == 0, "whole turns");
+  const int r0 = threadIdx.x / V, c = threadIdx.x % V * 4;
+  const int rows = col0 + c < d ? (int)min((int64_t)kC, stop - i0) : 0;
+  const float *at = (const float *)src + walk_row(p, b, n, i0 + r0) * stride + (int64_t)h * d + col0 + c;
+  const int64_t step = (p.reverse ? -kRows : kRows) * stride;
+  float *to = dst + r0 * pitch + c;
 #pragma unroll
-    for (int e = 0; e < E; ++e) dst[r * pitch + c + e] = x[e];
+  for (int r = 0; r < kC; r += kRows, at += step, to += kRows * pitch) {
+    const bool live = r + r0 < rows;
+    copy_or_zero(to, live ? at : (const float *)src, live);
   }
 }
 
-// ---------------------------------------------------------------------------
-// The general kernel: fp32 on the CUDA cores (and, for no tokens at all, the
-// states of either type), any width up to 128 (padded with zeros to DA).  A CTA of 16 x 16 threads owns kNS columns of c
-// and of the state for one segment; each thread forms 4 x 4 elements of every
-// product.  STATES: only the segment's own state is formed.  The CUDA cores
-// bind: about 24 us for a chunk of 64 tokens, 128 x 128, of one slice.
-// ---------------------------------------------------------------------------
+struct Tf32 {
+  uint32_t hi, lo;
+};
+__device__ __forceinline__ Tf32 split(float x) {
+  constexpr uint32_t kUpper = 0xffffe000u;
+  const uint32_t hi = __float_as_uint(x) & kUpper;
+  return {hi, (__float_as_uint(x - __uint_as_float(hi)) + 0x1000u) & kUpper};
+}
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// A left operand's 16 x 8 elements: rows g, g + 8 at the lane's first k (x0, x1) and its second (x2, x3).
+struct Left {
+  uint32_t hi[4], lo[4];
+  __device__ __forceinline__ Left(float x0, float x1, float x2, float x3) {
+    const float x[4] = {x0, x1, x2, x3};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const Tf32 s = split(x[i]);
+      hi[i] = s.hi;
+      lo[i] = s.lo;
+    }
+  }
+};
+// One 16 x 8 tile of sums: the large products and the small ones.
+struct Tile {
+  float big[4] = {}, small[4] = {};
+  __device__ __forceinline__ void add(const Left &a, float y0, float y1) {
+    const Tf32 b0 = split(y0), b1 = split(y1);
+    mma_tf32(big, a.hi, b0.hi, b1.hi);
+    mma_tf32(small, a.hi, b0.lo, b1.lo);
+    mma_tf32(small, a.lo, b0.hi, b1.hi);
+  }
+  __device__ __forceinline__ float at(int i) const { return big[i] + small[i]; }
+};
+
+// Floats of shared memory: two stages of b, a [kC][DA + 8] and c [kC][kPitchC], the state, the decay's powers.
+constexpr int kPitchC = kNS + 8, kPitchS = kNS + 4;
+template <int DA, bool STATES> struct Room {
+  static constexpr int kPitch = DA + 8;
+  static constexpr int kB = 0, kA = kC * kPitch, kCc = (STATES ? 1 : 2) * kC * kPitch;
+  static constexpr int kStage = kCc + kC * kPitchC;
+  static constexpr int kS = 2 * kStage, kPow = kS + (STATES ? 0 : DA * kPitchS);
+  static constexpr int kFloats = kPow + kC + 4;
+};
+
 template <int DA, bool STATES>
 __global__ void __launch_bounds__(kThreads) linear_general_kernel(const LinearParams p) {
-  constexpr int kPitch = DA + 4, MB = DA / 64;
+  using R = Room<DA, STATES>;
+  constexpr int kPitch = R::kPitch;
+  constexpr int kHolders = STATES ? 8 : 4;             // warps with parts of the state
+  constexpr int kParts = DA / 32 * (kNS / 32);         // of 32 x 32
+  constexpr int kOwn = (kParts + kHolders - 1) / kHolders;
   extern __shared__ float4 smem4[];
-  float *sa = reinterpret_cast<float *>(smem4);        // [kC][kPitch]
-  float *sb = sa + kC * kPitch;                        // [kC][kPitch]
-  float *sc = sb + kC * kPitch;                        // [kC][kPadS]
-  float *sp = sc + kC * kPadS;                         // [kC][kPadS]
-  float *ss = sp + kC * kPadS;                         // [DA][kPadS]
-  float *pw = ss + DA * kPadS;                         // [kC + 1]
+  float *sm = reinterpret_cast<float *>(smem4), *ss = sm + R::kS, *pw = sm + R::kPow;
   grid_dependency_wait();
   const int seg = blockIdx.x % p.nseg, slice = blockIdx.x / p.nseg % p.slices;
   const int64_t bh = blockIdx.x / (p.nseg * p.slices), b = bh / p.H;
   const int h = (int)(bh % p.H), col0 = slice * kNS;
   const int64_t n = seq_length(p, b);
   const int64_t begin = seg * p.seg_len, end = min(p.T, begin + p.seg_len), stop = min(n, end);
-  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, g8 = lane / 4, t = lane % 4;
   const float g = p.log_decay[h];
   if (threadIdx.x <= kC) pw[threadIdx.x] = decay_pow(g, threadIdx.x);
 
-  float s[MB * 4][4];                                  // state rows mb * 64 + ty * 4 + i, columns tx * 4 + j
+  // The lane's elements of part i of the state: tile (m, j) holds rows g8, g8 + 8 of 16 and columns 2 t, 2 t + 1 of 8.
+  const int holder = STATES ? warp : warp - 4;
+  auto part_of = [&](int i) { return holder * kOwn + i; };
+  auto row_of = [&](int i, int m, int e) { return part_of(i) / 2 * 32 + m * 16 + g8 + (e / 2) * 8; };
+  auto col_of = [&](int i, int j, int e) { return part_of(i) % 2 * 32 + j * 8 + 2 * t + e % 2; };
+  const bool holds = holder >= 0 && holder * kOwn < kParts;
+  float s[kOwn][2][4][4];
   float *states = p.states + ((bh * p.nstates + seg * p.step) * p.da) * p.dc;
 #pragma unroll
-  for (int m = 0; m < MB * 4; ++m) {
-    const int row = (m / 4) * 64 + ty * 4 + m % 4;
+  for (int i = 0; i < kOwn; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int col = col0 + tx * 4 + j;
-      s[m][j] = 0.f;
-      if (!STATES && row < p.da && col < p.dc) {
-        if (p.nseg > 1) s[m][j] = p.states_t ? states[(int64_t)col * p.da + row] : states[(int64_t)row * p.dc + col];
-        else if (p.first) s[m][j] = first_at(p, bh, row, col);
-      }
-    }
-  }
-  for (int64_t i0 = begin; i0 < stop; i0 += kC) {
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[i][m][j][e] = 0.f;
+          if (!holds) continue;
+          const int row = row_of(i, m, e), col = col0 + col_of(i, j, e);
+          if (!STATES && row < p.da && col < p.dc) {
+            if (p.nseg > 1)
+              s[i][m][j][e] = p.states_t ? states[(int64_t)col * p.da + row] : states[(int64_t)row * p.dc + col];
+            else if (p.first) s[i][m][j][e] = first_at(p, bh, row, col);
+          }
+        }
+  auto copy = [&](int64_t i0, int stage) {
+    float *to = sm + stage * R::kStage;
+    copy_rows<DA>(p, to + R::kB, kPitch, p.b, p.b_stride, h, p.da, 0, b, n, i0, stop);
+    if (!STATES) copy_rows<DA>(p, to + R::kA, kPitch, p.a, p.a_stride, h, p.da, 0, b, n, i0, stop);
+    copy_rows<kNS>(p, to + R::kCc, kPitchC, p.c, p.c_stride, h, p.dc, col0, b, n, i0, stop);
+    cp_async_commit();
+  };
+  if (begin < stop) copy(begin, 0);
+  int stage = 0;
+  for (int64_t i0 = begin; i0 < stop; i0 += kC, stage ^= 1) {
     const int len = (int)min((int64_t)kC, stop - i0);
     const int lead = (i0 == 0) ? p.first_pow : 1;      // the first row's weight of the state: lambda^lead
-    __syncthreads();                                   // the last chunk's tiles are read
-    if (!STATES) load_rows<DA>(p, sa, kPitch, p.a, p.a_stride, h, p.da, 0, b, n, i0, stop);
-    load_rows<DA>(p, sb, kPitch, p.b, p.b_stride, h, p.da, 0, b, n, i0, stop);
-    load_rows<kNS>(p, sc, kPadS, p.c, p.c_stride, h, p.dc, col0, b, n, i0, stop);
-    if (!STATES) {
+    const float *sb = sm + stage * R::kStage + R::kB, *sa = sm + stage * R::kStage + R::kA;
+    const float *sc = sm + stage * R::kStage + R::kCc;
+    if (!STATES && holds) {
 #pragma unroll
-      for (int m = 0; m < MB * 4; ++m) {
-        const int row = (m / 4) * 64 + ty * 4 + m % 4;
-        *reinterpret_cast<float4 *>(ss + row * kPadS + tx * 4) = make_float4(s[m][0], s[m][1], s[m][2], s[m][3]);
-      }
-    }
-    __syncthreads();
-    if (!STATES) {
-      // P: rows ty + 16 i, columns tx + 16 j
-      float acc[4][4] = {};
-#pragma unroll 4
-      for (int k = 0; k < DA; k += 4) {
-        float4 x[4], y[4];
+      for (int i = 0; i < kOwn; ++i)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(sa + (ty + 16 * i) * kPitch + k);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4 *>(sb + (tx + 16 * j) * kPitch + k);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            acc[i][j] = fmaf(x[i].x, y[j].x, fmaf(x[i].y, y[j].y, fmaf(x[i].z, y[j].z, fmaf(x[i].w, y[j].w, acc[i][j]))));
-      }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+            for (int e = 0; e < 4; e += 2)
+              *reinterpret_cast<float2 *>(ss + row_of(i, m, e) * kPitchS + col_of(i, j, e)) =
+                  make_float2(s[i][m][j][e], s[i][m][j][e + 1]);
+    }
+    cp_async_wait<0>();
+    __syncthreads();                                   // the chunk and the state are there; the other stage is read
+    if (i0 + kC < stop) copy(i0 + kC, stage ^ 1);
+    if (!STATES && warp < 4) {
+      const int m0 = warp * 16;
+      const float *xa = sa + (m0 + g8) * kPitch + 2 * t;
+      // P, up to the diagonal: rows m0 + g8 (+ 8), columns 8 j + 2 t (+ 1); k in the order 2 t, 2 t + 1
+      float pr[kC / 8][4];
+      {
+        Tile acc[kC / 8];
+#pragma unroll 2
+        for (int k = 0; k < DA; k += 8) {
+          const float2 x = *reinterpret_cast<const float2 *>(xa + k);
+          const float2 y = *reinterpret_cast<const float2 *>(xa + 8 * kPitch + k);
+          const Left a(x.x, y.x, x.y, y.y);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int r = ty + 16 * i, c = tx + 16 * j;
-          sp[r * kPadS + c] = r >= c ? acc[i][j] * pw[r - c] : 0.f;
-        }
-      __syncthreads();
-      // rows ty * 4 + i, columns tx * 4 + j: the state's part, weighted by row, then the chunk's own
-      float o[4][4] = {};
-#pragma unroll 4
-      for (int k = 0; k < DA; k += 4) {
-        float4 x[4], y[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(sa + (ty * 4 + i) * kPitch + k);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4 *>(ss + (k + j) * kPadS + tx * 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            o[i][0] = fmaf(xs[j], y[j].x, o[i][0]);
-            o[i][1] = fmaf(xs[j], y[j].y, o[i][1]);
-            o[i][2] = fmaf(xs[j], y[j].z, o[i][2]);
-            o[i][3] = fmaf(xs[j], y[j].w, o[i][3]);
+          for (int j = 0; j < kC / 8; ++j) {
+            if (j > 2 * warp + 1) continue;
+            const float2 z = *reinterpret_cast<const float2 *>(sb + (8 * j + g8) * kPitch + k + 2 * t);
+            acc[j].add(a, z.x, z.y);
           }
         }
+#pragma unroll
+        for (int j = 0; j < kC / 8; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int back = m0 + g8 + (e / 2) * 8 - (8 * j + 2 * t + e % 2);
+            pr[j][e] = back >= 0 ? acc[j].at(e) * pw[back] : 0.f;
+          }
+      }
+      // the state's part, weighted by row, then the chunk's own
+      float o[kNS / 8][4];
+      {
+        Tile acc[kNS / 8];
+#pragma unroll 2
+        for (int k = 0; k < DA; k += 8) {
+          const float2 x = *reinterpret_cast<const float2 *>(xa + k);
+          const float2 y = *reinterpret_cast<const float2 *>(xa + 8 * kPitch + k);
+          const Left a(x.x, y.x, x.y, y.y);
+          const float *z = ss + (k + 2 * t) * kPitchS + g8;
+#pragma unroll
+          for (int j = 0; j < kNS / 8; ++j) acc[j].add(a, z[8 * j], z[kPitchS + 8 * j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kNS / 8; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[j][e] = acc[j].at(e) * pw[m0 + g8 + (e / 2) * 8 + lead];
+      }
+      Tile acc[kNS / 8];
+#pragma unroll
+      for (int i = 0; i < kC / 8; ++i) {
+        if (i > 2 * warp + 1) continue;
+        const Left a(pr[i][0], pr[i][2], pr[i][1], pr[i][3]);
+        const float *z = sc + (8 * i + 2 * t) * kPitchC + g8;
+#pragma unroll
+        for (int j = 0; j < kNS / 8; ++j) acc[j].add(a, z[8 * j], z[kPitchC + 8 * j]);
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int e = 0; e < 4; e += 2) {
+        const int r = m0 + g8 + (e / 2) * 8;
+        if (r >= len) continue;
+        float *y = (float *)p.out + (walk_row(p, b, n, i0 + r) * p.H + h) * p.dc + col0 + 2 * t;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) o[i][j] *= pw[ty * 4 + i + lead];
-#pragma unroll 4
-      for (int k = 0; k < kC; k += 4) {
-        float4 x[4], y[4];
+        for (int j = 0; j < kNS / 8; ++j)
+          if (col0 + 8 * j + 2 * t < p.dc)
+            *reinterpret_cast<float2 *>(y + 8 * j) =
+                make_float2((o[j][e] + acc[j].at(e)) * p.alpha, (o[j][e + 1] + acc[j].at(e + 1)) * p.alpha);
+      }
+    } else if (holds) {
+      // S = lambda^len S + sum_j lambda^{len-1-j} b_j c_j^T
+      const float keep = decay_pow(g, len - 1 + lead);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(sp + (ty * 4 + i) * kPadS + k);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4 *>(sc + (k + j) * kPadS + tx * 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float xs[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+      for (int i = 0; i < kOwn; ++i) {
+        Tile acc[2][4];
+        const float *xb = sb + part_of(i) / 2 * 32 + g8, *xc = sc + part_of(i) % 2 * 32 + g8;
+#pragma unroll 2
+        for (int k = 0; k < kC; k += 8) {
+          const int k0 = k + t, k1 = k0 + 4;
+          const float w0 = k0 < len ? pw[len - 1 - k0] : 0.f, w1 = k1 < len ? pw[len - 1 - k1] : 0.f;
+          const float *x = xb + k0 * kPitch, *y = x + 4 * kPitch;
+          const Left a0(x[0], x[8], y[0], y[8]), a1(x[16], x[24], y[16], y[24]);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            o[i][0] = fmaf(xs[j], y[j].x, o[i][0]);
-            o[i][1] = fmaf(xs[j], y[j].y, o[i][1]);
-            o[i][2] = fmaf(xs[j], y[j].z, o[i][2]);
-            o[i][3] = fmaf(xs[j], y[j].w, o[i][3]);
+            const float z0 = xc[k0 * kPitchC + 8 * j] * w0, z1 = xc[k1 * kPitchC + 8 * j] * w1;
+            acc[0][j].add(a0, z0, z1);
+            acc[1][j].add(a1, z0, z1);
           }
         }
-      }
-      const int col = col0 + tx * 4;
-      if (col < p.dc) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = ty * 4 + i;
-          if (r >= len) continue;
-          float *y = (float *)p.out + (walk_row(p, b, n, i0 + r) * p.H + h) * p.dc + col;
-          *reinterpret_cast<float4 *>(y) =
-              make_float4(o[i][0] * p.alpha, o[i][1] * p.alpha, o[i][2] * p.alpha, o[i][3] * p.alpha);
-        }
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[i][m][j][e] = fmaf(s[i][m][j][e], keep, acc[m][j].at(e));
       }
     }
-    // S = lambda^len S + sum_j lambda^{len-1-j} b_j c_j^T
-    const float keep = decay_pow(g, len - 1 + lead);
-#pragma unroll
-    for (int m = 0; m < MB * 4; ++m)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) s[m][j] *= keep;
-#pragma unroll 4
-    for (int k = 0; k < len; ++k) {
-      float4 y = *reinterpret_cast<const float4 *>(sc + k * kPadS + tx * 4);
-      const float wk = pw[len - 1 - k];
-      y.x *= wk; y.y *= wk; y.z *= wk; y.w *= wk;
-#pragma unroll
-      for (int mb = 0; mb < MB; ++mb) {
-        const float4 x = *reinterpret_cast<const float4 *>(sb + k * kPitch + mb * 64 + ty * 4);
-        const float xs[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[mb * 4 + i][0] = fmaf(xs[i], y.x, s[mb * 4 + i][0]);
-          s[mb * 4 + i][1] = fmaf(xs[i], y.y, s[mb * 4 + i][1]);
-          s[mb * 4 + i][2] = fmaf(xs[i], y.z, s[mb * 4 + i][2]);
-          s[mb * 4 + i][3] = fmaf(xs[i], y.w, s[mb * 4 + i][3]);
-        }
-      }
-    }
+    if (!STATES) __syncthreads();                      // the state is read
   }
   const bool write_last = !STATES && p.nseg == 1 && p.last;
-  if (STATES || write_last) {
+  if ((STATES || write_last) && holds) {
     float *dst = STATES ? states : p.last + bh * p.da * p.dc;
     // no token at all: the state passes through unchanged
     const float f = STATES ? 1.f : p.last_scale * (n > 0 ? decay_pow(g, p.last_pow) : 1.f);
 #pragma unroll
-    for (int m = 0; m < MB * 4; ++m) {
-      const int row = (m / 4) * 64 + ty * 4 + m % 4;
+    for (int i = 0; i < kOwn; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int col = col0 + tx * 4 + j;
-        if (row < p.da && col < p.dc) dst[(int64_t)row * p.dc + col] = s[m][j] * f;
-      }
-    }
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int row = row_of(i, m, e), col = col0 + col_of(i, j, e);
+            if (row < p.da && col < p.dc) dst[(int64_t)row * p.dc + col] = s[i][m][j][e] * f;
+          }
   }
   if (!STATES) {
     // rows behind the sequence are zero
@@ -384,30 +474,31 @@ bool linear_supported(int64_t da, int64_t dc, int dtype) {
   return da >= e && dc >= e && da <= kMaxDim && dc <= kMaxDim && da % e == 0 && dc % e == 0;
 }
 
-// Segments of the general kernel: the split with the least cost in waves of CTAs
-// (two per SM up to 64 wide, else one: 137 KB of shared memory) times their
-// chunks, in units of a chunk of the main kernel.  A chunk of the states' kernel
-// is worth a third of one, a CTA's start 0.3 (with its state 0.6), the scan and
-// the launches 0.4, a state written, scanned and read 0.0015.  Measured, fp32, 128 x 128,
-// uncut against cut: 4 heads x 512 tokens 195 against 43 us, 4 heads x 4096
-// 1506 against 145, 64 heads x 2048 767 against 1097 (three segments: uncut
-// it stays).  The same with da and dc exchanged, so that two calls can share
-// the segments' states.
+// Segments of the fp32 kernel: the split with the least cost in waves of CTAs, one
+// per SM, times their chunks, in units of a chunk of the main kernel (11.3 us).  A
+// chunk of the states' kernel is worth a quarter of one, a CTA's start 0.8 (the
+// states' kernel's 0.33), the scan 0.35, a state written, scanned and read 0.001.
+// The same with da and dc exchanged, so that two calls can share the segments'
+// states.
+// Measured, uncut against cut: 4 heads of 128 x 128, 100 tokens 34 against 26 us,
+// 512 102 against 27, 4096 728 against 71; 64 heads of 64 x 64, 1024 tokens 110
+// against 77; 40 heads of 128 x 128, 4096 tokens 730 against 549, 1024 tokens 191
+// against 194 (uncut); 64 heads, 4096 tokens 732 against 917 (uncut).
 static Split linear_split(int64_t B, int64_t T, int H, int da, int dc, int dtype) {
   if (B * H < 1 || T < 1) return {kChunk, 1, 1};
   const int64_t chunks = (T + kC - 1) / kC;
   if (B * H > 65535) return {chunks * kC, 1, 1};                 // the scan's grid; and the SMs are full
   if (linear_tc_supported(T, dtype)) return linear_tc_split(B * H, T);
   const int wide = da > dc ? da : dc;
-  const int64_t have = B * H * general_slices(wide), slots = sm_count() * (int64_t)(wide <= 64 ? 2 : 1);
+  const int64_t have = B * H * general_slices(wide), slots = sm_count();
   auto waves = [&](int64_t ctas) { return (double)((ctas + slots - 1) / slots); };
   int64_t per = chunks;
-  double least = waves(have) * ((double)chunks + 0.3);
+  double least = waves(have) * ((double)chunks + 0.8);
   for (int n = 2; n <= 128 && n <= chunks; ++n) {
     const int64_t len = (chunks + n - 1) / n, segments = (chunks + len - 1) / len;
-    const double cost = waves(have * segments) * ((double)len + 0.3) +
-                        0.35 * waves(have * (segments - 1)) * ((double)len + 1.) + 0.4 +
-                        0.0015 * (double)(B * H * segments);
+    const double cost = waves(have * segments) * ((double)len + 0.8) +
+                        0.25 * waves(have * (segments - 1)) * ((double)len + 1.3) + 0.35 +
+                        0.001 * (double)(B * H * segments);
     if (cost < least) {
       least = cost;
       per = len;
@@ -446,7 +537,7 @@ cudaError_t launch_linear(const LinearArgs &a) {
     const int64_t ctas = BH * p.nseg * p.slices;
     auto go = [&](auto da) -> cudaError_t {
       constexpr int DA = decltype(da)::value;
-      const size_t smem = (size_t)(2 * kC * (DA + 4) + 2 * kC * kPadS + DA * kPadS + kC + 4) * sizeof(float);
+      const size_t smem = (size_t)(states ? Room<DA, true>::kFloats : Room<DA, false>::kFloats) * sizeof(float);
       return states ? launch_big(linear_general_kernel<DA, true>, ctas, smem, a.stream, p)
                     : launch_big(linear_general_kernel<DA, false>, ctas, smem, a.stream, p);
     };

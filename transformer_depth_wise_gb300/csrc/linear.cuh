@@ -12,7 +12,7 @@ struct LinearParams {
   int64_t a_stride, b_stride, c_stride;
   void *out;
   int64_t T, seg_len;
-  int H, da, dc, nseg, slices;         // slices: CTAs over the columns of c (general kernel)
+  int H, da, dc, nseg, slices;         // slices: CTAs over the columns of c (fp32 kernel)
   const float *log_decay;
   const int32_t *lengths;
   float alpha;
@@ -62,10 +62,9 @@ struct Split {
 };
 // The tensor-core form (bf16): its split, and the launches of the states'
 // kernel and of the main one.
-// Every bf16 prompt of one token or more takes it: where the other kernel
-// (CUDA cores, 64-token chunks whatever they hold) was tried on bf16, 4 heads of
-// 128 x 128 took 19.4 us against 9.9 for one token, 26.2 against 9.6 for 63 and
-// 25.8 against 9.5 for 64.
+// Every bf16 prompt of one token or more takes it: on the CUDA cores, in
+// 64-token chunks whatever they hold, 4 heads of 128 x 128 took 19.4 us against
+// 9.9 for one token and 26.2 against 9.6 for 63.
 inline bool linear_tc_supported(int64_t T, int dtype) { return dtype == ATTNRES_BF16 && T > 0; }
 Split linear_tc_split(int64_t BH, int64_t T);
 cudaError_t launch_linear_tc(const LinearParams &p, int64_t BH, bool states, cudaStream_t stream);
