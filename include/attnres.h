@@ -365,7 +365,9 @@ int64_t attnres_head_norm_rotate_backward_workspace_rows(void);
  *               (other streams, graphs launched side by side) need one each.
  * An empty sequence gives zeros and lse = -infinity.  Cache contents behind
  * lengths[b] are never used, whatever they hold; tokens on a page whose
- * number is outside [0, num_pages) are left out.
+ * number is outside [0, num_pages) are left out.  A NaN in a query or in a
+ * key that is attended over gives NaN in out and lse, one in a value in its
+ * element of out; an infinite value gives an infinity or NaN.
  */
 int attnres_paged_attention(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
                             int64_t num_pages, int page_size, const int32_t *page_table, int max_pages,

@@ -649,8 +649,11 @@ __global__ void __launch_bounds__(kWarpsM * 32, MmaShape<D>::kCtas) paged_mma_ke
       float M = -INFINITY, L = 0.f;
 #pragma unroll
       for (int k = 0; k < kWarpsM; ++k) M = fmaxf(M, smax[k][g]);
+      // A warp without a finite score adds nothing, or the NaN that its sum holds: the maximum alone, which
+      // passes NaN scores over, does not tell.
 #pragma unroll
-      for (int k = 0; k < kWarpsM; ++k) L += smax[k][g] == -INFINITY ? 0.f : ssum[k][g] * exp2_fast(smax[k][g] - M);
+      for (int k = 0; k < kWarpsM; ++k)
+        L += ssum[k][g] * (smax[k][g] == -INFINITY ? 0.f : exp2_fast(smax[k][g] - M));
       float4 x = *reinterpret_cast<const float4 *>(so + g * S::kOutPitch + e);
       const float r = L == 0.f ? 0.f : 1.f / L;
       x.x *= r; x.y *= r; x.z *= r; x.w *= r;
