@@ -231,6 +231,7 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
     __syncthreads();
     bh = rest % (BH / p.H) * p.H + *found;
     seg = (int)(rest / (BH / p.H));
+    fence_async_smem();                               // tensor-map copies will write over what was kept here
     __syncthreads();
   }
   const int64_t b = bh / p.H;
