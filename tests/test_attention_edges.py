@@ -4,8 +4,9 @@ import math
 import pytest
 import torch
 
-from test_attention_ops import BF, F32, paged_inputs
+from test_attention_ops import BF, E, F32, U, linear_grad_ref, linear_inputs, paged_inputs, rand, within
 from transformer_depth_wise_gb300 import api
+from transformer_depth_wise_gb300 import workloads as wk
 
 gpu_only = pytest.mark.gpu
 
@@ -56,3 +57,50 @@ def test_paged_nan_values(gpu, dtype, length, at):
     hit = torch.zeros(8, 128, dtype=torch.bool, device=gpu)
     hit[:4, 9] = True
     assert torch.equal(lse, wlse) and bool(out[0][hit].isnan().all()) and torch.equal(out[0][~hit], want[0][~hit])
+
+
+# --------------------------------------------------------------------------
+# linear attention: gradients by value under any decay, and with any scale
+# --------------------------------------------------------------------------
+def check_gradients(gpu, dtype, q, k, v, ld, scale, go, state, n, gs):
+    got = api.linear_attention_backward(q, k, v, ld, scale, go, state=state, lengths=n, grad_state=gs)
+    want = linear_grad_ref(q, k, v, ld, scale, go, state, n, gs)
+    absn = lambda t: None if t is None else t.abs()  # noqa: E731
+    mags = linear_grad_ref(q.abs(), k.abs(), v.abs(), ld, abs(scale), go.abs(), absn(state), n, absn(gs))
+    # as in test_linear_backward: fp32 roundings in units of the absolute sums (a decay's exponent among them, at most
+    # 100 E before it underflows), for bf16 the masked products and the state rounded once on their way into a product;
+    # 1e-36: products of decays below fp32's smallest normal number are zero
+    f = (max(q.shape[-1], v.shape[-1]) + 64 + 100 + 2 * q.shape[1] / 64) * E
+    for i, (a, b, m) in enumerate(zip(got, want, mags)):
+        rounding = 2.0 ** -8 if dtype is BF and i < 3 else 0.0
+        within(a, b, (U[dtype] if i < 3 else E) * b.abs() + (f + rounding) * m + 1e-36, "qkvs"[i])
+    return got
+
+
+@gpu_only
+@pytest.mark.parametrize("dtype,T,lengths", [(BF, 150, None), (BF, 1500, [1500, 700]), (F32, 200, None),
+                                             (F32, 700, [0, 700])])
+@pytest.mark.parametrize("scale", [1e-30, -0.3, 7.0])
+def test_linear_gradients_with_any_scale(gpu, dtype, T, lengths, scale):
+    # what reaches the state's gradient through the outputs is scale grad_out, some 1e6 for the smallest one
+    q, k, v, ld, _ = linear_inputs(gpu, dtype, 2, T, 2, 64, 64, T)
+    g = wk.generator(9, gpu)
+    n = None if lengths is None else torch.tensor(lengths, device=gpu).int()
+    small = abs(scale) < 1e-20
+    state, gs = (rand(g, 2, 2, 64, 64, dtype=F32, scale=x) for x in (1.0, 1e10 if small else 1.0))
+    go = rand(g, 2, T, 2, 64, dtype=dtype, scale=1e36 if small else 1.0)
+    check_gradients(gpu, dtype, q, k, v, ld, scale, go, state, n, gs)
+
+
+@gpu_only
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T", [0, 100, 1500])
+def test_linear_gradient_of_an_unused_state_is_the_state_gradient(gpu, dtype, T):
+    q, k, v, ld, _ = linear_inputs(gpu, dtype, 3, T, 2, 64, 64, T)
+    g = wk.generator(9, gpu)
+    state, gs = (rand(g, 3, 2, 64, 64, dtype=F32) for _ in range(2))
+    n = torch.tensor([0, T, 0], device=gpu).int()
+    _, last = api.linear_attention(q, k, v, ld, 0.3, state=state, lengths=n)
+    assert torch.equal(last[::2], state[::2])
+    ds = api.linear_attention_backward(q, k, v, ld, 0.3, v.clone(), state=state, lengths=n, grad_state=gs)[3]
+    assert torch.equal(ds[::2], gs[::2])

@@ -19,7 +19,7 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 int vec_elems(int dtype) { return dtype == ATTNRES_BF16 ? 8 : 4; }
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? ATTNRES_OK : ATTNRES_ERR_CUDA; }
 bool good_eps(float eps) { return std::isfinite(eps) && eps >= 0.f; }
-// Finite, and 1 / scale is too (the backward divides by it).
+// Finite and no zero, and 1 / scale is finite too.
 bool good_scale(float s) { return std::isfinite(s) && s != 0.f && std::isfinite(1.f / s); }
 
 // A row stride: a multiple of the vector width; `apart`: no less than the row's width.
@@ -251,7 +251,7 @@ int attnres_linear_attention(const void *q, const void *k, const void *v, int64_
   a.a = q; a.b = k; a.c = v; a.a_stride = q_stride; a.b_stride = k_stride; a.c_stride = v_stride;
   a.out = out; a.B = B; a.T = T; a.H = H; a.da = (int)dk; a.dc = (int)dv; a.dtype = dtype;
   a.log_decay = log_decay; a.lengths = lengths; a.alpha = scale;
-  a.first = state; a.first_pow = 1; a.first_scale = 1.f; a.last = state_out; a.last_scale = 1.f;
+  a.carry = scale; a.gain = 1.f; a.first = state; a.first_pow = 1; a.last = state_out;
   a.workspace = static_cast<float *>(workspace); a.stream = static_cast<cudaStream_t>(stream);
   return cuda_status(launch_linear(a));
 }
@@ -288,16 +288,17 @@ int attnres_linear_attention_backward(const void *q, const void *k, const void *
   // dq = scale F(grad_out, v, k; S_0^T)
   a.a = grad_out; a.a_stride = grad_out_stride; a.b = v; a.b_stride = v_stride; a.c = k; a.c_stride = k_stride;
   a.da = (int)dv; a.dc = (int)dk; a.out = dq;
-  a.first = state; a.first_t = true; a.first_pow = 1; a.first_scale = 1.f;
+  a.carry = scale; a.gain = 1.f; a.first = state; a.first_t = true; a.first_pow = 1;
   cudaError_t e = cudaSuccess;
   if (rows) e = launch_linear(a);
   // dv, backwards: scale F(k, q, grad_out) + grad_state's part, which scale
-  // does not multiply; its last state is the initial one's gradient
+  // does not multiply: the state is the gradient itself, scale enters with
+  // the tokens.  Its last state is the initial one's gradient
   a.reverse = true;
-  a.first = grad_state; a.first_t = false; a.first_pow = 0; a.first_scale = 1.f / scale;
+  a.carry = 1.f; a.gain = scale; a.first = grad_state; a.first_t = false; a.first_pow = 0;
   a.a = k; a.a_stride = k_stride; a.b = q; a.b_stride = q_stride; a.c = grad_out; a.c_stride = grad_out_stride;
   a.da = (int)dk; a.dc = (int)dv; a.out = dv_out;
-  a.last = grad_initial; a.last_scale = scale; a.last_pow = 1;
+  a.last = grad_initial; a.last_pow = 1;
   if (e == cudaSuccess) e = launch_linear(a);
   // dk, backwards: scale F(v, grad_out, q) + grad_state^T's part; its states are dv's, transposed
   a.a = v; a.a_stride = v_stride; a.b = grad_out; a.b_stride = grad_out_stride; a.c = q; a.c_stride = q_stride;

@@ -238,7 +238,9 @@ int paged_ctas(int64_t d, int dtype);
 int64_t paged_workspace_bytes(int G, int64_t d, int dtype);
 cudaError_t launch_paged(const PagedArgs &a);
 
-struct LinearArgs {              // out_i = alpha (sum_{j <= i} e^{g (i - j)} (a_i . b_j) c_j + e^{g (i + first_pow)} a_i . first)
+// out_i = alpha sum_{j <= i} e^{g (i - j)} (a_i . b_j) c_j + carry e^{g (i + first_pow)} a_i . first, through the state
+// S_i = e^g S_{i-1} + gain b_i c_i^T (S_{-1} = e^{g (first_pow - 1)} first), with alpha = carry gain
+struct LinearArgs {
   const void *a, *b, *c;         // [B, T, H, da], [.., da], [.., dc]
   int64_t a_stride, b_stride, c_stride;   // elements from one token row to the next
   void *out;                     // [B, T, H, dc], contiguous
@@ -246,15 +248,13 @@ struct LinearArgs {              // out_i = alpha (sum_{j <= i} e^{g (i - j)} (a
   int H, da, dc, dtype;
   const float *log_decay;        // [H]
   const int32_t *lengths;        // [B] or nullptr
-  float alpha;
+  float alpha, carry, gain;
   bool reverse;                  // i counts from a sequence's last token back
   const float *first;            // [B, H, da, dc] or nullptr; first_t: stored as [.., dc, da]
   bool first_t;
   int first_pow;
-  float first_scale;             // `first` is taken times this
-  float *last;                   // [B, H, da, dc] or nullptr: the state after the last token
-  float last_scale;              // times this ...
-  int last_pow;                  // ... and e^{g last_pow}
+  float *last;                   // [B, H, da, dc] or nullptr: the state after the last token ...
+  int last_pow;                  // ... times e^{g last_pow}
   float *workspace;
   bool states_ready;             // the workspace holds the segments' first states already ...
   bool states_t;                 // ... as [.., dc, da]: another call's with a and c's roles exchanged

@@ -7,9 +7,12 @@
 // lambda^{t+1} S_0^T q_t), one form F(a, b, c; first) = sum_{j <= i}
 // lambda^{i-j} (a_i . b_j) c_j + lambda^{i+1} a_i . first that the gradients
 // share: dq = scale F(do, v, k; S_0^T), and with time running backwards
-// dk = scale F'(v, do, q; dS^T), dv = scale F'(k, q, do; dS), where dS, the
-// gradient of the final state, meets the last token undecayed, and
-// dS_0 = lambda times the state that the last of them ends with.
+// dk = scale F'(v, do, q) and dv = scale F'(k, q, do) with dS^T and dS as
+// their first states, where dS, the gradient of the final state, meets the
+// last token undecayed and unscaled: there scale goes into the state with
+// the tokens instead of multiplying what is read out of it, and dS_0 is
+// lambda times the state that the last of them ends with, dS itself where
+// there is no token.
 //
 // Chunks.  Within a chunk of kC tokens the masked, decayed product matrix
 // P_ij = lambda^{i-j} a_i . b_j is formed once and applied to c; what came
@@ -204,7 +207,7 @@ __global__ void __launch_bounds__(kThreads) linear_general_kernel(const LinearPa
 #pragma unroll
             for (int e = 0; e < 4; e += 2)
               *reinterpret_cast<float2 *>(ss + row_of(i, m, e) * kPitchS + col_of(i, j, e)) =
-                  make_float2(s[i][m][j][e], s[i][m][j][e + 1]);
+                  make_float2(s[i][m][j][e] * p.carry, s[i][m][j][e + 1] * p.carry);
     }
     cp_async_wait<0>();
     __syncthreads();                                   // the chunk and the state are there; the other stage is read
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(kThreads) linear_general_kernel(const LinearPa
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int back = m0 + g8 + (e / 2) * 8 - (8 * j + 2 * t + e % 2);
-            pr[j][e] = back >= 0 ? acc[j].at(e) * pw[back] : 0.f;
+            pr[j][e] = back >= 0 ? acc[j].at(e) * (p.alpha * pw[back]) : 0.f;
           }
       }
       // the state's part, weighted by row, then the chunk's own
@@ -271,11 +274,10 @@ __global__ void __launch_bounds__(kThreads) linear_general_kernel(const LinearPa
 #pragma unroll
         for (int j = 0; j < kNS / 8; ++j)
           if (col0 + 8 * j + 2 * t < p.dc)
-            *reinterpret_cast<float2 *>(y + 8 * j) =
-                make_float2((o[j][e] + acc[j].at(e)) * p.alpha, (o[j][e + 1] + acc[j].at(e + 1)) * p.alpha);
+            *reinterpret_cast<float2 *>(y + 8 * j) = make_float2(o[j][e] + acc[j].at(e), o[j][e + 1] + acc[j].at(e + 1));
       }
     } else if (holds) {
-      // S = lambda^len S + sum_j lambda^{len-1-j} b_j c_j^T
+      // S = lambda^len S + gain sum_j lambda^{len-1-j} b_j c_j^T
       const float keep = decay_pow(g, len - 1 + lead);
 #pragma unroll
       for (int i = 0; i < kOwn; ++i) {
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(kThreads) linear_general_kernel(const LinearPa
 #pragma unroll 2
         for (int k = 0; k < kC; k += 8) {
           const int k0 = k + t, k1 = k0 + 4;
-          const float w0 = k0 < len ? pw[len - 1 - k0] : 0.f, w1 = k1 < len ? pw[len - 1 - k1] : 0.f;
+          const float w0 = k0 < len ? p.gain * pw[len - 1 - k0] : 0.f, w1 = k1 < len ? p.gain * pw[len - 1 - k1] : 0.f;
           const float *x = xb + k0 * kPitch, *y = x + 4 * kPitch;
           const Left a0(x[0], x[8], y[0], y[8]), a1(x[16], x[24], y[16], y[24]);
 #pragma unroll
@@ -308,7 +310,7 @@ __global__ void __launch_bounds__(kThreads) linear_general_kernel(const LinearPa
   if ((STATES || write_last) && holds) {
     float *dst = STATES ? states : p.last + bh * p.da * p.dc;
     // no token at all: the state passes through unchanged
-    const float f = STATES ? 1.f : p.last_scale * (n > 0 ? decay_pow(g, p.last_pow) : 1.f);
+    const float f = STATES || n == 0 ? 1.f : decay_pow(g, p.last_pow);
 #pragma unroll
     for (int i = 0; i < kOwn; ++i)
 #pragma unroll
@@ -364,7 +366,7 @@ __global__ void __launch_bounds__(kThreads) linear_scan_kernel(const LinearParam
     after = later;
   }
   if (p.last) {
-    const float f = p.last_scale * (n > 0 ? decay_pow(g, p.last_pow) : 1.f);
+    const float f = n > 0 ? decay_pow(g, p.last_pow) : 1.f;
     reinterpret_cast<float4 *>(p.last)[bh * per + e] = make_float4(cur.x * f, cur.y * f, cur.z * f, cur.w * f);
   }
 }
@@ -523,9 +525,10 @@ cudaError_t launch_linear(const LinearArgs &a) {
   p.seg_len = split.seg_len;
   p.nstates = split.nseg * split.nsub;
   p.step = split.nsub;
-  p.log_decay = a.log_decay; p.lengths = a.lengths; p.alpha = a.alpha; p.reverse = a.reverse;
-  p.first = a.first; p.first_t = a.first_t; p.first_pow = a.first_pow; p.first_scale = a.first_scale;
-  p.last = a.last; p.last_scale = a.last_scale; p.last_pow = a.last_pow;
+  p.log_decay = a.log_decay; p.lengths = a.lengths; p.reverse = a.reverse;
+  p.alpha = a.alpha; p.carry = a.carry; p.gain = a.gain;
+  p.first = a.first; p.first_t = a.first_t; p.first_pow = a.first_pow;
+  p.last = a.last; p.last_pow = a.last_pow;
   p.states = a.workspace;
   p.states_t = a.states_t;
   p.wait_limit = std::min(wait_limit_cycles(), 1ll << 48);    // times a CTA's length, within 63 bits

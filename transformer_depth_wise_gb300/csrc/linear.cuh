@@ -15,13 +15,11 @@ struct LinearParams {
   int H, da, dc, nseg, slices;         // slices: CTAs over the columns of c (fp32 kernel)
   const float *log_decay;
   const int32_t *lengths;
-  float alpha;
+  float alpha, carry, gain;            // of the masked products, of the state read out, of what enters it
   int reverse;
   const float *first;
   int first_t, first_pow;
-  float first_scale;
   float *last;
-  float last_scale;
   int last_pow;
   // The states that the segments begin with (nseg > 1): [B, H, nstates, da, dc],
   // segment s of this launch's begins with state s * step.  The states' kernel
@@ -40,10 +38,10 @@ __device__ __forceinline__ int64_t seq_length(const LinearParams &p, int64_t b) 
 // lambda^n; lambda^0 = 1 whatever g is.
 __device__ __forceinline__ float decay_pow(float g, int64_t n) { return n == 0 ? 1.f : expf(g * (float)n); }
 
-// The first state's element (m, n), scaled.
+// The first state's element (m, n).
 __device__ __forceinline__ float first_at(const LinearParams &p, int64_t bh, int m, int n) {
   const float *f = p.first + bh * p.da * p.dc;
-  return p.first_scale * (p.first_t ? f[(int64_t)n * p.da + m] : f[(int64_t)m * p.dc + n]);
+  return p.first_t ? f[(int64_t)n * p.da + m] : f[(int64_t)m * p.dc + n];
 }
 
 // Token i of the walk (reverse: from the last token back) as a row of the [B, T] axis.

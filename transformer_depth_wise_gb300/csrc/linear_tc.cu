@@ -4,8 +4,9 @@
 //
 // Per chunk of 64 tokens, with S the state before it (da x dc, fp32):
 //   P  = a b^T, masked and decayed                    (M 64,  N 64,  K da)
-//   O^T = S^T a^T (weighted by token) + c^T P^T       (M dc,  N 64,  K da; K 64)
-//   S^T <- lambda^n S^T + (w c)^T b, w_j = lambda^{n-1-j} (M dc, N da, K 64)
+//   O^T = carry S^T a^T (weighted by token) + c^T P^T (M dc,  N 64,  K da; K 64)
+//   S^T <- lambda^n S^T + (w c)^T b, w_j = gain lambda^{n-1-j} (M dc, N da, K 64)
+// (one of carry and gain is the call's scale, the other 1).
 // The outputs and the state are formed transposed, so that every product but
 // the small P has M = 128, the full rate, and S^T is a left operand as it
 // lies: a thread's row of it goes to tensor memory as bf16.  c^T, (w c)^T and
@@ -17,7 +18,7 @@
 // is split into parts.  Three of them (24 bits) make the product exact to
 // fp32's rounding, for a state that may be handed out; two (16 bits, an error
 // of 2^-17 at most) serve the main kernel's where the states' kernel has
-// formed the exact ones.  P and the copy of S that
+// formed the exact ones.  P and the copy of S (times carry) that
 // forms the outputs are rounded to bf16 once: each adds an error of the size
 // of the output's own rounding at most.
 //
@@ -428,12 +429,12 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
       const float *src = (own ? p.states + (bh * p.nstates + seg * p.step) * p.da * p.dc : p.first + bh * p.da * p.dc) +
                          (across ? (int64_t)row * p.da + col0 : (int64_t)col0 * p.dc + row);
       const int step = across ? 1 : p.dc;
-      const float f = own ? 1.f : p.first_scale;
       const int have = !STATES && (own || p.first) ? cols : 0;
 #pragma unroll
-      for (int j = 0; j < 32; ++j, src += 2 * step) st[j] = 2 * j < have ? pair(f * src[0], f * src[step]) : 0ull;
+      for (int j = 0; j < 32; ++j, src += 2 * step) st[j] = 2 * j < have ? pair(src[0], src[step]) : 0ull;
     }
     const float keep_full = decay_pow(g, kC);
+    const uint64_t carry = pair(p.carry, p.carry);
     for (int c = 0; c < chunks; ++c) {
       if (!STATES) {
         // its bf16 copy in tensor memory
@@ -444,7 +445,11 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
         for (int q = 0; q < 2; ++q) {
           uint32_t w[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) w[i] = narrow(st[q * 16 + i]);
+          for (int i = 0; i < 16; ++i) {
+            uint64_t x = st[q * 16 + i];
+            scale_pair(x, carry);
+            w[i] = narrow(x);
+          }
           tmem_st16(quad_addr + kColST + group * 32 + q * 16, w);
         }
         tmem_wait_st();
@@ -472,7 +477,7 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
     if (STATES || (p.nseg == 1 && p.last)) {
       float *out = STATES ? states : p.last + (bh * p.da + col0) * p.dc + row;
       // no token at all: the state passes through unchanged
-      const float f = STATES ? 1.f : p.last_scale * (n > 0 ? decay_pow(g, p.last_pow) : 1.f);
+      const float f = STATES || n == 0 ? 1.f : decay_pow(g, p.last_pow);
 #pragma unroll
       for (int j = 0; j < 32; ++j, out += 2 * p.dc) {
         if (2 * j < cols) {
@@ -497,7 +502,7 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
     const uint64_t minus = pair(-1.f, -1.f);
     float w[kPer];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) w[i] = pw[kC - 1 - place(row0 + i * kRows)];
+    for (int i = 0; i < kPer; ++i) w[i] = p.gain * pw[kC - 1 - place(row0 + i * kRows)];
     for (int use = team; use < chunks * kSteps; use += 2) {
       const int c = use / kSteps, s = c % L::kStages, len = length_of(c);
       wait(kFull + s, c / L::kStages);
@@ -505,7 +510,7 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
           const int li = place(row0 + i * kRows);
-          w[i] = li < len ? pw[len - 1 - li] : 0.f;
+          w[i] = li < len ? p.gain * pw[len - 1 - li] : 0.f;
         }
         if (unclean) {
           // the rows behind the sequence, of b and c (those of a only reach
@@ -591,7 +596,7 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
     // ---------------- outputs: weights, sum, transposition through shared memory, store ----------------
     share_registers<L::kRegsOut, L::kRegs>();
     const int tid = threadIdx.x - 5 * 128;
-    float w[16];                                        // alpha and the decay of the thread's 16 tokens
+    float w[16];                                        // the decay of the thread's 16 tokens
     int lead = -1;
     // the matrix stores: this lane names a token's row and 8 columns of c
     const uint32_t put = base + L::kOffOut + (8 * (lane / 16) + lane % 8) * kOutPitch + (quad * 4 + lane / 8 % 2) * 16;
@@ -605,7 +610,7 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
       if (now != lead) {
         lead = now;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = p.alpha * pw[place(8 * (i / 2) + 2 * (lane % 4) + i % 2) + lead];
+        for (int i = 0; i < 16; ++i) w[i] = pw[place(8 * (i / 2) + 2 * (lane % 4) + i % 2) + lead];
       }
       wait(kPV, c);
       __syncwarp();
