@@ -400,7 +400,8 @@ int64_t attnres_paged_attention_workspace_bytes(int Hq, int Hk, int64_t d, int d
  * products there too, of operands split into two parts, exact to 2^-19 at worst
  * and 2^-22 on average, and an fp32 state.  Prompts are
  * worked on in chunks of 64 tokens: a NaN or infinity in a token's q, k or v
- * may also show in out of the tokens before it in its chunk.
+ * may also show in out of the tokens before it in its chunk.  One in k or v
+ * stays in the state, as an infinity or NaN, however strong the decay.
  */
 int attnres_linear_attention(const void *q, const void *k, const void *v, int64_t B, int64_t T, int H, int64_t dk,
                              int64_t dv, int dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride,

@@ -60,6 +60,72 @@ def test_paged_nan_values(gpu, dtype, length, at):
 
 
 # --------------------------------------------------------------------------
+# linear attention: what is no number stays in the state
+# --------------------------------------------------------------------------
+LINEAR_NAN = [  # T, decay, token, n: in one segment and in several, with what the token leaves decayed to nothing
+    (150, -0.3, 20, 150), (3000, -0.5, 100, 3000), (3000, -20.0, 1000, 3000), (3000, -0.5, 1500, 2500),
+    (3000, -math.inf, 700, 3000), (3000, -0.01, 100, 3000), (20000, -1.0, 5000, 19999),
+]
+
+
+@gpu_only
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("T,g,t,n", LINEAR_NAN)
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_linear_keeps_what_is_no_number(gpu, dtype, bad, T, g, t, n, which):
+    q, k, v, _, scale = linear_inputs(gpu, dtype, 2, T, 2, 64, 72, T)
+    ld = torch.tensor([g, -0.05], device=gpu)
+    lens = torch.tensor([n, T], device=gpu).int()
+    want, wlast = api.linear_attention(q, k, v, ld, scale, lengths=lens)
+    (k if which == "k" else v)[0, t, 0, 5] = bad
+    out, last = api.linear_attention(q, k, v, ld, scale, lengths=lens)
+    # by the recurrence: a row of the state (k) or a column of it (v) is no number from token t on, so every output
+    # after it is none (k) or its element 5 (v); tokens before t in its chunk of 64 may be either
+    cols = slice(None) if which == "k" else slice(5, 6)
+    assert not bool(torch.isfinite(out[0, t:n, 0, cols]).any())
+    row = last[0, 0, 5] if which == "k" else last[0, 0, :, 5]
+    assert not bool(torch.isfinite(row).any())
+    # all else is as before
+    rest = torch.ones_like(out, dtype=torch.bool)
+    rest[0, t // 64 * 64:n, 0, cols] = False
+    assert torch.equal(out[rest], want[rest])
+    rest = torch.ones_like(last, dtype=torch.bool)
+    if which == "k":
+        rest[0, 0, 5] = False
+    else:
+        rest[0, 0, :, 5] = False
+    assert torch.equal(last[rest], wlast[rest])
+
+
+@gpu_only
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("T,g,t,n", LINEAR_NAN)
+def test_linear_backward_keeps_what_is_no_number(gpu, dtype, T, g, t, n):
+    q, k, v, _, scale = linear_inputs(gpu, dtype, 1, T, 2, 64, 72, T)
+    ld = torch.tensor([g, -0.05], device=gpu)
+    lens = torch.tensor([n], device=gpu).int()
+    go = rand(wk.generator(5, gpu), 1, T, 2, 72, dtype=dtype)
+    state = rand(wk.generator(6, gpu), 1, 2, 64, 72, dtype=F32)
+    at = n - 1 - t                                           # far from the sequence's end, near its beginning, or neither
+    want = api.linear_attention_backward(q, k, v, ld, scale, go, state=state, lengths=lens)
+    go[0, at, 0, 5] = math.nan
+    dq, dk, dv, ds = api.linear_attention_backward(q, k, v, ld, scale, go, state=state, lengths=lens)
+    # the gradient of the state has its column 5 lost for all tokens up to `at`
+    assert bool(dk[0, :at + 1, 0].isnan().all()) and bool(dv[0, :at + 1, 0, 5].isnan().all())
+    assert bool(ds[0, 0, :, 5].isnan().all())
+    # tokens behind it only where they share a chunk with it: 64 tokens counted from the sequence's end
+    late = n - t // 64 * 64
+    for got, ref in ((dk, want[1]), (dv, want[2])):
+        assert torch.equal(got[0, late:, 0], ref[0, late:, 0]) and torch.equal(got[:, :, 1], ref[:, :, 1])
+    keep = [i for i in range(72) if i != 5]
+    assert torch.equal(dv[..., keep], want[2][..., keep]) and torch.equal(ds[0, 0][:, keep], want[3][0, 0][:, keep])
+    assert bool(dq[0, at, 0].isnan().all())
+    rest = [i for i in range(T) if i // 64 != at // 64]
+    assert torch.equal(dq[0, rest], want[0][0, rest])
+
+
+# --------------------------------------------------------------------------
 # linear attention: gradients by value under any decay, and with any scale
 # --------------------------------------------------------------------------
 def check_gradients(gpu, dtype, q, k, v, ld, scale, go, state, n, gs):

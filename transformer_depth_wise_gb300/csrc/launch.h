@@ -261,7 +261,7 @@ struct LinearArgs {
   cudaStream_t stream;
 };
 bool linear_supported(int64_t da, int64_t dc, int dtype);
-// The fp32 workspace of a call: the segments' states.
+// The workspace of a call, in words of 32 bits: the segments' states, and the marks of what is no number in them.
 int64_t linear_workspace_floats(int64_t B, int64_t T, int H, int da, int dc, int dtype);
 cudaError_t launch_linear(const LinearArgs &a);
 

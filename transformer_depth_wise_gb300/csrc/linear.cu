@@ -342,6 +342,7 @@ __global__ void __launch_bounds__(kThreads) linear_scan_kernel(const LinearParam
   const int64_t bh = blockIdx.y;
   const int e = blockIdx.x * kThreads + threadIdx.x;
   if (e >= per) return;
+  if (p.done && e == 0) p.done[bh] = 0;
   const int64_t n = seq_length(p, bh / p.H);
   const float g = p.log_decay[bh % p.H];
   const int row = e * 4 / p.dc, col = e * 4 % p.dc;      // dc is a multiple of 4
@@ -511,7 +512,9 @@ static Split linear_split(int64_t B, int64_t T, int H, int da, int dc, int dtype
 
 int64_t linear_workspace_floats(int64_t B, int64_t T, int H, int da, int dc, int dtype) {
   const Split s = linear_split(B, T, H, da, dc, dtype);
-  return s.nseg > 1 ? B * H * s.nseg * s.nsub * da * dc : 0;
+  if (s.nseg == 1) return 0;
+  const int64_t marks = linear_tc_supported(T, dtype) ? B * H * (s.nseg * kMarks + 1) : 0;
+  return B * H * s.nseg * s.nsub * da * dc + marks;
 }
 
 cudaError_t launch_linear(const LinearArgs &a) {
@@ -534,6 +537,11 @@ cudaError_t launch_linear(const LinearArgs &a) {
   p.wait_limit = std::min(wait_limit_cycles(), 1ll << 48);    // times a CTA's length, within 63 bits
   const int64_t BH = a.B * a.H;
   const bool tc = linear_tc_supported(a.T, a.dtype);
+  if (tc && p.nseg > 1) {
+    p.marks = reinterpret_cast<uint32_t *>(p.states + BH * p.nstates * a.da * a.dc);
+    p.done = p.marks + BH * p.nseg * kMarks;
+    p.piece = (float)(p.seg_len / split.nsub);
+  }
   // The states' kernel (states = true) or the main one.
   auto chunks = [&](const LinearParams &p, bool states) -> cudaError_t {
     if (tc) return launch_linear_tc(p, BH, states, a.stream);

@@ -27,8 +27,15 @@ struct LinearParams {
   float *states;
   int nstates, step;
   int states_t;                        // or [.., dc, da], for the main kernel
+  // Tensor-core form, nseg > 1: which columns of a segment's last state hold
+  // what is no number, [B, H, nseg][kMarks] words, and a count of the (sequence,
+  // head)'s CTAs that are done, [B, H]: zero before the main kernel and after it.
+  uint32_t *marks, *done;
+  float piece;                         // tokens that a CTA of the states' kernel had
   long long wait_limit;                // SM clock cycles any wait of the tensor-core kernel may take
 };
+
+constexpr int kMarks = 8;              // 128 columns for each half of the rows
 
 __device__ __forceinline__ int64_t seq_length(const LinearParams &p, int64_t b) {
   if (!p.lengths) return p.T;

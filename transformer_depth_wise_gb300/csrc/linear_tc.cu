@@ -38,6 +38,14 @@
 // 2.15 GB of inputs and outputs (6.6 TB/s) and 106 us for the segments'
 // states; 4 x 4096 tokens, 16 heads, 51 us and 21 us.
 //
+// What is no number.  By the recurrence a NaN or an infinity in b or c stays in
+// the state however small its token's weight becomes, but the states' kernel
+// leaves out tokens whose finite traces are zero.  The main kernel sees every
+// token: a CTA whose segment's last state holds what is no number marks its
+// columns, which also go into the call's last state, and the last CTA of a
+// (sequence, head) to finish carries the marks on to the outputs of the later
+// segments.
+//
 // Every wait is bounded: one that runs out records a flag and an abort mark
 // in shared memory, on which every other wait returns at once; the issuing
 // roles stop and drain what they have in flight, and the CTA ends.
@@ -140,6 +148,20 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
   return one != 0;
 }
+// What a CTA of the main kernel has stored, before its first group counts it
+// as done: that group waits for the other state's and the outputs'.
+__device__ __forceinline__ void stored_arrive() {
+  __syncwarp();
+  asm volatile("bar.arrive 2, 384;" ::: "memory");
+}
+__device__ __forceinline__ void stored_wait() {
+  __syncwarp();
+  asm volatile("bar.sync 2, 384;" ::: "memory");
+}
+__device__ __forceinline__ void first_group_barrier() {
+  __syncwarp();
+  asm volatile("bar.sync 3, 128;" ::: "memory");
+}
 // The outputs' four warps.
 __device__ __forceinline__ void output_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
@@ -189,6 +211,13 @@ __device__ __forceinline__ void stmatrix4_t(uint32_t addr, const uint32_t (&w)[4
                ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
 }
 
+// A token whose weight in its segment's last state is below e^-kReach leaves no
+// trace there: even the largest finite product of gain, b and c comes below
+// fp32's smallest number (e^-193 of e^88.8).
+constexpr float kReach = 193.f;
+
+__device__ __forceinline__ bool no_number(uint32_t bits) { return (bits & 0x7f800000u) == 0x7f800000u; }
+
 // The tensors as [B][H][T][d], boxes of 64 tokens x 64 columns.
 struct Maps {
   CUtensorMap b, c, a;
@@ -203,7 +232,7 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
   unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t base = smem_u32(sm);
   float *pw = reinterpret_cast<float *>(sm + L::kOffPow);                       // lambda^0 .. lambda^65
-  volatile uint32_t *ctl = reinterpret_cast<uint32_t *>(sm + L::kOffBar + kBars * 8);   // TMEM address, skip, abort
+  volatile uint32_t *ctl = reinterpret_cast<uint32_t *>(sm + L::kOffBar + kBars * 8);   // TMEM address, skip, abort, done
   auto bar = [&](int b) { return base + L::kOffBar + 8u * b; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp >> 2, quad = warp & 3;
 
@@ -242,10 +271,9 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
   const float g = p.log_decay[h];
   int64_t from = begin;
   if (STATES && g < 0.f && stop > begin) {
-    // Tokens whose weight in the segment's last state is so small that even
-    // the largest finite product of a b and a c comes below fp32's smallest
-    // number (e^-193 of e^88.8) add exactly nothing: start behind them.
-    const float reach = 193.f / -g;
+    // What finite tokens before these add to the segment's last state is
+    // exactly nothing: start behind them.
+    const float reach = kReach / -g;
     if (reach < (float)(stop - begin)) from = max(begin, (stop - 1 - (int64_t)reach) / kC * kC);
   }
   const int chunks = stop > from ? (int)((stop - from + kC - 1) / kC) : 0;
@@ -319,6 +347,9 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
   // Token count of chunk c, and a row's place in the walk.
   auto length_of = [&](int c) { return c + 1 < chunks ? kC : tail; };
   auto place = [&](int r) { return p.reverse ? kC - 1 - r : r; };
+  // Whether the states' kernel may have left out tokens of this head (its own
+  // test divides: a margin for the roundings of both).
+  auto left_out = [&]() -> bool { return !STATES && p.nseg > 1 && -g * p.piece > 0.99f * kReach; };
   const bool three = STATES || p.nseg == 1;            // parts of w c: this kernel's state is the one handed out
   const uint32_t quad_addr = tmem + ((uint32_t)(quad * 32) << 16);
 
@@ -488,6 +519,51 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
         }
       }
     }
+    if (left_out()) {
+      // columns behind da hold no number only where those before them do
+      uint64_t sum = 0;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) sum = fma2(st[j], 0ull, sum);
+      float lo, hi;
+      unpair(sum, lo, hi);
+      const bool bad = row < p.dc && isnan(lo + hi);
+      if (bad && p.last) {
+        float *last = p.last + (bh * p.da + col0) * p.dc + row;
+#pragma unroll
+        for (int j = 0; j < 64; ++j)
+          if (j < cols && no_number((uint32_t)(st[j / 2] >> (j % 2 * 32)))) last[(int64_t)j * p.dc] = __int_as_float(0x7fffffff);
+      }
+      uint32_t *marks = p.marks + bh * p.nseg * kMarks;
+      const uint32_t word = __ballot_sync(0xffffffffu, bad);
+      if (lane == 0) marks[seg * kMarks + group * 4 + quad] = word;
+      if (group == 1) {
+        stored_arrive();
+      } else {
+        stored_wait();                                  // this CTA's marks and outputs are stored
+        if (threadIdx.x == 0) {
+          __threadfence();
+          ctl[3] = atomicAdd(p.done + bh, 1u) + 1 == (uint32_t)p.nseg ? 1 : 0;
+        }
+        first_group_barrier();
+        if (ctl[3]) {                                   // and so are all others' of this (sequence, head)
+          __threadfence();
+          uint32_t any = 0;
+          for (int i = threadIdx.x; i < p.nseg * kMarks; i += 128) any |= __ldcg(marks + i);
+          if (any) ctl[3] = 2;
+          if (threadIdx.x == 0) p.done[bh] = 0;         // for a launch that shares the workspace
+          first_group_barrier();
+          if (ctl[3] == 2 && row < p.dc) {              // a thread per column
+            bool lost = false;
+            for (int s = 0; s + 1 < p.nseg; ++s) {
+              lost |= ((__ldcg(marks + s * kMarks + quad) | __ldcg(marks + s * kMarks + 4 + quad)) >> lane) & 1u;
+              if (!lost) continue;
+              for (int64_t i = (s + 1) * p.seg_len; i < min(n, (s + 2) * p.seg_len); ++i)
+                ((__nv_bfloat16 *)p.out)[(walk_row(p, b, n, i) * p.H + h) * p.dc + row] = __ushort_as_bfloat16(0x7fff);
+            }
+          }
+        }
+      }
+    }
   } else if (group < 2 + L::kPartGroups) {
     // ---------------- w c in three parts, each in the tile's own layout ----------------
     share_registers<L::kRegsParts, L::kRegs>();
@@ -653,6 +729,7 @@ __global__ void __launch_bounds__(Shape<STATES>::kThreads, 1)
     // rows behind the sequence are zero
     for (int64_t t = max(stop, begin) + tid / 16; t < end; t += 8)
       if (col < p.dc) st_vec((__nv_bfloat16 *)p.out + ((b * p.T + t) * p.H + h) * p.dc + col, make_uint4(0, 0, 0, 0));
+    if (left_out()) stored_arrive();
     tc_fence_before();
   }
   __syncthreads();
