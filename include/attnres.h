@@ -296,7 +296,9 @@ int attnres_rms_norm(const void *x, int64_t B, int64_t T, int64_t D, int dtype, 
  *   inv_freq    device fp64 [rot/2], radians per position (NULL if rot == 0)
  *   rot         0 .. d, a multiple of 16 (bf16) or 8 (fp32)
  *   q_out, k_out  device, rows q_out_stride / k_out_stride elements apart;
- *               may be q / k themselves with the same stride
+ *               may be q / k themselves with the same stride, and overlap
+ *               nothing else (VALUE where an output starts at another
+ *               tensor of the call, or at its own input with other rows)
  */
 int attnres_head_norm_rotate(const void *q, const void *k, int64_t B, int64_t T, int Hq, int Hk, int64_t d, int dtype,
                              int64_t q_stride, int64_t k_stride, const float *q_weight, const float *k_weight,
@@ -311,6 +313,8 @@ int attnres_head_norm_rotate(const void *q, const void *k, int64_t B, int64_t T,
  *   page_table  device int32 [B, max_pages]: page i of sequence b holds its
  *               positions i * page_size .. (i + 1) * page_size - 1;
  *               page_size * max_pages at most 2^30
+ *   q_out       may be q with the same stride; it and the caches overlap
+ *               nothing else
  * A token's place in the cache is its position.  A token whose position is
  * negative or behind the table, or whose page number is outside
  * [0, num_pages), is rotated into q_out but not stored (padding).  Two
@@ -329,7 +333,9 @@ int attnres_head_norm_rotate_append(const void *q, const void *k, const void *v,
  * grad_k of its outputs (nothing from the forward is needed but its inputs):
  *   dz = the gradient turned back, u = dz (.) weight, r = (mean x^2 + eps)^(-1/2)
  *   dx = r (u - x r^2 mean(u (.) x)),   grad_weight = sum over tokens and heads of dz (.) x r
- *   dq, dk      device, contiguous [B,T,Hq,d], [B,T,Hk,d]
+ *   dq, dk      device, contiguous [B,T,Hq,d], [B,T,Hk,d]; may be q / k or
+ *               grad_q / grad_k where those are contiguous, and overlap
+ *               nothing else
  *   grad_q_weight, grad_k_weight  device fp32 [d] or NULL
  *   workspace   device fp32 [workspace_rows, d], needed for a weight gradient;
  *               attnres_head_norm_rotate_backward_workspace_rows() rows fill

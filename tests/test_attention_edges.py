@@ -4,8 +4,9 @@ import math
 import pytest
 import torch
 
-from test_attention_ops import BF, E, F32, U, linear_grad_ref, linear_inputs, paged_inputs, rand, within
-from transformer_depth_wise_gb300 import api
+from test_attention_ops import (BF, E, F32, U, linear_grad_ref, linear_inputs, norm_inputs, paged_inputs, rand,
+                                within)
+from transformer_depth_wise_gb300 import _lib, api
 from transformer_depth_wise_gb300 import workloads as wk
 
 gpu_only = pytest.mark.gpu
@@ -170,3 +171,62 @@ def test_linear_gradient_of_an_unused_state_is_the_state_gradient(gpu, dtype, T)
     assert torch.equal(last[::2], state[::2])
     ds = api.linear_attention_backward(q, k, v, ld, 0.3, v.clone(), state=state, lengths=n, grad_state=gs)[3]
     assert torch.equal(ds[::2], gs[::2])
+
+
+# --------------------------------------------------------------------------
+# head norm
+# --------------------------------------------------------------------------
+def at(i):
+    return 0x7F0000000000 + (i << 24)      # a stand-in for a device pointer of its own (never dereferenced)
+
+
+def test_rotate_outputs_that_are_other_inputs_are_refused():
+    """In place is an output on its own input, row by row; on any other input, or with other rows, calls would read what
+    others have written.  Refused before any launch."""
+    value = -8                              # ATTNRES_ERR_VALUE
+
+    def rotate(q=at(0), k=at(1), qo=at(2), ko=at(3), qos=256, kos=256, T=2):
+        return _lib.lib().attnres_head_norm_rotate(q, k, 1, T, 4, 4, 64, 1, 512, 512, None, None, None, None, 0, 0, 1e-6,
+                                                   qo, ko, qos, kos, None)
+    assert rotate(qo=at(1)) == value and rotate(ko=at(0)) == value and rotate(ko=at(2)) == value
+    assert rotate(qo=at(1), qos=512) == value and rotate(qo=at(0)) == value and rotate(ko=at(1)) == value
+
+    def append(q=at(0), k=at(1), v=at(2), qo=at(3), kc=at(4), vc=at(5), qos=256):
+        return _lib.lib().attnres_head_norm_rotate_append(q, k, v, 1, 2, 4, 4, 64, 1, 512, 512, 512, None, None, None, None,
+                                                          0, 0, 1e-6, qo, qos, kc, vc, 8, 16, at(6), 4, None)
+    assert append(qo=at(1)) == value and append(qo=at(2)) == value and append(qo=at(0)) == value
+    assert append(kc=at(5)) == value and append(kc=at(0)) == value and append(vc=at(2)) == value and append(vc=at(3)) == value
+
+    def backward(dq=at(4), dk=at(5), qs=512, gs=512):
+        return _lib.lib().attnres_head_norm_rotate_backward(at(0), at(1), 1, 2, 4, 4, 64, 1, qs, 512, None, None, None, None,
+                                                            0, 0, 1e-6, at(2), at(3), gs, 512, dq, dk, None, None, None, 0,
+                                                            None)
+    assert backward(dq=at(0)) == value and backward(dq=at(2)) == value and backward(dk=at(1)) == value
+    assert backward(dq=at(1)) == value and backward(dq=at(3)) == value and backward(dk=at(0)) == value
+    assert backward(dk=at(2)) == value and backward(dq=at(5)) == value and backward(dq=at(1), qs=256) == value
+
+
+@gpu_only
+def test_rotate_outputs_that_are_other_inputs_are_refused_by_the_wrappers(gpu):
+    q, k, v, wq, wk_, pos, fr = norm_inputs(gpu, BF, 2, 5, 4, 4, 64, 64, 3, packed=False)
+    before = [t.clone() for t in (q, k, v)]
+    kc, vc = (torch.zeros(4, 4, 16, 64, dtype=BF, device=gpu) for _ in range(2))
+    table = torch.arange(4, device=gpu).view(2, 2).int()
+    wide = torch.cat((q, k), 2)             # q with rows of its own, and with rows of this one
+    for call in (lambda: api.head_norm_rotate(q, k, wq, wk_, pos, fr, q_out=k),
+                 lambda: api.head_norm_rotate(q, k, wq, wk_, pos, fr, k_out=q),
+                 lambda: api.head_norm_rotate(q, k, wq, wk_, pos, fr, q_out=v, k_out=v),
+                 lambda: api.head_norm_rotate(wide[:, :, :4], k, wq, wk_, pos, fr,
+                                              q_out=wide.view(-1)[:q.numel()].view(q.shape)),
+                 lambda: api.head_norm_rotate_append(q, k, v, wq, wk_, pos, fr, kc, vc, table, q_out=k),
+                 lambda: api.head_norm_rotate_append(q, k, v, wq, wk_, pos, fr, kc, kc, table)):
+        with pytest.raises(_lib.AttnResError):
+            call()
+    assert all(torch.equal(a, b) for a, b in zip((q, k, v), before)) and not bool(kc.any())
+    # each on its own input, rows apart as they are
+    want = api.head_norm_rotate(q, k, wq, wk_, pos, fr)
+    qv, kv = wide[:, :, :4], wide[:, :, 4:]
+    api.head_norm_rotate(qv, kv, wq, wk_, pos, fr, q_out=qv, k_out=kv)
+    assert torch.equal(qv, want[0]) and torch.equal(kv, want[1])
+    qa = api.head_norm_rotate_append(q, k, v, wq, wk_, pos, fr, kc, vc, table, q_out=q)
+    assert qa is q and torch.equal(q, want[0])

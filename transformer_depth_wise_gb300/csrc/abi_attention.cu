@@ -63,6 +63,12 @@ bool among(const void *out, const void *x, const void *y, const void *z, const v
   return out && (out == x || out == y || out == z || out == w);
 }
 
+// An output may lie on its own input, row on row (a work item reads a head
+// before it writes it); on other rows some would read what others have written.
+bool shifted(const void *out, int64_t out_stride, const void *in, int64_t in_stride, int64_t rows) {
+  return out == in && rows > 1 && out_stride != in_stride;
+}
+
 int check_linear(int64_t B, int64_t T, int H, int64_t dk, int64_t dv, int dtype, int64_t &rows) {
   int st = check_batch(B, T, dtype, rows);
   if (st) return st;
@@ -101,6 +107,9 @@ int attnres_head_norm_rotate(const void *q, const void *k, int64_t B, int64_t T,
   if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out) || misaligned(q_weight) ||
       misaligned(k_weight) || misaligned(positions, 4) || misaligned(inv_freq, 8))
     return ATTNRES_ERR_ALIGNMENT;
+  if (q_out == k || k_out == q || q_out == k_out || shifted(q_out, q_out_stride, q, q_stride, rows) ||
+      shifted(k_out, k_out_stride, k, k_stride, rows))
+    return ATTNRES_ERR_VALUE;
   HeadNormArgs a{};
   a.q = q; a.k = k; a.q_stride = q_stride; a.k_stride = k_stride; a.rows = rows; a.T = T;
   a.Hq = Hq; a.Hk = Hk; a.d = (int)d; a.dtype = dtype; a.q_weight = q_weight; a.k_weight = k_weight;
@@ -130,6 +139,9 @@ int attnres_head_norm_rotate_append(const void *q, const void *k, const void *v,
       misaligned(v_cache) || misaligned(q_weight) || misaligned(k_weight) || misaligned(positions, 4) ||
       misaligned(inv_freq, 8) || misaligned(page_table, 4))
     return ATTNRES_ERR_ALIGNMENT;
+  if (q_out == k || q_out == v || shifted(q_out, q_out_stride, q, q_stride, rows)) return ATTNRES_ERR_VALUE;
+  if (store && (k_cache == v_cache || among(k_cache, q, k, v, q_out) || among(v_cache, q, k, v, q_out)))
+    return ATTNRES_ERR_VALUE;
   HeadNormArgs a{};
   a.q = q; a.k = k; a.v = v; a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
   a.rows = rows; a.T = T; a.Hq = Hq; a.Hk = Hk; a.d = (int)d; a.dtype = dtype;
@@ -170,6 +182,10 @@ int attnres_head_norm_rotate_backward(const void *q, const void *k, int64_t B, i
   if (!aligned16(q) || !aligned16(k) || !aligned16(grad_q) || !aligned16(grad_k) || !aligned16(dq) || !aligned16(dk) ||
       misaligned(q_weight) || misaligned(k_weight) || misaligned(positions, 4) || misaligned(inv_freq, 8))
     return ATTNRES_ERR_ALIGNMENT;
+  if (dq == dk || among(dq, k, grad_k, nullptr) || among(dk, q, grad_q, nullptr) ||
+      shifted(dq, Hq * d, q, q_stride, rows) || shifted(dq, Hq * d, grad_q, grad_q_stride, rows) ||
+      shifted(dk, Hk * d, k, k_stride, rows) || shifted(dk, Hk * d, grad_k, grad_k_stride, rows))
+    return ATTNRES_ERR_VALUE;
   HeadNormBackwardArgs a{};
   a.q = q; a.k = k; a.grad_q = grad_q; a.grad_k = grad_k;
   a.q_stride = q_stride; a.k_stride = k_stride; a.gq_stride = grad_q_stride; a.gk_stride = grad_k_stride;
