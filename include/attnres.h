@@ -293,7 +293,9 @@ int attnres_rms_norm(const void *x, int64_t B, int64_t T, int64_t D, int dtype, 
  *   positions   device int32 [B,T], or NULL for 0 .. T-1 in every sequence;
  *               any value: angles are exact to 2^-25 of a half turn however
  *               far the position
- *   inv_freq    device fp64 [rot/2], radians per position (NULL if rot == 0)
+ *   inv_freq    device fp64 [rot/2], radians per position (NULL if rot == 0);
+ *               NaN and infinities give NaN, finite ones of 2^54 and more
+ *               turn nothing
  *   rot         0 .. d, a multiple of 16 (bf16) or 8 (fp32)
  *   q_out, k_out  device, rows q_out_stride / k_out_stride elements apart;
  *               may be q / k themselves with the same stride, and overlap

@@ -4,8 +4,8 @@ import math
 import pytest
 import torch
 
-from test_attention_ops import (BF, E, F32, U, linear_grad_ref, linear_inputs, norm_inputs, paged_inputs, rand,
-                                within)
+from test_attention_ops import (BF, E, EPS, F32, U, linear_grad_ref, linear_inputs, norm_inputs, paged_inputs,
+                                rand, within)
 from transformer_depth_wise_gb300 import _lib, api
 from transformer_depth_wise_gb300 import workloads as wk
 
@@ -230,3 +230,19 @@ def test_rotate_outputs_that_are_other_inputs_are_refused_by_the_wrappers(gpu):
     assert torch.equal(qv, want[0]) and torch.equal(kv, want[1])
     qa = api.head_norm_rotate_append(q, k, v, wq, wk_, pos, fr, kc, vc, table, q_out=q)
     assert qa is q and torch.equal(q, want[0])
+
+
+@gpu_only
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("inter", [False, True])
+def test_rotate_frequencies_that_are_no_number(gpu, dtype, inter):
+    q, k, _, wq, wk_, pos, fr = norm_inputs(gpu, dtype, 2, 5, 3, 2, 64, 64, 7)
+    pos[0, 0] = 0
+    want = api.head_norm_rotate(q, k, wq, wk_, pos, fr, EPS, interleaved=inter)
+    lost = [3, 9, 30]
+    fr[3], fr[9], fr[30] = math.nan, math.inf, -math.inf
+    got = api.head_norm_rotate(q, k, wq, wk_, pos, fr, EPS, interleaved=inter)
+    cols = [2 * i + j for i in lost for j in (0, 1)] if inter else [i + j for i in lost for j in (0, 32)]
+    rest = [i for i in range(64) if i not in cols]
+    for a, b in zip(got, want):
+        assert bool(a[..., cols].isnan().all()) and torch.equal(a[..., rest], b[..., rest])

@@ -42,10 +42,12 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBackFlight = 2;         // heads a team of the backward kernel has in flight
 
 // inv_freq (radians per position) as 2^-64ths of a turn per position, modulo
-// one turn; 0 for what is no number.
+// one turn.  The last bit says that inv_freq is no finite number (2^-64 of a
+// turn is less than what the angle is rounded by at any position).
 __device__ __forceinline__ uint64_t turn_step(double inv_freq) {
   const uint64_t bits = (uint64_t)__double_as_longlong(inv_freq);
   const int exponent = (int)((bits >> 52) & 0x7ff) - 1023;
+  if (exponent == 1024) return 1;
   if (exponent < -1000 || exponent > 53) return 0;          // nothing, or beyond any use
   const uint64_t mantissa = (bits & 0xfffffffffffffull) | 0x10000000000000ull;
   constexpr uint64_t kPerTurn = 11743562013128004906ull;    // 2^66 / (2 pi), rounded
@@ -53,13 +55,13 @@ __device__ __forceinline__ uint64_t turn_step(double inv_freq) {
   // the product times 2^(exponent - 52 - 66 + 64)
   const int right = 54 - exponent;
   const uint64_t t = right >= 128 ? 0 : right >= 64 ? hi >> (right - 64) : right == 0 ? lo : (lo >> right) | (hi << (64 - right));
-  return bits >> 63 ? 0 - t : t;
+  return (bits >> 63 ? 0 - t : t) & ~1ull;
 }
 
-// cosine and sine of `position` steps.
+// cosine and sine of `position` steps; NaN for a frequency that is no number.
 __device__ __forceinline__ float2 turned(uint64_t step, int position) {
   const uint64_t t = step * (uint64_t)(int64_t)position;
-  const float half_turns = (float)(int)(t >> 32) * 0x1p-31f;   // [-1, 1)
+  const float half_turns = step & 1 ? __int_as_float(0x7fffffff) : (float)(int)(t >> 32) * 0x1p-31f;   // [-1, 1)
   float2 cs;
   sincospif(half_turns, &cs.y, &cs.x);
   return cs;
