@@ -145,6 +145,23 @@ def check_gradients(gpu, dtype, q, k, v, ld, scale, go, state, n, gs):
 
 
 @gpu_only
+@pytest.mark.parametrize("dtype,B,T,H,dk,dv,lengths,with_state", [
+    (BF, 1, 150, 2, 64, 64, None, True), (BF, 2, 129, 4, 96, 80, [64, 129], False), (BF, 1, 1500, 2, 128, 128, None, True),
+    (BF, 1, 2100, 2, 128, 128, None, True), (BF, 2, 1300, 3, 128, 96, [1300, 700], True),
+    (BF, 2, 1000, 2, 72, 128, [100, 993], False), (F32, 1, 150, 2, 64, 64, None, True),
+    (F32, 1, 257, 1, 128, 128, None, True), (F32, 2, 1100, 1, 64, 64, [1100, 513], True),
+])
+@pytest.mark.parametrize("decay", [0.0, -0.7, -3.0, -math.inf])
+def test_linear_gradients_under_any_decay(gpu, dtype, B, T, H, dk, dv, lengths, with_state, decay):
+    q, k, v, ld, scale = linear_inputs(gpu, dtype, B, T, H, dk, dv, B + T + dv, decay)
+    g = wk.generator(8, gpu)
+    n = None if lengths is None else torch.tensor(lengths, device=gpu).int()
+    state = rand(g, B, H, dk, dv, dtype=F32, scale=2.0) if with_state else None
+    gs = rand(g, B, H, dk, dv, dtype=F32) if with_state else None
+    check_gradients(gpu, dtype, q, k, v, ld, scale, rand(g, B, T, H, dv, dtype=dtype), state, n, gs)
+
+
+@gpu_only
 @pytest.mark.parametrize("dtype,T,lengths", [(BF, 150, None), (BF, 1500, [1500, 700]), (F32, 200, None),
                                              (F32, 700, [0, 700])])
 @pytest.mark.parametrize("scale", [1e-30, -0.3, 7.0])
