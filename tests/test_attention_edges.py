@@ -263,3 +263,20 @@ def test_rotate_frequencies_that_are_no_number(gpu, dtype, inter):
     rest = [i for i in range(64) if i not in cols]
     for a, b in zip(got, want):
         assert bool(a[..., cols].isnan().all()) and torch.equal(a[..., rest], b[..., rest])
+
+
+# --------------------------------------------------------------------------
+# the build
+# --------------------------------------------------------------------------
+def test_build_checks_the_planned_registers():
+    from transformer_depth_wise_gb300 import build as b
+    log = "".join(f"ptxas info    : Compiling entry function '_ZN7attnres{name}' for 'sm_103a'\n"
+                  f"ptxas info    : Function properties for _ZN7attnres{name}\n    0 bytes stack frame\n"
+                  f"ptxas info    : Used {n} registers, used 2 barriers\n"
+                  for name, n in (("16linear_tc_kernelILb0EE", 72), ("5otherE", 40), ("16linear_tc_kernelILb1EE", 72)))
+    b.check_registers(log, "linear_tc_kernel", 72)
+    for bad in (log.replace("72", "70", 1), log.replace("Used 72", "Used 80"), ""):
+        with pytest.raises(RuntimeError):
+            b.check_registers(bad, "linear_tc_kernel", 72)
+    for name in b.REGISTER_SHARES:
+        assert b.planned_registers(f"{b.CSRC}/{name}") % 8 == 0

@@ -7,6 +7,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import hashlib
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -47,6 +48,28 @@ def _deps_stamp() -> str:
     return h.hexdigest()
 
 
+def check_registers(log: str, kernel: str, want: int) -> None:
+    """Raise unless ptxas's report (-v) gives every instance of `kernel` exactly `want` registers.
+
+    A kernel whose roles take over registers from one another (setmaxnreg) counts on the number that its launch gives a
+    thread; with any other, the host refuses every call.
+    """
+    used = re.findall(r"Compiling entry function '([^']+)'.*?Used (\d+) registers", log, re.S)
+    found = [(name, int(n)) for name, n in used if kernel in name]
+    if not found or any(n != want for _, n in found):
+        raise RuntimeError(f"{kernel} is planned for {want} registers a thread, ptxas gave {[n for _, n in found]}")
+
+
+def planned_registers(src: str) -> int:
+    """kRegs of a source file: the registers a thread that its roles' shares start from."""
+    with open(src) as fh:
+        return int(re.search(r"constexpr int kRegs = (\d+);", fh.read()).group(1))
+
+
+# Sources with a kernel of register shares.
+REGISTER_SHARES = {"linear_tc.cu": "linear_tc_kernel"}
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     """Compile every csrc/*.cu for sm_103a and link libattnres.so; returns its path."""
     stamp_file = os.path.join(OBJDIR, "stamp")
@@ -61,11 +84,14 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
 
     def compile_one(src: str) -> str:
         obj = os.path.join(OBJDIR, os.path.basename(src)[:-3] + ".o")
-        cmd = [cc, *ARCH, *flags, "-c", src, "-o", obj]
+        shares = REGISTER_SHARES.get(os.path.basename(src))
+        cmd = [cc, *ARCH, *flags, *(["-Xptxas", "-v"] if shares else []), "-c", src, "-o", obj]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
-        if verbose and (r.stdout or r.stderr):
+        if shares:
+            check_registers(r.stdout + r.stderr, shares, planned_registers(src))
+        if verbose and (r.stdout or r.stderr) and (extra_flags or not shares):
             print(r.stdout + r.stderr, file=sys.stderr)
         return obj
 

@@ -770,7 +770,8 @@ Split linear_tc_split(int64_t BH, int64_t T) {
 namespace {
 // The shares above start from the registers a launch gives each thread: what
 // the compiler chose has to be that number, or a role would wait for
-// registers that nobody gives.
+// registers that nobody gives.  The build checks it too, so that another
+// compiler's choice shows there.
 template <bool STATES> bool registers_as_planned() {
   static const bool ok = [] {
     cudaFuncAttributes a;
