@@ -126,6 +126,46 @@ def test_linear_backward_keeps_what_is_no_number(gpu, dtype, T, g, t, n):
     assert torch.equal(dq[0, rest], want[0][0, rest])
 
 
+@gpu_only
+def test_linear_captured_calls_and_streams_with_what_is_no_number(gpu):
+    """A captured forward and backward pass in several segments, replayed with a NaN that has decayed away and without
+    it again, and the same calls on three streams at once, each with a workspace of its own."""
+    q, k, v, _, scale = linear_inputs(gpu, BF, 2, 3000, 3, 128, 128, 41)
+    ld = torch.tensor([-20.0, -0.7, -0.01], device=gpu)
+    go = rand(wk.generator(5, gpu), 2, 3000, 3, 128)
+
+    def run():
+        out, last = api.linear_attention(q, k, v, ld, scale)
+        return (out, last, *api.linear_attention_backward(q, k, v, ld, scale, go, grad_state=last, want_initial=True))
+    clean = [t.clone() for t in run()]
+    v1 = v.clone()
+    v1[0, 200, 0, 7] = math.nan
+    v0 = v.clone()
+    v.copy_(v1)
+    spoilt = [t.clone() for t in run()]
+    assert bool(spoilt[0][0, 200:, 0, 7].isnan().all()) and bool(spoilt[1][0, 0, :, 7].isnan().all())
+    v.copy_(v0)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for now, want in ((v0, clean), (v1, spoilt), (v1, spoilt), (v0, clean)):
+        v.copy_(now)
+        graph.replay()
+        assert all(torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0)) and torch.equal(a.isnan(), b.isnan())
+                   for a, b in zip(got, want))
+    v.copy_(v1)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    results = []
+    for s in streams:
+        with torch.cuda.stream(s):
+            results.append(run())
+    torch.cuda.synchronize()
+    for r in results:
+        assert all(torch.equal(a.nan_to_num(7.0), b.nan_to_num(7.0)) and torch.equal(a.isnan(), b.isnan())
+                   for a, b in zip(r, spoilt))
+
+
 # --------------------------------------------------------------------------
 # linear attention: gradients by value under any decay, and with any scale
 # --------------------------------------------------------------------------
