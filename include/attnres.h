@@ -385,9 +385,9 @@ int attnres_paged_attention(const void *q, int64_t q_stride, const void *k_cache
 int64_t attnres_paged_attention_workspace_bytes(int Hq, int Hk, int64_t d, int dtype);
 
 /*
- * Linear attention with one decay per head, over prompts (the delta-free
- * linear layers that "Attention Residuals：当网络深度也拥有寻址能力", section "Kimi
- * Linear 与 K3 中的接入", puts between the aggregations):
+ * Linear attention with one fixed decay per head, over prompts.  (It is not
+ * the gated delta rule: nothing of the state is taken back, and the decay is
+ * a constant without a gradient.)
  *   S_t = e^{g_h} S_{t-1} + k_t v_t^T,   out_t = scale S_t^T q_t
  *   q, k        device [B,T,H,dk];  v device [B,T,H,dv];  dk, dv up to 128,
  *               multiples of 8 (bf16) or 4 (fp32)
@@ -404,7 +404,9 @@ int64_t attnres_paged_attention_workspace_bytes(int Hq, int Hk, int64_t d, int d
  *               Two calls that may overlap need one each
  * bf16 inputs: products on the tensor cores with fp32
  * accumulators and an fp32 state; the masked products and the state are
- * rounded to bf16 where they enter the product that forms out.  fp32 inputs:
+ * rounded to bf16 where they enter the product that forms out (0.0023 of
+ * out's norm for normal inputs, 0.0017 of it the rounding of out itself).
+ * fp32 inputs:
  * products there too, of operands split into two parts, exact to 2^-19 at worst
  * and 2^-22 on average, and an fp32 state.  Prompts are
  * worked on in chunks of 64 tokens: a NaN or infinity in a token's q, k or v
@@ -551,6 +553,9 @@ int attnres_take_device_error(void);
  * launches made after this call (process-wide; 0 restores the default of
  * 4e9 cycles, about 2 s).  A very short limit makes waits run out on
  * purpose, which exercises the give-up path above without a GPU fault.
+ * In attnres_linear_attention and its backward on bf16 the limit holds for
+ * all waits of a CTA together, from its start, and counts once more for every
+ * 8192 chunks of 64 tokens that the CTA works through.
  * The final drain of a CTA's own operations in flight always keeps the
  * default limit.  cycles < 0: ATTNRES_ERR_VALUE.
  */

@@ -763,7 +763,8 @@ def head_norm_rotate(q, k, q_weight=None, k_weight=None, positions=None, inv_fre
     """RMS norm of every query and key head and the position rotation, in one pass; returns (q_out, k_out).
 
     q [B,T,Hq,d], k [B,T,Hk,d]: contiguous, or views of one projection's output.  positions int32 [B,T]
-    (None: 0 .. T-1), inv_freq float64 [rot/2] (rotary_frequencies; None: no rotation).  q_out / k_out may be q / k.
+    (None: 0 .. T-1), inv_freq float64 [rot/2] (rotary_frequencies; None: no rotation).  q_out / k_out may be q / k
+    themselves, row on row, and overlap nothing else.
     """
     B, T, Hq, Hk, d, qs, ks, rot = _norm_args(q, k, q_weight, k_weight, positions, inv_freq)
     if q_out is None:

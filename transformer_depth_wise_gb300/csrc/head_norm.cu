@@ -18,8 +18,9 @@
 // flight; no warp waits for another.
 //
 // Measured on GB300, bf16: 65536 tokens of 56 + 8 heads of 128, 332 us
-// (6.5 TB/s); 256 tokens of 56 + 8 + 8 heads into a cache, 7.0 us, a chain of
-// dependent loads; backward over 16384 tokens of 16 + 16 heads, 69 us (5.8
+// (6.5 TB/s); 256 tokens of 56 + 8 + 8 heads into a cache, 7.1 us (frequencies,
+// position, page and heads are read one after the other, although only the
+// store's address needs the page); backward over 16384 tokens of 16 + 16 heads, 69 us (5.8
 // TB/s, two heads in flight: three take 77 us, four 82) and 4.4 us for the
 // weights' sums.
 //

@@ -62,7 +62,7 @@ constexpr int kMaxDim = 128;
 // are issued: splitting, loads of operands, and 1100 products a scheduler.
 //
 // Measured on GB300, 128 x 128: 11.3 us for a chunk and slice (on the CUDA
-// cores 24), 2.8 in the states' kernel; 64 heads x 4096 tokens 733 us (1532).
+// cores 24), 2.8 in the states' kernel; 64 heads x 4096 tokens 740 us (1532).
 // Twelve and sixteen warps (a S by four of its own, the state in eight) take
 // 708 and 738 there, and 4 to 9 % longer with 64 x 64.
 // ---------------------------------------------------------------------------
