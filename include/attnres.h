@@ -68,6 +68,8 @@ typedef enum {
 #define ATTNRES_MAX_SOURCES 256
 /* Most queries one phase-1 call may batch (S). */
 #define ATTNRES_MAX_QUERIES 64
+/* Most axes of a token's position. */
+#define ATTNRES_MAX_AXES 8
 
 /*
  * Depth aggregation, eq. A1-A3 ("DepthResidual.forward"; the pages'
@@ -265,6 +267,58 @@ int attnres_block_merge_update(const void *inter_out, const float *inter_lse, co
 int attnres_rms_norm(const void *x, int64_t B, int64_t T, int64_t D, int dtype, const float *weight,
                      float eps, void *y, void *stream);
 
+/*
+ * The pre-norm of a sublayer that keeps a plain residual stream (a running
+ * partial, or a model's layers without depth attention): the addition and the
+ * norm in one pass.
+ *   s = x + residual (fp32),  sum = s,  y = s / sqrt(mean_d s^2 + eps) (.) weight
+ * Both outputs are rounded once from the unrounded s.
+ *   residual    device [B,T,D] or NULL (s = x)
+ *   weight      device fp32 [D] or NULL (ones)
+ *   sum_out     device [B,T,D] or NULL
+ *   y           device [B,T,D]
+ * sum_out and y may each be x or residual, but not the same, and overlap
+ * nothing else.  D up to 2048 16-byte vectors.
+ */
+int attnres_add_rms_norm(const void *x, const void *residual, int64_t B, int64_t T, int64_t D, int dtype,
+                         const float *weight, float eps, void *sum_out, void *y, void *stream);
+
+/*
+ * The same with y in 8 bits for a matrix product: e4m3 values (largest 448)
+ * and fp32 scales, y ~ y8 * scale with
+ *   scale = max(max |y| over the group / 448, 2^-126),  y8 = y / scale to nearest even
+ *   group       elements per scale: 32, 64 or 128 (D a multiple), or 0: one
+ *               scale per token row (VALUE otherwise)
+ *   y8          device bytes [B,T,D];  scales device fp32 [B,T,D/group] or [B,T]
+ * y8 and scales overlap nothing else.  A NaN among a group's y (an infinity
+ * in a row makes one) gives a NaN scale and NaN y8 in that group.
+ */
+int attnres_add_rms_norm_8bit(const void *x, const void *residual, int64_t B, int64_t T, int64_t D, int dtype,
+                              const float *weight, float eps, int group, void *sum_out, void *y8, float *scales,
+                              void *stream);
+
+/*
+ * Backward of attnres_add_rms_norm at the stored sum s (x's and the
+ * residual's gradient are the same):
+ *   u = grad_y (.) weight,  r = (mean s^2 + eps)^(-1/2)
+ *   dx = grad_sum + r (u - s r^2 mean(u (.) s)),   grad_weight = sum over rows of grad_y (.) s r
+ *   grad_sum    device [B,T,D], the upstream gradient of sum, or NULL (zero)
+ *   dx          device [B,T,D]; may be s, grad_y or grad_sum, and overlaps
+ *               nothing else
+ *   grad_weight device fp32 [D] or NULL
+ *   workspace   device fp32 [workspace_rows, D], needed for grad_weight;
+ *               attnres_add_rms_norm_backward_workspace_rows() rows fill the
+ *               current device, fewer (at least 1) run fewer CTAs.  Its
+ *               contents on entry do not matter; calls that may overlap need
+ *               one each.
+ * The weight's sums run in a fixed order: the same inputs and workspace_rows
+ * give the same bits.  B*T == 0: grad_weight is set to zero.
+ */
+int attnres_add_rms_norm_backward(const void *s, int64_t B, int64_t T, int64_t D, int dtype, const float *weight,
+                                  float eps, const void *grad_y, const void *grad_sum, void *dx, float *grad_weight,
+                                  float *workspace, int64_t workspace_rows, void *stream);
+int64_t attnres_add_rms_norm_backward_workspace_rows(void);
+
 /* -------------------------------------------------------------------------
  * The attention sublayer's operators.  They work on head tensors: a query,
  * key or value tensor is [B, T, H, d] with the heads of a token side by side
@@ -354,6 +408,44 @@ int attnres_head_norm_rotate_backward(const void *q, const void *k, int64_t B, i
                                       float *grad_q_weight, float *grad_k_weight, float *workspace,
                                       int64_t workspace_rows, void *stream);
 int64_t attnres_head_norm_rotate_backward_workspace_rows(void);
+
+/*
+ * The three calls above with positions of several axes (time, height and
+ * width of an image's or a video's patches; text has the same position on
+ * all of them): pair i turns by positions[token][axes[i]] * inv_freq[i].
+ *   num_axes    1 .. ATTNRES_MAX_AXES (SHAPE otherwise)
+ *   positions   device int32 [B,T,num_axes]; NULL only with one axis (0 ..
+ *               T-1) or without a rotation
+ *   axes        device int32 [rot/2]: the axis of each pair, in any order
+ *               (sections of the pairs, or the axes taking turns); a pair
+ *               whose axis is outside 0 .. num_axes - 1 is not turned.  NULL:
+ *               the first axis for all pairs
+ *   places      device int32 [B,T] (_append): each token's place in the
+ *               cache, which several axes do not give.  Negative ones and
+ *               ones behind the table are not stored, as above
+ * Everything else is as there, and one axis gives the same bits as there.
+ */
+int attnres_head_norm_rotate_axes(const void *q, const void *k, int64_t B, int64_t T, int Hq, int Hk, int64_t d,
+                                  int dtype, int64_t q_stride, int64_t k_stride, const float *q_weight,
+                                  const float *k_weight, const int32_t *positions, int num_axes, const int32_t *axes,
+                                  const double *inv_freq, int rot, int interleaved, float eps, void *q_out,
+                                  void *k_out, int64_t q_out_stride, int64_t k_out_stride, void *stream);
+int attnres_head_norm_rotate_axes_append(const void *q, const void *k, const void *v, int64_t B, int64_t T, int Hq,
+                                         int Hk, int64_t d, int dtype, int64_t q_stride, int64_t k_stride,
+                                         int64_t v_stride, const float *q_weight, const float *k_weight,
+                                         const int32_t *positions, int num_axes, const int32_t *axes,
+                                         const int32_t *places, const double *inv_freq, int rot, int interleaved,
+                                         float eps, void *q_out, int64_t q_out_stride, void *k_cache, void *v_cache,
+                                         int64_t num_pages, int page_size, const int32_t *page_table, int max_pages,
+                                         void *stream);
+int attnres_head_norm_rotate_axes_backward(const void *q, const void *k, int64_t B, int64_t T, int Hq, int Hk,
+                                           int64_t d, int dtype, int64_t q_stride, int64_t k_stride,
+                                           const float *q_weight, const float *k_weight, const int32_t *positions,
+                                           int num_axes, const int32_t *axes, const double *inv_freq, int rot,
+                                           int interleaved, float eps, const void *grad_q, const void *grad_k,
+                                           int64_t grad_q_stride, int64_t grad_k_stride, void *dq, void *dk,
+                                           float *grad_q_weight, float *grad_k_weight, float *workspace,
+                                           int64_t workspace_rows, void *stream);
 
 /*
  * Attention of one new token per sequence over a paged key-value cache, split

@@ -16,6 +16,7 @@ ATTNRES_F32 = 0
 ATTNRES_BF16 = 1
 ATTNRES_MAX_SOURCES = 256
 ATTNRES_MAX_QUERIES = 64
+ATTNRES_MAX_AXES = 8
 
 STATUS = {
     0: "ATTNRES_OK",
@@ -46,6 +47,10 @@ SIGNATURES = {
     "attnres_block_merge_update": (_int, [_vp, _vp, _vp, _vp, _vp, _i64, _i64, _i64, _int, _vp, _vp, _f,
                                           _vp, _vp, _vp, _vp, _f, _vp, _vp]),
     "attnres_rms_norm": (_int, [_vp, _i64, _i64, _i64, _int, _vp, _f, _vp, _vp]),
+    "attnres_add_rms_norm": (_int, [_vp, _vp, _i64, _i64, _i64, _int, _vp, _f, _vp, _vp, _vp]),
+    "attnres_add_rms_norm_8bit": (_int, [_vp, _vp, _i64, _i64, _i64, _int, _vp, _f, _int, _vp, _vp, _vp, _vp]),
+    "attnres_add_rms_norm_backward": (_int, [_vp, _i64, _i64, _i64, _int, _vp, _f, _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
+    "attnres_add_rms_norm_backward_workspace_rows": (_i64, []),
     "attnres_depth_aggregate_backward": (_int, [_vp, _int, _i64, _i64, _i64, _int, _vp, _vp, _f, _vp, _vp,
                                                 _int, _vp, _vp, _vp, _i64, _vp]),
     "attnres_depth_aggregate_backward_workspace_rows": (_i64, [_i64, _int]),
@@ -65,6 +70,14 @@ SIGNATURES = {
                                                  _vp, _vp, _int, _int, _f, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _vp,
                                                  _vp, _i64, _vp]),
     "attnres_head_norm_rotate_backward_workspace_rows": (_i64, []),
+    "attnres_head_norm_rotate_axes": (_int, [_vp, _vp, _i64, _i64, _int, _int, _i64, _int, _i64, _i64, _vp, _vp, _vp,
+                                             _int, _vp, _vp, _int, _int, _f, _vp, _vp, _i64, _i64, _vp]),
+    "attnres_head_norm_rotate_axes_append": (_int, [_vp, _vp, _vp, _i64, _i64, _int, _int, _i64, _int, _i64, _i64,
+                                                    _i64, _vp, _vp, _vp, _int, _vp, _vp, _vp, _int, _int, _f, _vp,
+                                                    _i64, _vp, _vp, _i64, _int, _vp, _int, _vp]),
+    "attnres_head_norm_rotate_axes_backward": (_int, [_vp, _vp, _i64, _i64, _int, _int, _i64, _int, _i64, _i64, _vp,
+                                                      _vp, _vp, _int, _vp, _vp, _int, _int, _f, _vp, _vp, _i64, _i64,
+                                                      _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
     "attnres_paged_attention": (_int, [_vp, _i64, _vp, _vp, _i64, _int, _vp, _int, _vp, _i64, _int, _int, _i64, _int,
                                        _f, _vp, _vp, _vp, _i64, _vp]),
     "attnres_paged_attention_workspace_bytes": (_i64, [_int, _int, _i64, _int]),

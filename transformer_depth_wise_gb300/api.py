@@ -314,6 +314,92 @@ def rms_norm(x, weight, eps: float = 1e-6, out=None):
     return out
 
 
+def _rows_like(t, name: str, x):
+    """A contiguous tensor of x's type, shape and device (None stays None)."""
+    return _plain(t, name, x.dtype, x.shape, x.device)
+
+
+def _add_norm_args(x, residual, weight, sum_out):
+    """Checks shared by the two forms of the norm with the residual's addition; (B, T, D, sum_out)."""
+    _cuda(x, "x")
+    _code(x)
+    B, T, D = _btd(x)
+    _rows_like(residual, "residual", x)
+    _plain(weight, "weight", torch.float32, (D,), x.device)
+    if sum_out is None and residual is not None:
+        sum_out = torch.empty_like(x)
+    _rows_like(sum_out, "sum_out", x)
+    return B, T, D, sum_out
+
+
+def add_rms_norm(x, residual, weight=None, eps: float = 1e-6, sum_out=None, out=None):
+    """s = x + residual and y = s / sqrt(mean(s^2) + eps) (.) weight in one pass; returns (y, sum).
+
+    x, residual [B,T,D] or [rows,D]; residual None: s = x, and sum is None unless sum_out is given.  sum_out and out
+    may each be x or residual.
+    """
+    B, T, D, sum_out = _add_norm_args(x, residual, weight, sum_out)
+    if out is None:
+        out = torch.empty_like(x)
+    _rows_like(out, "out", x)
+    _call("attnres_add_rms_norm", x.device, x.data_ptr(), _ptr(residual), B, T, D, _CODES[x.dtype], _ptr(weight),
+          float(eps), _ptr(sum_out), out.data_ptr())
+    return out, sum_out
+
+
+def add_rms_norm_8bit(x, residual, weight=None, eps: float = 1e-6, group: int = 0, sum_out=None, out=None, scales=None):
+    """add_rms_norm with y in e4m3 and fp32 scales, one per `group` elements (32, 64, 128; 0: a row).
+
+    Returns (y8 float8_e4m3fn [..,D], scales [.., D/group] or [..], sum); y is y8 * scale.
+    """
+    B, T, D, sum_out = _add_norm_args(x, residual, weight, sum_out)
+    lead = x.shape[:-1]
+    if group and D % group:
+        raise ValueError(f"group must divide {D}")
+    shape = (*lead, D // group) if group else lead
+    if out is None:
+        out = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+    _plain(out, "out", torch.float8_e4m3fn, x.shape, x.device)
+    if scales is None:
+        scales = torch.empty(shape, dtype=torch.float32, device=x.device)
+    _plain(scales, "scales", torch.float32, shape, x.device)
+    _call("attnres_add_rms_norm_8bit", x.device, x.data_ptr(), _ptr(residual), B, T, D, _CODES[x.dtype], _ptr(weight),
+          float(eps), int(group), _ptr(sum_out), out.data_ptr(), scales.data_ptr())
+    return out, scales, sum_out
+
+
+def add_rms_norm_backward(s, weight, eps: float, grad_y, grad_sum=None, want_weight: bool = True, dx=None,
+                          workspace=None):
+    """Gradients of add_rms_norm at its sum s for the upstream grad_y and, when given, grad_sum.
+
+    Returns (dx, grad_weight [D] fp32 or None); dx is the gradient of x and of the residual alike, and may be s, grad_y
+    or grad_sum.  workspace: fp32 [rows, D] scratch (allocated when None).
+    """
+    _cuda(s, "s")
+    _code(s)
+    B, T, D = _btd(s)
+    dev = s.device
+    _plain(weight, "weight", torch.float32, (D,), dev)
+    _given(grad_y, "grad_y", s.dtype, s.shape, dev)
+    _rows_like(grad_sum, "grad_sum", s)
+    if dx is None:
+        dx = torch.empty_like(s)
+    _rows_like(dx, "dx", s)
+    gw, rows = None, 0
+    if want_weight:
+        gw = torch.empty(D, dtype=torch.float32, device=dev)
+        if workspace is None:
+            rows = min(_sized("attnres_add_rms_norm_backward_workspace_rows", dev), max(1, B * T))
+            workspace = torch.empty((rows, D), dtype=torch.float32, device=dev)
+        else:
+            rows = _f32(workspace, "workspace").numel() // D
+            if workspace.device != dev:
+                raise ValueError(f"workspace must be on {dev}")
+    _call("attnres_add_rms_norm_backward", dev, s.data_ptr(), B, T, D, _CODES[s.dtype], _ptr(weight), float(eps),
+          grad_y.data_ptr(), _ptr(grad_sum), dx.data_ptr(), _ptr(gw), _ptr(workspace) if want_weight else None, rows)
+    return dx, gw
+
+
 class TwoPhaseBlock:
     """One block of the two-phase Block scheme over preallocated buffers.
 
@@ -736,8 +822,27 @@ def rotary_frequencies(rot: int, base: float = 10000.0, device="cuda") -> torch.
     return base ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / max(rot, 1))
 
 
-def _norm_args(q, k, q_weight, k_weight, positions, inv_freq):
-    """Checks shared by the head norm's three calls; (B, T, Hq, Hk, d, q's and k's row strides, rot)."""
+def rotary_axes(sections, interleaved: bool = False, device="cuda") -> torch.Tensor:
+    """axes of head_norm_rotate, int32 [sum of sections]: sections[a] pairs turn with axis a.
+
+    The sections lie side by side, or with `interleaved` the axes take turns over the pairs until each has had its own.
+    """
+    left = [int(n) for n in sections]
+    if not 1 <= len(left) <= _lib.ATTNRES_MAX_AXES or min(left) < 0:
+        raise ValueError(f"sections must be 1 .. {_lib.ATTNRES_MAX_AXES} counts of pairs")
+    if not interleaved:
+        return torch.tensor([a for a, n in enumerate(left) for _ in range(n)], dtype=torch.int32, device=device)
+    order = []
+    while any(left):
+        turn = [a for a, n in enumerate(left) if n]
+        order += turn
+        for a in turn:
+            left[a] -= 1
+    return torch.tensor(order, dtype=torch.int32, device=device)
+
+
+def _norm_args(q, k, q_weight, k_weight, positions, inv_freq, axes=None, places=None):
+    """Checks shared by the head norm's three calls; (B, T, Hq, Hk, d, q's and k's row strides, rot, axes)."""
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be a [B, T, H, d] tensor")
     qs = _heads(q, "q")
@@ -749,24 +854,40 @@ def _norm_args(q, k, q_weight, k_weight, positions, inv_freq):
     dev = q.device
     _plain(q_weight, "q_weight", torch.float32, (d,), dev)
     _plain(k_weight, "k_weight", torch.float32, (d,), dev)
-    _plain(positions, "positions", torch.int32, (B, T), dev)
     rot = 0
     if inv_freq is not None:
         pairs = inv_freq.numel()
         rot = 2 * pairs
         _plain(inv_freq, "inv_freq", torch.float64, (pairs,), dev)
-    return B, T, Hq, Hk, d, qs, ks, rot
+    if axes is None:
+        _plain(positions, "positions", torch.int32, (B, T), dev)
+        num_axes = 0 if places is None else 1
+    else:
+        if inv_freq is None:
+            raise ValueError("axes go with inv_freq")
+        _plain(axes, "axes", torch.int32, (pairs,), dev)
+        if not isinstance(positions, torch.Tensor) or positions.dim() != 3:
+            raise ValueError("positions must be a [B, T, axes] tensor")
+        num_axes = positions.shape[2]
+        if not 1 <= num_axes <= _lib.ATTNRES_MAX_AXES:
+            raise ValueError(f"positions must have 1 .. {_lib.ATTNRES_MAX_AXES} axes")
+        _plain(positions, "positions", torch.int32, (B, T, num_axes), dev)
+    _plain(places, "places", torch.int32, (B, T), dev)
+    return B, T, Hq, Hk, d, qs, ks, rot, num_axes
 
 
 def head_norm_rotate(q, k, q_weight=None, k_weight=None, positions=None, inv_freq=None, eps: float = 1e-6,
-                     interleaved: bool = False, q_out=None, k_out=None):
+                     interleaved: bool = False, q_out=None, k_out=None, axes=None):
     """RMS norm of every query and key head and the position rotation, in one pass; returns (q_out, k_out).
 
     q [B,T,Hq,d], k [B,T,Hk,d]: contiguous, or views of one projection's output.  positions int32 [B,T]
     (None: 0 .. T-1), inv_freq float64 [rot/2] (rotary_frequencies; None: no rotation).  q_out / k_out may be q / k
     themselves, row on row, and overlap nothing else.
+
+    axes int32 [rot/2] (rotary_axes): positions have several axes, int32 [B,T,A], and pair i turns with positions[..,
+    axes[i]].
     """
-    B, T, Hq, Hk, d, qs, ks, rot = _norm_args(q, k, q_weight, k_weight, positions, inv_freq)
+    B, T, Hq, Hk, d, qs, ks, rot, num_axes = _norm_args(q, k, q_weight, k_weight, positions, inv_freq, axes)
     if q_out is None:
         q_out, qos = torch.empty((B, T, Hq, d), dtype=q.dtype, device=q.device), Hq * d
     else:
@@ -775,20 +896,27 @@ def head_norm_rotate(q, k, q_weight=None, k_weight=None, positions=None, inv_fre
         k_out, kos = torch.empty((B, T, Hk, d), dtype=q.dtype, device=q.device), Hk * d
     else:
         kos = _heads(k_out, "k_out", q, k.shape)
-    _call("attnres_head_norm_rotate", q.device, q.data_ptr(), k.data_ptr(), B, T, Hq, Hk, d, _CODES[q.dtype], qs, ks,
-          _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq), rot, 1 if interleaved else 0, float(eps),
-          q_out.data_ptr(), k_out.data_ptr(), qos, kos)
+    name, more = ("attnres_head_norm_rotate", ()) if axes is None else \
+        ("attnres_head_norm_rotate_axes", (num_axes, axes.data_ptr()))
+    _call(name, q.device, q.data_ptr(), k.data_ptr(), B, T, Hq, Hk, d, _CODES[q.dtype], qs, ks,
+          _ptr(q_weight), _ptr(k_weight), _ptr(positions), *more, _ptr(inv_freq), rot, 1 if interleaved else 0,
+          float(eps), q_out.data_ptr(), k_out.data_ptr(), qos, kos)
     return q_out, k_out
 
 
 def head_norm_rotate_append(q, k, v, q_weight, k_weight, positions, inv_freq, k_cache, v_cache, page_table,
-                            eps: float = 1e-6, interleaved: bool = False, q_out=None):
+                            eps: float = 1e-6, interleaved: bool = False, q_out=None, axes=None, places=None):
     """head_norm_rotate whose keys go into a paged cache with the values, at each token's position; returns q_out.
 
     k_cache, v_cache [num_pages, Hk, page_size, d]; page_table int32 [B, max_pages].  Tokens whose position has no
     page (negative, behind the table, a page number outside the pool) are not stored.
+
+    axes: as head_norm_rotate's.  places int32 [B,T]: the tokens' places in the cache where they are not their
+    positions; positions with axes need them.
     """
-    B, T, Hq, Hk, d, qs, ks, rot = _norm_args(q, k, q_weight, k_weight, positions, inv_freq)
+    if axes is not None and places is None:
+        raise ValueError("axes need places")
+    B, T, Hq, Hk, d, qs, ks, rot, num_axes = _norm_args(q, k, q_weight, k_weight, positions, inv_freq, axes, places)
     dev = q.device
     vs = _heads(v, "v", q, (B, T, Hk, d))
     num_pages, page_size, max_pages = _cache_args(k_cache, v_cache, page_table, q, B, Hk, d)
@@ -796,8 +924,10 @@ def head_norm_rotate_append(q, k, v, q_weight, k_weight, positions, inv_freq, k_
         q_out, qos = torch.empty((B, T, Hq, d), dtype=q.dtype, device=dev), Hq * d
     else:
         qos = _heads(q_out, "q_out", q, q.shape)
-    _call("attnres_head_norm_rotate_append", dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), B, T, Hq, Hk, d,
-          _CODES[q.dtype], qs, ks, vs, _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq), rot,
+    name, more = ("attnres_head_norm_rotate_append", ()) if places is None else \
+        ("attnres_head_norm_rotate_axes_append", (num_axes, _ptr(axes), places.data_ptr()))
+    _call(name, dev, q.data_ptr(), k.data_ptr(), v.data_ptr(), B, T, Hq, Hk, d,
+          _CODES[q.dtype], qs, ks, vs, _ptr(q_weight), _ptr(k_weight), _ptr(positions), *more, _ptr(inv_freq), rot,
           1 if interleaved else 0, float(eps), q_out.data_ptr(), qos, k_cache.data_ptr(), v_cache.data_ptr(),
           num_pages, page_size, page_table.data_ptr(), max_pages)
     return q_out
@@ -821,13 +951,13 @@ def _cache_args(k_cache, v_cache, page_table, q, B, Hk, d):
 
 
 def head_norm_rotate_backward(q, k, q_weight, k_weight, positions, inv_freq, eps: float, grad_q, grad_k,
-                              interleaved: bool = False, want_weights: bool = True, workspace=None):
+                              interleaved: bool = False, want_weights: bool = True, workspace=None, axes=None):
     """Gradients of head_norm_rotate for the upstream grad_q, grad_k.
 
     Returns (dq, dk, grad_q_weight [d] fp32, grad_k_weight [d] fp32); the last two are None without want_weights.
-    workspace: fp32 [rows, d] scratch (allocated when None).
+    workspace: fp32 [rows, d] scratch (allocated when None).  axes: as head_norm_rotate's.
     """
-    B, T, Hq, Hk, d, qs, ks, rot = _norm_args(q, k, q_weight, k_weight, positions, inv_freq)
+    B, T, Hq, Hk, d, qs, ks, rot, num_axes = _norm_args(q, k, q_weight, k_weight, positions, inv_freq, axes)
     dev = q.device
     gqs, gks = _heads(grad_q, "grad_q", q, q.shape), _heads(grad_k, "grad_k", q, k.shape)
     dq = torch.empty((B, T, Hq, d), dtype=q.dtype, device=dev)
@@ -844,8 +974,10 @@ def head_norm_rotate_backward(q, k, q_weight, k_weight, positions, inv_freq, eps
             rows = _f32(workspace, "workspace").numel() // d
             if workspace.device != dev:
                 raise ValueError(f"workspace must be on {dev}")
-    _call("attnres_head_norm_rotate_backward", dev, q.data_ptr(), k.data_ptr(), B, T, Hq, Hk, d, _CODES[q.dtype], qs,
-          ks, _ptr(q_weight), _ptr(k_weight), _ptr(positions), _ptr(inv_freq), rot, 1 if interleaved else 0,
+    name, more = ("attnres_head_norm_rotate_backward", ()) if axes is None else \
+        ("attnres_head_norm_rotate_axes_backward", (num_axes, axes.data_ptr()))
+    _call(name, dev, q.data_ptr(), k.data_ptr(), B, T, Hq, Hk, d, _CODES[q.dtype], qs,
+          ks, _ptr(q_weight), _ptr(k_weight), _ptr(positions), *more, _ptr(inv_freq), rot, 1 if interleaved else 0,
           float(eps), grad_q.data_ptr(), grad_k.data_ptr(), gqs, gks, dq.data_ptr(), dk.data_ptr(), _ptr(gw),
           _ptr(gkw), _ptr(workspace) if want_weights else None, rows)
     return dq, dk, gw, gkw

@@ -54,6 +54,33 @@ int check_eps(float eps) {
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? ATTNRES_OK : ATTNRES_ERR_CUDA; }
 
+// What both forms of the norm with the residual's addition check of their
+// common arguments.  sum and y may lie on x or residual (a thread reads its
+// vectors of a row before it writes them), but not on one another.
+int add_norm_args(const void *x, const void *residual, int64_t B, int64_t T, int64_t D, int dtype, const float *weight,
+                  float eps, void *sum_out, void *y, void *stream, AddNormArgs &a) {
+  int st = check_rows(B, T, D, dtype, a.rows);
+  if (st) return st;
+  if ((st = check_eps(eps))) return st;
+  if (!add_norm_supported(D, dtype)) return ATTNRES_ERR_SHAPE;
+  if (a.rows == 0) return ATTNRES_OK;
+  if (!x || !y) return ATTNRES_ERR_NULL;
+  if (!aligned16(x) || (residual && !aligned16(residual)) || (weight && !aligned16(weight)) ||
+      (sum_out && !aligned16(sum_out)) || !aligned16(y))
+    return ATTNRES_ERR_ALIGNMENT;
+  if (y == sum_out || (weight && (y == weight || sum_out == weight))) return ATTNRES_ERR_VALUE;
+  a.x = x;
+  a.residual = residual;
+  a.D = (int)D;
+  a.dtype = dtype;
+  a.weight = weight;
+  a.eps = eps;
+  a.sum_out = sum_out;
+  a.y = y;
+  a.stream = static_cast<cudaStream_t>(stream);
+  return ATTNRES_OK;
+}
+
 // The checks both backward entry points make on everything but the workspace;
 // rows receives B*T.  With no token rows, only the query and the parameter
 // gradients must be valid (the data pointers of empty tensors may be NULL).
@@ -208,6 +235,60 @@ int attnres_rms_norm(const void *x, int64_t B, int64_t T, int64_t D, int dtype, 
   if (!aligned16(x) || !aligned16(weight) || !aligned16(y)) return ATTNRES_ERR_ALIGNMENT;
   RmsNormArgs a{x, rows, (int)D, dtype, weight, eps, y, static_cast<cudaStream_t>(stream)};
   return cuda_status(launch_rms_norm(a));
+}
+
+int attnres_add_rms_norm(const void *x, const void *residual, int64_t B, int64_t T, int64_t D, int dtype,
+                         const float *weight, float eps, void *sum_out, void *y, void *stream) {
+  AddNormArgs a{};
+  int st = add_norm_args(x, residual, B, T, D, dtype, weight, eps, sum_out, y, stream, a);
+  if (st || a.rows == 0) return st;
+  return cuda_status(launch_add_norm(a));
+}
+
+int attnres_add_rms_norm_8bit(const void *x, const void *residual, int64_t B, int64_t T, int64_t D, int dtype,
+                              const float *weight, float eps, int group, void *sum_out, void *y8, float *scales,
+                              void *stream) {
+  if (group != 0 && group != 32 && group != 64 && group != 128) return ATTNRES_ERR_VALUE;
+  AddNormArgs a{};
+  int st = add_norm_args(x, residual, B, T, D, dtype, weight, eps, sum_out, y8, stream, a);
+  if (st) return st;
+  if (group && D % group) return ATTNRES_ERR_SHAPE;
+  if (a.rows == 0) return ATTNRES_OK;
+  if (!scales) return ATTNRES_ERR_NULL;
+  if (reinterpret_cast<uintptr_t>(scales) & 3u) return ATTNRES_ERR_ALIGNMENT;
+  const void *sc = scales;
+  if (y8 == x || y8 == residual || sc == x || sc == residual || sc == y8 || sc == sum_out || sc == weight)
+    return ATTNRES_ERR_VALUE;
+  a.bits8 = true;
+  a.group = group;
+  a.scales = scales;
+  return cuda_status(launch_add_norm(a));
+}
+
+int64_t attnres_add_rms_norm_backward_workspace_rows(void) { return add_norm_backward_ctas(); }
+
+int attnres_add_rms_norm_backward(const void *s, int64_t B, int64_t T, int64_t D, int dtype, const float *weight,
+                                  float eps, const void *grad_y, const void *grad_sum, void *dx, float *grad_weight,
+                                  float *workspace, int64_t workspace_rows, void *stream) {
+  int64_t rows = 0;
+  int st = check_rows(B, T, D, dtype, rows);
+  if (st) return st;
+  if ((st = check_eps(eps))) return st;
+  if (!add_norm_supported(D, dtype)) return ATTNRES_ERR_SHAPE;
+  if (grad_weight && !aligned16(grad_weight)) return ATTNRES_ERR_ALIGNMENT;
+  if (rows == 0)
+    return grad_weight ? cuda_status(cudaMemsetAsync(grad_weight, 0, (size_t)D * sizeof(float),
+                                                     static_cast<cudaStream_t>(stream)))
+                       : ATTNRES_OK;
+  if (!s || !grad_y || !dx || (grad_weight && !workspace)) return ATTNRES_ERR_NULL;
+  if (grad_weight && workspace_rows < 1) return ATTNRES_ERR_CAPACITY;
+  if (!aligned16(s) || !aligned16(grad_y) || (grad_sum && !aligned16(grad_sum)) || !aligned16(dx) ||
+      (weight && !aligned16(weight)) || (grad_weight && !aligned16(workspace)))
+    return ATTNRES_ERR_ALIGNMENT;
+  if (grad_weight && (grad_weight == weight || workspace == grad_weight)) return ATTNRES_ERR_VALUE;
+  AddNormBackwardArgs a{s, grad_y, grad_sum, rows, (int)D, dtype, weight, eps, dx, grad_weight,
+                        grad_weight ? workspace : nullptr, workspace_rows, static_cast<cudaStream_t>(stream)};
+  return cuda_status(launch_add_norm_backward(a));
 }
 
 int attnres_depth_aggregate_backward(const void *const *sources, int n, int64_t B, int64_t T, int64_t D,

@@ -86,26 +86,21 @@ int64_t backward_bytes(int64_t B, int64_t T, int H, int64_t dk, int64_t dv, int 
   return a > b ? a : b;
 }
 
-}  // namespace
-}  // namespace attnres
-
-using namespace attnres;
-
-extern "C" {
-
-int attnres_head_norm_rotate(const void *q, const void *k, int64_t B, int64_t T, int Hq, int Hk, int64_t d, int dtype,
-                             int64_t q_stride, int64_t k_stride, const float *q_weight, const float *k_weight,
-                             const int32_t *positions, const double *inv_freq, int rot, int interleaved, float eps,
-                             void *q_out, void *k_out, int64_t q_out_stride, int64_t k_out_stride, void *stream) {
+// The head norm's three calls, with num_axes 0 for positions of one number each (axes and places unused).
+int rotate(const void *q, const void *k, int64_t B, int64_t T, int Hq, int Hk, int64_t d, int dtype, int64_t q_stride,
+           int64_t k_stride, const float *q_weight, const float *k_weight, const int32_t *positions, int num_axes,
+           const int32_t *axes, const double *inv_freq, int rot, int interleaved, float eps, void *q_out, void *k_out,
+           int64_t q_out_stride, int64_t k_out_stride, void *stream) {
   int64_t rows = 0;
   int st = check_heads(B, T, Hq, Hk, d, dtype, q_stride, k_stride, rot, interleaved, eps, rows);
   if (st) return st;
   if ((st = check_stride(q_out_stride, Hq * d, dtype, true))) return st;
   if ((st = check_stride(k_out_stride, Hk * d, dtype, true))) return st;
   if (rows == 0) return ATTNRES_OK;
-  if (!q || !k || !q_out || !k_out || (rot && !inv_freq)) return ATTNRES_ERR_NULL;
+  if (!q || !k || !q_out || !k_out || (rot && !inv_freq) || (rot && num_axes > 1 && !positions))
+    return ATTNRES_ERR_NULL;
   if (!aligned16(q) || !aligned16(k) || !aligned16(q_out) || !aligned16(k_out) || misaligned(q_weight) ||
-      misaligned(k_weight) || misaligned(positions, 4) || misaligned(inv_freq, 8))
+      misaligned(k_weight) || misaligned(positions, 4) || misaligned(inv_freq, 8) || misaligned(axes, 4))
     return ATTNRES_ERR_ALIGNMENT;
   if (q_out == k || k_out == q || q_out == k_out || shifted(q_out, q_out_stride, q, q_stride, rows) ||
       shifted(k_out, k_out_stride, k, k_stride, rows))
@@ -114,17 +109,17 @@ int attnres_head_norm_rotate(const void *q, const void *k, int64_t B, int64_t T,
   a.q = q; a.k = k; a.q_stride = q_stride; a.k_stride = k_stride; a.rows = rows; a.T = T;
   a.Hq = Hq; a.Hk = Hk; a.d = (int)d; a.dtype = dtype; a.q_weight = q_weight; a.k_weight = k_weight;
   a.positions = positions; a.inv_freq = inv_freq; a.rot = rot; a.interleaved = interleaved; a.eps = eps;
+  a.num_axes = num_axes; a.axes = axes;
   a.q_out = q_out; a.k_out = k_out; a.q_out_stride = q_out_stride; a.k_out_stride = k_out_stride;
   a.stream = static_cast<cudaStream_t>(stream);
   return cuda_status(launch_head_norm(a));
 }
 
-int attnres_head_norm_rotate_append(const void *q, const void *k, const void *v, int64_t B, int64_t T, int Hq, int Hk,
-                                    int64_t d, int dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride,
-                                    const float *q_weight, const float *k_weight, const int32_t *positions,
-                                    const double *inv_freq, int rot, int interleaved, float eps, void *q_out,
-                                    int64_t q_out_stride, void *k_cache, void *v_cache, int64_t num_pages,
-                                    int page_size, const int32_t *page_table, int max_pages, void *stream) {
+int append(const void *q, const void *k, const void *v, int64_t B, int64_t T, int Hq, int Hk, int64_t d, int dtype,
+           int64_t q_stride, int64_t k_stride, int64_t v_stride, const float *q_weight, const float *k_weight,
+           const int32_t *positions, int num_axes, const int32_t *axes, const int32_t *places, const double *inv_freq,
+           int rot, int interleaved, float eps, void *q_out, int64_t q_out_stride, void *k_cache, void *v_cache,
+           int64_t num_pages, int page_size, const int32_t *page_table, int max_pages, void *stream) {
   int64_t rows = 0;
   int st = check_heads(B, T, Hq, Hk, d, dtype, q_stride, k_stride, rot, interleaved, eps, rows);
   if (st) return st;
@@ -133,11 +128,12 @@ int attnres_head_norm_rotate_append(const void *q, const void *k, const void *v,
   if ((st = check_pages(num_pages, page_size, max_pages))) return st;
   if (rows == 0) return ATTNRES_OK;
   const bool store = num_pages > 0 && max_pages > 0;
-  if (!q || !k || !v || !q_out || (rot && !inv_freq)) return ATTNRES_ERR_NULL;
+  if (!q || !k || !v || !q_out || (rot && !inv_freq) || (rot && num_axes > 1 && !positions) || (num_axes && !places))
+    return ATTNRES_ERR_NULL;
   if (store && (!k_cache || !v_cache || !page_table)) return ATTNRES_ERR_NULL;
   if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || misaligned(k_cache) ||
       misaligned(v_cache) || misaligned(q_weight) || misaligned(k_weight) || misaligned(positions, 4) ||
-      misaligned(inv_freq, 8) || misaligned(page_table, 4))
+      misaligned(inv_freq, 8) || misaligned(axes, 4) || misaligned(places, 4) || misaligned(page_table, 4))
     return ATTNRES_ERR_ALIGNMENT;
   if (q_out == k || q_out == v || shifted(q_out, q_out_stride, q, q_stride, rows)) return ATTNRES_ERR_VALUE;
   if (store && (k_cache == v_cache || among(k_cache, q, k, v, q_out) || among(v_cache, q, k, v, q_out)))
@@ -147,21 +143,19 @@ int attnres_head_norm_rotate_append(const void *q, const void *k, const void *v,
   a.rows = rows; a.T = T; a.Hq = Hq; a.Hk = Hk; a.d = (int)d; a.dtype = dtype;
   a.q_weight = q_weight; a.k_weight = k_weight; a.positions = positions; a.inv_freq = inv_freq; a.rot = rot;
   a.interleaved = interleaved; a.eps = eps; a.q_out = q_out; a.q_out_stride = q_out_stride;
+  a.num_axes = num_axes; a.axes = axes; a.places = places;
   a.k_out = k_cache; a.v_cache = v_cache; a.page_table = page_table; a.num_pages = num_pages;
   a.page_size = page_size; a.max_pages = store ? max_pages : 0;
   a.stream = static_cast<cudaStream_t>(stream);
   return cuda_status(launch_head_norm(a));
 }
 
-int64_t attnres_head_norm_rotate_backward_workspace_rows(void) { return 2 * (int64_t)head_norm_backward_ctas(); }
-
-int attnres_head_norm_rotate_backward(const void *q, const void *k, int64_t B, int64_t T, int Hq, int Hk, int64_t d,
-                                      int dtype, int64_t q_stride, int64_t k_stride, const float *q_weight,
-                                      const float *k_weight, const int32_t *positions, const double *inv_freq, int rot,
-                                      int interleaved, float eps, const void *grad_q, const void *grad_k,
-                                      int64_t grad_q_stride, int64_t grad_k_stride, void *dq, void *dk,
-                                      float *grad_q_weight, float *grad_k_weight, float *workspace,
-                                      int64_t workspace_rows, void *stream) {
+int rotate_backward(const void *q, const void *k, int64_t B, int64_t T, int Hq, int Hk, int64_t d, int dtype,
+                    int64_t q_stride, int64_t k_stride, const float *q_weight, const float *k_weight,
+                    const int32_t *positions, int num_axes, const int32_t *axes, const double *inv_freq, int rot,
+                    int interleaved, float eps, const void *grad_q, const void *grad_k, int64_t grad_q_stride,
+                    int64_t grad_k_stride, void *dq, void *dk, float *grad_q_weight, float *grad_k_weight,
+                    float *workspace, int64_t workspace_rows, void *stream) {
   int64_t rows = 0;
   int st = check_heads(B, T, Hq, Hk, d, dtype, q_stride, k_stride, rot, interleaved, eps, rows);
   if (st) return st;
@@ -176,11 +170,13 @@ int attnres_head_norm_rotate_backward(const void *q, const void *k, int64_t B, i
     if (e == cudaSuccess && grad_k_weight) e = cudaMemsetAsync(grad_k_weight, 0, (size_t)d * sizeof(float), s);
     return cuda_status(e);
   }
-  if (!q || !k || !grad_q || !grad_k || !dq || !dk || (rot && !inv_freq) || (weights && !workspace))
+  if (!q || !k || !grad_q || !grad_k || !dq || !dk || (rot && !inv_freq) || (rot && num_axes > 1 && !positions) ||
+      (weights && !workspace))
     return ATTNRES_ERR_NULL;
   if (weights && workspace_rows < 2) return ATTNRES_ERR_CAPACITY;
   if (!aligned16(q) || !aligned16(k) || !aligned16(grad_q) || !aligned16(grad_k) || !aligned16(dq) || !aligned16(dk) ||
-      misaligned(q_weight) || misaligned(k_weight) || misaligned(positions, 4) || misaligned(inv_freq, 8))
+      misaligned(q_weight) || misaligned(k_weight) || misaligned(positions, 4) || misaligned(inv_freq, 8) ||
+      misaligned(axes, 4))
     return ATTNRES_ERR_ALIGNMENT;
   if (dq == dk || among(dq, k, grad_k, nullptr) || among(dk, q, grad_q, nullptr) ||
       shifted(dq, Hq * d, q, q_stride, rows) || shifted(dq, Hq * d, grad_q, grad_q_stride, rows) ||
@@ -191,10 +187,89 @@ int attnres_head_norm_rotate_backward(const void *q, const void *k, int64_t B, i
   a.q_stride = q_stride; a.k_stride = k_stride; a.gq_stride = grad_q_stride; a.gk_stride = grad_k_stride;
   a.rows = rows; a.T = T; a.Hq = Hq; a.Hk = Hk; a.d = (int)d; a.dtype = dtype;
   a.q_weight = q_weight; a.k_weight = k_weight; a.positions = positions; a.inv_freq = inv_freq; a.rot = rot;
+  a.num_axes = num_axes; a.axes = axes;
   a.interleaved = interleaved; a.eps = eps; a.dq = dq; a.dk = dk;
   a.grad_q_weight = grad_q_weight; a.grad_k_weight = grad_k_weight;
   a.workspace = weights ? workspace : nullptr; a.workspace_rows = workspace_rows; a.stream = s;
   return cuda_status(launch_head_norm_backward(a));
+}
+
+}  // namespace
+}  // namespace attnres
+
+using namespace attnres;
+
+extern "C" {
+
+int attnres_head_norm_rotate(const void *q, const void *k, int64_t B, int64_t T, int Hq, int Hk, int64_t d, int dtype,
+                             int64_t q_stride, int64_t k_stride, const float *q_weight, const float *k_weight,
+                             const int32_t *positions, const double *inv_freq, int rot, int interleaved, float eps,
+                             void *q_out, void *k_out, int64_t q_out_stride, int64_t k_out_stride, void *stream) {
+  return rotate(q, k, B, T, Hq, Hk, d, dtype, q_stride, k_stride, q_weight, k_weight, positions, 0, nullptr, inv_freq,
+                rot, interleaved, eps, q_out, k_out, q_out_stride, k_out_stride, stream);
+}
+
+int attnres_head_norm_rotate_axes(const void *q, const void *k, int64_t B, int64_t T, int Hq, int Hk, int64_t d,
+                                  int dtype, int64_t q_stride, int64_t k_stride, const float *q_weight,
+                                  const float *k_weight, const int32_t *positions, int num_axes, const int32_t *axes,
+                                  const double *inv_freq, int rot, int interleaved, float eps, void *q_out,
+                                  void *k_out, int64_t q_out_stride, int64_t k_out_stride, void *stream) {
+  if (num_axes < 1 || num_axes > ATTNRES_MAX_AXES) return ATTNRES_ERR_SHAPE;
+  return rotate(q, k, B, T, Hq, Hk, d, dtype, q_stride, k_stride, q_weight, k_weight, positions, num_axes, axes,
+                inv_freq, rot, interleaved, eps, q_out, k_out, q_out_stride, k_out_stride, stream);
+}
+
+int attnres_head_norm_rotate_append(const void *q, const void *k, const void *v, int64_t B, int64_t T, int Hq, int Hk,
+                                    int64_t d, int dtype, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                                    const float *q_weight, const float *k_weight, const int32_t *positions,
+                                    const double *inv_freq, int rot, int interleaved, float eps, void *q_out,
+                                    int64_t q_out_stride, void *k_cache, void *v_cache, int64_t num_pages,
+                                    int page_size, const int32_t *page_table, int max_pages, void *stream) {
+  return append(q, k, v, B, T, Hq, Hk, d, dtype, q_stride, k_stride, v_stride, q_weight, k_weight, positions, 0, nullptr,
+                nullptr, inv_freq, rot, interleaved, eps, q_out, q_out_stride, k_cache, v_cache, num_pages, page_size,
+                page_table, max_pages, stream);
+}
+
+int attnres_head_norm_rotate_axes_append(const void *q, const void *k, const void *v, int64_t B, int64_t T, int Hq,
+                                         int Hk, int64_t d, int dtype, int64_t q_stride, int64_t k_stride,
+                                         int64_t v_stride, const float *q_weight, const float *k_weight,
+                                         const int32_t *positions, int num_axes, const int32_t *axes,
+                                         const int32_t *places, const double *inv_freq, int rot, int interleaved,
+                                         float eps, void *q_out, int64_t q_out_stride, void *k_cache, void *v_cache,
+                                         int64_t num_pages, int page_size, const int32_t *page_table, int max_pages,
+                                         void *stream) {
+  if (num_axes < 1 || num_axes > ATTNRES_MAX_AXES) return ATTNRES_ERR_SHAPE;
+  return append(q, k, v, B, T, Hq, Hk, d, dtype, q_stride, k_stride, v_stride, q_weight, k_weight, positions, num_axes,
+                axes, places, inv_freq, rot, interleaved, eps, q_out, q_out_stride, k_cache, v_cache, num_pages,
+                page_size, page_table, max_pages, stream);
+}
+
+int64_t attnres_head_norm_rotate_backward_workspace_rows(void) { return 2 * (int64_t)head_norm_backward_ctas(); }
+
+int attnres_head_norm_rotate_backward(const void *q, const void *k, int64_t B, int64_t T, int Hq, int Hk, int64_t d,
+                                      int dtype, int64_t q_stride, int64_t k_stride, const float *q_weight,
+                                      const float *k_weight, const int32_t *positions, const double *inv_freq, int rot,
+                                      int interleaved, float eps, const void *grad_q, const void *grad_k,
+                                      int64_t grad_q_stride, int64_t grad_k_stride, void *dq, void *dk,
+                                      float *grad_q_weight, float *grad_k_weight, float *workspace,
+                                      int64_t workspace_rows, void *stream) {
+  return rotate_backward(q, k, B, T, Hq, Hk, d, dtype, q_stride, k_stride, q_weight, k_weight, positions, 0, nullptr,
+                         inv_freq, rot, interleaved, eps, grad_q, grad_k, grad_q_stride, grad_k_stride, dq, dk,
+                         grad_q_weight, grad_k_weight, workspace, workspace_rows, stream);
+}
+
+int attnres_head_norm_rotate_axes_backward(const void *q, const void *k, int64_t B, int64_t T, int Hq, int Hk,
+                                           int64_t d, int dtype, int64_t q_stride, int64_t k_stride,
+                                           const float *q_weight, const float *k_weight, const int32_t *positions,
+                                           int num_axes, const int32_t *axes, const double *inv_freq, int rot,
+                                           int interleaved, float eps, const void *grad_q, const void *grad_k,
+                                           int64_t grad_q_stride, int64_t grad_k_stride, void *dq, void *dk,
+                                           float *grad_q_weight, float *grad_k_weight, float *workspace,
+                                           int64_t workspace_rows, void *stream) {
+  if (num_axes < 1 || num_axes > ATTNRES_MAX_AXES) return ATTNRES_ERR_SHAPE;
+  return rotate_backward(q, k, B, T, Hq, Hk, d, dtype, q_stride, k_stride, q_weight, k_weight, positions, num_axes,
+                         axes, inv_freq, rot, interleaved, eps, grad_q, grad_k, grad_q_stride, grad_k_stride, dq, dk,
+                         grad_q_weight, grad_k_weight, workspace, workspace_rows, stream);
 }
 
 int64_t attnres_paged_attention_workspace_bytes(int Hq, int Hk, int64_t d, int dtype) {

@@ -1,0 +1,460 @@
+// add_norm.cu -- RMS norm with the residual's addition, its form with an
+// output in 8 bits, and its backward pass.
+//
+// Per token row, with s = x + residual in fp32:  sum = s rounded once,
+// y = s r w, r = (mean s^2 + eps)^(-1/2), rounded once to the row's type, or
+// in e4m3 with one fp32 scale per group of a row's elements (or per row):
+// scale = max|y| / 448 over the group, y8 = y / scale.
+// Backward at the stored sum s:  u = grad_y w,  dx = grad_sum + r (u - s r^2
+// mean(u s)),  grad_weight = sum over rows of grad_y s r.
+//
+// Memory binds: every tensor passes once.  A thread holds the same vectors of
+// each of its team's rows (a CTA per row, or 8 or 32 lanes for narrow rows);
+// the next row's loads are issued before the present row's reduction, so that
+// the reduction's barriers leave no gap in the loads.
+#include <type_traits>
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace attnres {
+namespace {
+
+constexpr float kTop = 448.f;              // the largest e4m3 value
+constexpr float kLeast = 0x1p-126f;        // the smallest scale: its reciprocal is finite
+
+enum Mode { kPlain, kGroups, kRow8 };      // y in the row's type, in e4m3 by groups, in e4m3 by rows
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// A vector from pairs of fp32 values, rounded to the element type.
+template <typename T>
+__device__ __forceinline__ uint4 from_pairs(const uint64_t *x) {
+  constexpr int NP = Pairs<T>::NP;
+  float f[2 * NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) unpair(x[i], f[2 * i], f[2 * i + 1]);
+  return Elt<T>::pack(f);
+}
+
+// Four values in e4m3, to nearest even, held within +-448; NaN stays NaN.
+__device__ __forceinline__ uint32_t to_e4m3(uint64_t a, uint64_t b) {
+  float f[4];
+  unpair(a, f[0], f[1]);
+  unpair(b, f[2], f[3]);
+  uint16_t lo, hi;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(f[1]), "f"(f[0]));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(f[3]), "f"(f[2]));
+  return (uint32_t)hi << 16 | lo;
+}
+
+// |x|'s bits: as unsigned numbers they are ordered like the values, with NaN
+// above infinity, so their maximum keeps a NaN.
+__device__ __forceinline__ uint32_t magnitude(uint64_t x) {
+  const uint32_t lo = (uint32_t)x & 0x7fffffffu, hi = (uint32_t)(x >> 32) & 0x7fffffffu;
+  return lo > hi ? lo : hi;
+}
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// The scale of a group with this largest magnitude (a NaN gives NaN).
+__device__ __forceinline__ float scale_of(uint32_t top) {
+  const float s = __uint_as_float(top) / kTop;
+  return s < kLeast ? kLeast : s;
+}
+
+template <typename T>
+__device__ __forceinline__ void load_weight(uint64_t *w, const float *src) {
+#pragma unroll
+  for (int i = 0; i < Pairs<T>::NP; i += 2) {
+    const float4 a = src ? ld_f4(src + 2 * i) : make_float4(1.f, 1.f, 1.f, 1.f);
+    w[i] = pair(a.x, a.y);
+    w[i + 1] = pair(a.z, a.w);
+  }
+}
+
+struct AddNormParams {
+  const void *x, *residual;                // residual: nullptr for none
+  void *sum, *y;                           // sum: nullptr if not wanted; y: the row's type or bytes
+  float *scales;                           // [rows, D / group] or [rows]
+  const float *w;                          // [D] or nullptr
+  int64_t rows;
+  int nvec, lanes;                         // vectors of a row; lanes of a group (kGroups)
+  float inv_D, eps;
+};
+
+template <typename T, int VPT, int TEAM, int MODE>
+__global__ void __launch_bounds__(TEAM ? 256 : 512) add_norm_kernel(const AddNormParams p) {
+  constexpr int EPV = Elt<T>::EPV, NP = Pairs<T>::NP;
+  __shared__ float red[TEAM ? 1 : 2 * 32];
+  __shared__ uint32_t top_red[TEAM || MODE != kRow8 ? 1 : 2 * 32];
+  grid_dependency_wait();
+  const int tpr = TEAM ? TEAM : blockDim.x, lt = TEAM ? threadIdx.x % TEAM : threadIdx.x;
+  const int teams = TEAM ? blockDim.x / TEAM : 1, team = TEAM ? threadIdx.x / TEAM : 0;
+  const int64_t steps = (p.rows + teams - 1) / teams;
+  const char *x = (const char *)p.x, *res = (const char *)p.residual;
+  uint4 xv[VPT], rv[VPT];
+  auto load = [&](int64_t step) {
+    const int64_t row = step * teams + team;
+    const int64_t at = (row * p.nvec + lt) * 16;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      xv[k] = rv[k] = make_uint4(0, 0, 0, 0);
+      if (row < p.rows && lt + k * tpr < p.nvec) {
+        xv[k] = *reinterpret_cast<const uint4 *>(x + at + (int64_t)k * tpr * 16);
+        if (res) rv[k] = *reinterpret_cast<const uint4 *>(res + at + (int64_t)k * tpr * 16);
+      }
+    }
+  };
+  int parity = 0;
+  if (blockIdx.x < steps) load(blockIdx.x);
+  for (int64_t step = blockIdx.x; step < steps; step += gridDim.x) {
+    const int64_t row = step * teams + team;
+    uint64_t s[VPT * NP], sq = 0;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      uint64_t b[NP];
+      Pairs<T>::split(xv[k], s + k * NP);
+      Pairs<T>::split(rv[k], b);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        if (res) s[k * NP + i] = add2(s[k * NP + i], b[i]);
+        fma_pair(sq, s[k * NP + i], s[k * NP + i]);
+      }
+    }
+    if (step + gridDim.x < steps) load(step + gridDim.x);
+    float ss = pair_sum(sq);
+    if (TEAM) {
+      ss = team_sum_shfl<TEAM ? TEAM : 1>(ss);
+    } else {
+      float v[1] = {ss};
+      cta_sum<1>(v, red, parity);
+      ss = v[0];
+    }
+    const float r = rsqrtf(fmaf(ss, p.inv_D, p.eps));
+    const uint64_t r2 = pair(r, r);
+    uint32_t top = 0;
+    const bool row_ok = row < p.rows;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int j = lt + k * tpr;
+      const bool live = row_ok && j < p.nvec;
+      const int64_t at = (row * p.nvec + j) * 16;
+      uint64_t *v = s + k * NP;
+      if (live && p.sum) st_vec((char *)p.sum + at, from_pairs<T>(v));
+      uint64_t w[NP];
+      if (live) load_weight<T>(w, p.w ? p.w + (int64_t)j * EPV : nullptr);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) v[i] = live ? mul2(mul2(v[i], r2), w[i]) : 0ull;
+      if (MODE == kPlain) {
+        if (live) st_vec((char *)p.y + at, from_pairs<T>(v));
+        continue;
+      }
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) m = larger(m, magnitude(v[i]));
+      if (MODE == kRow8) {
+        top = larger(top, m);
+        continue;
+      }
+      for (int o = p.lanes / 2; o > 0; o >>= 1) m = larger(m, __shfl_xor_sync(0xffffffffu, m, o));
+      if (!live) continue;
+      const float scale = scale_of(m), inv = 1.f / scale;
+      const uint64_t inv2 = pair(inv, inv);
+      uint32_t q[NP / 2];
+#pragma unroll
+      for (int i = 0; i < NP; i += 2) q[i / 2] = to_e4m3(mul2(v[i], inv2), mul2(v[i + 1], inv2));
+      char *y = (char *)p.y + (row * p.nvec + j) * EPV;
+      if constexpr (NP == 4) *reinterpret_cast<uint2 *>(y) = make_uint2(q[0], q[1]);
+      else *reinterpret_cast<uint32_t *>(y) = q[0];
+      if (j % p.lanes == 0) p.scales[row * (p.nvec / p.lanes) + j / p.lanes] = scale;
+    }
+    if (MODE == kRow8) {
+      if (TEAM) {
+#pragma unroll
+        for (int o = TEAM / 2; o > 0; o >>= 1) top = larger(top, __shfl_xor_sync(0xffffffffu, top, o));
+      } else {
+        top = __reduce_max_sync(0xffffffffu, top);
+        uint32_t *slot = top_red + parity * 32;
+        if (threadIdx.x % 32 == 0) slot[threadIdx.x / 32] = top;
+        __syncthreads();
+        for (int i = 0; i < (int)(blockDim.x / 32); ++i) top = larger(top, slot[i]);
+      }
+      const float scale = scale_of(top), inv = 1.f / scale;
+      const uint64_t inv2 = pair(inv, inv);
+#pragma unroll
+      for (int k = 0; k < VPT; ++k) {
+        const int j = lt + k * tpr;
+        if (!row_ok || j >= p.nvec) continue;
+        const uint64_t *v = s + k * NP;
+        uint32_t q[NP / 2];
+#pragma unroll
+        for (int i = 0; i < NP; i += 2) q[i / 2] = to_e4m3(mul2(v[i], inv2), mul2(v[i + 1], inv2));
+        char *y = (char *)p.y + (row * p.nvec + j) * EPV;
+        if constexpr (NP == 4) *reinterpret_cast<uint2 *>(y) = make_uint2(q[0], q[1]);
+        else *reinterpret_cast<uint32_t *>(y) = q[0];
+      }
+      if (row_ok && lt == 0) p.scales[row] = scale;
+    }
+    parity ^= 1;
+  }
+}
+
+struct AddNormBackwardParams {
+  const void *s, *gy, *gs;                 // gs: nullptr for none
+  void *dx;
+  const float *w;                          // [D] or nullptr
+  float *partials;                         // [gridDim.x][D] or nullptr
+  int64_t rows;
+  int nvec;
+  float inv_D, eps;
+};
+
+template <typename T, int VPT, int TEAM>
+__global__ void __launch_bounds__(TEAM ? 256 : 512) add_norm_backward_kernel(const AddNormBackwardParams p) {
+  constexpr int EPV = Elt<T>::EPV, NP = Pairs<T>::NP;
+  __shared__ float red[TEAM ? 1 : 2 * 32 * 2];
+  extern __shared__ float team_dw[];       // TEAM: [teams][VPT * TEAM * EPV]
+  grid_dependency_wait();
+  const int tpr = TEAM ? TEAM : blockDim.x, lt = TEAM ? threadIdx.x % TEAM : threadIdx.x;
+  const int teams = TEAM ? blockDim.x / TEAM : 1, team = TEAM ? threadIdx.x / TEAM : 0;
+  const int64_t steps = (p.rows + teams - 1) / teams;
+  const char *sp = (const char *)p.s, *gp = (const char *)p.gy, *rp = (const char *)p.gs;
+  uint4 sv[VPT], gv[VPT], rv[VPT];
+  auto load = [&](int64_t step) {
+    const int64_t row = step * teams + team;
+    const int64_t at = (row * p.nvec + lt) * 16;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      sv[k] = gv[k] = rv[k] = make_uint4(0, 0, 0, 0);
+      if (row < p.rows && lt + k * tpr < p.nvec) {
+        sv[k] = *reinterpret_cast<const uint4 *>(sp + at + (int64_t)k * tpr * 16);
+        gv[k] = *reinterpret_cast<const uint4 *>(gp + at + (int64_t)k * tpr * 16);
+        if (rp) rv[k] = *reinterpret_cast<const uint4 *>(rp + at + (int64_t)k * tpr * 16);
+      }
+    }
+  };
+  uint64_t dw[VPT * NP];
+#pragma unroll
+  for (int i = 0; i < VPT * NP; ++i) dw[i] = 0;
+  int parity = 0;
+  if (blockIdx.x < steps) load(blockIdx.x);
+  for (int64_t step = blockIdx.x; step < steps; step += gridDim.x) {
+    const int64_t row = step * teams + team;
+    uint64_t s[VPT * NP], g[VPT * NP], sq = 0, dot = 0;
+    uint4 gs[VPT];
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int j = lt + k * tpr;
+      uint64_t w[NP];
+      Pairs<T>::split(sv[k], s + k * NP);
+      Pairs<T>::split(gv[k], g + k * NP);
+      gs[k] = rv[k];
+#pragma unroll
+      for (int i = 0; i < NP; ++i) w[i] = 0;
+      if (j < p.nvec) load_weight<T>(w, p.w ? p.w + (int64_t)j * EPV : nullptr);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const uint64_t a = s[k * NP + i];
+        fma_pair(sq, a, a);
+        fma_pair(dot, mul2(g[k * NP + i], w[i]), a);
+      }
+    }
+    if (step + gridDim.x < steps) load(step + gridDim.x);
+    float ss = pair_sum(sq), us = pair_sum(dot);
+    if (TEAM) {
+      ss = team_sum_shfl<TEAM ? TEAM : 1>(ss);
+      us = team_sum_shfl<TEAM ? TEAM : 1>(us);
+    } else {
+      float v[2] = {ss, us};
+      cta_sum<2>(v, red, parity);
+      parity ^= 1;
+      ss = v[0];
+      us = v[1];
+    }
+    if (row >= p.rows) continue;
+    const float r = rsqrtf(fmaf(ss, p.inv_D, p.eps)), rc = -us * p.inv_D * r * r * r;
+    const uint64_t r2 = pair(r, r), rc2 = pair(rc, rc);
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int j = lt + k * tpr;
+      if (j >= p.nvec) continue;
+      uint64_t w[NP], b[NP];
+      load_weight<T>(w, p.w ? p.w + (int64_t)j * EPV : nullptr);
+      Pairs<T>::split(gs[k], b);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const uint64_t a = s[k * NP + i], gr = mul2(g[k * NP + i], r2);
+        fma_pair(dw[k * NP + i], gr, a);
+        b[i] = fma2(a, rc2, fma2(gr, w[i], b[i]));
+      }
+      st_vec((char *)p.dx + (row * p.nvec + j) * 16, from_pairs<T>(b));
+    }
+  }
+  if (!p.partials) return;
+  float *out = p.partials + (int64_t)blockIdx.x * p.nvec * EPV;
+  if (TEAM) {
+    // the teams' sums, in a fixed order
+    const int D = p.nvec * EPV;
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int j = lt + k * tpr;
+      if (j >= p.nvec) continue;
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+        *reinterpret_cast<uint64_t *>(team_dw + team * D + j * EPV + 2 * i) = dw[k * NP + i];
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < D; i += blockDim.x) {
+      float sum = 0.f;
+      for (int t = 0; t < teams; ++t) sum += team_dw[t * D + i];
+      out[i] = sum;
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < VPT; ++k) {
+      const int j = lt + k * tpr;
+      if (j >= p.nvec) continue;
+#pragma unroll
+      for (int i = 0; i < NP; i += 2) {
+        float4 f;
+        unpair(dw[k * NP + i], f.x, f.y);
+        unpair(dw[k * NP + i + 1], f.z, f.w);
+        *reinterpret_cast<float4 *>(out + (int64_t)j * EPV + 2 * i) = f;
+      }
+    }
+  }
+}
+
+// The weight's gradient: the CTAs' sums added in a fixed order, eight strands
+// of every eighth CTA per column, 32 columns per CTA.
+__global__ void __launch_bounds__(256) add_norm_weight_kernel(const float *partials, int ctas, int D, float *dw) {
+  __shared__ float red[8][33];
+  grid_dependency_wait();
+  const int col = blockIdx.x * 32 + threadIdx.x % 32, strand = threadIdx.x / 32;
+  float s = 0.f;
+  if (col < D)
+    for (int c = strand; c < ctas; c += 8) s += partials[(int64_t)c * D + col];
+  red[strand][threadIdx.x % 32] = s;
+  __syncthreads();
+  if (strand == 0 && col < D) {
+    s = 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) s += red[k][threadIdx.x];
+    dw[col] = s;
+  }
+}
+
+// Most shared memory of the backward's teams: 32 rows of 128 elements, 8 of 512.
+constexpr size_t kTeamBytes = 16384;
+
+// Lanes of a row (0: a CTA's), vectors per thread and the CTA's threads for
+// rows of nvec vectors; `whole`: no less than a warp per row.
+struct RowShape {
+  int team, vpt, threads;
+};
+RowShape shape_of(int nvec, bool whole) {
+  if (nvec <= 16 && !whole) return {8, 2, 256};
+  if (nvec <= 64) return {32, 2, 256};
+  const int vpt = nvec <= 1024 ? 2 : 4;
+  return {0, vpt, ((nvec + vpt - 1) / vpt + 31) / 32 * 32};
+}
+
+// CTAs of `kern` that an SM holds (with the most shared memory it takes),
+// asked once per device and CTA size.
+template <auto kern>
+int resident(int threads, size_t smem) {
+  static int known[16][17] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  int &n = known[dev & 15][threads / 32];
+  if (n == 0 && (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem) != cudaSuccess || n < 1)) n = 1;
+  return n;
+}
+
+// Call f with the vectors per thread and the lanes of a row as types.
+template <bool WHOLE, typename F>
+cudaError_t with_shape(const RowShape &s, F f) {
+  using I2 = std::integral_constant<int, 2>;
+  if constexpr (!WHOLE)
+    if (s.team == 8) return f(I2{}, std::integral_constant<int, 8>{});
+  if (s.team == 32) return f(I2{}, std::integral_constant<int, 32>{});
+  if (s.vpt == 2) return f(I2{}, std::integral_constant<int, 0>{});
+  return f(std::integral_constant<int, 4>{}, std::integral_constant<int, 0>{});
+}
+
+template <typename T, int MODE>
+cudaError_t forward(const AddNormArgs &a, const AddNormParams &p) {
+  const RowShape s = shape_of(p.nvec, MODE != kPlain);
+  return with_shape<MODE != kPlain>(s, [&](auto vpt, auto team) -> cudaError_t {
+    constexpr int TEAM = decltype(team)::value;
+    constexpr auto kern = add_norm_kernel<T, decltype(vpt)::value, TEAM, MODE>;
+    const int teams = TEAM ? s.threads / (TEAM ? TEAM : 1) : 1;
+    const int64_t steps = (p.rows + teams - 1) / teams, most = (int64_t)resident<kern>(s.threads, 0) * sm_count();
+    return launch_dependent(kern, dim3((unsigned)(steps < most ? steps : most)), dim3(s.threads), 0, a.stream, p);
+  });
+}
+
+template <typename T>
+cudaError_t forward(const AddNormArgs &a, const AddNormParams &p) {
+  return !a.bits8 ? forward<T, kPlain>(a, p) : a.group ? forward<T, kGroups>(a, p) : forward<T, kRow8>(a, p);
+}
+
+int elements(int dtype) { return dtype == ATTNRES_BF16 ? 8 : 4; }
+
+}  // namespace
+
+bool add_norm_supported(int64_t D, int dtype) { return D / elements(dtype) <= 2048; }
+
+cudaError_t launch_add_norm(const AddNormArgs &a) {
+  AddNormParams p{};
+  p.x = a.x; p.residual = a.residual; p.sum = a.sum_out; p.y = a.y; p.scales = a.scales; p.w = a.weight;
+  p.rows = a.rows; p.nvec = a.D / elements(a.dtype); p.lanes = a.group / elements(a.dtype);
+  p.inv_D = 1.f / (float)a.D; p.eps = a.eps;
+  return a.dtype == ATTNRES_BF16 ? forward<__nv_bfloat16>(a, p) : forward<float>(a, p);
+}
+
+// Each CTA leaves one row of partial sums.
+int add_norm_backward_ctas() { return 4 * sm_count(); }
+
+cudaError_t launch_add_norm_backward(const AddNormBackwardArgs &a) {
+  AddNormBackwardParams p{};
+  p.s = a.s; p.gy = a.grad_y; p.gs = a.grad_sum; p.dx = a.dx; p.w = a.weight; p.partials = a.workspace;
+  p.rows = a.rows; p.nvec = a.D / elements(a.dtype); p.inv_D = 1.f / (float)a.D; p.eps = a.eps;
+  const RowShape s = shape_of(p.nvec, false);
+  int ctas = 0;
+  auto go = [&](auto elt) -> cudaError_t {
+    using T = decltype(elt);
+    return with_shape<false>(s, [&](auto vpt, auto team) -> cudaError_t {
+      constexpr int TEAM = decltype(team)::value;
+      constexpr auto kern = add_norm_backward_kernel<T, decltype(vpt)::value, TEAM>;
+      const int teams = TEAM ? s.threads / (TEAM ? TEAM : 1) : 1;
+      const size_t smem = TEAM && p.partials ? (size_t)teams * a.D * sizeof(float) : 0;
+      int64_t most = (int64_t)resident<kern>(s.threads, TEAM ? kTeamBytes : 0) * sm_count();
+      if (most > add_norm_backward_ctas()) most = add_norm_backward_ctas();
+      if (p.partials && most > a.workspace_rows) most = a.workspace_rows;
+      const int64_t steps = (p.rows + teams - 1) / teams;
+      ctas = (int)(steps < most ? steps : most);
+      return launch_dependent(kern, dim3((unsigned)ctas), dim3(s.threads), smem, a.stream, p);
+    });
+  };
+  cudaError_t e = a.dtype == ATTNRES_BF16 ? go(__nv_bfloat16{}) : go(float{});
+  if (e != cudaSuccess || !a.workspace) return e;
+  return launch_dependent(add_norm_weight_kernel, dim3((unsigned)((a.D + 31) / 32)), dim3(256), 0, a.stream,
+                          (const float *)a.workspace, ctas, a.D, a.grad_weight);
+}
+
+}  // namespace attnres

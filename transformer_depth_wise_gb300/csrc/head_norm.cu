@@ -29,7 +29,10 @@
 // nothing: the angle is off by the rounding of inv_freq / 2 pi in 64 bits and
 // by 2^-25 of half a turn when its upper 32 bits become an fp32 argument.
 // The fraction is formed in integers (the mantissa times 2^66 / 2 pi), since
-// fp64 instructions are slow on this GPU.
+// fp64 instructions are slow on this GPU.  With several axes a token has one
+// position on each (time, height, width), and axes[i] says which of them turns
+// pair i: a row's positions are read by the lanes, one each, and handed to the
+// pairs by shuffles, so the rotation costs what it does with one axis.
 #include <type_traits>
 
 #include "common.cuh"
@@ -155,25 +158,51 @@ __device__ __forceinline__ void load_weight(uint64_t *w, const float *src, int o
 
 // The frequencies' steps, once per CTA; then each warp forms its rows' angles
 // from them.
+template <bool AXES>
 struct Angles {
   const uint64_t *steps;             // [rot / 2]
   float *c, *s;                      // cosines and sines [rot / 2], the warp's own
+  const uint8_t *axis;               // AXES: [rot / 2]
   int n;
-  __device__ __forceinline__ Angles(char *smem, const double *inv_freq, int rot) {
+  __device__ __forceinline__ Angles(char *smem, const double *inv_freq, int rot, const int32_t *axes, int num_axes) {
     n = rot / 2;                     // a multiple of 4
     uint64_t *st = reinterpret_cast<uint64_t *>(smem);
-    for (int i = threadIdx.x; i < n; i += kThreads) st[i] = turn_step(inv_freq[i]);
+    uint8_t *ax = reinterpret_cast<uint8_t *>(st + n * (1 + kWarps));
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      uint64_t step = turn_step(inv_freq[i]);
+      if (AXES) {                    // a pair of no axis is not turned
+        const int a = axes ? axes[i] : 0;
+        const bool in = a >= 0 && a < num_axes;
+        if (!in) step = 0;
+        ax[i] = in ? (uint8_t)a : 0;
+      }
+      st[i] = step;
+    }
     steps = st;
+    axis = ax;
     c = reinterpret_cast<float *>(st + n) + threadIdx.x / 32 * 2 * n;
     s = c + n;
     __syncthreads();
   }
+  // `position`: the row's; with AXES the lane's axis' (lanes 0 .. num_axes - 1).
   __device__ __forceinline__ void form(int position) const {
     __syncwarp();                    // the last row's are read
-    for (int i = threadIdx.x % 32; i < n; i += 32) {
-      const float2 cs = turned(steps[i], position);
-      c[i] = cs.x;
-      s[i] = cs.y;
+    if (AXES) {
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        const int i = i0 + threadIdx.x % 32;
+        const int at = __shfl_sync(0xffffffffu, position, i < n ? axis[i] : 0);
+        if (i < n) {
+          const float2 cs = turned(steps[i], at);
+          c[i] = cs.x;
+          s[i] = cs.y;
+        }
+      }
+    } else {
+      for (int i = threadIdx.x % 32; i < n; i += 32) {
+        const float2 cs = turned(steps[i], position);
+        c[i] = cs.x;
+        s[i] = cs.y;
+      }
     }
     __syncwarp();
   }
@@ -186,15 +215,29 @@ struct Angles {
       sines[i] = y.x; sines[i + 1] = y.y; sines[i + 2] = y.z; sines[i + 3] = y.w;
     }
   }
-  static size_t bytes(int rot) { return (size_t)(rot / 2) * 8 * (1 + kWarps); }
+  // A multiple of 16 where `rot` is one.
+  static __host__ __device__ size_t bytes(int rot) {
+    return (size_t)(rot / 2) * 8 * (1 + kWarps) + (AXES ? (size_t)(rot / 2 + 15) / 16 * 16 : 0);
+  }
 };
+
+// What a lane reads of a row's positions: the row's only one, or its own axis'.
+template <bool AXES>
+__device__ __forceinline__ int position_of(const int32_t *positions, int64_t row, int64_t T, int num_axes) {
+  if (!positions) return (int)(row % T);
+  if (!AXES) return positions[row];
+  return positions[row * num_axes + min((int)threadIdx.x % 32, num_axes - 1)];
+}
 
 struct HeadParams {
   const void *q, *k, *v;
   void *q_out, *k_out, *v_out;       // k_out, v_out: the caches when page > 0
   int64_t q_stride, k_stride, v_stride, qo_stride, ko_stride;   // elements from one token row to the next
   const float *wq, *wk;
-  const int32_t *positions;          // [rows] or nullptr: the row's index in its sequence
+  const int32_t *positions;          // [rows, num_axes] or nullptr: the row's index in its sequence
+  const int32_t *axes;               // [rot / 2]: the axis of each pair, or nullptr: all on the first
+  const int32_t *places;             // [rows]: places in the cache, AXES only
+  int num_axes;
   const double *inv_freq;
   const int32_t *table;              // [B, max_pages]
   int64_t rows, T;
@@ -205,14 +248,14 @@ struct HeadParams {
   float eps, inv_d;
 };
 
-template <typename T, int TEAM, bool INTER, bool CACHE>
+template <typename T, int TEAM, bool INTER, bool CACHE, bool AXES>
 __global__ void __launch_bounds__(kThreads, 2) head_norm_kernel(const HeadParams p) {
   constexpr int E = Elt<T>::EPV, NP = Pairs<T>::NP;
   constexpr int kTeams = 32 / TEAM;              // of a warp
   constexpr int kFlight = 4;                     // heads in flight per team
   extern __shared__ char smem[];
   grid_dependency_wait();
-  const Angles ang(smem, p.inv_freq, p.rot);
+  const Angles<AXES> ang(smem, p.inv_freq, p.rot, p.axes, p.num_axes);
   const int lane = threadIdx.x % TEAM, team = threadIdx.x % 32 / TEAM;
   const bool active = lane * 2 * E < p.d;
   const Unit<T, INTER> u(lane, p.rot);
@@ -222,13 +265,14 @@ __global__ void __launch_bounds__(kThreads, 2) head_norm_kernel(const HeadParams
   for (int64_t item = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32; item < items; item += stride) {
     const int64_t row = p.parts == 1 ? item : item / p.parts;
     const int from = p.parts == 1 ? 0 : (int)(item - row * p.parts) * p.per_part, to = min(heads, from + p.per_part);
-    const int position = p.positions ? p.positions[row] : (int)(row % p.T);
-    // A row without a place in the cache (a negative position, one behind the
+    const int position = position_of<AXES>(p.positions, row, p.T, p.num_axes);
+    const int place = CACHE && AXES ? p.places[row] : position;
+    // A row without a place in the cache (a negative one, one behind the
     // table, a page outside the pool) is rotated but not stored.
     int64_t slot = -1;
-    if (CACHE && position >= 0 && position / p.page < p.max_pages) {
-      const int64_t pg = p.table[row / p.T * p.max_pages + position / p.page];
-      if (pg >= 0 && pg < p.num_pages) slot = (pg * p.Hk * p.page + position % p.page) * p.d;
+    if (CACHE && place >= 0 && place / p.page < p.max_pages) {
+      const int64_t pg = p.table[row / p.T * p.max_pages + place / p.page];
+      if (pg >= 0 && pg < p.num_pages) slot = (pg * p.Hk * p.page + place % p.page) * p.d;
     }
     bool formed = false;
     // The queries', then the keys' heads.
@@ -311,7 +355,8 @@ struct HeadBackwardParams {
   int64_t stride[2], gstride[2];
   const float *w[2];
   float *partials;                   // [gridDim.x][2][d] or nullptr
-  const int32_t *positions;
+  const int32_t *positions, *axes;   // as in HeadParams
+  int num_axes;
   const double *inv_freq;
   int64_t rows, T;
   int H[2], d, rot;
@@ -319,14 +364,14 @@ struct HeadBackwardParams {
   float eps, inv_d;
 };
 
-template <typename T, int TEAM, bool INTER>
+template <typename T, int TEAM, bool INTER, bool AXES>
 __global__ void __launch_bounds__(kThreads, 2) head_norm_backward_kernel(const HeadBackwardParams p) {
   constexpr int E = Elt<T>::EPV, NP = Pairs<T>::NP;
   constexpr int kTeams = 32 / TEAM;
   constexpr int kFlight = kBackFlight;
   extern __shared__ char smem[];
   grid_dependency_wait();
-  const Angles ang(smem, p.inv_freq, p.rot);
+  const Angles<AXES> ang(smem, p.inv_freq, p.rot, p.axes, p.num_axes);
   const int lane = threadIdx.x % TEAM, team = threadIdx.x % 32 / TEAM;
   const bool active = lane * 2 * E < p.d;
   const Unit<T, INTER> u(lane, p.rot);
@@ -344,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 2) head_norm_backward_kernel(const H
     for (int64_t item = (int64_t)blockIdx.x * kWarps + threadIdx.x / 32; item < p.rows * parts; item += stride) {
       const int64_t row = parts == 1 ? item : item / parts;
       const int h0 = parts == 1 ? 0 : (int)(item - row * parts) * p.per_part[which], h1 = min(H, h0 + p.per_part[which]);
-      const int position = p.positions ? p.positions[row] : (int)(row % p.T);
+      const int position = position_of<AXES>(p.positions, row, p.T, p.num_axes);
       const T *x0 = (const T *)p.x[which] + row * p.stride[which];
       const T *g0 = (const T *)p.g[which] + row * p.gstride[which];
       T *y0 = (T *)p.dx[which] + row * H * p.d;
@@ -402,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 2) head_norm_backward_kernel(const H
     if (!p.partials) continue;
     // The CTA's sums: over the teams of a warp by shuffles, over the warps
     // through shared memory in a fixed order (reproducible).
-    float *red = reinterpret_cast<float *>(smem) + p.rot / 2 * 2 * (1 + kWarps);   // [warps][d], behind the angles
+    float *red = reinterpret_cast<float *>(smem + Angles<AXES>::bytes(p.rot));   // [warps][d], behind the angles
 #pragma unroll
     for (int i = 0; i < 2 * NP; ++i) {
       float lo, hi;
@@ -453,15 +498,19 @@ int row_parts(int64_t rows, int heads, int round, int64_t want, int &per_part) {
   return (heads + per_part - 1) / per_part;
 }
 
-// Call f with the element type, the lanes per head and the pairing as types.
+// Call f with the element type, the lanes per head, the pairing and whether
+// positions have axes as types.
 template <typename F>
-cudaError_t dispatch(int dtype, int d, int interleaved, F f) {
+cudaError_t dispatch(int dtype, int d, int interleaved, int num_axes, F f) {
   const int units = d / (dtype == ATTNRES_BF16 ? 16 : 8);
+  auto with_axes = [&](auto elt, auto team, auto inter) -> cudaError_t {
+    return num_axes > 0 ? f(elt, team, inter, std::true_type{}) : f(elt, team, inter, std::false_type{});
+  };
   auto with_team = [&](auto elt, auto inter) -> cudaError_t {
-    if (units <= 4) return f(elt, std::integral_constant<int, 4>{}, inter);
-    if (units <= 8) return f(elt, std::integral_constant<int, 8>{}, inter);
-    if (units <= 16) return f(elt, std::integral_constant<int, 16>{}, inter);
-    return f(elt, std::integral_constant<int, 32>{}, inter);
+    if (units <= 4) return with_axes(elt, std::integral_constant<int, 4>{}, inter);
+    if (units <= 8) return with_axes(elt, std::integral_constant<int, 8>{}, inter);
+    if (units <= 16) return with_axes(elt, std::integral_constant<int, 16>{}, inter);
+    return with_axes(elt, std::integral_constant<int, 32>{}, inter);
   };
   auto with_pairs = [&](auto elt) -> cudaError_t {
     return interleaved ? with_team(elt, std::true_type{}) : with_team(elt, std::false_type{});
@@ -484,15 +533,16 @@ cudaError_t launch_head_norm(const HeadNormArgs &a) {
   p.qo_stride = a.q_out_stride; p.ko_stride = a.k_out_stride;
   p.wq = a.q_weight; p.wk = a.k_weight;
   p.positions = a.positions; p.inv_freq = a.inv_freq; p.table = a.page_table;
+  p.axes = a.axes; p.places = a.places; p.num_axes = a.num_axes;
   p.rows = a.rows; p.T = a.T; p.Hq = a.Hq; p.Hk = a.Hk; p.d = a.d; p.rot = a.rot;
   p.num_pages = a.num_pages; p.page = a.page_size; p.max_pages = a.max_pages;
   p.eps = a.eps; p.inv_d = 1.f / (float)a.d;
   const bool cache = a.page_size > 0;
   const int sms = sm_count();
-  return dispatch(a.dtype, a.d, a.interleaved, [&](auto elt, auto team, auto inter) -> cudaError_t {
+  return dispatch(a.dtype, a.d, a.interleaved, a.num_axes, [&](auto elt, auto team, auto inter, auto axes) -> cudaError_t {
     using T = decltype(elt);
     constexpr int TEAM = decltype(team)::value;
-    constexpr bool INTER = decltype(inter)::value;
+    constexpr bool INTER = decltype(inter)::value, AXES = decltype(axes)::value;
     // A row per work item, cut into parts of no less than one round of a
     // warp's teams where the rows alone would not give every SM eight warps.
     // Measured, 32 + 8 heads of 128, cut against whole rows: 1 to 64 rows 4.0 against 7.4
@@ -502,9 +552,9 @@ cudaError_t launch_head_norm(const HeadNormArgs &a) {
     p.parts = row_parts(a.rows, heads, 32 / TEAM, 8 * (int64_t)sms, p.per_part);
     const int64_t ctas = (a.rows * p.parts + kWarps - 1) / kWarps, most = (int64_t)sms * 8;
     const dim3 grid((unsigned)(ctas < most ? ctas : most));
-    const size_t smem = Angles::bytes(a.rot);
-    return cache ? launch_dependent(head_norm_kernel<T, TEAM, INTER, true>, grid, dim3(kThreads), smem, a.stream, p)
-                 : launch_dependent(head_norm_kernel<T, TEAM, INTER, false>, grid, dim3(kThreads), smem, a.stream, p);
+    const size_t smem = Angles<AXES>::bytes(a.rot);
+    return cache ? launch_dependent(head_norm_kernel<T, TEAM, INTER, true, AXES>, grid, dim3(kThreads), smem, a.stream, p)
+                 : launch_dependent(head_norm_kernel<T, TEAM, INTER, false, AXES>, grid, dim3(kThreads), smem, a.stream, p);
   });
 }
 
@@ -518,13 +568,13 @@ cudaError_t launch_head_norm_backward(const HeadNormBackwardArgs &a) {
   p.gstride[0] = a.gq_stride; p.gstride[1] = a.gk_stride;
   p.w[0] = a.q_weight; p.w[1] = a.k_weight;
   p.partials = a.workspace;
-  p.positions = a.positions; p.inv_freq = a.inv_freq;
+  p.positions = a.positions; p.inv_freq = a.inv_freq; p.axes = a.axes; p.num_axes = a.num_axes;
   p.rows = a.rows; p.T = a.T; p.H[0] = a.Hq; p.H[1] = a.Hk; p.d = a.d; p.rot = a.rot;
   p.eps = a.eps; p.inv_d = 1.f / (float)a.d;
   const int limit = a.workspace && a.workspace_rows / 2 < head_norm_backward_ctas() ? (int)(a.workspace_rows / 2)
                                                                                 : head_norm_backward_ctas();
   int ctas = 0;
-  cudaError_t e = dispatch(a.dtype, a.d, a.interleaved, [&](auto elt, auto team, auto inter) -> cudaError_t {
+  cudaError_t e = dispatch(a.dtype, a.d, a.interleaved, a.num_axes, [&](auto elt, auto team, auto inter, auto axes) -> cudaError_t {
     using T = decltype(elt);
     constexpr int TEAM = decltype(team)::value;
     // The parts with the least work for the busiest warp.  An item costs its
@@ -550,8 +600,9 @@ cudaError_t launch_head_norm_backward(const HeadNormBackwardArgs &a) {
     }
     const int64_t want = (most + kWarps - 1) / kWarps;
     ctas = (int)(want < limit ? want : limit);
-    const size_t smem = Angles::bytes(a.rot) + (size_t)kWarps * a.d * sizeof(float);
-    return launch_dependent(head_norm_backward_kernel<T, TEAM, decltype(inter)::value>, dim3((unsigned)ctas),
+    constexpr bool AXES = decltype(axes)::value;
+    const size_t smem = Angles<AXES>::bytes(a.rot) + (size_t)kWarps * a.d * sizeof(float);
+    return launch_dependent(head_norm_backward_kernel<T, TEAM, decltype(inter)::value, AXES>, dim3((unsigned)ctas),
                             dim3(kThreads), smem, a.stream, p);
   });
   if (e != cudaSuccess || !a.workspace) return e;

@@ -176,13 +176,47 @@ struct Phase1ManyArgs {
 bool phase1_many_supported(int n, int D, int dtype, int S, int64_t rows);
 cudaError_t launch_phase1_many(const Phase1ManyArgs &a);
 
+struct AddNormArgs {
+  const void *x, *residual;    // [rows, D]; residual may be nullptr
+  int64_t rows;
+  int D, dtype;
+  const float *weight;         // [D] or nullptr
+  float eps;
+  void *sum_out;               // [rows, D] or nullptr
+  void *y;                     // [rows, D], of the type, or e4m3 with bits8
+  bool bits8;
+  int group;                   // elements per scale (0: a row)
+  float *scales;
+  cudaStream_t stream;
+};
+bool add_norm_supported(int64_t D, int dtype);
+cudaError_t launch_add_norm(const AddNormArgs &a);
+
+struct AddNormBackwardArgs {
+  const void *s, *grad_y, *grad_sum;   // [rows, D]; grad_sum may be nullptr
+  int64_t rows;
+  int D, dtype;
+  const float *weight;
+  float eps;
+  void *dx;                    // [rows, D]
+  float *grad_weight;          // [D], with a workspace
+  float *workspace;            // [workspace_rows, D], nullptr without a weight gradient
+  int64_t workspace_rows;      // one per CTA
+  cudaStream_t stream;
+};
+int add_norm_backward_ctas();  // the most CTAs of a launch on the current device
+cudaError_t launch_add_norm_backward(const AddNormBackwardArgs &a);
+
 struct HeadNormArgs {
   const void *q, *k, *v;       // [rows, Hq, d], [rows, Hk, d]; v only into a cache
   int64_t q_stride, k_stride, v_stride;
   int64_t rows, T;             // rows = B * T
   int Hq, Hk, d, dtype;
   const float *q_weight, *k_weight;    // [d] or nullptr
-  const int32_t *positions;    // [rows] or nullptr (0 .. T - 1)
+  const int32_t *positions;    // [rows], with axes [rows, num_axes], or nullptr (0 .. T - 1)
+  int num_axes;                // 0: positions without axes
+  const int32_t *axes;         // [rot / 2] the axis of each pair, or nullptr (the first); num_axes > 0
+  const int32_t *places;       // [rows] places in the cache, with axes and a cache
   const double *inv_freq;      // [rot / 2]
   int rot, interleaved;
   float eps;
@@ -204,6 +238,8 @@ struct HeadNormBackwardArgs {
   int Hq, Hk, d, dtype;
   const float *q_weight, *k_weight;
   const int32_t *positions;
+  int num_axes;                // as in HeadNormArgs
+  const int32_t *axes;
   const double *inv_freq;
   int rot, interleaved;
   float eps;
