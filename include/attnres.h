@@ -477,6 +477,36 @@ int attnres_paged_attention(const void *q, int64_t q_stride, const void *k_cache
 int64_t attnres_paged_attention_workspace_bytes(int Hq, int Hk, int64_t d, int dtype);
 
 /*
+ * The same for a batch whose sequences share a prefix in the cache (a system
+ * prompt, a document that many questions are about): the prefix's tokens are
+ * worked on once for all sequences, as matrix products with the queries of the
+ * whole batch, and joined (OS2) with each sequence's own tokens, which follow.
+ *   prefix_table   device int32 [prefix_pages]: the prefix's pages, as a row
+ *                  of page_table; page_size * prefix_pages at most 2^30
+ *   prefix_length  device int32 [1]: tokens of the prefix, taken as 0 if
+ *                  negative and at most prefix_pages * page_size; it need not
+ *                  end with a page (NULL allowed if prefix_pages is 0)
+ *   page_table, max_pages, lengths: the sequences' own pages and tokens, the
+ *                  first of them on a page of their own; a sequence may have none
+ *   q, k_cache, v_cache, out, lse, scale: as there
+ *   workspace      device, attnres_shared_prefix_attention_workspace_bytes()
+ *                  bytes; its contents on entry do not matter.  Two calls that
+ *                  may overlap need one each.
+ * The prefix's weights enter the product with the values as bf16 (bf16, heads
+ * of up to 128 elements; sums and maxima in fp32).  An empty prefix is allowed;
+ * a sequence without any token gives zeros and lse = -infinity.  Pages outside
+ * [0, num_pages) are left out, and NaN and infinities show, as there.
+ */
+int attnres_shared_prefix_attention(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
+                                    int64_t num_pages, int page_size, const int32_t *prefix_table, int prefix_pages,
+                                    const int32_t *prefix_length, const int32_t *page_table, int max_pages,
+                                    const int32_t *lengths, int64_t B, int Hq, int Hk, int64_t d, int dtype, float scale,
+                                    void *out, float *lse, void *workspace, int64_t workspace_bytes, void *stream);
+/* Its workspace bytes on the current device: they depend on what the prefix's table covers, not on the lengths. */
+int64_t attnres_shared_prefix_attention_workspace_bytes(int64_t B, int Hq, int Hk, int64_t d, int dtype, int page_size,
+                                                        int prefix_pages);
+
+/*
  * Linear attention with one fixed decay per head, over prompts.  (It is not
  * the gated delta rule: nothing of the state is taken back, and the decay is
  * a constant without a gradient.)

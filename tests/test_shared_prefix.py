@@ -1,0 +1,415 @@
+"""Attention of one new token per sequence behind a shared prefix, against a plain float64 form, and a serving layer's
+operators in a row.
+
+Tolerances are bounds, not fits.  u is the rounding of a stored result (half a step: 2^-8 relative for bf16, 2^-24 for
+fp32); every other term counts the roundings on the way, as the comment at each check says (E = 2^-24).
+"""
+import math
+
+import pytest
+import torch
+
+from transformer_depth_wise_gb300 import _lib, api
+from transformer_depth_wise_gb300 import workloads as wk
+
+gpu_only = pytest.mark.gpu
+BF, F32 = torch.bfloat16, torch.float32
+U = {BF: 2.0 ** -8, F32: 2.0 ** -24}
+E = 2.0 ** -24
+FAKE = 0x7F0000000000      # 16-byte aligned stand-in for a device pointer (never dereferenced)
+OK, NULL, SHAPE, DTYPE, ALIGN, CAP, VALUE = 0, -1, -2, -3, -4, -7, -8
+
+
+def cpu(t):
+    return t.detach().cpu().double()
+
+
+def within(got, want, tol, what=""):
+    got, want = cpu(got), want.double()
+    assert got.shape == want.shape, (what, got.shape, want.shape)
+    fine = torch.isfinite(want)
+    assert torch.equal(fine, torch.isfinite(got)), f"{what}: finite in different places"
+    assert torch.equal(got[~fine & ~want.isnan()], want[~fine & ~want.isnan()]), what
+    d = torch.where(fine, (got - want).abs() - tol, torch.full_like(want, -1.0))
+    assert d.numel() == 0 or float(d.max()) <= 0.0, f"{what}: over the bound by {float(d.max()):.3e}"
+
+
+def rand(g, *shape, dtype=BF, scale=1.0):
+    return (torch.empty(shape, dtype=F32, device=g.device).normal_(generator=g) * scale).to(dtype)
+
+
+def tokens_of(table, n, page, pool):
+    """Pages and slots of the first n tokens of a table's row, those on pages outside the pool left out."""
+    j = torch.arange(min(max(int(n), 0), table.numel() * page))
+    pg = table.cpu().long()[j // page] if len(j) else j
+    ok = (pg >= 0) & (pg < pool)
+    return pg[ok], (j % page)[ok]
+
+
+def shared_ref(q, kc, vc, prefix_table, prefix, table, lengths, scale, coarse):
+    """(out, lse, bound on out's error before its last rounding, the same of lse) in float64; `coarse`: the rounding of
+    the prefix's weights on their way into the product with the values."""
+    q, kc, vc = cpu(q), cpu(kc), cpu(vc)
+    B, Hq, d = q.shape
+    N, Hk, page, _ = kc.shape
+    G = Hq // Hk
+    out, lse = torch.zeros_like(q), torch.full((B, Hq), -math.inf, dtype=torch.float64)
+    tol, ltol = torch.zeros_like(q), torch.zeros(B, Hq, dtype=torch.float64)
+    fp, fs = tokens_of(prefix_table, int(prefix), page, N)
+    for hk in range(Hk):
+        kp, vp = kc[fp, hk, fs], vc[fp, hk, fs]
+        for b in range(B):
+            op, os_ = tokens_of(table[b], int(lengths[b]), page, N)
+            k, v = torch.cat((kp, kc[op, hk, os_])), torch.cat((vp, vc[op, hk, os_]))
+            n, h = len(k), slice(hk * G, hk * G + G)
+            if n == 0:
+                continue
+            qh = q[b, h]
+            s = qh @ k.T * scale
+            p = torch.softmax(s, -1)
+            out[b, h], lse[b, h] = p @ v, torch.logsumexp(s, -1)
+            # a score is a sum of d products: d roundings of its absolute sum; the exponential's argument and value
+            # 16 E + |s - max| E, once more at the join; sums over n tokens in at least eight strands; the own tokens'
+            # weights enter the second product with 16 bits or more (2^-17), the prefix's with `coarse`
+            ds = (d + 2) * E * (qh.abs() @ k.abs().T).amax(-1) * abs(scale)
+            ds = ds + 4 * E * (s.amax(-1) - s.amin(-1)) + (32 + n / 8) * E
+            tol[b, h] = (2 * ds[:, None] + 2.0 ** -17) * (p @ v.abs()) + coarse * (p[:, :len(kp)] @ vp.abs())
+            ltol[b, h] = ds + 2 * E * lse[b, h].abs()
+    return out, lse, tol, ltol
+
+
+def inputs(dev, dtype, Hq, Hk, d, page, prefix, lengths, seed, spare=0):
+    g = wk.generator(seed, dev)
+    B = len(lengths)
+    first, per = -(-prefix // page) + spare, max(1, -(-max(lengths) // page)) + spare
+    pool = first + B * per + 1
+    pages = torch.randperm(first + B * per, device=dev, generator=g).int()
+    q = rand(g, B, Hq, d, dtype=dtype, scale=1.5)
+    kc, vc = rand(g, pool, Hk, page, d, dtype=dtype), rand(g, pool, Hk, page, d, dtype=dtype)
+    return [q, kc, vc, pages[:first].contiguous(), torch.tensor([prefix], device=dev).int(),
+            pages[first:].view(B, per).contiguous(), torch.tensor(lengths, device=dev).int(), 1 / math.sqrt(d)]
+
+
+def coarse_of(dtype, d):
+    return 2.0 ** -8 if dtype is BF and d <= 128 else 0.0
+
+
+def check(args, dtype, d, what=""):
+    out, lse = api.shared_prefix_attention(*args)
+    want, wlse, tol, ltol = shared_ref(*args, coarse_of(dtype, d))
+    within(out, want, U[dtype] * want.abs() + tol, what + " out")
+    within(lse, wlse, ltol, what + " lse")
+    again = api.shared_prefix_attention(*args)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    return out, lse
+
+
+CASES = [  # dtype, Hq, Hk, d, page, prefix, lengths
+    (BF, 1, 1, 128, 16, 1, [1]), (BF, 16, 16, 128, 16, 1111, [0, 100, 37, 1]), (BF, 8, 2, 64, 32, 127, [5, 0, 31]),
+    (BF, 56, 8, 128, 64, 1000, [0, 1, 63, 64, 65, 300]), (BF, 16, 1, 128, 64, 129, list(range(17))),
+    (BF, 32, 2, 64, 16, 700, [i % 5 for i in range(40)]), (BF, 6, 2, 96, 16, 257, [3, 200]),
+    (BF, 4, 4, 80, 8, 90, [9, 1]), (BF, 8, 2, 256, 64, 300, [70, 5]), (BF, 3, 1, 8, 1, 33, [2]),
+    (BF, 9, 1, 128, 128, 384, [3, 0, 7]), (BF, 10, 2, 128, 7, 500, [10, 50]), (BF, 2, 2, 192, 3, 65, [3, 65]),
+    (BF, 14, 2, 128, 16, 2049, [1] * 37), (BF, 2, 1, 40, 16, 1030, [4] * 130), (BF, 4, 2, 128, 64, 20000, [20, 1]),
+    (BF, 7, 1, 128, 32, 128, [6] * 300), (F32, 4, 4, 64, 16, 70, [0, 300]), (F32, 6, 3, 128, 16, 333, [65, 0, 3]),
+    (F32, 3, 3, 256, 8, 77, [5]), (F32, 8, 2, 64, 32, 1025, [7] * 33), (F32, 7, 1, 128, 32, 513, [1] * 19),
+    (F32, 2, 1, 4, 1, 9, [1]), (F32, 12, 4, 100, 5, 64, [64, 1]), (F32, 16, 1, 192, 64, 200, [1] * 9),
+]
+
+
+@gpu_only
+@pytest.mark.parametrize("dtype,Hq,Hk,d,page,prefix,lengths", CASES)
+def test_shared(gpu, dtype, Hq, Hk, d, page, prefix, lengths):
+    check(inputs(gpu, dtype, Hq, Hk, d, page, prefix, lengths, prefix + d), dtype, d)
+
+
+@gpu_only
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("prefix,lengths", [(0, [5, 0, 17]), (0, [0, 0]), (200, [0, 0, 0]), (1, [0]), (64, [64, 1])])
+def test_empty_parts(gpu, dtype, prefix, lengths):
+    # tables that cover more than the lengths say, a prefix of no tokens with a table and without one
+    a = inputs(gpu, dtype, 8, 2, 64, 16, prefix, lengths, 3, spare=2)
+    out, lse = check(a, dtype, 64)
+    if prefix == 0:
+        a[3] = a[3][:0].contiguous()
+        none = api.shared_prefix_attention(*a)
+        alone = api.paged_attention(a[0], a[1], a[2], a[5], a[6], a[7])
+        assert torch.equal(none[0], out)
+        within(none[0], cpu(alone[0]), 2 * U[dtype] * cpu(alone[0]).abs())
+        within(none[1], cpu(alone[1]), 4 * E * cpu(alone[1]).abs().clamp_min(1))
+    a[5] = a[5][:, :0].contiguous()                  # no own pages at all
+    a[6] = a[6] * 0
+    check(a, dtype, 64)
+    a[4] = a[4] * 0 - 5                              # lengths below zero and behind the tables
+    a[6] = a[6] - 1
+    out, lse = check(a, dtype, 64)
+    assert not bool(out.any()) and bool((lse == -math.inf).all())
+    if a[3].numel():
+        a[4] = a[4] * 0 + 10 ** 6
+        check(a, dtype, 64)
+
+
+@gpu_only
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 256), (F32, 64)])
+def test_one_cache_or_two(gpu, dtype, d):
+    # a prefix of whole pages in front of each sequence's own table is the same attention
+    q, kc, vc, pt, n, t, lengths, scale = inputs(gpu, dtype, 8, 2, d, 16, 160, [0, 1, 16, 100, 33], 5)
+    out, lse = api.shared_prefix_attention(q, kc, vc, pt, n, t, lengths, scale)
+    whole = torch.cat((pt.expand(5, -1), t), 1).contiguous()
+    want, wlse = api.paged_attention(q, kc, vc, whole, lengths + 160, scale)
+    _, _, tol, ltol = shared_ref(q, kc, vc, pt, n, t, lengths, scale, coarse_of(dtype, d))
+    within(out, cpu(want), 2 * U[dtype] * cpu(want).abs() + 2 * tol)
+    within(lse, cpu(wlse), 2 * ltol)
+
+
+@gpu_only
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (BF, 256), (F32, 64)])
+def test_unused_cache_and_bad_pages(gpu, dtype, d):
+    a = inputs(gpu, dtype, 6, 2, d, 16, 300, [33, 0, 5, 47], 7)
+    q, kc, vc, pt, n, t, lengths, _ = a
+    pt[3], pt[7], t[0, 1] = -1, kc.shape[0], kc.shape[0] + 5        # pages outside the pool are left out
+    used = torch.zeros(kc.shape[0], 16, dtype=torch.bool)
+    for table, count in ((pt, 300), *((t[b], int(lengths[b])) for b in range(4))):
+        pg, sl = tokens_of(table, count, 16, kc.shape[0])
+        used[pg, sl] = True
+    want = api.shared_prefix_attention(*a)
+    check(a, dtype, d)
+    for fill in (math.nan, math.inf, -math.inf):
+        mask = (~used).to(gpu)[:, None, :, None]
+        kc.masked_fill_(mask, fill)
+        vc.masked_fill_(mask, fill)
+        got = api.shared_prefix_attention(*a)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    pt.fill_(-1)                                                     # nothing of the prefix is left
+    kc, vc = kc.nan_to_num(0.5, 0.5, 0.5), vc.nan_to_num(0.5, 0.5, 0.5)
+    check([q, kc, vc, *a[3:]], dtype, d)
+
+
+@gpu_only
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (BF, 256), (F32, 64)])
+def test_what_is_no_number(gpu, dtype, d):
+    a = inputs(gpu, dtype, 8, 2, d, 16, 400, [20, 3, 0], 9)
+    q, kc, vc, pt, _, t, _, _ = a
+    k0, v0, want = kc.clone(), vc.clone(), api.shared_prefix_attention(*a)
+
+    def reset():
+        kc.copy_(k0)
+        vc.copy_(v0)
+
+    heads = torch.arange(8, device=gpu) // 4 == 1
+    kc[pt[12], 1, 3, 2] = math.nan                                   # a key of the prefix: its key head's queries, all rows
+    out, lse = api.shared_prefix_attention(*a)
+    assert torch.equal(lse.isnan(), heads.expand(3, 8)) and torch.equal(out.isnan().all(-1), heads.expand(3, 8))
+    assert torch.equal(out[:, :4], want[0][:, :4])
+    reset()
+    vc[pt[5], 0, 7, 9] = math.nan                                    # a value: one element of its head's queries
+    out, lse = api.shared_prefix_attention(*a)
+    bad = torch.zeros(3, 8, d, dtype=torch.bool, device=gpu)
+    bad[:, :4, 9] = True
+    assert torch.equal(out.isnan(), bad) and torch.equal(lse, want[1])
+    reset()
+    vc[pt[5], 0, 7, 9] = math.inf
+    out, lse = api.shared_prefix_attention(*a)
+    assert torch.equal(~out.isfinite(), bad) and torch.equal(lse, want[1])
+    reset()
+    q0 = q.clone()
+    q[1, 3, 0] = math.nan                                            # a query: its row alone
+    out, lse = api.shared_prefix_attention(*a)
+    bad = torch.zeros(3, 8, dtype=torch.bool, device=gpu)
+    bad[1, 3] = True
+    assert torch.equal(lse.isnan(), bad) and torch.equal(out.isnan().all(-1), bad) and torch.equal(out.isnan().any(-1), bad)
+    q.copy_(q0)
+    kc[t[0, 0], 0, 2, 1] = math.nan                                  # an own key: its sequence alone
+    out, lse = api.shared_prefix_attention(*a)
+    bad = torch.zeros(3, 8, dtype=torch.bool, device=gpu)
+    bad[0, :4] = True
+    assert torch.equal(lse.isnan(), bad) and torch.equal(out[1:], want[0][1:])
+    reset()
+    q[:, :, :] = q.abs() + 0.1                                       # keys at minus infinity take no part
+    gone = torch.arange(0, 400, 3)
+    kc[pt.cpu().long()[gone // 16], :, gone % 16] = -math.inf
+    out, lse = api.shared_prefix_attention(*a)
+    kept = torch.ones(400, dtype=torch.bool)
+    kept[gone] = False
+    reset()
+    pages, slots = pt.cpu().long()[torch.arange(400) // 16][kept], (torch.arange(400) % 16)[kept]
+    for b in range(3):
+        op, os_ = tokens_of(t[b], int(a[6][b]), 16, kc.shape[0])
+        for hk in range(2):
+            k = cpu(torch.cat((kc[pages, hk, slots], kc[op, hk, os_])))
+            s = cpu(q[b, hk * 4:hk * 4 + 4]) @ k.T * a[7]
+            # as shared_ref's bound on lse, with scores below 64 in size
+            within(lse[b, hk * 4:hk * 4 + 4], torch.logsumexp(s, -1), (d + 2) * E * 64 + 4 * E * 128 + 90 * E)
+
+
+@gpu_only
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (BF, 256), (F32, 64)])
+def test_rising_and_large_scores(gpu, dtype, d):
+    # the maximum rises from tile to tile, then falls; and scores far apart
+    for seed, order in ((1, 1), (2, -1), (3, 0)):
+        a = inputs(gpu, dtype, 4, 1, d, 16, 1500, [40] * 40, seed)
+        q, kc, pt = a[0], a[1], a[3]
+        q.copy_(q.abs())
+        up = torch.linspace(-4, 4, 1500, device=gpu)
+        up = up if order > 0 else up.flip(0) if order < 0 else torch.where(torch.arange(1500, device=gpu) % 500 == 77, 12.0, -3.0)
+        j = torch.arange(1500, device=gpu)
+        kc[pt.long()[j // 16], 0, j % 16] = (kc[pt.long()[j // 16], 0, j % 16].float() * 0.1 + up[:, None]).to(dtype)
+        check(a, dtype, d, f"order {order}")
+
+
+@gpu_only
+@pytest.mark.parametrize("seed", range(12))
+def test_ragged_batches(gpu, seed):
+    g = torch.Generator().manual_seed(100 + seed)
+    pick = lambda *x: x[int(torch.randint(0, len(x), (1,), generator=g))]  # noqa: E731
+    dtype, d, Hk, G, page = pick(BF, BF, F32), pick(64, 128, 128, 72, 16, 256), pick(1, 2, 5), pick(1, 2, 7, 16), pick(1, 16, 24, 64)
+    B = int(torch.randint(1, 70, (1,), generator=g))
+    prefix = int(torch.randint(1, 1800, (1,), generator=g))
+    lengths = [int(x) for x in torch.randint(0, 90, (B,), generator=g)]
+    check(inputs(gpu, dtype, G * Hk, Hk, d, page, prefix, lengths, seed), dtype, d)
+
+
+@gpu_only
+def test_strided_and_broadcast_queries(gpu):
+    q, kc, vc, pt, n, t, lengths, scale = inputs(gpu, BF, 8, 2, 128, 16, 300, [5, 9, 0, 20], 4)
+    wide = torch.zeros(4, 24 * 128, device=gpu, dtype=BF)
+    wide[:, 8 * 128:16 * 128] = q.flatten(1)
+    view = wide[:, 8 * 128:16 * 128].unflatten(1, (8, 128))
+    want = api.shared_prefix_attention(q, kc, vc, pt, n, t, lengths, scale)
+    got = api.shared_prefix_attention(view, kc, vc, pt, n, t, lengths, scale)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    same = q[:1].expand(4, 8, 128)                                   # one query for all
+    got = api.shared_prefix_attention(same, kc, vc, pt, n, t, lengths, scale)
+    want = api.shared_prefix_attention(same.contiguous(), kc, vc, pt, n, t, lengths, scale)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@gpu_only
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (F32, 64)])
+def test_graph_with_growing_lengths_and_two_streams(gpu, dtype, d):
+    a = inputs(gpu, dtype, 8, 2, d, 16, 500, [40, 3, 17], 6, spare=3)
+    n, lengths = a[4], a[6]
+    full = n.clone(), lengths.clone()
+    need = api._sized("attnres_shared_prefix_attention_workspace_bytes", gpu, 3, 8, 2, d, api._CODES[dtype], 16,
+                      a[3].numel())
+    ws = [torch.full((need,), 255, device=gpu, dtype=torch.uint8) for _ in range(2)]
+    sides = [torch.cuda.Stream(gpu) for _ in range(2)]
+    graphs, outs = [], []
+    for w, s in zip(ws, sides):
+        s.wait_stream(torch.cuda.current_stream(gpu))
+        with torch.cuda.stream(s):
+            api.shared_prefix_attention(*a, workspace=w)
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                outs.append(api.shared_prefix_attention(*a, workspace=w))
+            graphs.append(graph)
+    torch.cuda.synchronize()
+    for step in range(3):                                            # the lengths on the device decide
+        n.copy_(full[0] - 200 * step)
+        lengths.copy_((full[1] + 5 * step) * (step != 1))
+        torch.cuda.synchronize()
+        for graph, s in zip(graphs, sides):                          # side by side, a workspace each
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        want = api.shared_prefix_attention(*a)
+        for got in outs:
+            assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@gpu_only
+def test_serving_layer(gpu):
+    """One decoded token of a batch behind a shared image and text prefix: add + norm in 8 bits, the projection, head
+    norm with three axes into the cache, attention behind the prefix."""
+    g = wk.generator(12, gpu)
+    B, D, Hq, Hk, d, page, prefix = 9, 512, 8, 2, 64, 16, 200
+    proj = rand(g, D, (Hq + 2 * Hk) * d, dtype=F32, scale=D ** -0.5)
+    wn, fr, axes = 1 + rand(g, D, dtype=F32, scale=0.1), api.rotary_frequencies(d, device=gpu), api.rotary_axes((8, 12, 12), device=gpu)
+    pages = torch.randperm(13 + 2 * B, device=gpu, generator=g).int()
+    pt, t = pages[:13].contiguous(), pages[13:].view(B, 2).contiguous()
+    kc, vc = (torch.zeros(13 + 2 * B, Hk, page, d, device=gpu, dtype=BF) for _ in range(2))
+
+    def layer(x, r, pos, places, table):
+        y8, sc, total = api.add_rms_norm_8bit(x, r, wn, group=128)
+        h = (y8.float().unflatten(-1, (-1, 128)) * sc[..., None]).flatten(-2) @ proj
+        q, k, v = (u.unflatten(-1, (-1, d)) for u in h.bfloat16().split([Hq * d, Hk * d, Hk * d], -1))
+        q = api.head_norm_rotate_append(q, k, v, None, None, pos, fr, kc, vc, table, axes=axes, places=places)
+        return q, total
+
+    # the prefix: an image of 14 x 14 patches and four text tokens, once for all
+    i = torch.arange(prefix, device=gpu)
+    img = i < 196
+    pos = torch.stack((torch.where(img, 0, i - 182), torch.where(img, i // 14, i - 182), torch.where(img, i % 14, i - 182)), -1)
+    x0, r0 = rand(g, 1, prefix, D), rand(g, 1, prefix, D, scale=3.0)
+    layer(x0, r0, pos[None].int().contiguous(), i[None].int().contiguous(), pt[None].contiguous())
+    # each sequence has 0 .. 8 tokens and appends one
+    have = torch.arange(B, device=gpu)
+    x1, r1 = rand(g, B, 9, D), rand(g, B, 9, D, scale=3.0)
+    own = 18 + torch.arange(9, device=gpu)[None, :, None].expand(B, 9, 3)
+    places = torch.where(torch.arange(9, device=gpu)[None] < have[:, None], torch.arange(9, device=gpu)[None], -1).int()
+    layer(x1, r1, own.int().contiguous(), places.contiguous(), t)
+    x2, r2 = rand(g, B, 1, D), rand(g, B, 1, D, scale=3.0)
+    last = (18 + have)[:, None, None].expand(B, 1, 3).int().contiguous()
+    q, total = layer(x2, r2, last, have[:, None].int().contiguous(), t)
+    n, lengths = torch.tensor([prefix], device=gpu).int(), (have + 1).int()
+    args = [q[:, 0], kc, vc, pt, n, t, lengths, d ** -0.5]
+    check(args, BF, d)
+    assert torch.equal(total, (x2.float() + r2.float()).bfloat16())
+    # the cache holds what was normed, turned and appended
+    y8, sc, _ = api.add_rms_norm_8bit(x2, r2, wn, group=128)
+    h = (y8.float().unflatten(-1, (-1, 128)) * sc[..., None]).flatten(-2) @ proj
+    q2, k2, v2 = (u.unflatten(-1, (-1, d)) for u in h.bfloat16().split([Hq * d, Hk * d, Hk * d], -1))
+    qr, kr = api.head_norm_rotate(q2, k2, None, None, last, fr, axes=axes)
+    for b in range(B):
+        pg = int(t[b, b // page])
+        assert torch.equal(kc[pg, :, b % page], kr[b, 0]) and torch.equal(vc[pg, :, b % page], v2[b, 0])
+    assert torch.equal(qr, q)
+
+
+# --------------------------------------------------------------------------
+# refusals
+# --------------------------------------------------------------------------
+def shared(q=FAKE, qs=512, kc=FAKE + 64, vc=FAKE + 128, num=8, page=16, ptab=FAKE, pp=4, pl=FAKE, table=FAKE, maxp=4,
+           n=FAKE, B=2, Hq=8, Hk=2, d=64, dtype=1, scale=0.1, out=FAKE + 192, lse=None, ws=FAKE + 256, bytes_=1 << 40):
+    return _lib.lib().attnres_shared_prefix_attention(q, qs, kc, vc, num, page, ptab, pp, pl, table, maxp, n, B, Hq, Hk, d,
+                                                      dtype, scale, out, lse, ws, bytes_, None)
+
+
+def test_refusals():
+    size = _lib.lib().attnres_shared_prefix_attention_workspace_bytes
+    need = size(2, 8, 2, 64, 1, 16, 4)
+    assert need > 0 and size(2, 8, 2, 64, 1, 16, 0) > 0 and size(0, 8, 2, 64, 1, 16, 4) > 0
+    assert size(2, 8, 2, 64, 5, 16, 4) == DTYPE and size(2, 8, 3, 64, 1, 16, 4) == SHAPE and size(2, 8, 2, 60, 1, 16, 4) == ALIGN
+    assert size(2, 17, 1, 64, 1, 16, 4) == SHAPE and size(2, 8, 2, 264, 1, 16, 4) == SHAPE and size(-1, 8, 2, 64, 1, 16, 4) == SHAPE
+    assert size(2, 8, 2, 64, 1, 0, 4) == SHAPE and size(2, 8, 2, 64, 1, 16, -1) == SHAPE
+    assert size(2, 8, 2, 64, 1, 1 << 20, 1 << 12) == SHAPE and size(1 << 30, 8, 2, 64, 1, 16, 4) == SHAPE
+    assert shared(dtype=3) == DTYPE and shared(B=-1) == SHAPE and shared(page=0) == SHAPE and shared(maxp=-1) == SHAPE
+    assert shared(pp=-1) == SHAPE and shared(num=-1) == SHAPE and shared(Hq=7) == SHAPE and shared(d=4) == ALIGN
+    assert shared(scale=math.inf) == VALUE and shared(scale=math.nan) == VALUE
+    for name in ("q", "kc", "vc", "ptab", "pl", "table", "n", "out", "ws"):
+        assert shared(**{name: None}) == NULL, name
+    assert shared(bytes_=need - 1) == CAP and shared(qs=516) == ALIGN
+    for name in ("q", "kc", "vc", "out", "ws"):
+        assert shared(**{name: FAKE + 8}) == ALIGN, name
+    for name in ("ptab", "pl", "table", "n", "lse"):
+        assert shared(**{name: FAKE + 2}) == ALIGN, name
+    assert shared(out=FAKE + 64) == VALUE and shared(ws=FAKE + 128) == VALUE and shared(ws=FAKE) == VALUE
+    assert shared(B=0, q=None, out=None, n=None) == OK
+
+
+@gpu_only
+def test_wrapper_refusals(gpu):
+    a = inputs(gpu, BF, 4, 2, 64, 16, 40, [3, 5], 1)
+    for at, bad in ((0, a[0].cpu()), (0, a[0][0]), (1, a[1][:, :1].contiguous()), (2, a[2][:1]), (3, a[3][None]), (4, None),
+                    (4, a[4].repeat(2)), (5, a[5][:1]), (6, a[6][:1]), (6, None)):
+        b = list(a)
+        b[at] = bad
+        with pytest.raises(ValueError):
+            api.shared_prefix_attention(*b)
+    for at in (3, 4, 5, 6):
+        b = list(a)
+        b[at] = a[at].long()
+        with pytest.raises(TypeError):
+            api.shared_prefix_attention(*b)
+    with pytest.raises(_lib.AttnResError):
+        api.shared_prefix_attention(*a, workspace=torch.empty(64, device=gpu, dtype=torch.uint8))

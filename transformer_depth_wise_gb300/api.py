@@ -1016,6 +1016,46 @@ def paged_attention(q, k_cache, v_cache, page_table, lengths, scale: float, out=
     return out, lse
 
 
+def shared_prefix_attention(q, k_cache, v_cache, prefix_table, prefix_length, page_table, lengths, scale: float,
+                            out=None, lse=None, workspace=None):
+    """paged_attention of a batch whose sequences share a prefix, which is worked on once for all of them.
+
+    prefix_table int32 [prefix_pages], prefix_length int32 [1]: the prefix's pages and tokens; page_table int32
+    [B, max_pages], lengths int32 [B]: what each sequence goes on with, from a page of its own, the new token among
+    them.  The rest as paged_attention; returns (out [B,Hq,d], lse [B,Hq] fp32).  workspace: uint8 CUDA scratch of
+    attnres_shared_prefix_attention_workspace_bytes (allocated when None); calls that may overlap need one each.
+    """
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a [B, H, d] tensor")
+    qs = _heads(q, "q")
+    B, Hq, d = q.shape
+    dev, code = q.device, _CODES[q.dtype]
+    Hk = k_cache.shape[1] if isinstance(k_cache, torch.Tensor) and k_cache.dim() == 4 else 0
+    num_pages, page_size, max_pages = _cache_args(k_cache, v_cache, page_table, q, B, Hk, d)
+    if not isinstance(prefix_table, torch.Tensor) or prefix_table.dim() != 1:
+        raise ValueError("prefix_table must be a [prefix_pages] tensor")
+    pages = prefix_table.shape[0]
+    _plain(prefix_table, "prefix_table", torch.int32, (pages,), dev)
+    _given(prefix_length, "prefix_length", torch.int32, (1,), dev)
+    _given(lengths, "lengths", torch.int32, (B,), dev)
+    if out is None:
+        out = torch.empty((B, Hq, d), dtype=q.dtype, device=dev)
+    else:
+        _plain(out, "out", q.dtype, q.shape, dev)
+    if lse is None:
+        lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+    else:
+        _plain(lse, "lse", torch.float32, (B, Hq), dev)
+    need = 0
+    if workspace is None:
+        need = _sized("attnres_shared_prefix_attention_workspace_bytes", dev, B, Hq, Hk, d, code, page_size, pages)
+    ws, wp, wn = _workspace(workspace, need, dev)
+    _call("attnres_shared_prefix_attention", dev, q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), num_pages,
+          page_size, prefix_table.data_ptr(), pages, prefix_length.data_ptr(), page_table.data_ptr(), max_pages,
+          lengths.data_ptr(), B, Hq, Hk, d, code, float(scale), out.data_ptr(), lse.data_ptr(), wp, wn)
+    return out, lse
+
+
 def _linear_args(q, k, v, log_decay, lengths, state):
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be a [B, T, H, d] tensor")

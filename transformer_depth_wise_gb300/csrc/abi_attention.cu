@@ -306,6 +306,47 @@ int attnres_paged_attention(const void *q, int64_t q_stride, const void *k_cache
   return cuda_status(launch_paged(a));
 }
 
+int64_t attnres_shared_prefix_attention_workspace_bytes(int64_t B, int Hq, int Hk, int64_t d, int dtype, int page_size,
+                                                        int prefix_pages) {
+  const int64_t own = attnres_paged_attention_workspace_bytes(Hq, Hk, d, dtype);
+  if (own < 0) return own;
+  const int st = check_pages(0, page_size, prefix_pages);
+  if (st) return st;
+  if (B < 0 || B > INT32_MAX / 64 / Hq) return ATTNRES_ERR_SHAPE;      // rows and grids stay within 32 bits
+  return shared_layout(B, Hq, Hk, d, dtype, (int64_t)page_size * prefix_pages).bytes;
+}
+
+int attnres_shared_prefix_attention(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
+                                    int64_t num_pages, int page_size, const int32_t *prefix_table, int prefix_pages,
+                                    const int32_t *prefix_length, const int32_t *page_table, int max_pages,
+                                    const int32_t *lengths, int64_t B, int Hq, int Hk, int64_t d, int dtype, float scale,
+                                    void *out, float *lse, void *workspace, int64_t workspace_bytes, void *stream) {
+  const int64_t need = attnres_shared_prefix_attention_workspace_bytes(B, Hq, Hk, d, dtype, page_size, prefix_pages);
+  if (need < 0) return (int)need;
+  int st = check_stride(q_stride, Hq * d, dtype, false);
+  if (st) return st;
+  if ((st = check_pages(num_pages, page_size, max_pages))) return st;
+  if (!std::isfinite(scale)) return ATTNRES_ERR_VALUE;
+  if (B == 0) return ATTNRES_OK;
+  if (!q || !lengths || !out || !workspace || (prefix_pages && !prefix_length)) return ATTNRES_ERR_NULL;
+  if (num_pages > 0 && ((max_pages > 0 && !page_table) || (prefix_pages > 0 && !prefix_table) ||
+                        ((max_pages > 0 || prefix_pages > 0) && (!k_cache || !v_cache))))
+    return ATTNRES_ERR_NULL;
+  if (workspace_bytes < need) return ATTNRES_ERR_CAPACITY;
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || misaligned(k_cache) || misaligned(v_cache) ||
+      misaligned(prefix_table, 4) || misaligned(prefix_length, 4) || misaligned(page_table, 4) ||
+      misaligned(lengths, 4) || misaligned(lse, 4))
+    return ATTNRES_ERR_ALIGNMENT;
+  if (among(out, k_cache, v_cache, workspace) || among(workspace, q, k_cache, v_cache, lse)) return ATTNRES_ERR_VALUE;
+  SharedArgs a{};
+  a.q = q; a.q_stride = q_stride; a.k_cache = k_cache; a.v_cache = v_cache; a.num_pages = num_pages;
+  a.page_size = page_size; a.prefix_pages = num_pages > 0 ? prefix_pages : 0;
+  a.max_pages = num_pages > 0 ? max_pages : 0; a.prefix_table = prefix_table; a.prefix_length = prefix_length;
+  a.page_table = page_table; a.lengths = lengths; a.B = B; a.Hq = Hq; a.Hk = Hk; a.d = (int)d; a.dtype = dtype;
+  a.scale = scale; a.out = out; a.lse = lse; a.workspace = workspace; a.stream = static_cast<cudaStream_t>(stream);
+  return cuda_status(launch_shared(a));
+}
+
 int64_t attnres_linear_attention_workspace_bytes(int64_t B, int64_t T, int H, int64_t dk, int64_t dv, int dtype) {
   int64_t rows = 0;
   const int st = check_linear(B, T, H, dk, dv, dtype, rows);

@@ -267,12 +267,41 @@ struct PagedArgs {
   float *lse;                  // [B, Hq] or nullptr
   void *workspace;             // paged_workspace_bytes()
   cudaStream_t stream;
+  bool out_f32;                // out is fp32 whatever the type
 };
 bool paged_supported(int64_t d, int dtype);
 // CTAs the split runs on the current device, and the workspace they need.
 int paged_ctas(int64_t d, int dtype);
 int64_t paged_workspace_bytes(int G, int64_t d, int dtype);
 cudaError_t launch_paged(const PagedArgs &a);
+
+struct SharedArgs {
+  const void *q;               // as in PagedArgs
+  int64_t q_stride;
+  const void *k_cache, *v_cache;
+  int64_t num_pages;
+  int page_size, prefix_pages, max_pages;
+  const int32_t *prefix_table; // [prefix_pages]
+  const int32_t *prefix_length;    // [1]
+  const int32_t *page_table;   // [B, max_pages]
+  const int32_t *lengths;      // [B]
+  int64_t B;
+  int Hq, Hk, d, dtype;
+  float scale;
+  void *out;                   // [B, Hq, d]
+  float *lse;                  // [B, Hq] or nullptr
+  void *workspace;             // SharedLayout::bytes
+  cudaStream_t stream;
+};
+// A workspace: the paged kernel's own, then lse and outputs of the prefix's
+// parts and of the sequences' own one, in bytes from its start.
+struct SharedLayout {
+  int splits;                  // parts of the prefix
+  int64_t part_lse, part_o, bytes;
+};
+// `tokens`: what the prefix's table covers.
+SharedLayout shared_layout(int64_t B, int Hq, int Hk, int64_t d, int dtype, int64_t tokens);
+cudaError_t launch_shared(const SharedArgs &a);
 
 // out_i = alpha sum_{j <= i} e^{g (i - j)} (a_i . b_j) c_j + carry e^{g (i + first_pow)} a_i . first, through the state
 // S_i = e^g S_{i-1} + gain b_i c_i^T (S_{-1} = e^{g (first_pow - 1)} first), with alpha = carry gain

@@ -49,6 +49,7 @@ struct PagedParams {
   int64_t num_pages;
   float scale;
   void *out;                           // [B, Hq, d]
+  bool out_f32;                        // out in fp32 whatever the type (a part of a longer attention)
   float *lse;                          // [B, Hq] or nullptr
   float *part_o, *part_lse;            // [ctas][2][G][d], [ctas][2][G]
   Cut *cuts;                           // [ctas]
@@ -154,7 +155,11 @@ template <typename T>
 __device__ __forceinline__ void write_empty(const PagedParams &p) {
   for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
     if (clamped_length(p, b) != 0) continue;
-    for (int i = threadIdx.x; i < p.Hq * p.d; i += blockDim.x) ((T *)p.out)[(int64_t)b * p.Hq * p.d + i] = T(0.f);
+    for (int i = threadIdx.x; i < p.Hq * p.d; i += blockDim.x) {
+      const int64_t at = (int64_t)b * p.Hq * p.d + i;
+      if (p.out_f32) ((float *)p.out)[at] = 0.f;
+      else ((T *)p.out)[at] = T(0.f);
+    }
     if (p.lse)
       for (int i = threadIdx.x; i < p.Hq; i += blockDim.x) p.lse[(int64_t)b * p.Hq + i] = -INFINITY;
   }
@@ -176,6 +181,7 @@ __device__ __forceinline__ void store_piece(const PagedParams &p, const Walk &w,
     const int64_t row = (int64_t)w.b * p.Hq + w.hk * p.G + g;
     T *dst = (T *)p.out + row * p.d + e;
     if constexpr (std::is_same<T, float>::value) *reinterpret_cast<float4 *>(dst) = o;
+    else if (p.out_f32) *reinterpret_cast<float4 *>((float *)p.out + row * p.d + e) = o;
     else *reinterpret_cast<uint2 *>(dst) = make_uint2(Elt<T>::pack_word(o.x, o.y), Elt<T>::pack_word(o.z, o.w));
     if (e == 0 && p.lse) p.lse[row] = lse;
   } else {
@@ -723,7 +729,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Paged
     float x = 0.f;
 #pragma unroll
     for (int k = 0; k < kJoinWarps; ++k) x += sums[k * p.d + e];
-    if constexpr (std::is_same<T, float>::value) ((float *)p.out)[row * p.d + e] = x * r;
+    if (std::is_same<T, float>::value || p.out_f32) ((float *)p.out)[row * p.d + e] = x * r;
     else ((__nv_bfloat16 *)p.out)[row * p.d + e] = __float2bfloat16_rn(x * r);
   }
   if (threadIdx.x == 0 && p.lse) p.lse[row] = L == 0.f ? -INFINITY : M + logf(L);
@@ -752,7 +758,7 @@ cudaError_t launch_paged(const PagedArgs &a) {
   p.page_shift = -1;
   for (int i = 0; i < 31; ++i)
     if (a.page_size == 1 << i) p.page_shift = i;
-  p.scale = a.scale; p.out = a.out; p.lse = a.lse;
+  p.scale = a.scale; p.out = a.out; p.lse = a.lse; p.out_f32 = a.out_f32;
   const int ctas = paged_ctas(a.d, a.dtype);
   p.cuts = static_cast<Cut *>(a.workspace);
   p.part_o = reinterpret_cast<float *>(p.cuts + ctas);

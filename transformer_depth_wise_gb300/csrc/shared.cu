@@ -1,0 +1,276 @@
+// shared.cu -- attention of one new token per sequence of a batch that shares
+// a prefix in the paged cache, each sequence going on with pages of its own.
+//
+// For sequence b and query head h:  out = softmax of scale q.k over the
+// prefix's tokens and the sequence's own ones, times v; lse.  The prefix is
+// the same for all sequences, so the query heads of all of them that share a
+// key head are the rows of one matrix Q [B G, d], and the prefix costs two
+// matrix products, Q K^T and P V, which read the prefix once per tile of rows
+// instead of once per sequence.  The rows' tiles and the prefix's ranges are
+// dealt out over the CTAs; each leaves its part, normalised, with its lse.
+// The sequences' own tokens go through the kernel of attnres_paged_attention,
+// which leaves one more part, and a last kernel joins the parts by the
+// online-softmax merge (OS2).
+//
+// This file: the parts of the prefix in fp32 arithmetic for any type and
+// width, and the join.  A tile of 64 rows and 32 tokens at a time goes through
+// shared memory as fp32; a thread forms 2 x 4 scores, and then adds to two
+// rows of the output, so that each 16-byte read from shared memory feeds eight
+// multiply-adds.
+#include <type_traits>
+
+#include "common.cuh"
+#include "launch.h"
+#include "shared.cuh"
+
+namespace attnres {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRows = 64;                // query rows of a CTA
+constexpr int kKeys = 32;                // tokens of a tile
+
+template <int D> struct Shape {
+  static constexpr int kPitch = D + 4;   // floats: rows of eight lanes meet no bank twice
+  static constexpr int kCols = D / 32;   // 16-byte columns of a thread's output row
+  static constexpr size_t kSmem = ((size_t)(kRows + 2 * kKeys) * kPitch + kRows * (kKeys + 1)) * sizeof(float);
+};
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) shared_prefix_kernel(const PrefixParams p) {
+  using S = Shape<D>;
+  constexpr int E = Elt<T>::EPV, P = S::kPitch, NC = S::kCols;
+  extern __shared__ __align__(16) float sm[];
+  float *qs = sm, *ks = qs + kRows * P, *vs = ks + kKeys * P, *ps = vs + kKeys * P;
+  __shared__ int live[kKeys];
+  grid_dependency_wait();
+  const int tiles = (p.B * p.G + kRows - 1) / kRows;
+  const int hk = blockIdx.x / tiles, row0 = (blockIdx.x - hk * tiles) * kRows, split = blockIdx.y;
+  const int n = p.tokens();
+  int j0, j1;
+  p.range<kKeys>(n, split, j0, j1);
+  const int nvec = p.d / E, warp_row = threadIdx.x / 8, l8 = threadIdx.x % 8;
+
+  // the tile's queries, zero behind the batch and behind d, in powers of two
+  const float scale2 = p.scale * 1.44269504088896340736f;
+  for (int i = threadIdx.x; i < kRows * (D / E); i += kThreads) {
+    const int r = i / (D / E), c = i % (D / E), row = row0 + r;
+    float x[E] = {};
+    if (row < p.B * p.G && c < nvec) {
+      const T *src = (const T *)p.q + (int64_t)(row / p.G) * p.q_stride + (int64_t)(hk * p.G + row % p.G) * p.d + c * E;
+      Elt<T>::unpack(*reinterpret_cast<const uint4 *>(src), x);
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) qs[r * P + c * E + e] = x[e] * scale2;
+  }
+
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[2][NC * 4] = {};
+  for (int j = j0; j < j1; j += kKeys) {
+    __syncthreads();                       // the last tile is read
+    if (threadIdx.x < kKeys) live[threadIdx.x] = j + threadIdx.x < j1 && p.row(j + threadIdx.x, hk) >= 0;
+    for (int i = threadIdx.x; i < kKeys * (D / E); i += kThreads) {
+      const int t = i / (D / E), c = i % (D / E);
+      const int64_t at = j + t < j1 ? p.row(j + t, hk) : -1;
+      float x[E] = {}, y[E] = {};
+      if (at >= 0 && c < nvec) {
+        Elt<T>::unpack(*reinterpret_cast<const uint4 *>((const T *)p.k + at + c * E), x);
+        Elt<T>::unpack(*reinterpret_cast<const uint4 *>((const T *)p.v + at + c * E), y);
+      }
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        *reinterpret_cast<float4 *>(ks + t * P + c * E + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+        *reinterpret_cast<float4 *>(vs + t * P + c * E + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+      }
+    }
+    __syncthreads();
+    // scores of rows warp_row and warp_row + 32 with tokens l8 + 8 i
+    float s[2][4] = {};
+    for (int c = 0; c < D; c += 4) {
+      const float4 a = *reinterpret_cast<const float4 *>(qs + warp_row * P + c);
+      const float4 b = *reinterpret_cast<const float4 *>(qs + (warp_row + 32) * P + c);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 k = *reinterpret_cast<const float4 *>(ks + (l8 + 8 * i) * P + c);
+        s[0][i] = fmaf(a.x, k.x, fmaf(a.y, k.y, fmaf(a.z, k.z, fmaf(a.w, k.w, s[0][i]))));
+        s[1][i] = fmaf(b.x, k.x, fmaf(b.y, k.y, fmaf(b.z, k.z, fmaf(b.w, k.w, s[1][i]))));
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (!live[l8 + 8 * i]) s[r][i] = -INFINITY;
+        top = fmaxf(top, s[r][i]);
+      }
+#pragma unroll
+      for (int x = 1; x < 8; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+      const float mn = fmaxf(m[r], top), keep = m[r] == mn ? 1.f : exp2_fast(m[r] - mn);
+      const float base = mn == -INFINITY ? 0.f : mn;
+      m[r] = mn;
+      l[r] *= keep;
+#pragma unroll
+      for (int i = 0; i < NC * 4; ++i) o[r][i] *= keep;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float w = exp2_fast(s[r][i] - base);
+        l[r] += w;
+        ps[(warp_row + 32 * r) * (kKeys + 1) + l8 + 8 * i] = w;
+      }
+    }
+    __syncwarp();                          // a row's weights come from its own eight lanes
+    const int left = min(kKeys, j1 - j);
+    for (int t = 0; t < left; ++t) {
+      const float a = ps[warp_row * (kKeys + 1) + t], b = ps[(warp_row + 32) * (kKeys + 1) + t];
+#pragma unroll
+      for (int i = 0; i < NC; ++i) {
+        const float4 v = *reinterpret_cast<const float4 *>(vs + t * P + i * 32 + l8 * 4);
+        o[0][4 * i] = fmaf(a, v.x, o[0][4 * i]);
+        o[0][4 * i + 1] = fmaf(a, v.y, o[0][4 * i + 1]);
+        o[0][4 * i + 2] = fmaf(a, v.z, o[0][4 * i + 2]);
+        o[0][4 * i + 3] = fmaf(a, v.w, o[0][4 * i + 3]);
+        o[1][4 * i] = fmaf(b, v.x, o[1][4 * i]);
+        o[1][4 * i + 1] = fmaf(b, v.y, o[1][4 * i + 1]);
+        o[1][4 * i + 2] = fmaf(b, v.z, o[1][4 * i + 2]);
+        o[1][4 * i + 3] = fmaf(b, v.w, o[1][4 * i + 3]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int row = row0 + warp_row + 32 * r;
+    float L = l[r];
+#pragma unroll
+    for (int x = 1; x < 8; x <<= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
+    if (row >= p.B * p.G) continue;
+    const int64_t at = p.part(split, row, hk);
+    const float f = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll
+    for (int i = 0; i < NC; ++i)
+      if (i * 32 + l8 * 4 < p.d)
+        *reinterpret_cast<float4 *>(p.part_o + at * p.d + i * 32 + l8 * 4) =
+            make_float4(o[r][4 * i] * f, o[r][4 * i + 1] * f, o[r][4 * i + 2] * f, o[r][4 * i + 3] * f);
+    if (l8 == 0) p.part_lse[at] = L == 0.f ? -INFINITY : (m[r] + log2f(L)) * 0.69314718055994530942f;
+  }
+}
+
+// One warp per (sequence, query head): the parts' weights by their lse, then
+// their weighted sum, part after part in order.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) shared_join_kernel(const float *part_o, const float *part_lse, int parts,
+                                                               int64_t rows, int d, T *out, float *lse) {
+  grid_dependency_wait();
+  const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  if (row >= rows) return;
+  float M = -INFINITY;
+  for (int k = lane; k < parts; k += 32) M = fmaxf(M, part_lse[k * rows + row]);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+  float L = 0.f;
+  for (int k = 0; k < parts; ++k) {
+    const float x = part_lse[k * rows + row];
+    L += x == -INFINITY ? 0.f : expf(x - M);
+  }
+  const float f = L == 0.f ? 0.f : 1.f / L;
+  for (int e = lane * 4; e < d; e += 128) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < parts; ++k) {
+      const float x = part_lse[k * rows + row];
+      if (x == -INFINITY) continue;        // a part without a weight may hold nothing
+      const float w = expf(x - M) * f;
+      const float4 y = *reinterpret_cast<const float4 *>(part_o + (k * rows + row) * d + e);
+      s.x = fmaf(y.x, w, s.x);
+      s.y = fmaf(y.y, w, s.y);
+      s.z = fmaf(y.z, w, s.z);
+      s.w = fmaf(y.w, w, s.w);
+    }
+    T *dst = out + row * d + e;
+    if constexpr (std::is_same<T, float>::value) *reinterpret_cast<float4 *>(dst) = s;
+    else *reinterpret_cast<uint2 *>(dst) = make_uint2(Elt<T>::pack_word(s.x, s.y), Elt<T>::pack_word(s.z, s.w));
+  }
+  if (lane == 0 && lse) lse[row] = L == 0.f ? -INFINITY : M + logf(L);
+}
+
+// Ranges that the prefix is cut into so that the CTAs fill the GPU's SMs
+// about twice, none shorter than four tiles.
+int general_splits(int64_t B, int G, int Hk, int64_t tokens) {
+  const int64_t items = (B * G + kRows - 1) / kRows * Hk, tiles = (tokens + kKeys - 1) / kKeys;
+  int64_t n = (4 * (int64_t)sm_count() + items - 1) / items;
+  if (n > tiles / 4) n = tiles / 4;
+  return (int)(n < 1 ? 1 : n > kMaxPrefixParts ? kMaxPrefixParts : n);
+}
+
+template <typename T>
+cudaError_t launch_general(const PrefixParams &p, cudaStream_t stream) {
+  const dim3 grid((unsigned)((int64_t)p.Hk * ((p.B * p.G + kRows - 1) / kRows)), (unsigned)p.splits);
+  auto go = [&](auto D) -> cudaError_t {
+    using S = Shape<decltype(D)::value>;
+    auto kern = shared_prefix_kernel<T, decltype(D)::value>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kern, grid, dim3(kThreads), S::kSmem, stream, p);
+  };
+  return p.d <= 64 ? go(std::integral_constant<int, 64>{}) : p.d <= 128 ? go(std::integral_constant<int, 128>{})
+                                                                     : go(std::integral_constant<int, 256>{});
+}
+
+int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
+
+}  // namespace
+
+SharedLayout shared_layout(int64_t B, int Hq, int Hk, int64_t d, int dtype, int64_t tokens) {
+  SharedLayout w{};
+  const int G = Hq / Hk;
+  w.splits = B > 0 && tokens > 0 ? general_splits(B, G, Hk, tokens) : 0;
+  const int64_t rows = B * Hq, parts = w.splits + 1;
+  w.part_lse = up16(paged_workspace_bytes(G, d, dtype));
+  w.part_o = w.part_lse + up16(parts * rows * (int64_t)sizeof(float));
+  w.bytes = w.part_o + parts * rows * d * (int64_t)sizeof(float);
+  return w;
+}
+
+cudaError_t launch_shared(const SharedArgs &a) {
+  const int64_t tokens = (int64_t)a.prefix_pages * a.page_size;
+  const SharedLayout w = shared_layout(a.B, a.Hq, a.Hk, a.d, a.dtype, tokens);
+  char *ws = static_cast<char *>(a.workspace);
+  const int64_t rows = a.B * a.Hq;
+  PrefixParams p{};
+  p.q = a.q; p.k = a.k_cache; p.v = a.v_cache; p.q_stride = a.q_stride;
+  p.table = a.prefix_table; p.length = a.prefix_length;
+  p.B = (int)a.B; p.Hq = a.Hq; p.Hk = a.Hk; p.G = a.Hq / a.Hk; p.d = a.d;
+  p.page = a.page_size; p.most = (int)tokens; p.num_pages = a.num_pages; p.scale = a.scale;
+  p.page_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (a.page_size == 1 << i) p.page_shift = i;
+  p.part_o = reinterpret_cast<float *>(ws + w.part_o);
+  p.part_lse = reinterpret_cast<float *>(ws + w.part_lse);
+  p.splits = w.splits;
+  cudaError_t e = cudaSuccess;
+  if (w.splits > 0)
+    e = a.dtype == ATTNRES_BF16 ? launch_general<__nv_bfloat16>(p, a.stream) : launch_general<float>(p, a.stream);
+  if (e != cudaSuccess) return e;
+  // the sequences' own tokens: the last part
+  PagedArgs s{};
+  s.q = a.q; s.q_stride = a.q_stride; s.k_cache = a.k_cache; s.v_cache = a.v_cache; s.num_pages = a.num_pages;
+  s.page_size = a.page_size; s.max_pages = a.max_pages; s.page_table = a.page_table; s.lengths = a.lengths;
+  s.B = a.B; s.Hq = a.Hq; s.Hk = a.Hk; s.d = a.d; s.dtype = a.dtype; s.scale = a.scale;
+  s.out = p.part_o + w.splits * rows * a.d; s.lse = p.part_lse + w.splits * rows; s.out_f32 = true;
+  s.workspace = ws; s.stream = a.stream;
+  if ((e = launch_paged(s)) != cudaSuccess) return e;
+  const dim3 grid((unsigned)((rows + kThreads / 32 - 1) / (kThreads / 32)));
+  if (a.dtype == ATTNRES_BF16)
+    return launch_dependent(shared_join_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, a.stream, (const float *)p.part_o,
+                            (const float *)p.part_lse, w.splits + 1, rows, a.d, static_cast<__nv_bfloat16 *>(a.out),
+                            a.lse);
+  return launch_dependent(shared_join_kernel<float>, grid, dim3(kThreads), 0, a.stream, (const float *)p.part_o,
+                          (const float *)p.part_lse, w.splits + 1, rows, a.d, static_cast<float *>(a.out), a.lse);
+}
+
+}  // namespace attnres

@@ -1,0 +1,46 @@
+// shared.cuh -- what the kernels of a shared prefix's parts have in common.
+#pragma once
+
+#include <stdint.h>
+
+namespace attnres {
+
+constexpr int kMaxPrefixParts = 64;      // ranges of the prefix
+
+struct PrefixParams {
+  const void *q, *k, *v;
+  int64_t q_stride;                      // elements from one sequence's queries to the next
+  const int32_t *table, *length;         // the prefix's pages; its tokens
+  int B, Hq, Hk, G, d;
+  int page, page_shift, most;            // page_shift: log2(page), or -1; most: tokens that the table covers
+  int64_t num_pages;
+  float scale;
+  float *part_o, *part_lse;              // [splits][B Hq][d], [splits][B Hq]
+  int splits;
+
+#ifdef __CUDACC__
+  // The prefix's tokens, held within what the table covers.
+  __device__ __forceinline__ int tokens() const {
+    const int n = *length;
+    return n < 0 ? 0 : n < most ? n : most;
+  }
+  // Range `split` of the first n tokens, in whole tiles of TILE.
+  template <int TILE> __device__ __forceinline__ void range(int n, int split, int &from, int &to) const {
+    const int64_t tiles = (n + TILE - 1) / TILE;
+    from = (int)(tiles * split / splits) * TILE;
+    to = min(n, (int)(tiles * (split + 1) / splits) * TILE);
+  }
+  // The cache row of token j: element offset, or -1 for a page outside the pool.
+  __device__ __forceinline__ int64_t row(int j, int hk) const {
+    const int64_t pg = table[page_shift >= 0 ? j >> page_shift : j / page];
+    if (pg < 0 || pg >= num_pages) return -1;
+    return ((pg * Hk + hk) * page + (page_shift >= 0 ? j & (page - 1) : j % page)) * d;
+  }
+  // The part's row of row r (sequence r / G, head r % G of key head hk).
+  __device__ __forceinline__ int64_t part(int split, int r, int hk) const {
+    return ((int64_t)split * B + r / G) * Hq + hk * G + r % G;
+  }
+#endif
+};
+
+}  // namespace attnres
