@@ -67,7 +67,7 @@ def planned_registers(src: str) -> int:
 
 
 # Sources with a kernel of register shares.
-REGISTER_SHARES = {"linear_tc.cu": "linear_tc_kernel"}
+REGISTER_SHARES = {"linear_tc.cu": "linear_tc_kernel", "shared_tc.cu": "shared_tc_kernel"}
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:

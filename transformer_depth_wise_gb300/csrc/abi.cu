@@ -511,7 +511,7 @@ int attnres_set_wait_limit(int64_t cycles) {
 int attnres_take_device_error(void) {
   if (cudaDeviceSynchronize() != cudaSuccess) return ATTNRES_ERR_CUDA;
   const unsigned int f = take_error_aggregate() | take_error_merge() | take_error_phase1() |
-                           take_error_phase1_tc() | take_error_linear();
+                           take_error_phase1_tc() | take_error_linear() | take_error_shared();
   if (f & 2u) return ATTNRES_ERR_CUDA;
   return f ? ATTNRES_ERR_TIMEOUT : ATTNRES_OK;
 }

@@ -351,5 +351,6 @@ unsigned int take_error_merge();
 unsigned int take_error_phase1();
 unsigned int take_error_phase1_tc();
 unsigned int take_error_linear();
+unsigned int take_error_shared();
 
 }  // namespace attnres

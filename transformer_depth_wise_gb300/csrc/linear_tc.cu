@@ -107,15 +107,6 @@ constexpr uint32_t kColKV = 0, kColP = 256, kColInter = 320, kColIntra = 384, kC
 enum Bar { kFull = 0, kEmpty = 4, kPartsFull = 8, kPartsEmpty = 10, kKV = 12, kKVFree = 14, kPV = 16, kOutFree, kQK, kSReady,
            kQS, kPReady, kClean, kDrain, kDrainKV, kBars };
 
-// A role's share of the registers: it gives some of the launch's back, or
-// takes some that others have given.
-template <int N, int LAUNCHED> __device__ __forceinline__ void share_registers() {
-  static_assert(N % 8 == 0 && N >= 24 && N <= 256, "what the instruction takes");
-  if constexpr (N < LAUNCHED) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-  if constexpr (N > LAUNCHED) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 // A box of a [B][H][T][d] view (coordinates innermost first) to shared memory.
 __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, int x, int t, int h, int b, uint32_t bar) {
   asm volatile(
@@ -123,32 +114,11 @@ __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap *map, i
       " [%0], [%1, {%2, %3, %4, %5}], [%6];"
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(t), "r"(h), "r"(b), "r"(bar) : "memory");
 }
-// D[tmem] += A[tmem] B: the left operand from tensor memory, a row per lane.
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
-      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate));
-}
-// 16 columns of this thread's tensor-memory lane.
-__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&w)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
-      ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]),
-        "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15]) : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&w)[4]) {
   asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr));
 }
 __device__ __forceinline__ void sts128(uint32_t addr, const uint32_t (&w)[4]) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
-}
-// True in one lane of a converged warp.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t one;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
-  return one != 0;
 }
 // What a CTA of the main kernel has stored, before its first group counts it
 // as done: that group waits for the other state's and the outputs'.
@@ -166,17 +136,6 @@ __device__ __forceinline__ void first_group_barrier() {
 }
 // The outputs' four warps.
 __device__ __forceinline__ void output_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-
-// Descriptors from a tile's address: K-major tiles (groups of eight rows 1024
-// bytes apart) and MN-major ones; `d` moves along them by whole 16-byte units.
-struct Desc {
-  uint32_t lo;
-  __device__ __forceinline__ uint64_t at(uint32_t bytes) const {
-    return ((uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32) | (lo + (bytes >> 4));
-  }
-};
-__device__ __forceinline__ Desc desc_k(uint32_t addr) { return {((addr & 0x3FFFFu) >> 4) | 1u << 16}; }
-__device__ __forceinline__ Desc desc_mn(uint32_t addr, uint32_t lbo) { return {((addr & 0x3FFFFu) >> 4) | (lbo >> 4) << 16}; }
 
 // Two fp32 values in a register pair, from and to bf16 pairs.
 __device__ __forceinline__ uint64_t widen(uint32_t w) { return ((uint64_t)(w & 0xffff0000u) << 32) | (uint64_t)(w << 16); }

@@ -228,7 +228,8 @@ int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
 SharedLayout shared_layout(int64_t B, int Hq, int Hk, int64_t d, int dtype, int64_t tokens) {
   SharedLayout w{};
   const int G = Hq / Hk;
-  w.splits = B > 0 && tokens > 0 ? general_splits(B, G, Hk, tokens) : 0;
+  if (B > 0 && tokens > 0)
+    w.splits = shared_tc_supported(d, dtype) ? shared_tc_splits(B, G, Hk, d, tokens) : general_splits(B, G, Hk, tokens);
   const int64_t rows = B * Hq, parts = w.splits + 1;
   w.part_lse = up16(paged_workspace_bytes(G, d, dtype));
   w.part_o = w.part_lse + up16(parts * rows * (int64_t)sizeof(float));
@@ -252,9 +253,12 @@ cudaError_t launch_shared(const SharedArgs &a) {
   p.part_o = reinterpret_cast<float *>(ws + w.part_o);
   p.part_lse = reinterpret_cast<float *>(ws + w.part_lse);
   p.splits = w.splits;
+  p.wait_limit = wait_limit_cycles();
   cudaError_t e = cudaSuccess;
   if (w.splits > 0)
-    e = a.dtype == ATTNRES_BF16 ? launch_general<__nv_bfloat16>(p, a.stream) : launch_general<float>(p, a.stream);
+    e = shared_tc_supported(a.d, a.dtype) ? launch_shared_tc(p, a.stream)
+        : a.dtype == ATTNRES_BF16         ? launch_general<__nv_bfloat16>(p, a.stream)
+                                          : launch_general<float>(p, a.stream);
   if (e != cudaSuccess) return e;
   // the sequences' own tokens: the last part
   PagedArgs s{};

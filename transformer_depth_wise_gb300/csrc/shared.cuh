@@ -1,7 +1,10 @@
 // shared.cuh -- what the kernels of a shared prefix's parts have in common.
 #pragma once
 
+#include <cuda_runtime.h>
 #include <stdint.h>
+
+#include "attnres.h"
 
 namespace attnres {
 
@@ -17,6 +20,7 @@ struct PrefixParams {
   float scale;
   float *part_o, *part_lse;              // [splits][B Hq][d], [splits][B Hq]
   int splits;
+  long long wait_limit;                  // SM clock cycles a wait of the tensor-core kernel may take
 
 #ifdef __CUDACC__
   // The prefix's tokens, held within what the table covers.
@@ -42,5 +46,11 @@ struct PrefixParams {
   }
 #endif
 };
+
+// The parts on the 5th-generation tensor cores (bf16, heads of up to 128
+// elements): how many, and the launch.
+inline bool shared_tc_supported(int64_t d, int dtype) { return dtype == ATTNRES_BF16 && d <= 128; }
+int shared_tc_splits(int64_t B, int G, int Hk, int64_t d, int64_t tokens);
+cudaError_t launch_shared_tc(const PrefixParams &p, cudaStream_t stream);
 
 }  // namespace attnres

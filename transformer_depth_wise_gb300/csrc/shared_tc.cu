@@ -1,0 +1,442 @@
+// shared_tc.cu -- the parts of a shared prefix on the 5th-generation tensor
+// cores (bf16, heads of up to 128 elements; see shared.cu for the operator).
+//
+// A CTA takes 256 rows (query heads of one key head, over the sequences) as
+// two tiles of 128, and one range of the prefix's tokens, 128 at a time:
+//   S = Q K^T (M 128, N 128, K d),  P = 2^(scale S - m),  O += P V (M 128, N d, K 128)
+// S and O are fp32 in tensor memory; a thread of a tile's warpgroup has one row
+// of S, so the softmax needs no exchange between threads; P, rounded to bf16,
+// goes back to tensor memory over S, as the left operand of the second
+// product.  While one tile's weights are formed, the tensor cores work on the
+// other's products.
+//
+// m is a reference, not the maximum: it moves only when a score passes it by
+// 2^8, and O and the sum are rescaled then (fp32 holds what 2^8 adds).  So the
+// scores are read once, and the maximum is taken beside the exponentials.
+// Rounding P to bf16 adds an error of the size of the output's own rounding;
+// the sum is that of the unrounded weights.
+//
+// Roles (a warpgroup each): the two tiles' softmax; copies (cp.async of 16
+// bytes a lane, a row's page looked up by its own lane, into a ring of tiles
+// with the 128-byte swizzle; tokens behind the range or on no page arrive as
+// zeros and are masked); and one thread that issues the products.
+//
+// Every wait is bounded: one that runs out records a flag and an abort mark in
+// shared memory, on which every other wait returns at once; what is in flight
+// is drained and the CTA ends.
+#include "common.cuh"
+#include "launch.h"
+#include "shared.cuh"
+#include "tcgen05.cuh"
+
+ATTNRES_DEFINE_ERROR_FLAG(take_error_shared)
+
+namespace attnres {
+namespace {
+
+constexpr int kTileRows = 128;             // rows of a tile: one per thread
+constexpr int kKeys = 128;                 // tokens of a step
+constexpr int kThreads = 512;
+constexpr uint32_t kBlock = 128 * 128;     // bytes: 128 rows of 64 bf16 columns
+constexpr int kRegs = 128;                 // a thread's registers at the launch, then the roles' shares
+constexpr int kRegsSoftmax = 192, kRegsCopy = 64, kRegsMma = 64;
+static_assert(2 * kRegsSoftmax + kRegsCopy + kRegsMma <= 4 * kRegs, "more registers than the launch has");
+constexpr float kSlack = 8.f;              // powers of two that a score may lie above the reference
+constexpr int kMasks = 4;                  // steps whose masks are kept
+
+template <int D> struct Layout {
+  static constexpr int kBlocks = D / 64;
+  static constexpr uint32_t kTile = kBlocks * kBlock;                 // a tile of Q, K or V
+  static constexpr int kRing = D == 128 ? 5 : 6;                      // tiles of K and V, in turn
+  static constexpr uint32_t kOffRing = 2 * kTile;
+  static constexpr uint32_t kOffMask = kOffRing + kRing * kTile;
+  static constexpr uint32_t kOffBar = kOffMask + kMasks * 16;
+  static constexpr uint32_t kOffCtl = kOffBar + (2 * kRing + kMasks + 7) * 8;
+  static constexpr uint32_t kBytes = kOffCtl + 16 + 1024;             // and the alignment's slack
+  // barriers
+  static constexpr int kFull = 0, kEmpty = kRing, kMask = 2 * kRing, kScores = kMask + kMasks, kWeights = kScores + 2,
+                       kOut = kWeights + 2, kDrain = kOut + 2;
+};
+// Tensor memory columns: S (P over its first half) of both tiles, O.
+constexpr uint32_t kColO = 256;
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+// 32 columns of this thread's tensor-memory lane.
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// A row's weights for 32 tokens: from scores, reference and mask to 16 bf16
+// pairs; `top` takes the largest exponent, `sum` the weights.
+template <bool MASKED>
+__device__ __forceinline__ void weigh(const uint32_t (&s)[32], uint64_t scale2, uint64_t minus, uint32_t mask, float &top,
+                                      uint64_t &sum, uint32_t *out) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    float a, b;
+    unpair(fma2((uint64_t)s[2 * i + 1] << 32 | s[2 * i], scale2, minus), a, b);
+    if (MASKED) {
+      if (!(mask >> (2 * i) & 1u)) a = -INFINITY;
+      if (!(mask >> (2 * i + 1) & 1u)) b = -INFINITY;
+    }
+    top = fmaxf(top, fmaxf(a, b));
+    a = exp2_fast(a);
+    b = exp2_fast(b);
+    sum = add2(sum, pair(a, b));
+    out[i] = Elt<__nv_bfloat16>::pack_word(a, b);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_constant__ PrefixParams p) {
+  using L = Layout<D>;
+  constexpr int NB = L::kBlocks, NR = L::kRing;
+  extern __shared__ unsigned char smem_raw[];
+  grid_dependency_wait();
+  unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  const uint32_t base = smem_u32(sm);
+  volatile uint32_t *masks = reinterpret_cast<uint32_t *>(sm + L::kOffMask);
+  volatile uint32_t *ctl = reinterpret_cast<uint32_t *>(sm + L::kOffCtl);      // TMEM address, skip, abort
+  auto bar = [&](int b) { return base + L::kOffBar + 8u * b; };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp >> 2, quad = warp & 3;
+
+  const int all = p.B * p.G, tiles = (all + 2 * kTileRows - 1) / (2 * kTileRows);
+  const int hk = blockIdx.x / tiles, row0 = (blockIdx.x - hk * tiles) * 2 * kTileRows, split = blockIdx.y;
+  const int active = all - row0 > kTileRows ? 2 : 1;                          // tiles with rows
+  int j0, j1;
+  p.range<kKeys>(p.tokens(), split, j0, j1);
+  const int steps = j1 > j0 ? (j1 - j0 + kKeys - 1) / kKeys : 0;
+  if (steps == 0) {                        // an empty range's part weighs nothing
+    for (int i = threadIdx.x; i < 2 * kTileRows && row0 + i < all; i += kThreads)
+      p.part_lse[p.part(split, row0 + i, hk)] = -INFINITY;
+    return;
+  }
+
+  if (threadIdx.x == 0) {
+    ctl[1] = *reinterpret_cast<volatile unsigned int *>(&g_error_flag) != 0 ? 1u : 0u;
+    ctl[2] = 0;
+    for (int i = 0; i < NR; ++i) {
+      mbar_init(bar(L::kFull + i), 4);
+      mbar_init(bar(L::kEmpty + i), 1);
+    }
+    for (int i = 0; i < kMasks; ++i) mbar_init(bar(L::kMask + i), 4);
+    for (int g = 0; g < 2; ++g) {
+      mbar_init(bar(L::kScores + g), 1);
+      mbar_init(bar(L::kWeights + g), 4);
+      mbar_init(bar(L::kOut + g), 1);
+    }
+    mbar_init(bar(L::kDrain), 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (ctl[1]) return;                      // an earlier error has not been taken: nothing is issued
+  constexpr int kMmaWarp = 12;
+  if (warp == kMmaWarp) tmem_alloc(base + L::kOffCtl, 512);
+  // the queries, zero behind the batch and behind d, each tile by half of the threads
+  {
+    const int tile = threadIdx.x >> 8, nvec = p.d / 8;
+    for (int i = threadIdx.x & 255; i < kTileRows * (D / 8); i += 256) {
+      const int r = i / (D / 8), c = i % (D / 8), row = row0 + tile * kTileRows + r;
+      uint4 x = make_uint4(0, 0, 0, 0);
+      if (row < all && c < nvec)
+        x = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)p.q + (int64_t)(row / p.G) * p.q_stride +
+                                             (int64_t)(hk * p.G + row % p.G) * p.d + c * 8);
+      *reinterpret_cast<uint4 *>(sm + tile * L::kTile + c / 8 * kBlock + r * 128 + ((c % 8) ^ (r & 7)) * 16) = x;
+    }
+    fence_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl[0];
+
+  // Wait for a phase; false once any wait of the CTA has run out.
+  auto wait = [&](int which, uint32_t parity) -> bool {
+    const uint32_t at = bar(which);
+    if (mbar_try(at, parity & 1)) return true;
+    const long long t0 = clock64();
+    while (!mbar_try(at, parity & 1)) {
+      if (ctl[2]) return false;
+      if (clock64() - t0 > p.wait_limit) {
+        ctl[2] = 1;
+        raise_timeout();
+      }
+    }
+    return true;
+  };
+
+  if (group == 2) {
+    // ---------------- copies: 32 rows of every tile per warp ----------------
+    share_registers<kRegsCopy, kRegs>();
+    constexpr int CH = D / 8, kPer = 32 / CH;          // 16-byte pieces of a row, rows per instruction
+    constexpr int kLag = 3;                             // tiles in flight before one is reported
+    const int c = lane % CH, sub = lane / CH;
+    const bool inside = c * 8 < p.d;
+    int told = 0;
+    auto tell = [&](int upto) {                         // tiles before `upto` are there
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0)
+        for (int s = told; s < upto; ++s) mbar_arrive(bar(L::kFull + s % NR));
+      told = upto;
+    };
+    auto ready = [&](int s) -> bool {                   // the ring's place for tile s is free
+      if (s < NR) return true;
+      if (__all_sync(0xffffffffu, mbar_try(bar(L::kEmpty + s % NR), (s / NR - 1) & 1))) return true;
+      cp_async_wait<0>();
+      tell(s);
+      return __all_sync(0xffffffffu, wait(L::kEmpty + s % NR, s / NR - 1));
+    };
+    auto page_row = [&](int step) -> int64_t {          // this lane's token of a step
+      const int j = j0 + step * kKeys + quad * 32 + lane;
+      return j < j1 ? p.row(j, hk) : -1;
+    };
+    int64_t next = page_row(0);
+    bool ok = true;
+    for (int i = 0; ok && i < steps; ++i) {
+      const int64_t row = next;
+      if (i + 1 < steps) next = page_row(i + 1);
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        const int s = 2 * i + kv;
+        if (!(ok = ready(s))) break;
+        if (kv == 0) {
+          const uint32_t live = __ballot_sync(0xffffffffu, row >= 0);
+          if (lane == 0) {
+            masks[i % kMasks * 4 + quad] = live;
+            mbar_arrive(bar(L::kMask + i % kMasks));
+          }
+        }
+        const __nv_bfloat16 *from = (const __nv_bfloat16 *)(kv ? p.v : p.k);
+        const uint32_t to = base + L::kOffRing + s % NR * L::kTile + c / 8 * kBlock;
+#pragma unroll
+        for (int k = 0; k < 32 / kPer; ++k) {
+          const int r = k * kPer + sub;
+          const int64_t at = __shfl_sync(0xffffffffu, row, r);
+          const bool live = at >= 0 && inside;
+          copy16(to + (quad * 32 + r) * 128 + ((c % 8) ^ (r & 7)) * 16, from + (live ? at + c * 8 : 0), live);
+        }
+        cp_async_commit();
+        if (s >= kLag) {
+          cp_async_wait<kLag>();
+          tell(s - kLag + 1);
+        }
+      }
+    }
+    cp_async_wait<0>();
+    if (ok) tell(2 * steps);
+  } else if (group == 3) {
+    share_registers<kRegsMma, kRegs>();
+    if (warp == kMmaWarp && elect_one()) {
+      // ---------------- products ----------------
+      const int ks = (p.d + 15) / 16;                   // K steps over d
+      auto scores = [&](int g, int s) {                 // S of tile g with the K tile s
+        const Desc q = desc_k(base + g * L::kTile), k = desc_k(base + L::kOffRing + s % NR * L::kTile);
+#pragma unroll 2
+        for (int x = 0; x < ks; ++x) {
+          const uint32_t off = x / 4 * kBlock + x % 4 * 32;
+          mma_bf16(tmem + g * 128, q.at(off), k.at(off), idesc_bf16(128, 128), x > 0);
+        }
+        mma_commit(bar(L::kScores + g));
+      };
+      bool ok = wait(L::kFull, 0);
+      if (ok) {
+        tc_fence_after();
+        for (int g = 0; g < active; ++g) scores(g, 0);
+        mma_commit(bar(L::kEmpty));
+      }
+      for (int i = 0; ok && i < steps; ++i) {
+        const int sv = 2 * i + 1, sk = 2 * i + 2;
+        for (int g = 0; ok && g < active; ++g) {
+          if (!(ok = wait(L::kWeights + g, i) && wait(L::kFull + sv % NR, sv / NR))) break;
+          tc_fence_after();
+          const Desc v = desc_mn(base + L::kOffRing + sv % NR * L::kTile, kBlock);
+#pragma unroll
+          for (int x = 0; x < kKeys / 16; ++x)
+            mma_bf16_ts(tmem + kColO + g * D, tmem + g * 128 + 8 * x, v.at(x * 2048), idesc_bf16(128, D) | kIdescMnB, i + x > 0);
+          mma_commit(bar(L::kOut + g));
+          if (g + 1 == active) mma_commit(bar(L::kEmpty + sv % NR));
+          if (i + 1 == steps) continue;
+          // the next scores go over the weights that this product reads
+          if (!(ok = wait(L::kFull + sk % NR, sk / NR) && wait(L::kOut + g, i))) break;
+          tc_fence_after();
+          scores(g, sk);
+          if (g + 1 == active) mma_commit(bar(L::kEmpty + sk % NR));
+        }
+      }
+      // every product issued has completed before the memory it uses goes
+      mma_commit(bar(L::kDrain));
+      if (!mbar_wait_for(bar(L::kDrain), 0, kDrainLimitCycles)) raise_timeout();
+    }
+  } else {
+    // ---------------- softmax: a row per thread ----------------
+    share_registers<kRegsSoftmax, kRegs>();
+    const int g = group, row = row0 + g * kTileRows + quad * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16), at_s = lanes + g * 128, at_o = lanes + kColO + g * D;
+    const float scale = p.scale * 1.44269504088896340736f;               // scores in powers of two
+    const uint64_t scale2 = pair(scale, scale);
+    float m = -INFINITY;                                // the reference
+    float l = 0.f;
+    if (g < active) {
+      for (int i = 0; i < steps; ++i) {
+        wait(L::kMask + i % kMasks, i / kMasks);
+        uint32_t mask[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) mask[q] = masks[i % kMasks * 4 + q];
+        const bool whole = (mask[0] & mask[1] & mask[2] & mask[3]) == 0xffffffffu;
+        wait(L::kScores + g, i);
+        __syncwarp();
+        tc_fence_after();
+        uint32_t w[64];
+        auto form = [&](float ref, float &top, uint64_t &sum) {
+          const uint64_t minus = pair(-ref, -ref);
+          uint32_t a[32], b[32];
+          tmem_ld32(at_s, a);
+          tmem_wait_ld();
+          tmem_ld32(at_s + 32, b);
+          if (whole) weigh<false>(a, scale2, minus, 0, top, sum, w);
+          else weigh<true>(a, scale2, minus, mask[0], top, sum, w);
+          tmem_wait_ld();
+          tmem_ld32(at_s + 64, a);
+          if (whole) weigh<false>(b, scale2, minus, 0, top, sum, w + 16);
+          else weigh<true>(b, scale2, minus, mask[1], top, sum, w + 16);
+          tmem_wait_ld();
+          tmem_ld32(at_s + 96, b);
+          if (whole) weigh<false>(a, scale2, minus, 0, top, sum, w + 32);
+          else weigh<true>(a, scale2, minus, mask[2], top, sum, w + 32);
+          tmem_wait_ld();
+          if (whole) weigh<false>(b, scale2, minus, 0, top, sum, w + 48);
+          else weigh<true>(b, scale2, minus, mask[3], top, sum, w + 48);
+        };
+        float top = -INFINITY;
+        uint64_t sum = 0;
+        form(m == -INFINITY ? 0.f : m, top, sum);
+        if (__any_sync(0xffffffffu, top > (m == -INFINITY ? -INFINITY : kSlack))) {
+          // a new reference: the maximum, where it has passed the old one
+          const float old = m;
+          if (top > (old == -INFINITY ? -INFINITY : 0.f)) m = (old == -INFINITY ? 0.f : old) + top;
+          const float keep = m == old ? 1.f : exp2_fast(old - m);
+          l *= keep;
+          if (i > 0) {
+#pragma unroll 1
+            for (int q = 0; q < D / 16; ++q) {
+              float x[16];
+              tmem_ld16(at_o + q * 16, x);
+              tmem_wait_ld();
+              uint32_t y[16];
+#pragma unroll
+              for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(x[e] * keep);
+              tmem_st16(at_o + q * 16, y);
+            }
+          }
+          top = -INFINITY;
+          sum = 0;
+          form(m == -INFINITY ? 0.f : m, top, sum);
+        }
+        l += pair_sum(sum);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t y[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) y[e] = w[q * 16 + e];
+          tmem_st16(at_s + q * 16, y);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kWeights + g));
+      }
+      wait(L::kOut + g, steps - 1);
+      __syncwarp();
+      tc_fence_after();
+      const float f = l == 0.f ? 0.f : 1.f / l;
+      const int64_t at = row < all ? p.part(split, row, hk) : 0;
+#pragma unroll 1
+      for (int q = 0; q < D / 16; ++q) {
+        float x[16];
+        tmem_ld16(at_o + q * 16, x);
+        tmem_wait_ld();
+        if (row >= all) continue;
+#pragma unroll
+        for (int e = 0; e < 16; e += 4)
+          if (q * 16 + e < p.d)
+            *reinterpret_cast<float4 *>(p.part_o + at * p.d + q * 16 + e) =
+                make_float4(x[e] * f, x[e + 1] * f, x[e + 2] * f, x[e + 3] * f);
+      }
+      if (row < all) p.part_lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+      tc_fence_before();
+    }
+  }
+  __syncthreads();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+// The launch's registers have to be the number that the roles' shares start
+// from, or a role would wait for registers that nobody gives.
+template <int D> bool registers_as_planned() {
+  static const bool ok = [] {
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, shared_tc_kernel<D>) == cudaSuccess && a.numRegs == kRegs;
+  }();
+  return ok;
+}
+
+template <int D> cudaError_t launch(const PrefixParams &p, cudaStream_t stream) {
+  using L = Layout<D>;
+  if (!registers_as_planned<D>()) return cudaErrorInvalidConfiguration;
+  const cudaError_t e = cudaFuncSetAttribute(shared_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kBytes);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = ((int64_t)p.B * p.G + 2 * kTileRows - 1) / (2 * kTileRows);
+  return launch_dependent(shared_tc_kernel<D>, dim3((unsigned)(tiles * p.Hk), (unsigned)p.splits), dim3(kThreads), L::kBytes,
+                          stream, p);
+}
+
+}  // namespace
+
+// Ranges of the prefix with the least time, in microseconds: a CTA's start and
+// end, its steps, and the parts that the join reads and writes.
+int shared_tc_splits(int64_t B, int G, int Hk, int64_t d, int64_t tokens) {
+  const int64_t items = (B * G + 2 * kTileRows - 1) / (2 * kTileRows) * Hk, steps = (tokens + kKeys - 1) / kKeys;
+  const double row_us = (double)B * G * Hk * d * 8e-6 / 4.;
+  const int64_t slots = sm_count();
+  int best = 1;
+  double least = 1e300;
+  for (int n = 1; n <= kMaxPrefixParts && n <= steps; ++n) {
+    const double cost = (double)((items * n + slots - 1) / slots) * (8. + 1.3 * (double)((steps + n - 1) / n)) + row_us * n;
+    if (cost < least) {
+      least = cost;
+      best = n;
+    }
+  }
+  return best;
+}
+
+cudaError_t launch_shared_tc(const PrefixParams &p, cudaStream_t stream) {
+  return p.d <= 64 ? launch<64>(p, stream) : launch<128>(p, stream);
+}
+
+}  // namespace attnres

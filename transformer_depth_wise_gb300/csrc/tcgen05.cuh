@@ -1,7 +1,7 @@
 // tcgen05.cuh -- inline-PTX wrappers for the 5th-generation tensor cores
 // (tcgen05.mma with operands in shared memory and the accumulator in tensor
-// memory) and their shared-memory matrix descriptors, used by the phase-1
-// kernels.  sm_100 family only.
+// memory), their shared-memory matrix descriptors and a role's registers.
+// sm_100 family only.
 #pragma once
 
 #include <stdint.h>
@@ -62,5 +62,48 @@ __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
+// A role's share of the registers: it gives some of the launch's back, or
+// takes some that others have given.
+template <int N, int LAUNCHED> __device__ __forceinline__ void share_registers() {
+  static_assert(N % 8 == 0 && N >= 24 && N <= 256, "what the instruction takes");
+  if constexpr (N < LAUNCHED) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+  if constexpr (N > LAUNCHED) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// D[tmem] += A[tmem] B: the left operand from tensor memory, a row per lane.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+// 16 columns of this thread's tensor-memory lane.
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&w)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]), "r"(w[8]),
+        "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15]) : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+  return one != 0;
+}
+
+// Descriptors from a tile's address: K-major tiles (groups of eight rows 1024
+// bytes apart) and MN-major ones; `d` moves along them by whole 16-byte units.
+struct Desc {
+  uint32_t lo;
+  __device__ __forceinline__ uint64_t at(uint32_t bytes) const {
+    return ((uint64_t)((1024u >> 4) | (1u << 14) | (2u << 29)) << 32) | (lo + (bytes >> 4));
+  }
+};
+__device__ __forceinline__ Desc desc_k(uint32_t addr) { return {((addr & 0x3FFFFu) >> 4) | 1u << 16}; }
+__device__ __forceinline__ Desc desc_mn(uint32_t addr, uint32_t lbo) { return {((addr & 0x3FFFFu) >> 4) | (lbo >> 4) << 16}; }
 
 }  // namespace attnres
