@@ -68,6 +68,10 @@ __device__ __forceinline__ float exp2_fast(float x) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
+// This thread's arrival at a barrier, once its copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 // 32 columns of this thread's tensor-memory lane.
 __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
   asm volatile(
@@ -140,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     ctl[1] = *reinterpret_cast<volatile unsigned int *>(&g_error_flag) != 0 ? 1u : 0u;
     ctl[2] = 0;
     for (int i = 0; i < NR; ++i) {
-      mbar_init(bar(L::kFull + i), 4);
+      mbar_init(bar(L::kFull + i), 128);
       mbar_init(bar(L::kEmpty + i), 1);
     }
     for (int i = 0; i < kMasks; ++i) mbar_init(bar(L::kMask + i), 4);
@@ -193,24 +197,8 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     // ---------------- copies: 32 rows of every tile per warp ----------------
     share_registers<kRegsCopy, kRegs>();
     constexpr int CH = D / 8, kPer = 32 / CH;          // 16-byte pieces of a row, rows per instruction
-    constexpr int kLag = 3;                             // tiles in flight before one is reported
     const int c = lane % CH, sub = lane / CH;
     const bool inside = c * 8 < p.d;
-    int told = 0;
-    auto tell = [&](int upto) {                         // tiles before `upto` are there
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0)
-        for (int s = told; s < upto; ++s) mbar_arrive(bar(L::kFull + s % NR));
-      told = upto;
-    };
-    auto ready = [&](int s) -> bool {                   // the ring's place for tile s is free
-      if (s < NR) return true;
-      if (__all_sync(0xffffffffu, mbar_try(bar(L::kEmpty + s % NR), (s / NR - 1) & 1))) return true;
-      cp_async_wait<0>();
-      tell(s);
-      return __all_sync(0xffffffffu, wait(L::kEmpty + s % NR, s / NR - 1));
-    };
     auto page_row = [&](int step) -> int64_t {          // this lane's token of a step
       const int j = j0 + step * kKeys + quad * 32 + lane;
       return j < j1 ? p.row(j, hk) : -1;
@@ -223,7 +211,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
         const int s = 2 * i + kv;
-        if (!(ok = ready(s))) break;
+        if (s >= NR && !(ok = __all_sync(0xffffffffu, wait(L::kEmpty + s % NR, s / NR - 1)))) break;
         if (kv == 0) {
           const uint32_t live = __ballot_sync(0xffffffffu, row >= 0);
           if (lane == 0) {
@@ -240,15 +228,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           const bool live = at >= 0 && inside;
           copy16(to + (quad * 32 + r) * 128 + ((c % 8) ^ (r & 7)) * 16, from + (live ? at + c * 8 : 0), live);
         }
-        cp_async_commit();
-        if (s >= kLag) {
-          cp_async_wait<kLag>();
-          tell(s - kLag + 1);
-        }
+        copies_arrive(bar(L::kFull + s % NR));
       }
     }
     cp_async_wait<0>();
-    if (ok) tell(2 * steps);
   } else if (group == 3) {
     share_registers<kRegsMma, kRegs>();
     if (warp == kMmaWarp && elect_one()) {
@@ -263,7 +246,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         }
         mma_commit(bar(L::kScores + g));
       };
-      bool ok = wait(L::kFull, 0);
+      // A tile's copies are seen here through its barrier; the fence orders them before the products' reads.
+      auto landed = [&](int s) -> bool {
+        if (!wait(L::kFull + s % NR, s / NR)) return false;
+        fence_async_smem();
+        return true;
+      };
+      bool ok = landed(0);
       if (ok) {
         tc_fence_after();
         for (int g = 0; g < active; ++g) scores(g, 0);
@@ -272,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       for (int i = 0; ok && i < steps; ++i) {
         const int sv = 2 * i + 1, sk = 2 * i + 2;
         for (int g = 0; ok && g < active; ++g) {
-          if (!(ok = wait(L::kWeights + g, i) && wait(L::kFull + sv % NR, sv / NR))) break;
+          if (!(ok = landed(sv) && wait(L::kWeights + g, i))) break;
           tc_fence_after();
           const Desc v = desc_mn(base + L::kOffRing + sv % NR * L::kTile, kBlock);
 #pragma unroll
@@ -282,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           if (g + 1 == active) mma_commit(bar(L::kEmpty + sv % NR));
           if (i + 1 == steps) continue;
           // the next scores go over the weights that this product reads
-          if (!(ok = wait(L::kFull + sk % NR, sk / NR) && wait(L::kOut + g, i))) break;
+          if (!(ok = landed(sk) && wait(L::kOut + g, i))) break;
           tc_fence_after();
           scores(g, sk);
           if (g + 1 == active) mma_commit(bar(L::kEmpty + sk % NR));
