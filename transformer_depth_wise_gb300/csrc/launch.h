@@ -252,6 +252,17 @@ struct HeadNormBackwardArgs {
 int head_norm_backward_ctas();   // CTAs that fill the current device
 cudaError_t launch_head_norm_backward(const HeadNormBackwardArgs &a);
 
+// A (sequence, key head) pair that its CTA begins and another one ends (b < 0: none).
+struct Cut {
+  int b, hk, last;             // the sequence, the key head, the last CTA with a part of it
+  int slot;                    // of the beginning's part
+};
+// Where a pair's result lies: in the outputs (first < 0), or in parts, one of
+// each CTA first .. last: row 2 first + slot, then 2 c of the later ones.
+struct Pieces {
+  int first, last, slot;
+};
+
 struct PagedArgs {
   const void *q;               // [B, Hq, d]
   int64_t q_stride;
@@ -268,11 +279,18 @@ struct PagedArgs {
   void *workspace;             // paged_workspace_bytes()
   cudaStream_t stream;
   bool out_f32;                // out is fp32 whatever the type
+  bool wait_last;              // started early by the kernel before, which it waits for at its end
+  Pieces *pieces;              // [B, Hk]: the caller joins the pairs that are cut (nullptr: joined here)
 };
 bool paged_supported(int64_t d, int dtype);
 // CTAs the split runs on the current device, and the workspace they need.
 int paged_ctas(int64_t d, int dtype);
 int64_t paged_workspace_bytes(int G, int64_t d, int dtype);
+// The parts in a workspace: [ctas][2][G][d] and [ctas][2][G].
+struct PagedParts {
+  float *o, *lse;
+};
+PagedParts paged_parts(void *workspace, int G, int64_t d, int dtype);
 cudaError_t launch_paged(const PagedArgs &a);
 
 struct SharedArgs {
@@ -293,11 +311,12 @@ struct SharedArgs {
   void *workspace;             // SharedLayout::bytes
   cudaStream_t stream;
 };
-// A workspace: the paged kernel's own, then lse and outputs of the prefix's
-// parts and of the sequences' own one, in bytes from its start.
+// A workspace: the paged kernel's own and its pairs' pieces, then lse and
+// outputs of the prefix's parts and of the sequences' own one, in bytes from
+// its start.
 struct SharedLayout {
   int splits;                  // parts of the prefix
-  int64_t part_lse, part_o, bytes;
+  int64_t pieces, part_lse, part_o, bytes;
 };
 // `tokens`: what the prefix's table covers.
 SharedLayout shared_layout(int64_t B, int Hq, int Hk, int64_t d, int dtype, int64_t tokens);

@@ -34,12 +34,6 @@ namespace {
 
 constexpr int kTile = 64;              // tokens per tile of the split
 
-// A pair that its CTA begins and another one ends (b < 0: none).
-struct Cut {
-  int b, hk, last;                     // the sequence, the key head, the last CTA with a part of it
-  int slot;                            // of the beginning's part
-};
-
 struct PagedParams {
   const void *q, *k, *v;
   int64_t q_stride;                    // elements from one sequence's queries to the next
@@ -49,10 +43,12 @@ struct PagedParams {
   int64_t num_pages;
   float scale;
   void *out;                           // [B, Hq, d]
+  bool wait_last;                      // the kernel before is waited for at the end: nothing of it is read here
   bool out_f32;                        // out in fp32 whatever the type (a part of a longer attention)
   float *lse;                          // [B, Hq] or nullptr
   float *part_o, *part_lse;            // [ctas][2][G][d], [ctas][2][G]
   Cut *cuts;                           // [ctas]
+  Pieces *pieces;                      // [B, Hk] or nullptr: where each pair's parts are, for a join elsewhere
   __device__ __forceinline__ int page_of(int j) const { return page_shift >= 0 ? j >> page_shift : j / page; }
   __device__ __forceinline__ int slot_of(int j) const { return page_shift >= 0 ? j & (page - 1) : j % page; }
 };
@@ -140,14 +136,19 @@ __device__ __forceinline__ Walk walk_begin(const PagedParams &p, int64_t total) 
   return w;
 }
 
-// One thread: note the pair that the walk's piece begins and does not end.
+// One thread: note the pair that the walk's piece begins.
 __device__ __forceinline__ void note_cut(const PagedParams &p, const Walk &w, int slot, int64_t total) {
   const int64_t last_tile = w.pair + w.tiles - 1;
   const int ctas = gridDim.x;
+  if (w.whole()) {
+    if (p.pieces) p.pieces[(int64_t)w.b * p.Hk + w.hk] = {-1, 0, 0};
+    return;
+  }
   int c = (int)(last_tile * ctas / total);
   while (range_begin(total, c + 1, ctas) <= last_tile) ++c;
   while (range_begin(total, c, ctas) > last_tile) --c;
-  p.cuts[blockIdx.x] = {w.b, w.hk, c, slot};
+  if (p.pieces) p.pieces[(int64_t)w.b * p.Hk + w.hk] = {(int)blockIdx.x, c, slot};
+  else p.cuts[blockIdx.x] = {w.b, w.hk, c, slot};
 }
 
 // Sequences without tokens: zeros and -infinity, dealt out over the CTAs.
@@ -162,6 +163,8 @@ __device__ __forceinline__ void write_empty(const PagedParams &p) {
     }
     if (p.lse)
       for (int i = threadIdx.x; i < p.Hq; i += blockDim.x) p.lse[(int64_t)b * p.Hq + i] = -INFINITY;
+    if (p.pieces)
+      for (int i = threadIdx.x; i < p.Hk; i += blockDim.x) p.pieces[(int64_t)b * p.Hk + i] = {-1, 0, 0};
   }
 }
 
@@ -215,7 +218,7 @@ __global__ void __launch_bounds__(kWarpsF * 32, resident(NV, GQ)) paged_f32_kern
   constexpr int E = 4, N = NV * E;
   extern __shared__ float sm[];                     // [warps][GQ][d] outputs, then [warps][GQ] m, then l
   __shared__ int64_t red[kWarpsF];
-  grid_dependency_wait();
+  if (!p.wait_last) grid_dependency_wait();
   const int64_t total = all_tiles(p, red) * p.Hk;
   Walk w = walk_begin(p, total);
   if (threadIdx.x == 0) p.cuts[blockIdx.x].b = -1;
@@ -370,10 +373,12 @@ __global__ void __launch_bounds__(kWarpsF * 32, resident(NV, GQ)) paged_f32_kern
       x.x *= r; x.y *= r; x.z *= r; x.w *= r;
       store_piece<float>(p, w, w.at == first ? 0 : 1, head, e, x, L == 0.f ? -INFINITY : M + logf(L));
     }
-    if (threadIdx.x == 0 && w.begins() && !w.whole()) note_cut(p, w, w.at == first ? 0 : 1, total);
+    if (threadIdx.x == 0 && w.begins()) note_cut(p, w, w.at == first ? 0 : 1, total);
     __syncthreads();
   }
   write_empty<float>(p);
+  // One CTA's wait holds the launch's end until the kernel before has ended.
+  if (p.wait_last && blockIdx.x + 1 == gridDim.x) grid_dependency_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -442,7 +447,7 @@ __global__ void __launch_bounds__(kWarpsM * 32, MmaShape<D>::kCtas) paged_mma_ke
   __shared__ float smax[kWarpsM][16], ssum[kWarpsM][16];
   __shared__ uint32_t live_bits[kWarpsM][S::kStages];
   float *so = reinterpret_cast<float *>(smem + kWarpsM * S::kStages * S::kStage);   // [16][kOutPitch]
-  grid_dependency_wait();
+  if (!p.wait_last) grid_dependency_wait();
   const int64_t total = all_tiles(p, red) * p.Hk;
   Walk w = walk_begin(p, total);
   if (threadIdx.x == 0) p.cuts[blockIdx.x].b = -1;
@@ -666,11 +671,13 @@ __global__ void __launch_bounds__(kWarpsM * 32, MmaShape<D>::kCtas) paged_mma_ke
       store_piece<__nv_bfloat16>(p, w, w.at == first ? 0 : 1, g, e, x,
                                  L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994530942f);
     }
-    if (threadIdx.x == 0 && w.begins() && !w.whole()) note_cut(p, w, w.at == first ? 0 : 1, total);
+    if (threadIdx.x == 0 && w.begins()) note_cut(p, w, w.at == first ? 0 : 1, total);
     __syncthreads();                                // the shared results are read
   }
   cp_async_wait<0>();
   write_empty<__nv_bfloat16>(p);
+  // One CTA's wait holds the launch's end until the kernel before has ended.
+  if (p.wait_last && blockIdx.x + 1 == gridDim.x) grid_dependency_wait();
 }
 
 // One CTA per (noted pair, query head): the parts' weights, then their sum.
@@ -749,6 +756,12 @@ int64_t paged_workspace_bytes(int G, int64_t d, int dtype) {
   return ctas * (int64_t)sizeof(Cut) + ctas * 2 * G * (d + 1) * (int64_t)sizeof(float);
 }
 
+PagedParts paged_parts(void *workspace, int G, int64_t d, int dtype) {
+  const int ctas = paged_ctas(d, dtype);
+  float *o = reinterpret_cast<float *>(static_cast<Cut *>(workspace) + ctas);
+  return {o, o + (int64_t)ctas * 2 * G * d};
+}
+
 cudaError_t launch_paged(const PagedArgs &a) {
   PagedParams p{};
   p.q = a.q; p.k = a.k_cache; p.v = a.v_cache; p.q_stride = a.q_stride;
@@ -758,11 +771,12 @@ cudaError_t launch_paged(const PagedArgs &a) {
   p.page_shift = -1;
   for (int i = 0; i < 31; ++i)
     if (a.page_size == 1 << i) p.page_shift = i;
-  p.scale = a.scale; p.out = a.out; p.lse = a.lse; p.out_f32 = a.out_f32;
+  p.scale = a.scale; p.out = a.out; p.lse = a.lse; p.out_f32 = a.out_f32; p.wait_last = a.wait_last; p.pieces = a.pieces;
   const int ctas = paged_ctas(a.d, a.dtype);
   p.cuts = static_cast<Cut *>(a.workspace);
-  p.part_o = reinterpret_cast<float *>(p.cuts + ctas);
-  p.part_lse = p.part_o + (int64_t)ctas * 2 * p.G * p.d;
+  const PagedParts parts = paged_parts(a.workspace, p.G, a.d, a.dtype);
+  p.part_o = parts.o;
+  p.part_lse = parts.lse;
   const dim3 grid((unsigned)ctas), join((unsigned)ctas, (unsigned)p.G);
   const size_t join_smem = ((size_t)(ctas + 3) / 4 * 4 + (size_t)kJoinWarps * a.d) * sizeof(float);
   cudaError_t err;
@@ -777,7 +791,7 @@ cudaError_t launch_paged(const PagedArgs &a) {
     err = a.d <= 64 ? go(std::integral_constant<int, 64>{}) : a.d <= 96 ? go(std::integral_constant<int, 96>{})
         : a.d <= 128 ? go(std::integral_constant<int, 128>{}) : a.d <= 192 ? go(std::integral_constant<int, 192>{})
         : go(std::integral_constant<int, 256>{});
-    if (err != cudaSuccess) return err;
+    if (err != cudaSuccess || p.pieces) return err;
     return launch_dependent(paged_join_kernel<__nv_bfloat16>, join, dim3(kJoinWarps * 32), join_smem, a.stream, p);
   }
   auto go = [&](auto NV) -> cudaError_t {
@@ -795,7 +809,7 @@ cudaError_t launch_paged(const PagedArgs &a) {
   const int nv = (a.d / 4 + 7) / 8;
   err = nv <= 2 ? go(std::integral_constant<int, 2>{}) : nv <= 4 ? go(std::integral_constant<int, 4>{})
                 : go(std::integral_constant<int, 8>{});
-  if (err != cudaSuccess) return err;
+  if (err != cudaSuccess || p.pieces) return err;
   return launch_dependent(paged_join_kernel<float>, join, dim3(kJoinWarps * 32), join_smem, a.stream, p);
 }
 

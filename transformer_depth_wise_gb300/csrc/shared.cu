@@ -9,8 +9,8 @@
 // instead of once per sequence.  The rows' tiles and the prefix's ranges are
 // dealt out over the CTAs; each leaves its part, normalised, with its lse.
 // The sequences' own tokens go through the kernel of attnres_paged_attention,
-// which leaves one more part, and a last kernel joins the parts by the
-// online-softmax merge (OS2).
+// which leaves one more part (or several, of a sequence that its split has
+// cut), and a last kernel joins the parts by the online-softmax merge (OS2).
 //
 // This file: the parts of the prefix in fp32 arithmetic for any type and
 // width, and the join.  A tile of 64 rows and 32 tokens at a time goes through
@@ -50,6 +50,7 @@ __global__ void __launch_bounds__(kThreads) shared_prefix_kernel(const PrefixPar
   float *qs = sm, *ks = qs + kRows * P, *vs = ks + kKeys * P, *ps = vs + kKeys * P;
   __shared__ int live[kKeys];
   grid_dependency_wait();
+  launch_dependents();
   const int tiles = (p.B * p.G + kRows - 1) / kRows;
   const int hk = blockIdx.x / tiles, row0 = (blockIdx.x - hk * tiles) * kRows, split = blockIdx.y;
   const int n = p.tokens();
@@ -160,42 +161,104 @@ __global__ void __launch_bounds__(kThreads) shared_prefix_kernel(const PrefixPar
   }
 }
 
-// One warp per (sequence, query head): the parts' weights by their lse, then
-// their weighted sum, part after part in order.
-template <typename T>
-__global__ void __launch_bounds__(kThreads) shared_join_kernel(const float *part_o, const float *part_lse, int parts,
-                                                               int64_t rows, int d, T *out, float *lse) {
+// What the join reads: parts [splits + 1][rows] of the prefix and, where a
+// pair's own tokens were not cut, of those; else their pieces.
+struct JoinParams {
+  const float *part_o, *part_lse, *piece_o, *piece_lse;
+  const Pieces *pieces;                    // [B, Hk]
+  int splits, Hq, G, d;
+  int64_t rows;                            // B Hq
+  void *out;
+  float *lse;
+};
+
+// WARPS warps per (sequence, query head), 32 parts at a time: their weights by
+// their lse, a lane each, then their weighted sum, a warp taking every
+// WARPS-th part, in an order that is always the same.
+constexpr int kJoinWarps = 8;
+
+template <typename T, int WARPS>
+__global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const JoinParams p) {
+  __shared__ float4 sums[WARPS == 1 ? 1 : kJoinWarps][WARPS == 1 ? 1 : 64];
   grid_dependency_wait();
-  const int64_t row = (int64_t)blockIdx.x * (kThreads / 32) + threadIdx.x / 32;
-  const int lane = threadIdx.x % 32;
-  if (row >= rows) return;
-  float M = -INFINITY;
-  for (int k = lane; k < parts; k += 32) M = fmaxf(M, part_lse[k * rows + row]);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int64_t row = WARPS == 1 ? (int64_t)blockIdx.x * kJoinWarps + warp : blockIdx.x;
+  const int first = WARPS == 1 ? 0 : warp, d = p.d;
+  if (row >= p.rows) return;
+  const int head = (int)(row % p.Hq), hk = head / p.G, g = head % p.G;
+  const Pieces own = p.pieces[row / p.Hq * (p.Hq / p.G) + hk];
+  const int parts = own.first < 0 ? p.splits + 1 : p.splits + own.last - own.first + 1;
+  // part k as a row of part_o, or of piece_o
+  auto row_of = [&](int k) -> int64_t {
+    if (k < p.splits || own.first < 0) return k * p.rows + row;
+    const int c = k - p.splits;
+    return ((int64_t)(own.first + c) * 2 + (c == 0 ? own.slot : 0)) * p.G + g;
+  };
+  auto piece = [&](int k) { return k >= p.splits && own.first >= 0; };
+  auto lse_of = [&](int k) { return k < parts ? (piece(k) ? p.piece_lse : p.part_lse)[row_of(k)] : -INFINITY; };
+  const float x0 = lse_of(lane);
+  float M = x0, L = 0.f;
+  for (int k = lane + 32; k < parts; k += 32) M = fmaxf(M, lse_of(k));
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-  float L = 0.f;
-  for (int k = 0; k < parts; ++k) {
-    const float x = part_lse[k * rows + row];
-    L += x == -INFINITY ? 0.f : expf(x - M);
-  }
-  const float f = L == 0.f ? 0.f : 1.f / L;
-  for (int e = lane * 4; e < d; e += 128) {
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = 0; k < parts; ++k) {
-      const float x = part_lse[k * rows + row];
-      if (x == -INFINITY) continue;        // a part without a weight may hold nothing
-      const float w = expf(x - M) * f;
-      const float4 y = *reinterpret_cast<const float4 *>(part_o + (k * rows + row) * d + e);
-      s.x = fmaf(y.x, w, s.x);
-      s.y = fmaf(y.y, w, s.y);
-      s.z = fmaf(y.z, w, s.z);
-      s.w = fmaf(y.w, w, s.w);
+  float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int k0 = 0; k0 < parts; k0 += 32) {
+    const float x = k0 == 0 ? x0 : lse_of(k0 + lane);
+    const float w = x == -INFINITY ? 0.f : expf(x - M);
+    L += w;
+    const int n = min(32, parts - k0);
+#pragma unroll 4
+    for (int k = first; k < n; k += WARPS) {
+      const float h = __shfl_sync(0xffffffffu, w, k);
+      const float *src = (piece(k0 + k) ? p.piece_o : p.part_o) + row_of(k0 + k) * d + lane * 4;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (h != 0.f && lane * 4 + i * 128 < d)        // a part without a weight may hold nothing
+          y = *reinterpret_cast<const float4 *>(src + i * 128);
+        s[i].x = fmaf(y.x, h, s[i].x);
+        s[i].y = fmaf(y.y, h, s[i].y);
+        s[i].z = fmaf(y.z, h, s[i].z);
+        s[i].w = fmaf(y.w, h, s[i].w);
+      }
     }
-    T *dst = out + row * d + e;
-    if constexpr (std::is_same<T, float>::value) *reinterpret_cast<float4 *>(dst) = s;
-    else *reinterpret_cast<uint2 *>(dst) = make_uint2(Elt<T>::pack_word(s.x, s.y), Elt<T>::pack_word(s.z, s.w));
   }
-  if (lane == 0 && lse) lse[row] = L == 0.f ? -INFINITY : M + logf(L);
+  L = team_sum_shfl<32>(L);
+  const float f = L == 0.f ? 0.f : 1.f / L;
+  if (WARPS > 1) {
+    sums[warp][lane] = s[0];
+    sums[warp][lane + 32] = s[1];
+    __syncthreads();
+    if (warp > 0) return;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int e = lane * 4 + i * 128;
+    if (e >= d) break;
+    float4 y = s[i];
+    if (WARPS > 1) {
+#pragma unroll
+      for (int k = 1; k < WARPS; ++k) {
+        const float4 z = sums[k][i * 32 + lane];
+        y.x += z.x;
+        y.y += z.y;
+        y.z += z.z;
+        y.w += z.w;
+      }
+    }
+    y.x *= f; y.y *= f; y.z *= f; y.w *= f;
+    T *dst = (T *)p.out + row * d + e;
+    if constexpr (std::is_same<T, float>::value) *reinterpret_cast<float4 *>(dst) = y;
+    else *reinterpret_cast<uint2 *>(dst) = make_uint2(Elt<T>::pack_word(y.x, y.y), Elt<T>::pack_word(y.z, y.w));
+  }
+  if (lane == 0 && p.lse) p.lse[row] = L == 0.f ? -INFINITY : M + logf(L);
+}
+
+template <typename T> cudaError_t launch_join(const JoinParams &p, cudaStream_t stream) {
+  if (p.rows >= 8 * (int64_t)sm_count())
+    return launch_dependent(shared_join_kernel<T, 1>, dim3((unsigned)((p.rows + kJoinWarps - 1) / kJoinWarps)),
+                            dim3(kJoinWarps * 32), 0, stream, p);
+  return launch_dependent(shared_join_kernel<T, kJoinWarps>, dim3((unsigned)p.rows), dim3(kJoinWarps * 32), 0, stream, p);
 }
 
 // Ranges that the prefix is cut into so that the CTAs fill the GPU's SMs
@@ -231,7 +294,8 @@ SharedLayout shared_layout(int64_t B, int Hq, int Hk, int64_t d, int dtype, int6
   if (B > 0 && tokens > 0)
     w.splits = shared_tc_supported(d, dtype) ? shared_tc_splits(B, G, Hk, d, tokens) : general_splits(B, G, Hk, tokens);
   const int64_t rows = B * Hq, parts = w.splits + 1;
-  w.part_lse = up16(paged_workspace_bytes(G, d, dtype));
+  w.pieces = up16(paged_workspace_bytes(G, d, dtype));
+  w.part_lse = w.pieces + up16(B * Hk * (int64_t)sizeof(Pieces));
   w.part_o = w.part_lse + up16(parts * rows * (int64_t)sizeof(float));
   w.bytes = w.part_o + parts * rows * d * (int64_t)sizeof(float);
   return w;
@@ -260,21 +324,23 @@ cudaError_t launch_shared(const SharedArgs &a) {
         : a.dtype == ATTNRES_BF16         ? launch_general<__nv_bfloat16>(p, a.stream)
                                           : launch_general<float>(p, a.stream);
   if (e != cudaSuccess) return e;
-  // the sequences' own tokens: the last part
+  // The sequences' own tokens: the last part.  It needs nothing of the prefix's
+  // kernel, which lets it start as soon as all of its own CTAs have (they have
+  // waited for what came before), so it fills the SMs that that one leaves, and
+  // waits for its end at its own.
   PagedArgs s{};
   s.q = a.q; s.q_stride = a.q_stride; s.k_cache = a.k_cache; s.v_cache = a.v_cache; s.num_pages = a.num_pages;
   s.page_size = a.page_size; s.max_pages = a.max_pages; s.page_table = a.page_table; s.lengths = a.lengths;
   s.B = a.B; s.Hq = a.Hq; s.Hk = a.Hk; s.d = a.d; s.dtype = a.dtype; s.scale = a.scale;
   s.out = p.part_o + w.splits * rows * a.d; s.lse = p.part_lse + w.splits * rows; s.out_f32 = true;
-  s.workspace = ws; s.stream = a.stream;
+  s.workspace = ws; s.stream = a.stream; s.wait_last = w.splits > 0;
+  s.pieces = reinterpret_cast<Pieces *>(ws + w.pieces);
   if ((e = launch_paged(s)) != cudaSuccess) return e;
-  const dim3 grid((unsigned)((rows + kThreads / 32 - 1) / (kThreads / 32)));
-  if (a.dtype == ATTNRES_BF16)
-    return launch_dependent(shared_join_kernel<__nv_bfloat16>, grid, dim3(kThreads), 0, a.stream, (const float *)p.part_o,
-                            (const float *)p.part_lse, w.splits + 1, rows, a.d, static_cast<__nv_bfloat16 *>(a.out),
-                            a.lse);
-  return launch_dependent(shared_join_kernel<float>, grid, dim3(kThreads), 0, a.stream, (const float *)p.part_o,
-                          (const float *)p.part_lse, w.splits + 1, rows, a.d, static_cast<float *>(a.out), a.lse);
+  JoinParams j{};
+  const PagedParts own = paged_parts(ws, p.G, a.d, a.dtype);
+  j.part_o = p.part_o; j.part_lse = p.part_lse; j.piece_o = own.o; j.piece_lse = own.lse; j.pieces = s.pieces;
+  j.splits = w.splits; j.Hq = a.Hq; j.G = p.G; j.d = a.d; j.rows = rows; j.out = a.out; j.lse = a.lse;
+  return a.dtype == ATTNRES_BF16 ? launch_join<__nv_bfloat16>(j, a.stream) : launch_join<float>(j, a.stream);
 }
 
 }  // namespace attnres

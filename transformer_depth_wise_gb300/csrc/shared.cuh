@@ -10,6 +10,10 @@ namespace attnres {
 
 constexpr int kMaxPrefixParts = 64;      // ranges of the prefix
 
+// The kernel that follows on the stream may start: called by kernels of a
+// prefix's parts, whose follower waits for them at its end only.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 struct PrefixParams {
   const void *q, *k, *v;
   int64_t q_stride;                      // elements from one sequence's queries to the next
@@ -22,7 +26,6 @@ struct PrefixParams {
   int splits;
   long long wait_limit;                  // SM clock cycles a wait of the tensor-core kernel may take
 
-#ifdef __CUDACC__
   // The prefix's tokens, held within what the table covers.
   __device__ __forceinline__ int tokens() const {
     const int n = *length;
@@ -44,7 +47,6 @@ struct PrefixParams {
   __device__ __forceinline__ int64_t part(int split, int r, int hk) const {
     return ((int64_t)split * B + r / G) * Hq + hk * G + r % G;
   }
-#endif
 };
 
 // The parts on the 5th-generation tensor cores (bf16, heads of up to 128
