@@ -4,9 +4,9 @@
 // A CTA takes 256 rows (query heads of one key head, over the sequences) as
 // two tiles of 128, and one range of the prefix's tokens, 128 at a time:
 //   S = Q K^T (M 128, N 128, K d),  P = 2^(scale S - m),  O += P V (M 128, N d, K 128)
-// S and O are fp32 in tensor memory; a thread of a tile's warpgroup has one row
-// of S, so the softmax needs no exchange between threads; P, rounded to bf16,
-// goes back to tensor memory over S, as the left operand of the second
+// S and O are fp32 in tensor memory; two threads have a row of S, half of the
+// tokens each (one per row took 121 us where two take XX: the tensor cores
+// waited for the softmax); P, rounded to bf16, goes back to tensor memory over S, as the left operand of the second
 // product.  While one tile's weights are formed, the tensor cores work on the
 // other's products.
 //
@@ -16,7 +16,7 @@
 // Rounding P to bf16 adds an error of the size of the output's own rounding;
 // the sum is that of the unrounded weights.
 //
-// Roles (a warpgroup each): the two tiles' softmax; copies (cp.async of 16
+// Roles: the two tiles' softmax (two warpgroups each); copies (cp.async of 16
 // bytes a lane, a row's page looked up by its own lane, into a ring of tiles
 // with the 128-byte swizzle; tokens behind the range or on no page arrive as
 // zeros and are masked); and one thread that issues the products.
@@ -36,11 +36,11 @@ namespace {
 
 constexpr int kTileRows = 128;             // rows of a tile: one per thread
 constexpr int kKeys = 128;                 // tokens of a step
-constexpr int kThreads = 512;
+constexpr int kThreads = 768;
 constexpr uint32_t kBlock = 128 * 128;     // bytes: 128 rows of 64 bf16 columns
-constexpr int kRegs = 128;                 // a thread's registers at the launch, then the roles' shares
-constexpr int kRegsSoftmax = 192, kRegsCopy = 64, kRegsMma = 64;
-static_assert(2 * kRegsSoftmax + kRegsCopy + kRegsMma <= 4 * kRegs, "more registers than the launch has");
+constexpr int kRegs = 80;                  // a thread's registers at the launch, then the roles' shares
+constexpr int kRegsSoftmax = 96, kRegsCopy = 48, kRegsMma = 48;
+static_assert(4 * kRegsSoftmax + kRegsCopy + kRegsMma <= 6 * kRegs, "more registers than the launch has");
 constexpr float kSlack = 8.f;              // powers of two that a score may lie above the reference
 constexpr int kMasks = 4;                  // steps whose masks are kept
 
@@ -50,7 +50,8 @@ template <int D> struct Layout {
   static constexpr int kRing = D == 128 ? 5 : 6;                      // tiles of K and V, in turn
   static constexpr uint32_t kOffRing = 2 * kTile;
   static constexpr uint32_t kOffMask = kOffRing + kRing * kTile;
-  static constexpr uint32_t kOffBar = kOffMask + kMasks * 16;
+  static constexpr uint32_t kOffRow = kOffMask + kMasks * 16;         // a float per row
+  static constexpr uint32_t kOffBar = kOffRow + 2 * kTileRows * 4;
   static constexpr uint32_t kOffCtl = kOffBar + (2 * kRing + kMasks + 7) * 8;
   static constexpr uint32_t kBytes = kOffCtl + 16 + 1024;             // and the alignment's slack
   // barriers
@@ -94,7 +95,7 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// A row's weights for 32 tokens: from scores, reference and mask to 16 bf16
+// Weights for 32 tokens of a row: from scores, reference and mask to 16 bf16
 // pairs; `top` takes the largest exponent, `sum` the weights.
 template <bool MASKED>
 __device__ __forceinline__ void weigh(const uint32_t (&s)[32], uint64_t scale2, uint64_t minus, uint32_t mask, float &top,
@@ -113,6 +114,20 @@ __device__ __forceinline__ void weigh(const uint32_t (&s)[32], uint64_t scale2, 
     sum = add2(sum, pair(a, b));
     out[i] = Elt<__nv_bfloat16>::pack_word(a, b);
   }
+}
+
+// Two warps that share rows: a barrier, and one with a vote of their 64 threads.
+__device__ __forceinline__ void pair_barrier(int id) {
+  __syncwarp();
+  asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ bool any_of_pair(int id, bool x) {
+  uint32_t any;
+  __syncwarp();
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %2, 0;\n bar.red.or.pred q, %1, 64, p;\n selp.u32 %0, 1, 0, q;\n}"
+      : "=r"(any) : "r"(id), "r"(x ? 1u : 0u) : "memory");
+  return any != 0;
 }
 
 template <int D>
@@ -151,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     for (int i = 0; i < kMasks; ++i) mbar_init(bar(L::kMask + i), 4);
     for (int g = 0; g < 2; ++g) {
       mbar_init(bar(L::kScores + g), 1);
-      mbar_init(bar(L::kWeights + g), 4);
+      mbar_init(bar(L::kWeights + g), 8);
       mbar_init(bar(L::kOut + g), 1);
     }
     mbar_init(bar(L::kDrain), 1);
@@ -159,13 +174,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   }
   __syncthreads();
   if (ctl[1]) return;                      // an earlier error has not been taken: nothing is issued
-  constexpr int kMmaWarp = 12;
+  constexpr int kMmaWarp = 20;
   if (warp == kMmaWarp) tmem_alloc(base + L::kOffCtl, 512);
-  // the queries, zero behind the batch and behind d, each tile by half of the threads
+  // the queries, zero behind the batch and behind d
   {
-    const int tile = threadIdx.x >> 8, nvec = p.d / 8;
-    for (int i = threadIdx.x & 255; i < kTileRows * (D / 8); i += 256) {
-      const int r = i / (D / 8), c = i % (D / 8), row = row0 + tile * kTileRows + r;
+    const int nvec = p.d / 8;
+    for (int i = threadIdx.x; i < 2 * kTileRows * (D / 8); i += kThreads) {
+      const int r = i / (D / 8) % kTileRows, c = i % (D / 8), tile = i / (D / 8) / kTileRows, row = row0 + tile * kTileRows + r;
       uint4 x = make_uint4(0, 0, 0, 0);
       if (row < all && c < nvec)
         x = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)p.q + (int64_t)(row / p.G) * p.q_stride +
@@ -194,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     return true;
   };
 
-  if (group == 2) {
+  if (group == 4) {
     // ---------------- copies: 32 rows of every tile per warp ----------------
     share_registers<kRegsCopy, kRegs>();
     constexpr int CH = D / 8, kPer = 32 / CH;          // 16-byte pieces of a row, rows per instruction
@@ -233,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       }
     }
     cp_async_wait<0>();
-  } else if (group == 3) {
+  } else if (group == 5) {
     share_registers<kRegsMma, kRegs>();
     if (warp == kMmaWarp && elect_one()) {
       // ---------------- products ----------------
@@ -283,57 +298,60 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       if (!mbar_wait_for(bar(L::kDrain), 0, kDrainLimitCycles)) raise_timeout();
     }
   } else {
-    // ---------------- softmax: a row per thread ----------------
+    // ---------------- softmax: two threads per row, 64 tokens of a step each ----------------
     share_registers<kRegsSoftmax, kRegs>();
-    const int g = group, row = row0 + g * kTileRows + quad * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16), at_s = lanes + g * 128, at_o = lanes + kColO + g * D;
+    const int g = group >> 1, half = group & 1, row = row0 + g * kTileRows + quad * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16), at_s = lanes + g * 128, at_o = lanes + kColO + g * D + half * (D / 2);
+    volatile float *slot = reinterpret_cast<float *>(sm + L::kOffRow) + g * kTileRows + quad * 32 + lane;
+    const int both = 1 + g * 4 + quad;                  // the barrier of the two warps with these rows
+    // f of the two threads' values (the first half's, the second's), for both
+    auto joined = [&](float x, auto f) -> float {
+      if (half == 0) *slot = x;
+      pair_barrier(both);
+      if (half == 1) *slot = f(*slot, x);
+      pair_barrier(both);
+      return *slot;
+    };
     const float scale = p.scale * 1.44269504088896340736f;               // scores in powers of two
     const uint64_t scale2 = pair(scale, scale);
-    float m = -INFINITY;                                // the reference
+    float m = -INFINITY;                                // the reference, the same in both threads
     float l = 0.f;
     if (g < active) {
       for (int i = 0; i < steps; ++i) {
         wait(L::kMask + i % kMasks, i / kMasks);
-        uint32_t mask[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) mask[q] = masks[i % kMasks * 4 + q];
-        const bool whole = (mask[0] & mask[1] & mask[2] & mask[3]) == 0xffffffffu;
+        const uint32_t mask0 = masks[i % kMasks * 4 + half * 2], mask1 = masks[i % kMasks * 4 + half * 2 + 1];
         wait(L::kScores + g, i);
         __syncwarp();
         tc_fence_after();
-        uint32_t w[64];
+        uint32_t w[32];
         auto form = [&](float ref, float &top, uint64_t &sum) {
           const uint64_t minus = pair(-ref, -ref);
           uint32_t a[32], b[32];
-          tmem_ld32(at_s, a);
+          tmem_ld32(at_s + half * 64, a);
+          tmem_ld32(at_s + half * 64 + 32, b);
           tmem_wait_ld();
-          tmem_ld32(at_s + 32, b);
-          if (whole) weigh<false>(a, scale2, minus, 0, top, sum, w);
-          else weigh<true>(a, scale2, minus, mask[0], top, sum, w);
-          tmem_wait_ld();
-          tmem_ld32(at_s + 64, a);
-          if (whole) weigh<false>(b, scale2, minus, 0, top, sum, w + 16);
-          else weigh<true>(b, scale2, minus, mask[1], top, sum, w + 16);
-          tmem_wait_ld();
-          tmem_ld32(at_s + 96, b);
-          if (whole) weigh<false>(a, scale2, minus, 0, top, sum, w + 32);
-          else weigh<true>(a, scale2, minus, mask[2], top, sum, w + 32);
-          tmem_wait_ld();
-          if (whole) weigh<false>(b, scale2, minus, 0, top, sum, w + 48);
-          else weigh<true>(b, scale2, minus, mask[3], top, sum, w + 48);
+          if ((mask0 & mask1) == 0xffffffffu) {
+            weigh<false>(a, scale2, minus, 0, top, sum, w);
+            weigh<false>(b, scale2, minus, 0, top, sum, w + 16);
+          } else {
+            weigh<true>(a, scale2, minus, mask0, top, sum, w);
+            weigh<true>(b, scale2, minus, mask1, top, sum, w + 16);
+          }
         };
         float top = -INFINITY;
         uint64_t sum = 0;
         form(m == -INFINITY ? 0.f : m, top, sum);
-        if (__any_sync(0xffffffffu, top > (m == -INFINITY ? -INFINITY : kSlack))) {
+        // both halves have read their scores, which the weights go over
+        if (any_of_pair(both, top > (m == -INFINITY ? -INFINITY : kSlack))) {
           // a new reference: the maximum, where it has passed the old one
+          top = joined(top, [](float a, float b) { return fmaxf(a, b); });
           const float old = m;
           if (top > (old == -INFINITY ? -INFINITY : 0.f)) m = (old == -INFINITY ? 0.f : old) + top;
           const float keep = m == old ? 1.f : exp2_fast(old - m);
           l *= keep;
           if (i > 0) {
 #pragma unroll 1
-            for (int q = 0; q < D / 16; ++q) {
+            for (int q = 0; q < D / 32; ++q) {
               float x[16];
               tmem_ld16(at_o + q * 16, x);
               tmem_wait_ld();
@@ -346,38 +364,41 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           top = -INFINITY;
           sum = 0;
           form(m == -INFINITY ? 0.f : m, top, sum);
+          pair_barrier(both);
         }
         l += pair_sum(sum);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < 2; ++q) {
           uint32_t y[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) y[e] = w[q * 16 + e];
-          tmem_st16(at_s + q * 16, y);
+          tmem_st16(at_s + half * 32 + q * 16, y);
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(L::kWeights + g));
       }
+      l = joined(l, [](float a, float b) { return a + b; });
       wait(L::kOut + g, steps - 1);
       __syncwarp();
       tc_fence_after();
       const float f = l == 0.f ? 0.f : 1.f / l;
       const int64_t at = row < all ? p.part(split, row, hk) : 0;
 #pragma unroll 1
-      for (int q = 0; q < D / 16; ++q) {
+      for (int q = 0; q < D / 32; ++q) {
         float x[16];
         tmem_ld16(at_o + q * 16, x);
         tmem_wait_ld();
         if (row >= all) continue;
 #pragma unroll
-        for (int e = 0; e < 16; e += 4)
-          if (q * 16 + e < p.d)
-            *reinterpret_cast<float4 *>(p.part_o + at * p.d + q * 16 + e) =
-                make_float4(x[e] * f, x[e + 1] * f, x[e + 2] * f, x[e + 3] * f);
+        for (int e = 0; e < 16; e += 4) {
+          const int c = half * (D / 2) + q * 16 + e;
+          if (c < p.d)
+            *reinterpret_cast<float4 *>(p.part_o + at * p.d + c) = make_float4(x[e] * f, x[e + 1] * f, x[e + 2] * f, x[e + 3] * f);
+        }
       }
-      if (row < all) p.part_lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+      if (row < all && half == 0) p.part_lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
       tc_fence_before();
     }
   }
