@@ -502,9 +502,9 @@ int attnres_shared_prefix_attention(const void *q, int64_t q_stride, const void 
                                     const int32_t *prefix_length, const int32_t *page_table, int max_pages,
                                     const int32_t *lengths, int64_t B, int Hq, int Hk, int64_t d, int dtype, float scale,
                                     void *out, float *lse, void *workspace, int64_t workspace_bytes, void *stream);
-/* Its workspace bytes on the current device: they depend on what the prefix's table covers, not on the lengths. */
+/* Its workspace bytes on the current device: they depend on what the tables cover, not on the lengths. */
 int64_t attnres_shared_prefix_attention_workspace_bytes(int64_t B, int Hq, int Hk, int64_t d, int dtype, int page_size,
-                                                        int prefix_pages);
+                                                        int prefix_pages, int max_pages);
 
 /*
  * Linear attention with one fixed decay per head, over prompts.  (It is not

@@ -291,7 +291,7 @@ def test_graph_with_growing_lengths_and_two_streams(gpu, dtype, d):
     n, lengths = a[4], a[6]
     full = n.clone(), lengths.clone()
     need = api._sized("attnres_shared_prefix_attention_workspace_bytes", gpu, 3, 8, 2, d, api._CODES[dtype], 16,
-                      a[3].numel())
+                      a[3].numel(), a[5].shape[1])
     ws = [torch.full((need,), 255, device=gpu, dtype=torch.uint8) for _ in range(2)]
     sides = [torch.cuda.Stream(gpu) for _ in range(2)]
     graphs, outs = [], []
@@ -376,13 +376,14 @@ def shared(q=FAKE, qs=512, kc=FAKE + 64, vc=FAKE + 128, num=8, page=16, ptab=FAK
 
 
 def test_refusals():
-    size = _lib.lib().attnres_shared_prefix_attention_workspace_bytes
-    need = size(2, 8, 2, 64, 1, 16, 4)
-    assert need > 0 and size(2, 8, 2, 64, 1, 16, 0) > 0 and size(0, 8, 2, 64, 1, 16, 4) > 0
-    assert size(2, 8, 2, 64, 5, 16, 4) == DTYPE and size(2, 8, 3, 64, 1, 16, 4) == SHAPE and size(2, 8, 2, 60, 1, 16, 4) == ALIGN
-    assert size(2, 17, 1, 64, 1, 16, 4) == SHAPE and size(2, 8, 2, 264, 1, 16, 4) == SHAPE and size(-1, 8, 2, 64, 1, 16, 4) == SHAPE
-    assert size(2, 8, 2, 64, 1, 0, 4) == SHAPE and size(2, 8, 2, 64, 1, 16, -1) == SHAPE
-    assert size(2, 8, 2, 64, 1, 1 << 20, 1 << 12) == SHAPE and size(1 << 30, 8, 2, 64, 1, 16, 4) == SHAPE
+    size = lambda B=2, Hq=8, Hk=2, d=64, dtype=1, page=16, pp=4, mp=4: \
+        _lib.lib().attnres_shared_prefix_attention_workspace_bytes(B, Hq, Hk, d, dtype, page, pp, mp)  # noqa: E731
+    need = size()
+    assert need > 0 and size(pp=0) > 0 and size(B=0) > 0 and size(mp=0) > 0
+    assert size(dtype=5) == DTYPE and size(Hk=3) == SHAPE and size(d=60) == ALIGN
+    assert size(Hq=17, Hk=1) == SHAPE and size(d=264) == SHAPE and size(B=-1) == SHAPE
+    assert size(page=0) == SHAPE and size(pp=-1) == SHAPE and size(mp=-1) == SHAPE
+    assert size(page=1 << 20, pp=1 << 12) == SHAPE and size(page=1 << 20, mp=1 << 12) == SHAPE and size(B=1 << 30) == SHAPE
     assert shared(dtype=3) == DTYPE and shared(B=-1) == SHAPE and shared(page=0) == SHAPE and shared(maxp=-1) == SHAPE
     assert shared(pp=-1) == SHAPE and shared(num=-1) == SHAPE and shared(Hq=7) == SHAPE and shared(d=4) == ALIGN
     assert shared(scale=math.inf) == VALUE and shared(scale=math.nan) == VALUE

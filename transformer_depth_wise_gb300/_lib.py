@@ -83,7 +83,7 @@ SIGNATURES = {
     "attnres_paged_attention_workspace_bytes": (_i64, [_int, _int, _i64, _int]),
     "attnres_shared_prefix_attention": (_int, [_vp, _i64, _vp, _vp, _i64, _int, _vp, _int, _vp, _vp, _int, _vp, _i64,
                                                _int, _int, _i64, _int, _f, _vp, _vp, _vp, _i64, _vp]),
-    "attnres_shared_prefix_attention_workspace_bytes": (_i64, [_i64, _int, _int, _i64, _int, _int, _int]),
+    "attnres_shared_prefix_attention_workspace_bytes": (_i64, [_i64, _int, _int, _i64, _int, _int, _int, _int]),
     "attnres_linear_attention": (_int, [_vp, _vp, _vp, _i64, _i64, _int, _i64, _i64, _int, _i64, _i64, _i64, _vp, _f,
                                         _vp, _vp, _vp, _vp, _vp, _i64, _vp]),
     "attnres_linear_attention_workspace_bytes": (_i64, [_i64, _i64, _int, _i64, _i64, _int]),

@@ -1048,7 +1048,8 @@ def shared_prefix_attention(q, k_cache, v_cache, prefix_table, prefix_length, pa
         _plain(lse, "lse", torch.float32, (B, Hq), dev)
     need = 0
     if workspace is None:
-        need = _sized("attnres_shared_prefix_attention_workspace_bytes", dev, B, Hq, Hk, d, code, page_size, pages)
+        need = _sized("attnres_shared_prefix_attention_workspace_bytes", dev, B, Hq, Hk, d, code, page_size, pages,
+                      max_pages)
     ws, wp, wn = _workspace(workspace, need, dev)
     _call("attnres_shared_prefix_attention", dev, q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), num_pages,
           page_size, prefix_table.data_ptr(), pages, prefix_length.data_ptr(), page_table.data_ptr(), max_pages,

@@ -277,7 +277,7 @@ int64_t attnres_paged_attention_workspace_bytes(int Hq, int Hk, int64_t d, int d
   if (Hk < 1 || Hq < Hk || Hq > kMaxHeads || Hq % Hk || Hq / Hk > kMaxGroup || d < 1) return ATTNRES_ERR_SHAPE;
   if (d % vec_elems(dtype)) return ATTNRES_ERR_ALIGNMENT;
   if (!paged_supported(d, dtype)) return ATTNRES_ERR_SHAPE;
-  return paged_workspace_bytes(Hq / Hk, d, dtype);
+  return paged_workspace_bytes(Hq / Hk, d, dtype, paged_ctas(d, dtype));
 }
 
 int attnres_paged_attention(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
@@ -302,18 +302,18 @@ int attnres_paged_attention(const void *q, int64_t q_stride, const void *k_cache
   a.q = q; a.q_stride = q_stride; a.k_cache = k_cache; a.v_cache = v_cache; a.num_pages = num_pages;
   a.page_size = page_size; a.max_pages = num_pages > 0 ? max_pages : 0; a.page_table = page_table; a.lengths = lengths;
   a.B = B; a.Hq = Hq; a.Hk = Hk; a.d = (int)d; a.dtype = dtype; a.scale = scale; a.out = out; a.lse = lse;
-  a.workspace = workspace; a.stream = static_cast<cudaStream_t>(stream);
+  a.workspace = workspace; a.stream = static_cast<cudaStream_t>(stream); a.ctas = paged_ctas(d, dtype);
   return cuda_status(launch_paged(a));
 }
 
 int64_t attnres_shared_prefix_attention_workspace_bytes(int64_t B, int Hq, int Hk, int64_t d, int dtype, int page_size,
-                                                        int prefix_pages) {
+                                                        int prefix_pages, int max_pages) {
   const int64_t own = attnres_paged_attention_workspace_bytes(Hq, Hk, d, dtype);
   if (own < 0) return own;
-  const int st = check_pages(0, page_size, prefix_pages);
-  if (st) return st;
+  int st = check_pages(0, page_size, prefix_pages);
+  if (st || (st = check_pages(0, page_size, max_pages))) return st;
   if (B < 0 || B > INT32_MAX / 64 / Hq) return ATTNRES_ERR_SHAPE;      // rows and grids stay within 32 bits
-  return shared_layout(B, Hq, Hk, d, dtype, (int64_t)page_size * prefix_pages).bytes;
+  return shared_layout(B, Hq, Hk, d, dtype, (int64_t)page_size * prefix_pages, (int64_t)page_size * max_pages).bytes;
 }
 
 int attnres_shared_prefix_attention(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
@@ -321,11 +321,11 @@ int attnres_shared_prefix_attention(const void *q, int64_t q_stride, const void 
                                     const int32_t *prefix_length, const int32_t *page_table, int max_pages,
                                     const int32_t *lengths, int64_t B, int Hq, int Hk, int64_t d, int dtype, float scale,
                                     void *out, float *lse, void *workspace, int64_t workspace_bytes, void *stream) {
-  const int64_t need = attnres_shared_prefix_attention_workspace_bytes(B, Hq, Hk, d, dtype, page_size, prefix_pages);
+  const int64_t need = attnres_shared_prefix_attention_workspace_bytes(B, Hq, Hk, d, dtype, page_size, prefix_pages, max_pages);
   if (need < 0) return (int)need;
   int st = check_stride(q_stride, Hq * d, dtype, false);
   if (st) return st;
-  if ((st = check_pages(num_pages, page_size, max_pages))) return st;
+  if (num_pages < 0) return ATTNRES_ERR_SHAPE;
   if (!std::isfinite(scale)) return ATTNRES_ERR_VALUE;
   if (B == 0) return ATTNRES_OK;
   if (!q || !lengths || !out || !workspace || (prefix_pages && !prefix_length)) return ATTNRES_ERR_NULL;

@@ -278,6 +278,7 @@ struct PagedArgs {
   float *lse;                  // [B, Hq] or nullptr
   void *workspace;             // paged_workspace_bytes()
   cudaStream_t stream;
+  int ctas;                    // paged_ctas(), or paged_fine_ctas()
   bool out_f32;                // out is fp32 whatever the type
   bool wait_last;              // started early by the kernel before, which it waits for at its end
   Pieces *pieces;              // [B, Hk]: the caller joins the pairs that are cut (nullptr: joined here)
@@ -285,12 +286,13 @@ struct PagedArgs {
 bool paged_supported(int64_t d, int dtype);
 // CTAs the split runs on the current device, and the workspace they need.
 int paged_ctas(int64_t d, int dtype);
-int64_t paged_workspace_bytes(int G, int64_t d, int dtype);
+int paged_fine_ctas(int64_t d, int dtype);   // in shorter ranges, for SMs that come free one after the other
+int64_t paged_workspace_bytes(int G, int64_t d, int dtype, int64_t ctas);
 // The parts in a workspace: [ctas][2][G][d] and [ctas][2][G].
 struct PagedParts {
   float *o, *lse;
 };
-PagedParts paged_parts(void *workspace, int G, int64_t d, int dtype);
+PagedParts paged_parts(void *workspace, int G, int64_t d, int64_t ctas);
 cudaError_t launch_paged(const PagedArgs &a);
 
 struct SharedArgs {
@@ -316,10 +318,11 @@ struct SharedArgs {
 // its start.
 struct SharedLayout {
   int splits;                  // parts of the prefix
+  int own_ctas;                // of the own tokens' kernel
   int64_t pieces, part_lse, part_o, bytes;
 };
-// `tokens`: what the prefix's table covers.
-SharedLayout shared_layout(int64_t B, int Hq, int Hk, int64_t d, int dtype, int64_t tokens);
+// tokens, own: what the prefix's table and a sequence's cover.
+SharedLayout shared_layout(int64_t B, int Hq, int Hk, int64_t d, int dtype, int64_t tokens, int64_t own);
 cudaError_t launch_shared(const SharedArgs &a);
 
 // out_i = alpha sum_{j <= i} e^{g (i - j)} (a_i . b_j) c_j + carry e^{g (i + first_pow)} a_i . first, through the state

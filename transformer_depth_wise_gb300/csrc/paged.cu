@@ -750,16 +750,15 @@ bool paged_supported(int64_t d, int dtype) {
 }
 // Two CTAs per SM but for bf16 heads wider than 128, whose rings fill the shared memory.
 int paged_ctas(int64_t d, int dtype) { return (dtype == ATTNRES_BF16 && d > 128 ? 1 : 2) * sm_count(); }
+int paged_fine_ctas(int64_t d, int dtype) { return 4 * paged_ctas(d, dtype); }
 
-int64_t paged_workspace_bytes(int G, int64_t d, int dtype) {
-  const int64_t ctas = paged_ctas(d, dtype);
+int64_t paged_workspace_bytes(int G, int64_t d, int dtype, int64_t ctas) {
   return ctas * (int64_t)sizeof(Cut) + ctas * 2 * G * (d + 1) * (int64_t)sizeof(float);
 }
 
-PagedParts paged_parts(void *workspace, int G, int64_t d, int dtype) {
-  const int ctas = paged_ctas(d, dtype);
+PagedParts paged_parts(void *workspace, int G, int64_t d, int64_t ctas) {
   float *o = reinterpret_cast<float *>(static_cast<Cut *>(workspace) + ctas);
-  return {o, o + (int64_t)ctas * 2 * G * d};
+  return {o, o + ctas * 2 * G * d};
 }
 
 cudaError_t launch_paged(const PagedArgs &a) {
@@ -772,9 +771,9 @@ cudaError_t launch_paged(const PagedArgs &a) {
   for (int i = 0; i < 31; ++i)
     if (a.page_size == 1 << i) p.page_shift = i;
   p.scale = a.scale; p.out = a.out; p.lse = a.lse; p.out_f32 = a.out_f32; p.wait_last = a.wait_last; p.pieces = a.pieces;
-  const int ctas = paged_ctas(a.d, a.dtype);
+  const int ctas = a.ctas;
   p.cuts = static_cast<Cut *>(a.workspace);
-  const PagedParts parts = paged_parts(a.workspace, p.G, a.d, a.dtype);
+  const PagedParts parts = paged_parts(a.workspace, p.G, a.d, ctas);
   p.part_o = parts.o;
   p.part_lse = parts.lse;
   const dim3 grid((unsigned)ctas), join((unsigned)ctas, (unsigned)p.G);

@@ -172,55 +172,66 @@ struct JoinParams {
   float *lse;
 };
 
-// WARPS warps per (sequence, query head), 32 parts at a time: their weights by
-// their lse, a lane each, then their weighted sum, a warp taking every
-// WARPS-th part, in an order that is always the same.
+// WARPS warps per (sequence, query head), 32 parts at a time: a lane finds a
+// part and its weight by its lse, then a warp adds every WARPS-th part, in an
+// order that is always the same.
 constexpr int kJoinWarps = 8;
 
 template <typename T, int WARPS>
 __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const JoinParams p) {
   __shared__ float4 sums[WARPS == 1 ? 1 : kJoinWarps][WARPS == 1 ? 1 : 64];
   grid_dependency_wait();
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const int64_t row = WARPS == 1 ? (int64_t)blockIdx.x * kJoinWarps + warp : blockIdx.x;
-  const int first = WARPS == 1 ? 0 : warp, d = p.d;
-  if (row >= p.rows) return;
-  const int head = (int)(row % p.Hq), hk = head / p.G, g = head % p.G;
-  const Pieces own = p.pieces[row / p.Hq * (p.Hq / p.G) + hk];
-  const int parts = own.first < 0 ? p.splits + 1 : p.splits + own.last - own.first + 1;
-  // part k as a row of part_o, or of piece_o
-  auto row_of = [&](int k) -> int64_t {
-    if (k < p.splits || own.first < 0) return k * p.rows + row;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, first = warp % WARPS, d = p.d;
+  const int64_t row = (int64_t)blockIdx.x * (kJoinWarps / WARPS) + warp / WARPS;
+  const bool live = row < p.rows;
+  const int head = (int)((live ? row : 0) % p.Hq), hk = head / p.G, g = head % p.G;
+  Pieces own{-1, 0, 0};
+  if (live) own = p.pieces[row / p.Hq * (p.Hq / p.G) + hk];
+  const int parts = !live ? 0 : own.first < 0 ? p.splits + 1 : p.splits + own.last - own.first + 1;
+  // part k's row, in part_o or in piece_o, and its lse
+  auto find = [&](int k, const float *&src) -> float {
+    src = p.part_o;
+    if (k >= parts) return -INFINITY;
+    if (k < p.splits || own.first < 0) {
+      const int64_t at = k * p.rows + row;
+      src = p.part_o + at * d;
+      return p.part_lse[at];
+    }
     const int c = k - p.splits;
-    return ((int64_t)(own.first + c) * 2 + (c == 0 ? own.slot : 0)) * p.G + g;
+    const int64_t at = ((int64_t)(own.first + c) * 2 + (c == 0 ? own.slot : 0)) * p.G + g;
+    src = p.piece_o + at * d;
+    return p.piece_lse[at];
   };
-  auto piece = [&](int k) { return k >= p.splits && own.first >= 0; };
-  auto lse_of = [&](int k) { return k < parts ? (piece(k) ? p.piece_lse : p.part_lse)[row_of(k)] : -INFINITY; };
-  const float x0 = lse_of(lane);
+  const float *src0, *src;
+  const float x0 = find(lane, src0);
   float M = x0, L = 0.f;
-  for (int k = lane + 32; k < parts; k += 32) M = fmaxf(M, lse_of(k));
+  for (int k = lane + 32; k < parts; k += 32) M = fmaxf(M, find(k, src));
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
   float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
   for (int k0 = 0; k0 < parts; k0 += 32) {
-    const float x = k0 == 0 ? x0 : lse_of(k0 + lane);
+    src = src0;
+    const float x = k0 == 0 ? x0 : find(k0 + lane, src);
     const float w = x == -INFINITY ? 0.f : expf(x - M);
     L += w;
     const int n = min(32, parts - k0);
 #pragma unroll 4
     for (int k = first; k < n; k += WARPS) {
       const float h = __shfl_sync(0xffffffffu, w, k);
-      const float *src = (piece(k0 + k) ? p.piece_o : p.part_o) + row_of(k0 + k) * d + lane * 4;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (h != 0.f && lane * 4 + i * 128 < d)        // a part without a weight may hold nothing
-          y = *reinterpret_cast<const float4 *>(src + i * 128);
-        s[i].x = fmaf(y.x, h, s[i].x);
-        s[i].y = fmaf(y.y, h, s[i].y);
-        s[i].z = fmaf(y.z, h, s[i].z);
-        s[i].w = fmaf(y.w, h, s[i].w);
+      const float *from = reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, (unsigned long long)src, k)) + lane * 4;
+      float4 y = make_float4(0.f, 0.f, 0.f, 0.f), z = y;
+      if (h != 0.f) {                      // a part without a weight may hold nothing
+        if (lane * 4 < d) y = *reinterpret_cast<const float4 *>(from);
+        if (d > 128 && lane * 4 + 128 < d) z = *reinterpret_cast<const float4 *>(from + 128);
       }
+      s[0].x = fmaf(y.x, h, s[0].x);
+      s[0].y = fmaf(y.y, h, s[0].y);
+      s[0].z = fmaf(y.z, h, s[0].z);
+      s[0].w = fmaf(y.w, h, s[0].w);
+      s[1].x = fmaf(z.x, h, s[1].x);
+      s[1].y = fmaf(z.y, h, s[1].y);
+      s[1].z = fmaf(z.z, h, s[1].z);
+      s[1].w = fmaf(z.w, h, s[1].w);
     }
   }
   L = team_sum_shfl<32>(L);
@@ -229,8 +240,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const Join
     sums[warp][lane] = s[0];
     sums[warp][lane + 32] = s[1];
     __syncthreads();
-    if (warp > 0) return;
+    if (first > 0) return;
   }
+  if (!live) return;
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int e = lane * 4 + i * 128;
@@ -239,7 +251,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const Join
     if (WARPS > 1) {
 #pragma unroll
       for (int k = 1; k < WARPS; ++k) {
-        const float4 z = sums[k][i * 32 + lane];
+        const float4 z = sums[warp + k][i * 32 + lane];
         y.x += z.x;
         y.y += z.y;
         y.z += z.z;
@@ -255,10 +267,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const Join
 }
 
 template <typename T> cudaError_t launch_join(const JoinParams &p, cudaStream_t stream) {
-  if (p.rows >= 8 * (int64_t)sm_count())
-    return launch_dependent(shared_join_kernel<T, 1>, dim3((unsigned)((p.rows + kJoinWarps - 1) / kJoinWarps)),
-                            dim3(kJoinWarps * 32), 0, stream, p);
-  return launch_dependent(shared_join_kernel<T, kJoinWarps>, dim3((unsigned)p.rows), dim3(kJoinWarps * 32), 0, stream, p);
+  auto go = [&](auto warps) -> cudaError_t {
+    constexpr int W = decltype(warps)::value, R = kJoinWarps / W;
+    return launch_dependent(shared_join_kernel<T, W>, dim3((unsigned)((p.rows + R - 1) / R)), dim3(kJoinWarps * 32), 0, stream,
+                            p);
+  };
+  return p.splits < 4 ? go(std::integral_constant<int, 1>{}) : p.splits < 24 ? go(std::integral_constant<int, 4>{})
+                                                                          : go(std::integral_constant<int, 8>{});
 }
 
 // Ranges that the prefix is cut into so that the CTAs fill the GPU's SMs
@@ -288,13 +303,18 @@ int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
 
 }  // namespace
 
-SharedLayout shared_layout(int64_t B, int Hq, int Hk, int64_t d, int dtype, int64_t tokens) {
+SharedLayout shared_layout(int64_t B, int Hq, int Hk, int64_t d, int dtype, int64_t tokens, int64_t own) {
   SharedLayout w{};
   const int G = Hq / Hk;
   if (B > 0 && tokens > 0)
     w.splits = shared_tc_supported(d, dtype) ? shared_tc_splits(B, G, Hk, d, tokens) : general_splits(B, G, Hk, tokens);
   const int64_t rows = B * Hq, parts = w.splits + 1;
-  w.pieces = up16(paged_workspace_bytes(G, d, dtype));
+  // Behind a prefix's kernel the SMs come free one after the other: ranges
+  // of a quarter of the length even that out, where the tables leave each of
+  // them 16 tiles of 64 tokens or more.
+  w.own_ctas = paged_ctas(d, dtype);
+  if (w.splits && B * Hk * (own / 64) >= 16 * (int64_t)paged_fine_ctas(d, dtype)) w.own_ctas = paged_fine_ctas(d, dtype);
+  w.pieces = up16(paged_workspace_bytes(G, d, dtype, w.own_ctas));
   w.part_lse = w.pieces + up16(B * Hk * (int64_t)sizeof(Pieces));
   w.part_o = w.part_lse + up16(parts * rows * (int64_t)sizeof(float));
   w.bytes = w.part_o + parts * rows * d * (int64_t)sizeof(float);
@@ -303,7 +323,7 @@ SharedLayout shared_layout(int64_t B, int Hq, int Hk, int64_t d, int dtype, int6
 
 cudaError_t launch_shared(const SharedArgs &a) {
   const int64_t tokens = (int64_t)a.prefix_pages * a.page_size;
-  const SharedLayout w = shared_layout(a.B, a.Hq, a.Hk, a.d, a.dtype, tokens);
+  const SharedLayout w = shared_layout(a.B, a.Hq, a.Hk, a.d, a.dtype, tokens, (int64_t)a.max_pages * a.page_size);
   char *ws = static_cast<char *>(a.workspace);
   const int64_t rows = a.B * a.Hq;
   PrefixParams p{};
@@ -333,11 +353,11 @@ cudaError_t launch_shared(const SharedArgs &a) {
   s.page_size = a.page_size; s.max_pages = a.max_pages; s.page_table = a.page_table; s.lengths = a.lengths;
   s.B = a.B; s.Hq = a.Hq; s.Hk = a.Hk; s.d = a.d; s.dtype = a.dtype; s.scale = a.scale;
   s.out = p.part_o + w.splits * rows * a.d; s.lse = p.part_lse + w.splits * rows; s.out_f32 = true;
-  s.workspace = ws; s.stream = a.stream; s.wait_last = w.splits > 0;
+  s.workspace = ws; s.stream = a.stream; s.wait_last = w.splits > 0; s.ctas = w.own_ctas;
   s.pieces = reinterpret_cast<Pieces *>(ws + w.pieces);
   if ((e = launch_paged(s)) != cudaSuccess) return e;
   JoinParams j{};
-  const PagedParts own = paged_parts(ws, p.G, a.d, a.dtype);
+  const PagedParts own = paged_parts(ws, p.G, a.d, w.own_ctas);
   j.part_o = p.part_o; j.part_lse = p.part_lse; j.piece_o = own.o; j.piece_lse = own.lse; j.pieces = s.pieces;
   j.splits = w.splits; j.Hq = a.Hq; j.G = p.G; j.d = a.d; j.rows = rows; j.out = a.out; j.lse = a.lse;
   return a.dtype == ATTNRES_BF16 ? launch_join<__nv_bfloat16>(j, a.stream) : launch_join<float>(j, a.stream);

@@ -37,11 +37,15 @@ struct PrefixParams {
     from = (int)(tiles * split / splits) * TILE;
     to = min(n, (int)(tiles * (split + 1) / splits) * TILE);
   }
-  // The cache row of token j: element offset, or -1 for a page outside the pool.
-  __device__ __forceinline__ int64_t row(int j, int hk) const {
+  // The cache row of token j as a number and as an element offset; -1 for a page outside the pool.
+  __device__ __forceinline__ int64_t row_number(int j, int hk) const {
     const int64_t pg = table[page_shift >= 0 ? j >> page_shift : j / page];
     if (pg < 0 || pg >= num_pages) return -1;
-    return ((pg * Hk + hk) * page + (page_shift >= 0 ? j & (page - 1) : j % page)) * d;
+    return (pg * Hk + hk) * page + (page_shift >= 0 ? j & (page - 1) : j % page);
+  }
+  __device__ __forceinline__ int64_t row(int j, int hk) const {
+    const int64_t r = row_number(j, hk);
+    return r < 0 ? r : r * d;
   }
   // The part's row of row r (sequence r / G, head r % G of key head hk).
   __device__ __forceinline__ int64_t part(int split, int r, int hk) const {

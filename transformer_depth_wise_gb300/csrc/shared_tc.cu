@@ -10,11 +10,13 @@
 // product.  While one tile's weights are formed, the tensor cores work on the
 // other's products.
 //
-// m is a reference, not the maximum: it moves only when a score passes it by
-// 2^8, and O and the sum are rescaled then (fp32 holds what 2^8 adds).  So the
-// scores are read once, and the maximum is taken beside the exponentials.
-// Rounding P to bf16 adds an error of the size of the output's own rounding;
-// the sum is that of the unrounded weights.
+// m is a reference, not the maximum: it moves, to the maximum, only when the
+// weights that a thread forms in a step add up to more than 2^10 (and at the
+// first step), and O and the sum are rescaled then; fp32 and bf16 hold what lies
+// above it.  So a step needs no maximum: four instructions for a pair of
+// scores, of which a maximum would be a fourth more.  Rounding P to bf16 adds an
+// error of the size of the output's own rounding; the sum is that of the
+// unrounded weights.
 //
 // Roles: the two tiles' softmax (two warpgroups each); copies (cp.async of 16
 // bytes a lane, a row's page looked up by its own lane, into a ring of tiles
@@ -41,7 +43,7 @@ constexpr uint32_t kBlock = 128 * 128;     // bytes: 128 rows of 64 bf16 columns
 constexpr int kRegs = 80;                  // a thread's registers at the launch, then the roles' shares
 constexpr int kRegsSoftmax = 96, kRegsCopy = 48, kRegsMma = 48;
 static_assert(4 * kRegsSoftmax + kRegsCopy + kRegsMma <= 6 * kRegs, "more registers than the launch has");
-constexpr float kSlack = 8.f;              // powers of two that a score may lie above the reference
+constexpr float kMost = 1024.f;            // the sum of a thread's weights of a step that the reference may stay for
 constexpr int kMasks = 4;                  // steps whose masks are kept
 
 template <int D> struct Layout {
@@ -65,6 +67,9 @@ __device__ __forceinline__ float exp2_fast(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
@@ -95,11 +100,10 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
-// Weights for 32 tokens of a row: from scores, reference and mask to 16 bf16
-// pairs; `top` takes the largest exponent, `sum` the weights.
-template <bool MASKED>
-__device__ __forceinline__ void weigh(const uint32_t (&s)[32], uint64_t scale2, uint64_t minus, uint32_t mask, float &top,
-                                      uint64_t &sum, uint32_t *out) {
+// The exponents of 32 tokens of a row, from scores, reference and mask, two at
+// a time to f.
+template <bool MASKED, typename F>
+__device__ __forceinline__ void exponents(const uint32_t (&s)[32], uint64_t scale2, uint64_t minus, uint32_t mask, F f) {
 #pragma unroll
   for (int i = 0; i < 16; ++i) {
     float a, b;
@@ -108,11 +112,7 @@ __device__ __forceinline__ void weigh(const uint32_t (&s)[32], uint64_t scale2, 
       if (!(mask >> (2 * i) & 1u)) a = -INFINITY;
       if (!(mask >> (2 * i + 1) & 1u)) b = -INFINITY;
     }
-    top = fmaxf(top, fmaxf(a, b));
-    a = exp2_fast(a);
-    b = exp2_fast(b);
-    sum = add2(sum, pair(a, b));
-    out[i] = Elt<__nv_bfloat16>::pack_word(a, b);
+    f(i, a, b);
   }
 }
 
@@ -215,6 +215,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     constexpr int CH = D / 8, kPer = 32 / CH;          // 16-byte pieces of a row, rows per instruction
     const int c = lane % CH, sub = lane / CH;
     const bool inside = c * 8 < p.d;
+    const bool side = p.page % 32 == 0 && p.d == D;     // 32 tokens never span two pages, and rows have no padding
+    const uint32_t mine = c / 8 * kBlock + (quad * 32 + sub) * 128;
+    // 16-byte piece c % 8 of row k kPer + sub of the warp, in the swizzle's place
+    auto swizzled = [&](int k) -> uint32_t { return ((c % 8) ^ ((k * kPer + sub) & 7)) * 16; };
+    bool alive = false;                                 // all of the warp's tokens are on a page
     auto page_row = [&](int step) -> int64_t {          // this lane's token of a step
       const int j = j0 + step * kKeys + quad * 32 + lane;
       return j < j1 ? p.row(j, hk) : -1;
@@ -230,19 +235,27 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         if (s >= NR && !(ok = __all_sync(0xffffffffu, wait(L::kEmpty + s % NR, s / NR - 1)))) break;
         if (kv == 0) {
           const uint32_t live = __ballot_sync(0xffffffffu, row >= 0);
+          alive = live == 0xffffffffu;
           if (lane == 0) {
             masks[i % kMasks * 4 + quad] = live;
             mbar_arrive(bar(L::kMask + i % kMasks));
           }
         }
-        const __nv_bfloat16 *from = (const __nv_bfloat16 *)(kv ? p.v : p.k);
-        const uint32_t to = base + L::kOffRing + s % NR * L::kTile + c / 8 * kBlock;
+        const char *from = reinterpret_cast<const char *>(kv ? p.v : p.k);
+        const uint32_t to = base + L::kOffRing + s % NR * L::kTile + mine;
+        if (side && alive) {
+          // the warp's rows lie side by side in one page
+          const char *src = from + (__shfl_sync(0xffffffffu, row, 0) + sub * p.d + c * 8) * 2;
+          const int step = kPer * p.d * 2;
 #pragma unroll
-        for (int k = 0; k < 32 / kPer; ++k) {
-          const int r = k * kPer + sub;
-          const int64_t at = __shfl_sync(0xffffffffu, row, r);
-          const bool live = at >= 0 && inside;
-          copy16(to + (quad * 32 + r) * 128 + ((c % 8) ^ (r & 7)) * 16, from + (live ? at + c * 8 : 0), live);
+          for (int k = 0; k < 32 / kPer; ++k, src += step) copy16(to + k * kPer * 128 + swizzled(k), src);
+        } else {
+#pragma unroll 4
+          for (int k = 0; k < 32 / kPer; ++k) {
+            const int64_t at = __shfl_sync(0xffffffffu, row, k * kPer + sub);
+            const bool live = at >= 0 && inside;
+            copy16(to + k * kPer * 128 + swizzled(k), from + (live ? (at + c * 8) * 2 : 0), live);
+          }
         }
         copies_arrive(bar(L::kFull + s % NR));
       }
@@ -277,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       for (int i = 0; ok && i < steps; ++i) {
         const int sv = 2 * i + 1, sk = 2 * i + 2;
         for (int g = 0; ok && g < active; ++g) {
-          if (!(ok = landed(sv) && wait(L::kWeights + g, i))) break;
+          if (!(ok = (g > 0 || landed(sv)) && wait(L::kWeights + g, i))) break;
           tc_fence_after();
           const Desc v = desc_mn(base + L::kOffRing + sv % NR * L::kTile, kBlock);
 #pragma unroll
@@ -287,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           if (g + 1 == active) mma_commit(bar(L::kEmpty + sv % NR));
           if (i + 1 == steps) continue;
           // the next scores go over the weights that this product reads
-          if (!(ok = landed(sk) && wait(L::kOut + g, i))) break;
+          if (!(ok = (g > 0 || landed(sk)) && wait(L::kOut + g, i))) break;
           tc_fence_after();
           scores(g, sk);
           if (g + 1 == active) mma_commit(bar(L::kEmpty + sk % NR));
@@ -323,29 +336,39 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         wait(L::kScores + g, i);
         __syncwarp();
         tc_fence_after();
-        uint32_t w[32];
-        auto form = [&](float ref, float &top, uint64_t &sum) {
+        uint32_t w[32], a[32], b[32];
+        // f of the exponents of this thread's tokens (m as an fp32 number)
+        auto each = [&](float ref, auto f) {
           const uint64_t minus = pair(-ref, -ref);
-          uint32_t a[32], b[32];
           tmem_ld32(at_s + half * 64, a);
-          tmem_ld32(at_s + half * 64 + 32, b);
           tmem_wait_ld();
-          if ((mask0 & mask1) == 0xffffffffu) {
-            weigh<false>(a, scale2, minus, 0, top, sum, w);
-            weigh<false>(b, scale2, minus, 0, top, sum, w + 16);
-          } else {
-            weigh<true>(a, scale2, minus, mask0, top, sum, w);
-            weigh<true>(b, scale2, minus, mask1, top, sum, w + 16);
-          }
+          tmem_ld32(at_s + half * 64 + 32, b);
+          if (mask0 == 0xffffffffu) exponents<false>(a, scale2, minus, 0, f);
+          else exponents<true>(a, scale2, minus, mask0, f);
+          tmem_wait_ld();
+          auto g2 = [&](int i, float x, float y) { f(i + 16, x, y); };
+          if (mask1 == 0xffffffffu) exponents<false>(b, scale2, minus, 0, g2);
+          else exponents<true>(b, scale2, minus, mask1, g2);
         };
-        float top = -INFINITY;
-        uint64_t sum = 0;
-        form(m == -INFINITY ? 0.f : m, top, sum);
-        // both halves have read their scores, which the weights go over
-        if (any_of_pair(both, top > (m == -INFINITY ? -INFINITY : kSlack))) {
+        uint64_t sum, sum1;
+        auto form = [&]() {
+          sum = sum1 = 0;
+          each(m == -INFINITY ? 0.f : m, [&](int i, float x, float y) {
+            x = exp2_fast(x);
+            y = exp2_fast(y);
+            if (i & 1) sum1 = add2(sum1, pair(x, y)); else sum = add2(sum, pair(x, y));
+            w[i] = Elt<__nv_bfloat16>::pack_word(x, y);
+          });
+          sum = add2(sum, sum1);
+        };
+        form();
+        // (the vote also says that both halves have read their scores, which the weights go over)
+        if (any_of_pair(both, m == -INFINITY || pair_sum(sum) > kMost)) {
           // a new reference: the maximum, where it has passed the old one
-          top = joined(top, [](float a, float b) { return fmaxf(a, b); });
+          float top = -INFINITY;
           const float old = m;
+          each(old == -INFINITY ? 0.f : old, [&](int, float x, float y) { top = fmaxf(top, fmaxf(x, y)); });
+          top = joined(top, [](float x, float y) { return fmaxf(x, y); });
           if (top > (old == -INFINITY ? -INFINITY : 0.f)) m = (old == -INFINITY ? 0.f : old) + top;
           const float keep = m == old ? 1.f : exp2_fast(old - m);
           l *= keep;
@@ -361,9 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
               tmem_st16(at_o + q * 16, y);
             }
           }
-          top = -INFINITY;
-          sum = 0;
-          form(m == -INFINITY ? 0.f : m, top, sum);
+          form();
           pair_barrier(both);
         }
         l += pair_sum(sum);
