@@ -172,19 +172,105 @@ struct JoinParams {
   float *lse;
 };
 
+struct Sum {
+  float4 v[2];                             // elements 4 lane .. and 128 + 4 lane ..
+  __device__ __forceinline__ void zero() { v[0] = v[1] = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load(const float *row, int lane, int d) {
+    zero();
+    if (lane * 4 < d) v[0] = *reinterpret_cast<const float4 *>(row + lane * 4);
+    if (d > 128 && lane * 4 + 128 < d) v[1] = *reinterpret_cast<const float4 *>(row + lane * 4 + 128);
+  }
+  __device__ __forceinline__ void add(const Sum &x, float h) {
+    if (h == 0.f) return;                  // a part without a weight may hold nothing
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      v[i].x = fmaf(x.v[i].x, h, v[i].x);
+      v[i].y = fmaf(x.v[i].y, h, v[i].y);
+      v[i].z = fmaf(x.v[i].z, h, v[i].z);
+      v[i].w = fmaf(x.v[i].w, h, v[i].w);
+    }
+  }
+  template <typename T> __device__ __forceinline__ void store(T *row, int lane, int d, float f) const {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int e = lane * 4 + i * 128;
+      if (e >= d) break;
+      const float4 y = make_float4(v[i].x * f, v[i].y * f, v[i].z * f, v[i].w * f);
+      if constexpr (std::is_same<T, float>::value) *reinterpret_cast<float4 *>(row + e) = y;
+      else *reinterpret_cast<uint2 *>(row + e) = make_uint2(Elt<T>::pack_word(y.x, y.y), Elt<T>::pack_word(y.z, y.w));
+    }
+  }
+};
+__device__ __forceinline__ float part_weight(float lse, float M) { return lse == -INFINITY ? 0.f : expf(lse - M); }
+__device__ __forceinline__ float warp_max(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+constexpr int kJoinWarps = 8;
+
+// A warp per (sequence, query head) and PARTS parts of the prefix: everything
+// whose place is known, the own tokens' part of a pair that was not cut among
+// it, is on its way at once, and only a cut pair's pieces need a second read.
+template <typename T, int PARTS>
+__global__ void __launch_bounds__(kJoinWarps * 32) shared_join_few_kernel(const JoinParams p) {
+  grid_dependency_wait();
+  const int lane = threadIdx.x % 32, d = p.d;
+  const int64_t row = (int64_t)blockIdx.x * kJoinWarps + threadIdx.x / 32;
+  if (row >= p.rows) return;
+  const int head = (int)(row % p.Hq), hk = head / p.G, g = head % p.G;
+  float x[PARTS + 1];
+  Sum y[PARTS + 1];
+#pragma unroll
+  for (int k = 0; k <= PARTS; ++k) {
+    x[k] = p.part_lse[k * p.rows + row];
+    y[k].load(p.part_o + (k * p.rows + row) * d, lane, d);
+  }
+  const Pieces own = p.pieces[row / p.Hq * (p.Hq / p.G) + hk];
+  const int pieces = own.first < 0 ? 0 : own.last - own.first + 1;
+  if (pieces) x[PARTS] = -INFINITY;
+  auto piece = [&](int c) { return ((int64_t)(own.first + c) * 2 + (c == 0 ? own.slot : 0)) * p.G + g; };
+  float M = -INFINITY;
+  for (int c = lane; c < pieces; c += 32) M = fmaxf(M, p.piece_lse[piece(c)]);
+  if (pieces) M = warp_max(M);
+#pragma unroll
+  for (int k = 0; k <= PARTS; ++k) M = fmaxf(M, x[k]);
+  float L = 0.f;
+  Sum s;
+  s.zero();
+#pragma unroll
+  for (int k = 0; k <= PARTS; ++k) {
+    const float w = part_weight(x[k], M);
+    L += w;
+    s.add(y[k], w);
+  }
+#pragma unroll 2
+  for (int c = 0; c < pieces; ++c) {
+    const int64_t at = piece(c);
+    Sum z;
+    z.load(p.piece_o + at * d, lane, d);
+    const float w = part_weight(p.piece_lse[at], M);
+    L += w;
+    s.add(z, w);
+  }
+  s.store((T *)p.out + row * d, lane, d, L == 0.f ? 0.f : 1.f / L);
+  if (lane == 0 && p.lse) p.lse[row] = L == 0.f ? -INFINITY : M + logf(L);
+}
+
 // WARPS warps per (sequence, query head), 32 parts at a time: a lane finds a
 // part and its weight by its lse, then a warp adds every WARPS-th part, in an
 // order that is always the same.
-constexpr int kJoinWarps = 8;
-
 template <typename T, int WARPS>
 __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const JoinParams p) {
-  __shared__ float4 sums[WARPS == 1 ? 1 : kJoinWarps][WARPS == 1 ? 1 : 64];
+  __shared__ Sum sums[kJoinWarps][32];
   grid_dependency_wait();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, first = warp % WARPS, d = p.d;
   const int64_t row = (int64_t)blockIdx.x * (kJoinWarps / WARPS) + warp / WARPS;
   const bool live = row < p.rows;
   const int head = (int)((live ? row : 0) % p.Hq), hk = head / p.G, g = head % p.G;
+  // the lse of the lane's part of the prefix, before the pieces' place is known
+  float x0 = live && lane < p.splits ? p.part_lse[lane * p.rows + row] : -INFINITY;
   Pieces own{-1, 0, 0};
   if (live) own = p.pieces[row / p.Hq * (p.Hq / p.G) + hk];
   const int parts = !live ? 0 : own.first < 0 ? p.splits + 1 : p.splits + own.last - own.first + 1;
@@ -195,7 +281,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const Join
     if (k < p.splits || own.first < 0) {
       const int64_t at = k * p.rows + row;
       src = p.part_o + at * d;
-      return p.part_lse[at];
+      return k < 32 && k < p.splits ? x0 : p.part_lse[at];
     }
     const int c = k - p.splits;
     const int64_t at = ((int64_t)(own.first + c) * 2 + (c == 0 ? own.slot : 0)) * p.G + g;
@@ -203,77 +289,56 @@ __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const Join
     return p.piece_lse[at];
   };
   const float *src0, *src;
-  const float x0 = find(lane, src0);
+  x0 = find(lane, src0);
   float M = x0, L = 0.f;
   for (int k = lane + 32; k < parts; k += 32) M = fmaxf(M, find(k, src));
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
-  float4 s[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  M = warp_max(M);
+  Sum s;
+  s.zero();
   for (int k0 = 0; k0 < parts; k0 += 32) {
     src = src0;
-    const float x = k0 == 0 ? x0 : find(k0 + lane, src);
-    const float w = x == -INFINITY ? 0.f : expf(x - M);
+    const float w = part_weight(k0 == 0 ? x0 : find(k0 + lane, src), M);
     L += w;
     const int n = min(32, parts - k0);
 #pragma unroll 4
     for (int k = first; k < n; k += WARPS) {
       const float h = __shfl_sync(0xffffffffu, w, k);
-      const float *from = reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, (unsigned long long)src, k)) + lane * 4;
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f), z = y;
-      if (h != 0.f) {                      // a part without a weight may hold nothing
-        if (lane * 4 < d) y = *reinterpret_cast<const float4 *>(from);
-        if (d > 128 && lane * 4 + 128 < d) z = *reinterpret_cast<const float4 *>(from + 128);
-      }
-      s[0].x = fmaf(y.x, h, s[0].x);
-      s[0].y = fmaf(y.y, h, s[0].y);
-      s[0].z = fmaf(y.z, h, s[0].z);
-      s[0].w = fmaf(y.w, h, s[0].w);
-      s[1].x = fmaf(z.x, h, s[1].x);
-      s[1].y = fmaf(z.y, h, s[1].y);
-      s[1].z = fmaf(z.z, h, s[1].z);
-      s[1].w = fmaf(z.w, h, s[1].w);
+      const float *from = reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, (unsigned long long)src, k));
+      Sum y;
+      y.zero();
+      if (h != 0.f) y.load(from, lane, d);
+      s.add(y, h);
     }
   }
   L = team_sum_shfl<32>(L);
-  const float f = L == 0.f ? 0.f : 1.f / L;
-  if (WARPS > 1) {
-    sums[warp][lane] = s[0];
-    sums[warp][lane + 32] = s[1];
-    __syncthreads();
-    if (first > 0) return;
-  }
-  if (!live) return;
+  sums[warp][lane] = s;
+  __syncthreads();
+  if (first > 0 || !live) return;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const int e = lane * 4 + i * 128;
-    if (e >= d) break;
-    float4 y = s[i];
-    if (WARPS > 1) {
-#pragma unroll
-      for (int k = 1; k < WARPS; ++k) {
-        const float4 z = sums[warp + k][i * 32 + lane];
-        y.x += z.x;
-        y.y += z.y;
-        y.z += z.z;
-        y.w += z.w;
-      }
-    }
-    y.x *= f; y.y *= f; y.z *= f; y.w *= f;
-    T *dst = (T *)p.out + row * d + e;
-    if constexpr (std::is_same<T, float>::value) *reinterpret_cast<float4 *>(dst) = y;
-    else *reinterpret_cast<uint2 *>(dst) = make_uint2(Elt<T>::pack_word(y.x, y.y), Elt<T>::pack_word(y.z, y.w));
-  }
+  for (int k = 1; k < WARPS; ++k) s.add(sums[warp + k][lane], 1.f);
+  s.store((T *)p.out + row * d, lane, d, L == 0.f ? 0.f : 1.f / L);
   if (lane == 0 && p.lse) p.lse[row] = L == 0.f ? -INFINITY : M + logf(L);
 }
 
+// Few parts of the prefix: a warp per row.  More: eight warps per row where the
+// rows are few, two where they fill the GPU.
 template <typename T> cudaError_t launch_join(const JoinParams &p, cudaStream_t stream) {
-  auto go = [&](auto warps) -> cudaError_t {
+  auto few = [&](auto n) -> cudaError_t {
+    return launch_dependent(shared_join_few_kernel<T, decltype(n)::value>,
+                            dim3((unsigned)((p.rows + kJoinWarps - 1) / kJoinWarps)), dim3(kJoinWarps * 32), 0, stream, p);
+  };
+  auto many = [&](auto warps) -> cudaError_t {
     constexpr int W = decltype(warps)::value, R = kJoinWarps / W;
     return launch_dependent(shared_join_kernel<T, W>, dim3((unsigned)((p.rows + R - 1) / R)), dim3(kJoinWarps * 32), 0, stream,
                             p);
   };
-  return p.splits < 4 ? go(std::integral_constant<int, 1>{}) : p.splits < 24 ? go(std::integral_constant<int, 4>{})
-                                                                          : go(std::integral_constant<int, 8>{});
+  switch (p.splits) {
+    case 0: return few(std::integral_constant<int, 0>{});
+    case 1: return few(std::integral_constant<int, 1>{});
+    case 2: return few(std::integral_constant<int, 2>{});
+    case 3: return few(std::integral_constant<int, 3>{});
+  }
+  return p.rows >= 8 * (int64_t)sm_count() ? many(std::integral_constant<int, 2>{}) : many(std::integral_constant<int, 8>{});
 }
 
 // Ranges that the prefix is cut into so that the CTAs fill the GPU's SMs
