@@ -151,6 +151,16 @@ def test_empty_parts(gpu, dtype, prefix, lengths):
 
 @gpu_only
 @pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 256), (F32, 64)])
+def test_empty_pool_and_empty_batch(gpu, dtype, d):
+    q, kc, vc, pt, n, t, lengths, scale = inputs(gpu, dtype, 4, 2, d, 16, 200, [20, 5], 2)
+    out, lse = api.shared_prefix_attention(q, kc[:0], vc[:0], pt, n, t, lengths, scale)
+    assert not bool(out.any()) and bool((lse == -math.inf).all())
+    out, lse = api.shared_prefix_attention(q[:0], kc, vc, pt, n, t[:0], lengths[:0], scale)
+    assert out.shape == (0, 4, d) and lse.shape == (0, 4)
+
+
+@gpu_only
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 256), (F32, 64)])
 def test_one_cache_or_two(gpu, dtype, d):
     # a prefix of whole pages in front of each sequence's own table is the same attention
     q, kc, vc, pt, n, t, lengths, scale = inputs(gpu, dtype, 8, 2, d, 16, 160, [0, 1, 16, 100, 33], 5)

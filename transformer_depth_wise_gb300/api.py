@@ -324,11 +324,14 @@ def _add_norm_args(x, residual, weight, sum_out):
     _cuda(x, "x")
     _code(x)
     B, T, D = _btd(x)
-    _rows_like(residual, "residual", x)
-    _plain(weight, "weight", torch.float32, (D,), x.device)
-    if sum_out is None and residual is not None:
+    if residual is not None:
+        _rows_like(residual, "residual", x)
+    if weight is not None:
+        _plain(weight, "weight", torch.float32, (D,), x.device)
+    if sum_out is not None:
+        _rows_like(sum_out, "sum_out", x)
+    elif residual is not None:
         sum_out = torch.empty_like(x)
-    _rows_like(sum_out, "sum_out", x)
     return B, T, D, sum_out
 
 
@@ -341,7 +344,8 @@ def add_rms_norm(x, residual, weight=None, eps: float = 1e-6, sum_out=None, out=
     B, T, D, sum_out = _add_norm_args(x, residual, weight, sum_out)
     if out is None:
         out = torch.empty_like(x)
-    _rows_like(out, "out", x)
+    else:
+        _rows_like(out, "out", x)
     _call("attnres_add_rms_norm", x.device, x.data_ptr(), _ptr(residual), B, T, D, _CODES[x.dtype], _ptr(weight),
           float(eps), _ptr(sum_out), out.data_ptr())
     return out, sum_out
@@ -359,10 +363,12 @@ def add_rms_norm_8bit(x, residual, weight=None, eps: float = 1e-6, group: int = 
     shape = (*lead, D // group) if group else lead
     if out is None:
         out = torch.empty_like(x, dtype=torch.float8_e4m3fn)
-    _plain(out, "out", torch.float8_e4m3fn, x.shape, x.device)
+    else:
+        _plain(out, "out", torch.float8_e4m3fn, x.shape, x.device)
     if scales is None:
         scales = torch.empty(shape, dtype=torch.float32, device=x.device)
-    _plain(scales, "scales", torch.float32, shape, x.device)
+    else:
+        _plain(scales, "scales", torch.float32, shape, x.device)
     _call("attnres_add_rms_norm_8bit", x.device, x.data_ptr(), _ptr(residual), B, T, D, _CODES[x.dtype], _ptr(weight),
           float(eps), int(group), _ptr(sum_out), out.data_ptr(), scales.data_ptr())
     return out, scales, sum_out
@@ -384,7 +390,8 @@ def add_rms_norm_backward(s, weight, eps: float, grad_y, grad_sum=None, want_wei
     _rows_like(grad_sum, "grad_sum", s)
     if dx is None:
         dx = torch.empty_like(s)
-    _rows_like(dx, "dx", s)
+    else:
+        _rows_like(dx, "dx", s)
     gw, rows = None, 0
     if want_weight:
         gw = torch.empty(D, dtype=torch.float32, device=dev)

@@ -86,6 +86,18 @@ int64_t backward_bytes(int64_t B, int64_t T, int H, int64_t dk, int64_t dv, int 
   return a > b ? a : b;
 }
 
+// The sizes of a call behind a shared prefix, and its workspace's layout.
+int check_shared(int64_t B, int Hq, int Hk, int64_t d, int dtype, int page_size, int prefix_pages, int max_pages,
+                 SharedLayout &w) {
+  const int64_t own = attnres_paged_attention_workspace_bytes(Hq, Hk, d, dtype);
+  if (own < 0) return (int)own;
+  int st = check_pages(0, page_size, prefix_pages);
+  if (st || (st = check_pages(0, page_size, max_pages))) return st;
+  if (B < 0 || B > INT32_MAX / 64 / Hq) return ATTNRES_ERR_SHAPE;      // rows and grids stay within 32 bits
+  w = shared_layout(B, Hq, Hk, d, dtype, (int64_t)page_size * prefix_pages, (int64_t)page_size * max_pages);
+  return ATTNRES_OK;
+}
+
 // The head norm's three calls, with num_axes 0 for positions of one number each (axes and places unused).
 int rotate(const void *q, const void *k, int64_t B, int64_t T, int Hq, int Hk, int64_t d, int dtype, int64_t q_stride,
            int64_t k_stride, const float *q_weight, const float *k_weight, const int32_t *positions, int num_axes,
@@ -308,12 +320,9 @@ int attnres_paged_attention(const void *q, int64_t q_stride, const void *k_cache
 
 int64_t attnres_shared_prefix_attention_workspace_bytes(int64_t B, int Hq, int Hk, int64_t d, int dtype, int page_size,
                                                         int prefix_pages, int max_pages) {
-  const int64_t own = attnres_paged_attention_workspace_bytes(Hq, Hk, d, dtype);
-  if (own < 0) return own;
-  int st = check_pages(0, page_size, prefix_pages);
-  if (st || (st = check_pages(0, page_size, max_pages))) return st;
-  if (B < 0 || B > INT32_MAX / 64 / Hq) return ATTNRES_ERR_SHAPE;      // rows and grids stay within 32 bits
-  return shared_layout(B, Hq, Hk, d, dtype, (int64_t)page_size * prefix_pages, (int64_t)page_size * max_pages).bytes;
+  SharedLayout w{};
+  const int st = check_shared(B, Hq, Hk, d, dtype, page_size, prefix_pages, max_pages, w);
+  return st ? st : w.bytes;
 }
 
 int attnres_shared_prefix_attention(const void *q, int64_t q_stride, const void *k_cache, const void *v_cache,
@@ -321,10 +330,9 @@ int attnres_shared_prefix_attention(const void *q, int64_t q_stride, const void 
                                     const int32_t *prefix_length, const int32_t *page_table, int max_pages,
                                     const int32_t *lengths, int64_t B, int Hq, int Hk, int64_t d, int dtype, float scale,
                                     void *out, float *lse, void *workspace, int64_t workspace_bytes, void *stream) {
-  const int64_t need = attnres_shared_prefix_attention_workspace_bytes(B, Hq, Hk, d, dtype, page_size, prefix_pages, max_pages);
-  if (need < 0) return (int)need;
-  int st = check_stride(q_stride, Hq * d, dtype, false);
-  if (st) return st;
+  SharedLayout w{};
+  int st = check_shared(B, Hq, Hk, d, dtype, page_size, prefix_pages, max_pages, w);
+  if (st || (st = check_stride(q_stride, Hq * d, dtype, false))) return st;
   if (num_pages < 0) return ATTNRES_ERR_SHAPE;
   if (!std::isfinite(scale)) return ATTNRES_ERR_VALUE;
   if (B == 0) return ATTNRES_OK;
@@ -332,7 +340,7 @@ int attnres_shared_prefix_attention(const void *q, int64_t q_stride, const void 
   if (num_pages > 0 && ((max_pages > 0 && !page_table) || (prefix_pages > 0 && !prefix_table) ||
                         ((max_pages > 0 || prefix_pages > 0) && (!k_cache || !v_cache))))
     return ATTNRES_ERR_NULL;
-  if (workspace_bytes < need) return ATTNRES_ERR_CAPACITY;
+  if (workspace_bytes < w.bytes) return ATTNRES_ERR_CAPACITY;
   if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || misaligned(k_cache) || misaligned(v_cache) ||
       misaligned(prefix_table, 4) || misaligned(prefix_length, 4) || misaligned(page_table, 4) ||
       misaligned(lengths, 4) || misaligned(lse, 4))
@@ -340,11 +348,11 @@ int attnres_shared_prefix_attention(const void *q, int64_t q_stride, const void 
   if (among(out, k_cache, v_cache, workspace) || among(workspace, q, k_cache, v_cache, lse)) return ATTNRES_ERR_VALUE;
   SharedArgs a{};
   a.q = q; a.q_stride = q_stride; a.k_cache = k_cache; a.v_cache = v_cache; a.num_pages = num_pages;
-  a.page_size = page_size; a.prefix_pages = num_pages > 0 ? prefix_pages : 0;
+  a.page_size = page_size; a.prefix_pages = prefix_pages;
   a.max_pages = num_pages > 0 ? max_pages : 0; a.prefix_table = prefix_table; a.prefix_length = prefix_length;
   a.page_table = page_table; a.lengths = lengths; a.B = B; a.Hq = Hq; a.Hk = Hk; a.d = (int)d; a.dtype = dtype;
   a.scale = scale; a.out = out; a.lse = lse; a.workspace = workspace; a.stream = static_cast<cudaStream_t>(stream);
-  return cuda_status(launch_shared(a));
+  return cuda_status(launch_shared(a, w));
 }
 
 int64_t attnres_linear_attention_workspace_bytes(int64_t B, int64_t T, int H, int64_t dk, int64_t dv, int dtype) {

@@ -323,7 +323,17 @@ struct SharedLayout {
 };
 // tokens, own: what the prefix's table and a sequence's cover.
 SharedLayout shared_layout(int64_t B, int Hq, int Hk, int64_t d, int dtype, int64_t tokens, int64_t own);
-cudaError_t launch_shared(const SharedArgs &a);
+cudaError_t launch_shared(const SharedArgs &a, const SharedLayout &w);
+// Raises a kernel's limit of dynamic shared memory, once per device.
+template <auto kern> cudaError_t allow_smem(size_t bytes) {
+  static bool done[16] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || (dev < 16 && done[dev])) return e;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev < 16) done[dev] = true;
+  return e;
+}
 
 // out_i = alpha sum_{j <= i} e^{g (i - j)} (a_i . b_j) c_j + carry e^{g (i + first_pow)} a_i . first, through the state
 // S_i = e^g S_{i-1} + gain b_i c_i^T (S_{-1} = e^{g (first_pow - 1)} first), with alpha = carry gain

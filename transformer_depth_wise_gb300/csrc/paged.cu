@@ -750,7 +750,7 @@ bool paged_supported(int64_t d, int dtype) {
 }
 // Two CTAs per SM but for bf16 heads wider than 128, whose rings fill the shared memory.
 int paged_ctas(int64_t d, int dtype) { return (dtype == ATTNRES_BF16 && d > 128 ? 1 : 2) * sm_count(); }
-int paged_fine_ctas(int64_t d, int dtype) { return 4 * paged_ctas(d, dtype); }
+int paged_fine_ctas(int64_t d, int dtype) { return 3 * paged_ctas(d, dtype); }
 
 int64_t paged_workspace_bytes(int G, int64_t d, int dtype, int64_t ctas) {
   return ctas * (int64_t)sizeof(Cut) + ctas * 2 * G * (d + 1) * (int64_t)sizeof(float);

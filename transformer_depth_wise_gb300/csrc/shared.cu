@@ -355,8 +355,8 @@ cudaError_t launch_general(const PrefixParams &p, cudaStream_t stream) {
   const dim3 grid((unsigned)((int64_t)p.Hk * ((p.B * p.G + kRows - 1) / kRows)), (unsigned)p.splits);
   auto go = [&](auto D) -> cudaError_t {
     using S = Shape<decltype(D)::value>;
-    auto kern = shared_prefix_kernel<T, decltype(D)::value>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)S::kSmem);
+    constexpr auto kern = shared_prefix_kernel<T, decltype(D)::value>;
+    const cudaError_t e = allow_smem<kern>(S::kSmem);
     if (e != cudaSuccess) return e;
     return launch_dependent(kern, grid, dim3(kThreads), S::kSmem, stream, p);
   };
@@ -375,8 +375,9 @@ SharedLayout shared_layout(int64_t B, int Hq, int Hk, int64_t d, int dtype, int6
     w.splits = shared_tc_supported(d, dtype) ? shared_tc_splits(B, G, Hk, d, tokens) : general_splits(B, G, Hk, tokens);
   const int64_t rows = B * Hq, parts = w.splits + 1;
   // Behind a prefix's kernel the SMs come free one after the other: ranges
-  // of a quarter of the length even that out, where the tables leave each of
-  // them 16 tiles of 64 tokens or more.
+  // of a third of the length even that out, where the tables leave each of
+  // them 16 tiles of 64 tokens or more (256 chats 277 us without, 266 to 261
+  // with halves to thirds, 265 with sixths).
   w.own_ctas = paged_ctas(d, dtype);
   if (w.splits && B * Hk * (own / 64) >= 16 * (int64_t)paged_fine_ctas(d, dtype)) w.own_ctas = paged_fine_ctas(d, dtype);
   w.pieces = up16(paged_workspace_bytes(G, d, dtype, w.own_ctas));
@@ -386,9 +387,9 @@ SharedLayout shared_layout(int64_t B, int Hq, int Hk, int64_t d, int dtype, int6
   return w;
 }
 
-cudaError_t launch_shared(const SharedArgs &a) {
-  const int64_t tokens = (int64_t)a.prefix_pages * a.page_size;
-  const SharedLayout w = shared_layout(a.B, a.Hq, a.Hk, a.d, a.dtype, tokens, (int64_t)a.max_pages * a.page_size);
+cudaError_t launch_shared(const SharedArgs &a, const SharedLayout &w) {
+  // without a pool no table is read
+  const int64_t tokens = a.num_pages > 0 ? (int64_t)a.prefix_pages * a.page_size : 0;
   char *ws = static_cast<char *>(a.workspace);
   const int64_t rows = a.B * a.Hq;
   PrefixParams p{};

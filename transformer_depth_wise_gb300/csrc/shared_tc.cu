@@ -440,7 +440,7 @@ template <int D> bool registers_as_planned() {
 template <int D> cudaError_t launch(const PrefixParams &p, cudaStream_t stream) {
   using L = Layout<D>;
   if (!registers_as_planned<D>()) return cudaErrorInvalidConfiguration;
-  const cudaError_t e = cudaFuncSetAttribute(shared_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)L::kBytes);
+  const cudaError_t e = allow_smem<shared_tc_kernel<D>>(L::kBytes);
   if (e != cudaSuccess) return e;
   const int64_t tiles = ((int64_t)p.B * p.G + 2 * kTileRows - 1) / (2 * kTileRows);
   return launch_dependent(shared_tc_kernel<D>, dim3((unsigned)(tiles * p.Hk), (unsigned)p.splits), dim3(kThreads), L::kBytes,
