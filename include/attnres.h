@@ -289,7 +289,7 @@ int attnres_add_rms_norm(const void *x, const void *residual, int64_t B, int64_t
  *   scale = max(max |y| over the group / 448, 2^-126),  y8 = y / scale to nearest even
  *   group       elements per scale: 32, 64 or 128 (D a multiple), or 0: one
  *               scale per token row (VALUE otherwise)
- *   y8          device bytes [B,T,D];  scales device fp32 [B,T,D/group] or [B,T]
+ *   y8          device bytes [B,T,D];  scales device fp32 [B,T,D/group] or [B,T,1]
  * y8 and scales overlap nothing else.  A NaN among a group's y (an infinity
  * in a row makes one) gives a NaN scale and NaN y8 in that group.
  */

@@ -110,7 +110,7 @@ def test_8bit(gpu, dtype, rows, D, residual, group):
         D = max(group, D // group * group)
     x, r, w = inputs(gpu, dtype, rows, D, residual, 3 * rows + D)
     y8, scales, total = api.add_rms_norm_8bit(x, r, w, EPS, group=group)
-    assert y8.dtype is F8 and scales.shape == ((rows, D // group) if group else (rows,))
+    assert y8.dtype is F8 and scales.shape == (rows, D // group if group else 1)
     check_8bit(x, r, w, group, y8, scales)
     y, want = api.add_rms_norm(x, r, w, EPS)
     assert total is None if not residual else torch.equal(total, want)

@@ -354,13 +354,13 @@ def add_rms_norm(x, residual, weight=None, eps: float = 1e-6, sum_out=None, out=
 def add_rms_norm_8bit(x, residual, weight=None, eps: float = 1e-6, group: int = 0, sum_out=None, out=None, scales=None):
     """add_rms_norm with y in e4m3 and fp32 scales, one per `group` elements (32, 64, 128; 0: a row).
 
-    Returns (y8 float8_e4m3fn [..,D], scales [.., D/group] or [..], sum); y is y8 * scale.
+    Returns (y8 float8_e4m3fn [..,D], scales [.., D/group] or [.., 1], sum); y is y8 * scale.
     """
     B, T, D, sum_out = _add_norm_args(x, residual, weight, sum_out)
     lead = x.shape[:-1]
     if group and D % group:
         raise ValueError(f"group must divide {D}")
-    shape = (*lead, D // group) if group else lead
+    shape = (*lead, D // group if group else 1)
     if out is None:
         out = torch.empty_like(x, dtype=torch.float8_e4m3fn)
     else:

@@ -62,18 +62,63 @@ __device__ __forceinline__ uint32_t to_e4m3(uint64_t a, uint64_t b) {
   return (uint32_t)hi << 16 | lo;
 }
 
-// |x|'s bits: as unsigned numbers they are ordered like the values, with NaN
-// above infinity, so their maximum keeps a NaN.
-__device__ __forceinline__ uint32_t magnitude(uint64_t x) {
-  const uint32_t lo = (uint32_t)x & 0x7fffffffu, hi = (uint32_t)(x >> 32) & 0x7fffffffu;
-  return lo > hi ? lo : hi;
+// The largest magnitude of a pair and of what is there; NaN stays NaN.
+__device__ __forceinline__ float top_of(uint64_t x, float top) {
+  float lo, hi;
+  unpair(x, lo, hi);
+  asm("max.NaN.abs.f32 %0, %1, %2, %0;" : "+f"(top) : "f"(lo), "f"(hi));
+  return top;
 }
-__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ float larger(float a, float b) {
+  asm("max.NaN.f32 %0, %0, %1;" : "+f"(a) : "f"(b));
+  return a;
+}
 
-// The scale of a group with this largest magnitude (a NaN gives NaN).
-__device__ __forceinline__ float scale_of(uint32_t top) {
-  const float s = __uint_as_float(top) / kTop;
+// The scale of a group with this largest magnitude (a NaN gives NaN): within a
+// rounding of the quotient, and its reciprocal is what y is multiplied by.
+__device__ __forceinline__ float scale_of(float top) {
+  const float s = top * (1.f / kTop);
   return s < kLeast ? kLeast : s;
+}
+
+// The sum over a CTA of at most 16 warps, by warp and then over the warps'
+// sums; `red` [2][16], the half taken in turn so that one barrier is enough.
+__device__ __forceinline__ float cta_total(float v, float *red, int parity) {
+  v = team_sum_shfl<32>(v);
+  float *slot = red + parity * 16;
+  if (threadIdx.x % 32 == 0) slot[threadIdx.x / 32] = v;
+  __syncthreads();
+  v = threadIdx.x % 32 < blockDim.x / 32 ? slot[threadIdx.x % 32] : 0.f;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return __shfl_sync(0xffffffffu, v, 0);
+}
+
+// The same for two values; `red` [2][2][16].
+__device__ __forceinline__ void cta_totals(float &a, float &b, float *red, int parity) {
+  a = team_sum_shfl<32>(a);
+  b = team_sum_shfl<32>(b);
+  float *slot = red + parity * 32;
+  const int lane = threadIdx.x % 32;
+  if (lane == 0) {
+    slot[threadIdx.x / 32] = a;
+    slot[16 + threadIdx.x / 32] = b;
+  }
+  __syncthreads();
+  float v = lane % 16 < blockDim.x / 32 ? slot[lane] : 0.f;
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  a = __shfl_sync(0xffffffffu, v, 0);
+  b = __shfl_sync(0xffffffffu, v, 16);
+}
+
+// A 16-byte load that leaves nothing in L1: each vector is read once (and may
+// be written later, where an output lies on an input).
+__device__ __forceinline__ uint4 ld_once(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
 }
 
 template <typename T>
@@ -96,119 +141,125 @@ struct AddNormParams {
   float inv_D, eps;
 };
 
+// Eight (bf16) or four (fp32) values times `inv` in e4m3.
+template <int NP>
+__device__ __forceinline__ void store_e4m3(char *y, const uint64_t *v, float inv) {
+  const uint64_t inv2 = pair(inv, inv);
+  uint32_t q[NP / 2];
+#pragma unroll
+  for (int i = 0; i < NP; i += 2) q[i / 2] = to_e4m3(mul2(v[i], inv2), mul2(v[i + 1], inv2));
+  if constexpr (NP == 4) *reinterpret_cast<uint2 *>(y) = make_uint2(q[0], q[1]);
+  else *reinterpret_cast<uint32_t *>(y) = q[0];
+}
+
 template <typename T, int VPT, int TEAM, int MODE>
 __global__ void __launch_bounds__(TEAM ? 256 : 512) add_norm_kernel(const AddNormParams p) {
   constexpr int EPV = Elt<T>::EPV, NP = Pairs<T>::NP;
-  __shared__ float red[TEAM ? 1 : 2 * 32];
-  __shared__ uint32_t top_red[TEAM || MODE != kRow8 ? 1 : 2 * 32];
+  __shared__ float red[TEAM ? 1 : 32], top_red[TEAM || MODE != kRow8 ? 1 : 32];
   grid_dependency_wait();
   const int tpr = TEAM ? TEAM : blockDim.x, lt = TEAM ? threadIdx.x % TEAM : threadIdx.x;
   const int teams = TEAM ? blockDim.x / TEAM : 1, team = TEAM ? threadIdx.x / TEAM : 0;
-  const int64_t steps = (p.rows + teams - 1) / teams;
-  const char *x = (const char *)p.x, *res = (const char *)p.residual;
+  // the thread's first vector of a row, and from one row of the team to its next
+  const int64_t start = (int64_t)blockIdx.x * teams + team, rows = p.rows, turn = (int64_t)gridDim.x * teams;
+  const int64_t step = turn * p.nvec * 16;
+  const char *x = (const char *)p.x + (start * p.nvec + lt) * 16;
+  const char *res = p.residual ? (const char *)p.residual + (start * p.nvec + lt) * 16 : nullptr;
+  char *sum = p.sum ? (char *)p.sum + (start * p.nvec + lt) * 16 : nullptr;
+  char *y = (char *)p.y + (start * p.nvec + lt) * (MODE == kPlain ? 16 : EPV);
+  float *scales = MODE == kGroups ? p.scales + start * (p.nvec / p.lanes) + lt / p.lanes : p.scales + start;
+  const float *w = p.w ? p.w + lt * EPV : nullptr;
+  bool in[VPT];                            // vectors that a row has
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) in[k] = lt + k * tpr < p.nvec;
   uint4 xv[VPT], rv[VPT];
-  auto load = [&](int64_t step) {
-    const int64_t row = step * teams + team;
-    const int64_t at = (row * p.nvec + lt) * 16;
+  auto load = [&](bool live) {
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       xv[k] = rv[k] = make_uint4(0, 0, 0, 0);
-      if (row < p.rows && lt + k * tpr < p.nvec) {
-        xv[k] = *reinterpret_cast<const uint4 *>(x + at + (int64_t)k * tpr * 16);
-        if (res) rv[k] = *reinterpret_cast<const uint4 *>(res + at + (int64_t)k * tpr * 16);
+      if (live && in[k]) {
+        xv[k] = ld_once(x + k * tpr * 16);
+        if (res) rv[k] = ld_once(res + k * tpr * 16);
       }
     }
   };
   int parity = 0;
-  if (blockIdx.x < steps) load(blockIdx.x);
-  for (int64_t step = blockIdx.x; step < steps; step += gridDim.x) {
-    const int64_t row = step * teams + team;
+  load(start < rows);
+  // a team's last turns may be idle ones that its warp's other teams need
+  for (int64_t row = start; row - team < rows; row += turn) {
+    const bool live = TEAM == 0 || row < rows;
     uint64_t s[VPT * NP], sq = 0;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      uint64_t b[NP];
       Pairs<T>::split(xv[k], s + k * NP);
-      Pairs<T>::split(rv[k], b);
+      if (res) {
+        uint64_t b[NP];
+        Pairs<T>::split(rv[k], b);
 #pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        if (res) s[k * NP + i] = add2(s[k * NP + i], b[i]);
-        fma_pair(sq, s[k * NP + i], s[k * NP + i]);
+        for (int i = 0; i < NP; ++i) s[k * NP + i] = add2(s[k * NP + i], b[i]);
       }
+#pragma unroll
+      for (int i = 0; i < NP; ++i) fma_pair(sq, s[k * NP + i], s[k * NP + i]);
     }
-    if (step + gridDim.x < steps) load(step + gridDim.x);
+    x += step;
+    if (res) res += step;
+    load(row + turn < rows);
     float ss = pair_sum(sq);
-    if (TEAM) {
-      ss = team_sum_shfl<TEAM ? TEAM : 1>(ss);
-    } else {
-      float v[1] = {ss};
-      cta_sum<1>(v, red, parity);
-      ss = v[0];
-    }
+    if (TEAM) ss = team_sum_shfl<TEAM ? TEAM : 1>(ss);
+    else ss = cta_total(ss, red, parity);
     const float r = rsqrtf(fmaf(ss, p.inv_D, p.eps));
     const uint64_t r2 = pair(r, r);
-    uint32_t top = 0;
-    const bool row_ok = row < p.rows;
+    float top = 0.f;
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int j = lt + k * tpr;
-      const bool live = row_ok && j < p.nvec;
-      const int64_t at = (row * p.nvec + j) * 16;
+      const bool here = live && in[k];
       uint64_t *v = s + k * NP;
-      if (live && p.sum) st_vec((char *)p.sum + at, from_pairs<T>(v));
-      uint64_t w[NP];
-      if (live) load_weight<T>(w, p.w ? p.w + (int64_t)j * EPV : nullptr);
+      if (here) {
+        if (sum) st_stream(sum + k * tpr * 16, from_pairs<T>(v));
+        uint64_t c[NP];
+        load_weight<T>(c, w ? w + k * tpr * EPV : nullptr);
 #pragma unroll
-      for (int i = 0; i < NP; ++i) v[i] = live ? mul2(mul2(v[i], r2), w[i]) : 0ull;
-      if (MODE == kPlain) {
-        if (live) st_vec((char *)p.y + at, from_pairs<T>(v));
-        continue;
+        for (int i = 0; i < NP; ++i) v[i] = mul2(mul2(v[i], r2), c[i]);
+        if (MODE == kPlain) st_vec(y + k * tpr * 16, from_pairs<T>(v));
       }
-      uint32_t m = 0;
+      if constexpr (MODE != kPlain) {
+        float m = 0.f;
+        if (here) {
 #pragma unroll
-      for (int i = 0; i < NP; ++i) m = larger(m, magnitude(v[i]));
-      if (MODE == kRow8) {
-        top = larger(top, m);
-        continue;
+          for (int i = 0; i < NP; ++i) m = top_of(v[i], m);
+        }
+        if constexpr (MODE == kRow8) {
+          top = larger(top, m);
+        } else {
+          for (int o = p.lanes / 2; o > 0; o >>= 1) m = larger(m, __shfl_xor_sync(0xffffffffu, m, o));
+          if (here) {
+            const float scale = scale_of(m);
+            store_e4m3<NP>(y + k * tpr * EPV, v, 1.f / scale);
+            if (lt % p.lanes == 0) scales[k * (tpr / p.lanes)] = scale;
+          }
+        }
       }
-      for (int o = p.lanes / 2; o > 0; o >>= 1) m = larger(m, __shfl_xor_sync(0xffffffffu, m, o));
-      if (!live) continue;
-      const float scale = scale_of(m), inv = 1.f / scale;
-      const uint64_t inv2 = pair(inv, inv);
-      uint32_t q[NP / 2];
-#pragma unroll
-      for (int i = 0; i < NP; i += 2) q[i / 2] = to_e4m3(mul2(v[i], inv2), mul2(v[i + 1], inv2));
-      char *y = (char *)p.y + (row * p.nvec + j) * EPV;
-      if constexpr (NP == 4) *reinterpret_cast<uint2 *>(y) = make_uint2(q[0], q[1]);
-      else *reinterpret_cast<uint32_t *>(y) = q[0];
-      if (j % p.lanes == 0) p.scales[row * (p.nvec / p.lanes) + j / p.lanes] = scale;
     }
-    if (MODE == kRow8) {
-      if (TEAM) {
+    if constexpr (MODE == kRow8) {
 #pragma unroll
-        for (int o = TEAM / 2; o > 0; o >>= 1) top = larger(top, __shfl_xor_sync(0xffffffffu, top, o));
-      } else {
-        top = __reduce_max_sync(0xffffffffu, top);
-        uint32_t *slot = top_red + parity * 32;
+      for (int o = (TEAM ? TEAM : 32) / 2; o > 0; o >>= 1) top = larger(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (!TEAM) {
+        float *slot = top_red + parity * 16;
         if (threadIdx.x % 32 == 0) slot[threadIdx.x / 32] = top;
         __syncthreads();
-        for (int i = 0; i < (int)(blockDim.x / 32); ++i) top = larger(top, slot[i]);
+        top = threadIdx.x % 32 < blockDim.x / 32 ? slot[threadIdx.x % 32] : 0.f;
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) top = larger(top, __shfl_xor_sync(0xffffffffu, top, o));
+        top = __shfl_sync(0xffffffffu, top, 0);
       }
       const float scale = scale_of(top), inv = 1.f / scale;
-      const uint64_t inv2 = pair(inv, inv);
 #pragma unroll
-      for (int k = 0; k < VPT; ++k) {
-        const int j = lt + k * tpr;
-        if (!row_ok || j >= p.nvec) continue;
-        const uint64_t *v = s + k * NP;
-        uint32_t q[NP / 2];
-#pragma unroll
-        for (int i = 0; i < NP; i += 2) q[i / 2] = to_e4m3(mul2(v[i], inv2), mul2(v[i + 1], inv2));
-        char *y = (char *)p.y + (row * p.nvec + j) * EPV;
-        if constexpr (NP == 4) *reinterpret_cast<uint2 *>(y) = make_uint2(q[0], q[1]);
-        else *reinterpret_cast<uint32_t *>(y) = q[0];
-      }
-      if (row_ok && lt == 0) p.scales[row] = scale;
+      for (int k = 0; k < VPT; ++k)
+        if (live && in[k]) store_e4m3<NP>(y + k * tpr * EPV, s + k * NP, inv);
+      if (live && lt == 0) *scales = scale;
     }
+    if (sum) sum += step;
+    y += MODE == kPlain ? step : step / 16 * EPV;
+    if (MODE != kPlain) scales += MODE == kGroups ? turn * (p.nvec / p.lanes) : turn;
     parity ^= 1;
   }
 }
@@ -226,86 +277,85 @@ struct AddNormBackwardParams {
 template <typename T, int VPT, int TEAM>
 __global__ void __launch_bounds__(TEAM ? 256 : 512) add_norm_backward_kernel(const AddNormBackwardParams p) {
   constexpr int EPV = Elt<T>::EPV, NP = Pairs<T>::NP;
-  __shared__ float red[TEAM ? 1 : 2 * 32 * 2];
+  __shared__ float red[TEAM ? 1 : 64];
   extern __shared__ float team_dw[];       // TEAM: [teams][VPT * TEAM * EPV]
   grid_dependency_wait();
   const int tpr = TEAM ? TEAM : blockDim.x, lt = TEAM ? threadIdx.x % TEAM : threadIdx.x;
   const int teams = TEAM ? blockDim.x / TEAM : 1, team = TEAM ? threadIdx.x / TEAM : 0;
-  const int64_t steps = (p.rows + teams - 1) / teams;
-  const char *sp = (const char *)p.s, *gp = (const char *)p.gy, *rp = (const char *)p.gs;
+  const int64_t start = (int64_t)blockIdx.x * teams + team, rows = p.rows, turn = (int64_t)gridDim.x * teams;
+  const int64_t step = turn * p.nvec * 16, at = (start * p.nvec + lt) * 16;
+  const char *sp = (const char *)p.s + at, *gp = (const char *)p.gy + at;
+  const char *rp = p.gs ? (const char *)p.gs + at : nullptr;
+  char *out = (char *)p.dx + at;
+  bool in[VPT];
+#pragma unroll
+  for (int k = 0; k < VPT; ++k) in[k] = lt + k * tpr < p.nvec;
   uint4 sv[VPT], gv[VPT], rv[VPT];
-  auto load = [&](int64_t step) {
-    const int64_t row = step * teams + team;
-    const int64_t at = (row * p.nvec + lt) * 16;
+  auto load = [&](bool live) {
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
       sv[k] = gv[k] = rv[k] = make_uint4(0, 0, 0, 0);
-      if (row < p.rows && lt + k * tpr < p.nvec) {
-        sv[k] = *reinterpret_cast<const uint4 *>(sp + at + (int64_t)k * tpr * 16);
-        gv[k] = *reinterpret_cast<const uint4 *>(gp + at + (int64_t)k * tpr * 16);
-        if (rp) rv[k] = *reinterpret_cast<const uint4 *>(rp + at + (int64_t)k * tpr * 16);
+      if (live && in[k]) {
+        sv[k] = ld_once(sp + k * tpr * 16);
+        gv[k] = ld_once(gp + k * tpr * 16);
+        if (rp) rv[k] = ld_once(rp + k * tpr * 16);
       }
     }
   };
-  uint64_t dw[VPT * NP];
+  uint64_t dw[VPT * NP], w[VPT * NP];
 #pragma unroll
-  for (int i = 0; i < VPT * NP; ++i) dw[i] = 0;
+  for (int i = 0; i < VPT * NP; ++i) dw[i] = w[i] = 0;
+#pragma unroll
+  for (int k = 0; k < VPT; ++k)
+    if (in[k]) load_weight<T>(w + k * NP, p.w ? p.w + (lt + k * tpr) * EPV : nullptr);
   int parity = 0;
-  if (blockIdx.x < steps) load(blockIdx.x);
-  for (int64_t step = blockIdx.x; step < steps; step += gridDim.x) {
-    const int64_t row = step * teams + team;
+  load(start < rows);
+  for (int64_t row = start; row - team < rows; row += turn, out += step) {
     uint64_t s[VPT * NP], g[VPT * NP], sq = 0, dot = 0;
     uint4 gs[VPT];
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int j = lt + k * tpr;
-      uint64_t w[NP];
       Pairs<T>::split(sv[k], s + k * NP);
       Pairs<T>::split(gv[k], g + k * NP);
       gs[k] = rv[k];
 #pragma unroll
-      for (int i = 0; i < NP; ++i) w[i] = 0;
-      if (j < p.nvec) load_weight<T>(w, p.w ? p.w + (int64_t)j * EPV : nullptr);
-#pragma unroll
       for (int i = 0; i < NP; ++i) {
         const uint64_t a = s[k * NP + i];
         fma_pair(sq, a, a);
-        fma_pair(dot, mul2(g[k * NP + i], w[i]), a);
+        fma_pair(dot, mul2(g[k * NP + i], w[k * NP + i]), a);
       }
     }
-    if (step + gridDim.x < steps) load(step + gridDim.x);
+    sp += step;
+    gp += step;
+    if (rp) rp += step;
+    load(row + turn < rows);
     float ss = pair_sum(sq), us = pair_sum(dot);
     if (TEAM) {
       ss = team_sum_shfl<TEAM ? TEAM : 1>(ss);
       us = team_sum_shfl<TEAM ? TEAM : 1>(us);
     } else {
-      float v[2] = {ss, us};
-      cta_sum<2>(v, red, parity);
+      cta_totals(ss, us, red, parity);
       parity ^= 1;
-      ss = v[0];
-      us = v[1];
     }
-    if (row >= p.rows) continue;
+    if (TEAM && row >= rows) continue;
     const float r = rsqrtf(fmaf(ss, p.inv_D, p.eps)), rc = -us * p.inv_D * r * r * r;
     const uint64_t r2 = pair(r, r), rc2 = pair(rc, rc);
 #pragma unroll
     for (int k = 0; k < VPT; ++k) {
-      const int j = lt + k * tpr;
-      if (j >= p.nvec) continue;
-      uint64_t w[NP], b[NP];
-      load_weight<T>(w, p.w ? p.w + (int64_t)j * EPV : nullptr);
+      if (!in[k]) continue;
+      uint64_t b[NP];
       Pairs<T>::split(gs[k], b);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const uint64_t a = s[k * NP + i], gr = mul2(g[k * NP + i], r2);
         fma_pair(dw[k * NP + i], gr, a);
-        b[i] = fma2(a, rc2, fma2(gr, w[i], b[i]));
+        b[i] = fma2(a, rc2, fma2(gr, w[k * NP + i], b[i]));
       }
-      st_vec((char *)p.dx + (row * p.nvec + j) * 16, from_pairs<T>(b));
+      st_stream(out + k * tpr * 16, from_pairs<T>(b));
     }
   }
   if (!p.partials) return;
-  float *out = p.partials + (int64_t)blockIdx.x * p.nvec * EPV;
+  float *sums = p.partials + (int64_t)blockIdx.x * p.nvec * EPV;
   if (TEAM) {
     // the teams' sums, in a fixed order
     const int D = p.nvec * EPV;
@@ -321,7 +371,7 @@ __global__ void __launch_bounds__(TEAM ? 256 : 512) add_norm_backward_kernel(con
     for (int i = threadIdx.x; i < D; i += blockDim.x) {
       float sum = 0.f;
       for (int t = 0; t < teams; ++t) sum += team_dw[t * D + i];
-      out[i] = sum;
+      sums[i] = sum;
     }
   } else {
 #pragma unroll
@@ -333,27 +383,30 @@ __global__ void __launch_bounds__(TEAM ? 256 : 512) add_norm_backward_kernel(con
         float4 f;
         unpair(dw[k * NP + i], f.x, f.y);
         unpair(dw[k * NP + i + 1], f.z, f.w);
-        *reinterpret_cast<float4 *>(out + (int64_t)j * EPV + 2 * i) = f;
+        *reinterpret_cast<float4 *>(sums + (int64_t)j * EPV + 2 * i) = f;
       }
     }
   }
 }
 
-// The weight's gradient: the CTAs' sums added in a fixed order, eight strands
-// of every eighth CTA per column, 32 columns per CTA.
-__global__ void __launch_bounds__(256) add_norm_weight_kernel(const float *partials, int ctas, int D, float *dw) {
-  __shared__ float red[8][33];
+// The weight's gradient: the CTAs' sums added in a fixed order, 16 strands of
+// every 16th CTA per column, 32 columns per CTA.
+constexpr int kStrands = 16;
+__global__ void __launch_bounds__(32 * kStrands) add_norm_weight_kernel(const float *partials, int ctas, int D, float *dw) {
+  __shared__ float red[kStrands][32];
   grid_dependency_wait();
   const int col = blockIdx.x * 32 + threadIdx.x % 32, strand = threadIdx.x / 32;
   float s = 0.f;
-  if (col < D)
-    for (int c = strand; c < ctas; c += 8) s += partials[(int64_t)c * D + col];
+  if (col < D) {
+#pragma unroll 8
+    for (int c = strand; c < ctas; c += kStrands) s += partials[(int64_t)c * D + col];
+  }
   red[strand][threadIdx.x % 32] = s;
   __syncthreads();
   if (strand == 0 && col < D) {
     s = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s += red[k][threadIdx.x];
+    for (int k = 0; k < kStrands; ++k) s += red[k][threadIdx.x];
     dw[col] = s;
   }
 }
@@ -453,7 +506,7 @@ cudaError_t launch_add_norm_backward(const AddNormBackwardArgs &a) {
   };
   cudaError_t e = a.dtype == ATTNRES_BF16 ? go(__nv_bfloat16{}) : go(float{});
   if (e != cudaSuccess || !a.workspace) return e;
-  return launch_dependent(add_norm_weight_kernel, dim3((unsigned)((a.D + 31) / 32)), dim3(256), 0, a.stream,
+  return launch_dependent(add_norm_weight_kernel, dim3((unsigned)((a.D + 31) / 32)), dim3(32 * kStrands), 0, a.stream,
                           (const float *)a.workspace, ctas, a.D, a.grad_weight);
 }
 

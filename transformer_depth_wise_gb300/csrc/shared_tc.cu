@@ -133,7 +133,7 @@ __device__ __forceinline__ bool any_of_pair(int id, bool x) {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_constant__ PrefixParams p) {
   using L = Layout<D>;
-  constexpr int NB = L::kBlocks, NR = L::kRing;
+  constexpr int NR = L::kRing;
   extern __shared__ unsigned char smem_raw[];
   grid_dependency_wait();
   launch_dependents();
