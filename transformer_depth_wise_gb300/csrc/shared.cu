@@ -68,28 +68,49 @@ __global__ void __launch_bounds__(kThreads) shared_prefix_kernel(const PrefixPar
       Elt<T>::unpack(*reinterpret_cast<const uint4 *>(src), x);
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e) qs[r * P + c * E + e] = x[e] * scale2;
+    for (int e = 0; e < E; e += 4)
+      *reinterpret_cast<float4 *>(qs + r * P + c * E + e) =
+          make_float4(x[e] * scale2, x[e + 1] * scale2, x[e + 2] * scale2, x[e + 3] * scale2);
   }
 
+  // A thread's share of a tile: pieces of 16 bytes, the next tile's on their
+  // way while the present one is worked on.
+  constexpr int kVecs = kKeys * (D / E) / kThreads > 0 ? kKeys * (D / E) / kThreads : 1;
+  uint4 kv[kVecs], vv[kVecs];
+  bool have[kVecs];
+  auto read = [&](int j) {
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      const int i = threadIdx.x + u * kThreads, t = i / (D / E), c = i % (D / E);
+      const int64_t at = t < kKeys && j + t < j1 ? p.row(j + t, hk) : -1;
+      kv[u] = vv[u] = make_uint4(0, 0, 0, 0);
+      have[u] = at >= 0;
+      if (at >= 0 && c < nvec) {
+        kv[u] = *reinterpret_cast<const uint4 *>((const T *)p.k + at + c * E);
+        vv[u] = *reinterpret_cast<const uint4 *>((const T *)p.v + at + c * E);
+      }
+    }
+  };
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[2][NC * 4] = {};
+  if (j0 < j1) read(j0);
   for (int j = j0; j < j1; j += kKeys) {
     __syncthreads();                       // the last tile is read
-    if (threadIdx.x < kKeys) live[threadIdx.x] = j + threadIdx.x < j1 && p.row(j + threadIdx.x, hk) >= 0;
-    for (int i = threadIdx.x; i < kKeys * (D / E); i += kThreads) {
-      const int t = i / (D / E), c = i % (D / E);
-      const int64_t at = j + t < j1 ? p.row(j + t, hk) : -1;
-      float x[E] = {}, y[E] = {};
-      if (at >= 0 && c < nvec) {
-        Elt<T>::unpack(*reinterpret_cast<const uint4 *>((const T *)p.k + at + c * E), x);
-        Elt<T>::unpack(*reinterpret_cast<const uint4 *>((const T *)p.v + at + c * E), y);
-      }
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      const int i = threadIdx.x + u * kThreads, t = i / (D / E), c = i % (D / E);
+      if (t >= kKeys) break;
+      float x[E], y[E];
+      Elt<T>::unpack(kv[u], x);
+      Elt<T>::unpack(vv[u], y);
 #pragma unroll
       for (int e = 0; e < E; e += 4) {
         *reinterpret_cast<float4 *>(ks + t * P + c * E + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
         *reinterpret_cast<float4 *>(vs + t * P + c * E + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
       }
+      if (c == 0) live[t] = have[u];
     }
     __syncthreads();
+    if (j + kKeys < j1) read(j + kKeys);
     // scores of rows warp_row and warp_row + 32 with tokens l8 + 8 i
     float s[2][4] = {};
     for (int c = 0; c < D; c += 4) {
@@ -341,12 +362,12 @@ template <typename T> cudaError_t launch_join(const JoinParams &p, cudaStream_t 
   return p.rows >= 8 * (int64_t)sm_count() ? many(std::integral_constant<int, 2>{}) : many(std::integral_constant<int, 8>{});
 }
 
-// Ranges that the prefix is cut into so that the CTAs fill the GPU's SMs
-// about twice, none shorter than four tiles.
+// Ranges that the prefix is cut into so that the GPU's SMs have about four CTAs
+// each, none shorter than two tiles.
 int general_splits(int64_t B, int G, int Hk, int64_t tokens) {
   const int64_t items = (B * G + kRows - 1) / kRows * Hk, tiles = (tokens + kKeys - 1) / kKeys;
   int64_t n = (4 * (int64_t)sm_count() + items - 1) / items;
-  if (n > tiles / 4) n = tiles / 4;
+  if (n > tiles / 2) n = tiles / 2;
   return (int)(n < 1 ? 1 : n > kMaxPrefixParts ? kMaxPrefixParts : n);
 }
 
