@@ -91,7 +91,8 @@ __global__ void __launch_bounds__(kThreads) shared_prefix_kernel(const PrefixPar
       }
     }
   };
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, o[2][NC * 4] = {};
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  uint64_t o[2][NC * 2] = {};              // pairs of the output's elements
   if (j0 < j1) read(j0);
   for (int j = j0; j < j1; j += kKeys) {
     __syncthreads();                       // the last tile is read
@@ -111,17 +112,26 @@ __global__ void __launch_bounds__(kThreads) shared_prefix_kernel(const PrefixPar
     }
     __syncthreads();
     if (j + kKeys < j1) read(j + kKeys);
-    // scores of rows warp_row and warp_row + 32 with tokens l8 + 8 i
-    float s[2][4] = {};
+    // scores of rows warp_row and warp_row + 32 with tokens l8 + 8 i, the sums of even and odd elements side by side
+    uint64_t s2[2][4] = {};
+#pragma unroll 4
     for (int c = 0; c < D; c += 4) {
-      const float4 a = *reinterpret_cast<const float4 *>(qs + warp_row * P + c);
-      const float4 b = *reinterpret_cast<const float4 *>(qs + (warp_row + 32) * P + c);
+      const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(qs + warp_row * P + c);
+      const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(qs + (warp_row + 32) * P + c);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float4 k = *reinterpret_cast<const float4 *>(ks + (l8 + 8 * i) * P + c);
-        s[0][i] = fmaf(a.x, k.x, fmaf(a.y, k.y, fmaf(a.z, k.z, fmaf(a.w, k.w, s[0][i]))));
-        s[1][i] = fmaf(b.x, k.x, fmaf(b.y, k.y, fmaf(b.z, k.z, fmaf(b.w, k.w, s[1][i]))));
+        const ulonglong2 k = *reinterpret_cast<const ulonglong2 *>(ks + (l8 + 8 * i) * P + c);
+        fma_pair(s2[0][i], a.x, k.x);
+        fma_pair(s2[0][i], a.y, k.y);
+        fma_pair(s2[1][i], b.x, k.x);
+        fma_pair(s2[1][i], b.y, k.y);
       }
+    }
+    float s[2][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      s[0][i] = pair_sum(s2[0][i]);
+      s[1][i] = pair_sum(s2[1][i]);
     }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -137,8 +147,10 @@ __global__ void __launch_bounds__(kThreads) shared_prefix_kernel(const PrefixPar
       const float base = mn == -INFINITY ? 0.f : mn;
       m[r] = mn;
       l[r] *= keep;
+      if (keep != 1.f) {
 #pragma unroll
-      for (int i = 0; i < NC * 4; ++i) o[r][i] *= keep;
+        for (int i = 0; i < NC * 2; ++i) scale_pair(o[r][i], pair(keep, keep));
+      }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const float w = exp2_fast(s[r][i] - base);
@@ -148,19 +160,17 @@ __global__ void __launch_bounds__(kThreads) shared_prefix_kernel(const PrefixPar
     }
     __syncwarp();                          // a row's weights come from its own eight lanes
     const int left = min(kKeys, j1 - j);
+#pragma unroll 4
     for (int t = 0; t < left; ++t) {
       const float a = ps[warp_row * (kKeys + 1) + t], b = ps[(warp_row + 32) * (kKeys + 1) + t];
+      const uint64_t a2 = pair(a, a), b2 = pair(b, b);
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
-        const float4 v = *reinterpret_cast<const float4 *>(vs + t * P + i * 32 + l8 * 4);
-        o[0][4 * i] = fmaf(a, v.x, o[0][4 * i]);
-        o[0][4 * i + 1] = fmaf(a, v.y, o[0][4 * i + 1]);
-        o[0][4 * i + 2] = fmaf(a, v.z, o[0][4 * i + 2]);
-        o[0][4 * i + 3] = fmaf(a, v.w, o[0][4 * i + 3]);
-        o[1][4 * i] = fmaf(b, v.x, o[1][4 * i]);
-        o[1][4 * i + 1] = fmaf(b, v.y, o[1][4 * i + 1]);
-        o[1][4 * i + 2] = fmaf(b, v.z, o[1][4 * i + 2]);
-        o[1][4 * i + 3] = fmaf(b, v.w, o[1][4 * i + 3]);
+        const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(vs + t * P + i * 32 + l8 * 4);
+        fma_pair(o[0][2 * i], a2, v.x);
+        fma_pair(o[0][2 * i + 1], a2, v.y);
+        fma_pair(o[1][2 * i], b2, v.x);
+        fma_pair(o[1][2 * i + 1], b2, v.y);
       }
     }
   }
@@ -175,9 +185,12 @@ __global__ void __launch_bounds__(kThreads) shared_prefix_kernel(const PrefixPar
     const float f = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
     for (int i = 0; i < NC; ++i)
-      if (i * 32 + l8 * 4 < p.d)
-        *reinterpret_cast<float4 *>(p.part_o + at * p.d + i * 32 + l8 * 4) =
-            make_float4(o[r][4 * i] * f, o[r][4 * i + 1] * f, o[r][4 * i + 2] * f, o[r][4 * i + 3] * f);
+      if (i * 32 + l8 * 4 < p.d) {
+        float4 x;
+        unpair(o[r][2 * i], x.x, x.y);
+        unpair(o[r][2 * i + 1], x.z, x.w);
+        *reinterpret_cast<float4 *>(p.part_o + at * p.d + i * 32 + l8 * 4) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+      }
     if (l8 == 0) p.part_lse[at] = L == 0.f ? -INFINITY : (m[r] + log2f(L)) * 0.69314718055994530942f;
   }
 }
