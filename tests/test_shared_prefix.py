@@ -91,7 +91,7 @@ def inputs(dev, dtype, Hq, Hk, d, page, prefix, lengths, seed, spare=0):
 
 
 def coarse_of(dtype, d):
-    return 2.0 ** -8 if dtype is BF and d <= 128 else 0.0
+    return 2.0 ** -8 if dtype is BF else 0.0           # the prefix's weights in bf16 are off by half a step
 
 
 def check(args, dtype, d, what=""):

@@ -12,11 +12,11 @@
 // which leaves one more part (or several, of a sequence that its split has
 // cut), and a last kernel joins the parts by the online-softmax merge (OS2).
 //
-// This file: the parts of the prefix in fp32 arithmetic for any type and
-// width, and the join.  A tile of 64 rows and 32 tokens at a time goes through
-// shared memory as fp32; a thread forms 2 x 4 scores, and then adds to two
-// rows of the output, so that each 16-byte read from shared memory feeds eight
-// multiply-adds.
+// This file: the parts of the prefix in fp32, and the join (bf16: shared_tc.cu).
+// A tile of 64 rows and 32 tokens at a time goes through shared memory; a
+// thread forms 2 x 4 scores, and then adds to two rows of the output.  The
+// reads from shared memory bind: a thread's 24 words for 32 multiply-adds, one
+// word a lane and cycle where the units could do four.
 #include <type_traits>
 
 #include "common.cuh"
@@ -42,8 +42,9 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) shared_prefix_kernel(const PrefixParams p) {
+template <int D>
+__global__ void __launch_bounds__(kThreads) shared_f32_kernel(const PrefixParams p) {
+  using T = float;
   using S = Shape<D>;
   constexpr int E = Elt<T>::EPV, P = S::kPitch, NC = S::kCols;
   extern __shared__ __align__(16) float sm[];
@@ -377,19 +378,18 @@ template <typename T> cudaError_t launch_join(const JoinParams &p, cudaStream_t 
 
 // Ranges that the prefix is cut into so that the GPU's SMs have about four CTAs
 // each, none shorter than two tiles.
-int general_splits(int64_t B, int G, int Hk, int64_t tokens) {
+int f32_splits(int64_t B, int G, int Hk, int64_t tokens) {
   const int64_t items = (B * G + kRows - 1) / kRows * Hk, tiles = (tokens + kKeys - 1) / kKeys;
   int64_t n = (4 * (int64_t)sm_count() + items - 1) / items;
   if (n > tiles / 2) n = tiles / 2;
   return (int)(n < 1 ? 1 : n > kMaxPrefixParts ? kMaxPrefixParts : n);
 }
 
-template <typename T>
-cudaError_t launch_general(const PrefixParams &p, cudaStream_t stream) {
+cudaError_t launch_shared_f32(const PrefixParams &p, cudaStream_t stream) {
   const dim3 grid((unsigned)((int64_t)p.Hk * ((p.B * p.G + kRows - 1) / kRows)), (unsigned)p.splits);
   auto go = [&](auto D) -> cudaError_t {
     using S = Shape<decltype(D)::value>;
-    constexpr auto kern = shared_prefix_kernel<T, decltype(D)::value>;
+    constexpr auto kern = shared_f32_kernel<decltype(D)::value>;
     const cudaError_t e = allow_smem<kern>(S::kSmem);
     if (e != cudaSuccess) return e;
     return launch_dependent(kern, grid, dim3(kThreads), S::kSmem, stream, p);
@@ -406,7 +406,7 @@ SharedLayout shared_layout(int64_t B, int Hq, int Hk, int64_t d, int dtype, int6
   SharedLayout w{};
   const int G = Hq / Hk;
   if (B > 0 && tokens > 0)
-    w.splits = shared_tc_supported(d, dtype) ? shared_tc_splits(B, G, Hk, d, tokens) : general_splits(B, G, Hk, tokens);
+    w.splits = dtype == ATTNRES_BF16 ? shared_tc_splits(B, G, Hk, d, tokens) : f32_splits(B, G, Hk, tokens);
   const int64_t rows = B * Hq, parts = w.splits + 1;
   // Behind a prefix's kernel the SMs come free one after the other: ranges
   // of a third of the length even that out, where the tables leave each of
@@ -440,9 +440,7 @@ cudaError_t launch_shared(const SharedArgs &a, const SharedLayout &w) {
   p.wait_limit = wait_limit_cycles();
   cudaError_t e = cudaSuccess;
   if (w.splits > 0)
-    e = shared_tc_supported(a.d, a.dtype) ? launch_shared_tc(p, a.stream)
-        : a.dtype == ATTNRES_BF16         ? launch_general<__nv_bfloat16>(p, a.stream)
-                                          : launch_general<float>(p, a.stream);
+    e = a.dtype == ATTNRES_BF16 ? launch_shared_tc(p, a.stream) : launch_shared_f32(p, a.stream);
   if (e != cudaSuccess) return e;
   // The sequences' own tokens: the last part.  It needs nothing of the prefix's
   // kernel, which lets it start as soon as all of its own CTAs have (they have

@@ -4,8 +4,6 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
-#include "attnres.h"
-
 namespace attnres {
 
 constexpr int kMaxPrefixParts = 64;      // ranges of the prefix
@@ -53,9 +51,7 @@ struct PrefixParams {
   }
 };
 
-// The parts on the 5th-generation tensor cores (bf16, heads of up to 128
-// elements): how many, and the launch.
-inline bool shared_tc_supported(int64_t d, int dtype) { return dtype == ATTNRES_BF16 && d <= 128; }
+// The parts on the 5th-generation tensor cores (bf16): how many, and the launch.
 int shared_tc_splits(int64_t B, int G, int Hk, int64_t d, int64_t tokens);
 cudaError_t launch_shared_tc(const PrefixParams &p, cudaStream_t stream);
 

@@ -1,8 +1,9 @@
 // shared_tc.cu -- the parts of a shared prefix on the 5th-generation tensor
-// cores (bf16, heads of up to 128 elements; see shared.cu for the operator).
+// cores (bf16; see shared.cu for the operator).
 //
 // A CTA takes 256 rows (query heads of one key head, over the sequences) as
-// two tiles of 128, and one range of the prefix's tokens, 128 at a time:
+// two tiles of 128, and one range of the prefix's tokens, 128 at a time (heads
+// wider than 128: one tile, and 64):
 //   S = Q K^T (M 128, N 128, K d),  P = 2^(scale S - m),  O += P V (M 128, N d, K 128)
 // S and O are fp32 in tensor memory; two threads have a row of S, half of the
 // tokens each (one per row took 121 us where two take XX: the tensor cores
@@ -37,31 +38,36 @@ namespace attnres {
 namespace {
 
 constexpr int kTileRows = 128;             // rows of a tile: one per thread
-constexpr int kKeys = 128;                 // tokens of a step
 constexpr int kThreads = 768;
-constexpr uint32_t kBlock = 128 * 128;     // bytes: 128 rows of 64 bf16 columns
+constexpr uint32_t kQBlock = 128 * 128;    // bytes: 128 rows of 64 bf16 columns
 constexpr int kRegs = 80;                  // a thread's registers at the launch, then the roles' shares
 constexpr int kRegsSoftmax = 96, kRegsCopy = 48, kRegsMma = 48;
 static_assert(4 * kRegsSoftmax + kRegsCopy + kRegsMma <= 6 * kRegs, "more registers than the launch has");
 constexpr float kMost = 1024.f;            // the sum of a thread's weights of a step that the reference may stay for
 constexpr int kMasks = 4;                  // steps whose masks are kept
 
+// Heads of up to 64, 128 and 256 elements.  The last take half of the tensor
+// memory for one tile's O and half of a step's tokens.
 template <int D> struct Layout {
-  static constexpr int kBlocks = D / 64;
-  static constexpr uint32_t kTile = kBlocks * kBlock;                 // a tile of Q, K or V
-  static constexpr int kRing = D == 128 ? 5 : 6;                      // tiles of K and V, in turn
-  static constexpr uint32_t kOffRing = 2 * kTile;
+  static constexpr int kTiles = D <= 128 ? 2 : 1, kRows = kTiles * kTileRows;
+  static constexpr int kKeys = D <= 128 ? 128 : 64;                   // tokens of a step
+  static constexpr uint32_t kBlock = kKeys * 128;                     // bytes: a step's rows of 64 bf16 columns
+  static constexpr uint32_t kQTile = D / 64 * kQBlock, kTile = D / 64 * kBlock;
+  static constexpr int kRing = D == 64 ? 6 : 5;                       // tiles of K and V, in turn
+  static constexpr uint32_t kOffRing = kTiles * kQTile;
   static constexpr uint32_t kOffMask = kOffRing + kRing * kTile;
   static constexpr uint32_t kOffRow = kOffMask + kMasks * 16;         // a float per row
-  static constexpr uint32_t kOffBar = kOffRow + 2 * kTileRows * 4;
-  static constexpr uint32_t kOffCtl = kOffBar + (2 * kRing + kMasks + 7) * 8;
-  static constexpr uint32_t kBytes = kOffCtl + 16 + 1024;             // and the alignment's slack
+  static constexpr uint32_t kOffBar = kOffRow + kRows * 4;
   // barriers
   static constexpr int kFull = 0, kEmpty = kRing, kMask = 2 * kRing, kScores = kMask + kMasks, kWeights = kScores + 2,
-                       kOut = kWeights + 2, kDrain = kOut + 2;
+                       kOut = kWeights + 2, kDrain = kOut + 2, kBars = kDrain + 1;
+  static constexpr uint32_t kOffCtl = kOffBar + kBars * 8;
+  static constexpr uint32_t kBytes = kOffCtl + 16 + 1024;             // and the alignment's slack
+  static_assert(kBytes <= 232448, "what a CTA can have");
+  // Tensor memory columns: S (P over its first half) of the tiles, O.
+  static constexpr uint32_t kColO = 256;
+  static_assert(kTiles * kKeys <= (int)kColO && kColO + kTiles * D <= 512, "tensor memory");
 };
-// Tensor memory columns: S (P over its first half) of both tiles, O.
-constexpr uint32_t kColO = 256;
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -133,7 +139,7 @@ __device__ __forceinline__ bool any_of_pair(int id, bool x) {
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_constant__ PrefixParams p) {
   using L = Layout<D>;
-  constexpr int NR = L::kRing;
+  constexpr int NR = L::kRing, kKeys = L::kKeys;
   extern __shared__ unsigned char smem_raw[];
   grid_dependency_wait();
   launch_dependents();
@@ -144,14 +150,14 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   auto bar = [&](int b) { return base + L::kOffBar + 8u * b; };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = warp >> 2, quad = warp & 3;
 
-  const int all = p.B * p.G, tiles = (all + 2 * kTileRows - 1) / (2 * kTileRows);
-  const int hk = blockIdx.x / tiles, row0 = (blockIdx.x - hk * tiles) * 2 * kTileRows, split = blockIdx.y;
-  const int active = all - row0 > kTileRows ? 2 : 1;                          // tiles with rows
+  const int all = p.B * p.G, tiles = (all + L::kRows - 1) / L::kRows;
+  const int hk = blockIdx.x / tiles, row0 = (blockIdx.x - hk * tiles) * L::kRows, split = blockIdx.y;
+  const int active = L::kTiles == 2 && all - row0 > kTileRows ? 2 : 1;                          // tiles with rows
   int j0, j1;
   p.range<kKeys>(p.tokens(), split, j0, j1);
   const int steps = j1 > j0 ? (j1 - j0 + kKeys - 1) / kKeys : 0;
   if (steps == 0) {                        // an empty range's part weighs nothing
-    for (int i = threadIdx.x; i < 2 * kTileRows && row0 + i < all; i += kThreads)
+    for (int i = threadIdx.x; i < L::kRows && row0 + i < all; i += kThreads)
       p.part_lse[p.part(split, row0 + i, hk)] = -INFINITY;
     return;
   }
@@ -179,13 +185,13 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   // the queries, zero behind the batch and behind d
   {
     const int nvec = p.d / 8;
-    for (int i = threadIdx.x; i < 2 * kTileRows * (D / 8); i += kThreads) {
+    for (int i = threadIdx.x; i < L::kRows * (D / 8); i += kThreads) {
       const int r = i / (D / 8) % kTileRows, c = i % (D / 8), tile = i / (D / 8) / kTileRows, row = row0 + tile * kTileRows + r;
       uint4 x = make_uint4(0, 0, 0, 0);
       if (row < all && c < nvec)
         x = *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)p.q + (int64_t)(row / p.G) * p.q_stride +
                                              (int64_t)(hk * p.G + row % p.G) * p.d + c * 8);
-      *reinterpret_cast<uint4 *>(sm + tile * L::kTile + c / 8 * kBlock + r * 128 + ((c % 8) ^ (r & 7)) * 16) = x;
+      *reinterpret_cast<uint4 *>(sm + tile * L::kQTile + c / 8 * kQBlock + r * 128 + ((c % 8) ^ (r & 7)) * 16) = x;
     }
     fence_async_smem();
   }
@@ -210,19 +216,19 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   };
 
   if (group == 4) {
-    // ---------------- copies: 32 rows of every tile per warp ----------------
+    // ---------------- copies: a quarter of every tile's rows per warp ----------------
     share_registers<kRegsCopy, kRegs>();
-    constexpr int CH = D / 8, kPer = 32 / CH;          // 16-byte pieces of a row, rows per instruction
+    constexpr int CH = D / 8, kPer = 32 / CH, kWord = kKeys / 4;   // 16-byte pieces of a row, rows per instruction, rows
     const int c = lane % CH, sub = lane / CH;
     const bool inside = c * 8 < p.d;
-    const bool side = p.page % 32 == 0 && p.d == D;     // 32 tokens never span two pages, and rows have no padding
-    const uint32_t mine = c / 8 * kBlock + (quad * 32 + sub) * 128;
+    const bool side = p.page % kWord == 0 && p.d == D;  // the warp's tokens never span two pages, and rows have no padding
+    const uint32_t mine = c / 8 * L::kBlock + (quad * kWord + sub) * 128;
     // 16-byte piece c % 8 of row k kPer + sub of the warp, in the swizzle's place
     auto swizzled = [&](int k) -> uint32_t { return ((c % 8) ^ ((k * kPer + sub) & 7)) * 16; };
     bool alive = false;                                 // all of the warp's tokens are on a page
     auto page_row = [&](int step) -> int64_t {          // this lane's token of a step
-      const int j = j0 + step * kKeys + quad * 32 + lane;
-      return j < j1 ? p.row(j, hk) : -1;
+      const int j = j0 + step * kKeys + quad * kWord + lane;
+      return lane < kWord && j < j1 ? p.row(j, hk) : -1;
     };
     int64_t next = page_row(0);
     bool ok = true;
@@ -235,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         if (s >= NR && !(ok = __all_sync(0xffffffffu, wait(L::kEmpty + s % NR, s / NR - 1)))) break;
         if (kv == 0) {
           const uint32_t live = __ballot_sync(0xffffffffu, row >= 0);
-          alive = live == 0xffffffffu;
+          alive = live == (uint32_t)((1ull << kWord) - 1);
           if (lane == 0) {
             masks[i % kMasks * 4 + quad] = live;
             mbar_arrive(bar(L::kMask + i % kMasks));
@@ -248,10 +254,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           const char *src = from + (__shfl_sync(0xffffffffu, row, 0) + sub * p.d + c * 8) * 2;
           const int step = kPer * p.d * 2;
 #pragma unroll
-          for (int k = 0; k < 32 / kPer; ++k, src += step) copy16(to + k * kPer * 128 + swizzled(k), src);
+          for (int k = 0; k < kWord / kPer; ++k, src += step) copy16(to + k * kPer * 128 + swizzled(k), src);
         } else {
 #pragma unroll 4
-          for (int k = 0; k < 32 / kPer; ++k) {
+          for (int k = 0; k < kWord / kPer; ++k) {
             const int64_t at = __shfl_sync(0xffffffffu, row, k * kPer + sub);
             const bool live = at >= 0 && inside;
             copy16(to + k * kPer * 128 + swizzled(k), from + (live ? (at + c * 8) * 2 : 0), live);
@@ -267,12 +273,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       // ---------------- products ----------------
       const int ks = (p.d + 15) / 16;                   // K steps over d
       auto scores = [&](int g, int s) {                 // S of tile g with the K tile s
-        const Desc q = desc_k(base + g * L::kTile), k = desc_k(base + L::kOffRing + s % NR * L::kTile);
+        const Desc q = desc_k(base + g * L::kQTile), k = desc_k(base + L::kOffRing + s % NR * L::kTile);
 #pragma unroll 2
-        for (int x = 0; x < ks; ++x) {
-          const uint32_t off = x / 4 * kBlock + x % 4 * 32;
-          mma_bf16(tmem + g * 128, q.at(off), k.at(off), idesc_bf16(128, 128), x > 0);
-        }
+        for (int x = 0; x < ks; ++x)
+          mma_bf16(tmem + g * kKeys, q.at(x / 4 * kQBlock + x % 4 * 32), k.at(x / 4 * L::kBlock + x % 4 * 32),
+                   idesc_bf16(128, kKeys), x > 0);
         mma_commit(bar(L::kScores + g));
       };
       // A tile's copies are seen here through its barrier; the fence orders them before the products' reads.
@@ -292,10 +297,10 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
         for (int g = 0; ok && g < active; ++g) {
           if (!(ok = (g > 0 || landed(sv)) && wait(L::kWeights + g, i))) break;
           tc_fence_after();
-          const Desc v = desc_mn(base + L::kOffRing + sv % NR * L::kTile, kBlock);
+          const Desc v = desc_mn(base + L::kOffRing + sv % NR * L::kTile, L::kBlock);
 #pragma unroll
           for (int x = 0; x < kKeys / 16; ++x)
-            mma_bf16_ts(tmem + kColO + g * D, tmem + g * 128 + 8 * x, v.at(x * 2048), idesc_bf16(128, D) | kIdescMnB, i + x > 0);
+            mma_bf16_ts(tmem + L::kColO + g * D, tmem + g * kKeys + 8 * x, v.at(x * 2048), idesc_bf16(128, D) | kIdescMnB, i + x > 0);
           mma_commit(bar(L::kOut + g));
           if (g + 1 == active) mma_commit(bar(L::kEmpty + sv % NR));
           if (i + 1 == steps) continue;
@@ -311,10 +316,11 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       if (!mbar_wait_for(bar(L::kDrain), 0, kDrainLimitCycles)) raise_timeout();
     }
   } else {
-    // ---------------- softmax: two threads per row, 64 tokens of a step each ----------------
+    // ---------------- softmax: two threads per row, half of a step's tokens each ----------------
     share_registers<kRegsSoftmax, kRegs>();
     const int g = group >> 1, half = group & 1, row = row0 + g * kTileRows + quad * 32 + lane;
-    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16), at_s = lanes + g * 128, at_o = lanes + kColO + g * D + half * (D / 2);
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16), at_s = lanes + g * kKeys, at_o = lanes + L::kColO + g * D + half * (D / 2);
+    constexpr int kHalf = kKeys / 2;
     volatile float *slot = reinterpret_cast<float *>(sm + L::kOffRow) + g * kTileRows + quad * 32 + lane;
     const int both = 1 + g * 4 + quad;                  // the barrier of the two warps with these rows
     // f of the two threads' values (the first half's, the second's), for both
@@ -332,42 +338,48 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
     if (g < active) {
       for (int i = 0; i < steps; ++i) {
         wait(L::kMask + i % kMasks, i / kMasks);
-        const uint32_t mask0 = masks[i % kMasks * 4 + half * 2], mask1 = masks[i % kMasks * 4 + half * 2 + 1];
+        uint32_t mask0 = masks[i % kMasks * 4 + half * 2], mask1 = masks[i % kMasks * 4 + half * 2 + 1];
+        if (kHalf == 32) mask0 |= mask1 << 16;          // of 32 tokens each
         wait(L::kScores + g, i);
         __syncwarp();
         tc_fence_after();
-        uint32_t w[32], a[32], b[32];
-        // f of the exponents of this thread's tokens (m as an fp32 number)
-        auto each = [&](float ref, auto f) {
+        uint32_t w[kHalf / 2], a[32], b[32];
+        // f of the exponents of this thread's tokens
+        auto each = [&](auto f) {
+          const float ref = m == -INFINITY ? 0.f : m;
           const uint64_t minus = pair(-ref, -ref);
-          tmem_ld32(at_s + half * 64, a);
+          tmem_ld32(at_s + half * kHalf, a);
           tmem_wait_ld();
-          tmem_ld32(at_s + half * 64 + 32, b);
+          if (kHalf == 64) tmem_ld32(at_s + half * kHalf + 32, b);
           if (mask0 == 0xffffffffu) exponents<false>(a, scale2, minus, 0, f);
           else exponents<true>(a, scale2, minus, mask0, f);
-          tmem_wait_ld();
-          auto g2 = [&](int i, float x, float y) { f(i + 16, x, y); };
-          if (mask1 == 0xffffffffu) exponents<false>(b, scale2, minus, 0, g2);
-          else exponents<true>(b, scale2, minus, mask1, g2);
+          if constexpr (kHalf == 64) {
+            tmem_wait_ld();
+            auto behind = [&](int i, float x, float y) { f(i + 16, x, y); };
+            if (mask1 == 0xffffffffu) exponents<false>(b, scale2, minus, 0, behind);
+            else exponents<true>(b, scale2, minus, mask1, behind);
+          }
         };
         uint64_t sum, sum1;
         auto form = [&]() {
           sum = sum1 = 0;
-          each(m == -INFINITY ? 0.f : m, [&](int i, float x, float y) {
+          each([&](int i, float x, float y) {
             x = exp2_fast(x);
             y = exp2_fast(y);
-            if (i & 1) sum1 = add2(sum1, pair(x, y)); else sum = add2(sum, pair(x, y));
+            if (i & 1) sum1 = add2(sum1, pair(x, y));
+            else sum = add2(sum, pair(x, y));
             w[i] = Elt<__nv_bfloat16>::pack_word(x, y);
           });
           sum = add2(sum, sum1);
         };
         form();
-        // (the vote also says that both halves have read their scores, which the weights go over)
+        // The vote also says that both halves have read their scores, which the weights go over.
+        tc_fence_before();
         if (any_of_pair(both, m == -INFINITY || pair_sum(sum) > kMost)) {
           // a new reference: the maximum, where it has passed the old one
           float top = -INFINITY;
           const float old = m;
-          each(old == -INFINITY ? 0.f : old, [&](int, float x, float y) { top = fmaxf(top, fmaxf(x, y)); });
+          each([&](int, float x, float y) { top = fmaxf(top, fmaxf(x, y)); });
           top = joined(top, [](float x, float y) { return fmaxf(x, y); });
           if (top > (old == -INFINITY ? -INFINITY : 0.f)) m = (old == -INFINITY ? 0.f : old) + top;
           const float keep = m == old ? 1.f : exp2_fast(old - m);
@@ -385,15 +397,17 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
             }
           }
           form();
+          tc_fence_before();
           pair_barrier(both);
         }
+        tc_fence_after();
         l += pair_sum(sum);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
+        for (int q = 0; q < kHalf / 32; ++q) {
           uint32_t y[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) y[e] = w[q * 16 + e];
-          tmem_st16(at_s + half * 32 + q * 16, y);
+          tmem_st16(at_s + half * (kHalf / 2) + q * 16, y);
         }
         tmem_wait_st();
         tc_fence_before();
@@ -442,7 +456,7 @@ template <int D> cudaError_t launch(const PrefixParams &p, cudaStream_t stream) 
   if (!registers_as_planned<D>()) return cudaErrorInvalidConfiguration;
   const cudaError_t e = allow_smem<shared_tc_kernel<D>>(L::kBytes);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = ((int64_t)p.B * p.G + 2 * kTileRows - 1) / (2 * kTileRows);
+  const int64_t tiles = ((int64_t)p.B * p.G + L::kRows - 1) / L::kRows;
   return launch_dependent(shared_tc_kernel<D>, dim3((unsigned)(tiles * p.Hk), (unsigned)p.splits), dim3(kThreads), L::kBytes,
                           stream, p);
 }
@@ -450,15 +464,17 @@ template <int D> cudaError_t launch(const PrefixParams &p, cudaStream_t stream) 
 }  // namespace
 
 // Ranges of the prefix with the least time, in microseconds: a CTA's start and
-// end, its steps, and the parts that the join reads and writes.
+// end, its steps (of one tile or two), and the parts that the join reads and
+// writes.
 int shared_tc_splits(int64_t B, int G, int Hk, int64_t d, int64_t tokens) {
-  const int64_t items = (B * G + 2 * kTileRows - 1) / (2 * kTileRows) * Hk, steps = (tokens + kKeys - 1) / kKeys;
-  const double row_us = (double)B * G * Hk * d * 8e-6 / 4.;
+  const int rows = d <= 128 ? Layout<128>::kRows : Layout<256>::kRows, keys = d <= 128 ? Layout<128>::kKeys : Layout<256>::kKeys;
+  const int64_t items = (B * G + rows - 1) / rows * Hk, steps = (tokens + keys - 1) / keys;
+  const double row_us = (double)B * G * Hk * d * 8e-6 / 4., step_us = B * G > kTileRows && d <= 128 ? 1.8 : 1.2;
   const int64_t slots = sm_count();
   int best = 1;
   double least = 1e300;
   for (int n = 1; n <= kMaxPrefixParts && n <= steps; ++n) {
-    const double cost = (double)((items * n + slots - 1) / slots) * (8. + 1.3 * (double)((steps + n - 1) / n)) + row_us * n;
+    const double cost = (double)((items * n + slots - 1) / slots) * (8. + step_us * (double)((steps + n - 1) / n)) + row_us * n;
     if (cost < least) {
       least = cost;
       best = n;
@@ -468,7 +484,7 @@ int shared_tc_splits(int64_t B, int G, int Hk, int64_t d, int64_t tokens) {
 }
 
 cudaError_t launch_shared_tc(const PrefixParams &p, cudaStream_t stream) {
-  return p.d <= 64 ? launch<64>(p, stream) : launch<128>(p, stream);
+  return p.d <= 64 ? launch<64>(p, stream) : p.d <= 128 ? launch<128>(p, stream) : launch<256>(p, stream);
 }
 
 }  // namespace attnres
