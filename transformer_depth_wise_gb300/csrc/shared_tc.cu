@@ -465,7 +465,9 @@ template <int D> cudaError_t launch(const PrefixParams &p, cudaStream_t stream) 
 
 // Ranges of the prefix with the least time, in microseconds: a CTA's start and
 // end, its steps (of one tile or two), and the parts that the join reads and
-// writes.
+// writes; and the own tokens' kernel, which runs beside the last CTAs where
+// they leave a tenth of the SMs free (64 questions about 131071 tokens: 127 us
+// with 16 SMs left, 137 with 8, 134 with none, 132 with 24).
 int shared_tc_splits(int64_t B, int G, int Hk, int64_t d, int64_t tokens) {
   const int rows = d <= 128 ? Layout<128>::kRows : Layout<256>::kRows, keys = d <= 128 ? Layout<128>::kKeys : Layout<256>::kKeys;
   const int64_t items = (B * G + rows - 1) / rows * Hk, steps = (tokens + keys - 1) / keys;
@@ -474,7 +476,8 @@ int shared_tc_splits(int64_t B, int G, int Hk, int64_t d, int64_t tokens) {
   int best = 1;
   double least = 1e300;
   for (int n = 1; n <= kMaxPrefixParts && n <= steps; ++n) {
-    const double cost = (double)((items * n + slots - 1) / slots) * (8. + step_us * (double)((steps + n - 1) / n)) + row_us * n;
+    const int64_t waves = (items * n + slots - 1) / slots, free = waves * slots - items * n;
+    const double cost = (double)waves * (8. + step_us * (double)((steps + n - 1) / n)) + row_us * n + (10 * free < slots ? 18. : 0.);
     if (cost < least) {
       least = cost;
       best = n;
