@@ -328,6 +328,68 @@ def test_graph_with_growing_lengths_and_two_streams(gpu, dtype, d):
 
 
 @gpu_only
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_wait_that_runs_out_reports_timeout(gpu, d):
+    a = inputs(gpu, BF, 8, 2, d, 16, 3000, [20] * 40, 11)
+    lib = _lib.lib()
+    want = api.shared_prefix_attention(*a)
+    assert lib.attnres_take_device_error() == 0
+    try:
+        assert lib.attnres_set_wait_limit(1) == 0
+        api.shared_prefix_attention(*a)
+        assert lib.attnres_take_device_error() == -9                 # and the flag is cleared
+    finally:
+        lib.attnres_set_wait_limit(0)
+    got = api.shared_prefix_attention(*a)
+    assert lib.attnres_take_device_error() == 0
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+@gpu_only
+def test_two_calls_at_once_and_many_in_a_row(gpu):
+    """Eager calls on two streams side by side, and calls whose kernels overlap the next call's."""
+    cases = [inputs(gpu, BF, 16, 2, 128, 16, 2000 + 500 * k, [50 + k] * 30, 20 + k) for k in range(2)]
+    want = [api.shared_prefix_attention(*a) for a in cases]
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream(gpu) for _ in range(2)]
+    for _ in range(20):
+        got = []
+        for s, a in zip(sides, cases):
+            with torch.cuda.stream(s):
+                got.append(api.shared_prefix_attention(*a))
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(g, w))
+    ws = torch.empty(1 << 26, device=gpu, dtype=torch.uint8)         # one workspace, one call after the other
+    out = [[torch.empty_like(t) for t in w] for w in want]
+    for k in range(40):
+        api.shared_prefix_attention(*cases[k % 2], out=out[k % 2][0], lse=out[k % 2][1], workspace=ws)
+    for g, w in zip(out, want):
+        assert all(torch.equal(x, y) for x, y in zip(g, w))
+
+
+@gpu_only
+def test_inputs_written_just_before_and_outputs_read_just_after(gpu):
+    """The kernels of one call overlap, but not what comes before and after it on the stream."""
+    a = inputs(gpu, BF, 16, 4, 128, 32, 4000, [200] * 16, 30)
+    n = a[1].shape[0] * a[1].shape[1]
+    k0, v0, q0 = (t.clone() for t in a[:3][1:] + a[:1])
+    for step in range(10):
+        f = 1.0 + 0.125 * step
+        torch.mul(k0, f, out=a[1])
+        torch.mul(v0, f, out=a[2])
+        torch.mul(q0, 1.0 / f, out=a[0])
+        out, lse = api.shared_prefix_attention(*a)
+        got = out.clone(), lse.clone()
+        a[1].zero_()
+        torch.cuda.synchronize()
+        torch.mul(k0, f, out=a[1])
+        torch.cuda.synchronize()
+        want = api.shared_prefix_attention(*a)
+        assert all(torch.equal(x, y) for x, y in zip(got, want)), (step, n)
+
+
+@gpu_only
 def test_serving_layer(gpu):
     """One decoded token of a batch behind a shared image and text prefix: add + norm in 8 bits, the projection, head
     norm with three axes into the cache, attention behind the prefix."""
