@@ -201,8 +201,8 @@ __global__ void __launch_bounds__(kThreads) shared_f32_kernel(const PrefixParams
 struct JoinParams {
   const float *part_o, *part_lse, *piece_o, *piece_lse;
   const Pieces *pieces;                    // [B, Hk]
-  int splits, Hq, G, d;
-  int64_t rows;                            // B Hq
+  int splits, Hq, Hk, G, d;
+  int rows;                                // B Hq
   void *out;
   float *lse;
 };
@@ -252,20 +252,21 @@ template <typename T, int PARTS>
 __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_few_kernel(const JoinParams p) {
   grid_dependency_wait();
   const int lane = threadIdx.x % 32, d = p.d;
-  const int64_t row = (int64_t)blockIdx.x * kJoinWarps + threadIdx.x / 32;
+  const int row = blockIdx.x * kJoinWarps + threadIdx.x / 32;
   if (row >= p.rows) return;
-  const int head = (int)(row % p.Hq), hk = head / p.G, g = head % p.G;
+  const int b = row / p.Hq, head = row - b * p.Hq, hk = head / p.G, g = head - hk * p.G;
   float x[PARTS + 1];
   Sum y[PARTS + 1];
 #pragma unroll
   for (int k = 0; k <= PARTS; ++k) {
-    x[k] = p.part_lse[k * p.rows + row];
-    y[k].load(p.part_o + (k * p.rows + row) * d, lane, d);
+    const int64_t at = (int64_t)k * p.rows + row;
+    x[k] = p.part_lse[at];
+    y[k].load(p.part_o + at * d, lane, d);
   }
-  const Pieces own = p.pieces[row / p.Hq * (p.Hq / p.G) + hk];
+  const Pieces own = p.pieces[b * p.Hk + hk];
   const int pieces = own.first < 0 ? 0 : own.last - own.first + 1;
   if (pieces) x[PARTS] = -INFINITY;
-  auto piece = [&](int c) { return ((int64_t)(own.first + c) * 2 + (c == 0 ? own.slot : 0)) * p.G + g; };
+  auto piece = [&](int c) { return ((own.first + c) * 2 + (c == 0 ? own.slot : 0)) * p.G + g; };
   float M = -INFINITY;
   for (int c = lane; c < pieces; c += 32) M = fmaxf(M, p.piece_lse[piece(c)]);
   if (pieces) M = warp_max(M);
@@ -282,14 +283,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_few_kernel(const 
   }
 #pragma unroll 2
   for (int c = 0; c < pieces; ++c) {
-    const int64_t at = piece(c);
+    const int at = piece(c);
     Sum z;
-    z.load(p.piece_o + at * d, lane, d);
+    z.load(p.piece_o + (int64_t)at * d, lane, d);
     const float w = part_weight(p.piece_lse[at], M);
     L += w;
     s.add(z, w);
   }
-  s.store((T *)p.out + row * d, lane, d, L == 0.f ? 0.f : 1.f / L);
+  s.store((T *)p.out + (int64_t)row * d, lane, d, L == 0.f ? 0.f : 1.f / L);
   if (lane == 0 && p.lse) p.lse[row] = L == 0.f ? -INFINITY : M + logf(L);
 }
 
@@ -301,20 +302,20 @@ __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const Join
   __shared__ Sum sums[kJoinWarps][32];
   grid_dependency_wait();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, first = warp % WARPS, d = p.d;
-  const int64_t row = (int64_t)blockIdx.x * (kJoinWarps / WARPS) + warp / WARPS;
+  const int row = blockIdx.x * (kJoinWarps / WARPS) + warp / WARPS;
   const bool live = row < p.rows;
-  const int head = (int)((live ? row : 0) % p.Hq), hk = head / p.G, g = head % p.G;
+  const int b = row / p.Hq, head = row - b * p.Hq, hk = head / p.G, g = head - hk * p.G;
   // the lse of the lane's part of the prefix, before the pieces' place is known
-  float x0 = live && lane < p.splits ? p.part_lse[lane * p.rows + row] : -INFINITY;
+  float x0 = live && lane < p.splits ? p.part_lse[(int64_t)lane * p.rows + row] : -INFINITY;
   Pieces own{-1, 0, 0};
-  if (live) own = p.pieces[row / p.Hq * (p.Hq / p.G) + hk];
+  if (live) own = p.pieces[b * p.Hk + hk];
   const int parts = !live ? 0 : own.first < 0 ? p.splits + 1 : p.splits + own.last - own.first + 1;
   // part k's row, in part_o or in piece_o, and its lse
   auto find = [&](int k, const float *&src) -> float {
     src = p.part_o;
     if (k >= parts) return -INFINITY;
     if (k < p.splits || own.first < 0) {
-      const int64_t at = k * p.rows + row;
+      const int64_t at = (int64_t)k * p.rows + row;
       src = p.part_o + at * d;
       return k < 32 && k < p.splits ? x0 : p.part_lse[at];
     }
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const Join
   if (first > 0 || !live) return;
 #pragma unroll
   for (int k = 1; k < WARPS; ++k) s.add(sums[warp + k][lane], 1.f);
-  s.store((T *)p.out + row * d, lane, d, L == 0.f ? 0.f : 1.f / L);
+  s.store((T *)p.out + (int64_t)row * d, lane, d, L == 0.f ? 0.f : 1.f / L);
   if (lane == 0 && p.lse) p.lse[row] = L == 0.f ? -INFINITY : M + logf(L);
 }
 
@@ -457,7 +458,7 @@ cudaError_t launch_shared(const SharedArgs &a, const SharedLayout &w) {
   JoinParams j{};
   const PagedParts own = paged_parts(ws, p.G, a.d, w.own_ctas);
   j.part_o = p.part_o; j.part_lse = p.part_lse; j.piece_o = own.o; j.piece_lse = own.lse; j.pieces = s.pieces;
-  j.splits = w.splits; j.Hq = a.Hq; j.G = p.G; j.d = a.d; j.rows = rows; j.out = a.out; j.lse = a.lse;
+  j.splits = w.splits; j.Hq = a.Hq; j.Hk = a.Hk; j.G = p.G; j.d = a.d; j.rows = (int)rows; j.out = a.out; j.lse = a.lse;
   return a.dtype == ATTNRES_BF16 ? launch_join<__nv_bfloat16>(j, a.stream) : launch_join<float>(j, a.stream);
 }
 
