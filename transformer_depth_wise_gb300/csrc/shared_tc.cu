@@ -6,23 +6,33 @@
 // wider than 128: one tile, and 64):
 //   S = Q K^T (M 128, N 128, K d),  P = 2^(scale S - m),  O += P V (M 128, N d, K 128)
 // S and O are fp32 in tensor memory; two threads have a row of S, half of the
-// tokens each (one per row took 121 us where two take XX: the tensor cores
-// waited for the softmax); P, rounded to bf16, goes back to tensor memory over S, as the left operand of the second
-// product.  While one tile's weights are formed, the tensor cores work on the
-// other's products.
+// tokens each (113 us where one per row took 121); P, rounded to bf16, goes back
+// to tensor memory over S, as the left operand of the second product.  While
+// one tile's weights are formed, the tensor cores work on the other's products.
 //
 // m is a reference, not the maximum: it moves, to the maximum, only when the
 // weights that a thread forms in a step add up to more than 2^10 (and at the
 // first step), and O and the sum are rescaled then; fp32 and bf16 hold what lies
-// above it.  So a step needs no maximum: four instructions for a pair of
-// scores, of which a maximum would be a fourth more.  Rounding P to bf16 adds an
-// error of the size of the output's own rounding; the sum is that of the
-// unrounded weights.
+// above it.  So a step needs no maximum.  Rounding P to bf16 adds an error of
+// the size of the output's own rounding; the sum is that of the unrounded
+// weights.
 //
 // Roles: the two tiles' softmax (two warpgroups each); copies (cp.async of 16
 // bytes a lane, a row's page looked up by its own lane, into a ring of tiles
 // with the 128-byte swizzle; tokens behind the range or on no page arrive as
 // zeros and are masked); and one thread that issues the products.
+//
+// What bounds it: the products.  One of 128 x 128 x 16 with both operands in
+// shared memory takes 94 cycles of the 64 that the tensor cores need (8 KB at
+// 87 bytes a cycle, beside the copies' 19), and with the hand-overs between the
+// roles a step of both tiles takes some 3400 cycles for 2048.  Measured on GB300:
+// 512 rows and 131071 tokens, four key heads of 128: 102 us on 152 SMs (1.35
+// PFLOP/s, 67 % of cuBLAS's), 119 on the 136 that the launch takes; 1792 rows
+// and 8192 tokens, eight key heads: 67 to 72 us on 112 SMs.  Measured and not
+// kept (whole call of the first, 136 us when these were tried): tiles copied by
+// tensor-map boxes of 32 rows 136; steps of 80 tokens, whose P fits beside S, so
+// that the next scores need not wait for the weights' use, 148; a thread per
+// tile that issues, 148; a sixth of the exponentials as polynomials 161.
 //
 // Every wait is bounded: one that runs out records a flag and an abort mark in
 // shared memory, on which every other wait returns at once; what is in flight
