@@ -2,9 +2,11 @@
 
 The depth-wise softmax aggregation -- Full, Block and the two-phase Block
 inference scheme -- and the attention sublayer's operators between two
-aggregations (head norm with rotation, paged attention of one token, linear
-attention with decay) as hand-written CUDA kernels behind a C ABI
-(include/attnres.h, libattnres.so), with thin PyTorch wrappers.
+aggregations (head norm with rotation over one or several axes, paged
+attention of one token, also behind a prefix that a batch shares, linear
+attention with decay, the norm with the residual's addition) as hand-written
+CUDA kernels behind a C ABI (include/attnres.h, libattnres.so), with thin
+PyTorch wrappers.
 
 ``workloads`` (seeded synthetic inputs) imports without the CUDA library;
 everything in ``api`` needs libattnres.so and raises if it is missing.
@@ -16,7 +18,8 @@ __all__ = [
     "full_stack_forward", "TwoPhaseBlock", "block_two_phase", "block_schedule",
     "atomic_block_size", "head_norm_rotate", "head_norm_rotate_append", "head_norm_rotate_backward",
     "rotary_frequencies", "paged_attention", "linear_attention", "linear_attention_backward",
-    "linear_attention_step", "workloads",
+    "linear_attention_step", "rotary_axes", "add_rms_norm", "add_rms_norm_8bit", "add_rms_norm_backward",
+    "shared_prefix_attention", "workloads",
 ]
 
 
