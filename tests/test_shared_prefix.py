@@ -268,6 +268,16 @@ def test_rising_and_large_scores(gpu, dtype, d):
 
 
 @gpu_only
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (BF, 256), (F32, 64)])
+@pytest.mark.parametrize("scale", [-0.2, 0.0])
+def test_scales_that_are_not_positive(gpu, dtype, d, scale):
+    # the largest weight is the lowest product's; with none, every token weighs the same
+    a = inputs(gpu, dtype, 12, 2, d, 16, 300, [0, 3, 70, 1] * 12, 23)
+    a[7] = scale
+    check(a, dtype, d)
+
+
+@gpu_only
 @pytest.mark.parametrize("seed", range(12))
 def test_ragged_batches(gpu, seed):
     g = torch.Generator().manual_seed(100 + seed)
