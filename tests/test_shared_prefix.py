@@ -290,6 +290,14 @@ def test_ragged_batches(gpu, seed):
 
 
 @gpu_only
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("B", [1, 31, 33, 63, 97, 127, 129, 161, 191, 255, 257])
+def test_warps_partly_behind_the_batch(gpu, d, B):
+    # B rows per key head: in one warp of a tile some lanes have a row and others none
+    check(inputs(gpu, BF, 2, 2, d, 16, 150, [b % 3 for b in range(B)], 40 + B), BF, d)
+
+
+@gpu_only
 def test_strided_and_broadcast_queries(gpu):
     q, kc, vc, pt, n, t, lengths, scale = inputs(gpu, BF, 8, 2, 128, 16, 300, [5, 9, 0, 20], 4)
     wide = torch.zeros(4, 24 * 128, device=gpu, dtype=BF)

@@ -325,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
       mma_commit(bar(L::kDrain));
       if (!mbar_wait_for(bar(L::kDrain), 0, kDrainLimitCycles)) raise_timeout();
     }
+    __syncwarp();
   } else {
     // ---------------- softmax: two threads per row, half of a step's tokens each ----------------
     share_registers<kRegsSoftmax, kRegs>();
@@ -394,6 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
           if (top > (old == -INFINITY ? -INFINITY : 0.f)) m = (old == -INFINITY ? 0.f : old) + top;
           const float keep = m == old ? 1.f : exp2_fast(old - m);
           l *= keep;
+          __syncwarp();                                 // what each lane chose for itself is behind: loads and stores of the warp
           if (i > 0) {
 #pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
@@ -433,16 +435,17 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
 #pragma unroll 1
       for (int q = 0; q < D / 32; ++q) {
         float x[16];
+        __syncwarp();                                   // lanes behind the batch store nothing; the loads take all of them
         tmem_ld16(at_o + q * 16, x);
         tmem_wait_ld();
-        if (row >= all) continue;
 #pragma unroll
         for (int e = 0; e < 16; e += 4) {
           const int c = half * (D / 2) + q * 16 + e;
-          if (c < p.d)
+          if (row < all && c < p.d)
             *reinterpret_cast<float4 *>(p.part_o + at * p.d + c) = make_float4(x[e] * f, x[e + 1] * f, x[e + 2] * f, x[e + 3] * f);
         }
       }
+      __syncwarp();
       if (row < all && half == 0) p.part_lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
       tc_fence_before();
     }
