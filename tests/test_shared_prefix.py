@@ -408,6 +408,41 @@ def test_inputs_written_just_before_and_outputs_read_just_after(gpu):
 
 
 @gpu_only
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 256), (F32, 64)])
+@pytest.mark.parametrize("per", [3, 40])
+def test_every_input_written_just_before(gpu, dtype, d, per):
+    """Caches, queries, tables, the prefix's length and the sequences' own, each from a kernel right before the call; with
+    short tables, and with long ones, whose tokens are worked on beside the prefix."""
+    B, Hk, page, first = 32, 4, 16, 250
+    g = wk.generator(31, gpu)
+    pool = first + B * per
+    sets = []
+    for k in range(2):
+        pages = torch.randperm(pool, device=gpu, generator=g).int()
+        sets.append([rand(g, B, 16, d, dtype=dtype), rand(g, pool, Hk, page, d, dtype=dtype),
+                     rand(g, pool, Hk, page, d, dtype=dtype), pages[:first].contiguous(),
+                     torch.tensor([4000 - 777 * k], device=gpu).int(), pages[first:].view(B, per).contiguous(),
+                     torch.randint(0, per * page + 1, (B,), device=gpu, generator=g).int()])
+    want = [api.shared_prefix_attention(*s, d ** -0.5) for s in sets]
+    torch.cuda.synchronize()
+    a = [torch.zeros_like(t) for t in sets[0]]
+    ws = torch.full((1 << 28,), 1, device=gpu, dtype=torch.uint8)
+    out, lse = (torch.empty_like(t) for t in want[0])
+    for step in range(12):
+        k = step % 2
+        for to, t in zip(a, sets[k]):
+            to.copy_(t)
+        if step % 3 == 0:                                             # what a workspace held does not matter
+            ws.view(torch.int32).fill_(1)
+        api.shared_prefix_attention(*a, d ** -0.5, out=out, lse=lse, workspace=ws)
+        got = out.clone(), lse.clone()
+        for to in a:
+            to.zero_()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want[k])), step
+
+
+@gpu_only
 def test_serving_layer(gpu):
     """One decoded token of a batch behind a shared image and text prefix: add + norm in 8 bits, the projection, head
     norm with three axes into the cache, attention behind the prefix."""

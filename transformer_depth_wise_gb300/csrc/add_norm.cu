@@ -118,15 +118,6 @@ __device__ __forceinline__ void cta_totals(float &a, float &b, float *red, int p
   b = __shfl_sync(0xffffffffu, v, 16);
 }
 
-// A 16-byte load that leaves nothing in L1: each vector is read once (and may
-// be written later, where an output lies on an input).
-__device__ __forceinline__ uint4 ld_once(const void *p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
-  return v;
-}
-
 template <typename T>
 __device__ __forceinline__ void load_weight(uint64_t *w, const float *src) {
 #pragma unroll

@@ -147,6 +147,15 @@ __device__ __forceinline__ uint4 ld_stream_vec(const char *base, int k, int tpr)
   return ld_stream(base + (size_t)k * tpr * 16);
 }
 
+// The same through the ordinary path: for memory that the kernel writes later,
+// or that another kernel may have written while this one was already running.
+__device__ __forceinline__ uint4 ld_once(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+
 // Plain 16-byte load through L1 (small, reused operands: queries, gains, u).
 __device__ __forceinline__ float4 ld_f4(const float *p) {
   return __ldg(reinterpret_cast<const float4 *>(p));
@@ -216,14 +225,35 @@ __device__ __forceinline__ void prefetch_l2_bulk(const void *gmem, uint32_t byte
 // and its first instruction, grid_dependency_wait(), returns once that grid
 // has completed and its writes are visible; every kernel launched this way
 // starts with it, so no access to another kernel's data comes earlier (the
-// caller may have just written the query or gain on the same stream).  No
-// kernel triggers its dependents early: CTAs launched into the few SMs an
-// earlier grid has left idle crowded onto them, and measured on a GB300 the
-// early trigger was slower everywhere (Full stack 26.9 -> 28.4 ms, its
-// two-phase schedule 9.04 -> 9.96 ms, decode graph 188 -> 196 us).  For a
+// caller may have just written the query or gain on the same stream).  For a
 // kernel launched without the attribute the wait is a no-op.
+//
+// As a rule no kernel triggers its dependents early: CTAs launched into the
+// few SMs an earlier grid has left idle crowded onto them, and measured on a
+// GB300 the early trigger was slower everywhere (Full stack 26.9 -> 28.4 ms,
+// its two-phase schedule 9.04 -> 9.96 ms, decode graph 188 -> 196 us).  The
+// one exception is attention behind a shared prefix (shared.cu): a kernel of
+// one warp triggers before its wait (its follower waits for its end), and the
+// prefix's kernels trigger after theirs, so that the paged kernel that follows
+// may work beside them.  That one reads nothing of theirs, but what the
+// kernels before them wrote, and only a thread that has waited sees that by
+// the grids' own order.  So it either waits like every other kernel, or finds
+// a mark raised (acquired there, released by a thread that has waited), and
+// then one of its CTAs waits at the end, for the kernels that follow.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// A mark in global memory that one kernel raises for another: what the raising thread has seen before is visible to
+// a thread that finds it raised.
+__device__ __forceinline__ void raise_mark(unsigned *mark) {
+  asm volatile("st.release.gpu.global.u32 [%0], 1;" ::"l"(mark) : "memory");
+}
+__device__ __forceinline__ bool mark_raised(const unsigned *mark) {
+  unsigned v;
+  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(mark) : "memory");
+  return v == 1u;
+}
 
 // Launch `kern` with programmatic stream serialization: its launch overlaps
 // the end of the previous kernel on the stream (it must call

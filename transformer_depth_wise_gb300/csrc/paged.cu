@@ -43,7 +43,7 @@ struct PagedParams {
   int64_t num_pages;
   float scale;
   void *out;                           // [B, Hq, d]
-  bool wait_last;                      // the kernel before is waited for at the end: nothing of it is read here
+  const unsigned *ready;               // a mark of the kernel before, which is waited for at the end only (or nullptr)
   bool out_f32;                        // out in fp32 whatever the type (a part of a longer attention)
   float *lse;                          // [B, Hq] or nullptr
   float *part_o, *part_lse;            // [ctas][2][G][d], [ctas][2][G]
@@ -52,6 +52,18 @@ struct PagedParams {
   __device__ __forceinline__ int page_of(int j) const { return page_shift >= 0 ? j >> page_shift : j / page; }
   __device__ __forceinline__ int slot_of(int j) const { return page_shift >= 0 ? j & (page - 1) : j % page; }
 };
+
+// What a kernel starts with, all threads: the wait for what came before.  With
+// a mark the kernel before has started this one early, and nothing of that one
+// is read here; a thread that finds the mark raised sees all that it waited
+// for itself, and one that does not waits for its end.
+__device__ __forceinline__ void wait_for_inputs(const PagedParams &p) {
+  if (!p.ready || !mark_raised(p.ready)) grid_dependency_wait();
+}
+// What it ends with: one CTA's wait holds the launch's end until the kernel before has ended.
+__device__ __forceinline__ void wait_for_last(const PagedParams &p) {
+  if (p.ready && blockIdx.x + 1 == gridDim.x) grid_dependency_wait();
+}
 
 // The sequence's length, held within what its row of the page table covers.
 __device__ __forceinline__ int64_t clamped_length(const PagedParams &p, int b) {
@@ -218,7 +230,7 @@ __global__ void __launch_bounds__(kWarpsF * 32, resident(NV, GQ)) paged_f32_kern
   constexpr int E = 4, N = NV * E;
   extern __shared__ float sm[];                     // [warps][GQ][d] outputs, then [warps][GQ] m, then l
   __shared__ int64_t red[kWarpsF];
-  if (!p.wait_last) grid_dependency_wait();
+  wait_for_inputs(p);
   const int64_t total = all_tiles(p, red) * p.Hk;
   Walk w = walk_begin(p, total);
   if (threadIdx.x == 0) p.cuts[blockIdx.x].b = -1;
@@ -268,8 +280,8 @@ __global__ void __launch_bounds__(kWarpsF * 32, resident(NV, GQ)) paged_f32_kern
         for (int v = 0; v < NV; ++v) {
           nk[v] = nv[v] = make_uint4(0, 0, 0, 0);
           if (next_live && v * 8 + l8 < nvec) {
-            nk[v] = ld_stream((const float *)p.k + row + (v * 8 + l8) * E);
-            nv[v] = ld_stream((const float *)p.v + row + (v * 8 + l8) * E);
+            nk[v] = ld_once((const float *)p.k + row + (v * 8 + l8) * E);
+            nv[v] = ld_once((const float *)p.v + row + (v * 8 + l8) * E);
           }
         }
       };
@@ -377,8 +389,7 @@ __global__ void __launch_bounds__(kWarpsF * 32, resident(NV, GQ)) paged_f32_kern
     __syncthreads();
   }
   write_empty<float>(p);
-  // One CTA's wait holds the launch's end until the kernel before has ended.
-  if (p.wait_last && blockIdx.x + 1 == gridDim.x) grid_dependency_wait();
+  wait_for_last(p);
 }
 
 // ---------------------------------------------------------------------------
@@ -447,7 +458,7 @@ __global__ void __launch_bounds__(kWarpsM * 32, MmaShape<D>::kCtas) paged_mma_ke
   __shared__ float smax[kWarpsM][16], ssum[kWarpsM][16];
   __shared__ uint32_t live_bits[kWarpsM][S::kStages];
   float *so = reinterpret_cast<float *>(smem + kWarpsM * S::kStages * S::kStage);   // [16][kOutPitch]
-  if (!p.wait_last) grid_dependency_wait();
+  wait_for_inputs(p);
   const int64_t total = all_tiles(p, red) * p.Hk;
   Walk w = walk_begin(p, total);
   if (threadIdx.x == 0) p.cuts[blockIdx.x].b = -1;
@@ -676,8 +687,7 @@ __global__ void __launch_bounds__(kWarpsM * 32, MmaShape<D>::kCtas) paged_mma_ke
   }
   cp_async_wait<0>();
   write_empty<__nv_bfloat16>(p);
-  // One CTA's wait holds the launch's end until the kernel before has ended.
-  if (p.wait_last && blockIdx.x + 1 == gridDim.x) grid_dependency_wait();
+  wait_for_last(p);
 }
 
 // One CTA per (noted pair, query head): the parts' weights, then their sum.
@@ -770,7 +780,7 @@ cudaError_t launch_paged(const PagedArgs &a) {
   p.page_shift = -1;
   for (int i = 0; i < 31; ++i)
     if (a.page_size == 1 << i) p.page_shift = i;
-  p.scale = a.scale; p.out = a.out; p.lse = a.lse; p.out_f32 = a.out_f32; p.wait_last = a.wait_last; p.pieces = a.pieces;
+  p.scale = a.scale; p.out = a.out; p.lse = a.lse; p.out_f32 = a.out_f32; p.ready = a.ready; p.pieces = a.pieces;
   const int ctas = a.ctas;
   p.cuts = static_cast<Cut *>(a.workspace);
   const PagedParts parts = paged_parts(a.workspace, p.G, a.d, ctas);

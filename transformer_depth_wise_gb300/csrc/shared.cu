@@ -53,8 +53,7 @@ __global__ void __launch_bounds__(kThreads) shared_f32_kernel(const PrefixParams
   extern __shared__ __align__(16) float sm[];
   float *qs = sm, *ks = sm + S::kOffK, *vs = sm + S::kOffV, *ps = sm + S::kOffP;
   __shared__ int live[kKeys];
-  grid_dependency_wait();
-  launch_dependents();
+  p.begin();
   const int all = p.B * p.G, tiles = (all + ROWS - 1) / ROWS;
   const int hk = blockIdx.x / tiles, row0 = (blockIdx.x - hk * tiles) * ROWS, split = blockIdx.y;
   int j0, j1;
@@ -461,6 +460,13 @@ cudaError_t launch_shared_f32(const PrefixParams &p, cudaStream_t stream) {
   return wide ? go(R64{}, R128{}) : go(R64{}, R64{});
 }
 
+// Lowers the own tokens' mark, whatever the workspace holds.
+__global__ void __launch_bounds__(32) shared_lower_kernel(unsigned *ready) {
+  launch_dependents();                   // the prefix's kernel, which waits for this one's end
+  grid_dependency_wait();
+  if (threadIdx.x == 0) *ready = 0;
+}
+
 int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
 
 }  // namespace
@@ -478,7 +484,8 @@ SharedLayout shared_layout(int64_t B, int Hq, int Hk, int64_t d, int dtype, int6
   w.own_ctas = paged_ctas(d, dtype);
   if (w.splits && B * Hk * (own / 64) >= 16 * (int64_t)paged_fine_ctas(d, dtype)) w.own_ctas = paged_fine_ctas(d, dtype);
   w.pieces = up16(paged_workspace_bytes(G, d, dtype, w.own_ctas));
-  w.part_lse = w.pieces + up16(B * Hk * (int64_t)sizeof(Pieces));
+  w.ready = w.pieces + up16(B * Hk * (int64_t)sizeof(Pieces));
+  w.part_lse = w.ready + 16;
   w.part_o = w.part_lse + up16(parts * rows * (int64_t)sizeof(float));
   w.bytes = w.part_o + parts * rows * d * (int64_t)sizeof(float);
   return w;
@@ -502,19 +509,24 @@ cudaError_t launch_shared(const SharedArgs &a, const SharedLayout &w) {
   p.splits = w.splits;
   p.wait_limit = wait_limit_cycles();
   cudaError_t e = cudaSuccess;
-  if (w.splits > 0)
+  if (w.splits > 0) {
+    p.ready = reinterpret_cast<unsigned *>(ws + w.ready);
+    e = launch_dependent(shared_lower_kernel, dim3(1), dim3(32), 0, a.stream, p.ready);
+  }
+  if (e == cudaSuccess && w.splits > 0)
     e = a.dtype == ATTNRES_BF16 ? launch_shared_tc(p, a.stream) : launch_shared_f32(p, a.stream);
   if (e != cudaSuccess) return e;
   // The sequences' own tokens: the last part.  It needs nothing of the prefix's
-  // kernel, which lets it start as soon as all of its own CTAs have (they have
-  // waited for what came before), so it fills the SMs that that one leaves, and
-  // waits for its end at its own.
+  // kernel, which lets it start as soon as all of its own CTAs have: by the mark
+  // it fills the SMs that that one leaves, and waits for its end at its own (256
+  // chats 258 us, 280 where it waits at its start; four chats 14 and 19 us; the
+  // launch that lowers the mark shows in neither).
   PagedArgs s{};
   s.q = a.q; s.q_stride = a.q_stride; s.k_cache = a.k_cache; s.v_cache = a.v_cache; s.num_pages = a.num_pages;
   s.page_size = a.page_size; s.max_pages = a.max_pages; s.page_table = a.page_table; s.lengths = a.lengths;
   s.B = a.B; s.Hq = a.Hq; s.Hk = a.Hk; s.d = a.d; s.dtype = a.dtype; s.scale = a.scale;
   s.out = p.part_o + w.splits * rows * a.d; s.lse = p.part_lse + w.splits * rows; s.out_f32 = true;
-  s.workspace = ws; s.stream = a.stream; s.wait_last = w.splits > 0; s.ctas = w.own_ctas;
+  s.workspace = ws; s.stream = a.stream; s.ready = p.ready; s.ctas = w.own_ctas;
   s.pieces = reinterpret_cast<Pieces *>(ws + w.pieces);
   if ((e = launch_paged(s)) != cudaSuccess) return e;
   JoinParams j{};

@@ -1,16 +1,12 @@
 // shared.cuh -- what the kernels of a shared prefix's parts have in common.
 #pragma once
 
-#include <cuda_runtime.h>
+#include "common.cuh"
 #include <stdint.h>
 
 namespace attnres {
 
 constexpr int kMaxPrefixParts = 64;      // ranges of the prefix
-
-// The kernel that follows on the stream may start: called by kernels of a
-// prefix's parts, whose follower waits for them at its end only.
-__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 struct PrefixParams {
   const void *q, *k, *v;
@@ -23,6 +19,17 @@ struct PrefixParams {
   float *part_o, *part_lse;              // [splits][B Hq][d], [splits][B Hq]
   int splits;
   long long wait_limit;                  // SM clock cycles a wait of the tensor-core kernel may take
+  unsigned *ready;                       // the follower's mark, or nullptr: it waits for this kernel's end
+
+  // What every thread of a prefix's kernel starts with: the wait for what
+  // came before.  Then the own tokens' kernel may start; with `ready` it goes
+  // to work at once, and sees by the mark that this thread has waited.
+  __device__ __forceinline__ void begin() const {
+    grid_dependency_wait();
+    if (threadIdx.x != 0) return;
+    if (ready && blockIdx.x == 0 && blockIdx.y == 0) raise_mark(ready);
+    launch_dependents();
+  }
 
   // The prefix's tokens, held within what the table covers.
   __device__ __forceinline__ int tokens() const {

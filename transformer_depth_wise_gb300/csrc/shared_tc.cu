@@ -151,8 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1) shared_tc_kernel(const __grid_con
   using L = Layout<D>;
   constexpr int NR = L::kRing, kKeys = L::kKeys;
   extern __shared__ unsigned char smem_raw[];
-  grid_dependency_wait();
-  launch_dependents();
+  p.begin();
   unsigned char *sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const uint32_t base = smem_u32(sm);
   volatile uint32_t *masks = reinterpret_cast<uint32_t *>(sm + L::kOffMask);
