@@ -279,7 +279,7 @@ struct PagedArgs {
   void *workspace;             // paged_workspace_bytes()
   cudaStream_t stream;
   int ctas;                    // paged_ctas(), or paged_fine_ctas()
-  bool out_f32;                // out is fp32 whatever the type
+  bool out_f32;                // out is fp32 whatever the type (with pieces)
   const unsigned *ready;       // the mark of the kernel before, which starts this one early (nullptr: none)
   Pieces *pieces;              // [B, Hk]: the caller joins the pairs that are cut (nullptr: joined here)
 };

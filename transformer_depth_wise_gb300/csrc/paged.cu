@@ -44,7 +44,7 @@ struct PagedParams {
   float scale;
   void *out;                           // [B, Hq, d]
   const unsigned *ready;               // a mark of the kernel before, which is waited for at the end only (or nullptr)
-  bool out_f32;                        // out in fp32 whatever the type (a part of a longer attention)
+  bool out_f32;                        // out in fp32 whatever the type (a part of a longer attention, with pieces)
   float *lse;                          // [B, Hq] or nullptr
   float *part_o, *part_lse;            // [ctas][2][G][d], [ctas][2][G]
   Cut *cuts;                           // [ctas]
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kWarpsF * 32, resident(NV, GQ)) paged_f32_kern
   wait_for_inputs(p);
   const int64_t total = all_tiles(p, red) * p.Hk;
   Walk w = walk_begin(p, total);
-  if (threadIdx.x == 0) p.cuts[blockIdx.x].b = -1;
+  if (threadIdx.x == 0 && !p.pieces) p.cuts[blockIdx.x].b = -1;
   if (!w.more())                                    // an empty range's part weighs nothing
     for (int g = threadIdx.x; g < p.G; g += blockDim.x) p.part_lse[(int64_t)blockIdx.x * 2 * p.G + g] = -INFINITY;
   const int64_t first = w.at;
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kWarpsM * 32, MmaShape<D>::kCtas) paged_mma_ke
   wait_for_inputs(p);
   const int64_t total = all_tiles(p, red) * p.Hk;
   Walk w = walk_begin(p, total);
-  if (threadIdx.x == 0) p.cuts[blockIdx.x].b = -1;
+  if (threadIdx.x == 0 && !p.pieces) p.cuts[blockIdx.x].b = -1;
   if (!w.more())                                    // an empty range's part weighs nothing
     for (int g = threadIdx.x; g < p.G; g += blockDim.x) p.part_lse[(int64_t)blockIdx.x * 2 * p.G + g] = -INFINITY;
   const int64_t first = w.at;
@@ -746,7 +746,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Paged
     float x = 0.f;
 #pragma unroll
     for (int k = 0; k < kJoinWarps; ++k) x += sums[k * p.d + e];
-    if (std::is_same<T, float>::value || p.out_f32) ((float *)p.out)[row * p.d + e] = x * r;
+    if constexpr (std::is_same<T, float>::value) ((float *)p.out)[row * p.d + e] = x * r;
     else ((__nv_bfloat16 *)p.out)[row * p.d + e] = __float2bfloat16_rn(x * r);
   }
   if (threadIdx.x == 0 && p.lse) p.lse[row] = L == 0.f ? -INFINITY : M + logf(L);
