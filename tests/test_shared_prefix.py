@@ -267,6 +267,86 @@ def test_rising_and_large_scores(gpu, dtype, d):
         check(a, dtype, d, f"order {order}")
 
 
+def ranges_of(dev, dtype, B, Hq, Hk, d, page, pages):
+    """Ranges that a call without own pages cuts the prefix into: each adds its outputs and lse to the workspace."""
+    size = lambda n: api._sized("attnres_shared_prefix_attention_workspace_bytes", dev, B, Hq, Hk, d,  # noqa: E731
+                                api._CODES[dtype], page, n, 0)
+    part, over = divmod(size(pages) - size(0), 4 * B * Hq * (d + 1))
+    assert over == 0 and B * Hq % 4 == 0
+    return part
+
+
+def prefix_ref(q, kc, vc, fp, fs, scale, coarse):
+    """shared_ref for a prefix alone, in float64 on the GPU; fp, fs: its tokens' pages and slots."""
+    B, Hq, d = q.shape
+    Hk, n = kc.shape[1], len(fp)
+    parts = []
+    for hk in range(Hk):
+        k, v = kc[fp, hk, fs].double(), vc[fp, hk, fs].double()
+        rows = q.unflatten(1, (Hk, -1))[:, hk].flatten(0, 1).double()
+        x = rows @ k.T * scale
+        lse = torch.logsumexp(x, -1)
+        p = torch.exp(x - lse[:, None])
+        size = p @ v.abs()
+        ds = (d + 2) * E * (rows.abs() @ k.abs().T).amax(-1) * abs(scale)
+        ds = ds + 4 * E * (x.amax(-1) - x.amin(-1)) + (32 + n / 8) * E
+        o = p @ v
+        tol = (2 * ds[:, None] + 2.0 ** -17 + coarse) * size
+        parts.append([t.unflatten(0, (B, -1)) for t in (o, lse, tol, ds + 2 * E * lse.abs())])
+    return [torch.stack(t, 1).flatten(1, 2).cpu() for t in zip(*parts)]
+
+
+@gpu_only
+@pytest.mark.parametrize("pattern", ["random", "rising", "falling", "slowly rising", "spikes", "gaps"])
+@pytest.mark.parametrize("dtype,d,B,G,tile", [(BF, 64, 3, 2, 128), (BF, 64, 150, 1, 128), (BF, 128, 4, 3, 128), (BF, 128, 50, 4, 128),
+                                              (BF, 96, 41, 4, 128), (BF, 256, 2, 1, 64), (BF, 256, 33, 3, 64),
+                                              (F32, 64, 3, 2, 64), (F32, 128, 20, 4, 64), (F32, 256, 2, 1, 64)])
+def test_many_steps_in_one_range(gpu, dtype, d, B, G, tile, pattern):
+    """So many key heads that a range has 20 steps and more: references, maxima and sums go on from step to step, and
+    every ring's places are used again and again."""
+    Hk, page = 136, 16
+    steps = 45 if dtype is F32 and d == 64 else 23
+    prefix = steps * tile - 37                                       # the last step is a partial one
+    g = wk.generator(50, gpu)
+    pages = -(-prefix // page)
+    if torch.cuda.get_device_properties(gpu).multi_processor_count == 152:
+        assert steps // ranges_of(gpu, dtype, B, G * Hk, Hk, d, page, pages) >= 20
+    pt = torch.randperm(pages, device=gpu, generator=g).int()
+    q = rand(g, B, G * Hk, d, dtype=dtype, scale=1.5).abs()
+    kc, vc = rand(g, pages, Hk, page, d, dtype=dtype), rand(g, pages, Hk, page, d, dtype=dtype)
+    j = torch.arange(pages * page, device=gpu)
+    # a query's product with one key is some 1.2 sqrt(d) times what is added to the key's elements: 9 to 19 here
+    if pattern == "random":
+        up = None
+    elif pattern in ("rising", "falling"):                           # by 70 to 150 in all, a few powers of two per step
+        up = torch.linspace(-4, 4, pages * page, device=gpu) * (1 if pattern == "rising" else -1)
+    elif pattern == "slowly rising":                                 # the weights pass the reference, mostly within 2^10
+        up = torch.linspace(0, 0.8, pages * page, device=gpu)
+    elif pattern == "spikes":                                        # alone by hundreds of powers of two, each above the last
+        up = torch.full((pages * page,), -3.0, device=gpu)
+        for i, at in enumerate((5 * tile + 3, 11 * tile + tile // 2, 11 * tile + tile // 2 + 1, prefix - 1)):
+            up[at] = 6.0 + 6 * i
+    else:                                                            # the first steps, one in the middle and parts of others on no page
+        up = torch.linspace(-2, 2, pages * page, device=gpu)
+        pt[:2 * tile // page + 1] = -1
+        pt[9 * tile // page:10 * tile // page] = pages
+        pt[12 * tile // page + 1:14 * tile // page - 1] = -7
+    if up is not None:
+        at = pt.long()[j // page]
+        ok = at >= 0
+        ok &= at < pages
+        kc[at[ok], :, (j % page)[ok]] = (kc[at[ok], :, (j % page)[ok]].float() * 0.1 + up[ok, None, None]).to(dtype)
+    a = [q, kc, vc, pt, torch.tensor([prefix], device=gpu).int(), torch.empty(B, 0, device=gpu, dtype=torch.int32),
+         torch.zeros(B, device=gpu, dtype=torch.int32), d ** -0.5]
+    out, lse = api.shared_prefix_attention(*a)
+    want, wlse, tol, ltol = prefix_ref(q, kc, vc, *(t.to(gpu) for t in tokens_of(pt, prefix, page, pages)), a[7],
+                                       coarse_of(dtype, d))
+    within(out, want, U[dtype] * want.abs() + tol, "out")
+    within(lse, wlse, ltol, "lse")
+    again = api.shared_prefix_attention(*a)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+
+
 @gpu_only
 @pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (BF, 256), (F32, 64)])
 @pytest.mark.parametrize("scale", [-0.2, 0.0])
