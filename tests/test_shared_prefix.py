@@ -253,6 +253,36 @@ def test_what_is_no_number(gpu, dtype, d):
 
 
 @gpu_only
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 256), (F32, 64), (F32, 128)])
+@pytest.mark.parametrize("prefix,own", [(100, 40), (4000, 40), (100, 3000), (20000, 5000)])
+def test_infinity_behind_a_weight_that_is_too_small(gpu, dtype, d, prefix, own):
+    """Values that are no numbers show however far their token's score lies below the others', in whichever part."""
+    for far in ("prefix", "own"):
+        a = inputs(gpu, dtype, 4, 2, d, 16, prefix, [own, own // 2, own], 70)
+        q, kc, vc, pt, n, t, lengths, _ = a
+        q.copy_(q.abs() + 0.5)                       # scores of some +-8 sqrt(d): more than e^-100 apart
+        low, high = (pt, t.flatten()) if far == "prefix" else (t.flatten(), pt)
+        kc[low.long()], kc[high.long()] = -8.0, 8.0
+        if far == "prefix":
+            vc[pt[3], 0, 5, 9], vc[pt[2], 1, 0, 4] = math.inf, math.nan
+            rows = [0, 1, 2]
+        else:
+            vc[t[1, 0], 0, 5, 9], vc[t[1, 1], 1, 0, 4] = math.inf, math.nan
+            rows = [1]
+        out, lse = api.shared_prefix_attention(*a)
+        bad = torch.zeros(3, 4, d, dtype=torch.bool, device=gpu)
+        for b in rows:
+            bad[b, :2, 9] = bad[b, 2:, 4] = True
+        assert torch.equal(~out.isfinite(), bad), far
+        assert bool(lse.isfinite().all())
+        # the same of one cache
+        whole = torch.cat((pt.expand(3, -1), t), 1).contiguous()
+        if prefix % 16 == 0:
+            out, _ = api.paged_attention(q, kc, vc, whole, lengths + prefix, a[7])
+            assert torch.equal(~out.isfinite(), bad), far
+
+
+@gpu_only
 @pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (BF, 256), (F32, 64)])
 def test_rising_and_large_scores(gpu, dtype, d):
     # the maximum rises from tile to tile, then falls; and scores far apart

@@ -697,6 +697,9 @@ constexpr int kJoinWarps = 8;
 
 template <typename T>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const PagedParams p) {
+  // A part without tokens, or none with a weight, may hold nothing and is left out.  One whose weight is too small
+  // for fp32 is not: it may hold an infinity or a NaN, which shows.
+  constexpr float kNone = -1.f;
   extern __shared__ float weight[];                 // [parts], then the warps' sums [kJoinWarps][d]
   __shared__ float red[kJoinWarps];
   grid_dependency_wait();
@@ -720,18 +723,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const Paged
 #pragma unroll
   for (int k = 0; k < kJoinWarps; ++k) M = fmaxf(M, red[k]);
   for (int k = threadIdx.x; k < parts; k += kJoinWarps * 32)
-    weight[k] = weight[k] == -INFINITY ? 0.f : expf(weight[k] - M);
+    weight[k] = weight[k] == -INFINITY ? kNone : expf(weight[k] - M);
   __syncthreads();
   float L = 0.f;
-  for (int k = 0; k < parts; ++k) L += weight[k];
+  for (int k = 0; k < parts; ++k) L += weight[k] == kNone ? 0.f : weight[k];
   for (int e = lane * 4; e < p.d; e += 128) {
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int k = warp; k < parts; k += kJoinWarps) {
       const float h = weight[k];
-      float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (h != 0.f)                                 // a part without a weight may hold nothing
-        y = *reinterpret_cast<const float4 *>(p.part_o + row_of(k) * p.d + e);
+      if (h == kNone) continue;
+      const float4 y = *reinterpret_cast<const float4 *>(p.part_o + row_of(k) * p.d + e);
       x.x = fmaf(y.x, h, x.x);
       x.y = fmaf(y.y, h, x.y);
       x.z = fmaf(y.z, h, x.z);

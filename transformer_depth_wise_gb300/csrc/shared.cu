@@ -256,7 +256,6 @@ struct Sum {
     if (d > 128 && lane * 4 + 128 < d) v[1] = *reinterpret_cast<const float4 *>(row + lane * 4 + 128);
   }
   __device__ __forceinline__ void add(const Sum &x, float h) {
-    if (h == 0.f) return;                  // a part without a weight may hold nothing
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       v[i].x = fmaf(x.v[i].x, h, v[i].x);
@@ -276,7 +275,10 @@ struct Sum {
     }
   }
 };
-__device__ __forceinline__ float part_weight(float lse, float M) { return lse == -INFINITY ? 0.f : expf(lse - M); }
+// A part without tokens, or none with a weight, may hold nothing and is left out.  One whose weight is too small for
+// fp32 is not: it may hold an infinity or a NaN, which shows.
+__device__ __forceinline__ bool part_counts(float lse) { return lse != -INFINITY; }
+__device__ __forceinline__ float part_weight(float lse, float M) { return part_counts(lse) ? expf(lse - M) : 0.f; }
 __device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
@@ -319,16 +321,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_few_kernel(const 
   for (int k = 0; k <= PARTS; ++k) {
     const float w = part_weight(x[k], M);
     L += w;
-    s.add(y[k], w);
+    if (part_counts(x[k])) s.add(y[k], w);
   }
 #pragma unroll 2
   for (int c = 0; c < pieces; ++c) {
     const int at = piece(c);
     Sum z;
     z.load(p.piece_o + (int64_t)at * d, lane, d);
-    const float w = part_weight(p.piece_lse[at], M);
+    const float lse = p.piece_lse[at], w = part_weight(lse, M);
     L += w;
-    s.add(z, w);
+    if (part_counts(lse)) s.add(z, w);
   }
   s.store((T *)p.out + (int64_t)row * d, lane, d, L == 0.f ? 0.f : 1.f / L);
   if (lane == 0 && p.lse) p.lse[row] = L == 0.f ? -INFINITY : M + logf(L);
@@ -373,16 +375,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const Join
   s.zero();
   for (int k0 = 0; k0 < parts; k0 += 32) {
     src = src0;
-    const float w = part_weight(k0 == 0 ? x0 : find(k0 + lane, src), M);
+    const float lse = k0 == 0 ? x0 : find(k0 + lane, src), w = part_weight(lse, M);
     L += w;
+    const unsigned counts = __ballot_sync(0xffffffffu, part_counts(lse));
     const int n = min(32, parts - k0);
 #pragma unroll 4
     for (int k = first; k < n; k += WARPS) {
       const float h = __shfl_sync(0xffffffffu, w, k);
       const float *from = reinterpret_cast<const float *>(__shfl_sync(0xffffffffu, (unsigned long long)src, k));
+      if (!(counts >> k & 1u)) continue;
       Sum y;
-      y.zero();
-      if (h != 0.f) y.load(from, lane, d);
+      y.load(from, lane, d);
       s.add(y, h);
     }
   }
