@@ -278,7 +278,7 @@ int attnres_rms_norm(const void *x, int64_t B, int64_t T, int64_t D, int dtype, 
  *   sum_out     device [B,T,D] or NULL
  *   y           device [B,T,D]
  * sum_out and y may each be x or residual, but not the same, and overlap
- * nothing else.  D up to 2048 16-byte vectors.
+ * nothing else, in part neither (VALUE).  D up to 2048 16-byte vectors.
  */
 int attnres_add_rms_norm(const void *x, const void *residual, int64_t B, int64_t T, int64_t D, int dtype,
                          const float *weight, float eps, void *sum_out, void *y, void *stream);
@@ -290,7 +290,7 @@ int attnres_add_rms_norm(const void *x, const void *residual, int64_t B, int64_t
  *   group       elements per scale: 32, 64 or 128 (D a multiple), or 0: one
  *               scale per token row (VALUE otherwise)
  *   y8          device bytes [B,T,D];  scales device fp32 [B,T,D/group] or [B,T,1]
- * y8 and scales overlap nothing else.  A NaN among a group's y (an infinity
+ * y8 and scales overlap nothing else (VALUE).  A NaN among a group's y (an infinity
  * in a row makes one) gives a NaN scale and NaN y8 in that group.
  */
 int attnres_add_rms_norm_8bit(const void *x, const void *residual, int64_t B, int64_t T, int64_t D, int dtype,
@@ -304,7 +304,7 @@ int attnres_add_rms_norm_8bit(const void *x, const void *residual, int64_t B, in
  *   dx = grad_sum + r (u - s r^2 mean(u (.) s)),   grad_weight = sum over rows of grad_y (.) s r
  *   grad_sum    device [B,T,D], the upstream gradient of sum, or NULL (zero)
  *   dx          device [B,T,D]; may be s, grad_y or grad_sum, and overlaps
- *               nothing else
+ *               nothing else, nor do grad_weight and workspace (VALUE)
  *   grad_weight device fp32 [D] or NULL
  *   workspace   device fp32 [workspace_rows, D], needed for grad_weight;
  *               attnres_add_rms_norm_backward_workspace_rows() rows fill the

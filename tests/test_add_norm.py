@@ -317,6 +317,56 @@ def test_refusals():
     assert _lib.lib().attnres_add_rms_norm_backward_workspace_rows() >= 1
 
 
+def test_refusal_of_partial_overlaps():
+    """Outputs lie on an input row on row, or apart: anything between is a race of one row's reads with another's writes."""
+    far, row, n = FAKE + (1 << 20), 512, 1024                        # two rows of 256 bf16
+    apart = dict(x=FAKE, r=far, y=far + (1 << 20))
+    for name in ("y", "total"):
+        for at in (FAKE + row, FAKE - row, FAKE + n - 16, FAKE + 16 - n, far + row, far - 16):
+            assert norm(**(apart | {name: at})) == VALUE, (name, at - FAKE)
+        assert norm(**(apart | {name: FAKE, "r": FAKE + row})) == VALUE, name           # on x, and the residual half on it
+        assert norm(**(apart | {name: far, "w": far + n - 64})) == VALUE, name          # the weight (1024 bytes) too
+        assert norm(**(apart | {name: far + n, "w": far + n - 64})) == VALUE, name
+    assert norm(**(apart | {"total": apart["y"] + row})) == VALUE and norm(**(apart | {"total": apart["y"] - row})) == VALUE
+    eight = dict(x=FAKE, r=far, y=far + (1 << 20), sc=far + (1 << 21), total=far + (1 << 22))
+    assert norm8(**(eight | {"total": FAKE + row})) == VALUE and norm8(**(eight | {"total": far - row})) == VALUE
+    for base, size in ((FAKE, n), (far, n), (eight["total"], n)):
+        for at in (base, base + row, base + size - 16, base - 256):  # y8 has 512 bytes
+            assert norm8(**(eight | {"y": at})) == VALUE
+        for at in (base, base + row, base + size - 4, base - 28):    # the scales 32
+            assert norm8(**(eight | {"sc": at})) == VALUE
+    assert norm8(**(eight | {"sc": eight["y"] + 508})) == VALUE and norm8(**(eight | {"sc": eight["y"] - 28})) == VALUE
+    assert norm8(**(eight | {"w": eight["sc"] - 1008})) == VALUE and norm8(**(eight | {"w": eight["y"] + 496})) == VALUE
+    back = dict(s=FAKE, gy=far, gs=far + (1 << 20), dx=far + (1 << 21), gw=far + (1 << 22), ws=far + (1 << 23))
+    for base in (back["s"], back["gy"], back["gs"]):
+        assert backward(**(back | {"dx": base + row})) == VALUE and backward(**(back | {"dx": base - row})) == VALUE
+        for name in ("gw", "ws"):
+            assert backward(**(back | {name: base})) == VALUE and backward(**(back | {name: base - row})) == VALUE
+            assert backward(**(back | {name: base + n - 16})) == VALUE
+    for at in (back["dx"] + row, back["gw"] + row, back["ws"] + row):
+        assert backward(**(back | {"w": at})) == VALUE
+    assert backward(**(back | {"gw": back["dx"] - 16})) == VALUE and backward(**(back | {"ws": back["gw"] - row})) == VALUE
+    assert backward(**(back | {"ws": back["gw"] - 4096, "rows": 5})) == VALUE           # a later row of the workspace
+
+
+@gpu_only
+def test_neighbours_are_no_overlap(gpu):
+    """Rows right behind one another in one buffer are apart."""
+    g = wk.generator(14, gpu)
+    for dtype in (BF, F32):
+        buf = rand(g, 12, 256, dtype=dtype)
+        x, r, w = buf[0:3].clone(), buf[3:6].clone(), 1 + rand(g, 256, dtype=F32, scale=0.1)
+        want = api.add_rms_norm(x, r, w)
+        got = api.add_rms_norm(buf[0:3], buf[3:6], w, sum_out=buf[6:9], out=buf[9:12])
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+        dx, dw = api.add_rms_norm_backward(want[1], w, EPS, x, r)
+        buf[0:3], buf[3:6], buf[6:9] = want[1], x, r
+        got = api.add_rms_norm_backward(buf[0:3], w, EPS, buf[3:6], buf[6:9], dx=buf[9:12])
+        assert torch.equal(got[0], dx) and torch.equal(got[1], dw)
+        with pytest.raises(_lib.AttnResError):
+            api.add_rms_norm(buf[1:4], r, w, out=buf[0:3])
+
+
 @gpu_only
 def test_wrapper_refusals(gpu):
     x, r, w = inputs(gpu, BF, 4, 256, True, 1)

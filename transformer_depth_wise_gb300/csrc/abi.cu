@@ -54,11 +54,17 @@ int check_eps(float eps) {
 
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? ATTNRES_OK : ATTNRES_ERR_CUDA; }
 
+struct AddNormSpans {
+  Span x, residual, sum, weight;
+  bool bad_sum() const { return shifted(sum, x) || shifted(sum, residual) || share(sum, weight); }
+  bool on_any(const Span &s) const { return share(s, x) || share(s, residual) || share(s, sum) || share(s, weight); }
+};
+
 // What both forms of the norm with the residual's addition check of their
 // common arguments.  sum and y may lie on x or residual (a thread reads its
 // vectors of a row before it writes them), but not on one another.
 int add_norm_args(const void *x, const void *residual, int64_t B, int64_t T, int64_t D, int dtype, const float *weight,
-                  float eps, void *sum_out, void *y, void *stream, AddNormArgs &a) {
+                  float eps, void *sum_out, void *y, void *stream, AddNormArgs &a, AddNormSpans &sp) {
   int st = check_rows(B, T, D, dtype, a.rows);
   if (st) return st;
   if ((st = check_eps(eps))) return st;
@@ -69,6 +75,9 @@ int add_norm_args(const void *x, const void *residual, int64_t B, int64_t T, int
       (sum_out && !aligned16(sum_out)) || !aligned16(y))
     return ATTNRES_ERR_ALIGNMENT;
   if (y == sum_out || (weight && (y == weight || sum_out == weight))) return ATTNRES_ERR_VALUE;
+  const int64_t width = D * (16 / vec_elems(dtype));
+  sp = {rows_span(x, a.rows, width), rows_span(residual, a.rows, width), rows_span(sum_out, a.rows, width),
+        {weight, D * (int64_t)sizeof(float)}};
   a.x = x;
   a.residual = residual;
   a.D = (int)D;
@@ -240,8 +249,12 @@ int attnres_rms_norm(const void *x, int64_t B, int64_t T, int64_t D, int dtype, 
 int attnres_add_rms_norm(const void *x, const void *residual, int64_t B, int64_t T, int64_t D, int dtype,
                          const float *weight, float eps, void *sum_out, void *y, void *stream) {
   AddNormArgs a{};
-  int st = add_norm_args(x, residual, B, T, D, dtype, weight, eps, sum_out, y, stream, a);
+  AddNormSpans sp{};
+  int st = add_norm_args(x, residual, B, T, D, dtype, weight, eps, sum_out, y, stream, a, sp);
   if (st || a.rows == 0) return st;
+  const Span out{y, sp.x.bytes};
+  if (sp.bad_sum() || shifted(out, sp.x) || shifted(out, sp.residual) || share(out, sp.sum) || share(out, sp.weight))
+    return ATTNRES_ERR_VALUE;
   return cuda_status(launch_add_norm(a));
 }
 
@@ -250,15 +263,15 @@ int attnres_add_rms_norm_8bit(const void *x, const void *residual, int64_t B, in
                               void *stream) {
   if (group != 0 && group != 32 && group != 64 && group != 128) return ATTNRES_ERR_VALUE;
   AddNormArgs a{};
-  int st = add_norm_args(x, residual, B, T, D, dtype, weight, eps, sum_out, y8, stream, a);
+  AddNormSpans sp{};
+  int st = add_norm_args(x, residual, B, T, D, dtype, weight, eps, sum_out, y8, stream, a, sp);
   if (st) return st;
   if (group && D % group) return ATTNRES_ERR_SHAPE;
   if (a.rows == 0) return ATTNRES_OK;
   if (!scales) return ATTNRES_ERR_NULL;
   if (reinterpret_cast<uintptr_t>(scales) & 3u) return ATTNRES_ERR_ALIGNMENT;
-  const void *sc = scales;
-  if (y8 == x || y8 == residual || sc == x || sc == residual || sc == y8 || sc == sum_out || sc == weight)
-    return ATTNRES_ERR_VALUE;
+  const Span out = rows_span(y8, a.rows, D), sc = rows_span(scales, a.rows, (group ? D / group : 1) * (int64_t)sizeof(float));
+  if (sp.bad_sum() || sp.on_any(out) || sp.on_any(sc) || share(out, sc)) return ATTNRES_ERR_VALUE;
   a.bits8 = true;
   a.group = group;
   a.scales = scales;
@@ -285,7 +298,15 @@ int attnres_add_rms_norm_backward(const void *s, int64_t B, int64_t T, int64_t D
   if (!aligned16(s) || !aligned16(grad_y) || (grad_sum && !aligned16(grad_sum)) || !aligned16(dx) ||
       (weight && !aligned16(weight)) || (grad_weight && !aligned16(workspace)))
     return ATTNRES_ERR_ALIGNMENT;
-  if (grad_weight && (grad_weight == weight || workspace == grad_weight)) return ATTNRES_ERR_VALUE;
+  const int64_t width = D * (16 / vec_elems(dtype)), line = D * (int64_t)sizeof(float);
+  const Span out = rows_span(dx, rows, width), w{weight, line}, gw{grad_weight, line},
+             ws = rows_span(grad_weight ? workspace : nullptr, workspace_rows, line);
+  for (const void *p : {s, grad_y, grad_sum}) {
+    const Span in = rows_span(p, rows, width);
+    if (shifted(out, in) || share(gw, in) || share(ws, in)) return ATTNRES_ERR_VALUE;
+  }
+  if (share(out, w) || share(out, gw) || share(out, ws) || share(gw, w) || share(gw, ws) || share(ws, w))
+    return ATTNRES_ERR_VALUE;
   AddNormBackwardArgs a{s, grad_y, grad_sum, rows, (int)D, dtype, weight, eps, dx, grad_weight,
                         grad_weight ? workspace : nullptr, workspace_rows, static_cast<cudaStream_t>(stream)};
   return cuda_status(launch_add_norm_backward(a));

@@ -14,6 +14,22 @@ int sm_count();
 // it gives up (attnres_set_wait_limit; about 2 s by default).
 long long wait_limit_cycles();
 
+// Memory that a call reads or writes (nullptr: none).
+struct Span {
+  const void *p;
+  int64_t bytes;
+};
+inline Span rows_span(const void *p, int64_t rows, int64_t row_bytes) {
+  return {p, rows > INT64_MAX / row_bytes ? INT64_MAX : rows * row_bytes};
+}
+inline bool share(const Span &a, const Span &b) {
+  if (!a.p || !b.p) return false;
+  const uint64_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+  return x < y ? y - x < (uint64_t)a.bytes : x - y < (uint64_t)b.bytes;
+}
+// An output that lies on an input's rows other than its own: some would be read after others have been written.
+inline bool shifted(const Span &out, const Span &in) { return out.p != in.p && share(out, in); }
+
 struct AggregateArgs {
   const void *const *sources;  // host array of n device pointers
   int n;
