@@ -492,6 +492,8 @@ int64_t attnres_paged_attention_workspace_bytes(int Hq, int Hk, int64_t d, int d
  *   workspace      device, attnres_shared_prefix_attention_workspace_bytes()
  *                  bytes; its contents on entry do not matter.  Two calls that
  *                  may overlap need one each.
+ * workspace, out and lse overlap nothing else, in part neither (VALUE); out
+ * and lse may lie on q.
  * bf16: the prefix's weights enter the product with the values as bf16 (sums
  * and references in fp32).  An empty prefix is allowed;
  * a sequence without any token gives zeros and lse = -infinity.  Pages outside

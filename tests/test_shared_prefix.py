@@ -633,6 +633,30 @@ def test_refusals():
     assert shared(B=0, q=None, out=None, n=None) == OK
 
 
+def test_refusal_of_partial_overlaps():
+    M = 1 << 30
+    apart = dict(q=FAKE, kc=FAKE + M, vc=FAKE + 2 * M, ptab=FAKE + 3 * M, pl=FAKE + 4 * M, table=FAKE + 5 * M, n=FAKE + 6 * M,
+                 out=FAKE + 7 * M, lse=FAKE + 8 * M, ws=FAKE + 9 * M)
+    need = _lib.lib().attnres_shared_prefix_attention_workspace_bytes(2, 8, 2, 64, 1, 16, 4, 4)
+    size = dict(q=2 * 1024, kc=8 * 2 * 16 * 128, vc=8 * 2 * 16 * 128, ptab=16, pl=4, table=32, n=8, out=2048, lse=64, ws=need)
+    assert need < M
+    for name in ("out", "lse", "ws"):
+        for other in apart:
+            if other == name or (other == "q" and name != "ws"):
+                continue
+            for at in (apart[other], apart[other] + (size[other] - 1) // 16 * 16, apart[other] - size[name] // 16 * 16 + 16):
+                assert shared(**(apart | {name: at})) == VALUE, (name, other, at - apart[other])
+
+
+@gpu_only
+def test_outputs_on_the_queries(gpu):
+    for dtype, d in ((BF, 128), (F32, 64)):
+        q, kc, vc, pt, n, t, lengths, scale = inputs(gpu, dtype, 8, 2, d, 16, 700, [20, 300, 0] * 9, 80)
+        want = api.shared_prefix_attention(q, kc, vc, pt, n, t, lengths, scale)
+        got = api.shared_prefix_attention(q, kc, vc, pt, n, t, lengths, scale, out=q)
+        assert got[0] is q and all(torch.equal(x, y) for x, y in zip(got, want))
+
+
 @gpu_only
 def test_wrapper_refusals(gpu):
     a = inputs(gpu, BF, 4, 2, 64, 16, 40, [3, 5], 1)

@@ -345,7 +345,17 @@ int attnres_shared_prefix_attention(const void *q, int64_t q_stride, const void 
       misaligned(prefix_table, 4) || misaligned(prefix_length, 4) || misaligned(page_table, 4) ||
       misaligned(lengths, 4) || misaligned(lse, 4))
     return ATTNRES_ERR_ALIGNMENT;
-  if (among(out, k_cache, v_cache, workspace) || among(workspace, q, k_cache, v_cache, lse)) return ATTNRES_ERR_VALUE;
+  // What is written lies apart from what the call reads and from one another;
+  // only the outputs may lie on the queries, which have been read by then.
+  const int64_t e = 16 / vec_elems(dtype), i32 = sizeof(int32_t), head = d * e;
+  const Span scratch{workspace, w.bytes}, o{out, B * Hq * head}, l{lse, B * Hq * (int64_t)sizeof(float)};
+  const Span read[] = {rows_span(k_cache, num_pages, (int64_t)Hk * page_size * head), rows_span(v_cache, num_pages, (int64_t)Hk * page_size * head),
+                       {prefix_table, prefix_pages * i32}, {prefix_pages ? prefix_length : nullptr, i32},
+                       {page_table, B * max_pages * i32}, {lengths, B * i32}};
+  for (const Span &in : read)
+    if (share(scratch, in) || share(o, in) || share(l, in)) return ATTNRES_ERR_VALUE;
+  if (share(scratch, {q, ((B - 1) * q_stride + Hq * d) * e}) || share(scratch, o) || share(scratch, l) || share(o, l))
+    return ATTNRES_ERR_VALUE;
   SharedArgs a{};
   a.q = q; a.q_stride = q_stride; a.k_cache = k_cache; a.v_cache = v_cache; a.num_pages = num_pages;
   a.page_size = page_size; a.prefix_pages = prefix_pages;
