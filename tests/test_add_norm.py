@@ -282,6 +282,53 @@ def test_empty_shapes_views_and_streams(gpu):
     assert all(torch.equal(a, b) for a, b in zip(got, step()))
 
 
+FIRST_CALLS = """
+import threading, torch
+from transformer_depth_wise_gb300 import api
+dev = torch.device("cuda:0")
+x = torch.linspace(-3, 3, 64 * 2048, device=dev).view(64, 2048)
+w = torch.linspace(0.5, 1.5, 2048, device=dev)
+cache = x.view(-1)[:32 * 2 * 16 * 64].view(32, 2, 16, 64).contiguous()
+pages, table = torch.arange(20, device=dev).int(), torch.arange(20, 32, device=dev).view(4, 3).int()
+length, own = torch.tensor([310], device=dev).int(), torch.tensor([40, 1, 0, 17], device=dev).int()
+query = x.view(-1)[:4 * 8 * 64].view(4, 8, 64).contiguous()
+torch.cuda.synchronize()
+start, got = threading.Barrier(8), [None] * 8
+
+def work(i):
+    dtype = (torch.float32, torch.bfloat16)[i % 2]
+    a, q, c = x.to(dtype), query.to(dtype), cache.to(dtype)
+    with torch.cuda.stream(torch.cuda.Stream(dev)):
+        torch.cuda.synchronize()
+        start.wait()
+        y, s = api.add_rms_norm(a, a, w)
+        y8, sc, _ = api.add_rms_norm_8bit(a, None, w, group=64)
+        dx, dw = api.add_rms_norm_backward(s, w, 1e-6, y)
+        o, lse = api.shared_prefix_attention(q, c, c, pages, length, table, own, 0.125)
+        torch.cuda.current_stream().synchronize()
+    got[i] = (y, s, y8.float(), sc, dx, dw, o, lse)
+
+threads = [threading.Thread(target=work, args=(i,)) for i in range(8)]
+for t in threads:
+    t.start()
+for t in threads:
+    t.join()
+torch.cuda.synchronize()
+for i in range(2, 8):
+    assert all(torch.equal(p, q) for p, q in zip(got[i], got[i % 2])), i
+"""
+
+
+@gpu_only
+def test_first_calls_from_several_threads(gpu):
+    """What the library finds once and keeps (SMs, resident CTAs, shared-memory limits) may be found by threads at once."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, check=True, timeout=300)
+
+
 # --------------------------------------------------------------------------
 # refusals
 # --------------------------------------------------------------------------

@@ -11,16 +11,12 @@
 namespace attnres {
 
 int sm_count() {
-  static int cache[64] = {0};
-  int dev = 0;
+  static Kept kept[64];
+  int dev = 0, n = 1;
   if (cudaGetDevice(&dev) != cudaSuccess) return 1;
-  int &c = cache[dev & 63];
-  if (c == 0) {
-    int v = 0;
-    if (cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v < 1) v = 1;
-    c = v;
-  }
-  return c;
+  const cudaError_t e = kept[dev & 63].get(
+      n, [&](int *v) { return cudaDeviceGetAttribute(v, cudaDevAttrMultiProcessorCount, dev); });
+  return e == cudaSuccess ? n : 1;
 }
 
 namespace {

@@ -427,12 +427,12 @@ RowShape shape_of(int nvec, bool whole) {
 // asked once per device and CTA size.
 template <auto kern>
 int resident(int threads, size_t smem) {
-  static int known[16][17] = {};
-  int dev = 0;
+  static Kept kept[16][17];
+  int dev = 0, n = 1;
   cudaGetDevice(&dev);
-  int &n = known[dev & 15][threads / 32];
-  if (n == 0 && (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem) != cudaSuccess || n < 1)) n = 1;
-  return n;
+  const cudaError_t e = kept[dev & 15][threads / 32].get(
+      n, [&](int *v) { return cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, kern, threads, smem); });
+  return e == cudaSuccess ? n : 1;
 }
 
 // Call f with the vectors per thread and the lanes of a row as types.

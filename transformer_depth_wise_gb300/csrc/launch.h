@@ -5,7 +5,25 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace attnres {
+
+// A number that is found once (per device, kernel and so on) and kept, 0
+// until then.  Two host threads may find it at the same time; both store the
+// same value.
+struct Kept {
+  std::atomic<int> value{0};
+  template <typename F> cudaError_t get(int &out, F find) {
+    out = value.load(std::memory_order_relaxed);
+    if (out != 0) return cudaSuccess;
+    const cudaError_t e = find(&out);
+    if (e != cudaSuccess) return e;
+    if (out < 1) out = 1;
+    value.store(out, std::memory_order_relaxed);
+    return cudaSuccess;
+  }
+};
 
 // Streaming-multiprocessor count of the current device (cached per device).
 int sm_count();
@@ -342,12 +360,12 @@ SharedLayout shared_layout(int64_t B, int Hq, int Hk, int64_t d, int dtype, int6
 cudaError_t launch_shared(const SharedArgs &a, const SharedLayout &w);
 // Raises a kernel's limit of dynamic shared memory, once per device.
 template <auto kern> cudaError_t allow_smem(size_t bytes) {
-  static bool done[16] = {};
+  static std::atomic<bool> done[16];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess || (dev < 16 && done[dev])) return e;
+  if (e != cudaSuccess || (dev < 16 && done[dev].load(std::memory_order_relaxed))) return e;
   e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess && dev < 16) done[dev] = true;
+  if (e == cudaSuccess && dev < 16) done[dev].store(true, std::memory_order_relaxed);
   return e;
 }
 
