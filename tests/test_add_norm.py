@@ -305,8 +305,12 @@ def work(i):
         y8, sc, _ = api.add_rms_norm_8bit(a, None, w, group=64)
         dx, dw = api.add_rms_norm_backward(s, w, 1e-6, y)
         o, lse = api.shared_prefix_attention(q, c, c, pages, length, table, own, 0.125)
+        n = api.rms_norm(a, w)
+        h = api.depth_aggregate([a, y, s], w)
+        grads, gq, gg = api.depth_aggregate_backward([a, y, s], w, w, 1e-6, h)
+        p1, _, p1_lse = api.block_phase1([a, y, s], torch.stack((w, 2 * w)))
         torch.cuda.current_stream().synchronize()
-    got[i] = (y, s, y8.float(), sc, dx, dw, o, lse)
+    got[i] = (y, s, y8.float(), sc, dx, dw, o, lse, n, h, *grads, gq, gg, p1, p1_lse)
 
 threads = [threading.Thread(target=work, args=(i,)) for i in range(8)]
 for t in threads:

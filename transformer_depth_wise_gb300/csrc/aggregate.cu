@@ -685,15 +685,12 @@ bool choose(int D, int dtype, Cfg &c) {
 template <typename T, int VPT, int TEAM, bool F>
 cudaError_t run(const AggParams &p, const Cfg &c, cudaStream_t st) {
   auto kern = aggregate_kernel<T, VPT, TEAM, F>;
-  static int occ[16] = {0};  // resident CTAs per SM, per device
-  int dev = 0;
+  static Kept occ[16];  // resident CTAs per SM, per device
+  int dev = 0, o = 0;
   cudaGetDevice(&dev);
-  int &o = occ[dev & 15];
-  if (o == 0) {
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, kern, c.threads, 0);
-    if (e != cudaSuccess) return e;
-    if (o < 1) o = 1;
-  }
+  const cudaError_t found = occ[dev & 15].get(
+      o, [&](int *v) { return cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, kern, c.threads, 0); });
+  if (found != cudaSuccess) return found;
   const int per_cta = TEAM ? c.threads / TEAM : 1;
   const int64_t groups = (p.rows + per_cta - 1) / per_cta;
   const int64_t cap = (int64_t)o * sm_count();

@@ -346,18 +346,12 @@ bool choose(int D, int dtype, Cfg &c) {
 // Resident CTAs per SM of one instantiation on the current device.
 template <typename T, int TEAM, int TPR>
 cudaError_t occupancy(const Cfg &c, int &o) {
-  static int occ[16] = {0};
+  static Kept occ[16];
   int dev = 0;
   cudaGetDevice(&dev);
-  int &slot = occ[dev & 15];
-  if (slot == 0) {
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&slot, aggregate_backward_kernel<T, 2, TEAM, TPR>,
-                                                                  c.threads, 0);
-    if (e != cudaSuccess) return e;
-    if (slot < 1) slot = 1;
-  }
-  o = slot;
-  return cudaSuccess;
+  return occ[dev & 15].get(o, [&](int *v) {
+    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, aggregate_backward_kernel<T, 2, TEAM, TPR>, c.threads, 0);
+  });
 }
 
 template <typename T, int TEAM, int TPR>

@@ -646,15 +646,12 @@ bool choose(int D, int dtype, Cfg &c) {
 template <typename T, int VPT, int TEAM>
 cudaError_t run(const MergeParams &p, const Cfg &c, cudaStream_t st) {
   auto kern = merge_kernel<T, VPT, TEAM>;
-  static int occ[16] = {0};
-  int dev = 0;
+  static Kept occ[16];
+  int dev = 0, o = 0;
   cudaGetDevice(&dev);
-  int &o = occ[dev & 15];
-  if (o == 0) {
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, kern, c.threads, 0);
-    if (e != cudaSuccess) return e;
-    if (o < 1) o = 1;
-  }
+  const cudaError_t found = occ[dev & 15].get(
+      o, [&](int *v) { return cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, kern, c.threads, 0); });
+  if (found != cudaSuccess) return found;
   const int per_cta = TEAM ? c.threads / TEAM : 1;
   const int64_t groups = (p.rows + per_cta - 1) / per_cta;
   const int64_t cap = (int64_t)o * sm_count();
@@ -683,20 +680,25 @@ template <typename T, int VPT, int TEAM, bool SYNTH, bool NORM, int TPR = 0>
 cudaError_t run_mu(const MergeUpdateParams &P, const Cfg &c, cudaStream_t st) {
   auto kern = merge_update_kernel<T, VPT, TEAM, SYNTH, NORM, TPR>;
   const size_t smem = (size_t)P.m.D * sizeof(float) * (1 + (SYNTH ? 1 : 0) + (NORM ? 1 : 0));
-  struct Entry { int dev; size_t smem; int occ; };
-  static Entry cache[16];
-  static int used = 0;
+  // resident CTAs by device and shared memory: (memory, device, CTAs) in one word, 0 where nothing is kept yet
+  static std::atomic<uint64_t> cache[16];
   int dev = 0, o = 0;
   cudaGetDevice(&dev);
-  for (int i = 0; i < used; ++i)
-    if (cache[i].dev == dev && cache[i].smem == smem) o = cache[i].occ;
+  const uint64_t key = (uint64_t)smem << 32 | (uint64_t)(dev & 0xffff) << 16;
+  int at = 0;
+  for (; at < 16 && o == 0; ++at) {
+    const uint64_t kept = cache[at].load(std::memory_order_relaxed);
+    if (kept == 0) break;
+    if ((kept & ~(uint64_t)0xffff) == key) o = (int)(kept & 0xffff);
+  }
   if (o == 0) {
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, mu_max_smem(NORM));
     if (e != cudaSuccess) return e;
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, kern, c.threads, smem);
     if (e != cudaSuccess) return e;
     if (o < 1) o = 1;
-    if (used < 16) cache[used++] = {dev, smem, o};
+    uint64_t empty = 0;                // another thread's entry may have come here meanwhile: then this one is not kept
+    if (at < 16) cache[at].compare_exchange_strong(empty, key | (uint64_t)o, std::memory_order_relaxed);
   }
   const int per_cta = TEAM ? c.threads / TEAM : 1;
   const int64_t groups = (P.m.rows + per_cta - 1) / per_cta;
@@ -747,15 +749,12 @@ cudaError_t dispatch_mu_t(const MergeUpdateParams &P, const Cfg &c, cudaStream_t
 template <typename T, int VPT, int TEAM>
 cudaError_t run_norm(const RmsNormArgs &a, const Cfg &c) {
   auto kern = rms_norm_kernel<T, VPT, TEAM>;
-  static int occ[16] = {0};
-  int dev = 0;
+  static Kept occ[16];
+  int dev = 0, o = 0;
   cudaGetDevice(&dev);
-  int &o = occ[dev & 15];
-  if (o == 0) {
-    cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&o, kern, c.threads, 0);
-    if (e != cudaSuccess) return e;
-    if (o < 1) o = 1;
-  }
+  const cudaError_t found = occ[dev & 15].get(
+      o, [&](int *v) { return cudaOccupancyMaxActiveBlocksPerMultiprocessor(v, kern, c.threads, 0); });
+  if (found != cudaSuccess) return found;
   const int per_cta = TEAM ? c.threads / TEAM : 1;
   const int64_t groups = (a.rows + per_cta - 1) / per_cta;
   const int64_t cap = (int64_t)o * sm_count();
