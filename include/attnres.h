@@ -287,6 +287,9 @@ int attnres_add_rms_norm(const void *x, const void *residual, int64_t B, int64_t
  * The same with y in 8 bits for a matrix product: e4m3 values (largest 448)
  * and fp32 scales, y ~ y8 * scale with
  *   scale = max(max |y| over the group / 448, 2^-126),  y8 = y / scale to nearest even
+ * Both quotients are formed as products with fp32 reciprocals: the scale is
+ * within two roundings of that quotient, and a y / scale within two roundings
+ * (2^-23 of itself) of the middle of two e4m3 values may go to either.
  *   group       elements per scale: 32, 64 or 128 (D a multiple), or 0: one
  *               scale per token row (VALUE otherwise)
  *   y8          device bytes [B,T,D];  scales device fp32 [B,T,D/group] or [B,T,1]

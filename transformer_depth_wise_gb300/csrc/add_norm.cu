@@ -4,7 +4,9 @@
 // Per token row, with s = x + residual in fp32:  sum = s rounded once,
 // y = s r w, r = (mean s^2 + eps)^(-1/2), rounded once to the row's type, or
 // in e4m3 with one fp32 scale per group of a row's elements (or per row):
-// scale = max|y| / 448 over the group, y8 = y / scale.
+// scale = max|y| / 448 over the group, y8 = y / scale (as products with the
+// rounded reciprocals of 448 and of the scale: a division per element would
+// change only values within two roundings of a tie).
 // Backward at the stored sum s:  u = grad_y w,  dx = grad_sum + r (u - s r^2
 // mean(u s)),  grad_weight = sum over rows of grad_y s r.
 //
