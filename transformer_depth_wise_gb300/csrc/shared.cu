@@ -478,7 +478,7 @@ SharedLayout shared_layout(int64_t B, int Hq, int Hk, int64_t d, int dtype, int6
   SharedLayout w{};
   const int G = Hq / Hk;
   if (B > 0 && tokens > 0)
-    w.splits = dtype == ATTNRES_BF16 ? shared_tc_splits(B, G, Hk, d, tokens) : f32_splits(B, G, Hk, (int)d, tokens);
+    w.splits = dtype == ATTNRES_BF16 ? shared_tc_splits(B, G, Hk, d, tokens, own) : f32_splits(B, G, Hk, (int)d, tokens);
   const int64_t rows = B * Hq, parts = w.splits + 1;
   // Behind a prefix's kernel the SMs come free one after the other: ranges
   // of a third of the length even that out, where the tables leave each of

@@ -58,8 +58,9 @@ struct PrefixParams {
   }
 };
 
-// The parts on the 5th-generation tensor cores (bf16): how many, and the launch.
-int shared_tc_splits(int64_t B, int G, int Hk, int64_t d, int64_t tokens);
+// The parts on the 5th-generation tensor cores (bf16): how many, and the launch.  tokens, own: what the prefix's table
+// and a sequence's cover.
+int shared_tc_splits(int64_t B, int G, int Hk, int64_t d, int64_t tokens, int64_t own);
 cudaError_t launch_shared_tc(const PrefixParams &p, cudaStream_t stream);
 
 }  // namespace attnres

@@ -477,19 +477,24 @@ template <int D> cudaError_t launch(const PrefixParams &p, cudaStream_t stream) 
 
 // Ranges of the prefix with the least time, in microseconds: a CTA's start and
 // end, its steps (of one tile or two), and the parts that the join reads and
-// writes; and the own tokens' kernel, which runs beside the last CTAs where
-// they leave a tenth of the SMs free (64 questions about 131071 tokens: 127 us
-// with 16 SMs left, 137 with 8, 134 with none, 132 with 24).
-int shared_tc_splits(int64_t B, int G, int Hk, int64_t d, int64_t tokens) {
+// writes; and the own tokens' kernel, which runs beside the prefix's CTAs where
+// they leave a tenth of the SMs free.  That is worth it where the tables cover
+// 40 MB of own tokens and more.  64 questions about 131071 tokens, us with 16
+// SMs left and with none: 512 own tokens at most 126 and 132 (67 MB; 137 with 8
+// left, 132 with 24), 1024 143 and 139, 2048 159 and 158; two key heads and 65536 tokens,
+// 1024 own ones (50 MB) 58 and 61.  Below, it is not: 256 126 and 125, 128 127 and 126,
+// a page of 64 126 and 120, none 125 and 116.
+int shared_tc_splits(int64_t B, int G, int Hk, int64_t d, int64_t tokens, int64_t own) {
   const int rows = d <= 128 ? Layout<128>::kRows : Layout<256>::kRows, keys = d <= 128 ? Layout<128>::kKeys : Layout<256>::kKeys;
   const int64_t items = (B * G + rows - 1) / rows * Hk, steps = (tokens + keys - 1) / keys;
   const double row_us = (double)B * G * Hk * d * 8e-6 / 4., step_us = B * G > kTileRows && d <= 128 ? 1.8 : 1.2;
   const int64_t slots = sm_count();
+  const double beside_us = (double)B * Hk * own * d * 4. >= 40e6 ? 18. : 0.;
   int best = 1;
   double least = 1e300;
   for (int n = 1; n <= kMaxPrefixParts && n <= steps; ++n) {
     const int64_t waves = (items * n + slots - 1) / slots, free = waves * slots - items * n;
-    const double cost = (double)waves * (8. + step_us * (double)((steps + n - 1) / n)) + row_us * n + (10 * free < slots ? 18. : 0.);
+    const double cost = (double)waves * (8. + step_us * (double)((steps + n - 1) / n)) + row_us * n + (10 * free < slots ? beside_us : 0.);
     if (cost < least) {
       least = cost;
       best = n;
