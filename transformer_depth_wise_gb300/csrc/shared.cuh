@@ -6,7 +6,10 @@
 
 namespace attnres {
 
-constexpr int kMaxPrefixParts = 64;      // ranges of the prefix
+// Most ranges of the prefix: what a part adds to the workspace and to the
+// join's reads grows with them.  With one key head and up to 256 rows they are
+// fewer than the SMs.
+constexpr int kMaxPrefixParts = 64;
 
 struct PrefixParams {
   const void *q, *k, *v;

@@ -47,7 +47,7 @@ ATTNRES_DEFINE_ERROR_FLAG(take_error_shared)
 namespace attnres {
 namespace {
 
-constexpr int kTileRows = 128;             // rows of a tile: one per thread
+constexpr int kTileRows = 128;             // rows of a tile: two threads have one
 constexpr int kThreads = 768;
 constexpr uint32_t kQBlock = 128 * 128;    // bytes: 128 rows of 64 bf16 columns
 constexpr int kRegs = 80;                  // a thread's registers at the launch, then the roles' shares
