@@ -33,32 +33,6 @@ constexpr float kLeast = 0x1p-126f;        // the smallest scale: its reciprocal
 
 enum Mode { kPlain, kGroups, kRow8 };      // y in the row's type, in e4m3 by groups, in e4m3 by rows
 
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-
-// A vector from pairs of fp32 values, rounded to the element type.
-template <typename T>
-__device__ __forceinline__ uint4 from_pairs(const uint64_t *x) {
-  constexpr int NP = Pairs<T>::NP;
-  float f[2 * NP];
-#pragma unroll
-  for (int i = 0; i < NP; ++i) unpair(x[i], f[2 * i], f[2 * i + 1]);
-  return Elt<T>::pack(f);
-}
-
 // Four values in e4m3, to nearest even, held within +-448; NaN stays NaN.
 __device__ __forceinline__ uint32_t to_e4m3(uint64_t a, uint64_t b) {
   float f[4];

@@ -297,6 +297,28 @@ __device__ __forceinline__ void fma_pair(uint64_t &acc, uint64_t a, uint64_t b) 
 __device__ __forceinline__ void scale_pair(uint64_t &acc, uint64_t s) {
   asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(acc) : "l"(s), "l"(0ull));
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+// 2^x by the exponential unit: within 2^-22 of itself, subnormal results as zero.
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
 
 template <typename T> struct Pairs;
 template <> struct Pairs<float> {
@@ -314,6 +336,16 @@ template <> struct Pairs<__nv_bfloat16> {
     for (int i = 0; i < 4; ++i) x[i] = ((uint64_t)(w[i] & 0xffff0000u) << 32) | (uint64_t)(w[i] << 16);
   }
 };
+
+// A vector from pairs of fp32 values, rounded to the element type.
+template <typename T>
+__device__ __forceinline__ uint4 from_pairs(const uint64_t *x) {
+  constexpr int NP = Pairs<T>::NP;
+  float f[2 * NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) unpair(x[i], f[2 * i], f[2 * i + 1]);
+  return Elt<T>::pack(f);
+}
 
 // Sum of K (a power of two, <= 32) values over a whole CTA, every thread
 // getting all K totals.  Each warp reduce-scatters (butterflies down to K
@@ -372,7 +404,14 @@ constexpr long long kDrainLimitCycles = 4000000000ll;
 __device__ __forceinline__ uint32_t smem_u32(const void *p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
-// Asynchronous copies into shared memory by threads: the end of a group, and all but the last N groups there.
+// Asynchronous copies of 16 bytes into shared memory by threads (of zeros where not live); the end of a group, and all
+// but the last N groups there.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");

@@ -94,27 +94,7 @@ struct Unit {
   }
 };
 
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 __device__ __forceinline__ uint64_t swapped(uint64_t a) { return a >> 32 | a << 32; }
-
-// A vector from pairs of fp32 values, rounded to the element type.
-template <typename T>
-__device__ __forceinline__ uint4 from_pairs(const uint64_t *x) {
-  constexpr int NP = Pairs<T>::NP;
-  float f[2 * NP];
-#pragma unroll
-  for (int i = 0; i < NP; ++i) unpair(x[i], f[2 * i], f[2 * i + 1]);
-  return Elt<T>::pack(f);
-}
 
 // Turn a unit (2 NP pairs of fp32 values: vector 0, then vector 1) by the
 // angles at c and s, forwards or back.

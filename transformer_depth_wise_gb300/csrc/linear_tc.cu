@@ -144,11 +144,6 @@ __device__ __forceinline__ uint32_t narrow(uint64_t v) {
   unpair(v, lo, hi);
   return Elt<__nv_bfloat16>::pack_word(lo, hi);
 }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
 
 // 16 lanes x 32 columns spread over the warp as four matrix fragments of 16 x
 // 8: pair 2 i + j of a thread is row lane / 4 + 8 j, columns 8 i + 2 (lane %

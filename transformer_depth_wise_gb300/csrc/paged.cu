@@ -420,9 +420,6 @@ template <int D> struct MmaShape {
   static constexpr size_t kSmem = (size_t)kWarpsM * kStages * kStage + 16 * kOutPitch * sizeof(float);
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
-}
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -435,11 +432,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
 }
 // A pair of weights as its nearest bf16 pair and the bf16 pair of what is left.
 __device__ __forceinline__ void split_pair(float a, float b, uint32_t &hi, uint32_t &lo) {
@@ -503,16 +495,16 @@ __global__ void __launch_bounds__(kWarpsM * 32, MmaShape<D>::kCtas) paged_mma_ke
           for (int i = 0; i < kPerRow; ++i, ks += step, vs += step) {
             const int r = (i * 32 + lane) / CH;
             const uint32_t to = dst + r * S::kPitch + (((lane % CH) ^ (r & 7)) * 16);
-            cp_async16(to, ks, true);
-            cp_async16(to + kRow * S::kPitch, vs, true);
+            copy16(to, ks, true);
+            copy16(to + kRow * S::kPitch, vs, true);
           }
         } else if (lane % CH * 8 < D) {             // a row's padding
 #pragma unroll
           for (int i = 0; i < kPerRow; ++i) {
             const int r = (i * 32 + lane) / CH;
             const uint32_t to = dst + r * S::kPitch + (((lane % CH) ^ (r & 7)) * 16);
-            cp_async16(to, p.k, false);
-            cp_async16(to + kRow * S::kPitch, p.v, false);
+            copy16(to, p.k, false);
+            copy16(to + kRow * S::kPitch, p.v, false);
           }
         }
       } else {
@@ -524,8 +516,8 @@ __global__ void __launch_bounds__(kWarpsM * 32, MmaShape<D>::kCtas) paged_mma_ke
           const int64_t at = live ? off + c * 8 : 0;
           const uint32_t to = dst + r * S::kPitch + ((c ^ (r & 7)) * 16);
           if (c * 8 < D) {
-            cp_async16(to, (const __nv_bfloat16 *)p.k + at, live);
-            cp_async16(to + kRow * S::kPitch, (const __nv_bfloat16 *)p.v + at, live);
+            copy16(to, (const __nv_bfloat16 *)p.k + at, live);
+            copy16(to + kRow * S::kPitch, (const __nv_bfloat16 *)p.v + at, live);
           }
         }
       }

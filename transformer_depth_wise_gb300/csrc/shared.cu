@@ -40,12 +40,6 @@ template <int D, int ROWS> struct Shape {
   static constexpr int kPieces = kKeys * D / 4 / kThreads;            // 16-byte pieces of a tile per thread and tensor
 };
 
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kThreads) shared_f32_kernel(const PrefixParams p) {
   using S = Shape<D, ROWS>;
