@@ -334,7 +334,21 @@ def prefix_ref(q, kc, vc, fp, fs, scale, coarse):
 def test_many_steps_in_one_range(gpu, dtype, d, B, G, tile, pattern):
     """So many key heads that a range has 20 steps and more: references, maxima and sums go on from step to step, and
     every ring's places are used again and again."""
-    Hk, page = 136, 16
+    many_steps(gpu, dtype, d, B, G, tile, pattern, 16)
+
+
+@gpu_only
+@pytest.mark.parametrize("pattern", ["rising", "spikes", "gaps"])
+@pytest.mark.parametrize("dtype,d,B,G,tile", [(BF, 64, 150, 1, 128), (BF, 128, 50, 4, 128), (BF, 72, 9, 2, 128), (BF, 256, 5, 4, 64),
+                                              (F32, 64, 3, 2, 64)])
+@pytest.mark.parametrize("page", [128, 64, 32, 12])
+def test_many_steps_over_other_pages(gpu, dtype, d, B, G, tile, pattern, page):
+    """Pages that hold a warp's tokens of a step side by side, and pages that end inside them."""
+    many_steps(gpu, dtype, d, B, G, tile, pattern, page)
+
+
+def many_steps(gpu, dtype, d, B, G, tile, pattern, page):
+    Hk = 136
     steps = 45 if dtype is F32 and d == 64 else 23
     prefix = steps * tile - 37                                       # the last step is a partial one
     g = wk.generator(50, gpu)
@@ -359,8 +373,8 @@ def test_many_steps_in_one_range(gpu, dtype, d, B, G, tile, pattern):
     else:                                                            # the first steps, one in the middle and parts of others on no page
         up = torch.linspace(-2, 2, pages * page, device=gpu)
         pt[:2 * tile // page + 1] = -1
-        pt[9 * tile // page:10 * tile // page] = pages
-        pt[12 * tile // page + 1:14 * tile // page - 1] = -7
+        pt[9 * tile // page:10 * tile // page + 1] = pages
+        pt[12 * tile // page + 1:max(14 * tile // page - 1, 12 * tile // page + 2)] = -7
     if up is not None:
         at = pt.long()[j // page]
         ok = at >= 0
@@ -405,6 +419,24 @@ def test_ragged_batches(gpu, seed):
 def test_warps_partly_behind_the_batch(gpu, d, B):
     # B rows per key head: in one warp of a tile some lanes have a row and others none
     check(inputs(gpu, BF, 2, 2, d, 16, 150, [b % 3 for b in range(B)], 40 + B), BF, d)
+
+
+@gpu_only
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_cache_offsets_past_32_bits(gpu, dtype):
+    """Pages whose elements and bytes lie behind 2^31 and 2^32."""
+    Hk, page, d, B = 2, 64, 128, 5
+    pool = 2 ** 32 // (Hk * page * d) + 40
+    q, kc, vc, pt, n, t, lengths, scale = inputs(gpu, dtype, 8, Hk, d, page, 700, [100, 0, 64, 1, 128], 90)
+    size = pt.numel() + t.numel()
+    far_k, far_v = (torch.empty(pool, Hk, page, d, device=gpu, dtype=dtype) for _ in range(2))
+    # the same pages at the pool's end, and some about the borders
+    at = torch.arange(pool - size, pool, device=gpu)
+    at[:4] = torch.tensor([2 ** 31 // (Hk * page * d) - 1, 2 ** 31 // (Hk * page * d), 2 ** 32 // (Hk * page * d) - 1, 0], device=gpu)
+    far_k[at], far_v[at] = kc[:size], vc[:size]
+    got = api.shared_prefix_attention(q, far_k, far_v, at[pt.long()].int(), n, at[t.long()].int(), lengths, scale)
+    want = api.shared_prefix_attention(q, kc, vc, pt, n, t, lengths, scale)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
 
 
 @gpu_only
