@@ -439,3 +439,11 @@ def test_wrapper_refusals(gpu):
         api.add_rms_norm(x, r, w, sum_out=r, out=r)
     with pytest.raises(ValueError):
         api.add_rms_norm_backward(x, w, EPS, None)
+
+
+@gpu_only
+@pytest.mark.parametrize("group", [-32, -1])
+def test_negative_group_is_refused_by_name(gpu, group):
+    x, r, w = inputs(gpu, BF, 4, 256, True, 1)
+    with pytest.raises(ValueError, match="group"):
+        api.add_rms_norm_8bit(x, r, w, group=group)

@@ -358,7 +358,7 @@ def add_rms_norm_8bit(x, residual, weight=None, eps: float = 1e-6, group: int = 
     """
     B, T, D, sum_out = _add_norm_args(x, residual, weight, sum_out)
     lead = x.shape[:-1]
-    if group and D % group:
+    if group < 0 or (group and D % group):
         raise ValueError(f"group must divide {D}")
     shape = (*lead, D // group if group else 1)
     if out is None:
