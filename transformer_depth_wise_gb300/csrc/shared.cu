@@ -476,14 +476,16 @@ SharedLayout shared_layout(int64_t B, int Hq, int Hk, int64_t d, int dtype, int6
   const int64_t rows = B * Hq, parts = w.splits + 1;
   // Behind a prefix's kernel the SMs come free one after the other: ranges
   // of a third of the length even that out, where the tables leave each of
-  // them 16 tiles of 64 tokens or more.  With thirds and without: 256 chats of up
-  // to 2048 tokens 259 and 269 us (halves, when it was 277 without, 266, sixths
-  // 265), 64 chats of as many behind 2048 tokens 82 and 92, 64 of up to 1024 with
-  // heads of 256 128 and 141; but 128 of up to 1024 with heads of 64 94 and 89.
-  // Below: 64 chats of up to 256 50 and 45, 48 of up to 1024 on two key heads 63 and
-  // 57, fp32 328 and 320; but 64 of up to 512 with heads of 256 130 and 154.
+  // them 8 tiles of 64 tokens or more (fp32: 16).  With thirds and without: 256
+  // chats of up to 2048 tokens 259 and 269 us (halves, when it was 277 without,
+  // 266, sixths 265), 64 of as many behind 2048 tokens 82 and 92, with heads of 256
+  // 64 of up to 1024 128 and 141 and of up to 512 130 and 154, 64 of up to 2048 behind
+  // 131071 155 and 159; but 128 of up to 1024 with heads of 64 94 and 89.  Below: 64 chats
+  // of up to 256 50 and 45, 48 of up to 1024 on two key heads 63 and 57, fp32 with
+  // 9 tiles 328 and 320.
   w.own_ctas = paged_ctas(d, dtype);
-  if (w.splits && B * Hk * (own / 64) >= 16 * (int64_t)paged_fine_ctas(d, dtype)) w.own_ctas = paged_fine_ctas(d, dtype);
+  const int64_t fine = paged_fine_ctas(d, dtype), least = dtype == ATTNRES_BF16 ? 8 : 16;
+  if (w.splits && B * Hk * (own / 64) >= least * fine) w.own_ctas = (int)fine;
   w.pieces = up16(paged_workspace_bytes(G, d, dtype, w.own_ctas));
   w.ready = w.pieces + up16(B * Hk * (int64_t)sizeof(Pieces));
   w.part_lse = w.ready + 16;
