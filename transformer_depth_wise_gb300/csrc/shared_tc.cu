@@ -15,7 +15,12 @@
 // first step), and O and the sum are rescaled then; fp32 and bf16 hold what lies
 // above it.  So a step needs no maximum.  Rounding P to bf16 adds an error of
 // the size of the output's own rounding; the sum is that of the unrounded
-// weights.
+// weights.  Two parts of P, as the own tokens' weights have them (paged.cu),
+// leave only the output's rounding (0.0017 of the outputs' norm in place of
+// 0.0019 to 0.0023), but they make the second product twice as long, and the
+// products bind: with 640 threads, whose softmax then has the registers for it,
+// 64 questions about 131071 tokens took 164 us instead of 127, 256 chats behind
+// 8192 278 instead of 259, 64 behind 8192 with heads of 128 51 instead of 46.
 //
 // Roles: the two tiles' softmax (two warpgroups each); copies (cp.async of 16
 // bytes a lane, a row's page looked up by its own lane, into a ring of tiles
@@ -456,18 +461,19 @@ template <int D> cudaError_t launch(const PrefixParams &p, cudaStream_t stream) 
 // Ranges of the prefix with the least time, in microseconds: a CTA's start and
 // end, its steps (of one tile or two), and the parts that the join reads and
 // writes; and the own tokens' kernel, which runs beside the prefix's CTAs where
-// they leave a tenth of the SMs free.  That is worth it where the tables cover
-// 40 MB of own tokens and more.  64 questions about 131071 tokens, us with 16
-// SMs left and with none: 512 own tokens at most 126 and 132 (67 MB; 137 with 8
-// left, 132 with 24), 1024 143 and 139, 2048 159 and 158; two key heads and 65536 tokens,
-// 1024 own ones (50 MB) 58 and 61.  Below, it is not: 256 126 and 125, 128 127 and 126,
-// a page of 64 126 and 120, none 125 and 116.
+// they leave a tenth of the SMs free, and else behind them: 4 and its bytes at
+// 6 TB/s, where there are own tokens, and no more than 18 (beyond that it
+// outlasts them either way).  64 questions about 131071 tokens, us with 16 SMs
+// left and with none: no own tokens 125 and 116, a page of 64 at most 126 and 120,
+// 256 126 and 125, 512 126 and 132 (137 with 8 left, 132 with 24), 1024 143 and 139, 2048
+// 159 and 158; two key heads and 65536 tokens, 1024 own ones 58 and 61; four short
+// chats 14 and 18.
 int shared_tc_splits(int64_t B, int G, int Hk, int64_t d, int64_t tokens, int64_t own) {
   const int rows = d <= 128 ? Layout<128>::kRows : Layout<256>::kRows, keys = d <= 128 ? Layout<128>::kKeys : Layout<256>::kKeys;
   const int64_t items = (B * G + rows - 1) / rows * Hk, steps = (tokens + keys - 1) / keys;
   const double row_us = (double)B * G * Hk * d * 8e-6 / 4., step_us = B * G > kTileRows && d <= 128 ? 1.8 : 1.2;
   const int64_t slots = sm_count();
-  const double beside_us = (double)B * Hk * own * d * 4. >= 40e6 ? 18. : 0.;
+  const double own_us = own > 0 ? 4. + (double)B * Hk * own * d * 4. / 6e6 : 0., beside_us = own_us < 18. ? own_us : 18.;
   int best = 1;
   double least = 1e300;
   for (int n = 1; n <= kMaxPrefixParts && n <= steps; ++n) {
