@@ -498,7 +498,9 @@ int64_t attnres_paged_attention_workspace_bytes(int Hq, int Hk, int64_t d, int d
  * workspace, out and lse overlap nothing else, in part neither (VALUE); out
  * and lse may lie on q.
  * bf16: the prefix's weights enter the product with the values as bf16 (sums
- * and references in fp32).  An empty prefix is allowed;
+ * and references in fp32), which adds about as much error as the outputs' own
+ * rounding does; the own tokens' weights enter with 16 bits, as all do in
+ * attnres_paged_attention.  An empty prefix is allowed;
  * a sequence without any token gives zeros and lse = -infinity.  Pages outside
  * [0, num_pages) are left out, and NaN and infinities show, as there.
  */
