@@ -584,6 +584,71 @@ def test_every_input_written_just_before(gpu, dtype, d, per):
         assert all(torch.equal(x, y) for x, y in zip(got, want[k])), step
 
 
+FIRST_CAPTURED = """
+import torch
+from transformer_depth_wise_gb300 import api
+dev = torch.device("cuda:0")
+g = torch.Generator(device=dev).manual_seed(5)
+B, Hk, page, d, first, per = 32, 4, 16, 128, 200, 40
+pool = first + B * per
+def some():
+    pages = torch.randperm(pool, device=dev, generator=g).int()
+    r = lambda *s: torch.empty(s, device=dev).normal_(generator=g).bfloat16()
+    return [r(B, 16, d), r(pool, Hk, page, d), r(pool, Hk, page, d), pages[:first].contiguous(),
+            torch.randint(1, first * page, (1,), device=dev, generator=g).int(), pages[first:].view(B, per).contiguous(),
+            torch.randint(0, per * page + 1, (B,), device=dev, generator=g).int()]
+sets, a = [some() for _ in range(4)], some()
+torch.cuda.synchronize()
+graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+with torch.cuda.graph(graph, stream=side):
+    got = [api.shared_prefix_attention(*a, 0.09) for _ in range(3)]
+for step in range(12):
+    with torch.cuda.stream(side):
+        for to, t in zip(a, sets[step % 4]):
+            to.copy_(t)
+        graph.replay()
+        for to in a:
+            to.zero_()
+    torch.cuda.synchronize()
+    want = api.shared_prefix_attention(*sets[step % 4], 0.09)
+    for out in got:
+        assert all(torch.equal(x, y) for x, y in zip(out, want)), step
+"""
+
+
+@gpu_only
+def test_first_call_is_captured(gpu):
+    """A process whose first call goes into a graph; replays read what was written right before them."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", FIRST_CAPTURED], cwd=root, check=True, timeout=300)
+
+
+@gpu_only
+def test_more_calls_than_marks(gpu):
+    """Calls side by side on two streams, so many that they take the same places in the table of marks again."""
+    cases = [inputs(gpu, dtype, 16, 4, 64, 16, 400, [200] * 8, 100 + k) for k, dtype in enumerate((BF, F32))]
+    want = [api.shared_prefix_attention(*a) for a in cases]
+    sides = [torch.cuda.Stream(gpu) for _ in range(2)]
+    ws = [torch.full((1 << 26,), 255, device=gpu, dtype=torch.uint8) for _ in range(2)]
+    got = [[torch.empty_like(t) for t in w] for w in want]
+    torch.cuda.synchronize()
+    for k in range(5000):
+        for i in range(2):
+            with torch.cuda.stream(sides[i]):
+                api.shared_prefix_attention(*cases[i], out=got[i][0], lse=got[i][1], workspace=ws[i])
+        if k % 1000 == 999:
+            torch.cuda.synchronize()
+            for x, y in zip(got, want):
+                assert all(torch.equal(a, b) for a, b in zip(x, y))
+            for x in got:
+                for t in x:
+                    t.zero_()
+            torch.cuda.synchronize()
+
+
 @gpu_only
 def test_serving_layer(gpu):
     """One decoded token of a batch behind a shared image and text prefix: add + norm in 8 bits, the projection, head

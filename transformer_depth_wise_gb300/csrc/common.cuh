@@ -232,28 +232,34 @@ __device__ __forceinline__ void prefetch_l2_bulk(const void *gmem, uint32_t byte
 // few SMs an earlier grid has left idle crowded onto them, and measured on a
 // GB300 the early trigger was slower everywhere (Full stack 26.9 -> 28.4 ms,
 // its two-phase schedule 9.04 -> 9.96 ms, decode graph 188 -> 196 us).  The
-// one exception is attention behind a shared prefix (shared.cu): a kernel of
-// one warp triggers before its wait (its follower waits for its end), and the
-// prefix's kernels trigger after theirs, so that the paged kernel that follows
-// may work beside them.  That one reads nothing of theirs, but what the
-// kernels before them wrote, and only a thread that has waited sees that by
-// the grids' own order.  So it either waits like every other kernel, or finds
-// a mark raised (acquired there, released by a thread that has waited), and
-// then one of its CTAs waits at the end, for the kernels that follow.
+// one exception is attention behind a shared prefix (shared.cu): the prefix's
+// kernels trigger after their wait, so that the paged kernel that follows may
+// work beside them.  That one reads nothing of theirs, but what the kernels
+// before them wrote, and only a thread that has waited sees that by the grids'
+// own order.  So it either waits like every other kernel, or finds a mark
+// raised (acquired there, released by a thread that has waited), and then one
+// of its CTAs waits at the end, for the kernels that follow.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
-// A mark in global memory that one kernel raises for another: what the raising thread has seen before is visible to
-// a thread that finds it raised.
-__device__ __forceinline__ void raise_mark(unsigned *mark) {
-  asm volatile("st.release.gpu.global.u32 [%0], 1;" ::"l"(mark) : "memory");
-}
-__device__ __forceinline__ bool mark_raised(const unsigned *mark) {
-  unsigned v;
-  asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(mark) : "memory");
-  return v == 1u;
-}
+// A mark that one kernel of a call raises for the next: what the raising thread has seen before is visible to a thread
+// that finds the call's number there.
+struct Mark {
+  unsigned long long *at;              // nullptr: none
+  unsigned long long number;
+  __device__ __forceinline__ void raise() const {
+    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(at), "l"(number) : "memory");
+  }
+  __device__ __forceinline__ bool raised() const {
+    unsigned long long v;
+    asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(at) : "memory");
+    return v == number;
+  }
+  __device__ __forceinline__ void take_away() const {
+    asm volatile("st.relaxed.gpu.global.u64 [%0], %1;" ::"l"(at), "l"(0ull) : "memory");
+  }
+};
 
 // Launch `kern` with programmatic stream serialization: its launch overlaps
 // the end of the previous kernel on the stream (it must call

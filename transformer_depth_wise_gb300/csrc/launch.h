@@ -7,6 +7,8 @@
 
 #include <atomic>
 
+#include "common.cuh"
+
 namespace attnres {
 
 // A number that is found once (per device, kernel and so on) and kept, 0
@@ -314,7 +316,7 @@ struct PagedArgs {
   cudaStream_t stream;
   int ctas;                    // paged_ctas(), or paged_fine_ctas()
   bool out_f32;                // out is fp32 whatever the type (with pieces)
-  const unsigned *ready;       // the mark of the kernel before, which starts this one early (nullptr: none)
+  Mark ready;                  // of the kernel before, which starts this one early
   Pieces *pieces;              // [B, Hk]: the caller joins the pairs that are cut (nullptr: joined here)
 };
 bool paged_supported(int64_t d, int dtype);
@@ -347,13 +349,13 @@ struct SharedArgs {
   void *workspace;             // SharedLayout::bytes
   cudaStream_t stream;
 };
-// A workspace: the paged kernel's own and its pairs' pieces, the mark that
-// lets that kernel work beside the prefix's, then lse and outputs of the
-// prefix's parts and of the sequences' own one, in bytes from its start.
+// A workspace: the paged kernel's own and its pairs' pieces, then lse and
+// outputs of the prefix's parts and of the sequences' own one, in bytes from
+// its start.
 struct SharedLayout {
   int splits;                  // parts of the prefix
   int own_ctas;                // of the own tokens' kernel
-  int64_t pieces, ready, part_lse, part_o, bytes;
+  int64_t pieces, part_lse, part_o, bytes;
 };
 // tokens, own: what the prefix's table and a sequence's cover.
 SharedLayout shared_layout(int64_t B, int Hq, int Hk, int64_t d, int dtype, int64_t tokens, int64_t own);

@@ -43,7 +43,7 @@ struct PagedParams {
   int64_t num_pages;
   float scale;
   void *out;                           // [B, Hq, d]
-  const unsigned *ready;               // a mark of the kernel before, which is waited for at the end only (or nullptr)
+  Mark ready;                          // of the kernel before, which is waited for at the end only (or none)
   bool out_f32;                        // out in fp32 whatever the type (a part of a longer attention, with pieces)
   float *lse;                          // [B, Hq] or nullptr
   float *part_o, *part_lse;            // [ctas][2][G][d], [ctas][2][G]
@@ -58,11 +58,11 @@ struct PagedParams {
 // is read here; a thread that finds the mark raised sees all that it waited
 // for itself, and one that does not waits for its end.
 __device__ __forceinline__ void wait_for_inputs(const PagedParams &p) {
-  if (!p.ready || !mark_raised(p.ready)) grid_dependency_wait();
+  if (!p.ready.at || !p.ready.raised()) grid_dependency_wait();
 }
 // What it ends with: one CTA's wait holds the launch's end until the kernel before has ended.
 __device__ __forceinline__ void wait_for_last(const PagedParams &p) {
-  if (p.ready && blockIdx.x + 1 == gridDim.x) grid_dependency_wait();
+  if (p.ready.at && blockIdx.x + 1 == gridDim.x) grid_dependency_wait();
 }
 
 // The sequence's length, held within what its row of the page table covers.

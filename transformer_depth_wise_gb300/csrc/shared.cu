@@ -20,6 +20,7 @@
 // bind: 12 words a lane for 32 multiply-adds, then 16 for 64.  Measured on
 // GB300: 64 sequences of 32 heads over 8 behind 8000 tokens, 128 wide 245 us (34
 // TFLOP/s), 64 wide and 16000 tokens 251 us, 256 wide and 4000 tokens 356 us (24).
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -237,6 +238,7 @@ struct JoinParams {
   const Pieces *pieces;                    // [B, Hk]
   int splits, Hq, Hk, G, d;
   int rows;                                // B Hq
+  Mark ready;                              // of the own tokens' kernel, taken away
   void *out;
   float *lse;
 };
@@ -287,6 +289,7 @@ constexpr int kJoinWarps = 8;
 template <typename T, int PARTS>
 __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_few_kernel(const JoinParams p) {
   grid_dependency_wait();
+  if (p.ready.at && blockIdx.x == 0 && threadIdx.x == 0) p.ready.take_away();
   const int lane = threadIdx.x % 32, d = p.d;
   const int row = blockIdx.x * kJoinWarps + threadIdx.x / 32;
   if (row >= p.rows) return;
@@ -337,6 +340,7 @@ template <typename T, int WARPS>
 __global__ void __launch_bounds__(kJoinWarps * 32) shared_join_kernel(const JoinParams p) {
   __shared__ Sum sums[kJoinWarps][32];
   grid_dependency_wait();
+  if (p.ready.at && blockIdx.x == 0 && threadIdx.x == 0) p.ready.take_away();
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, first = warp % WARPS, d = p.d;
   const int row = blockIdx.x * (kJoinWarps / WARPS) + warp / WARPS;
   const bool live = row < p.rows;
@@ -457,11 +461,28 @@ cudaError_t launch_shared_f32(const PrefixParams &p, cudaStream_t stream) {
   return wide ? go(R64{}, R128{}) : go(R64{}, R64{});
 }
 
-// Lowers the own tokens' mark, whatever the workspace holds.
-__global__ void __launch_bounds__(32) shared_lower_kernel(unsigned *ready) {
-  launch_dependents();                   // the prefix's kernel, which waits for this one's end
-  grid_dependency_wait();
-  if (threadIdx.x == 0) *ready = 0;
+// The own tokens' marks.  A call takes the next place and a number that no
+// other call has; its prefix's kernel writes the number there, and its join
+// takes it away, so that a captured call finds none of its last replay.  Calls
+// that share a place at the same time overwrite each other's number, and then
+// the own tokens' kernel waits like any other.
+constexpr int kMarks = 4096;
+__device__ unsigned long long g_marks[kMarks];
+
+Mark next_mark() {
+  static std::atomic<unsigned long long *> places[16];
+  static std::atomic<unsigned long long> calls{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 16) return {};
+  unsigned long long *p = places[dev].load(std::memory_order_relaxed);
+  if (!p) {
+    void *at = nullptr;
+    if (cudaGetSymbolAddress(&at, g_marks) != cudaSuccess) return {};
+    p = static_cast<unsigned long long *>(at);
+    places[dev].store(p, std::memory_order_relaxed);
+  }
+  const unsigned long long n = calls.fetch_add(1, std::memory_order_relaxed) + 1;
+  return {p + n % kMarks, n};
 }
 
 int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
@@ -487,8 +508,7 @@ SharedLayout shared_layout(int64_t B, int Hq, int Hk, int64_t d, int dtype, int6
   const int64_t fine = paged_fine_ctas(d, dtype), least = dtype == ATTNRES_BF16 ? 8 : 16;
   if (w.splits && B * Hk * (own / 64) >= least * fine) w.own_ctas = (int)fine;
   w.pieces = up16(paged_workspace_bytes(G, d, dtype, w.own_ctas));
-  w.ready = w.pieces + up16(B * Hk * (int64_t)sizeof(Pieces));
-  w.part_lse = w.ready + 16;
+  w.part_lse = w.pieces + up16(B * Hk * (int64_t)sizeof(Pieces));
   w.part_o = w.part_lse + up16(parts * rows * (int64_t)sizeof(float));
   w.bytes = w.part_o + parts * rows * d * (int64_t)sizeof(float);
   return w;
@@ -513,17 +533,14 @@ cudaError_t launch_shared(const SharedArgs &a, const SharedLayout &w) {
   p.wait_limit = wait_limit_cycles();
   cudaError_t e = cudaSuccess;
   if (w.splits > 0) {
-    p.ready = reinterpret_cast<unsigned *>(ws + w.ready);
-    e = launch_dependent(shared_lower_kernel, dim3(1), dim3(32), 0, a.stream, p.ready);
-  }
-  if (e == cudaSuccess && w.splits > 0)
+    p.ready = next_mark();
     e = a.dtype == ATTNRES_BF16 ? launch_shared_tc(p, a.stream) : launch_shared_f32(p, a.stream);
+  }
   if (e != cudaSuccess) return e;
   // The sequences' own tokens: the last part.  It needs nothing of the prefix's
   // kernel, which lets it start as soon as all of its own CTAs have: by the mark
   // it fills the SMs that that one leaves, and waits for its end at its own (256
-  // chats 258 us, 280 where it waits at its start; four chats 14 and 19 us; the
-  // launch that lowers the mark shows in neither).
+  // chats 258 us, 280 where it waits at its start; four chats 14 and 19 us).
   PagedArgs s{};
   s.q = a.q; s.q_stride = a.q_stride; s.k_cache = a.k_cache; s.v_cache = a.v_cache; s.num_pages = a.num_pages;
   s.page_size = a.page_size; s.max_pages = a.max_pages; s.page_table = a.page_table; s.lengths = a.lengths;
@@ -535,7 +552,7 @@ cudaError_t launch_shared(const SharedArgs &a, const SharedLayout &w) {
   JoinParams j{};
   const PagedParts own = paged_parts(ws, p.G, a.d, w.own_ctas);
   j.part_o = p.part_o; j.part_lse = p.part_lse; j.piece_o = own.o; j.piece_lse = own.lse; j.pieces = s.pieces;
-  j.splits = w.splits; j.Hq = a.Hq; j.Hk = a.Hk; j.G = p.G; j.d = a.d; j.rows = (int)rows; j.out = a.out; j.lse = a.lse;
+  j.splits = w.splits; j.Hq = a.Hq; j.Hk = a.Hk; j.G = p.G; j.d = a.d; j.rows = (int)rows; j.ready = p.ready; j.out = a.out; j.lse = a.lse;
   return a.dtype == ATTNRES_BF16 ? launch_join<__nv_bfloat16>(j, a.stream) : launch_join<float>(j, a.stream);
 }
 

@@ -22,7 +22,7 @@ struct PrefixParams {
   float *part_o, *part_lse;              // [splits][B Hq][d], [splits][B Hq]
   int splits;
   long long wait_limit;                  // SM clock cycles a wait of the tensor-core kernel may take
-  unsigned *ready;                       // the follower's mark, or nullptr: it waits for this kernel's end
+  Mark ready;                            // the follower's (none: it waits for this kernel's end)
 
   // What every thread of a prefix's kernel starts with: the wait for what
   // came before.  Then the own tokens' kernel may start; with `ready` it goes
@@ -30,7 +30,7 @@ struct PrefixParams {
   __device__ __forceinline__ void begin() const {
     grid_dependency_wait();
     if (threadIdx.x != 0) return;
-    if (ready && blockIdx.x == 0 && blockIdx.y == 0) raise_mark(ready);
+    if (ready.at && blockIdx.x == 0 && blockIdx.y == 0) ready.raise();
     launch_dependents();
   }
 
