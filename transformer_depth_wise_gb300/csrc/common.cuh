@@ -263,7 +263,7 @@ struct Mark {
 
 // Launch `kern` with programmatic stream serialization: its launch overlaps
 // the end of the previous kernel on the stream (it must call
-// grid_dependency_wait() before touching any data).
+// grid_dependency_wait() before touching any data, but for the exception above).
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                                     Args &&...args) {

@@ -470,19 +470,11 @@ constexpr int kMarks = 4096;
 __device__ unsigned long long g_marks[kMarks];
 
 Mark next_mark() {
-  static std::atomic<unsigned long long *> places[16];
   static std::atomic<unsigned long long> calls{0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 16) return {};
-  unsigned long long *p = places[dev].load(std::memory_order_relaxed);
-  if (!p) {
-    void *at = nullptr;
-    if (cudaGetSymbolAddress(&at, g_marks) != cudaSuccess) return {};
-    p = static_cast<unsigned long long *>(at);
-    places[dev].store(p, std::memory_order_relaxed);
-  }
+  void *at = nullptr;                    // asked every time: a device that has been reset has the table elsewhere
+  if (cudaGetSymbolAddress(&at, g_marks) != cudaSuccess) return {};
   const unsigned long long n = calls.fetch_add(1, std::memory_order_relaxed) + 1;
-  return {p + n % kMarks, n};
+  return {static_cast<unsigned long long *>(at) + n % kMarks, n};
 }
 
 int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
